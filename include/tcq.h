@@ -310,6 +310,118 @@ int tcq_scale_field(const float *W, int64_t M, int64_t N, int64_t ldw, float *ro
                     float *col_scale, float *Wn, int64_t ldn, void *workspace,
                     size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * The coded linear layer: products of a batch of rows with a trellis-coded matrix in the
+ * layer's own type, its gradients, and 8-bit checkpoints of activations.
+ *
+ * Element types of x, y, gradients and the codebook, and the layer's activation function.
+ */
+typedef enum { TCQ_F32 = 0, TCQ_F16 = 1, TCQ_BF16 = 2 } tcq_dtype;
+typedef enum {
+    TCQ_ACT_NONE = 0, /* z */
+    TCQ_ACT_RELU = 1, /* max(z, 0); slope 1 for z > 0, else 0 */
+    TCQ_ACT_SILU = 2, /* z / (1 + exp(-z)) */
+    TCQ_ACT_GELU = 3  /* z Phi(z), Phi the standard normal distribution function */
+} tcq_act;
+
+/* Limits of the layer's entry points: M, N <= 2^21, batch B <= 2^23. */
+#define TCQ_LINEAR_MAX_DIM (1 << 21)
+#define TCQ_LINEAR_MAX_BATCH (1 << 23)
+
+/*
+ * tcq_decode_linear -- y = act(z) + residual, z = row_scale (x W_hat^T) + bias, for B rows of
+ * x and the coded M x N matrix W_hat, decoded inside the call:
+ *     z[b][r] = row_scale[r] * sum_c W_hat[r][c] x[b][c] + bias[r]
+ *     y[b][r] = act(z[b][r]) + residual[b][r]
+ *   bitstream, start_state : device, as written by tcq_encode for an M x N problem
+ *   codebook   : device, 2^L * V values of the layer's type `dtype`.  (An fp32 table is
+ *                rounded to 16 bits once by the caller; an encoder run with the rounded
+ *                table's values matches the layer exactly.)
+ *   dtype      : TCQ_F32, TCQ_F16 or TCQ_BF16: type of codebook, x, residual, y, pre
+ *   x, B, ldx  : device, B x N, leading dimension ldx >= N
+ *   row_scale  : nullable device, M floats (the row scale of tcq_scale_field, for instance)
+ *   bias       : nullable device, M floats
+ *   act        : tcq_act
+ *   residual   : nullable device, B x M, ldr >= M; may be y itself (with ldr == ldy)
+ *   y, ldy     : device out, B x M, ldy >= M
+ *   pre, ldp   : nullable device out, B x M: z, rounded to the layer's type (what
+ *                tcq_act_pack and tcq_decode_linear_backward take)
+ *   workspace  : >= what tcq_decode_linear_workspace_bytes reports
+ * Outputs other than y == residual must not overlap inputs or one another.  Products and
+ * sums are fp32 (those of 16-bit inputs exact products); z is not rounded before the
+ * activation; each output is rounded once.  Repeated calls give identical results.
+ * N == 0 gives z = bias; M == 0 or B == 0 is a no-op.
+ * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED, TCQ_EWORKSPACE, TCQ_EHIP.
+ */
+int tcq_decode_linear_workspace_bytes(int dtype, int64_t B, int64_t M, int64_t N, int L, int k,
+                                      int V, int T, size_t *bytes);
+int tcq_decode_linear(const uint32_t *bitstream, const uint32_t *start_state,
+                      const void *codebook, int64_t M, int64_t N, int L, int k, int V, int T,
+                      int dtype, const void *x, int64_t B, int64_t ldx,
+                      const float *row_scale, const float *bias, int act,
+                      const void *residual, int64_t ldr, void *y, int64_t ldy, void *pre,
+                      int64_t ldp, void *workspace, size_t workspace_bytes,
+                      hipStream_t stream);
+
+/*
+ * 8-bit checkpoints of activations.  Each group of 32 consecutive values of a row (the last
+ * one may be shorter) shares one scale byte e, the exponent field of its largest magnitude
+ * as an fp32 number, and each value is held as an int8 code
+ *     q = clamp(round_half_even(x 2^(133 - e)), -127, 127),
+ * which stands for q 2^(e - 133): within 2^(e - 134) of x (half a step), or within one step
+ * where the clamp acts.  A group with an infinity or a NaN gets e = 255 and stands for NaN
+ * throughout; a group of zeros gets e = 0.
+ *
+ * tcq_act_pack
+ *   X, rows, cols, ldx : device input of type dtype, ldx >= cols
+ *   codes, ldq         : device out, rows x cols int8, ldq >= cols
+ *   scale              : device out, rows x ceil(cols / 32) bytes
+ * tcq_act_unpack
+ *   codes, ldq, scale  : as written by tcq_act_pack
+ *   out, ldo           : device out of type dtype, ldo >= cols.  Values are exact in fp32
+ *                        and bf16; fp16 holds those of fp16 inputs exactly and rounds others.
+ * rows == 0 or cols == 0 is a no-op.
+ * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED (rows or cols above 2^31 - 1), TCQ_EHIP.
+ */
+int tcq_act_pack(const void *X, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                 int8_t *codes, int64_t ldq, uint8_t *scale, hipStream_t stream);
+int tcq_act_unpack(const int8_t *codes, int64_t ldq, const uint8_t *scale, int64_t rows,
+                   int64_t cols, int dtype, void *out, int64_t ldo, hipStream_t stream);
+
+/*
+ * tcq_decode_linear_backward -- gradients of tcq_decode_linear from the gradient dy of y and
+ * 8-bit checkpoints of z and x:
+ *     g[b][r]  = dy[b][r] act'(z[b][r])        z, x: the values the checkpoints stand for
+ *     dbias[r] = sum_b g[b][r]
+ *     s[b][r]  = g[b][r] row_scale[r]          rounded to the layer's type
+ *     dx[b][c] = sum_r s[b][r] W_hat[r][c]
+ *     dw[r][c] = sum_b s[b][r] x[b][c]         the gradient of W_hat (straight through to W)
+ * The residual's gradient is dy itself.  Sums are fp32 in a fixed order; outputs of the
+ * layer's type are rounded once.
+ *   dy, B, lddy : device, B x M of type dtype
+ *   z_codes, ldz, z_scale : device checkpoint of z (B x M); not read with TCQ_ACT_NONE
+ *   x_codes, ldx, x_scale : device checkpoint of x (B x N); read for dw only
+ *   dx, lddx    : nullable device out, B x N (bitstream, start_state and codebook are read
+ *                 for dx only)
+ *   dw, lddw    : nullable device out, M x N
+ *   dbias       : nullable device out, M floats
+ *   workspace   : >= what the workspace query reports for the same outputs (nonzero
+ *                 dx, dw, dbias: wanted)
+ * B == 0 gives dw = 0 and dbias = 0, M == 0 gives dx = 0.  At least one output is wanted.
+ * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED, TCQ_EWORKSPACE, TCQ_EHIP.
+ */
+int tcq_decode_linear_backward_workspace_bytes(int dtype, int64_t B, int64_t M, int64_t N,
+                                               int L, int k, int V, int T, int dx, int dw,
+                                               int dbias, size_t *bytes);
+int tcq_decode_linear_backward(const uint32_t *bitstream, const uint32_t *start_state,
+                               const void *codebook, int64_t M, int64_t N, int L, int k, int V,
+                               int T, int dtype, const void *dy, int64_t B, int64_t lddy,
+                               const float *row_scale, int act, const int8_t *z_codes,
+                               int64_t ldz, const uint8_t *z_scale, const int8_t *x_codes,
+                               int64_t ldx, const uint8_t *x_scale, void *dx, int64_t lddx,
+                               void *dw, int64_t lddw, float *dbias, void *workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

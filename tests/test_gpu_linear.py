@@ -1,0 +1,472 @@
+"""The coded linear layer (tcq_decode_linear) and its gradients (tcq_decode_linear_backward)
+against the oracle's decode followed by float64 products.
+
+Bars (see linear_check.py): on exact inputs (codebook on a 1/8 grid, small-integer x, scales
+that are powers of two) every product and sum is an fp32 number in any order, so each output
+must equal the reference rounded once; on N(0, 1) inputs each output must lie within a
+bound that counts the roundings.
+"""
+import sys
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU visible", allow_module_level=True)
+
+from trellis_coded_bit_amd import _lib, api  # noqa: E402
+from trellis_coded_bit_amd import workloads as wl  # noqa: E402
+
+import linear_check as lc  # noqa: E402
+
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+ACTS = ["none", "relu", "silu", "gelu"]
+
+
+def _say(msg):
+    sys.stdout.write(msg + "\n")
+    sys.stdout.flush()
+
+
+class Coded:
+    """A coded matrix on the GPU and its float64 values."""
+
+    def __init__(self, seed, M, N, L, k, V, T, dtype, exact, oracle=None, shift=0):
+        rng = np.random.default_rng(seed)
+        self.shape = (M, N, L, k, V, T)
+        bits, s0 = lc.random_streams(rng, M * (N // T), L, k, V, T)
+        if exact:
+            C = lc.grid_table(L, V, rng)
+        else:
+            C = rng.standard_normal((1 << L, V)).astype(np.float32)
+        table = torch.from_numpy(C).to(dtype)
+        flat = torch.zeros(table.numel() + shift, dtype=dtype)
+        flat[shift:] = table.reshape(-1)
+        self.table = flat.cuda()[shift:].view(table.shape)
+        self.bits = torch.from_numpy(bits.view(np.int32)).cuda()
+        self.s0 = torch.from_numpy(s0.view(np.int32)).cuda()
+        rounded = np.ascontiguousarray(table.float().numpy())
+        if oracle is not None:
+            W = torch.from_numpy(oracle.decode_matrix(bits, s0, rounded, M, N, L, k, V, T)).cuda()
+        else:  # the library's decode, which has tests of its own, bit for bit
+            W = api.decode(self.bits, self.s0, torch.from_numpy(rounded).cuda(), M, N, L, k, V, T)
+        self.W = W.double()
+
+    def linear(self, x, **kw):
+        return api.decode_linear(self.bits, self.s0, self.table, x, *self.shape, **kw)
+
+    def backward(self, dy, **kw):
+        return api.decode_linear_backward(self.bits, self.s0, self.table, dy, *self.shape, **kw)
+
+
+def _place(t, lead, first, fill=float("nan")):
+    """t as a column slice of a wider GPU matrix whose other columns are `fill`."""
+    wide = torch.full((t.shape[0] + 1, t.shape[1] + lead), fill, dtype=t.dtype, device="cuda")
+    view = wide[:t.shape[0], first:first + t.shape[1]]
+    view.copy_(t)
+    return view
+
+
+def _ints(rng, rows, cols, dtype, most=8):
+    return torch.from_numpy(rng.integers(-most, most + 1, size=(rows, cols)).astype(np.float32)
+                            ).to(dtype).cuda()
+
+
+# L, k, V, T, M, N: whole units and not, one to four values a step, odd sizes
+SHAPES = [
+    (16, 2, 1, 256, 130, 512), (16, 2, 2, 256, 33, 256), (16, 3, 1, 256, 70, 768),
+    (8, 2, 1, 64, 64, 64), (12, 2, 1, 64, 257, 192), (16, 4, 1, 256, 40, 256),
+    (10, 3, 2, 30, 21, 120), (16, 1, 1, 17, 19, 17 * 7), (4, 1, 1, 12, 5, 36),
+    (16, 2, 4, 64, 48, 128), (9, 4, 1, 100, 6, 300), (16, 3, 1, 1, 9, 5),
+]
+
+
+def _exact_forward(w, x, rng, dtype, act, residual, strided, bias=True):
+    M = w.shape[0]
+    B = x.shape[0]
+    a = torch.from_numpy(2.0 ** rng.integers(-1, 2, M)).float().cuda()
+    b = torch.from_numpy(rng.integers(-64, 65, M) / 16.0).float().cuda() if bias else None
+    res = _ints(rng, B, M, dtype) if residual else None
+    if strided and res is not None:
+        res = _place(res, 5, 2)
+    z, y, _ = lc.forward(w.W, x.double(), a.double(), None if b is None else b.double(), act,
+                         None if res is None else res.double())
+    got, pre = w.linear(x, row_scale=a, bias=b, act=act, residual=res, pre=True)
+    torch.cuda.synchronize()
+    assert torch.equal(pre, z.to(dtype))
+    assert torch.equal(got, y.to(dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_linear_exact(oracle_lib, shape, dtype):
+    import oracle
+    L, k, V, T, M, N = shape
+    rng = np.random.default_rng(M * 31 + N)
+    w = Coded(M + N, M, N, L, k, V, T, dtype, True, oracle)
+    for B in (1, 2, 7, 16, 33, 100, 129):
+        _say(f"linear exact {shape} {dtype} B={B}")
+        for strided in (False, True):
+            x = _ints(rng, B, N, dtype)
+            x = _place(x, 9, 3) if strided else x
+            _exact_forward(w, x, rng, dtype, "relu" if B % 2 else "none", strided, strided)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("L,k,V,T,M,N,B", [
+    (16, 2, 1, 256, 2048, 2048, 1), (16, 2, 2, 256, 14336, 4096, 3),
+    (16, 3, 1, 256, 4096, 14336, 17), (16, 2, 1, 256, 4096, 4096, 500),
+    (16, 2, 1, 256, 4100, 4096, 2049), (12, 2, 1, 64, 1031, 4160, 1027)])
+def test_linear_exact_large(L, k, V, T, M, N, B, dtype):
+    _say(f"linear exact large L={L} k={k} V={V} M={M} N={N} B={B} {dtype}")
+    rng = np.random.default_rng(B)
+    w = Coded(B, M, N, L, k, V, T, dtype, True)
+    _exact_forward(w, _ints(rng, B, N, dtype), rng, dtype, "none", True, False)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("shape,B", [(SHAPES[0], 5), (SHAPES[1], 64), (SHAPES[2], 200),
+                                     (SHAPES[6], 3)])
+def test_linear_within_bounds(oracle_lib, shape, B, act, dtype):
+    import oracle
+    L, k, V, T, M, N = shape
+    _say(f"linear bounds {shape} B={B} {act} {dtype}")
+    rng = np.random.default_rng(N + B)
+    w = Coded(N, M, N, L, k, V, T, dtype, False, oracle)
+
+    def normal(*size):
+        return torch.from_numpy(rng.standard_normal(size)).to(dtype).cuda()
+    x, res = normal(B, N), normal(B, M)
+    a = torch.from_numpy(rng.standard_normal(M) / np.sqrt(N)).float().cuda()
+    b = torch.from_numpy(rng.standard_normal(M)).float().cuda()
+    y, z = w.linear(x, row_scale=a, bias=b, act=act, residual=res, pre=True)
+    torch.cuda.synchronize()
+    ez, ey, mag = lc.forward(w.W, x.double(), a.double(), b.double(), act, res.double())
+    dz, dy = lc.forward_bounds(ez, ey, mag, res, act, N, dtype)
+    rz, ry = float(((z.double() - ez).abs() / dz).max()), float(((y.double() - ey).abs() / dy).max())
+    _say(f"  worst error / bound: z {rz:.3g}, y {ry:.3g}")
+    assert rz <= 1 and ry <= 1
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("B", [1, 5, 40, 300])
+def test_linear_rows_are_their_own(dtype, B):
+    """A NaN or an infinity in a row of x reaches that row alone, padding is not read, and
+    nothing outside the output is written; in place of the residual too."""
+    L, k, V, T, M, N = 16, 2, 1, 256, 150, 512
+    _say(f"linear rows {dtype} B={B}")
+    rng = np.random.default_rng(B)
+    w = Coded(B, M, N, L, k, V, T, dtype, True)
+    x = _place(_ints(rng, B, N, dtype), 8, 0)
+    want = (x.double() @ w.W.t())
+    bad = B // 2
+    x[bad, N - 1] = float("inf") if B % 2 else float("nan")
+    buf = torch.full((B + 2, M + 6), 7.0, dtype=dtype, device="cuda")
+    out = buf[1:B + 1, 2:M + 2]
+    res = _ints(rng, B, M, dtype)
+    out.copy_(res)
+    y = w.linear(x, residual=out, out=out)
+    torch.cuda.synchronize()
+    assert y.data_ptr() == out.data_ptr()
+    keep = torch.arange(B, device="cuda") != bad
+    assert torch.equal(y[keep], (want + res.double())[keep].to(dtype))
+    col = w.W[:, N - 1]
+    hit = y[bad][col != 0]
+    assert not bool(torch.isfinite(hit).any())
+    buf[1:B + 1, 2:M + 2] = 7.0
+    assert bool((buf == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_linear_empty(dtype):
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    C = torch.zeros(1 << 16, 1, dtype=dtype, device="cuda")
+    for M, N, B in [(3, 0, 4), (3, 512, 0), (0, 512, 4), (0, 0, 0)]:
+        nb = M * (N // 256)
+        bits = torch.zeros(nb, 16, dtype=torch.int32, device="cuda")
+        s0 = torch.zeros(nb, dtype=torch.int32, device="cuda")
+        b = torch.arange(M, device="cuda", dtype=torch.float32)
+        x = torch.ones(B, N, dtype=dtype, device="cuda")
+        y = api.decode_linear(bits, s0, C, x, M, N, 16, 2, 1, 256, bias=b)
+        assert y.shape == (B, M)
+        if M and B and N == 0:
+            assert torch.equal(y, b.to(dtype).expand(B, M))
+        p = api.act_pack(x)
+        dx, dw, db = api.decode_linear_backward(bits, s0, C, torch.ones(B, M, dtype=dtype,
+                                                                        device="cuda"), M, N,
+                                                16, 2, 1, 256, x=p)
+        assert dx.shape == (B, N) and dw.shape == (M, N)
+        assert torch.equal(dx, torch.zeros_like(dx)) and torch.equal(db, torch.full_like(db, B))
+        if B == 0:
+            assert torch.equal(dw, torch.zeros_like(dw))
+    assert e.numel() == 0
+
+
+def _grad_reference(w, dy, a, act, z, x, dtype, rounded):
+    """float64 gradients from the checkpoints' values; s rounded to the layer's type when
+    `rounded`."""
+    g = dy.double()
+    if act != "none":
+        g = g * lc.slope(z, act)
+    s = g if a is None else g * a.double()
+    if rounded:
+        s = s.to(dtype).double()
+    return g, s, s @ w.W, s.t() @ x
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_backward_exact(oracle_lib, shape, dtype):
+    import oracle
+    L, k, V, T, M, N = shape
+    rng = np.random.default_rng(M * 17 + N)
+    w = Coded(M * 3 + N, M, N, L, k, V, T, dtype, True, oracle)
+    for B, act in [(1, "none"), (2, "relu"), (19, "relu"), (64, "none"), (131, "relu")]:
+        _say(f"backward exact {shape} {dtype} B={B} {act}")
+        dy = _place(_ints(rng, B, M, dtype, 4), 5, 1) if B != 64 else _ints(rng, B, M, dtype, 4)
+        a = torch.from_numpy(2.0 ** rng.integers(-1, 2, M)).float().cuda()
+        zp = api.act_pack(_ints(rng, B, M, dtype))
+        xp = api.act_pack(_ints(rng, B, N, dtype))
+        z, x = api.act_unpack(zp, torch.float32).double(), api.act_unpack(xp, torch.float32).double()
+        g, s, gx, gw = _grad_reference(w, dy, a, act, z, x, dtype, False)
+        dx, dw, db = w.backward(dy, row_scale=a, act=act, z=zp, x=xp)
+        torch.cuda.synchronize()
+        assert torch.equal(db.double(), g.sum(0))
+        assert torch.equal(dx, gx.to(dtype))
+        assert torch.equal(dw, gw.to(dtype))
+        # each alone gives the same
+        only = w.backward(dy, row_scale=a, act=act, z=zp, dbias=False)
+        assert only[1] is None and only[2] is None and torch.equal(only[0], dx)
+        only = w.backward(dy, row_scale=a, act=act, z=zp, x=xp, dx=False, dbias=False)
+        assert only[0] is None and torch.equal(only[1], dw)
+        only = w.backward(dy, row_scale=a, act=act, z=zp, dx=False)
+        assert only[0] is None and only[1] is None and torch.equal(only[2], db)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("L,k,V,T,M,N,B", [
+    (16, 2, 1, 256, 2048, 2048, 509), (16, 2, 2, 256, 4096, 1024, 2048),
+    (16, 3, 1, 256, 1031, 4096, 1025)])
+def test_backward_exact_large(L, k, V, T, M, N, B, dtype):
+    _say(f"backward exact large M={M} N={N} B={B} {dtype}")
+    rng = np.random.default_rng(B)
+    w = Coded(B, M, N, L, k, V, T, dtype, True)
+    dy = _ints(rng, B, M, dtype, 2)
+    zp, xp = api.act_pack(_ints(rng, B, M, dtype)), api.act_pack(_ints(rng, B, N, dtype))
+    z, x = api.act_unpack(zp, torch.float32).double(), api.act_unpack(xp, torch.float32).double()
+    g, s, gx, gw = _grad_reference(w, dy, None, "relu", z, x, dtype, False)
+    dx, dw, db = w.backward(dy, act="relu", z=zp, x=xp)
+    torch.cuda.synchronize()
+    assert torch.equal(db.double(), g.sum(0))
+    assert torch.equal(dx, gx.to(dtype))
+    assert torch.equal(dw, gw.to(dtype))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("shape,B", [(SHAPES[0], 37), (SHAPES[1], 128), (SHAPES[6], 9)])
+def test_backward_within_bounds(oracle_lib, shape, B, act, dtype):
+    import oracle
+    L, k, V, T, M, N = shape
+    _say(f"backward bounds {shape} B={B} {act} {dtype}")
+    rng = np.random.default_rng(N + B)
+    w = Coded(N, M, N, L, k, V, T, dtype, False, oracle)
+
+    def normal(*size):
+        return torch.from_numpy(rng.standard_normal(size)).to(dtype).cuda()
+    dy = normal(B, M)
+    a = torch.from_numpy(rng.standard_normal(M) / np.sqrt(N)).float().cuda()
+    zp, xp = api.act_pack(normal(B, M)), api.act_pack(normal(B, N))
+    z, x = api.act_unpack(zp, torch.float32).double(), api.act_unpack(xp, torch.float32).double()
+    # x as the product reads it: rounded to the type (exact but for fp16 values of codes
+    # packed from other types, which do not occur here)
+    g, s, gx, gw = _grad_reference(w, dy, a, act, z, x, dtype, False)
+    dx, dw, db = w.backward(dy, row_scale=a, act=act, z=zp, x=xp)
+    torch.cuda.synchronize()
+    eg = dy.double().abs() * lc.slope_error(z, act) + 2 * lc.U * g.abs()
+    es = eg * a.double().abs() + 2 * lc.U * s.abs()
+    es = es + lc.half(dtype) * (s.abs() + es) + lc.tiny(dtype)
+    bdb = eg.sum(0) + lc.gamma(B) * (g.abs() + eg).sum(0)
+    bdx = es @ w.W.abs() + lc.gamma(M) * ((s.abs() + es) @ w.W.abs())
+    bdx = bdx + lc.half(dtype) * (gx.abs() + bdx) + lc.tiny(dtype)
+    bdw = es.t() @ x.abs() + lc.gamma(B) * ((s.abs() + es).t() @ x.abs())
+    bdw = bdw + lc.half(dtype) * (gw.abs() + bdw) + lc.tiny(dtype)
+    r = [float(((got.double() - want).abs() / lim).max())
+         for got, want, lim in ((db, g.sum(0), bdb), (dx, gx, bdx), (dw, gw, bdw))]
+    _say(f"  worst error / bound: dbias {r[0]:.3g}, dx {r[1]:.3g}, dw {r[2]:.3g}")
+    assert max(r) <= 1
+
+
+def test_gradients_against_differences():
+    """fp32: the gradients of sum(y G) in x, W_hat and bias against central differences of
+    the float64 layer.  x is a small integer, which its checkpoint holds exactly; z is not
+    (|z| > 127/32 in units of 1/32), so the layer that is differentiated has a constant
+    added to z that moves it onto the checkpoint's value, where the slope is taken."""
+    L, k, V, T, M, N, B = 8, 2, 1, 16, 6, 16, 3
+    rng = np.random.default_rng(8)
+    dt = torch.float32
+    w = Coded(1, M, N, L, k, V, T, dt, True)
+    x = _ints(rng, B, N, dt, 1)
+    bias = torch.from_numpy(rng.integers(-8, 9, M) / 8.0).float().cuda()
+    a = torch.full((M,), 0.25, device="cuda")
+    G = torch.from_numpy(rng.standard_normal((B, M))).to(dt).cuda()
+    for act in ("silu", "gelu"):
+        z = (x.double() @ w.W.t()) * 0.25 + bias.double()
+        _, pre = w.linear(x, row_scale=a, bias=bias, act=act, pre=True)
+        assert torch.equal(pre.double(), z)
+        zp, xp = api.act_pack(pre), api.act_pack(x)
+        assert torch.equal(api.act_unpack(xp, dt), x)
+        shift = api.act_unpack(zp, dt).double() - z
+        assert float(shift.abs().max()) <= 1 / 32  # half a step of 1/16
+        dx, dw, db = w.backward(G, row_scale=a, act=act, z=zp, x=xp)
+
+        def loss(xx, ww, bb):
+            return float((lc.act((xx @ ww.t()) * 0.25 + bb + shift, act) * G.double()).sum())
+        h = 1e-4
+        args = [x.double(), w.W.clone(), bias.double()]
+        for n, grad in ((0, dx), (1, dw), (2, db)):
+            for _ in range(6):
+                at = tuple(rng.integers(0, d) for d in args[n].shape)
+                lo, hi = [t.clone() for t in args], [t.clone() for t in args]
+                lo[n][at] -= h
+                hi[n][at] += h
+                diff = (loss(*hi) - loss(*lo)) / (2 * h)
+                # third derivative of the loss along one argument: |act'''| <= 2, |x| and
+                # |W| at most 4, sums of B M terms of |G| below 4
+                trunc = h * h / 6 * 2 * 4 ** 3 * B * M * 4
+                assert abs(float(grad[at]) - diff) <= trunc + 1e-5 * max(1, abs(diff)) * 4
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_encode_then_train_step(dtype):
+    """The pieces as they are used together: a weight matrix is encoded with the layer's
+    table, the layer runs forward keeping z, z and x are packed, the backward pass reads
+    them; against the same step in float64 from the decoded matrix."""
+    L, k, V, T, M, N, B = 16, 2, 1, 256, 24, 512, 48
+    _say(f"encode and train step {dtype}")
+    W, _ = wl.random_small(3, M, N, False)
+    table = api.make_codebook(L, V, 3001).to(dtype)
+    Wn = torch.from_numpy(W).cuda()
+    a, _, _ = api.scale_field(Wn, normalized=False)
+    enc = api.encode(Wn / a[:, None], None, table.float(), L, k, V, T, recon=True)
+    w = Coded.__new__(Coded)
+    w.shape, w.bits, w.s0, w.table = (M, N, L, k, V, T), enc.bitstream, enc.start_state, table
+    w.W = enc.recon.double()
+    rng = np.random.default_rng(6)
+    x = torch.from_numpy(rng.standard_normal((B, N))).to(dtype).cuda()
+    bias = torch.from_numpy(rng.standard_normal(M)).float().cuda()
+    y, pre = w.linear(x, row_scale=a, bias=bias, act="gelu", pre=True)
+    zp, xp = api.act_pack(pre), api.act_pack(x)
+    del pre
+    dy = (y.float() * 0.5).to(dtype)
+    dx, dw, db = w.backward(dy, row_scale=a, act="gelu", z=zp, x=xp)
+    torch.cuda.synchronize()
+    ez, ey, mag = lc.forward(w.W, x.double(), a.double(), bias.double(), "gelu", None)
+    _, lim = lc.forward_bounds(ez, ey, mag, None, "gelu", N, dtype)
+    assert bool(((y.double() - ey).abs() <= lim).all())
+    z = api.act_unpack(zp, torch.float32).double()
+    # the checkpoint of z is within one step of z, itself rounded to the type
+    step = torch.ldexp(torch.ones_like(zp.scale, dtype=torch.float64), zp.scale.int() - 133)
+    step = step.repeat_interleave(32, 1)[:, :M]
+    dz, _ = lc.forward_bounds(ez, ey, mag, None, "gelu", N, dtype)
+    assert bool(((z - ez).abs() <= step + dz).all())
+    xv = api.act_unpack(xp, torch.float32).double()
+    g, s, gx, gw = _grad_reference(w, dy, a, "gelu", z, xv, dtype, False)
+    u = 4 * lc.half(dtype) + 64 * lc.U
+    assert bool(((db.double() - g.sum(0)).abs() <= 64 * lc.U * g.abs().sum(0) + 1e-12).all())
+    assert bool(((dx.double() - gx).abs() <= u * (s.abs() @ w.W.abs()) + 1e-6).all())
+    assert bool(((dw.double() - gw).abs() <= u * (s.abs().t() @ xv.abs()) + 1e-6).all())
+
+
+@pytest.mark.parametrize("B", [1, 20, 700])
+def test_stream_and_repeats(B):
+    """On another stream, and twice: the same bits."""
+    dtype = torch.bfloat16
+    w = Coded(2, 512, 1024, 16, 2, 1, 256, dtype, False)
+    rng = np.random.default_rng(B)
+    x = torch.from_numpy(rng.standard_normal((B, 1024))).to(dtype).cuda()
+    dy = torch.from_numpy(rng.standard_normal((B, 512))).to(dtype).cuda()
+    xp, zp = api.act_pack(x), api.act_pack(dy)
+
+    def once():
+        return [w.linear(x, act="silu"), *w.backward(dy, act="silu", z=zp, x=xp)]
+    first = once()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        second = once()
+    s.synchronize()
+    third = once()
+    torch.cuda.synchronize()
+    for p, q, r in zip(first, second, third):
+        assert torch.equal(p, q) and torch.equal(p, r)
+
+
+@pytest.mark.parametrize("B", [1, 24, 520])
+def test_captured_and_replayed(B):
+    """Two captured graphs, each with its own workspace, replayed in turn with eager calls
+    between: every replay equals the eager result on the inputs of the moment."""
+    dtype = torch.bfloat16
+    M, N = 384, 1024
+    w = Coded(4, M, N, 16, 2, 1, 256, dtype, False)
+    g = torch.Generator("cuda").manual_seed(B)
+    x = torch.randn(B, N, generator=g, device="cuda").to(dtype)
+    dy = torch.randn(B, M, generator=g, device="cuda").to(dtype)
+
+    def both():
+        y, z = w.linear(x, act="gelu", pre=True)
+        zp, xp = api.act_pack(z), api.act_pack(x)
+        return [y, *w.backward(dy, act="gelu", z=zp, x=xp)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        both()
+    side.synchronize()
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = both()
+        graphs.append((graph, outs))
+    for turn in range(3):
+        x.copy_(torch.randn(B, N, generator=g, device="cuda"))
+        want = both()
+        torch.cuda.synchronize()
+        for graph, outs in graphs:
+            for o in outs:
+                o.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            for p, q in zip(outs, want):
+                assert torch.equal(p, q), f"turn {turn}"
+            both()
+            torch.cuda.synchronize()
+
+
+def test_given_workspace_and_refusals():
+    dtype = torch.float16
+    M, N, B = 64, 512, 300
+    w = Coded(5, M, N, 16, 2, 1, 256, dtype, True)
+    x = _ints(np.random.default_rng(0), B, N, dtype)
+    need = _lib.tcq_decode_linear_workspace_bytes(_lib.TCQ_F16, B, *w.shape)
+    y = w.linear(x, workspace=api.Workspace(need))
+    assert torch.equal(y, (x.double() @ w.W.t()).to(dtype))
+    if need:
+        with pytest.raises(_lib.TcqError) as e:
+            w.linear(x, workspace=api.Workspace(need - 1))
+        assert e.value.status == _lib.TCQ_EWORKSPACE
+    with pytest.raises(AssertionError):
+        w.linear(x.float())                       # codebook of another type
+    with pytest.raises(AssertionError):
+        w.linear(x.t())                           # columns contiguous
+    with pytest.raises(AssertionError):
+        w.linear(x, bias=torch.zeros(M, device="cuda", dtype=dtype))
+    with pytest.raises(KeyError):
+        w.linear(x, act="tanh")
+    with pytest.raises(AssertionError):
+        w.backward(x[:, :M].contiguous(), act="gelu")   # no checkpoint of z
+    with pytest.raises(AssertionError):
+        w.backward(x[:, :M].contiguous(), dx=False, dbias=False)

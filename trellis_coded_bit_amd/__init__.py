@@ -16,6 +16,12 @@ from ._lib import (  # noqa: F401
     tcq_hadamard,
     tcq_scale_field_workspace_bytes,
     tcq_scale_field,
+    tcq_decode_linear_workspace_bytes,
+    tcq_decode_linear,
+    tcq_act_pack,
+    tcq_act_unpack,
+    tcq_decode_linear_backward_workspace_bytes,
+    tcq_decode_linear_backward,
     tcq_encode,
     tcq_encode_timed,
     tcq_encode_workspace_bytes,

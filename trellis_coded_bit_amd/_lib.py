@@ -21,12 +21,19 @@ TCQ_EWORKSPACE = -3
 TCQ_EHIP = -4
 TCQ_ENOMEM = -5
 
+# tcq_dtype and tcq_act
+TCQ_F32, TCQ_F16, TCQ_BF16 = 0, 1, 2
+TCQ_ACT_NONE, TCQ_ACT_RELU, TCQ_ACT_SILU, TCQ_ACT_GELU = 0, 1, 2, 3
+
 EXPORTED = ("tcq_version", "tcq_last_error", "tcq_make_codebook",
             "tcq_encode_workspace_bytes", "tcq_encode_workspace_min_bytes", "tcq_encode",
             "tcq_encode_timed", "tcq_encode_noalloc", "tcq_decode", "tcq_decode_gemv",
             "tcq_ldlq_workspace_bytes", "tcq_encode_ldlq", "tcq_bcjr_workspace_bytes",
             "tcq_bcjr", "tcq_hadamard", "tcq_scale_field_workspace_bytes", "tcq_scale_field",
-            "tcq_l16_stream_probe_bytes", "tcq_l16_stream_probe")
+            "tcq_l16_stream_probe_bytes", "tcq_l16_stream_probe",
+            "tcq_decode_linear_workspace_bytes", "tcq_decode_linear", "tcq_act_pack",
+            "tcq_act_unpack", "tcq_decode_linear_backward_workspace_bytes",
+            "tcq_decode_linear_backward")
 
 _lib = None
 
@@ -92,6 +99,23 @@ def load():
     lib.tcq_scale_field_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_size_t)]
     lib.tcq_scale_field.restype = i32
     lib.tcq_scale_field.argtypes = [vp, i64, i64, i64, vp, vp, vp, i64, vp, sz, vp]
+    shape = [i64, i64, i32, i32, i32, i32]  # M, N, L, k, V, T
+    lib.tcq_decode_linear_workspace_bytes.restype = i32
+    lib.tcq_decode_linear_workspace_bytes.argtypes = [i32, i64, *shape, ctypes.POINTER(sz)]
+    lib.tcq_decode_linear.restype = i32
+    lib.tcq_decode_linear.argtypes = [vp, vp, vp, *shape, i32, vp, i64, i64, vp, vp, i32, vp,
+                                      i64, vp, i64, vp, i64, vp, sz, vp]
+    lib.tcq_act_pack.restype = i32
+    lib.tcq_act_pack.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp]
+    lib.tcq_act_unpack.restype = i32
+    lib.tcq_act_unpack.argtypes = [vp, i64, vp, i64, i64, i32, vp, i64, vp]
+    lib.tcq_decode_linear_backward_workspace_bytes.restype = i32
+    lib.tcq_decode_linear_backward_workspace_bytes.argtypes = [i32, i64, *shape, i32, i32, i32,
+                                                               ctypes.POINTER(sz)]
+    lib.tcq_decode_linear_backward.restype = i32
+    lib.tcq_decode_linear_backward.argtypes = [vp, vp, vp, *shape, i32, vp, i64, i64, vp, i32,
+                                               vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp,
+                                               vp, sz, vp]
     _lib = lib
     return lib
 
@@ -238,3 +262,65 @@ def tcq_scale_field(W: int, M: int, N: int, ldw: int, row_scale: int, col_scale:
     _check("tcq_scale_field",
            load().tcq_scale_field(W, M, N, ldw, row_scale, col_scale, Wn or None, ldn,
                                   workspace, workspace_bytes, stream or None))
+
+
+def tcq_decode_linear_workspace_bytes(dtype: int, B: int, M: int, N: int, L: int, k: int,
+                                      V: int, T: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check("tcq_decode_linear_workspace_bytes",
+           load().tcq_decode_linear_workspace_bytes(dtype, B, M, N, L, k, V, T,
+                                                    ctypes.byref(b)))
+    return int(b.value)
+
+
+def tcq_decode_linear(bitstream: int, start_state: int, codebook: int, M: int, N: int, L: int,
+                      k: int, V: int, T: int, dtype: int, x: int, B: int, ldx: int,
+                      row_scale: int | None, bias: int | None, act: int,
+                      residual: int | None, ldr: int, y: int, ldy: int, pre: int | None,
+                      ldp: int, workspace: int | None, workspace_bytes: int,
+                      stream: int | None) -> None:
+    _check("tcq_decode_linear",
+           load().tcq_decode_linear(bitstream, start_state, codebook, M, N, L, k, V, T, dtype,
+                                    x, B, ldx, row_scale or None, bias or None, act,
+                                    residual or None, ldr, y, ldy, pre or None, ldp,
+                                    workspace or None, workspace_bytes, stream or None))
+
+
+def tcq_act_pack(X: int, dtype: int, rows: int, cols: int, ldx: int, codes: int, ldq: int,
+                 scale: int, stream: int | None) -> None:
+    _check("tcq_act_pack",
+           load().tcq_act_pack(X, dtype, rows, cols, ldx, codes, ldq, scale, stream or None))
+
+
+def tcq_act_unpack(codes: int, ldq: int, scale: int, rows: int, cols: int, dtype: int,
+                   out: int, ldo: int, stream: int | None) -> None:
+    _check("tcq_act_unpack",
+           load().tcq_act_unpack(codes, ldq, scale, rows, cols, dtype, out, ldo,
+                                 stream or None))
+
+
+def tcq_decode_linear_backward_workspace_bytes(dtype: int, B: int, M: int, N: int, L: int,
+                                               k: int, V: int, T: int, dx: bool, dw: bool,
+                                               dbias: bool) -> int:
+    b = ctypes.c_size_t(0)
+    _check("tcq_decode_linear_backward_workspace_bytes",
+           load().tcq_decode_linear_backward_workspace_bytes(
+               dtype, B, M, N, L, k, V, T, int(dx), int(dw), int(dbias), ctypes.byref(b)))
+    return int(b.value)
+
+
+def tcq_decode_linear_backward(bitstream: int | None, start_state: int | None,
+                               codebook: int | None, M: int, N: int, L: int, k: int, V: int,
+                               T: int, dtype: int, dy: int, B: int, lddy: int,
+                               row_scale: int | None, act: int, z_codes: int | None, ldz: int,
+                               z_scale: int | None, x_codes: int | None, ldx: int,
+                               x_scale: int | None, dx: int | None, lddx: int, dw: int | None,
+                               lddw: int, dbias: int | None, workspace: int | None,
+                               workspace_bytes: int, stream: int | None) -> None:
+    _check("tcq_decode_linear_backward",
+           load().tcq_decode_linear_backward(
+               bitstream or None, start_state or None, codebook or None, M, N, L, k, V, T,
+               dtype, dy, B, lddy, row_scale or None, act, z_codes or None, ldz,
+               z_scale or None, x_codes or None, ldx, x_scale or None, dx or None, lddx,
+               dw or None, lddw, dbias or None, workspace or None, workspace_bytes,
+               stream or None))

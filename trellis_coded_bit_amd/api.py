@@ -2,6 +2,7 @@
 addresses and the current stream to libtcq.  No arithmetic happens here."""
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import torch
@@ -165,3 +166,178 @@ def scale_field(W: torch.Tensor, normalized: bool = True
     _lib.tcq_scale_field(W.data_ptr(), M, N, W.stride(0), a.data_ptr(), b.data_ptr(),
                          None if Wn is None else Wn.data_ptr(), N, ws.ptr, ws.nbytes, _stream())
     return a, b, Wn
+
+
+_DTYPES = {torch.float32: _lib.TCQ_F32, torch.float16: _lib.TCQ_F16,
+           torch.bfloat16: _lib.TCQ_BF16}
+_ACTS = {"none": _lib.TCQ_ACT_NONE, "relu": _lib.TCQ_ACT_RELU, "silu": _lib.TCQ_ACT_SILU,
+         "gelu": _lib.TCQ_ACT_GELU}
+CHECKPOINT_GROUP = 32  # consecutive values of a row that share a scale byte
+
+
+def _on(device: torch.device):
+    """The tensors' device made current, where it is not: the launch and the stream are
+    its own."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return nullcontext()
+    return torch.cuda.device(device)
+
+
+def _rows(t: torch.Tensor, name: str, rows: int, cols: int, dtype: torch.dtype,
+          device: torch.device) -> int:
+    """Checks a rows x cols matrix whose rows are contiguous; its leading dimension."""
+    assert t.device == device and t.dtype == dtype, f"{name}: {dtype} on {device}"
+    assert t.shape == (rows, cols), f"{name}: shape {tuple(t.shape)}, not {(rows, cols)}"
+    # a dimension of at most one element may carry any stride
+    assert cols <= 1 or t.stride(1) == 1, f"{name}: rows must be contiguous"
+    ld = t.stride(0) if rows > 1 else cols
+    assert ld >= cols, f"{name}: rows overlap"
+    return max(ld, 1)
+
+
+def _vector(t: torch.Tensor | None, name: str, n: int, device: torch.device) -> int | None:
+    if t is None:
+        return None
+    assert t.device == device and t.dtype == torch.float32 and t.is_contiguous() and \
+        t.numel() == n, f"{name}: {n} contiguous float32 values on {device}"
+    return t.data_ptr()
+
+
+def _coded(bitstream: torch.Tensor, start_state: torch.Tensor, codebook: torch.Tensor, M: int,
+           N: int, L: int, k: int, V: int, T: int, dtype: torch.dtype,
+           device: torch.device) -> None:
+    blocks = M * (N // T)
+    assert bitstream.device == device and bitstream.is_contiguous() and \
+        bitstream.element_size() == 4 and bitstream.numel() == blocks * nwords(k, T)
+    assert start_state.device == device and start_state.is_contiguous() and \
+        start_state.element_size() == 4 and start_state.numel() == blocks
+    assert codebook.device == device and codebook.dtype == dtype and \
+        codebook.is_contiguous() and codebook.numel() == V << L, \
+        f"codebook: {V << L} contiguous values of the layer's type {dtype}"
+
+
+def decode_linear(bitstream: torch.Tensor, start_state: torch.Tensor, codebook: torch.Tensor,
+                  x: torch.Tensor, M: int, N: int, L: int, k: int, V: int, T: int,
+                  row_scale: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                  act: str = "none", residual: torch.Tensor | None = None, pre: bool = False,
+                  out: torch.Tensor | None = None, workspace: Workspace | None = None
+                  ) -> torch.Tensor | tuple[torch.Tensor, torch.Tensor]:
+    """act(row_scale (x W_hat^T) + bias) + residual for x [B, N] in float32, float16 or
+    bfloat16 and the coded matrix W_hat [M, N] (codebook in x's type); [B, M], or with
+    ``pre`` the pair of it and the pre-activation.  act: none, relu, silu or gelu.  ``out``
+    may be ``residual``."""
+    dev, dt = x.device, x.dtype
+    assert x.is_cuda and x.dim() == 2 and dt in _DTYPES
+    B = x.shape[0]
+    ldx = _rows(x, "x", B, N, dt, dev)
+    _coded(bitstream, start_state, codebook, M, N, L, k, V, T, dt, dev)
+    a, b = _vector(row_scale, "row_scale", M, dev), _vector(bias, "bias", M, dev)
+    with _on(dev):
+        y = torch.empty((B, M), dtype=dt, device=dev) if out is None else out
+        ldy = M if out is None else _rows(out, "out", B, M, dt, dev)
+        z = torch.empty((B, M), dtype=dt, device=dev) if pre else None
+        if workspace is None:
+            n = _lib.tcq_decode_linear_workspace_bytes(_DTYPES[dt], B, M, N, L, k, V, T)
+            workspace = Workspace(n, dev) if n else None
+        _lib.tcq_decode_linear(
+            bitstream.data_ptr(), start_state.data_ptr(), codebook.data_ptr(), M, N, L, k, V, T,
+            _DTYPES[dt], x.data_ptr(), B, ldx, a, b, _ACTS[act],
+            None if residual is None else residual.data_ptr(),
+            M if residual is None else _rows(residual, "residual", B, M, dt, dev),
+            y.data_ptr(), ldy, None if z is None else z.data_ptr(), M,
+            None if workspace is None else workspace.ptr,
+            0 if workspace is None else workspace.nbytes, _stream())
+    return y if z is None else (y, z)
+
+
+@dataclass
+class Packed:
+    """An 8-bit checkpoint of a matrix [rows, cols] (see tcq_act_pack)."""
+    codes: torch.Tensor  # int8 [rows, cols], rows contiguous
+    scale: torch.Tensor  # uint8 [rows, ceil(cols / 32)]
+
+    def check(self, name: str, rows: int, cols: int, device: torch.device) -> int:
+        groups = -(-cols // CHECKPOINT_GROUP)
+        assert self.scale.device == device and self.scale.dtype == torch.uint8 and \
+            self.scale.shape == (rows, groups) and self.scale.is_contiguous(), \
+            f"{name}: scale bytes [{rows}, {groups}]"
+        return _rows(self.codes, name, rows, cols, torch.int8, device)
+
+
+def act_pack(x: torch.Tensor) -> Packed:
+    """8-bit checkpoint of x [rows, cols] (float32, float16 or bfloat16)."""
+    assert x.is_cuda and x.dim() == 2 and x.dtype in _DTYPES
+    rows, cols = x.shape
+    ldx = _rows(x, "x", rows, cols, x.dtype, x.device)
+    groups = -(-cols // CHECKPOINT_GROUP)
+    with _on(x.device):
+        # rows start on whole groups
+        ldq = groups * CHECKPOINT_GROUP
+        codes = torch.empty((rows, ldq), dtype=torch.int8, device=x.device)[:, :cols]
+        scale = torch.empty((rows, groups), dtype=torch.uint8, device=x.device)
+        _lib.tcq_act_pack(x.data_ptr(), _DTYPES[x.dtype], rows, cols, ldx, codes.data_ptr(),
+                          max(ldq, 1), scale.data_ptr(), _stream())
+    return Packed(codes, scale)
+
+
+def act_unpack(packed: Packed, dtype: torch.dtype) -> torch.Tensor:
+    """The values a checkpoint stands for, [rows, cols] in float32, float16 or bfloat16."""
+    assert packed.codes.is_cuda and packed.codes.dim() == 2 and dtype in _DTYPES
+    rows, cols = packed.codes.shape
+    dev = packed.codes.device
+    ldq = packed.check("codes", rows, cols, dev)
+    with _on(dev):
+        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+        _lib.tcq_act_unpack(packed.codes.data_ptr(), ldq, packed.scale.data_ptr(), rows, cols,
+                            _DTYPES[dtype], out.data_ptr(), max(cols, 1), _stream())
+    return out
+
+
+def decode_linear_backward(bitstream: torch.Tensor, start_state: torch.Tensor,
+                           codebook: torch.Tensor, dy: torch.Tensor, M: int, N: int, L: int,
+                           k: int, V: int, T: int, row_scale: torch.Tensor | None = None,
+                           act: str = "none", z: Packed | None = None, x: Packed | None = None,
+                           dx: bool = True, dbias: bool = True,
+                           workspace: Workspace | None = None
+                           ) -> tuple[torch.Tensor | None, torch.Tensor | None,
+                                      torch.Tensor | None]:
+    """Gradients (dx [B, N], dw [M, N], dbias [M]) of decode_linear from dy [B, M] and the
+    checkpoints z of the pre-activation (needed unless act is "none") and x of the input
+    (dw is computed where it is given).  dw is the gradient of W_hat; the residual's
+    gradient is dy."""
+    dev, dt = dy.device, dy.dtype
+    assert dy.is_cuda and dy.dim() == 2 and dt in _DTYPES
+    assert dx or dbias or x is not None, "no gradient is wanted"
+    B = dy.shape[0]
+    lddy = _rows(dy, "dy", B, M, dt, dev)
+    if dx:
+        _coded(bitstream, start_state, codebook, M, N, L, k, V, T, dt, dev)
+    a = _vector(row_scale, "row_scale", M, dev)
+    assert act == "none" or z is not None, "the slope of act needs the checkpoint of z"
+    ldz = z.check("z", B, M, dev) if act != "none" else M
+    ldx = x.check("x", B, N, dev) if x is not None else N
+    with _on(dev):
+        gx = torch.empty((B, N), dtype=dt, device=dev) if dx else None
+        gw = torch.empty((M, N), dtype=dt, device=dev) if x is not None else None
+        gb = torch.empty(M, dtype=torch.float32, device=dev) if dbias else None
+        if workspace is None:
+            n = _lib.tcq_decode_linear_backward_workspace_bytes(
+                _DTYPES[dt], B, M, N, L, k, V, T, dx, x is not None, dbias)
+            workspace = Workspace(n, dev) if n else None
+        # an output of no elements has no address and nothing to be written
+        empty = (gx is None or gx.numel() == 0) and (gw is None or gw.numel() == 0) and \
+            (gb is None or gb.numel() == 0)
+        if not empty:
+            _lib.tcq_decode_linear_backward(
+                bitstream.data_ptr() if dx else None, start_state.data_ptr() if dx else None,
+                codebook.data_ptr() if dx else None, M, N, L, k, V, T, _DTYPES[dt],
+                dy.data_ptr(), B, lddy, a, _ACTS[act],
+                z.codes.data_ptr() if act != "none" else None, ldz,
+                z.scale.data_ptr() if act != "none" else None,
+                x.codes.data_ptr() if x is not None else None, ldx,
+                x.scale.data_ptr() if x is not None else None,
+                None if gx is None else gx.data_ptr(), N, None if gw is None else gw.data_ptr(),
+                N, None if gb is None else gb.data_ptr(),
+                None if workspace is None else workspace.ptr,
+                0 if workspace is None else workspace.nbytes, _stream())
+    return gx, gw, gb

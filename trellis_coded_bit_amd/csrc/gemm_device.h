@@ -1,0 +1,350 @@
+// Tiled matrix product of the coded linear layer on the matrix cores (device code).
+//
+//   D[i][j] = sum_k A(i, k) B(j, k),      i < I, j < J
+//
+// for operands of one type (float, _Float16 or __bf16) whose products are summed in fp32.
+// Each operand is stored either with k contiguous (X[row][k], "row-major in k") or with its
+// rows contiguous (X[k][row], "k-major"); the forward product, the input's gradient and
+// the matrix's gradient are the three combinations, so no operand is transposed in memory.
+//
+// A workgroup computes a TI x TJ tile of D over K steps of 128 bytes per row (64 16-bit or
+// 32 fp32 values).  Both operand tiles of a step go from global memory straight into LDS
+// (buffer_load_dwordx4 ... lds), double-buffered: the loads of step s + 1 are in flight
+// while step s is multiplied.  The buffers are separate LDS variables, and the loop is
+// unrolled over them, so that the compiler sees that reads of one cannot touch the loads
+// into the other and does not wait for those.  Rows past I or J and k past K read as zeros:
+// a buffer descriptor ends with the operand's last row, and lanes past K get an offset
+// past its end.
+//
+// LDS layout.  A k-contiguous tile has rows of 128 bytes, eight 16-byte chunks; chunk c of
+// row r sits in slot c ^ ((r >> 1) & 7), so the 16 rows that a fragment read touches lie in
+// 16 different 16-byte columns of the 256 bytes the banks span.  A k-major tile has one row
+// of T values per k; for 16-bit types its 32-byte units (16 columns, what one transposing
+// read takes from a row) are permuted by the key (k & 3) | (k >> 3 & 1) << 2, which sends
+// the eight k rows that two groups of 16 lanes read together to eight different units.
+// The permutation is applied to the global address of each lane, since LDS-direct loads
+// write LDS linearly.
+//
+// The matrix instruction takes B(j, .) as its first operand, so a lane ends up with four
+// consecutive j of one row i: outputs leave in 8- or 16-byte pieces.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace tcq {
+namespace gemm {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// One operand in global memory.  rows: valid rows (I or J); k: valid k.  For k-contiguous
+// storage element (row, kk) is at p[row * ld + kk], for k-major storage at p[kk * ld + row].
+// p is 16-byte aligned, ld * sizeof(T) a multiple of 16, and the contiguous extent (k, or
+// rows) a multiple of 16 bytes too.
+template <typename T>
+struct Operand {
+    const T *p;
+    int64_t ld;
+    int64_t rows;
+    int64_t k;
+};
+
+constexpr int kStepBytes = 128;  // bytes of k per row and step
+
+template <typename T>
+struct Traits;
+template <>
+struct Traits<float> {
+    static constexpr int kStep = 32;   // k per step
+    static constexpr int kSub = 2;     // fragment reads per step (16 k each)
+    using Frag = f32x4;                // 4 k of one row
+    static __device__ __forceinline__ f32x4 mma(const Frag &a, const Frag &b, f32x4 c) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[v], b[v], c, 0, 0, 0);
+        return c;
+    }
+};
+template <>
+struct Traits<__bf16> {
+    static constexpr int kStep = 64;
+    static constexpr int kSub = 2;     // 32 k each
+    using Frag = s16x8;                // 8 k of one row
+    static __device__ __forceinline__ f32x4 mma(const Frag &a, const Frag &b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+};
+template <>
+struct Traits<_Float16> {
+    static constexpr int kStep = 64;
+    static constexpr int kSub = 2;
+    using Frag = s16x8;
+    static __device__ __forceinline__ f32x4 mma(const Frag &a, const Frag &b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    }
+};
+
+typedef __attribute__((address_space(3))) void *LdsPtr;
+
+// Swizzle key of k row kk of a k-major tile, in units of 32 bytes (16-bit) or 64 (fp32).
+template <typename T>
+__device__ __forceinline__ int kmajor_key(int kk) {
+    if constexpr (sizeof(T) == 2) return (kk & 3) | ((kk >> 3 & 1) << 2);
+    return kk >> 2 & 3;
+}
+
+// The per-thread part of an operand's tile loads: TR rows by one step, NT threads.
+template <typename T, bool KM, int TR, int NT>
+struct TileLoader {
+    static constexpr int kChunks = TR * (kStepBytes / 16);  // 16-byte chunks of a tile
+    static constexpr int kLoads = kChunks / NT;
+    static_assert(kChunks % NT == 0, "whole loads per thread");
+    static constexpr int kRowChunks = KM ? TR * static_cast<int>(sizeof(T)) / 16 : 8;
+    static constexpr int kStep = Traits<T>::kStep;
+
+    const char *base;       // first byte of the tile at step 0
+    int64_t left;           // bytes from base to the operand's end
+    int64_t step_bytes;     // advance of base per step
+    int64_t k;              // valid k
+    uint32_t off[kLoads];   // byte offsets of this thread's chunks within the tile
+    int kchunk;             // k-contiguous: first k of this thread's chunks within a step
+
+    __device__ __forceinline__ void init(const Operand<T> &o, int64_t row0, int tid) {
+        constexpr int kPer16 = 16 / static_cast<int>(sizeof(T));
+        k = o.k;
+        if constexpr (KM) {
+            base = reinterpret_cast<const char *>(o.p + row0);
+            left = ((o.k - 1) * o.ld + o.rows - row0) * static_cast<int64_t>(sizeof(T));
+            step_bytes = o.ld * kStep * static_cast<int64_t>(sizeof(T));
+            kchunk = 0;
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const int q = u * NT + tid;
+                const int kk = q / kRowChunks, s = q % kRowChunks;
+                // chunks per swizzle unit: 2 (32 bytes) or 4 (64 bytes)
+                constexpr int kUnit = sizeof(T) == 2 ? 2 : 4;
+                const int c = ((s / kUnit) ^ kmajor_key<T>(kk)) * kUnit + s % kUnit;
+                // columns past the operand's rows: an offset past its end (zeros)
+                off[u] = row0 + c * kPer16 < o.rows
+                             ? static_cast<uint32_t>(kk * o.ld * sizeof(T) + c * 16u)
+                             : 0xFFFFFFF0u;
+            }
+        } else {
+            base = reinterpret_cast<const char *>(o.p + row0 * o.ld);
+            left = ((o.rows - row0 - 1) * o.ld + o.k) * static_cast<int64_t>(sizeof(T));
+            step_bytes = kStepBytes;
+            const int r0 = tid / 8, s = tid % 8;
+            const int c = s ^ (r0 >> 1 & 7);
+            kchunk = c * kPer16;
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u)
+                off[u] = static_cast<uint32_t>((r0 + u * (NT / 8)) * o.ld * sizeof(T) + c * 16u);
+        }
+    }
+
+    // Step s's tile into lds (every wave writes its own 1 KiB pieces).
+    __device__ __forceinline__ void load(char *lds, int s, int tid) const {
+        const int64_t at = s * step_bytes;
+        int64_t bytes = left - at;
+        if (bytes > 0xFFFFFF00ll) bytes = 0xFFFFFF00ll;
+        if (bytes < 0) bytes = 0;
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char *>(base + at), 0, static_cast<int>(bytes), 0x00020000);
+        const bool in = KM || s * static_cast<int64_t>(kStep) + kchunk < k;
+        const int wave0 = __builtin_amdgcn_readfirstlane(tid & ~63);
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rs, (LdsPtr)(lds + (u * NT + wave0) * 16), 16,
+                static_cast<int>(in ? off[u] : 0xFFFFFFF0u), 0, 0, 0);
+    }
+};
+
+// Fragment f (16 rows from r0 + 16 f) of sub-step ks: this lane's k values of its row.
+template <typename T, bool KM, int TR>
+struct FragReader {
+    using Frag = typename Traits<T>::Frag;
+    int lane;
+    int r0;
+    __device__ __forceinline__ Frag read(const char *lds, int f, int ks) const {
+        const int l16 = lane & 15, g = lane >> 4;
+        if constexpr (!KM) {
+            const int row = r0 + f * 16 + l16;
+            const int slot = (ks * 4 + g) ^ (l16 >> 1 & 7);
+            return *reinterpret_cast<const Frag *>(lds + row * 128 + slot * 16);
+        } else if constexpr (sizeof(T) == 2) {
+            // two transposing reads of 4 k by 16 columns per group of 16 lanes: lane s of
+            // the group addresses k row s / 4, columns 4 (s % 4) .. + 3, and receives
+            // column s of the four rows
+            typedef __attribute__((address_space(3))) s16x4 *P;
+            Frag out;
+            const int unit = (r0 >> 4) + f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int kk = ks * 32 + g * 8 + h * 4 + (l16 >> 2);
+                const char *p = lds + kk * (TR * 2) + (unit ^ kmajor_key<T>(kk)) * 32 +
+                                (l16 & 3) * 8;
+                const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)p);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) out[h * 4 + v] = t[v];
+            }
+            return out;
+        } else {
+            Frag out;
+            const int unit = (r0 >> 4) + f;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int kk = ks * 16 + g * 4 + v;
+                out[v] = *reinterpret_cast<const float *>(
+                    lds + kk * (TR * 4) + (unit ^ kmajor_key<T>(kk)) * 64 + l16 * 4);
+            }
+            return out;
+        }
+    }
+};
+
+// Tile (ti, tj) of workgroup `wg` of an ni x nj grid of tiles.  Workgroups go round the 8
+// XCDs; each XCD gets one contiguous run of the tile order, and that order takes i tiles
+// in groups of 8 per j, so that the tiles an XCD has in flight share operand rows in its L2.
+__device__ __forceinline__ void tile_of(uint32_t wg, uint32_t ni, uint32_t nj, uint32_t &ti,
+                                        uint32_t &tj) {
+    constexpr uint32_t kXcds = 8, kGroup = 8;
+    const uint32_t n = ni * nj;
+    const uint32_t q = n / kXcds, r = n % kXcds, x = wg % kXcds;
+    const uint32_t t = (x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q) + wg / kXcds;
+    const uint32_t per = kGroup * nj;
+    const uint32_t first = t / per * kGroup;
+    const uint32_t rows = ni - first < kGroup ? ni - first : kGroup;
+    const uint32_t in = t % per;
+    ti = first + in % rows;
+    tj = in / rows;
+}
+
+// Computes the tile and hands it out in pieces of four: Epi::Column col(epi, j) once per
+// lane, then epi.put(col, i, D[i][j .. j + 3]) for its rows; i and j may lie past I or J.
+template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, typename Epi>
+__device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> &B, int64_t i0,
+                                          int64_t j0, int64_t K, char *a0, char *a1, char *b0,
+                                          char *b1, const Epi &epi) {
+    constexpr int NT = WI * WJ * 64;
+    constexpr int FI = TI / WI / 16, FJ = TJ / WJ / 16;
+    constexpr int kSub = Traits<T>::kSub;
+    using Frag = typename Traits<T>::Frag;
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wi = wave / WJ, wj = wave % WJ;
+    TileLoader<T, AKM, TI, NT> la;
+    TileLoader<T, BKM, TJ, NT> lb;
+    la.init(A, i0, tid);
+    lb.init(B, j0, tid);
+    const FragReader<T, AKM, TI> ra{lane, wi * FI * 16};
+    const FragReader<T, BKM, TJ> rb{lane, wj * FJ * 16};
+    f32x4 acc[FI][FJ];
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // A step is kSub sub-steps of two phases, each half of the wave's rows i against all its
+    // columns j.  A phase first requests the next phase's fragments, then multiplies its
+    // own.  Before the last phase all waves meet: every fragment of this step is in
+    // registers then, so its buffers are refilled (step s + 2) and the next step's first
+    // fragments are read while the last phase multiplies.
+    constexpr int FH = FI / 2;
+    constexpr int kPhases = 2 * kSub;
+    static_assert(FI % 2 == 0, "two phases per sub-step");
+    const int steps = static_cast<int>((K + Traits<T>::kStep - 1) / Traits<T>::kStep);
+    Frag fa[2][FH], fb[2][FJ];
+    auto read_phase = [&](const char *ta, const char *tb, int ph) {
+        const int ks = ph / 2, half = ph % 2;
+        if (half == 0) {
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) fb[ks % 2][j] = rb.read(tb, j, ks);
+        }
+#pragma unroll
+        for (int i = 0; i < FH; ++i) fa[ph % 2][i] = ra.read(ta, half * FH + i, ks);
+    };
+    auto mul_phase = [&](int ph) {
+        const int ks = ph / 2, half = ph % 2;
+#pragma unroll
+        for (int i = 0; i < FH; ++i)
+#pragma unroll
+            for (int j = 0; j < FJ; ++j)
+                acc[half * FH + i][j] =
+                    Traits<T>::mma(fb[ks % 2][j], fa[ph % 2][i], acc[half * FH + i][j]);
+    };
+    // Everyone's LDS reads and LDS-direct loads are done; no access moves across.
+    auto meet = [&]() {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    };
+    // Step s from (ta, tb); (na, nb) hold step s + 1 from the meeting on.
+    auto step = [&](int s, char *ta, char *tb, const char *na, const char *nb) {
+#pragma unroll
+        for (int ph = 0; ph + 1 < kPhases; ++ph) {
+            read_phase(ta, tb, ph + 1);
+            mul_phase(ph);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        meet();
+        la.load(ta, s + 2, tid);
+        lb.load(tb, s + 2, tid);
+        read_phase(na, nb, 0);
+        mul_phase(kPhases - 1);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (steps > 0) {
+        la.load(a0, 0, tid);
+        lb.load(b0, 0, tid);
+        meet();
+        la.load(a1, 1, tid);
+        lb.load(b1, 1, tid);
+        read_phase(a0, b0, 0);
+        // two steps per turn; steps past the last one multiply zeros
+        for (int s = 0; s < steps; s += 2) {
+            step(s, a0, b0, a1, b1);
+            step(s + 1, a1, b1, a0, b0);
+        }
+        meet();  // no load into LDS outlives the tile
+    }
+    // Outputs: 16 rows at a time through a piece of LDS of the wave's own (in a0, which is
+    // done with), so that a lane takes four consecutive j of always the same column group
+    // and a row leaves in one run.  The 16-byte chunks of row r are permuted by r: the 16
+    // rows of a fragment otherwise start in the same bank.
+    constexpr int kRow = FJ * 4;  // 16-byte chunks of a row
+    static_assert(WI * WJ * FJ * 1024 <= TI * kStepBytes, "the waves' pieces fit the buffer");
+    static_assert(64 % kRow == 0, "whole rows per wave and turn");
+    char *piece = a0 + wave * (FJ * 1024);
+    const int l16 = lane & 15, g = lane >> 4;
+    const int rr = lane / kRow, rc = lane % kRow;
+    const int64_t j = j0 + wj * FJ * 16 + rc * 4;
+    typename Epi::Column col(epi, j);
+#pragma unroll
+    for (int i = 0; i < FI; ++i) {
+#pragma unroll
+        for (int f = 0; f < FJ; ++f)
+            *reinterpret_cast<f32x4 *>(piece + l16 * (FJ * 64) +
+                                       (((f * 4 + g) ^ l16) % kRow) * 16) = acc[i][f];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int r = rr; r < 16; r += 64 / kRow) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(piece + r * (FJ * 64) +
+                                                             ((rc ^ r) % kRow) * 16);
+            epi.put(col, i0 + (wi * FI + i) * 16 + r, v);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+}  // namespace gemm
+}  // namespace tcq

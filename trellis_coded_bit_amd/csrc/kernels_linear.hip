@@ -1,0 +1,465 @@
+// The coded linear layer: y = act(row_scale (x W_hat^T) + bias) + residual for a batch of
+// rows x, with the trellis-coded matrix W_hat decoded inside the call, and its gradients.
+//
+// The matrix is decoded once into the workspace, in the layer's type, and multiplied on the
+// matrix cores (gemm_device.h).  With the table in the layer's own type a decoded weight is
+// a table entry copied bit for bit, so every product is exact and the sums are fp32: the
+// outputs' own rounding is the only one to 16 bits in the forward pass.  The backward pass
+// rounds the incoming gradient times the activation's slope and the row scale once, to the
+// layer's type, because both of its products read it through the matrix cores.
+#include <hip/hip_runtime.h>
+
+#include "gemm_device.h"
+#include "linear_device.h"
+#include "tcq.h"
+#include "tcq_internal.h"
+
+namespace tcq {
+namespace {
+
+using gemm::f32x4;
+using gemm::Operand;
+
+// ---------------------------------------------------------------- decode into memory
+
+struct DecodeArgs {
+    const uint32_t *bits;
+    const uint32_t *s0;
+    const void *table;
+    int64_t M, N, ld;  // out is M x ld, ld >= N a multiple of 8; columns past N are zeros
+    int L, kv, V, T, nwords;
+};
+
+// Any trellis: a thread decodes eight consecutive columns, each on its own.  Step t's state
+// is the L-bit window of s_0 || b_1 || ... that ends with b_t, inside the word that holds
+// the chunk's last bit and the word before it (s_0 for the first word).
+template <typename T>
+__global__ __launch_bounds__(256) void decode_matrix_kernel(DecodeArgs a, T *__restrict__ out) {
+    const int64_t cpr = a.ld / 8;
+    const int64_t chunks = a.M * cpr;
+    const int64_t bpr = a.N / a.T;
+    const T *table = static_cast<const T *>(a.table);
+    const uint32_t mask = (1u << a.L) - 1u;
+    for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < chunks;
+         q += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t row = q / cpr;
+        const int64_t c0 = (q - row * cpr) * 8;
+        struct alignas(8 * sizeof(T)) Eight { T v[8]; } o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t c = c0 + e;
+            T w = static_cast<T>(0.0f);
+            if (c < a.N) {
+                const int64_t blk = row * bpr + c / a.T;
+                const int i = static_cast<int>(c % a.T);
+                const int end = (i / a.V + 1) * a.kv;  // stream bits up to the chunk's end
+                const int j = (end - 1) >> 5;
+                const uint32_t *wb = a.bits + blk * a.nwords;
+                const uint32_t hi = j ? wb[j - 1] : a.s0[blk];
+                const uint32_t st =
+                    __builtin_amdgcn_alignbit(hi, wb[j], 32 * (j + 1) - end) & mask;
+                w = table[static_cast<int64_t>(st) * a.V + i % a.V];
+            }
+            o.v[e] = w;
+        }
+        *reinterpret_cast<Eight *>(out + row * a.ld + c0) = o;
+    }
+}
+
+// Rows of x into a padded, aligned copy: out is B x ld, columns past N zeros.
+template <typename T>
+__global__ __launch_bounds__(256) void stage_kernel(const T *__restrict__ x, int64_t B, int64_t N,
+                                                    int64_t ldx, T *__restrict__ out,
+                                                    int64_t ld) {
+    const int64_t total = B * ld;
+    for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < total;
+         q += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = q / ld, c = q - r * ld;
+        out[q] = c < N ? x[r * ldx + c] : static_cast<T>(0.0f);
+    }
+}
+
+// ---------------------------------------------------------------- epilogues
+
+template <typename T>
+__device__ __forceinline__ void store4(T *p, int64_t j, int64_t J, bool vec, f32x4 v) {
+    struct alignas(4 * sizeof(T)) Four { T v[4]; } o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o.v[e] = static_cast<T>(v[e]);
+    if (vec && j + 4 <= J) {
+        *reinterpret_cast<Four *>(p) = o;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (j + e < J) p[e] = o.v[e];
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ f32x4 load4(const T *p, int64_t j, int64_t J, bool vec) {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (vec && j + 4 <= J) {
+        struct alignas(4 * sizeof(T)) Four { T v[4]; };
+        const Four o = *reinterpret_cast<const Four *>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(o.v[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (j + e < J) v[e] = static_cast<float>(p[e]);
+    }
+    return v;
+}
+
+// y = act(scale s + bias) + residual, z = scale s + bias, in fp32, rounded once each.
+template <typename T>
+struct LayerEpilogue {
+    const float *scale;
+    const float *bias;
+    const T *res;
+    T *y;
+    T *pre;
+    int64_t ldr, ldy, ldp;
+    int64_t I, J;
+    int act;
+    int vec_y, vec_r, vec_p;  // four consecutive values are aligned
+
+    struct Column {
+        int64_t j;
+        f32x4 a, b;
+        __device__ __forceinline__ Column(const LayerEpilogue &e, int64_t j_) : j(j_) {
+            a = f32x4{1.f, 1.f, 1.f, 1.f};
+            b = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (e.scale && j < e.J) a = load4(e.scale + j, j, e.J, false);
+            if (e.bias && j < e.J) b = load4(e.bias + j, j, e.J, false);
+        }
+    };
+    __device__ __forceinline__ void put(const Column &c, int64_t i, f32x4 s) const {
+        if (i >= I || c.j >= J) return;
+        f32x4 z, o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[e] = __builtin_fmaf(c.a[e], s[e], c.b[e]);
+        if (pre) store4(pre + i * ldp + c.j, c.j, J, vec_p, z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = act_value(z[e], act);
+        if (res) {
+            const f32x4 r = load4(res + i * ldr + c.j, c.j, J, vec_r);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] += r[e];
+        }
+        store4(y + i * ldy + c.j, c.j, J, vec_y, o);
+    }
+};
+
+template <typename T>
+struct PlainEpilogue {
+    T *y;
+    int64_t ldy, I, J;
+    int vec_y;
+    struct Column {
+        int64_t j;
+        __device__ __forceinline__ Column(const PlainEpilogue &, int64_t j_) : j(j_) {}
+    };
+    __device__ __forceinline__ void put(const Column &c, int64_t i, f32x4 s) const {
+        if (i < I && c.j < J) store4(y + i * ldy + c.j, c.j, J, vec_y, s);
+    }
+};
+
+// ---------------------------------------------------------------- products
+
+template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, typename Epi>
+__global__ __launch_bounds__(WI *WJ * 64) void gemm_kernel(Operand<T> A, Operand<T> B, int64_t K,
+                                                           Epi epi, uint32_t ni, uint32_t nj) {
+    __shared__ __align__(16) char a0[TI * gemm::kStepBytes];
+    __shared__ __align__(16) char a1[TI * gemm::kStepBytes];
+    __shared__ __align__(16) char b0[TJ * gemm::kStepBytes];
+    __shared__ __align__(16) char b1[TJ * gemm::kStepBytes];
+    uint32_t ti, tj;
+    gemm::tile_of(blockIdx.x, ni, nj, ti, tj);
+    gemm::gemm_tile<T, AKM, BKM, TI, TJ, WI, WJ>(A, B, static_cast<int64_t>(ti) * TI,
+                                                 static_cast<int64_t>(tj) * TJ, K, a0, a1, b0,
+                                                 b1, epi);
+}
+
+template <typename T, bool AKM, bool BKM, typename Epi>
+hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, int64_t K, const Epi &epi,
+                       hipStream_t s) {
+    const int64_t I = A.rows, J = B.rows;
+    if (I <= 0 || J <= 0) return hipSuccess;
+    const auto tiles = [&](int64_t t) { return ((I + t - 1) / t) * ((J + t - 1) / t); };
+    if constexpr (sizeof(T) == 2) {
+        if (tiles(256) >= 128) {
+            const uint32_t ni = static_cast<uint32_t>((I + 255) / 256);
+            const uint32_t nj = static_cast<uint32_t>((J + 255) / 256);
+            hipLaunchKernelGGL((gemm_kernel<T, AKM, BKM, 256, 256, 2, 4, Epi>), dim3(ni * nj),
+                               dim3(512), 0, s, A, B, K, epi, ni, nj);
+            return hipGetLastError();
+        }
+    }
+    const uint32_t ni = static_cast<uint32_t>((I + 127) / 128);
+    const uint32_t nj = static_cast<uint32_t>((J + 127) / 128);
+    hipLaunchKernelGGL((gemm_kernel<T, AKM, BKM, 128, 128, 2, 2, Epi>), dim3(ni * nj), dim3(256),
+                       0, s, A, B, K, epi, ni, nj);
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- incoming gradient
+
+struct SlopeArgs {
+    const void *dy;
+    int64_t B, M, lddy;
+    const float *scale;      // row scale, or NULL
+    const int8_t *zq;        // pre-activation checkpoint, or NULL (no activation)
+    const uint8_t *ze;
+    int64_t ldz;
+    int act;
+    int64_t ld;              // of the result: a multiple of 8, columns past M are zeros
+    float *part;             // [slabs][M] sums of dy act'(z) over a slab's rows, or NULL
+    int64_t rows_per_slab;
+};
+
+// out = dy act'(z) scale rounded to T; part = sums over rows of dy act'(z), in fp32, rows
+// ascending within a slab (four interleaved chains, added in order).
+template <typename T>
+__global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__ out) {
+    __shared__ float red[4][64][9];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t c0 = (static_cast<int64_t>(blockIdx.x) * 64 + lane) * 8;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.rows_per_slab;
+    const int64_t r1 = r0 + a.rows_per_slab < a.B ? r0 + a.rows_per_slab : a.B;
+    const T *dy = static_cast<const T *>(a.dy);
+    const int64_t groups = (a.M + 31) / 32;
+    float sum[8], sc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        sum[e] = 0.0f;
+        sc[e] = a.scale && c0 + e < a.M ? a.scale[c0 + e] : 1.0f;
+    }
+    if (c0 < a.ld) {
+        for (int64_t r = r0 + w; r < r1; r += 4) {
+            struct alignas(8 * sizeof(T)) Eight { T v[8]; } o;
+            const int ez = a.zq && c0 < a.M ? a.ze[r * groups + c0 / 32] : 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float g = 0.0f;
+                if (c0 + e < a.M) {
+                    g = static_cast<float>(dy[r * a.lddy + c0 + e]);
+                    if (a.zq) g *= act_slope(code_value(a.zq[r * a.ldz + c0 + e], ez), a.act);
+                }
+                sum[e] += g;
+                o.v[e] = static_cast<T>(g * sc[e]);
+            }
+            if (out) *reinterpret_cast<Eight *>(out + r * a.ld + c0) = o;
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) red[w][lane][e] = sum[e];
+    __syncthreads();
+    if (w == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c0 + e < a.M)
+                a.part[static_cast<int64_t>(blockIdx.y) * a.M + c0 + e] =
+                    ((red[0][lane][e] + red[1][lane][e]) + red[2][lane][e]) + red[3][lane][e];
+    }
+}
+
+// sum[c] = part[0][c] + part[1][c] + ... in order.
+__global__ __launch_bounds__(256) void slab_sum_kernel(const float *__restrict__ part,
+                                                       int64_t slabs, int64_t M,
+                                                       float *__restrict__ sum) {
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (c >= M) return;
+    float s = 0.0f;
+    for (int64_t i = 0; i < slabs; ++i) s += part[i * M + c];
+    sum[c] = s;
+}
+
+// ---------------------------------------------------------------- host side
+
+template <typename T>
+bool four_aligned(const T *p, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T))) == 0 && ld % 4 == 0;
+}
+
+// Whether rows of p can be read 16 bytes at a time by the product: aligned, and the
+// contiguous extent a whole number of 16-byte pieces.
+bool sixteen_aligned(const void *p, int64_t ld, int64_t extent, size_t size) {
+    const int64_t per = static_cast<int64_t>(16 / size);
+    // (a tile's byte offsets fit 32 bits: 256 rows of at most 2^21 values)
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % per == 0 && extent % per == 0 &&
+           ld <= TCQ_LINEAR_MAX_DIM;
+}
+
+unsigned grid_for(int64_t work, int64_t per, int64_t most) {
+    int64_t g = (work + per - 1) / per;
+    if (g > most) g = most;
+    return static_cast<unsigned>(g < 1 ? 1 : g);
+}
+
+int64_t slope_slabs(int64_t B) {
+    const int64_t s = (B + 63) / 64;
+    return s < 1 ? 1 : (s > 256 ? 256 : s);
+}
+
+template <typename T>
+hipError_t decode_matrix(const CodedMatrix &w, T *out, int64_t ld, hipStream_t s) {
+    DecodeArgs a{w.bits, w.s0, w.table, w.M, w.N, ld, w.L, w.k * w.V, w.V, w.T,
+                 (w.k * w.T + 31) / 32};
+    if (w.M <= 0 || w.N <= 0) return hipSuccess;
+    hipLaunchKernelGGL(decode_matrix_kernel<T>, dim3(grid_for(w.M * (ld / 8), 256, 1 << 20)),
+                       dim3(256), 0, s, a, out);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t forward(const CodedMatrix &w, const LinearCall &c, char *ws, hipStream_t s) {
+    const LinearLayout lay = linear_layout(sizeof(T), c.B, w.M, w.N);
+    T *W = reinterpret_cast<T *>(ws + lay.matrix);
+    hipError_t e = decode_matrix(w, W, lay.ldn, s);
+    if (e != hipSuccess) return e;
+    const T *x = static_cast<const T *>(c.x);
+    int64_t ldx = c.ldx, K = w.N;
+    if (w.N > 0 && !sixteen_aligned(x, ldx, w.N, sizeof(T))) {
+        T *st = reinterpret_cast<T *>(ws + lay.rows);
+        hipLaunchKernelGGL(stage_kernel<T>, dim3(grid_for(c.B * lay.ldn, 1024, 1 << 16)),
+                           dim3(256), 0, s, x, c.B, w.N, ldx, st, lay.ldn);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        x = st;
+        ldx = lay.ldn;
+        K = lay.ldn;
+    }
+    LayerEpilogue<T> epi{};
+    epi.scale = c.row_scale;
+    epi.bias = c.bias;
+    epi.res = static_cast<const T *>(c.residual);
+    epi.y = static_cast<T *>(c.y);
+    epi.pre = static_cast<T *>(c.pre);
+    epi.ldr = c.ldr;
+    epi.ldy = c.ldy;
+    epi.ldp = c.ldp;
+    epi.I = c.B;
+    epi.J = w.M;
+    epi.act = c.act;
+    epi.vec_y = four_aligned(epi.y, c.ldy);
+    epi.vec_r = four_aligned(epi.res, c.ldr);
+    epi.vec_p = four_aligned(epi.pre, c.ldp);
+    const Operand<T> A{x, ldx, c.B, K};
+    const Operand<T> Bm{W, lay.ldn, w.M, K};
+    return launch_gemm<T, false, false>(A, Bm, K, epi, s);
+}
+
+template <typename T>
+hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStream_t s) {
+    const LinearLayout lay = linear_grad_layout(sizeof(T), c.B, w.M, w.N, c.dx, c.dw, c.dbias);
+    hipError_t e;
+    T *S = reinterpret_cast<T *>(ws + lay.grad);
+    const int64_t slabs = slope_slabs(c.B);
+    if (c.B > 0 && w.M > 0) {
+        SlopeArgs a{};
+        a.dy = c.dy;
+        a.B = c.B;
+        a.M = w.M;
+        a.lddy = c.lddy;
+        a.scale = c.row_scale;
+        a.zq = c.act == TCQ_ACT_NONE ? nullptr : c.zq;
+        a.ze = c.ze;
+        a.ldz = c.ldz;
+        a.act = c.act;
+        a.ld = lay.ldm;
+        a.part = c.dbias ? reinterpret_cast<float *>(ws + lay.part) : nullptr;
+        a.rows_per_slab = (c.B + slabs - 1) / slabs;
+        hipLaunchKernelGGL(slope_kernel<T>,
+                           dim3(static_cast<unsigned>((lay.ldm / 8 + 63) / 64),
+                                static_cast<unsigned>(slabs)),
+                           dim3(256), 0, s, a, c.dx || c.dw ? S : nullptr);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (c.dbias && w.M > 0) {
+        hipLaunchKernelGGL(slab_sum_kernel, dim3(static_cast<unsigned>((w.M + 255) / 256)),
+                           dim3(256), 0, s, reinterpret_cast<const float *>(ws + lay.part),
+                           c.B > 0 ? slabs : 0, w.M, c.dbias);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (c.dx && c.B > 0 && w.N > 0) {
+        T *W = reinterpret_cast<T *>(ws + lay.matrix);
+        e = decode_matrix(w, W, lay.ldn, s);
+        if (e != hipSuccess) return e;
+        const PlainEpilogue<T> epi{static_cast<T *>(c.dx), c.lddx, c.B, w.N,
+                                   four_aligned(static_cast<T *>(c.dx), c.lddx)};
+        const Operand<T> A{S, lay.ldm, c.B, w.M > 0 ? lay.ldm : 0};
+        // (columns past N are zeros and not stored; rows past M read as zeros)
+        const Operand<T> Bm{W, lay.ldn, lay.ldn, w.M};
+        e = launch_gemm<T, false, true>(A, Bm, w.M, epi, s);
+        if (e != hipSuccess) return e;
+    }
+    if (c.dw && w.M > 0 && w.N > 0) {
+        T *X = reinterpret_cast<T *>(ws + lay.rows);
+        if (c.B > 0) {
+            e = launch_act_unpack(c.xq, c.ldxq, c.xe, c.B, w.N, dtype_of<T>(), X, lay.ldn,
+                                  lay.ldn, s);
+            if (e != hipSuccess) return e;
+        }
+        const PlainEpilogue<T> epi{static_cast<T *>(c.dw), c.lddw, w.M, w.N,
+                                   four_aligned(static_cast<T *>(c.dw), c.lddw)};
+        const Operand<T> A{S, lay.ldm, lay.ldm, c.B};
+        const Operand<T> Bm{X, lay.ldn, lay.ldn, c.B};
+        e = launch_gemm<T, true, true>(A, Bm, c.B, epi, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+size_t pad8(int64_t n) { return static_cast<size_t>((n + 7) / 8 * 8); }
+
+}  // namespace
+
+LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N) {
+    LinearLayout l{};
+    l.ldn = static_cast<int64_t>(pad8(N));
+    l.matrix = 0;
+    l.rows = align_up(static_cast<size_t>(M) * l.ldn * size, 256);
+    l.bytes = l.rows + align_up(static_cast<size_t>(B) * l.ldn * size, 256);
+    return l;
+}
+
+LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bool dx, bool dw,
+                                bool dbias) {
+    LinearLayout l{};
+    l.ldn = static_cast<int64_t>(pad8(N));
+    l.ldm = static_cast<int64_t>(pad8(M));
+    size_t off = 0;
+    l.matrix = off;
+    if (dx) off += align_up(static_cast<size_t>(M) * l.ldn * size, 256);
+    l.grad = off;
+    if (dx || dw) off += align_up(static_cast<size_t>(B) * l.ldm * size, 256);
+    l.rows = off;
+    if (dw) off += align_up(static_cast<size_t>(B) * l.ldn * size, 256);
+    l.part = off;
+    if (dbias) off += align_up(static_cast<size_t>(slope_slabs(B)) * M * sizeof(float), 256);
+    l.bytes = off;
+    return l;
+}
+
+hipError_t launch_linear(const CodedMatrix &w, const LinearCall &c, char *ws, hipStream_t s) {
+    switch (c.dtype) {
+        case TCQ_F32: return forward<float>(w, c, ws, s);
+        case TCQ_F16: return forward<_Float16>(w, c, ws, s);
+        default: return forward<__bf16>(w, c, ws, s);
+    }
+}
+
+hipError_t launch_linear_grad(const CodedMatrix &w, const LinearGrad &c, char *ws,
+                              hipStream_t s) {
+    switch (c.dtype) {
+        case TCQ_F32: return backward<float>(w, c, ws, s);
+        case TCQ_F16: return backward<_Float16>(w, c, ws, s);
+        default: return backward<__bf16>(w, c, ws, s);
+    }
+}
+
+}  // namespace tcq

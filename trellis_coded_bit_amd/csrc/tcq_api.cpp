@@ -27,11 +27,11 @@ void set_error(const char *fmt, ...) {
     g_error = buf;
 }
 
-static void clear_error() { g_error.clear(); }
+void clear_error() { g_error.clear(); }
 
 // Workspaces must start on a 256-byte boundary (as every hipMalloc or torch allocation
 // does): the kernels lay out their buffers at 256-byte offsets from it.
-static int check_workspace_alignment(const char *fn, const void *workspace) {
+int check_workspace_alignment(const char *fn, const void *workspace) {
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) {
         set_error("%s: workspace %p is not 256-byte aligned", fn, workspace);
         return TCQ_EINVAL;
@@ -74,7 +74,7 @@ Plan plan_for(const Problem &p) {
 }
 
 // Shared shape checks for encode and decode.
-static int check_trellis(const char *fn, int64_t M, int64_t N, int L, int k, int V, int T) {
+int check_trellis(const char *fn, int64_t M, int64_t N, int L, int k, int V, int T) {
     if (M < 0 || N < 0) {
         set_error("%s: negative matrix size (M=%lld N=%lld)", fn, (long long)M, (long long)N);
         return TCQ_EINVAL;
@@ -123,7 +123,7 @@ static Problem make_problem(int64_t M, int64_t N, int64_t ldw, int L, int k, int
     return p;
 }
 
-static int hip_fail(const char *fn, const char *what, hipError_t e) {
+int hip_fail(const char *fn, const char *what, hipError_t e) {
     set_error("%s: %s failed: %s", fn, what, hipGetErrorString(e));
     return TCQ_EHIP;
 }

@@ -51,6 +51,12 @@ int encode_impl(const char *fn, const float *W, int64_t M, int64_t N, int64_t ld
 
 // Per-thread error message of the C ABI (tcq_last_error).
 void set_error(const char *fmt, ...);
+void clear_error();
+
+// Checks shared by the entry points; each returns a status and sets the error message.
+int check_trellis(const char *fn, int64_t M, int64_t N, int L, int k, int V, int T);
+int check_workspace_alignment(const char *fn, const void *workspace);
+int hip_fail(const char *fn, const char *what, hipError_t e);
 
 // Kernel launchers (return hipError_t of the launch).
 hipError_t launch_acs_generic(const Problem &p, const Plan &pl, const float *W,
@@ -91,6 +97,62 @@ hipError_t launch_hadamard(const float *X, int64_t ldx, float *Y, int64_t ldy, i
 size_t scale_field_slabs(int64_t M);
 hipError_t launch_scale_field(const float *W, int64_t ldw, int64_t M, int64_t N, float *a,
                               float *b, float *Wn, int64_t ldn, float *part, hipStream_t s);
+
+// The coded linear layer and its gradients.
+struct CodedMatrix {
+    const uint32_t *bits, *s0;
+    const void *table;       // 2^L x V entries of the layer's type
+    int64_t M, N;
+    int L, k, V, T;
+};
+struct LinearCall {
+    int dtype, act;
+    const void *x;
+    int64_t B, ldx;
+    const float *row_scale, *bias;
+    const void *residual;
+    int64_t ldr;
+    void *y;
+    int64_t ldy;
+    void *pre;
+    int64_t ldp;
+};
+struct LinearGrad {
+    int dtype, act;
+    const void *dy;
+    int64_t B, lddy;
+    const float *row_scale;
+    const int8_t *zq;        // checkpoint of the pre-activation: codes, scale bytes
+    int64_t ldz;
+    const uint8_t *ze;
+    const int8_t *xq;        // checkpoint of the input
+    int64_t ldxq;
+    const uint8_t *xe;
+    void *dx;
+    int64_t lddx;
+    void *dw;
+    int64_t lddw;
+    float *dbias;
+};
+// Workspace of a call: byte offsets of the decoded matrix (M x ldn), the staged or unpacked
+// input rows (B x ldn), the scaled gradient (B x ldm) and the bias gradient's partial sums.
+struct LinearLayout {
+    size_t matrix, rows, grad, part, bytes;
+    int64_t ldn, ldm;
+};
+LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N);
+LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bool dx, bool dw,
+                                bool dbias);
+hipError_t launch_linear(const CodedMatrix &w, const LinearCall &c, char *ws, hipStream_t s);
+hipError_t launch_linear_grad(const CodedMatrix &w, const LinearGrad &c, char *ws,
+                              hipStream_t s);
+
+// 8-bit checkpoints (unpack also writes zeros to columns cols .. padded - 1 of out).
+hipError_t launch_act_pack(const void *X, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                           int8_t *codes, int64_t ldq, uint8_t *scale, hipStream_t s);
+hipError_t launch_act_unpack(const int8_t *codes, int64_t ldq, const uint8_t *scale,
+                             int64_t rows, int64_t cols, int dtype, void *out, int64_t ldo,
+                             int64_t padded, hipStream_t s);
 
 // Error feedback over coding blocks.
 hipError_t launch_ldlq_update(float *tgt, int64_t ldt, const float *W, int64_t ldw,
