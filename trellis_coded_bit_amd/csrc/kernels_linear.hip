@@ -9,6 +9,7 @@
 // layer's type, because both of its products read it through the matrix cores.
 #include <hip/hip_runtime.h>
 
+#include "decode_device.h"
 #include "gemm_device.h"
 #include "linear_device.h"
 #include "tcq.h"
@@ -63,6 +64,118 @@ __global__ __launch_bounds__(256) void decode_matrix_kernel(DecodeArgs a, T *__r
             o.v[e] = w;
         }
         *reinterpret_cast<Eight *>(out + row * a.ld + c0) = o;
+    }
+}
+
+// Blocks of whole chunks (T a multiple of 8): eight columns per thread and turn, decoded
+// from the table in LDS.  The matrix is dense then (ld = N), so chunk g's values are out's
+// values 8 g .. 8 g + 7 and its block is g / (T / 8).  A table of more than 128 KiB goes
+// through LDS in parts: every pass ORs in the steps whose state lies in its part, the others
+// read a row of zeros after the part, so the values' bits arrive unchanged.
+struct ChunkArgs {
+    const uint32_t *bits;
+    const uint32_t *s0;
+    const char *table;
+    uint32_t chunks;         // of the matrix
+    uint32_t chunks_per_wg;
+    uint32_t cpb;            // chunks per block
+    int cpb_log2;            // log2(cpb), or -1
+    int L, nwords;
+    int part_log2;           // log2(states per part)
+    int parts;
+    int vec;                 // the table is 16-byte aligned
+};
+
+constexpr int kChunkThreads = 1024;
+constexpr int kPartBytes = 128 << 10;
+
+// Chunks a thread holds at a time: each keeps its values over the passes.
+template <typename T, int KV, int V>
+constexpr int chunk_rows() {
+    return sizeof(T) == 2 ? 8 : 4;
+}
+
+template <typename T, int KV, int V, bool ONE>
+__global__ __launch_bounds__(kChunkThreads) void decode_chunks_kernel(ChunkArgs a,
+                                                                      T *__restrict__ out) {
+    using C = Chunk<KV, V>;
+    constexpr int RT = chunk_rows<T, KV, V>();
+    constexpr int kRowBytes = V * static_cast<int>(sizeof(T));
+    constexpr int kLog = kRowBytes == 2 ? 1 : (kRowBytes == 4 ? 2 : (kRowBytes == 8 ? 3 : 4));
+    constexpr int kWords = 8 * static_cast<int>(sizeof(T)) / 4;  // 32-bit words of a chunk
+    extern __shared__ __align__(16) char tab[];
+    const int tid = threadIdx.x;
+    const int part_bytes = 1 << (a.part_log2 + kLog);
+    const uint32_t dummy = static_cast<uint32_t>(part_bytes);
+    const uint32_t begin = blockIdx.x * a.chunks_per_wg;
+    const uint32_t end = begin + a.chunks_per_wg < a.chunks ? begin + a.chunks_per_wg : a.chunks;
+    auto copy = [&](int p) {
+        table_to_lds<kChunkThreads>(tab, a.table + static_cast<int64_t>(p) * part_bytes,
+                                    part_bytes, sizeof(T), a.vec, tid);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (!ONE) {
+            if (tid < 4) reinterpret_cast<uint32_t *>(tab + part_bytes)[tid] = 0u;
+            __syncthreads();
+        }
+    };
+    if (ONE) copy(0);
+    for (uint32_t t0 = begin; t0 < end; t0 += kChunkThreads * RT) {
+        uint32_t n[RT][C::NW];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            uint32_t g = t0 + i * kChunkThreads + tid;
+            g = g < end ? g : begin;  // (decoded again and not stored)
+            const uint32_t blk = a.cpb_log2 >= 0 ? g >> a.cpb_log2 : g / a.cpb;
+            const int q = static_cast<int>(g - blk * a.cpb);
+            uint32_t w[C::NW + 1];
+            chunk_words<KV, V>(a.bits + static_cast<int64_t>(blk) * a.nwords, a.s0 + blk, q, w);
+            chunk_align<KV, V>(w, q, n[i]);
+        }
+        uint32_t val[RT][kWords];
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < kWords; ++j) val[i][j] = 0u;
+        const int parts = ONE ? 1 : a.parts;
+        for (int p = 0; p < parts; ++p) {
+            if (!ONE) {
+                __syncthreads();  // the previous part is done with
+                copy(p);
+            }
+            const uint32_t base = static_cast<uint32_t>(p) * dummy;
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+#pragma unroll
+                for (int t = 0; t < C::kSteps; ++t) {
+                    uint32_t off = chunk_state<KV, V>(n[i], t, a.L) << kLog;
+                    if (!ONE) {
+                        off -= base;  // wraps below the part
+                        off = off < dummy ? off : dummy;
+                    }
+                    const char *row = tab + off;
+                    if constexpr (kRowBytes == 2) {
+                        const uint32_t v = *reinterpret_cast<const uint16_t *>(row);
+                        val[i][t / 2] |= v << (16 * (t % 2));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kRowBytes / 4; ++j)
+                            val[i][t * (kRowBytes / 4) + j] |=
+                                reinterpret_cast<const uint32_t *>(row)[j];
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const uint32_t g = t0 + i * kChunkThreads + tid;
+            if (g < end) {
+                uint4 *o = reinterpret_cast<uint4 *>(out + static_cast<int64_t>(g) * 8);
+#pragma unroll
+                for (int j = 0; j < kWords; j += 4)
+                    o[j / 4] = make_uint4(val[i][j], val[i][j + 1], val[i][j + 2], val[i][j + 3]);
+            }
+        }
     }
 }
 
@@ -303,11 +416,91 @@ int64_t slope_slabs(int64_t B) {
     return s < 1 ? 1 : (s > 256 ? 256 : s);
 }
 
+// Compute units of the current device (asked on every call: devices of one process, such
+// as partitions of one GPU, need not have the same count).
+int cu_count() {
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) == hipSuccess &&
+        hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess &&
+        n > 0)
+        return n;
+    return 256;
+}
+
+// The chunk kernel of (kV, V), or nullptr.
+template <typename T>
+const void *chunk_kernel(int kv, int V, bool one) {
+#define TCQ_CHUNK_CASE(KV_, V_)                                                             \
+    if (kv == KV_ && V == V_)                                                               \
+        return one ? reinterpret_cast<const void *>(decode_chunks_kernel<T, KV_, V_, true>) \
+                   : reinterpret_cast<const void *>(decode_chunks_kernel<T, KV_, V_, false>);
+    TCQ_CHUNK_CASE(1, 1)
+    TCQ_CHUNK_CASE(2, 1)
+    TCQ_CHUNK_CASE(2, 2)
+    TCQ_CHUNK_CASE(3, 1)
+    TCQ_CHUNK_CASE(4, 1)
+    TCQ_CHUNK_CASE(4, 2)
+    TCQ_CHUNK_CASE(4, 4)
+    TCQ_CHUNK_CASE(6, 1)
+    TCQ_CHUNK_CASE(6, 2)
+    TCQ_CHUNK_CASE(8, 1)
+    TCQ_CHUNK_CASE(8, 2)
+    TCQ_CHUNK_CASE(8, 4)
+#undef TCQ_CHUNK_CASE
+    return nullptr;
+}
+
+// Raises the dynamic LDS limit of a kernel (the attribute is per function and device; the
+// call is a table lookup in the runtime, made on every launch).
+hipError_t allow_lds(const void *kern, size_t bytes) {
+    return hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(bytes));
+}
+
 template <typename T>
 hipError_t decode_matrix(const CodedMatrix &w, T *out, int64_t ld, hipStream_t s) {
-    DecodeArgs a{w.bits, w.s0, w.table, w.M, w.N, ld, w.L, w.k * w.V, w.V, w.T,
-                 (w.k * w.T + 31) / 32};
     if (w.M <= 0 || w.N <= 0) return hipSuccess;
+    const int kv = w.k * w.V;
+    const int nwords = (w.k * w.T + 31) / 32;
+    const int64_t chunks = w.M * (w.N / 8);
+    const size_t row = w.V * sizeof(T);
+    const size_t table = row << w.L;
+    const bool one = table <= kPartBytes;
+    const void *kern = w.T % 8 == 0 && chunks < (int64_t{1} << 31) && table % 16 == 0
+                           ? chunk_kernel<T>(kv, w.V, one)
+                           : nullptr;
+    if (kern) {
+        ChunkArgs a{};
+        a.bits = w.bits;
+        a.s0 = w.s0;
+        a.table = static_cast<const char *>(w.table);
+        a.chunks = static_cast<uint32_t>(chunks);
+        a.cpb = static_cast<uint32_t>(w.T / 8);
+        a.cpb_log2 = -1;
+        for (int b = 0; b < 16; ++b)
+            if (a.cpb == (1u << b)) a.cpb_log2 = b;
+        a.L = w.L;
+        a.nwords = nwords;
+        a.part_log2 = w.L;
+        while ((row << a.part_log2) > kPartBytes) --a.part_log2;
+        a.parts = 1 << (w.L - a.part_log2);
+        a.vec = (reinterpret_cast<uintptr_t>(w.table) & 15) == 0;
+        // the part, the row of zeros, and the room a partly filled wave of the copy writes
+        const size_t lds = (row << a.part_log2) + 1024;
+        const int64_t slots = static_cast<int64_t>(cu_count()) * (lds <= (72 << 10) ? 2 : 1);
+        int64_t grid = (chunks + kChunkThreads - 1) / kChunkThreads;
+        if (grid > slots) grid = slots;
+        a.chunks_per_wg = static_cast<uint32_t>((chunks + grid - 1) / grid);
+        grid = (chunks + a.chunks_per_wg - 1) / a.chunks_per_wg;
+        hipError_t e = allow_lds(kern, lds);
+        if (e != hipSuccess) return e;
+        T *o = out;
+        void *args[] = {&a, &o};
+        e = hipLaunchKernel(kern, dim3(static_cast<unsigned>(grid)), dim3(kChunkThreads), args,
+                            lds, s);
+        return e != hipSuccess ? e : hipGetLastError();
+    }
+    const DecodeArgs a{w.bits, w.s0, w.table, w.M, w.N, ld, w.L, kv, w.V, w.T, nwords};
     hipLaunchKernelGGL(decode_matrix_kernel<T>, dim3(grid_for(w.M * (ld / 8), 256, 1 << 20)),
                        dim3(256), 0, s, a, out);
     return hipGetLastError();
