@@ -17,50 +17,128 @@ namespace {
 
 constexpr int kGroup = 32;
 
+// Eight consecutive values per thread; four neighbouring lanes share a group.  Global
+// loads and stores of any alignment are legal on this hardware, so rows may start anywhere.
+struct Index {
+    uint32_t cpr;      // eights per row: 4 per group
+    int64_t total;     // rows x cpr
+};
+
 template <typename T>
-__global__ __launch_bounds__(256) void act_pack_kernel(const T *__restrict__ X, int64_t rows,
-                                                       int64_t cols, int64_t ldx,
-                                                       int8_t *__restrict__ codes, int64_t ldq,
-                                                       uint8_t *__restrict__ scale) {
-    const int64_t groups = (cols + kGroup - 1) / kGroup;
-    const int64_t total = rows * groups;
-    const int el = threadIdx.x & 31;
-    for (int64_t gq = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); gq < total;
-         gq += static_cast<int64_t>(gridDim.x) * 8) {
-        const int64_t r = gq / groups, g = gq - r * groups;
-        const int64_t c = g * kGroup + el;
-        const float x = c < cols ? static_cast<float>(X[r * ldx + c]) : 0.0f;
-        // magnitudes order like their bit patterns (NaN above infinity)
-        uint32_t top = __float_as_uint(x) & 0x7FFFFFFFu;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            const uint32_t other = __shfl_xor(top, o);
-            top = top > other ? top : other;
-        }
-        const int e = static_cast<int>(top >> 23);
-        float q = __builtin_rintf(__builtin_amdgcn_ldexpf(x, 133 - e));
-        q = q > 127.0f ? 127.0f : (q < -127.0f ? -127.0f : q);
-        if (e == 255) q = 0.0f;
-        if (c < cols) codes[r * ldq + c] = static_cast<int8_t>(static_cast<int>(q));
-        if (el == 0) scale[gq] = static_cast<uint8_t>(e);
+struct __attribute__((packed)) Eight {
+    T v[8];
+};
+
+// Row r and eight c of flat index i (32-bit division where the total allows it).
+template <bool SMALL>
+__device__ __forceinline__ void split(int64_t i, uint32_t cpr, int64_t &r, uint32_t &c) {
+    if constexpr (SMALL) {
+        const uint32_t q = static_cast<uint32_t>(i) / cpr;
+        r = q;
+        c = static_cast<uint32_t>(i) - q * cpr;
+    } else {
+        r = i / cpr;
+        c = static_cast<uint32_t>(i - r * cpr);
     }
 }
 
-template <typename T>
+template <typename T, bool SMALL>
+__global__ __launch_bounds__(256) void act_pack_kernel(const T *__restrict__ X, Index ix,
+                                                       int64_t cols, int64_t ldx,
+                                                       int8_t *__restrict__ codes, int64_t ldq,
+                                                       uint8_t *__restrict__ scale) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < ix.total;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        int64_t r;
+        uint32_t c;
+        split<SMALL>(i, ix.cpr, r, c);
+        const int64_t col = static_cast<int64_t>(c) * 8;
+        const int left = cols - col < 8 ? static_cast<int>(cols - col) : 8;  // may be <= 0
+        float x[8];
+        if (left == 8) {
+            const Eight<T> e = *reinterpret_cast<const Eight<T> *>(X + r * ldx + col);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = static_cast<float>(e.v[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = k < left ? static_cast<float>(X[r * ldx + col + k]) : 0.0f;
+        }
+        // magnitudes order like their bit patterns (NaN above infinity)
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t m = __float_as_uint(x[k]) & 0x7FFFFFFFu;
+            top = top > m ? top : m;
+        }
+        // the group's four lanes: total and the grid are multiples of 4, so they are here
+        // together
+        uint32_t o = __builtin_amdgcn_update_dpp(0, top, 0xB1, 0xF, 0xF, false);  // lanes 1 0 3 2
+        top = top > o ? top : o;
+        o = __builtin_amdgcn_update_dpp(0, top, 0x4E, 0xF, 0xF, false);           // lanes 2 3 0 1
+        top = top > o ? top : o;
+        const int e = static_cast<int>(top >> 23);
+        uint32_t word[2] = {0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float q = __builtin_rintf(__builtin_amdgcn_ldexpf(x[k], 133 - e));
+            q = __builtin_amdgcn_fmed3f(q, -127.0f, 127.0f);
+            const uint32_t b = e == 255 ? 0u : static_cast<uint32_t>(static_cast<int>(q)) & 0xFFu;
+            word[k / 4] |= b << (8 * (k % 4));
+        }
+        int8_t *q = codes + r * ldq + col;
+        if (left == 8) {
+            struct __attribute__((packed)) Two { uint32_t a, b; };
+            *reinterpret_cast<Two *>(q) = Two{word[0], word[1]};
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < left) q[k] = static_cast<int8_t>(word[k / 4] >> (8 * (k % 4)));
+        }
+        if ((c & 3) == 0) scale[i >> 2] = static_cast<uint8_t>(e);
+    }
+}
+
+// out's columns cols .. padded - 1 are zeros.  cpr counts the eights of a padded row.
+template <typename T, bool SMALL>
 __global__ __launch_bounds__(256) void act_unpack_kernel(const int8_t *__restrict__ codes,
                                                          int64_t ldq,
                                                          const uint8_t *__restrict__ scale,
-                                                         int64_t rows, int64_t cols,
+                                                         Index ix, int64_t cols,
                                                          T *__restrict__ out, int64_t ldo,
                                                          int64_t padded) {
     const int64_t groups = (cols + kGroup - 1) / kGroup;
-    const int64_t total = rows * padded;
-    for (int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; q < total;
-         q += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t r = q / padded, c = q - r * padded;
-        float v = 0.0f;
-        if (c < cols) v = code_value(codes[r * ldq + c], scale[r * groups + c / kGroup]);
-        out[r * ldo + c] = static_cast<T>(v);
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < ix.total;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        int64_t r;
+        uint32_t c;
+        split<SMALL>(i, ix.cpr, r, c);
+        const int64_t col = static_cast<int64_t>(c) * 8;
+        const int left = cols - col < 8 ? static_cast<int>(cols - col) : 8;  // may be <= 0
+        const int8_t *q = codes + r * ldq + col;
+        const int e = left > 0 ? scale[r * groups + (c >> 2)] : 0;
+        float v[8];
+        if (left == 8) {
+            struct __attribute__((packed)) Two { uint32_t w[2]; };
+            const Two t = *reinterpret_cast<const Two *>(q);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = code_value(static_cast<int8_t>(t.w[k / 4] >> (8 * (k % 4))), e);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = k < left ? code_value(q[k], e) : 0.0f;
+        }
+        T *o = out + r * ldo + col;
+        if (col + 8 <= padded) {
+            Eight<T> s;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s.v[k] = static_cast<T>(v[k]);
+            *reinterpret_cast<Eight<T> *>(o) = s;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (col + k < padded) o[k] = static_cast<T>(v[k]);
+        }
     }
 }
 
@@ -74,16 +152,23 @@ template <typename T>
 hipError_t pack(const void *X, int64_t rows, int64_t cols, int64_t ldx, int8_t *codes,
                 int64_t ldq, uint8_t *scale, hipStream_t s) {
     const int64_t groups = (cols + kGroup - 1) / kGroup;
-    hipLaunchKernelGGL(act_pack_kernel<T>, dim3(grid_for(rows * groups, 8)), dim3(256), 0, s,
-                       static_cast<const T *>(X), rows, cols, ldx, codes, ldq, scale);
+    const Index ix{static_cast<uint32_t>(groups * 4), rows * groups * 4};
+    const auto kern = ix.total < (int64_t{1} << 32) ? act_pack_kernel<T, true>
+                                                    : act_pack_kernel<T, false>;
+    hipLaunchKernelGGL(kern, dim3(grid_for(ix.total, 256)), dim3(256), 0, s,
+                       static_cast<const T *>(X), ix, cols, ldx, codes, ldq, scale);
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t unpack(const int8_t *codes, int64_t ldq, const uint8_t *scale, int64_t rows,
                   int64_t cols, void *out, int64_t ldo, int64_t padded, hipStream_t s) {
-    hipLaunchKernelGGL(act_unpack_kernel<T>, dim3(grid_for(rows * padded, 256)), dim3(256), 0, s,
-                       codes, ldq, scale, rows, cols, static_cast<T *>(out), ldo, padded);
+    const int64_t cpr = (padded + 7) / 8;
+    const Index ix{static_cast<uint32_t>(cpr), rows * cpr};
+    const auto kern = ix.total < (int64_t{1} << 32) ? act_unpack_kernel<T, true>
+                                                    : act_unpack_kernel<T, false>;
+    hipLaunchKernelGGL(kern, dim3(grid_for(ix.total, 256)), dim3(256), 0, s, codes, ldq, scale,
+                       ix, cols, static_cast<T *>(out), ldo, padded);
     return hipGetLastError();
 }
 
