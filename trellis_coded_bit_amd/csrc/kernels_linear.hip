@@ -262,6 +262,14 @@ struct LayerEpilogue {
         }
         store4(y + i * ldy + c.j, c.j, J, vec_y, o);
     }
+    __device__ __forceinline__ void put_one(int64_t i, int64_t j, float s) const {
+        if (i >= I || j >= J) return;
+        const float z = __builtin_fmaf(scale ? scale[j] : 1.0f, s, bias ? bias[j] : 0.0f);
+        if (pre) pre[i * ldp + j] = static_cast<T>(z);
+        float o = act_value(z, act);
+        if (res) o += static_cast<float>(res[i * ldr + j]);
+        y[i * ldy + j] = static_cast<T>(o);
+    }
 };
 
 template <typename T>
@@ -314,6 +322,137 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, int64_t K, cons
     hipLaunchKernelGGL((gemm_kernel<T, AKM, BKM, 128, 128, 2, 2, Epi>), dim3(ni * nj), dim3(256),
                        0, s, A, B, K, epi, ni, nj);
     return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- few rows of x
+
+// y for a few rows of x (at most 16 BT) with the matrix decoded inside the product: nothing
+// but the streams, x and y moves through memory.  A workgroup of 16 waves takes 16 rows of
+// the matrix at a time; the waves split its columns.  A lane of the matrix instruction's first
+// operand holds 8 consecutive columns of one row, which is a chunk: the lane decodes it
+// from the table in LDS into four registers and multiplies.  The second operand is 16 rows
+// of x, 16 bytes per lane straight from memory (any alignment), the same columns.  The
+// waves' sums meet in LDS and are added in wave order.
+// Bounded by the table reads: 8 two-byte reads at random banks per lane and step.
+constexpr int kSmallWaves = 16;
+constexpr int kSmallSteps = 4;  // steps of 32 columns in flight per wave
+
+struct SmallArgs {
+    const uint32_t *bits;
+    const uint32_t *s0;
+    const char *table;
+    const void *x;
+    int64_t B, ldx;
+    int64_t M;
+    uint32_t chunks;   // per row, N / 8
+    uint32_t bpr;      // blocks per row
+    uint32_t cpb;      // chunks per block
+    int cpb_log2;
+    int L, nwords;
+    int table_bytes;   // a power of two
+    int red;           // byte offset of the waves' sums in LDS
+    int vec;
+};
+
+template <typename T, int KV, int V, int BT>
+__global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
+                                                                 LayerEpilogue<T> epi) {
+    using C = Chunk<KV, V>;
+    using Tr = gemm::Traits<T>;
+    constexpr int HC = kSmallSteps;
+    constexpr int kLog = V == 1 ? 1 : (V == 2 ? 2 : 3);  // log2 of a table row's bytes
+    static_assert(sizeof(T) == 2, "16-bit types");
+    typedef uint32_t Words __attribute__((ext_vector_type(4)));
+    typedef uint32_t Load __attribute__((ext_vector_type(4), aligned(2)));
+    extern __shared__ __align__(16) char tab[];
+    float *red = reinterpret_cast<float *>(tab + a.red);
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int l16 = lane & 15, g = lane >> 4;
+    const uint32_t steps = (a.chunks + 3) / 4;  // of 32 columns
+    const uint32_t s_begin = wave * steps / kSmallWaves;
+    const uint32_t s_end = (wave + 1) * steps / kSmallWaves;
+    const T *xrow[BT];
+#pragma unroll
+    for (int t = 0; t < BT; ++t) {
+        // rows past B read the last one; their sums are not stored
+        const int64_t b = t * 16 + l16 < a.B ? t * 16 + l16 : a.B - 1;
+        xrow[t] = static_cast<const T *>(a.x) + b * a.ldx;
+    }
+    table_to_lds<kSmallWaves * 64>(tab, a.table, a.table_bytes, 2, a.vec, tid);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    const int64_t tiles = (a.M + 15) / 16;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t row = tile * 16 + l16 < a.M ? tile * 16 + l16 : a.M - 1;
+        const uint32_t *rbits = a.bits + row * a.bpr * a.nwords;
+        const uint32_t *rs0 = a.s0 + row * a.bpr;
+        f32x4 acc[BT];
+#pragma unroll
+        for (int t = 0; t < BT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (uint32_t s = s_begin; s < s_end; s += HC) {
+            uint32_t w[HC][C::NW + 1];
+            int q[HC];
+            bool in[HC];
+            Words xv[HC][BT];
+#pragma unroll
+            for (int i = 0; i < HC; ++i) {
+                uint32_t c = (s + i) * 4 + g;
+                in[i] = s + i < s_end && c < a.chunks;
+                c = in[i] ? c : 0;
+                const uint32_t blk = a.cpb_log2 >= 0 ? c >> a.cpb_log2 : c / a.cpb;
+                q[i] = static_cast<int>(c - blk * a.cpb);
+                chunk_words<KV, V>(rbits + static_cast<int64_t>(blk) * a.nwords, rs0 + blk, q[i],
+                                   w[i]);
+#pragma unroll
+                for (int t = 0; t < BT; ++t)
+                    xv[i][t] = *reinterpret_cast<const Load *>(xrow[t] + c * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < HC; ++i) {
+                uint32_t n[C::NW];
+                chunk_align<KV, V>(w[i], q[i], n);
+                Words val;
+                if constexpr (V == 1) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t lo = *reinterpret_cast<const uint16_t *>(
+                            tab + (chunk_state<KV, V>(n, 2 * j, a.L) << kLog));
+                        const uint32_t hi = *reinterpret_cast<const uint16_t *>(
+                            tab + (chunk_state<KV, V>(n, 2 * j + 1, a.L) << kLog));
+                        val[j] = lo | hi << 16;
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < C::kSteps; ++t)
+#pragma unroll
+                        for (int j = 0; j < V / 2; ++j)
+                            val[t * (V / 2) + j] = reinterpret_cast<const uint32_t *>(
+                                tab + (chunk_state<KV, V>(n, t, a.L) << kLog))[j];
+                }
+                if (!in[i]) val = Words{0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int t = 0; t < BT; ++t) {
+                    Words xf = xv[i][t];
+                    if (!in[i]) xf = Words{0u, 0u, 0u, 0u};
+                    acc[t] = Tr::mma(__builtin_bit_cast(gemm::s16x8, val),
+                                     __builtin_bit_cast(gemm::s16x8, xf), acc[t]);
+                }
+            }
+        }
+        // acc[t]: rows 4 g .. 4 g + 3 of the tile, row t 16 + l16 of x
+        __syncthreads();  // the previous tile's sums are read
+#pragma unroll
+        for (int t = 0; t < BT; ++t)
+            *reinterpret_cast<f32x4 *>(red + ((wave * BT + t) * 16 + l16) * 16 + g * 4) = acc[t];
+        __syncthreads();
+        for (int o = tid; o < BT * 256; o += kSmallWaves * 64) {
+            float sum = red[o];
+#pragma unroll
+            for (int v = 1; v < kSmallWaves; ++v) sum += red[v * BT * 256 + o];
+            epi.put_one(o / 16, tile * 16 + o % 16, sum);
+        }
+    }
 }
 
 // ---------------------------------------------------------------- incoming gradient
@@ -507,23 +646,7 @@ hipError_t decode_matrix(const CodedMatrix &w, T *out, int64_t ld, hipStream_t s
 }
 
 template <typename T>
-hipError_t forward(const CodedMatrix &w, const LinearCall &c, char *ws, hipStream_t s) {
-    const LinearLayout lay = linear_layout(sizeof(T), c.B, w.M, w.N);
-    T *W = reinterpret_cast<T *>(ws + lay.matrix);
-    hipError_t e = decode_matrix(w, W, lay.ldn, s);
-    if (e != hipSuccess) return e;
-    const T *x = static_cast<const T *>(c.x);
-    int64_t ldx = c.ldx, K = w.N;
-    if (w.N > 0 && !sixteen_aligned(x, ldx, w.N, sizeof(T))) {
-        T *st = reinterpret_cast<T *>(ws + lay.rows);
-        hipLaunchKernelGGL(stage_kernel<T>, dim3(grid_for(c.B * lay.ldn, 1024, 1 << 16)),
-                           dim3(256), 0, s, x, c.B, w.N, ldx, st, lay.ldn);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        x = st;
-        ldx = lay.ldn;
-        K = lay.ldn;
-    }
+LayerEpilogue<T> layer_epilogue(const CodedMatrix &w, const LinearCall &c) {
     LayerEpilogue<T> epi{};
     epi.scale = c.row_scale;
     epi.bias = c.bias;
@@ -539,6 +662,85 @@ hipError_t forward(const CodedMatrix &w, const LinearCall &c, char *ws, hipStrea
     epi.vec_y = four_aligned(epi.y, c.ldy);
     epi.vec_r = four_aligned(epi.res, c.ldr);
     epi.vec_p = four_aligned(epi.pre, c.ldp);
+    return epi;
+}
+
+template <typename T, int BT>
+const void *small_kernel_of(int kv, int V) {
+#define TCQ_SMALL_CASE(KV_, V_) \
+    if (kv == KV_ && V == V_) return reinterpret_cast<const void *>(small_kernel<T, KV_, V_, BT>);
+    TCQ_SMALL_CASE(1, 1)
+    TCQ_SMALL_CASE(2, 1)
+    TCQ_SMALL_CASE(2, 2)
+    TCQ_SMALL_CASE(3, 1)
+    TCQ_SMALL_CASE(4, 1)
+    TCQ_SMALL_CASE(4, 2)
+    TCQ_SMALL_CASE(4, 4)
+#undef TCQ_SMALL_CASE
+    return nullptr;
+}
+
+template <typename T>
+hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, const LayerEpilogue<T> &epi,
+                         hipStream_t s) {
+    SmallArgs a{};
+    a.bits = w.bits;
+    a.s0 = w.s0;
+    a.table = static_cast<const char *>(w.table);
+    a.x = c.x;
+    a.B = c.B;
+    a.ldx = c.ldx;
+    a.M = w.M;
+    a.chunks = static_cast<uint32_t>(w.N / 8);
+    a.bpr = static_cast<uint32_t>(w.N / w.T);
+    a.cpb = static_cast<uint32_t>(w.T / 8);
+    a.cpb_log2 = -1;
+    for (int b = 0; b < 16; ++b)
+        if (a.cpb == (1u << b)) a.cpb_log2 = b;
+    a.L = w.L;
+    a.nwords = (w.k * w.T + 31) / 32;
+    a.table_bytes = static_cast<int>((w.V * sizeof(T)) << w.L);
+    a.vec = (reinterpret_cast<uintptr_t>(w.table) & 15) == 0;
+    const int kv = w.k * w.V;
+    const int bt = c.B <= 16 ? 1 : 2;
+    // (a partly filled wave of the table's copy writes up to 1 KiB past it)
+    a.red = a.table_bytes < 1024 ? 1024 : a.table_bytes;
+    const size_t lds = a.red + static_cast<size_t>(kSmallWaves) * bt * 1024;
+    const void *kern = bt == 1 ? small_kernel_of<T, 1>(kv, w.V) : small_kernel_of<T, 2>(kv, w.V);
+    hipError_t e = allow_lds(kern, lds);
+    if (e != hipSuccess) return e;
+    const int64_t tiles = (w.M + 15) / 16;
+    const int64_t slots = static_cast<int64_t>(cu_count()) * (lds <= (80 << 10) ? 2 : 1);
+    LayerEpilogue<T> ep = epi;
+    void *args[] = {&a, &ep};
+    e = hipLaunchKernel(kern, dim3(static_cast<unsigned>(tiles < slots ? tiles : slots)),
+                        dim3(kSmallWaves * 64), args, lds, s);
+    return e != hipSuccess ? e : hipGetLastError();
+}
+
+template <typename T>
+hipError_t forward(const CodedMatrix &w, const LinearCall &c, char *ws, hipStream_t s) {
+    const LinearLayout lay = linear_layout(sizeof(T), c.B, w.M, w.N);
+    if constexpr (sizeof(T) == 2) {
+        if (linear_small(c.dtype, c.B, w.N, w.L, w.k, w.V, w.T))
+            return forward_small<T>(w, c, layer_epilogue<T>(w, c), s);
+    }
+    T *W = reinterpret_cast<T *>(ws + lay.matrix);
+    hipError_t e = decode_matrix(w, W, lay.ldn, s);
+    if (e != hipSuccess) return e;
+    const T *x = static_cast<const T *>(c.x);
+    int64_t ldx = c.ldx, K = w.N;
+    if (w.N > 0 && !sixteen_aligned(x, ldx, w.N, sizeof(T))) {
+        T *st = reinterpret_cast<T *>(ws + lay.rows);
+        hipLaunchKernelGGL(stage_kernel<T>, dim3(grid_for(c.B * lay.ldn, 1024, 1 << 16)),
+                           dim3(256), 0, s, x, c.B, w.N, ldx, st, lay.ldn);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        x = st;
+        ldx = lay.ldn;
+        K = lay.ldn;
+    }
+    const LayerEpilogue<T> epi = layer_epilogue<T>(w, c);
     const Operand<T> A{x, ldx, c.B, K};
     const Operand<T> Bm{W, lay.ldn, w.M, K};
     return launch_gemm<T, false, false>(A, Bm, K, epi, s);
@@ -610,6 +812,14 @@ hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStre
 size_t pad8(int64_t n) { return static_cast<size_t>((n + 7) / 8 * 8); }
 
 }  // namespace
+
+bool linear_small(int dtype, int64_t B, int64_t N, int L, int k, int V, int T) {
+    const int kv = k * V;
+    return dtype != TCQ_F32 && B <= 32 && N > 0 && T % 8 == 0 &&
+           (kv <= 4 && (V == 1 || V == 2 || (V == 4 && kv == 4))) &&
+           ((static_cast<size_t>(V) * 2) << L) <= kPartBytes &&
+           (((static_cast<size_t>(V) * 2) << L) % 16) == 0;
+}
 
 LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N) {
     LinearLayout l{};
