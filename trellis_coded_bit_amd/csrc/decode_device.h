@@ -31,9 +31,9 @@ __device__ __forceinline__ void chunk_words(const uint32_t *wb, const uint32_t *
     const int j = ((q + 1) * C::kBits - 1) >> 5;  // word of the chunk's last bit
 #pragma unroll
     for (int i = 0; i <= C::NW; ++i) {
-        const int at = j - i;
-        // (words before s_0 are past every window)
-        w[i] = at >= 0 ? wb[at] : (at == -1 ? *s0 : 0u);
+        // (words before s_0 are past every window: any value does)
+        const uint32_t *p = j - i >= 0 ? wb + (j - i) : s0;
+        w[i] = *p;
     }
 }
 
@@ -57,6 +57,36 @@ __device__ __forceinline__ uint32_t chunk_state(const uint32_t (&n)[Chunk<KV, V>
     if (off % 32 + 16 <= 32 || i + 1 >= C::NW)
         return __builtin_amdgcn_ubfe(n[i], off % 32, L);
     return __builtin_amdgcn_ubfe(__builtin_amdgcn_alignbit(n[i + 1], n[i], off % 32), 0, L);
+}
+
+// Four chunks of one run of 32 columns (K = kV / V words, word-aligned) from the run's words
+// w[1 .. K] and the word before them, w[0]: every shift is a constant.
+template <int KV, int V>
+__device__ __forceinline__ void run_align(const uint32_t (&w)[KV / V + 1], int s,
+                                          uint32_t (&n)[Chunk<KV, V>::NW]) {
+    using C = Chunk<KV, V>;
+    const int e = (s + 1) * C::kBits;
+    const int j = (e - 1) / 32, sh = (32 - e % 32) % 32;
+#pragma unroll
+    for (int i = 0; i < C::NW; ++i) {
+        // (words before w[0] are past every window)
+        const uint32_t lo = j - i >= -1 ? w[j - i + 1] : 0u;
+        const uint32_t hi = j - i - 1 >= -1 ? w[j - i] : 0u;
+        n[i] = sh ? __builtin_amdgcn_alignbit(hi, lo, sh) : lo;
+    }
+}
+
+// Registers r[s] of lane group g (16 lanes each) to registers r[g] of lane group s.
+__device__ __forceinline__ void transpose4(uint32_t &r0, uint32_t &r1, uint32_t &r2,
+                                           uint32_t &r3) {
+    auto a = __builtin_amdgcn_permlane32_swap(r0, r2, false, false);
+    auto b = __builtin_amdgcn_permlane32_swap(r1, r3, false, false);
+    auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    r0 = c[0];
+    r1 = c[1];
+    r2 = d[0];
+    r3 = d[1];
 }
 
 // `bytes` (a multiple of 16) of a table part from global memory straight into LDS, by THREADS

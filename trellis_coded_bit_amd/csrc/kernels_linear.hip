@@ -328,14 +328,20 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, int64_t K, cons
 
 // y for a few rows of x (at most 16 BT) with the matrix decoded inside the product: nothing
 // but the streams, x and y moves through memory.  A workgroup of 16 waves takes 16 rows of
-// the matrix at a time; the waves split its columns.  A lane of the matrix instruction's first
-// operand holds 8 consecutive columns of one row, which is a chunk: the lane decodes it
-// from the table in LDS into four registers and multiplies.  The second operand is 16 rows
-// of x, 16 bytes per lane straight from memory (any alignment), the same columns.  The
-// waves' sums meet in LDS and are added in wave order.
-// Bounded by the table reads: 8 two-byte reads at random banks per lane and step.
+// the matrix at a time; the waves split its columns into units of 128.
+//   Lane (row l16, group g) reads the K words of columns 32 g .. 32 g + 31 of a unit and the
+// word before them: the vector memory unit takes about four clocks per cache line of an
+// instruction, and a read per chunk (two or three words of 16 rows each) had bounded the
+// kernel (one row, 4096 x 14336 at k = 3: 45 us, now 18).  Its four chunks are aligned with
+// constant shifts and exchanged between the lane groups, so that in step s lane (l16, g)
+// holds columns 32 s + 8 g .. + 7, its piece of the matrix instruction's first operand,
+// decodes it from the table in LDS and multiplies with 16 rows of x (16-bit types: 16 bytes
+// per lane straight from memory, any alignment).  The waves' sums meet in LDS and are
+// added in wave order.
+//   A table of more than 128 KiB goes through LDS in parts; TR tiles' units are then held
+// decoded in registers while the parts pass (a step whose state lies elsewhere reads a row
+// of zeros), so that each weight is multiplied once, whatever x holds.
 constexpr int kSmallWaves = 16;
-constexpr int kSmallSteps = 4;  // steps of 32 columns in flight per wave
 
 struct SmallArgs {
     const uint32_t *bits;
@@ -344,113 +350,225 @@ struct SmallArgs {
     const void *x;
     int64_t B, ldx;
     int64_t M;
-    uint32_t chunks;   // per row, N / 8
+    uint32_t runs;     // per row, N / 32
+    uint32_t rpb;      // runs per block
+    int rpb_log2;
     uint32_t bpr;      // blocks per row
-    uint32_t cpb;      // chunks per block
-    int cpb_log2;
-    int L, nwords;
-    int table_bytes;   // a power of two
+    int L;
+    int part_bytes;    // a power of two
+    int parts;
     int red;           // byte offset of the waves' sums in LDS
     int vec;
 };
 
-template <typename T, int KV, int V, int BT>
+template <typename T, bool ONE>
+struct SmallShape {
+    static constexpr int TR = ONE || sizeof(T) == 4 ? 1 : 2;  // tiles held at a time
+    static constexpr int UN = ONE ? 1 : 2;                    // units held per tile
+};
+
+template <typename T, int KV, int V, int BT, bool ONE>
 __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
                                                                  LayerEpilogue<T> epi) {
     using C = Chunk<KV, V>;
     using Tr = gemm::Traits<T>;
-    constexpr int HC = kSmallSteps;
-    constexpr int kLog = V == 1 ? 1 : (V == 2 ? 2 : 3);  // log2 of a table row's bytes
-    static_assert(sizeof(T) == 2, "16-bit types");
-    typedef uint32_t Words __attribute__((ext_vector_type(4)));
-    typedef uint32_t Load __attribute__((ext_vector_type(4), aligned(2)));
+    constexpr int K = KV / V;
+    constexpr int TR = SmallShape<T, ONE>::TR, UN = SmallShape<T, ONE>::UN;
+    constexpr int kRow = V * static_cast<int>(sizeof(T));  // bytes of a table row
+    constexpr int kLog = kRow == 2 ? 1 : (kRow == 4 ? 2 : (kRow == 8 ? 3 : 4));
+    constexpr int kWords = 2 * static_cast<int>(sizeof(T));  // 32-bit words of a chunk
+    constexpr int kThreads = kSmallWaves * 64;
+    struct __attribute__((packed, aligned(2))) Piece { uint32_t w[kWords]; };
+    struct __attribute__((packed, aligned(4))) RunWords { uint32_t w[K]; };
     extern __shared__ __align__(16) char tab[];
     float *red = reinterpret_cast<float *>(tab + a.red);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l16 = lane & 15, g = lane >> 4;
-    const uint32_t steps = (a.chunks + 3) / 4;  // of 32 columns
-    const uint32_t s_begin = wave * steps / kSmallWaves;
-    const uint32_t s_end = (wave + 1) * steps / kSmallWaves;
+    const uint32_t units = (a.runs + 3) / 4;
+    const uint32_t u_begin = wave * units / kSmallWaves;
+    const uint32_t u_end = (wave + 1) * units / kSmallWaves;
+    // every wave takes the same number of turns: they meet at the table's parts
+    const uint32_t most = (units + kSmallWaves - 1) / kSmallWaves;
+    const uint32_t dummy = static_cast<uint32_t>(a.part_bytes);
     const T *xrow[BT];
 #pragma unroll
     for (int t = 0; t < BT; ++t) {
         // rows past B read the last one; their sums are not stored
         const int64_t b = t * 16 + l16 < a.B ? t * 16 + l16 : a.B - 1;
-        xrow[t] = static_cast<const T *>(a.x) + b * a.ldx;
+        xrow[t] = static_cast<const T *>(a.x) + b * a.ldx + g * 8;
     }
-    table_to_lds<kSmallWaves * 64>(tab, a.table, a.table_bytes, 2, a.vec, tid);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    const int64_t tiles = (a.M + 15) / 16;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t row = tile * 16 + l16 < a.M ? tile * 16 + l16 : a.M - 1;
-        const uint32_t *rbits = a.bits + row * a.bpr * a.nwords;
-        const uint32_t *rs0 = a.s0 + row * a.bpr;
-        f32x4 acc[BT];
+    auto copy = [&](int p) {
+        table_to_lds<kThreads>(tab, a.table + static_cast<int64_t>(p) * a.part_bytes,
+                               a.part_bytes, sizeof(T), a.vec, tid);
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (!ONE) {
+            if (tid < 4) reinterpret_cast<uint32_t *>(tab + a.part_bytes)[tid] = 0u;
+            __syncthreads();
+        }
+    };
+    // words of unit u of a matrix row, this lane's run of it
+    auto request = [&](const uint32_t *rbits, const uint32_t *rs0, uint32_t u,
+                       uint32_t (&w)[K + 1]) {
+        uint32_t run = u * 4 + g;
+        run = run < a.runs ? run : a.runs - 1;  // (decoded and not multiplied)
+        const uint32_t blk = a.rpb_log2 >= 0 ? run >> a.rpb_log2 : run / a.rpb;
+        const uint32_t *p = rbits + run * K;
+        const uint32_t *before = run == blk * a.rpb ? rs0 + blk : p - 1;
+        w[0] = *before;
+        const RunWords r = *reinterpret_cast<const RunWords *>(p);
 #pragma unroll
-        for (int t = 0; t < BT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (uint32_t s = s_begin; s < s_end; s += HC) {
-            uint32_t w[HC][C::NW + 1];
-            int q[HC];
-            bool in[HC];
-            Words xv[HC][BT];
+        for (int i = 0; i < K; ++i) w[i + 1] = r.w[i];
+    };
+    // the unit's four chunks as the steps need them
+    auto align = [&](const uint32_t (&w)[K + 1], uint32_t (&n)[4][C::NW]) {
 #pragma unroll
-            for (int i = 0; i < HC; ++i) {
-                uint32_t c = (s + i) * 4 + g;
-                in[i] = s + i < s_end && c < a.chunks;
-                c = in[i] ? c : 0;
-                const uint32_t blk = a.cpb_log2 >= 0 ? c >> a.cpb_log2 : c / a.cpb;
-                q[i] = static_cast<int>(c - blk * a.cpb);
-                chunk_words<KV, V>(rbits + static_cast<int64_t>(blk) * a.nwords, rs0 + blk, q[i],
-                                   w[i]);
+        for (int s = 0; s < 4; ++s) run_align<KV, V>(w, s, n[s]);
 #pragma unroll
-                for (int t = 0; t < BT; ++t)
-                    xv[i][t] = *reinterpret_cast<const Load *>(xrow[t] + c * 8);
+        for (int i = 0; i < C::NW; ++i) transpose4(n[0][i], n[1][i], n[2][i], n[3][i]);
+    };
+    auto decode = [&](const uint32_t (&n)[C::NW], uint32_t base, uint32_t (&val)[kWords]) {
+#pragma unroll
+        for (int t = 0; t < C::kSteps; ++t) {
+            uint32_t off = chunk_state<KV, V>(n, t, a.L) << kLog;
+            if (!ONE) {
+                off -= base;  // wraps below the part
+                off = off < dummy ? off : dummy;
             }
+            const char *row = tab + off;
+            if constexpr (kRow == 2) {
+                const uint32_t v = *reinterpret_cast<const uint16_t *>(row);
+                val[t / 2] |= v << (16 * (t % 2));
+            } else {
 #pragma unroll
-            for (int i = 0; i < HC; ++i) {
-                uint32_t n[C::NW];
-                chunk_align<KV, V>(w[i], q[i], n);
-                Words val;
-                if constexpr (V == 1) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t lo = *reinterpret_cast<const uint16_t *>(
-                            tab + (chunk_state<KV, V>(n, 2 * j, a.L) << kLog));
-                        const uint32_t hi = *reinterpret_cast<const uint16_t *>(
-                            tab + (chunk_state<KV, V>(n, 2 * j + 1, a.L) << kLog));
-                        val[j] = lo | hi << 16;
-                    }
-                } else {
-#pragma unroll
-                    for (int t = 0; t < C::kSteps; ++t)
-#pragma unroll
-                        for (int j = 0; j < V / 2; ++j)
-                            val[t * (V / 2) + j] = reinterpret_cast<const uint32_t *>(
-                                tab + (chunk_state<KV, V>(n, t, a.L) << kLog))[j];
-                }
-                if (!in[i]) val = Words{0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int t = 0; t < BT; ++t) {
-                    Words xf = xv[i][t];
-                    if (!in[i]) xf = Words{0u, 0u, 0u, 0u};
-                    acc[t] = Tr::mma(__builtin_bit_cast(gemm::s16x8, val),
-                                     __builtin_bit_cast(gemm::s16x8, xf), acc[t]);
-                }
+                for (int j = 0; j < kRow / 4; ++j)
+                    val[t * (kRow / 4) + j] |= reinterpret_cast<const uint32_t *>(row)[j];
             }
         }
-        // acc[t]: rows 4 g .. 4 g + 3 of the tile, row t 16 + l16 of x
-        __syncthreads();  // the previous tile's sums are read
+    };
+    auto multiply = [&](const uint32_t (&val)[kWords], const Piece &x, f32x4 acc) {
+        if constexpr (sizeof(T) == 2) {
+            struct Four { uint32_t w[4]; };
+            const Four v{{val[0], val[1], val[2], val[3]}};
+            const Four xx{{x.w[0], x.w[1], x.w[2], x.w[3]}};
+            return Tr::mma(__builtin_bit_cast(gemm::s16x8, v),
+                           __builtin_bit_cast(gemm::s16x8, xx), acc);
+        } else {
 #pragma unroll
-        for (int t = 0; t < BT; ++t)
-            *reinterpret_cast<f32x4 *>(red + ((wave * BT + t) * 16 + l16) * 16 + g * 4) = acc[t];
+            for (int j = 0; j < 8; ++j)
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                    __uint_as_float(val[j]), __uint_as_float(x.w[j]), acc, 0, 0, 0);
+            return acc;
+        }
+    };
+
+    if (ONE) copy(0);
+    const int64_t tiles = (a.M + 15) / 16;
+    for (int64_t tile0 = static_cast<int64_t>(blockIdx.x) * TR; tile0 < tiles;
+         tile0 += static_cast<int64_t>(gridDim.x) * TR) {
+        const uint32_t *rbits[TR];
+        const uint32_t *rs0[TR];
+        f32x4 acc[TR][BT];
+#pragma unroll
+        for (int r = 0; r < TR; ++r) {
+            int64_t row = (tile0 + r) * 16 + l16;
+            row = row < a.M ? row : a.M - 1;  // (not stored)
+            rbits[r] = a.bits + row * a.runs * K;
+            rs0[r] = a.s0 + row * a.bpr;
+#pragma unroll
+            for (int t = 0; t < BT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        if constexpr (ONE) {
+            uint32_t w[K + 1];
+            if (u_begin < u_end) request(rbits[0], rs0[0], u_begin, w);
+            for (uint32_t u = u_begin; u < u_end; ++u) {
+                uint32_t n[4][C::NW];
+                align(w, n);
+                // (the last turn asks for its own unit again)
+                request(rbits[0], rs0[0], u + 1 < u_end ? u + 1 : u, w);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    if (u * 4 + s < a.runs) {
+                        Piece x[BT];
+#pragma unroll
+                        for (int t = 0; t < BT; ++t)
+                            x[t] = *reinterpret_cast<const Piece *>(xrow[t] + (u * 4 + s) * 32);
+                        uint32_t val[kWords] = {};
+                        decode(n[s], 0u, val);
+#pragma unroll
+                        for (int t = 0; t < BT; ++t) acc[0][t] = multiply(val, x[t], acc[0][t]);
+                    }
+                }
+            }
+        } else {
+            for (uint32_t k0 = 0; k0 < most; k0 += UN) {
+                uint32_t n[TR][UN][4][C::NW];
+                uint32_t val[TR][UN][4][kWords];
+#pragma unroll
+                for (int r = 0; r < TR; ++r)
+#pragma unroll
+                    for (int u = 0; u < UN; ++u) {
+                        uint32_t w[K + 1];
+                        request(rbits[r], rs0[r], u_begin + k0 + u, w);
+                        align(w, n[r][u]);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+#pragma unroll
+                            for (int j = 0; j < kWords; ++j) val[r][u][s][j] = 0u;
+                    }
+                for (int p = 0; p < a.parts; ++p) {
+                    __syncthreads();  // the previous part, and the sums, are done with
+                    copy(p);
+                    const uint32_t base = static_cast<uint32_t>(p) * dummy;
+#pragma unroll
+                    for (int r = 0; r < TR; ++r)
+#pragma unroll
+                        for (int u = 0; u < UN; ++u)
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) {
+                                // (the states are extracted again for every part, one
+                                // instruction each, rather than kept in registers)
+#pragma unroll
+                                for (int i = 0; i < C::NW; ++i)
+                                    asm volatile("" : "+v"(n[r][u][s][i]));
+                                decode(n[r][u][s], base, val[r][u][s]);
+                                // (all chunks' reads at once do not fit the registers)
+                                __builtin_amdgcn_sched_barrier(0);
+                            }
+                }
+#pragma unroll
+                for (int u = 0; u < UN; ++u)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const uint32_t at = (u_begin + k0 + u) * 4 + s;
+                        if (u_begin + k0 + u < u_end && at < a.runs) {
+#pragma unroll
+                            for (int t = 0; t < BT; ++t) {
+                                const Piece x = *reinterpret_cast<const Piece *>(xrow[t] + at * 32);
+#pragma unroll
+                                for (int r = 0; r < TR; ++r)
+                                    acc[r][t] = multiply(val[r][u][s], x, acc[r][t]);
+                            }
+                        }
+                    }
+            }
+        }
+        // acc[r][t]: rows 4 g .. 4 g + 3 of the tile, row t 16 + l16 of x
+        __syncthreads();  // the previous sums (or the table's last part) are read
+#pragma unroll
+        for (int r = 0; r < TR; ++r)
+#pragma unroll
+            for (int t = 0; t < BT; ++t)
+                *reinterpret_cast<f32x4 *>(red + (((wave * TR + r) * BT + t) * 16 + l16) * 16 +
+                                           g * 4) = acc[r][t];
         __syncthreads();
-        for (int o = tid; o < BT * 256; o += kSmallWaves * 64) {
+        for (int o = tid; o < TR * BT * 256; o += kThreads) {
             float sum = red[o];
 #pragma unroll
-            for (int v = 1; v < kSmallWaves; ++v) sum += red[v * BT * 256 + o];
-            epi.put_one(o / 16, tile * 16 + o % 16, sum);
+            for (int v = 1; v < kSmallWaves; ++v) sum += red[v * TR * BT * 256 + o];
+            const int r = o / (BT * 256), i = o % (BT * 256);
+            epi.put_one(i / 16, (tile0 + r) * 16 + i % 16, sum);
         }
     }
 }
@@ -665,10 +783,13 @@ LayerEpilogue<T> layer_epilogue(const CodedMatrix &w, const LinearCall &c) {
     return epi;
 }
 
-template <typename T, int BT>
+template <typename T, int BT, bool ONE>
 const void *small_kernel_of(int kv, int V) {
-#define TCQ_SMALL_CASE(KV_, V_) \
-    if (kv == KV_ && V == V_) return reinterpret_cast<const void *>(small_kernel<T, KV_, V_, BT>);
+// (a 16-bit table of V = 1 always fits one part)
+#define TCQ_SMALL_CASE(KV_, V_)                        \
+    if constexpr (ONE || V_ > 1 || sizeof(T) == 4)     \
+        if (kv == KV_ && V == V_)                      \
+            return reinterpret_cast<const void *>(small_kernel<T, KV_, V_, BT, ONE>);
     TCQ_SMALL_CASE(1, 1)
     TCQ_SMALL_CASE(2, 1)
     TCQ_SMALL_CASE(2, 2)
@@ -681,8 +802,7 @@ const void *small_kernel_of(int kv, int V) {
 }
 
 template <typename T>
-hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, const LayerEpilogue<T> &epi,
-                         hipStream_t s) {
+hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, hipStream_t s) {
     SmallArgs a{};
     a.bits = w.bits;
     a.s0 = w.s0;
@@ -691,29 +811,41 @@ hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, const LayerE
     a.B = c.B;
     a.ldx = c.ldx;
     a.M = w.M;
-    a.chunks = static_cast<uint32_t>(w.N / 8);
+    a.runs = static_cast<uint32_t>(w.N / 32);
     a.bpr = static_cast<uint32_t>(w.N / w.T);
-    a.cpb = static_cast<uint32_t>(w.T / 8);
-    a.cpb_log2 = -1;
+    a.rpb = static_cast<uint32_t>(w.T / 32);
+    a.rpb_log2 = -1;
     for (int b = 0; b < 16; ++b)
-        if (a.cpb == (1u << b)) a.cpb_log2 = b;
+        if (a.rpb == (1u << b)) a.rpb_log2 = b;
     a.L = w.L;
-    a.nwords = (w.k * w.T + 31) / 32;
-    a.table_bytes = static_cast<int>((w.V * sizeof(T)) << w.L);
+    const size_t row = w.V * sizeof(T);
+    int plog = w.L;
+    while ((row << plog) > kPartBytes) --plog;
+    a.part_bytes = static_cast<int>(row << plog);
+    a.parts = 1 << (w.L - plog);
     a.vec = (reinterpret_cast<uintptr_t>(w.table) & 15) == 0;
     const int kv = w.k * w.V;
     const int bt = c.B <= 16 ? 1 : 2;
-    // (a partly filled wave of the table's copy writes up to 1 KiB past it)
-    a.red = a.table_bytes < 1024 ? 1024 : a.table_bytes;
-    const size_t lds = a.red + static_cast<size_t>(kSmallWaves) * bt * 1024;
-    const void *kern = bt == 1 ? small_kernel_of<T, 1>(kv, w.V) : small_kernel_of<T, 2>(kv, w.V);
+    const bool one = a.parts == 1;
+    const int tr = one || sizeof(T) == 4 ? 1 : 2;
+    const size_t sums = static_cast<size_t>(kSmallWaves) * bt * tr * 1024;
+    // One part: the sums lie behind the table (and behind the 1 KiB that a partly filled wave
+    // of its copy writes).  Several: over the table, which is read again afterwards.
+    a.red = one ? (a.part_bytes < 1024 ? 1024 : a.part_bytes) : 0;
+    const size_t lds = one ? a.red + sums : static_cast<size_t>(a.part_bytes) + 1024;
+    const void *kern;
+    if (one)
+        kern = bt == 1 ? small_kernel_of<T, 1, true>(kv, w.V) : small_kernel_of<T, 2, true>(kv, w.V);
+    else
+        kern = bt == 1 ? small_kernel_of<T, 1, false>(kv, w.V)
+                       : small_kernel_of<T, 2, false>(kv, w.V);
     hipError_t e = allow_lds(kern, lds);
     if (e != hipSuccess) return e;
-    const int64_t tiles = (w.M + 15) / 16;
+    const int64_t turns = ((w.M + 15) / 16 + tr - 1) / tr;
     const int64_t slots = static_cast<int64_t>(cu_count()) * (lds <= (80 << 10) ? 2 : 1);
-    LayerEpilogue<T> ep = epi;
-    void *args[] = {&a, &ep};
-    e = hipLaunchKernel(kern, dim3(static_cast<unsigned>(tiles < slots ? tiles : slots)),
+    LayerEpilogue<T> epi = layer_epilogue<T>(w, c);
+    void *args[] = {&a, &epi};
+    e = hipLaunchKernel(kern, dim3(static_cast<unsigned>(turns < slots ? turns : slots)),
                         dim3(kSmallWaves * 64), args, lds, s);
     return e != hipSuccess ? e : hipGetLastError();
 }
@@ -721,10 +853,7 @@ hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, const LayerE
 template <typename T>
 hipError_t forward(const CodedMatrix &w, const LinearCall &c, char *ws, hipStream_t s) {
     const LinearLayout lay = linear_layout(sizeof(T), c.B, w.M, w.N);
-    if constexpr (sizeof(T) == 2) {
-        if (linear_small(c.dtype, c.B, w.N, w.L, w.k, w.V, w.T))
-            return forward_small<T>(w, c, layer_epilogue<T>(w, c), s);
-    }
+    if (linear_small(c.B, w.N, w.k, w.V, w.T)) return forward_small<T>(w, c, s);
     T *W = reinterpret_cast<T *>(ws + lay.matrix);
     hipError_t e = decode_matrix(w, W, lay.ldn, s);
     if (e != hipSuccess) return e;
@@ -813,12 +942,9 @@ size_t pad8(int64_t n) { return static_cast<size_t>((n + 7) / 8 * 8); }
 
 }  // namespace
 
-bool linear_small(int dtype, int64_t B, int64_t N, int L, int k, int V, int T) {
+bool linear_small(int64_t B, int64_t N, int k, int V, int T) {
     const int kv = k * V;
-    return dtype != TCQ_F32 && B <= 32 && N > 0 && T % 8 == 0 &&
-           (kv <= 4 && (V == 1 || V == 2 || (V == 4 && kv == 4))) &&
-           ((static_cast<size_t>(V) * 2) << L) <= kPartBytes &&
-           (((static_cast<size_t>(V) * 2) << L) % 16) == 0;
+    return B <= 32 && N > 0 && T % 32 == 0 && kv <= 4 && (V == 1 || V == 2 || V == 4);
 }
 
 LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N) {

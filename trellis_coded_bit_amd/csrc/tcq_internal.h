@@ -141,7 +141,7 @@ struct LinearLayout {
     int64_t ldn, ldm;
 };
 // Whether a forward call runs with the matrix decoded inside the product (no workspace).
-bool linear_small(int dtype, int64_t B, int64_t N, int L, int k, int V, int T);
+bool linear_small(int64_t B, int64_t N, int k, int V, int T);
 LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N);
 LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bool dx, bool dw,
                                 bool dbias);
