@@ -7,12 +7,12 @@
 // rows contiguous (X[k][row], "k-major"); the forward product, the input's gradient and
 // the matrix's gradient are the three combinations, so no operand is transposed in memory.
 //
-// A workgroup computes a TI x TJ tile of D over K steps of 128 bytes per row (64 16-bit or
+// A workgroup computes a TI x TJ tile of D over steps of 128 bytes of k per row (64 16-bit or
 // 32 fp32 values).  Both operand tiles of a step go from global memory straight into LDS
-// (buffer_load_dwordx4 ... lds), double-buffered: the loads of step s + 1 are in flight
-// while step s is multiplied.  The buffers are separate LDS variables, and the loop is
+// (buffer_load_dwordx4 ... lds), in NB stages: the loads of the next NB - 1 steps are in
+// flight while a step is multiplied.  The stages are separate LDS variables, and the loop is
 // unrolled over them, so that the compiler sees that reads of one cannot touch the loads
-// into the other and does not wait for those.  Rows past I or J and k past K read as zeros:
+// into the others and does not wait for those.  Rows past I or J and k past K read as zeros:
 // a buffer descriptor ends with the operand's last row, and lanes past K get an offset
 // past its end.
 //
@@ -55,6 +55,7 @@ struct Operand {
 };
 
 constexpr int kStepBytes = 128;  // bytes of k per row and step
+constexpr int kPastEnd = -1;     // a step that reads as zeros
 
 template <typename T>
 struct Traits;
@@ -93,10 +94,12 @@ struct Traits<_Float16> {
 
 typedef __attribute__((address_space(3))) void *LdsPtr;
 
-// Swizzle key of k row kk of a k-major tile, in units of 32 bytes (16-bit) or 64 (fp32).
-template <typename T>
+// Swizzle key of row kk of a k-major tile of TR rows, in units of 32 bytes (16-bit) or 64
+// (fp32); a 64-row tile has four units of 32 bytes, so its key keeps two bits.
+template <typename T, int TR>
 __device__ __forceinline__ int kmajor_key(int kk) {
-    if constexpr (sizeof(T) == 2) return (kk & 3) | ((kk >> 3 & 1) << 2);
+    if constexpr (sizeof(T) == 2)
+        return ((kk & 3) | ((kk >> 3 & 1) << 2)) & (TR / 16 - 1);
     return kk >> 2 & 3;
 }
 
@@ -130,7 +133,7 @@ struct TileLoader {
                 const int kk = q / kRowChunks, s = q % kRowChunks;
                 // chunks per swizzle unit: 2 (32 bytes) or 4 (64 bytes)
                 constexpr int kUnit = sizeof(T) == 2 ? 2 : 4;
-                const int c = ((s / kUnit) ^ kmajor_key<T>(kk)) * kUnit + s % kUnit;
+                const int c = ((s / kUnit) ^ kmajor_key<T, TR>(kk)) * kUnit + s % kUnit;
                 // columns past the operand's rows: an offset past its end (zeros)
                 off[u] = row0 + c * kPer16 < o.rows
                              ? static_cast<uint32_t>(kk * o.ld * sizeof(T) + c * 16u)
@@ -151,8 +154,8 @@ struct TileLoader {
 
     // Step s's tile into lds (every wave writes its own 1 KiB pieces).
     __device__ __forceinline__ void load(char *lds, int s, int tid) const {
-        const int64_t at = s * step_bytes;
-        int64_t bytes = left - at;
+        const int64_t at = s == kPastEnd ? 0 : s * step_bytes;
+        int64_t bytes = s == kPastEnd ? 0 : left - at;
         if (bytes > 0xFFFFFF00ll) bytes = 0xFFFFFF00ll;
         if (bytes < 0) bytes = 0;
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
@@ -189,7 +192,7 @@ struct FragReader {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int kk = ks * 32 + g * 8 + h * 4 + (l16 >> 2);
-                const char *p = lds + kk * (TR * 2) + (unit ^ kmajor_key<T>(kk)) * 32 +
+                const char *p = lds + kk * (TR * 2) + (unit ^ kmajor_key<T, TR>(kk)) * 32 +
                                 (l16 & 3) * 8;
                 const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)p);
 #pragma unroll
@@ -203,7 +206,7 @@ struct FragReader {
             for (int v = 0; v < 4; ++v) {
                 const int kk = ks * 16 + g * 4 + v;
                 out[v] = *reinterpret_cast<const float *>(
-                    lds + kk * (TR * 4) + (unit ^ kmajor_key<T>(kk)) * 64 + l16 * 4);
+                    lds + kk * (TR * 4) + (unit ^ kmajor_key<T, TR>(kk)) * 64 + l16 * 4);
             }
             return out;
         }
@@ -227,12 +230,27 @@ __device__ __forceinline__ void tile_of(uint32_t wg, uint32_t ni, uint32_t nj, u
     tj = in / rows;
 }
 
-// Computes the tile and hands it out in pieces of four: Epi::Column col(epi, j) once per
-// lane, then epi.put(col, i, D[i][j .. j + 3]) for its rows; i and j may lie past I or J.
-template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, typename Epi>
+// Waits until at most LOADS of this wave's loads are in flight and its LDS accesses are
+// done, then meets the workgroup; no memory access moves across.
+template <int LOADS>
+__device__ __forceinline__ void meet() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
+}
+
+// The tile's stages in LDS, each a variable of its own.
+template <int NB>
+struct Stages {
+    char *a[NB];
+    char *b[NB];
+};
+
+// Computes the tile's sums over steps s_begin .. s_end - 1 and hands it out in pieces of
+// four: Epi::Column col(epi, j) once per lane, then epi.put(col, i, D[i][j .. j + 3]) for its
+// rows; i and j may lie past I or J.
+template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, int NB, typename Epi>
 __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> &B, int64_t i0,
-                                          int64_t j0, int64_t K, char *a0, char *a1, char *b0,
-                                          char *b1, const Epi &epi) {
+                                          int64_t j0, int s_begin, int s_end,
+                                          const Stages<NB> &st, const Epi &epi) {
     constexpr int NT = WI * WJ * 64;
     constexpr int FI = TI / WI / 16, FJ = TJ / WJ / 16;
     constexpr int kSub = Traits<T>::kSub;
@@ -256,12 +274,13 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
     // A step is kSub sub-steps of two phases, each half of the wave's rows i against all its
     // columns j.  A phase first requests the next phase's fragments, then multiplies its
     // own.  Before the last phase all waves meet: every fragment of this step is in
-    // registers then, so its buffers are refilled (step s + 2) and the next step's first
+    // registers then, so its stage is refilled (step s + NB), and the next step's first
     // fragments are read while the last phase multiplies.
     constexpr int FH = FI / 2;
     constexpr int kPhases = 2 * kSub;
     static_assert(FI % 2 == 0, "two phases per sub-step");
-    const int steps = static_cast<int>((K + Traits<T>::kStep - 1) / Traits<T>::kStep);
+    // loads in flight at a meeting: the stages after the next one
+    constexpr int kAhead = (NB - 2) * (decltype(la)::kLoads + decltype(lb)::kLoads);
     Frag fa[2][FH], fb[2][FJ];
     auto read_phase = [&](const char *ta, const char *tb, int ph) {
         const int ks = ph / 2, half = ph % 2;
@@ -281,14 +300,8 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
                 acc[half * FH + i][j] =
                     Traits<T>::mma(fb[ks % 2][j], fa[ph % 2][i], acc[half * FH + i][j]);
     };
-    // Everyone's LDS reads and LDS-direct loads are done; no access moves across.
-    auto meet = [&]() {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-    };
-    // Step s from (ta, tb); (na, nb) hold step s + 1 from the meeting on.
+    // Step s from (ta, tb); (na, nb) hold step s + 1 from the meeting on.  Steps past s_end
+    // load nothing that is there and multiply zeros.
     auto step = [&](int s, char *ta, char *tb, const char *na, const char *nb) {
 #pragma unroll
         for (int ph = 0; ph + 1 < kPhases; ++ph) {
@@ -296,35 +309,36 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
             mul_phase(ph);
             __builtin_amdgcn_sched_barrier(0);
         }
-        meet();
-        la.load(ta, s + 2, tid);
-        lb.load(tb, s + 2, tid);
+        meet<kAhead>();
+        la.load(ta, s + NB < s_end ? s + NB : kPastEnd, tid);
+        lb.load(tb, s + NB < s_end ? s + NB : kPastEnd, tid);
         read_phase(na, nb, 0);
         mul_phase(kPhases - 1);
         __builtin_amdgcn_sched_barrier(0);
     };
-    if (steps > 0) {
-        la.load(a0, 0, tid);
-        lb.load(b0, 0, tid);
-        meet();
-        la.load(a1, 1, tid);
-        lb.load(b1, 1, tid);
-        read_phase(a0, b0, 0);
-        // two steps per turn; steps past the last one multiply zeros
-        for (int s = 0; s < steps; s += 2) {
-            step(s, a0, b0, a1, b1);
-            step(s + 1, a1, b1, a0, b0);
+    if (s_begin < s_end) {
+#pragma unroll
+        for (int t = 0; t < NB; ++t) {
+            la.load(st.a[t], s_begin + t < s_end ? s_begin + t : kPastEnd, tid);
+            lb.load(st.b[t], s_begin + t < s_end ? s_begin + t : kPastEnd, tid);
         }
-        meet();  // no load into LDS outlives the tile
+        meet<(NB - 1) * (decltype(la)::kLoads + decltype(lb)::kLoads)>();
+        read_phase(st.a[0], st.b[0], 0);
+        for (int s = s_begin; s < s_end; s += NB) {
+#pragma unroll
+            for (int t = 0; t < NB; ++t)
+                step(s + t, st.a[t], st.b[t], st.a[(t + 1) % NB], st.b[(t + 1) % NB]);
+        }
+        meet<0>();  // no load into LDS outlives the tile
     }
-    // Outputs: 16 rows at a time through a piece of LDS of the wave's own (in a0, which is
-    // done with), so that a lane takes four consecutive j of always the same column group
+    // Outputs: 16 rows at a time through a piece of LDS of the wave's own (in a stage,
+    // which is done with), so that a lane takes four consecutive j of always the same column group
     // and a row leaves in one run.  The 16-byte chunks of row r are permuted by r: the 16
     // rows of a fragment otherwise start in the same bank.
     constexpr int kRow = FJ * 4;  // 16-byte chunks of a row
     static_assert(WI * WJ * FJ * 1024 <= TI * kStepBytes, "the waves' pieces fit the buffer");
     static_assert(64 % kRow == 0, "whole rows per wave and turn");
-    char *piece = a0 + wave * (FJ * 1024);
+    char *piece = st.a[0] + wave * (FJ * 1024);
     const int l16 = lane & 15, g = lane >> 4;
     const int rr = lane / kRow, rc = lane % kRow;
     const int64_t j = j0 + wj * FJ * 16 + rc * 4;

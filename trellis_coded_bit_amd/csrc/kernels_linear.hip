@@ -286,42 +286,102 @@ struct PlainEpilogue {
     }
 };
 
+// One split's share of the sums over k, in fp32: part[split][i][j], rows of ld values.
+struct PartEpilogue {
+    float *part;
+    int64_t ld, I, J;
+    struct Column {
+        int64_t j;
+        __device__ __forceinline__ Column(const PartEpilogue &, int64_t j_) : j(j_) {}
+    };
+    __device__ __forceinline__ void put(const Column &c, int64_t i, f32x4 s) const {
+        if (i < I && c.j < J) *reinterpret_cast<f32x4 *>(part + i * ld + c.j) = s;
+    }
+};
+
 // ---------------------------------------------------------------- products
 
-template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, typename Epi>
-__global__ __launch_bounds__(WI *WJ * 64) void gemm_kernel(Operand<T> A, Operand<T> B, int64_t K,
+template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, int NB, typename Epi>
+__global__ __launch_bounds__(WI *WJ * 64) void gemm_kernel(Operand<T> A, Operand<T> B,
+                                                           int steps, int steps_per_split,
                                                            Epi epi, uint32_t ni, uint32_t nj) {
+    static_assert(NB == 2 || NB == 4, "stages");
     __shared__ __align__(16) char a0[TI * gemm::kStepBytes];
     __shared__ __align__(16) char a1[TI * gemm::kStepBytes];
     __shared__ __align__(16) char b0[TJ * gemm::kStepBytes];
     __shared__ __align__(16) char b1[TJ * gemm::kStepBytes];
+    gemm::Stages<NB> st;
+    st.a[0] = a0;
+    st.a[1] = a1;
+    st.b[0] = b0;
+    st.b[1] = b1;
+    if constexpr (NB == 4) {
+        __shared__ __align__(16) char a2[TI * gemm::kStepBytes];
+        __shared__ __align__(16) char a3[TI * gemm::kStepBytes];
+        __shared__ __align__(16) char b2[TJ * gemm::kStepBytes];
+        __shared__ __align__(16) char b3[TJ * gemm::kStepBytes];
+        st.a[2] = a2;
+        st.a[3] = a3;
+        st.b[2] = b2;
+        st.b[3] = b3;
+    }
     uint32_t ti, tj;
     gemm::tile_of(blockIdx.x, ni, nj, ti, tj);
-    gemm::gemm_tile<T, AKM, BKM, TI, TJ, WI, WJ>(A, B, static_cast<int64_t>(ti) * TI,
-                                                 static_cast<int64_t>(tj) * TJ, K, a0, a1, b0,
-                                                 b1, epi);
+    const int s0 = blockIdx.y * steps_per_split;
+    const int s1 = s0 + steps_per_split < steps ? s0 + steps_per_split : steps;
+    if constexpr (__is_same(Epi, PartEpilogue))
+        epi.part += static_cast<int64_t>(blockIdx.y) * epi.I * epi.ld;
+    gemm::gemm_tile<T, AKM, BKM, TI, TJ, WI, WJ, NB>(A, B, static_cast<int64_t>(ti) * TI,
+                                                     static_cast<int64_t>(tj) * TJ, s0, s1, st,
+                                                     epi);
+}
+
+// The splits' shares added in order, four values per thread, and handed to the epilogue.
+template <typename Epi>
+__global__ __launch_bounds__(256) void split_sum_kernel(const float *__restrict__ part, int splits,
+                                                        int64_t I, int64_t ld, Epi epi) {
+    const int64_t quads = ld / 4;
+    const int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (q >= I * quads) return;
+    const int64_t i = q / quads, j = (q - i * quads) * 4;
+    const float *p = part + i * ld + j;
+    f32x4 s = *reinterpret_cast<const f32x4 *>(p);
+    for (int v = 1; v < splits; ++v) s += *reinterpret_cast<const f32x4 *>(p + v * I * ld);
+    const typename Epi::Column col(epi, j);
+    epi.put(col, i, s);
+}
+
+template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, int NB, typename Epi>
+hipError_t launch_tiles(const Operand<T> &A, const Operand<T> &B, const GemmPlan &pl,
+                        const Epi &epi, hipStream_t s) {
+    const uint32_t ni = static_cast<uint32_t>((A.rows + TI - 1) / TI);
+    const uint32_t nj = static_cast<uint32_t>((B.rows + TJ - 1) / TJ);
+    hipLaunchKernelGGL((gemm_kernel<T, AKM, BKM, TI, TJ, WI, WJ, NB, Epi>),
+                       dim3(ni * nj, static_cast<unsigned>(pl.splits)), dim3(WI * WJ * 64), 0, s,
+                       A, B, pl.steps, pl.steps_per_split, epi, ni, nj);
+    return hipGetLastError();
 }
 
 template <typename T, bool AKM, bool BKM, typename Epi>
-hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, int64_t K, const Epi &epi,
-                       hipStream_t s) {
-    const int64_t I = A.rows, J = B.rows;
-    if (I <= 0 || J <= 0) return hipSuccess;
-    const auto tiles = [&](int64_t t) { return ((I + t - 1) / t) * ((J + t - 1) / t); };
-    if constexpr (sizeof(T) == 2) {
-        if (tiles(256) >= 128) {
-            const uint32_t ni = static_cast<uint32_t>((I + 255) / 256);
-            const uint32_t nj = static_cast<uint32_t>((J + 255) / 256);
-            hipLaunchKernelGGL((gemm_kernel<T, AKM, BKM, 256, 256, 2, 4, Epi>), dim3(ni * nj),
-                               dim3(512), 0, s, A, B, K, epi, ni, nj);
-            return hipGetLastError();
-        }
+hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan &pl,
+                       const Epi &epi, char *part, hipStream_t s) {
+    if (A.rows <= 0 || B.rows <= 0) return hipSuccess;
+    if (pl.splits > 1) {
+        const PartEpilogue pe{reinterpret_cast<float *>(part), pl.part_ld, A.rows, B.rows};
+        // (only 64 x 128 tiles are split)
+        const hipError_t e = launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 4>(A, B, pl, pe, s);
+        if (e != hipSuccess) return e;
+        const int64_t quads = A.rows * (pl.part_ld / 4);
+        hipLaunchKernelGGL(split_sum_kernel<Epi>, dim3(static_cast<unsigned>((quads + 255) / 256)),
+                           dim3(256), 0, s, pe.part, pl.splits, A.rows, pl.part_ld, epi);
+        return hipGetLastError();
     }
-    const uint32_t ni = static_cast<uint32_t>((I + 127) / 128);
-    const uint32_t nj = static_cast<uint32_t>((J + 127) / 128);
-    hipLaunchKernelGGL((gemm_kernel<T, AKM, BKM, 128, 128, 2, 2, Epi>), dim3(ni * nj), dim3(256),
-                       0, s, A, B, K, epi, ni, nj);
-    return hipGetLastError();
+    if constexpr (sizeof(T) == 2) {
+        if (pl.tile == kTile256)
+            return launch_tiles<T, AKM, BKM, 256, 256, 2, 4, 2>(A, B, pl, epi, s);
+    }
+    if (pl.tile == kTile64) return launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 4>(A, B, pl, epi, s);
+    return launch_tiles<T, AKM, BKM, 128, 128, 2, 2, sizeof(T) == 2 ? 4 : 2>(A, B, pl, epi, s);
 }
 
 // ---------------------------------------------------------------- few rows of x
@@ -872,7 +932,7 @@ hipError_t forward(const CodedMatrix &w, const LinearCall &c, char *ws, hipStrea
     const LayerEpilogue<T> epi = layer_epilogue<T>(w, c);
     const Operand<T> A{x, ldx, c.B, K};
     const Operand<T> Bm{W, lay.ldn, w.M, K};
-    return launch_gemm<T, false, false>(A, Bm, K, epi, s);
+    return launch_gemm<T, false, false>(A, Bm, lay.forward, epi, ws + lay.sums, s);
 }
 
 template <typename T>
@@ -918,7 +978,7 @@ hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStre
         const Operand<T> A{S, lay.ldm, c.B, w.M > 0 ? lay.ldm : 0};
         // (columns past N are zeros and not stored; rows past M read as zeros)
         const Operand<T> Bm{W, lay.ldn, lay.ldn, w.M};
-        e = launch_gemm<T, false, true>(A, Bm, w.M, epi, s);
+        e = launch_gemm<T, false, true>(A, Bm, lay.dx, epi, ws + lay.sums, s);
         if (e != hipSuccess) return e;
     }
     if (c.dw && w.M > 0 && w.N > 0) {
@@ -932,7 +992,7 @@ hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStre
                                    four_aligned(static_cast<T *>(c.dw), c.lddw)};
         const Operand<T> A{S, lay.ldm, lay.ldm, c.B};
         const Operand<T> Bm{X, lay.ldn, lay.ldn, c.B};
-        e = launch_gemm<T, true, true>(A, Bm, c.B, epi, s);
+        e = launch_gemm<T, true, true>(A, Bm, lay.dw, epi, ws + lay.sums, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -947,12 +1007,52 @@ bool linear_small(int64_t B, int64_t N, int k, int V, int T) {
     return B <= 32 && N > 0 && T % 32 == 0 && kv <= 4 && (V == 1 || V == 2 || V == 4);
 }
 
+// Tile and splits of an I x J product over K.  The choice depends on sizes alone (and on
+// the 256 compute units of the part this library is built for), so the workspace query
+// and the call agree.
+//   256 x 256 tiles where they fill half the card: 8 waves, one workgroup per compute unit.
+//   128 x 128 where those fill the card, else 64 x 128; both keep four steps of loads in
+// flight, since few workgroups with short steps otherwise wait for memory on every step.
+//   Where 64 x 128 tiles leave compute units idle, k is split (at least 4 steps each) and
+// the shares, in fp32, are added by a second kernel.
+GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K) {
+    constexpr int64_t kCus = 256;
+    const auto tiles = [&](int64_t ti, int64_t tj) {
+        return ((I + ti - 1) / ti) * ((J + tj - 1) / tj);
+    };
+    GemmPlan p{};
+    const int64_t step = gemm::kStepBytes / static_cast<int64_t>(size);
+    p.steps = static_cast<int>((K + step - 1) / step);
+    p.splits = 1;
+    p.part_ld = (J + 3) / 4 * 4;
+    if (size == 2 && tiles(256, 256) >= kCus / 2) {
+        p.tile = kTile256;
+    } else if (tiles(128, 128) >= kCus) {
+        p.tile = kTile128;
+    } else {
+        p.tile = kTile64;
+        const int64_t n = tiles(64, 128);
+        int64_t s = n > 0 ? 2 * kCus / n : 1;
+        if (s > p.steps / 4) s = p.steps / 4;
+        if (s > 16) s = 16;
+        if (n < kCus && s > 1) p.splits = static_cast<int>(s);
+    }
+    p.steps_per_split = p.splits > 0 ? (p.steps + p.splits - 1) / p.splits : p.steps;
+    if (p.steps_per_split > 0)
+        p.splits = (p.steps + p.steps_per_split - 1) / p.steps_per_split;
+    if (p.splits < 1) p.splits = 1;
+    p.part_bytes = p.splits > 1 ? static_cast<size_t>(p.splits) * I * p.part_ld * 4 : 0;
+    return p;
+}
+
 LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N) {
     LinearLayout l{};
     l.ldn = static_cast<int64_t>(pad8(N));
     l.matrix = 0;
     l.rows = align_up(static_cast<size_t>(M) * l.ldn * size, 256);
-    l.bytes = l.rows + align_up(static_cast<size_t>(B) * l.ldn * size, 256);
+    l.sums = l.rows + align_up(static_cast<size_t>(B) * l.ldn * size, 256);
+    l.forward = gemm_plan(size, B, M, l.ldn);
+    l.bytes = l.sums + align_up(l.forward.part_bytes, 256);
     return l;
 }
 
@@ -970,6 +1070,12 @@ LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bo
     if (dw) off += align_up(static_cast<size_t>(B) * l.ldn * size, 256);
     l.part = off;
     if (dbias) off += align_up(static_cast<size_t>(slope_slabs(B)) * M * sizeof(float), 256);
+    l.sums = off;  // (the two products run one after the other)
+    l.dx = gemm_plan(size, B, l.ldn, M);
+    l.dw = gemm_plan(size, l.ldm, l.ldn, B);
+    size_t sums = dx ? l.dx.part_bytes : 0;
+    if (dw && l.dw.part_bytes > sums) sums = l.dw.part_bytes;
+    off += align_up(sums, 256);
     l.bytes = off;
     return l;
 }
