@@ -395,9 +395,10 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
 // kernel (one row, 4096 x 14336 at k = 3: 45 us, now 18).  Its four chunks are aligned with
 // constant shifts and exchanged between the lane groups, so that in step s lane (l16, g)
 // holds columns 32 s + 8 g .. + 7, its piece of the matrix instruction's first operand,
-// decodes it from the table in LDS and multiplies with 16 rows of x (16-bit types: 16 bytes
-// per lane straight from memory, any alignment).  The waves' sums meet in LDS and are
-// added in wave order.
+// decodes it from the table in LDS and multiplies with 16 rows of x.  Up to 16 rows of x
+// are read as they are (any alignment); more are first laid out by pack_rows_kernel in the
+// order the steps read them, one contiguous KiB per instruction, since reads of 16 rows cost
+// 16 cache lines each.  The waves' sums meet in LDS and are added in wave order.
 //   A table of more than 128 KiB goes through LDS in parts; TR tiles' units are then held
 // decoded in registers while the parts pass (a step whose state lies elsewhere reads a row
 // of zeros), so that each weight is multiplied once, whatever x holds.
@@ -421,11 +422,42 @@ struct SmallArgs {
     int vec;
 };
 
-template <typename T, bool ONE>
+template <typename T, int BT, bool ONE>
 struct SmallShape {
-    static constexpr int TR = ONE || sizeof(T) == 4 ? 1 : 2;  // tiles held at a time
-    static constexpr int UN = ONE ? 1 : 2;                    // units held per tile
+    // tiles held at a time, and units held per tile (by the registers)
+    static constexpr int TR = ONE || sizeof(T) == 4 || BT > 2 ? 1 : 2;
+    static constexpr int UN = ONE || (sizeof(T) == 4 && BT > 4) ? 1 : 2;
+    static constexpr int kSums = BT < 2 ? BT : 2;  // batch tiles summed at a time
 };
+
+// x as small_kernel's steps read it, for groups of 16 BT rows: the 16-byte piece p of lane l
+// for step s, batch tile t of group y is piece (((y steps + s) BT + t) P + p) 64 + l, where P is
+// the pieces of 8 values.  Rows past B are zeros.
+template <typename T, int BT>
+__global__ __launch_bounds__(256) void pack_rows_kernel(const T *__restrict__ x, int64_t B,
+                                                        int64_t ldx, uint32_t steps,
+                                                        int64_t pieces, uint4 *__restrict__ out) {
+    constexpr int P = static_cast<int>(sizeof(T)) / 2;
+    constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+    struct __attribute__((packed, aligned(2))) Raw { uint32_t w[4]; };
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < pieces;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int l = static_cast<int>(i & 63);
+        const int64_t q = i >> 6;
+        const int p = static_cast<int>(q % P);
+        const int t = static_cast<int>(q / P % BT);
+        const uint32_t at = static_cast<uint32_t>(q / (P * BT));  // group and step
+        const uint32_t y = at / steps, s = at - y * steps;
+        const int64_t b = (static_cast<int64_t>(y) * BT + t) * 16 + (l & 15);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (b < B) {
+            const Raw r = *reinterpret_cast<const Raw *>(x + b * ldx + s * 32 + (l >> 4) * 8 +
+                                                         p * kPer);
+            v = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+        }
+        out[i] = v;
+    }
+}
 
 template <typename T, int KV, int V, int BT, bool ONE>
 __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
@@ -433,7 +465,9 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
     using C = Chunk<KV, V>;
     using Tr = gemm::Traits<T>;
     constexpr int K = KV / V;
-    constexpr int TR = SmallShape<T, ONE>::TR, UN = SmallShape<T, ONE>::UN;
+    using Sh = SmallShape<T, BT, ONE>;
+    constexpr int TR = Sh::TR, UN = Sh::UN, kSums = Sh::kSums;
+    constexpr bool kPacked = BT > 1;
     constexpr int kRow = V * static_cast<int>(sizeof(T));  // bytes of a table row
     constexpr int kLog = kRow == 2 ? 1 : (kRow == 4 ? 2 : (kRow == 8 ? 3 : 4));
     constexpr int kWords = 2 * static_cast<int>(sizeof(T));  // 32-bit words of a chunk
@@ -451,13 +485,27 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
     // every wave takes the same number of turns: they meet at the table's parts
     const uint32_t most = (units + kSmallWaves - 1) / kSmallWaves;
     const uint32_t dummy = static_cast<uint32_t>(a.part_bytes);
-    const T *xrow[BT];
+    // rows past B read the last one; their sums are not stored
+    const T *xrow = static_cast<const T *>(a.x) + (l16 < a.B ? l16 : a.B - 1) * a.ldx + g * 8;
+    const uint4 *xp = static_cast<const uint4 *>(a.x) +
+                      static_cast<int64_t>(blockIdx.y) * a.runs * BT * (kWords / 4) * 64 + lane;
+    // step s's piece of batch tile t
+    auto read_x = [&](uint32_t s, int t) {
+        Piece v;
+        if constexpr (kPacked) {
 #pragma unroll
-    for (int t = 0; t < BT; ++t) {
-        // rows past B read the last one; their sums are not stored
-        const int64_t b = t * 16 + l16 < a.B ? t * 16 + l16 : a.B - 1;
-        xrow[t] = static_cast<const T *>(a.x) + b * a.ldx + g * 8;
-    }
+            for (int p = 0; p < kWords / 4; ++p) {
+                const uint4 q = xp[((s * BT + t) * (kWords / 4) + p) * 64];
+                v.w[4 * p] = q.x;
+                v.w[4 * p + 1] = q.y;
+                v.w[4 * p + 2] = q.z;
+                v.w[4 * p + 3] = q.w;
+            }
+        } else {
+            v = *reinterpret_cast<const Piece *>(xrow + s * 32);
+        }
+        return v;
+    };
     auto copy = [&](int p) {
         table_to_lds<kThreads>(tab, a.table + static_cast<int64_t>(p) * a.part_bytes,
                                a.part_bytes, sizeof(T), a.vec, tid);
@@ -553,7 +601,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
                         Piece x[BT];
 #pragma unroll
                         for (int t = 0; t < BT; ++t)
-                            x[t] = *reinterpret_cast<const Piece *>(xrow[t] + (u * 4 + s) * 32);
+                            x[t] = read_x(u * 4 + s, t);
                         uint32_t val[kWords] = {};
                         decode(n[s], 0u, val);
 #pragma unroll
@@ -605,7 +653,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
                         if (u_begin + k0 + u < u_end && at < a.runs) {
 #pragma unroll
                             for (int t = 0; t < BT; ++t) {
-                                const Piece x = *reinterpret_cast<const Piece *>(xrow[t] + at * 32);
+                                const Piece x = read_x(at, t);
 #pragma unroll
                                 for (int r = 0; r < TR; ++r)
                                     acc[r][t] = multiply(val[r][u][s], x, acc[r][t]);
@@ -615,20 +663,25 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
             }
         }
         // acc[r][t]: rows 4 g .. 4 g + 3 of the tile, row t 16 + l16 of x
-        __syncthreads();  // the previous sums (or the table's last part) are read
 #pragma unroll
-        for (int r = 0; r < TR; ++r)
+        for (int t0 = 0; t0 < BT; t0 += kSums) {
+            __syncthreads();  // the previous sums (or the table's last part) are read
 #pragma unroll
-            for (int t = 0; t < BT; ++t)
-                *reinterpret_cast<f32x4 *>(red + (((wave * TR + r) * BT + t) * 16 + l16) * 16 +
-                                           g * 4) = acc[r][t];
-        __syncthreads();
-        for (int o = tid; o < TR * BT * 256; o += kThreads) {
-            float sum = red[o];
+            for (int r = 0; r < TR; ++r)
 #pragma unroll
-            for (int v = 1; v < kSmallWaves; ++v) sum += red[v * TR * BT * 256 + o];
-            const int r = o / (BT * 256), i = o % (BT * 256);
-            epi.put_one(i / 16, (tile0 + r) * 16 + i % 16, sum);
+                for (int t = 0; t < kSums; ++t)
+                    *reinterpret_cast<f32x4 *>(
+                        red + (((wave * TR + r) * kSums + t) * 16 + l16) * 16 + g * 4) =
+                        acc[r][t0 + t];
+            __syncthreads();
+            for (int o = tid; o < TR * kSums * 256; o += kThreads) {
+                float sum = red[o];
+#pragma unroll
+                for (int v = 1; v < kSmallWaves; ++v) sum += red[v * TR * kSums * 256 + o];
+                const int r = o / (kSums * 256), i = o % (kSums * 256);
+                epi.put_one((static_cast<int64_t>(blockIdx.y) * BT + t0) * 16 + i / 16,
+                            (tile0 + r) * 16 + i % 16, sum);
+            }
         }
     }
 }
@@ -861,8 +914,8 @@ const void *small_kernel_of(int kv, int V) {
     return nullptr;
 }
 
-template <typename T>
-hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, hipStream_t s) {
+template <typename T, int BT>
+hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, char *ws, hipStream_t s) {
     SmallArgs a{};
     a.bits = w.bits;
     a.s0 = w.s0;
@@ -884,28 +937,37 @@ hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, hipStream_t 
     a.part_bytes = static_cast<int>(row << plog);
     a.parts = 1 << (w.L - plog);
     a.vec = (reinterpret_cast<uintptr_t>(w.table) & 15) == 0;
+    const int64_t groups = (c.B + 16 * BT - 1) / (16 * BT);
+    hipError_t e;
+    if (BT > 1) {
+        const int64_t pieces = groups * a.runs * BT * static_cast<int64_t>(sizeof(T) / 2) * 64;
+        hipLaunchKernelGGL((pack_rows_kernel<T, BT>), dim3(grid_for(pieces, 256, 1 << 16)),
+                           dim3(256), 0, s, static_cast<const T *>(c.x), c.B, c.ldx, a.runs,
+                           pieces, reinterpret_cast<uint4 *>(ws));
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        a.x = ws;
+    }
     const int kv = w.k * w.V;
-    const int bt = c.B <= 16 ? 1 : 2;
     const bool one = a.parts == 1;
-    const int tr = one || sizeof(T) == 4 ? 1 : 2;
-    const size_t sums = static_cast<size_t>(kSmallWaves) * bt * tr * 1024;
+    const int tr = one ? SmallShape<T, BT, true>::TR : SmallShape<T, BT, false>::TR;
+    const size_t sums =
+        static_cast<size_t>(kSmallWaves) * SmallShape<T, BT, true>::kSums * tr * 1024;
     // One part: the sums lie behind the table (and behind the 1 KiB that a partly filled wave
     // of its copy writes).  Several: over the table, which is read again afterwards.
     a.red = one ? (a.part_bytes < 1024 ? 1024 : a.part_bytes) : 0;
     const size_t lds = one ? a.red + sums : static_cast<size_t>(a.part_bytes) + 1024;
-    const void *kern;
-    if (one)
-        kern = bt == 1 ? small_kernel_of<T, 1, true>(kv, w.V) : small_kernel_of<T, 2, true>(kv, w.V);
-    else
-        kern = bt == 1 ? small_kernel_of<T, 1, false>(kv, w.V)
-                       : small_kernel_of<T, 2, false>(kv, w.V);
-    hipError_t e = allow_lds(kern, lds);
+    const void *kern = one ? small_kernel_of<T, BT, true>(kv, w.V)
+                           : small_kernel_of<T, BT, false>(kv, w.V);
+    e = allow_lds(kern, lds);
     if (e != hipSuccess) return e;
     const int64_t turns = ((w.M + 15) / 16 + tr - 1) / tr;
     const int64_t slots = static_cast<int64_t>(cu_count()) * (lds <= (80 << 10) ? 2 : 1);
     LayerEpilogue<T> epi = layer_epilogue<T>(w, c);
     void *args[] = {&a, &epi};
-    e = hipLaunchKernel(kern, dim3(static_cast<unsigned>(turns < slots ? turns : slots)),
+    e = hipLaunchKernel(kern,
+                        dim3(static_cast<unsigned>(turns < slots ? turns : slots),
+                             static_cast<unsigned>(groups)),
                         dim3(kSmallWaves * 64), args, lds, s);
     return e != hipSuccess ? e : hipGetLastError();
 }
@@ -913,7 +975,13 @@ hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, hipStream_t 
 template <typename T>
 hipError_t forward(const CodedMatrix &w, const LinearCall &c, char *ws, hipStream_t s) {
     const LinearLayout lay = linear_layout(sizeof(T), c.B, w.M, w.N);
-    if (linear_small(c.B, w.N, w.k, w.V, w.T)) return forward_small<T>(w, c, s);
+    switch (linear_small(sizeof(T), c.B, w.N, w.L, w.k, w.V, w.T)) {
+        case 1: return forward_small<T, 1>(w, c, ws, s);
+        case 2: return forward_small<T, 2>(w, c, ws, s);
+        case 4: return forward_small<T, 4>(w, c, ws, s);
+        case 8: return forward_small<T, 8>(w, c, ws, s);
+        default: break;
+    }
     T *W = reinterpret_cast<T *>(ws + lay.matrix);
     hipError_t e = decode_matrix(w, W, lay.ldn, s);
     if (e != hipSuccess) return e;
@@ -1002,9 +1070,19 @@ size_t pad8(int64_t n) { return static_cast<size_t>((n + 7) / 8 * 8); }
 
 }  // namespace
 
-bool linear_small(int64_t B, int64_t N, int k, int V, int T) {
+// Measured limits (us per call, decoded inside / through the workspace): tables of one part,
+// 4096 x 4096 in bf16, 128 rows 21 / 36, 256 rows 40 / 39; two parts, 14336 x 4096 V=2, 64 rows
+// 55 / 71, 128 rows 78 / 80.
+int linear_small(size_t size, int64_t B, int64_t N, int L, int k, int V, int T) {
     const int kv = k * V;
-    return B <= 32 && N > 0 && T % 32 == 0 && kv <= 4 && (V == 1 || V == 2 || V == 4);
+    if (N <= 0 || T % 32 != 0 || kv > 4 || (V != 1 && V != 2 && V != 4)) return 0;
+    const bool one = ((V * size) << L) <= kPartBytes;
+    if (B > (size == 2 ? (one ? 128 : 64) : 32)) return 0;
+    return B <= 16 ? 1 : (B <= 32 ? 2 : (B <= 64 ? 4 : 8));
+}
+
+size_t linear_small_bytes(size_t size, int64_t B, int64_t N, int bt) {
+    return bt > 1 ? static_cast<size_t>((B + 16 * bt - 1) / (16 * bt) * (16 * bt)) * N * size : 0;
 }
 
 // Tile and splits of an I x J product over K.  The choice depends on sizes alone (and on

@@ -151,8 +151,10 @@ struct LinearLayout {
     int64_t ldn, ldm;
     GemmPlan forward, dx, dw;
 };
-// Whether a forward call runs with the matrix decoded inside the product (no workspace).
-bool linear_small(int64_t B, int64_t N, int k, int V, int T);
+// Batch tiles of 16 rows that a forward call takes at a time with the matrix decoded inside
+// the product, or 0 where it is decoded into the workspace first.
+int linear_small(size_t size, int64_t B, int64_t N, int L, int k, int V, int T);
+size_t linear_small_bytes(size_t size, int64_t B, int64_t N, int bt);
 LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N);
 LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bool dx, bool dw,
                                 bool dbias);

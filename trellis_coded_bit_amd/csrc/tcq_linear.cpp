@@ -87,8 +87,10 @@ int check_workspace(const char *fn, const void *workspace, size_t bytes, size_t 
     return check_workspace_alignment(fn, workspace);
 }
 
-size_t forward_bytes(int dtype, int64_t B, int64_t M, int64_t N, int k, int V, int T) {
-    return linear_small(B, N, k, V, T) ? 0 : linear_layout(size_of(dtype), B, M, N).bytes;
+size_t forward_bytes(int dtype, int64_t B, int64_t M, int64_t N, int L, int k, int V, int T) {
+    const int bt = linear_small(size_of(dtype), B, N, L, k, V, T);
+    return bt ? linear_small_bytes(size_of(dtype), B, N, bt)
+              : linear_layout(size_of(dtype), B, M, N).bytes;
 }
 
 int check_pack(const char *fn, int dtype, int64_t rows, int64_t cols) {
@@ -119,7 +121,7 @@ extern "C" int tcq_decode_linear_workspace_bytes(int dtype, int64_t B, int64_t M
         set_error("%s: bytes is NULL", fn);
         return TCQ_EINVAL;
     }
-    *bytes = (B == 0 || M == 0) ? 0 : forward_bytes(dtype, B, M, N, k, V, T);
+    *bytes = (B == 0 || M == 0) ? 0 : forward_bytes(dtype, B, M, N, L, k, V, T);
     return TCQ_OK;
 }
 
@@ -163,7 +165,7 @@ extern "C" int tcq_decode_linear(const uint32_t *bitstream, const uint32_t *star
         }
     }
     rc = check_workspace(fn, workspace, workspace_bytes,
-                         forward_bytes(dtype, B, M, N, k, V, T));
+                         forward_bytes(dtype, B, M, N, L, k, V, T));
     if (rc != TCQ_OK) return rc;
     const CodedMatrix w{bitstream, start_state, codebook, M, N, L, k, V, T};
     const LinearCall c{dtype, act, x, B, ldx, row_scale, bias, residual, ldr, y, ldy, pre, ldp};
