@@ -24,11 +24,6 @@ struct Index {
     int64_t total;     // rows x cpr
 };
 
-template <typename T>
-struct __attribute__((packed)) Eight {
-    T v[8];
-};
-
 // Row r and eight c of flat index i (32-bit division where the total allows it).
 template <bool SMALL>
 __device__ __forceinline__ void split(int64_t i, uint32_t cpr, int64_t &r, uint32_t &c) {
@@ -56,7 +51,7 @@ __global__ __launch_bounds__(256) void act_pack_kernel(const T *__restrict__ X, 
         const int left = cols - col < 8 ? static_cast<int>(cols - col) : 8;  // may be <= 0
         float x[8];
         if (left == 8) {
-            const Eight<T> e = *reinterpret_cast<const Eight<T> *>(X + r * ldx + col);
+            const Packed<T> e = *reinterpret_cast<const Packed<T> *>(X + r * ldx + col);
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] = static_cast<float>(e.v[k]);
         } else {

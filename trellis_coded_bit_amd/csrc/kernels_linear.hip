@@ -253,8 +253,10 @@ struct LayerEpilogue {
 #pragma unroll
         for (int e = 0; e < 4; ++e) z[e] = __builtin_fmaf(c.a[e], s[e], c.b[e]);
         if (pre) store4(pre + i * ldp + c.j, c.j, J, vec_p, z);
+        with_act(act, [&](auto a) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = act_value(z[e], act);
+            for (int e = 0; e < 4; ++e) o[e] = act_value<decltype(a)::value>(z[e]);
+        });
         if (res) {
             const f32x4 r = load4(res + i * ldr + c.j, c.j, J, vec_r);
 #pragma unroll
@@ -266,7 +268,8 @@ struct LayerEpilogue {
         if (i >= I || j >= J) return;
         const float z = __builtin_fmaf(scale ? scale[j] : 1.0f, s, bias ? bias[j] : 0.0f);
         if (pre) pre[i * ldp + j] = static_cast<T>(z);
-        float o = act_value(z, act);
+        float o = 0.0f;
+        with_act(act, [&](auto a) { o = act_value<decltype(a)::value>(z); });
         if (res) o += static_cast<float>(res[i * ldr + j]);
         y[i * ldy + j] = static_cast<T>(o);
     }
@@ -695,40 +698,55 @@ struct SlopeArgs {
     const int8_t *zq;        // pre-activation checkpoint, or NULL (no activation)
     const uint8_t *ze;
     int64_t ldz;
-    int act;
     int64_t ld;              // of the result: a multiple of 8, columns past M are zeros
     float *part;             // [slabs][M] sums of dy act'(z) over a slab's rows, or NULL
     int64_t rows_per_slab;
 };
 
-// out = dy act'(z) scale rounded to T; part = sums over rows of dy act'(z), in fp32, rows
-// ascending within a slab (four interleaved chains, added in order).
-template <typename T>
+// out = dy act'(z) scale rounded to T; part = sums over a slab's rows of dy act'(z), in fp32
+// (each of the four waves adds every fourth row, then the four sums in order).  Eight
+// columns per thread: memory-bound but for gelu.
+template <typename T, int ACT>
 __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__ out) {
-    __shared__ float red[4][64][9];
+    __shared__ float red[4][8][65];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int64_t c0 = (static_cast<int64_t>(blockIdx.x) * 64 + lane) * 8;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.rows_per_slab;
     const int64_t r1 = r0 + a.rows_per_slab < a.B ? r0 + a.rows_per_slab : a.B;
     const T *dy = static_cast<const T *>(a.dy);
     const int64_t groups = (a.M + 31) / 32;
+    const int left = a.M - c0 < 8 ? static_cast<int>(a.M - c0) : 8;  // may be <= 0
     float sum[8], sc[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         sum[e] = 0.0f;
-        sc[e] = a.scale && c0 + e < a.M ? a.scale[c0 + e] : 1.0f;
+        sc[e] = a.scale && e < left ? a.scale[c0 + e] : 1.0f;
     }
     if (c0 < a.ld) {
+#pragma unroll 2
         for (int64_t r = r0 + w; r < r1; r += 4) {
+            Packed<T> d;
+            Packed<int8_t> z;
+            int ez = 0;
+            if (left == 8) {
+                d = *reinterpret_cast<const Packed<T> *>(dy + r * a.lddy + c0);
+                if constexpr (ACT != TCQ_ACT_NONE)
+                    z = *reinterpret_cast<const Packed<int8_t> *>(a.zq + r * a.ldz + c0);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    d.v[e] = e < left ? dy[r * a.lddy + c0 + e] : static_cast<T>(0.0f);
+                    if constexpr (ACT != TCQ_ACT_NONE)
+                        z.v[e] = e < left ? a.zq[r * a.ldz + c0 + e] : static_cast<int8_t>(0);
+                }
+            }
+            if constexpr (ACT != TCQ_ACT_NONE) ez = left > 0 ? a.ze[r * groups + c0 / 32] : 0;
             struct alignas(8 * sizeof(T)) Eight { T v[8]; } o;
-            const int ez = a.zq && c0 < a.M ? a.ze[r * groups + c0 / 32] : 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float g = 0.0f;
-                if (c0 + e < a.M) {
-                    g = static_cast<float>(dy[r * a.lddy + c0 + e]);
-                    if (a.zq) g *= act_slope(code_value(a.zq[r * a.ldz + c0 + e], ez), a.act);
-                }
+                float g = static_cast<float>(d.v[e]);
+                if constexpr (ACT != TCQ_ACT_NONE)
+                    if (e < left) g *= act_slope<ACT>(code_value(z.v[e], ez));
                 sum[e] += g;
                 o.v[e] = static_cast<T>(g * sc[e]);
             }
@@ -737,26 +755,34 @@ __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__
     }
     if (!a.part) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[w][lane][e] = sum[e];
+    for (int e = 0; e < 8; ++e) red[w][e][lane] = sum[e];
     __syncthreads();
-    if (w == 0) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (c0 + e < a.M)
-                a.part[static_cast<int64_t>(blockIdx.y) * a.M + c0 + e] =
-                    ((red[0][lane][e] + red[1][lane][e]) + red[2][lane][e]) + red[3][lane][e];
+    for (int i = threadIdx.x; i < 512; i += 256) {
+        const int l = i >> 3, e = i & 7;
+        const int64_t c = static_cast<int64_t>(blockIdx.x) * 512 + i;
+        if (c < a.M)
+            a.part[static_cast<int64_t>(blockIdx.y) * a.M + c] =
+                ((red[0][e][l] + red[1][e][l]) + red[2][e][l]) + red[3][e][l];
     }
 }
 
-// sum[c] = part[0][c] + part[1][c] + ... in order.
+// sum[c] = part[0][c] + part[1][c] + ...: each of four waves adds a run of slabs in order, then
+// the four sums in order; 64 columns per workgroup.
 __global__ __launch_bounds__(256) void slab_sum_kernel(const float *__restrict__ part,
                                                        int64_t slabs, int64_t M,
                                                        float *__restrict__ sum) {
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (c >= M) return;
+    __shared__ float red[4][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+    const int64_t i0 = w * slabs / 4, i1 = (w + 1) * slabs / 4;
     float s = 0.0f;
-    for (int64_t i = 0; i < slabs; ++i) s += part[i * M + c];
-    sum[c] = s;
+    if (c < M) {
+#pragma unroll 8
+        for (int64_t i = i0; i < i1; ++i) s += part[i * M + c];
+    }
+    red[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && c < M) sum[c] = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
 }
 
 // ---------------------------------------------------------------- host side
@@ -781,9 +807,23 @@ unsigned grid_for(int64_t work, int64_t per, int64_t most) {
     return static_cast<unsigned>(g < 1 ? 1 : g);
 }
 
-int64_t slope_slabs(int64_t B) {
-    const int64_t s = (B + 63) / 64;
-    return s < 1 ? 1 : (s > 256 ? 256 : s);
+// Row slabs of the incoming gradient's pass: about 1024 workgroups of 512 columns, at least
+// eight rows each.
+int64_t slope_slabs(int64_t B, int64_t M) {
+    const int64_t cols = (M + 511) / 512;
+    int64_t s = cols > 0 ? (1024 + cols - 1) / cols : 1;
+    if (s > (B + 7) / 8) s = (B + 7) / 8;
+    return s < 1 ? 1 : s;
+}
+
+template <typename T>
+const void *slope_kernel_of(int act) {
+    switch (act) {
+        case TCQ_ACT_RELU: return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_RELU>);
+        case TCQ_ACT_SILU: return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_SILU>);
+        case TCQ_ACT_GELU: return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_GELU>);
+        default: return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_NONE>);
+    }
 }
 
 // Compute units of the current device (asked on every call: devices of one process, such
@@ -1008,7 +1048,7 @@ hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStre
     const LinearLayout lay = linear_grad_layout(sizeof(T), c.B, w.M, w.N, c.dx, c.dw, c.dbias);
     hipError_t e;
     T *S = reinterpret_cast<T *>(ws + lay.grad);
-    const int64_t slabs = slope_slabs(c.B);
+    const int64_t slabs = slope_slabs(c.B, w.M);
     if (c.B > 0 && w.M > 0) {
         SlopeArgs a{};
         a.dy = c.dy;
@@ -1016,22 +1056,22 @@ hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStre
         a.M = w.M;
         a.lddy = c.lddy;
         a.scale = c.row_scale;
-        a.zq = c.act == TCQ_ACT_NONE ? nullptr : c.zq;
+        a.zq = c.zq;
         a.ze = c.ze;
         a.ldz = c.ldz;
-        a.act = c.act;
         a.ld = lay.ldm;
         a.part = c.dbias ? reinterpret_cast<float *>(ws + lay.part) : nullptr;
         a.rows_per_slab = (c.B + slabs - 1) / slabs;
-        hipLaunchKernelGGL(slope_kernel<T>,
-                           dim3(static_cast<unsigned>((lay.ldm / 8 + 63) / 64),
-                                static_cast<unsigned>(slabs)),
-                           dim3(256), 0, s, a, c.dx || c.dw ? S : nullptr);
-        e = hipGetLastError();
+        T *out = c.dx || c.dw ? S : nullptr;
+        void *args[] = {&a, &out};
+        e = hipLaunchKernel(slope_kernel_of<T>(c.act),
+                            dim3(static_cast<unsigned>((lay.ldm / 8 + 63) / 64),
+                                 static_cast<unsigned>(slabs)),
+                            dim3(256), args, 0, s);
         if (e != hipSuccess) return e;
     }
     if (c.dbias && w.M > 0) {
-        hipLaunchKernelGGL(slab_sum_kernel, dim3(static_cast<unsigned>((w.M + 255) / 256)),
+        hipLaunchKernelGGL(slab_sum_kernel, dim3(static_cast<unsigned>((w.M + 63) / 64)),
                            dim3(256), 0, s, reinterpret_cast<const float *>(ws + lay.part),
                            c.B > 0 ? slabs : 0, w.M, c.dbias);
         e = hipGetLastError();
@@ -1072,12 +1112,12 @@ size_t pad8(int64_t n) { return static_cast<size_t>((n + 7) / 8 * 8); }
 
 // Measured limits (us per call, decoded inside / through the workspace): tables of one part,
 // 4096 x 4096 in bf16, 128 rows 21 / 36, 256 rows 40 / 39; two parts, 14336 x 4096 V=2, 64 rows
-// 55 / 71, 128 rows 78 / 80.
+// 55 / 71, 128 rows 78 / 80; fp32, 4096 x 4096, 128 rows 62 / 77, 256 rows 116 / 112.
 int linear_small(size_t size, int64_t B, int64_t N, int L, int k, int V, int T) {
     const int kv = k * V;
     if (N <= 0 || T % 32 != 0 || kv > 4 || (V != 1 && V != 2 && V != 4)) return 0;
     const bool one = ((V * size) << L) <= kPartBytes;
-    if (B > (size == 2 ? (one ? 128 : 64) : 32)) return 0;
+    if (B > (size == 4 || one ? 128 : 64)) return 0;
     return B <= 16 ? 1 : (B <= 32 ? 2 : (B <= 64 ? 4 : 8));
 }
 
@@ -1147,7 +1187,7 @@ LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bo
     l.rows = off;
     if (dw) off += align_up(static_cast<size_t>(B) * l.ldn * size, 256);
     l.part = off;
-    if (dbias) off += align_up(static_cast<size_t>(slope_slabs(B)) * M * sizeof(float), 256);
+    if (dbias) off += align_up(static_cast<size_t>(slope_slabs(B, M)) * M * sizeof(float), 256);
     l.sums = off;  // (the two products run one after the other)
     l.dx = gemm_plan(size, B, l.ldn, M);
     l.dw = gemm_plan(size, l.ldm, l.ldn, B);
