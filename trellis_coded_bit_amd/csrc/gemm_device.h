@@ -10,7 +10,7 @@
 // A workgroup computes a TI x TJ tile of D over steps of 128 bytes of k per row (64 16-bit or
 // 32 fp32 values).  Both operand tiles of a step go from global memory straight into LDS
 // (buffer_load_dwordx4 ... lds), in NB stages: the loads of the next NB - 1 steps are in
-// flight while a step is multiplied.  The stages are separate LDS variables, and the loop is
+// flight while a step is multiplied (or in a ring of five pieces).  The stages are separate LDS variables, and the loop is
 // unrolled over them, so that the compiler sees that reads of one cannot touch the loads
 // into the others and does not wait for those.  Rows past I or J and k past K read as zeros:
 // a buffer descriptor ends with the operand's last row, and lanes past K get an offset
@@ -32,6 +32,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 namespace tcq {
 namespace gemm {
@@ -237,11 +238,19 @@ __device__ __forceinline__ void meet() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS) : "memory");
 }
 
-// The tile's stages in LDS, each a variable of its own.
+// The tile's stages in LDS, each a variable of its own.  kRing: five pieces, one operand's
+// tile each, that hold A(0) B(0) A(1) B(1) A(2) and go round: tile n is in piece n % 5.
+constexpr int kRing = 5;
 template <int NB>
 struct Stages {
     char *a[NB];
     char *b[NB];
+};
+template <>
+struct Stages<kRing> {
+    char *p[kRing];
+    // (the pieces of the outputs)
+    char *a[1];
 };
 
 // Computes the tile's sums over steps s_begin .. s_end - 1 and hands it out in pieces of
@@ -279,8 +288,6 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
     constexpr int FH = FI / 2;
     constexpr int kPhases = 2 * kSub;
     static_assert(FI % 2 == 0, "two phases per sub-step");
-    // loads in flight at a meeting: the stages after the next one
-    constexpr int kAhead = (NB - 2) * (decltype(la)::kLoads + decltype(lb)::kLoads);
     Frag fa[2][FH], fb[2][FJ];
     auto read_phase = [&](const char *ta, const char *tb, int ph) {
         const int ks = ph / 2, half = ph % 2;
@@ -300,36 +307,80 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
                 acc[half * FH + i][j] =
                     Traits<T>::mma(fb[ks % 2][j], fa[ph % 2][i], acc[half * FH + i][j]);
     };
-    // Step s from (ta, tb); (na, nb) hold step s + 1 from the meeting on.  Steps past s_end
-    // load nothing that is there and multiply zeros.
-    auto step = [&](int s, char *ta, char *tb, const char *na, const char *nb) {
+    constexpr int kLoadsA = decltype(la)::kLoads, kLoadsB = decltype(lb)::kLoads;
+    // (a step past s_end loads nothing that is there)
+    auto valid = [&](int s) { return s < s_end ? s : kPastEnd; };
+    if constexpr (NB == kRing) {
+        // Two whole steps of a 256 x 256 tile take 128 of the 160 KiB of LDS, and with two
+        // stages every load has one step to arrive.  Five pieces give A two steps: B(s + 2)
+        // goes into A(s)'s piece after the meeting of step s, A(s + 3) into B(s)'s in the
+        // first phase of step s + 1, so the loads are also spread (8192 x 4096 x 14336 in
+        // bf16: 815 us with two stages, 760 with the ring).
+        auto step = [&](int s, auto turn) {
+            constexpr int t = 2 * decltype(turn)::value;
+            char *sa = st.p[t % 5], *sb = st.p[(t + 1) % 5];
+            const char *na = st.p[(t + 2) % 5], *nb = st.p[(t + 3) % 5];
+            la.load(st.p[(t + 4) % 5], valid(s + 2), tid);
 #pragma unroll
-        for (int ph = 0; ph + 1 < kPhases; ++ph) {
-            read_phase(ta, tb, ph + 1);
-            mul_phase(ph);
+            for (int ph = 0; ph + 1 < kPhases; ++ph) {
+                read_phase(sa, sb, ph + 1);
+                mul_phase(ph);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            meet<kLoadsA>();
+            lb.load(sa, valid(s + 2), tid);
+            read_phase(na, nb, 0);
+            mul_phase(kPhases - 1);
             __builtin_amdgcn_sched_barrier(0);
+        };
+        if (s_begin < s_end) {
+            la.load(st.p[0], s_begin, tid);
+            lb.load(st.p[1], s_begin, tid);
+            la.load(st.p[2], valid(s_begin + 1), tid);
+            lb.load(st.p[3], valid(s_begin + 1), tid);
+            meet<kLoadsA + kLoadsB>();
+            read_phase(st.p[0], st.p[1], 0);
+            for (int s = s_begin; s < s_end; s += 5) {
+                step(s, std::integral_constant<int, 0>{});
+                if (s + 1 < s_end) step(s + 1, std::integral_constant<int, 1>{});
+                if (s + 2 < s_end) step(s + 2, std::integral_constant<int, 2>{});
+                if (s + 3 < s_end) step(s + 3, std::integral_constant<int, 3>{});
+                if (s + 4 < s_end) step(s + 4, std::integral_constant<int, 4>{});
+            }
+            meet<0>();  // no load into LDS outlives the tile
         }
-        meet<kAhead>();
-        la.load(ta, s + NB < s_end ? s + NB : kPastEnd, tid);
-        lb.load(tb, s + NB < s_end ? s + NB : kPastEnd, tid);
-        read_phase(na, nb, 0);
-        mul_phase(kPhases - 1);
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    if (s_begin < s_end) {
+    } else {
+        // Step s from (ta, tb); (na, nb) hold step s + 1 from the meeting on.  Steps past
+        // s_end multiply zeros.  At a meeting the stages after the next one are in flight.
+        auto step = [&](int s, char *ta, char *tb, const char *na, const char *nb) {
 #pragma unroll
-        for (int t = 0; t < NB; ++t) {
-            la.load(st.a[t], s_begin + t < s_end ? s_begin + t : kPastEnd, tid);
-            lb.load(st.b[t], s_begin + t < s_end ? s_begin + t : kPastEnd, tid);
-        }
-        meet<(NB - 1) * (decltype(la)::kLoads + decltype(lb)::kLoads)>();
-        read_phase(st.a[0], st.b[0], 0);
-        for (int s = s_begin; s < s_end; s += NB) {
+            for (int ph = 0; ph + 1 < kPhases; ++ph) {
+                read_phase(ta, tb, ph + 1);
+                mul_phase(ph);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            meet<(NB - 2) * (kLoadsA + kLoadsB)>();
+            la.load(ta, valid(s + NB), tid);
+            lb.load(tb, valid(s + NB), tid);
+            read_phase(na, nb, 0);
+            mul_phase(kPhases - 1);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        if (s_begin < s_end) {
 #pragma unroll
-            for (int t = 0; t < NB; ++t)
-                step(s + t, st.a[t], st.b[t], st.a[(t + 1) % NB], st.b[(t + 1) % NB]);
+            for (int t = 0; t < NB; ++t) {
+                la.load(st.a[t], valid(s_begin + t), tid);
+                lb.load(st.b[t], valid(s_begin + t), tid);
+            }
+            meet<(NB - 1) * (kLoadsA + kLoadsB)>();
+            read_phase(st.a[0], st.b[0], 0);
+            for (int s = s_begin; s < s_end; s += NB) {
+#pragma unroll
+                for (int t = 0; t < NB; ++t)
+                    step(s + t, st.a[t], st.b[t], st.a[(t + 1) % NB], st.b[(t + 1) % NB]);
+            }
+            meet<0>();  // no load into LDS outlives the tile
         }
-        meet<0>();  // no load into LDS outlives the tile
     }
     // Outputs: 16 rows at a time through a piece of LDS of the wave's own (in a stage,
     // which is done with), so that a lane takes four consecutive j of always the same column group

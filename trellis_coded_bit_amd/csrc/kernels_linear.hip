@@ -308,16 +308,26 @@ template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, int NB
 __global__ __launch_bounds__(WI *WJ * 64) void gemm_kernel(Operand<T> A, Operand<T> B,
                                                            int steps, int steps_per_split,
                                                            Epi epi, uint32_t ni, uint32_t nj) {
-    static_assert(NB == 2 || NB == 4, "stages");
+    static_assert(NB == 2 || NB == 4 || NB == gemm::kRing, "stages");
     __shared__ __align__(16) char a0[TI * gemm::kStepBytes];
     __shared__ __align__(16) char a1[TI * gemm::kStepBytes];
     __shared__ __align__(16) char b0[TJ * gemm::kStepBytes];
     __shared__ __align__(16) char b1[TJ * gemm::kStepBytes];
     gemm::Stages<NB> st;
     st.a[0] = a0;
-    st.a[1] = a1;
-    st.b[0] = b0;
-    st.b[1] = b1;
+    if constexpr (NB == gemm::kRing) {
+        static_assert(TI == TJ, "pieces of one size");
+        __shared__ __align__(16) char a2[TI * gemm::kStepBytes];
+        st.p[0] = a0;
+        st.p[1] = b0;
+        st.p[2] = a1;
+        st.p[3] = b1;
+        st.p[4] = a2;
+    } else {
+        st.a[1] = a1;
+        st.b[0] = b0;
+        st.b[1] = b1;
+    }
     if constexpr (NB == 4) {
         __shared__ __align__(16) char a2[TI * gemm::kStepBytes];
         __shared__ __align__(16) char a3[TI * gemm::kStepBytes];
@@ -381,7 +391,7 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
     }
     if constexpr (sizeof(T) == 2) {
         if (pl.tile == kTile256)
-            return launch_tiles<T, AKM, BKM, 256, 256, 2, 4, 2>(A, B, pl, epi, s);
+            return launch_tiles<T, AKM, BKM, 256, 256, 2, 4, gemm::kRing>(A, B, pl, epi, s);
     }
     if (pl.tile == kTile64) return launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 4>(A, B, pl, epi, s);
     return launch_tiles<T, AKM, BKM, 128, 128, 2, 2, sizeof(T) == 2 ? 4 : 2>(A, B, pl, epi, s);
