@@ -183,6 +183,12 @@ def _on(device: torch.device):
     return torch.cuda.device(device)
 
 
+def _stream_of(device: torch.device) -> int:
+    """The device's current stream, without the Stream object that the public query builds
+    (2.7 us of a 12 us call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _rows(t: torch.Tensor, name: str, rows: int, cols: int, dtype: torch.dtype,
           device: torch.device) -> int:
     """Checks a rows x cols matrix whose rows are contiguous; its leading dimension."""
@@ -246,7 +252,7 @@ def decode_linear(bitstream: torch.Tensor, start_state: torch.Tensor, codebook: 
             M if residual is None else _rows(residual, "residual", B, M, dt, dev),
             y.data_ptr(), ldy, None if z is None else z.data_ptr(), M,
             None if workspace is None else workspace.ptr,
-            0 if workspace is None else workspace.nbytes, _stream())
+            0 if workspace is None else workspace.nbytes, _stream_of(dev))
     return y if z is None else (y, z)
 
 
@@ -273,10 +279,12 @@ def act_pack(x: torch.Tensor) -> Packed:
     with _on(x.device):
         # rows start on whole groups
         ldq = groups * CHECKPOINT_GROUP
-        codes = torch.empty((rows, ldq), dtype=torch.int8, device=x.device)[:, :cols]
+        codes = torch.empty((rows, ldq), dtype=torch.int8, device=x.device)
+        if ldq != cols:
+            codes = codes[:, :cols]
         scale = torch.empty((rows, groups), dtype=torch.uint8, device=x.device)
         _lib.tcq_act_pack(x.data_ptr(), _DTYPES[x.dtype], rows, cols, ldx, codes.data_ptr(),
-                          max(ldq, 1), scale.data_ptr(), _stream())
+                          max(ldq, 1), scale.data_ptr(), _stream_of(x.device))
     return Packed(codes, scale)
 
 
@@ -289,7 +297,7 @@ def act_unpack(packed: Packed, dtype: torch.dtype) -> torch.Tensor:
     with _on(dev):
         out = torch.empty((rows, cols), dtype=dtype, device=dev)
         _lib.tcq_act_unpack(packed.codes.data_ptr(), ldq, packed.scale.data_ptr(), rows, cols,
-                            _DTYPES[dtype], out.data_ptr(), max(cols, 1), _stream())
+                            _DTYPES[dtype], out.data_ptr(), max(cols, 1), _stream_of(dev))
     return out
 
 
@@ -339,5 +347,5 @@ def decode_linear_backward(bitstream: torch.Tensor, start_state: torch.Tensor,
                 None if gx is None else gx.data_ptr(), N, None if gw is None else gw.data_ptr(),
                 N, None if gb is None else gb.data_ptr(),
                 None if workspace is None else workspace.ptr,
-                0 if workspace is None else workspace.nbytes, _stream())
+                0 if workspace is None else workspace.nbytes, _stream_of(dev))
     return gx, gw, gb
