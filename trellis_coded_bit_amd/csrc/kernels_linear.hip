@@ -78,6 +78,7 @@ struct ChunkArgs {
     const char *table;
     uint32_t chunks;         // of the matrix
     uint32_t chunks_per_wg;
+    int rows;                // chunks per thread and turn
     uint32_t cpb;            // chunks per block
     int cpb_log2;            // log2(cpb), or -1
     int L, nwords;
@@ -89,17 +90,18 @@ struct ChunkArgs {
 constexpr int kChunkThreads = 1024;
 constexpr int kPartBytes = 128 << 10;
 
-// Chunks a thread holds at a time: each keeps its values over the passes.
-template <typename T, int KV, int V>
+// Chunks a thread holds at a time: each keeps its values over the passes, so more of them
+// mean fewer copies of the table (14336 x 4096, V = 2, 16 bits: 43 us with 8, 35 with 14).
+template <typename T, bool ONE>
 constexpr int chunk_rows() {
-    return sizeof(T) == 2 ? 8 : 4;
+    return sizeof(T) == 4 ? (ONE ? 4 : 8) : (ONE ? 8 : 14);
 }
 
 template <typename T, int KV, int V, bool ONE>
 __global__ __launch_bounds__(kChunkThreads) void decode_chunks_kernel(ChunkArgs a,
                                                                       T *__restrict__ out) {
     using C = Chunk<KV, V>;
-    constexpr int RT = chunk_rows<T, KV, V>();
+    constexpr int RT = chunk_rows<T, ONE>();
     constexpr int kRowBytes = V * static_cast<int>(sizeof(T));
     constexpr int kLog = kRowBytes == 2 ? 1 : (kRowBytes == 4 ? 2 : (kRowBytes == 8 ? 3 : 4));
     constexpr int kWords = 8 * static_cast<int>(sizeof(T)) / 4;  // 32-bit words of a chunk
@@ -119,57 +121,76 @@ __global__ __launch_bounds__(kChunkThreads) void decode_chunks_kernel(ChunkArgs 
             __syncthreads();
         }
     };
-    if (ONE) copy(0);
-    for (uint32_t t0 = begin; t0 < end; t0 += kChunkThreads * RT) {
-        uint32_t n[RT][C::NW];
+    // the values of chunk words n whose states lie in the part that starts at `base`
+    auto decode = [&](const uint32_t (&n)[C::NW], uint32_t base, uint32_t (&val)[kWords]) {
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            uint32_t g = t0 + i * kChunkThreads + tid;
-            g = g < end ? g : begin;  // (decoded again and not stored)
-            const uint32_t blk = a.cpb_log2 >= 0 ? g >> a.cpb_log2 : g / a.cpb;
-            const int q = static_cast<int>(g - blk * a.cpb);
-            uint32_t w[C::NW + 1];
-            chunk_words<KV, V>(a.bits + static_cast<int64_t>(blk) * a.nwords, a.s0 + blk, q, w);
-            chunk_align<KV, V>(w, q, n[i]);
+        for (int t = 0; t < C::kSteps; ++t) {
+            uint32_t off = chunk_state<KV, V>(n, t, a.L) << kLog;
+            if (!ONE) {
+                off -= base;  // wraps below the part
+                off = off < dummy ? off : dummy;
+            }
+            const char *row = tab + off;
+            if constexpr (kRowBytes == 2) {
+                const uint32_t v = *reinterpret_cast<const uint16_t *>(row);
+                val[t / 2] |= v << (16 * (t % 2));
+            } else {
+#pragma unroll
+                for (int j = 0; j < kRowBytes / 4; ++j)
+                    val[t * (kRowBytes / 4) + j] |= reinterpret_cast<const uint32_t *>(row)[j];
+            }
         }
+    };
+    if (ONE) copy(0);
+    int first = 0;  // the tile's first part: the one the previous tile ended with
+    for (uint32_t t0 = begin; t0 < end; t0 += kChunkThreads * a.rows) {
+        uint32_t n[RT][C::NW];
         uint32_t val[RT][kWords];
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
+        for (int i = 0; i < RT; ++i) {
+            if (i < a.rows) {
+                uint32_t g = t0 + i * kChunkThreads + tid;
+                g = g < end ? g : begin;  // (decoded again and not stored)
+                const uint32_t blk = a.cpb_log2 >= 0 ? g >> a.cpb_log2 : g / a.cpb;
+                const int q = static_cast<int>(g - blk * a.cpb);
+                uint32_t w[C::NW + 1];
+                chunk_words<KV, V>(a.bits + static_cast<int64_t>(blk) * a.nwords, a.s0 + blk, q,
+                                   w);
+                chunk_align<KV, V>(w, q, n[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < C::NW; ++j) n[i][j] = 0u;
+            }
 #pragma unroll
             for (int j = 0; j < kWords; ++j) val[i][j] = 0u;
+        }
         const int parts = ONE ? 1 : a.parts;
-        for (int p = 0; p < parts; ++p) {
-            if (!ONE) {
+        for (int v = 0; v < parts; ++v) {
+            const int p = first == 0 ? v : parts - 1 - v;
+            if (!ONE && (v > 0 || t0 == begin)) {
                 __syncthreads();  // the previous part is done with
                 copy(p);
             }
             const uint32_t base = static_cast<uint32_t>(p) * dummy;
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
+                if (i < a.rows) {
+                    if constexpr (!ONE) {
+                        // (the states are extracted again for every part, one instruction
+                        // each, rather than kept in registers)
 #pragma unroll
-                for (int t = 0; t < C::kSteps; ++t) {
-                    uint32_t off = chunk_state<KV, V>(n[i], t, a.L) << kLog;
-                    if (!ONE) {
-                        off -= base;  // wraps below the part
-                        off = off < dummy ? off : dummy;
+                        for (int j = 0; j < C::NW; ++j) asm volatile("" : "+v"(n[i][j]));
                     }
-                    const char *row = tab + off;
-                    if constexpr (kRowBytes == 2) {
-                        const uint32_t v = *reinterpret_cast<const uint16_t *>(row);
-                        val[i][t / 2] |= v << (16 * (t % 2));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kRowBytes / 4; ++j)
-                            val[i][t * (kRowBytes / 4) + j] |=
-                                reinterpret_cast<const uint32_t *>(row)[j];
-                    }
+                    decode(n[i], base, val[i]);
+                    if constexpr (!ONE) __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
+        first = first == 0 ? parts - 1 : 0;
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             const uint32_t g = t0 + i * kChunkThreads + tid;
-            if (g < end) {
+            if (i < a.rows && g < end) {
                 uint4 *o = reinterpret_cast<uint4 *>(out + static_cast<int64_t>(g) * 8);
 #pragma unroll
                 for (int j = 0; j < kWords; j += 4)
@@ -382,7 +403,7 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
     if (pl.splits > 1) {
         const PartEpilogue pe{reinterpret_cast<float *>(part), pl.part_ld, A.rows, B.rows};
         // (only 64 x 128 tiles are split)
-        const hipError_t e = launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 4>(A, B, pl, pe, s);
+        const hipError_t e = launch_tiles<T, AKM, BKM, 64, 128, 1, 4, sizeof(T) == 2 ? 4 : 2>(A, B, pl, pe, s);
         if (e != hipSuccess) return e;
         const int64_t quads = A.rows * (pl.part_ld / 4);
         hipLaunchKernelGGL(split_sum_kernel<Epi>, dim3(static_cast<unsigned>((quads + 255) / 256)),
@@ -393,7 +414,7 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
         if (pl.tile == kTile256)
             return launch_tiles<T, AKM, BKM, 256, 256, 2, 4, gemm::kRing>(A, B, pl, epi, s);
     }
-    if (pl.tile == kTile64) return launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 4>(A, B, pl, epi, s);
+    if (pl.tile == kTile64) return launch_tiles<T, AKM, BKM, 64, 128, 1, 4, sizeof(T) == 2 ? 4 : 2>(A, B, pl, epi, s);
     return launch_tiles<T, AKM, BKM, 128, 128, 2, 2, sizeof(T) == 2 ? 4 : 2>(A, B, pl, epi, s);
 }
 
@@ -440,7 +461,9 @@ struct SmallShape {
     // tiles held at a time, and units held per tile (by the registers)
     static constexpr int TR = ONE || sizeof(T) == 4 || BT > 2 ? 1 : 2;
     static constexpr int UN = ONE || (sizeof(T) == 4 && BT > 4) ? 1 : 2;
-    static constexpr int kSums = BT < 2 ? BT : 2;  // batch tiles summed at a time
+    // tiles and batch tiles whose sums meet at a time (16 KiB each, beside the table)
+    static constexpr int kSumsR = ONE ? TR : 1;
+    static constexpr int kSums = ONE && BT > 1 ? 2 : 1;
 };
 
 // x as small_kernel's steps read it, for groups of 16 BT rows: the 16-byte piece p of lane l
@@ -479,7 +502,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
     using Tr = gemm::Traits<T>;
     constexpr int K = KV / V;
     using Sh = SmallShape<T, BT, ONE>;
-    constexpr int TR = Sh::TR, UN = Sh::UN, kSums = Sh::kSums;
+    constexpr int TR = Sh::TR, UN = Sh::UN, kSums = Sh::kSums, kSumsR = Sh::kSumsR;
     constexpr bool kPacked = BT > 1;
     constexpr int kRow = V * static_cast<int>(sizeof(T));  // bytes of a table row
     constexpr int kLog = kRow == 2 ? 1 : (kRow == 4 ? 2 : (kRow == 8 ? 3 : 4));
@@ -585,6 +608,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
     };
 
     if (ONE) copy(0);
+    int first = 0, held = -1;  // part a turn starts with, and the one in LDS
     const int64_t tiles = (a.M + 15) / 16;
     for (int64_t tile0 = static_cast<int64_t>(blockIdx.x) * TR; tile0 < tiles;
          tile0 += static_cast<int64_t>(gridDim.x) * TR) {
@@ -638,9 +662,13 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
 #pragma unroll
                             for (int j = 0; j < kWords; ++j) val[r][u][s][j] = 0u;
                     }
-                for (int p = 0; p < a.parts; ++p) {
-                    __syncthreads();  // the previous part, and the sums, are done with
-                    copy(p);
+                for (int v = 0; v < a.parts; ++v) {
+                    const int p = first == 0 ? v : a.parts - 1 - v;
+                    if (p != held) {
+                        __syncthreads();  // the previous part is done with
+                        copy(p);
+                        held = p;
+                    }
                     const uint32_t base = static_cast<uint32_t>(p) * dummy;
 #pragma unroll
                     for (int r = 0; r < TR; ++r)
@@ -658,6 +686,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
                                 __builtin_amdgcn_sched_barrier(0);
                             }
                 }
+                first = first == 0 ? a.parts - 1 : 0;  // the next turn starts with this one
 #pragma unroll
                 for (int u = 0; u < UN; ++u)
 #pragma unroll
@@ -677,25 +706,28 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
         }
         // acc[r][t]: rows 4 g .. 4 g + 3 of the tile, row t 16 + l16 of x
 #pragma unroll
-        for (int t0 = 0; t0 < BT; t0 += kSums) {
-            __syncthreads();  // the previous sums (or the table's last part) are read
+        for (int q0 = 0; q0 < TR; q0 += kSumsR)
 #pragma unroll
-            for (int r = 0; r < TR; ++r)
+            for (int t0 = 0; t0 < BT; t0 += kSums) {
+                __syncthreads();  // the previous sums are read
 #pragma unroll
-                for (int t = 0; t < kSums; ++t)
-                    *reinterpret_cast<f32x4 *>(
-                        red + (((wave * TR + r) * kSums + t) * 16 + l16) * 16 + g * 4) =
-                        acc[r][t0 + t];
-            __syncthreads();
-            for (int o = tid; o < TR * kSums * 256; o += kThreads) {
-                float sum = red[o];
+                for (int r = 0; r < kSumsR; ++r)
 #pragma unroll
-                for (int v = 1; v < kSmallWaves; ++v) sum += red[v * TR * kSums * 256 + o];
-                const int r = o / (kSums * 256), i = o % (kSums * 256);
-                epi.put_one((static_cast<int64_t>(blockIdx.y) * BT + t0) * 16 + i / 16,
-                            (tile0 + r) * 16 + i % 16, sum);
+                    for (int t = 0; t < kSums; ++t)
+                        *reinterpret_cast<f32x4 *>(
+                            red + (((wave * kSumsR + r) * kSums + t) * 16 + l16) * 16 + g * 4) =
+                            acc[q0 + r][t0 + t];
+                __syncthreads();
+                for (int o = tid; o < kSumsR * kSums * 256; o += kThreads) {
+                    float sum = red[o];
+#pragma unroll
+                    for (int v = 1; v < kSmallWaves; ++v)
+                        sum += red[v * kSumsR * kSums * 256 + o];
+                    const int r = q0 + o / (kSums * 256), i = o % (kSums * 256);
+                    epi.put_one((static_cast<int64_t>(blockIdx.y) * BT + t0) * 16 + i / 16,
+                                (tile0 + r) * 16 + i % 16, sum);
+                }
             }
-        }
     }
 }
 
@@ -912,6 +944,11 @@ hipError_t decode_matrix(const CodedMatrix &w, T *out, int64_t ld, hipStream_t s
         if (grid > slots) grid = slots;
         a.chunks_per_wg = static_cast<uint32_t>((chunks + grid - 1) / grid);
         grid = (chunks + a.chunks_per_wg - 1) / a.chunks_per_wg;
+        // the fewest turns, the chunks spread evenly over them
+        const int rt = one ? chunk_rows<T, true>() : chunk_rows<T, false>();
+        const int64_t per = (a.chunks_per_wg + kChunkThreads - 1) / kChunkThreads;
+        const int64_t turns = (per + rt - 1) / rt;
+        a.rows = static_cast<int>((per + turns - 1) / turns);
         hipError_t e = allow_lds(kern, lds);
         if (e != hipSuccess) return e;
         T *o = out;
@@ -1001,12 +1038,12 @@ hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, char *ws, hi
     const int kv = w.k * w.V;
     const bool one = a.parts == 1;
     const int tr = one ? SmallShape<T, BT, true>::TR : SmallShape<T, BT, false>::TR;
-    const size_t sums =
-        static_cast<size_t>(kSmallWaves) * SmallShape<T, BT, true>::kSums * tr * 1024;
-    // One part: the sums lie behind the table (and behind the 1 KiB that a partly filled wave
-    // of its copy writes).  Several: over the table, which is read again afterwards.
-    a.red = one ? (a.part_bytes < 1024 ? 1024 : a.part_bytes) : 0;
-    const size_t lds = one ? a.red + sums : static_cast<size_t>(a.part_bytes) + 1024;
+    const size_t sums = static_cast<size_t>(kSmallWaves) * 1024 *
+                        (one ? SmallShape<T, BT, true>::kSums : SmallShape<T, BT, false>::kSums);
+    // The sums lie behind the table: behind the 1 KiB that a partly filled wave of the copy
+    // of a small one writes, or the row of zeros after a part.
+    a.red = one ? (a.part_bytes < 1024 ? 1024 : a.part_bytes) : a.part_bytes + 64;
+    const size_t lds = a.red + sums;
     const void *kern = one ? small_kernel_of<T, BT, true>(kv, w.V)
                            : small_kernel_of<T, BT, false>(kv, w.V);
     e = allow_lds(kern, lds);
@@ -1139,8 +1176,10 @@ size_t linear_small_bytes(size_t size, int64_t B, int64_t N, int bt) {
 // the 256 compute units of the part this library is built for), so the workspace query
 // and the call agree.
 //   256 x 256 tiles where they fill half the card: 8 waves, one workgroup per compute unit.
-//   128 x 128 where those fill the card, else 64 x 128; both keep four steps of loads in
-// flight, since few workgroups with short steps otherwise wait for memory on every step.
+//   128 x 128 where those fill the card, else 64 x 128; in 16-bit types both keep four steps
+// of loads in flight, since few workgroups with short steps otherwise wait for memory on
+// every step (fp32 steps are eight times as long: two stages, and three workgroups per
+// compute unit, took 333 x 2048 x 2048 from 46 to 37 us).
 //   Where 64 x 128 tiles leave compute units idle, k is split (at least 4 steps each) and
 // the shares, in fp32, are added by a second kernel.
 GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K) {
