@@ -90,11 +90,12 @@ struct ChunkArgs {
 constexpr int kChunkThreads = 1024;
 constexpr int kPartBytes = 128 << 10;
 
-// Chunks a thread holds at a time: each keeps its values over the passes, so more of them
-// mean fewer copies of the table (14336 x 4096, V = 2, 16 bits: 43 us with 8, 35 with 14).
+// Chunks a thread holds at a time.  With several parts each keeps its values over the
+// passes (14336 x 4096, V = 2, 16 bits: 41-42 us with 7 to 14, 44 with 5); with one, two keep
+// the stores flowing (4096 x 4096, 16 bits: 12.9 us with 2 or 4, 14.1 with 8).
 template <typename T, bool ONE>
 constexpr int chunk_rows() {
-    return sizeof(T) == 4 ? (ONE ? 4 : 8) : (ONE ? 8 : 14);
+    return ONE ? 2 : (sizeof(T) == 4 ? 8 : 14);
 }
 
 template <typename T, int KV, int V, bool ONE>
@@ -330,14 +331,16 @@ __global__ __launch_bounds__(WI *WJ * 64) void gemm_kernel(Operand<T> A, Operand
                                                            int steps, int steps_per_split,
                                                            Epi epi, uint32_t ni, uint32_t nj) {
     static_assert(NB == 2 || NB == 4 || NB == gemm::kRing, "stages");
+    // (the ring's pieces hold either operand's tile)
+    constexpr int kBytesB = (NB == gemm::kRing ? TI : TJ) * gemm::kStepBytes;
     __shared__ __align__(16) char a0[TI * gemm::kStepBytes];
     __shared__ __align__(16) char a1[TI * gemm::kStepBytes];
-    __shared__ __align__(16) char b0[TJ * gemm::kStepBytes];
-    __shared__ __align__(16) char b1[TJ * gemm::kStepBytes];
+    __shared__ __align__(16) char b0[kBytesB];
+    __shared__ __align__(16) char b1[kBytesB];
     gemm::Stages<NB> st;
     st.a[0] = a0;
     if constexpr (NB == gemm::kRing) {
-        static_assert(TI == TJ, "pieces of one size");
+        static_assert(TI >= TJ, "pieces of one size");
         __shared__ __align__(16) char a2[TI * gemm::kStepBytes];
         st.p[0] = a0;
         st.p[1] = b0;
@@ -409,6 +412,10 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
         hipLaunchKernelGGL(split_sum_kernel<Epi>, dim3(static_cast<unsigned>((quads + 255) / 256)),
                            dim3(256), 0, s, pe.part, pl.splits, A.rows, pl.part_ld, epi);
         return hipGetLastError();
+    }
+    if constexpr (sizeof(T) == 2 && !BKM) {
+        if (pl.tile == kTile224)
+            return launch_tiles<T, AKM, BKM, 256, 224, 4, 2, gemm::kRing>(A, B, pl, epi, s);
     }
     if constexpr (sizeof(T) == 2) {
         if (pl.tile == kTile256)
@@ -1176,13 +1183,16 @@ size_t linear_small_bytes(size_t size, int64_t B, int64_t N, int bt) {
 // the 256 compute units of the part this library is built for), so the workspace query
 // and the call agree.
 //   256 x 256 tiles where they fill half the card: 8 waves, one workgroup per compute unit.
+// Tiles come in rounds of 256, so 256 x 224 ones, where B's rows are contiguous in k, are
+// taken where their rounds cost less (2048 x 14336 x 4096: 512 tiles in two rounds of 7/8 of
+// the work against 448 in two; 251 -> 244 us per call).
 //   128 x 128 where those fill the card, else 64 x 128; in 16-bit types both keep four steps
 // of loads in flight, since few workgroups with short steps otherwise wait for memory on
 // every step (fp32 steps are eight times as long: two stages, and three workgroups per
 // compute unit, took 333 x 2048 x 2048 from 46 to 37 us).
 //   Where 64 x 128 tiles leave compute units idle, k is split (at least 4 steps each) and
 // the shares, in fp32, are added by a second kernel.
-GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K) {
+GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K, bool k_contiguous) {
     constexpr int64_t kCus = 256;
     const auto tiles = [&](int64_t ti, int64_t tj) {
         return ((I + ti - 1) / ti) * ((J + tj - 1) / tj);
@@ -1193,7 +1203,10 @@ GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K) {
     p.splits = 1;
     p.part_ld = (J + 3) / 4 * 4;
     if (size == 2 && tiles(256, 256) >= kCus / 2) {
-        p.tile = kTile256;
+        const auto rounds = [&](int64_t n) { return (n + kCus - 1) / kCus; };
+        p.tile = k_contiguous && rounds(tiles(256, 224)) * 224 < rounds(tiles(256, 256)) * 256
+                     ? kTile224
+                     : kTile256;
     } else if (tiles(128, 128) >= kCus) {
         p.tile = kTile128;
     } else {
@@ -1218,7 +1231,7 @@ LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N) {
     l.matrix = 0;
     l.rows = align_up(static_cast<size_t>(M) * l.ldn * size, 256);
     l.sums = l.rows + align_up(static_cast<size_t>(B) * l.ldn * size, 256);
-    l.forward = gemm_plan(size, B, M, l.ldn);
+    l.forward = gemm_plan(size, B, M, l.ldn, true);
     l.bytes = l.sums + align_up(l.forward.part_bytes, 256);
     return l;
 }
@@ -1238,8 +1251,8 @@ LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bo
     l.part = off;
     if (dbias) off += align_up(static_cast<size_t>(slope_slabs(B, M)) * M * sizeof(float), 256);
     l.sums = off;  // (the two products run one after the other)
-    l.dx = gemm_plan(size, B, l.ldn, M);
-    l.dw = gemm_plan(size, l.ldm, l.ldn, B);
+    l.dx = gemm_plan(size, B, l.ldn, M, false);
+    l.dw = gemm_plan(size, l.ldm, l.ldn, B, false);
     size_t sums = dx ? l.dx.part_bytes : 0;
     if (dw && l.dw.part_bytes > sums) sums = l.dw.part_bytes;
     off += align_up(sums, 256);
