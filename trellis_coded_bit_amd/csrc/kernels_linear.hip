@@ -406,7 +406,7 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
     if (pl.splits > 1) {
         const PartEpilogue pe{reinterpret_cast<float *>(part), pl.part_ld, A.rows, B.rows};
         // (only 64 x 128 tiles are split)
-        const hipError_t e = launch_tiles<T, AKM, BKM, 64, 128, 1, 4, sizeof(T) == 2 ? 4 : 2>(A, B, pl, pe, s);
+        const hipError_t e = launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 2>(A, B, pl, pe, s);
         if (e != hipSuccess) return e;
         const int64_t quads = A.rows * (pl.part_ld / 4);
         hipLaunchKernelGGL(split_sum_kernel<Epi>, dim3(static_cast<unsigned>((quads + 255) / 256)),
@@ -421,7 +421,7 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
         if (pl.tile == kTile256)
             return launch_tiles<T, AKM, BKM, 256, 256, 2, 4, gemm::kRing>(A, B, pl, epi, s);
     }
-    if (pl.tile == kTile64) return launch_tiles<T, AKM, BKM, 64, 128, 1, 4, sizeof(T) == 2 ? 4 : 2>(A, B, pl, epi, s);
+    if (pl.tile == kTile64) return launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 2>(A, B, pl, epi, s);
     return launch_tiles<T, AKM, BKM, 128, 128, 2, 2, sizeof(T) == 2 ? 4 : 2>(A, B, pl, epi, s);
 }
 
@@ -1215,7 +1215,7 @@ GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K, bool k_contiguo
         int64_t s = n > 0 ? 2 * kCus / n : 1;
         if (s > p.steps / 4) s = p.steps / 4;
         if (s > 16) s = 16;
-        if (n < kCus && s > 1) p.splits = static_cast<int>(s);
+        if (s > 1) p.splits = static_cast<int>(s);
     }
     p.steps_per_split = p.splits > 0 ? (p.steps + p.splits - 1) / p.splits : p.steps;
     if (p.steps_per_split > 0)
