@@ -101,7 +101,7 @@ __device__ __forceinline__ void table_to_lds(char *lds, const char *src, int byt
         const int wave0 = __builtin_amdgcn_readfirstlane(tid & ~63);
         for (int at = 0; at < bytes; at += THREADS * 16) {
             // (whole waves past the end are skipped; lanes past it load zeros, inside the
-            // 1 KiB the caller leaves after the part)
+            // 1 KiB that the caller leaves for a part smaller than that)
             if (at + wave0 * 16 < bytes)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
                     rs, (__attribute__((address_space(3))) void *)(lds + at + wave0 * 16), 16,

@@ -473,13 +473,13 @@ struct SmallShape {
     static constexpr int kSums = ONE && BT > 1 ? 2 : 1;
 };
 
-// x as small_kernel's steps read it, for groups of 16 BT rows: the 16-byte piece p of lane l
-// for step s, batch tile t of group y is piece (((y steps + s) BT + t) P + p) 64 + l, where P is
-// the pieces of 8 values.  Rows past B are zeros.
+// x as small_kernel's steps read it: the 16-byte piece p of lane l for step s and batch tile t
+// is piece ((s BT + t) P + p) 64 + l, where P is the pieces of 8 values.  Rows past B are
+// zeros.
 template <typename T, int BT>
 __global__ __launch_bounds__(256) void pack_rows_kernel(const T *__restrict__ x, int64_t B,
-                                                        int64_t ldx, uint32_t steps,
-                                                        int64_t pieces, uint4 *__restrict__ out) {
+                                                        int64_t ldx, int64_t pieces,
+                                                        uint4 *__restrict__ out) {
     constexpr int P = static_cast<int>(sizeof(T)) / 2;
     constexpr int kPer = 16 / static_cast<int>(sizeof(T));
     struct __attribute__((packed, aligned(2))) Raw { uint32_t w[4]; };
@@ -489,9 +489,8 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const T *__restrict__ x,
         const int64_t q = i >> 6;
         const int p = static_cast<int>(q % P);
         const int t = static_cast<int>(q / P % BT);
-        const uint32_t at = static_cast<uint32_t>(q / (P * BT));  // group and step
-        const uint32_t y = at / steps, s = at - y * steps;
-        const int64_t b = (static_cast<int64_t>(y) * BT + t) * 16 + (l & 15);
+        const int64_t s = q / (P * BT);
+        const int64_t b = t * 16 + (l & 15);
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (b < B) {
             const Raw r = *reinterpret_cast<const Raw *>(x + b * ldx + s * 32 + (l >> 4) * 8 +
@@ -530,8 +529,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
     const uint32_t dummy = static_cast<uint32_t>(a.part_bytes);
     // rows past B read the last one; their sums are not stored
     const T *xrow = static_cast<const T *>(a.x) + (l16 < a.B ? l16 : a.B - 1) * a.ldx + g * 8;
-    const uint4 *xp = static_cast<const uint4 *>(a.x) +
-                      static_cast<int64_t>(blockIdx.y) * a.runs * BT * (kWords / 4) * 64 + lane;
+    const uint4 *xp = static_cast<const uint4 *>(a.x) + lane;
     // step s's piece of batch tile t
     auto read_x = [&](uint32_t s, int t) {
         Piece v;
@@ -731,8 +729,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
                     for (int v = 1; v < kSmallWaves; ++v)
                         sum += red[v * kSumsR * kSums * 256 + o];
                     const int r = q0 + o / (kSums * 256), i = o % (kSums * 256);
-                    epi.put_one((static_cast<int64_t>(blockIdx.y) * BT + t0) * 16 + i / 16,
-                                (tile0 + r) * 16 + i % 16, sum);
+                    epi.put_one(t0 * 16 + i / 16, (tile0 + r) * 16 + i % 16, sum);
                 }
             }
     }
@@ -889,10 +886,14 @@ int cu_count() {
 // The chunk kernel of (kV, V), or nullptr.
 template <typename T>
 const void *chunk_kernel(int kv, int V, bool one) {
-#define TCQ_CHUNK_CASE(KV_, V_)                                                             \
-    if (kv == KV_ && V == V_)                                                               \
-        return one ? reinterpret_cast<const void *>(decode_chunks_kernel<T, KV_, V_, true>) \
-                   : reinterpret_cast<const void *>(decode_chunks_kernel<T, KV_, V_, false>);
+// (a 16-bit table of V = 1 always fits one part)
+#define TCQ_CHUNK_CASE(KV_, V_)                                                           \
+    if (kv == KV_ && V == V_) {                                                           \
+        if constexpr (V_ > 1 || sizeof(T) == 4)                                           \
+            if (!one)                                                                     \
+                return reinterpret_cast<const void *>(decode_chunks_kernel<T, KV_, V_, false>); \
+        return reinterpret_cast<const void *>(decode_chunks_kernel<T, KV_, V_, true>);    \
+    }
     TCQ_CHUNK_CASE(1, 1)
     TCQ_CHUNK_CASE(2, 1)
     TCQ_CHUNK_CASE(2, 2)
@@ -909,8 +910,8 @@ const void *chunk_kernel(int kv, int V, bool one) {
     return nullptr;
 }
 
-// Raises the dynamic LDS limit of a kernel (the attribute is per function and device; the
-// call is a table lookup in the runtime, made on every launch).
+// Raises the dynamic LDS limit of a kernel.  Set on every launch: the attribute belongs to
+// the function on the current device, and nothing is kept between calls.
 hipError_t allow_lds(const void *kern, size_t bytes) {
     return hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(bytes));
@@ -1031,13 +1032,12 @@ hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, char *ws, hi
     a.part_bytes = static_cast<int>(row << plog);
     a.parts = 1 << (w.L - plog);
     a.vec = (reinterpret_cast<uintptr_t>(w.table) & 15) == 0;
-    const int64_t groups = (c.B + 16 * BT - 1) / (16 * BT);
     hipError_t e;
-    if (BT > 1) {
-        const int64_t pieces = groups * a.runs * BT * static_cast<int64_t>(sizeof(T) / 2) * 64;
+    if constexpr (BT > 1) {
+        const int64_t pieces = static_cast<int64_t>(a.runs) * BT * static_cast<int64_t>(sizeof(T) / 2) * 64;
         hipLaunchKernelGGL((pack_rows_kernel<T, BT>), dim3(grid_for(pieces, 256, 1 << 16)),
-                           dim3(256), 0, s, static_cast<const T *>(c.x), c.B, c.ldx, a.runs,
-                           pieces, reinterpret_cast<uint4 *>(ws));
+                           dim3(256), 0, s, static_cast<const T *>(c.x), c.B, c.ldx, pieces,
+                           reinterpret_cast<uint4 *>(ws));
         e = hipGetLastError();
         if (e != hipSuccess) return e;
         a.x = ws;
@@ -1060,8 +1060,7 @@ hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, char *ws, hi
     LayerEpilogue<T> epi = layer_epilogue<T>(w, c);
     void *args[] = {&a, &epi};
     e = hipLaunchKernel(kern,
-                        dim3(static_cast<unsigned>(turns < slots ? turns : slots),
-                             static_cast<unsigned>(groups)),
+                        dim3(static_cast<unsigned>(turns < slots ? turns : slots)),
                         dim3(kSmallWaves * 64), args, lds, s);
     return e != hipSuccess ? e : hipGetLastError();
 }
@@ -1170,13 +1169,15 @@ size_t pad8(int64_t n) { return static_cast<size_t>((n + 7) / 8 * 8); }
 int linear_small(size_t size, int64_t B, int64_t N, int L, int k, int V, int T) {
     const int kv = k * V;
     if (N <= 0 || T % 32 != 0 || kv > 4 || (V != 1 && V != 2 && V != 4)) return 0;
-    const bool one = ((V * size) << L) <= kPartBytes;
+    const size_t table = (V * size) << L;
+    if (table % 16 != 0) return 0;  // the table's copy moves 16 bytes at a time
+    const bool one = table <= kPartBytes;
     if (B > (size == 4 || one ? 128 : 64)) return 0;
     return B <= 16 ? 1 : (B <= 32 ? 2 : (B <= 64 ? 4 : 8));
 }
 
-size_t linear_small_bytes(size_t size, int64_t B, int64_t N, int bt) {
-    return bt > 1 ? static_cast<size_t>((B + 16 * bt - 1) / (16 * bt) * (16 * bt)) * N * size : 0;
+size_t linear_small_bytes(size_t size, int64_t N, int bt) {
+    return bt > 1 ? static_cast<size_t>(16 * bt) * N * size : 0;
 }
 
 // Tile and splits of an I x J product over K.  The choice depends on sizes alone (and on
@@ -1186,12 +1187,12 @@ size_t linear_small_bytes(size_t size, int64_t B, int64_t N, int bt) {
 // Tiles come in rounds of 256, so 256 x 224 ones, where B's rows are contiguous in k, are
 // taken where their rounds cost less (2048 x 14336 x 4096: 512 tiles in two rounds of 7/8 of
 // the work against 448 in two; 251 -> 244 us per call).
-//   128 x 128 where those fill the card, else 64 x 128; in 16-bit types both keep four steps
-// of loads in flight, since few workgroups with short steps otherwise wait for memory on
-// every step (fp32 steps are eight times as long: two stages, and three workgroups per
-// compute unit, took 333 x 2048 x 2048 from 46 to 37 us).
-//   Where 64 x 128 tiles leave compute units idle, k is split (at least 4 steps each) and
-// the shares, in fp32, are added by a second kernel.
+//   128 x 128 where those fill the card (in 16-bit types with four stages, one workgroup per
+// compute unit: 1000 x 4096 x 4096 64 us per call against 67 with two stages), else
+// 64 x 128 with two stages and three workgroups per compute unit.
+//   Where 64 x 128 tiles are at most one per compute unit, k is split into about 512
+// workgroups (at least 4 steps each) and the shares, in fp32, are added by a second kernel
+// (512 x 4096 x 4096 in bf16: 57 us per call unsplit, 45 split; 160 rows: 40 and 32).
 GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K, bool k_contiguous) {
     constexpr int64_t kCus = 256;
     const auto tiles = [&](int64_t ti, int64_t tj) {

@@ -154,7 +154,7 @@ struct LinearLayout {
 // Batch tiles of 16 rows that a forward call takes at a time with the matrix decoded inside
 // the product, or 0 where it is decoded into the workspace first.
 int linear_small(size_t size, int64_t B, int64_t N, int L, int k, int V, int T);
-size_t linear_small_bytes(size_t size, int64_t B, int64_t N, int bt);
+size_t linear_small_bytes(size_t size, int64_t N, int bt);
 LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N);
 LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bool dx, bool dw,
                                 bool dbias);

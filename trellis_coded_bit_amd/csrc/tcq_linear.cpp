@@ -89,7 +89,7 @@ int check_workspace(const char *fn, const void *workspace, size_t bytes, size_t 
 
 size_t forward_bytes(int dtype, int64_t B, int64_t M, int64_t N, int L, int k, int V, int T) {
     const int bt = linear_small(size_of(dtype), B, N, L, k, V, T);
-    return bt ? linear_small_bytes(size_of(dtype), B, N, bt)
+    return bt ? linear_small_bytes(size_of(dtype), N, bt)
               : linear_layout(size_of(dtype), B, M, N).bytes;
 }
 
