@@ -108,9 +108,8 @@ __device__ __forceinline__ int kmajor_key(int kk) {
 template <typename T, bool KM, int TR, int NT>
 struct TileLoader {
     static constexpr int kChunks = TR * (kStepBytes / 16);  // 16-byte chunks of a tile
-    static constexpr int kLoads = (kChunks + NT - 1) / NT;
-    static constexpr int kLeast = kChunks / NT;  // loads that every wave issues
-    static_assert(kChunks % 64 == 0, "whole waves");
+    static constexpr int kLoads = kChunks / NT;
+    static_assert(kChunks % NT == 0, "whole loads per thread");
     static constexpr int kRowChunks = KM ? TR * static_cast<int>(sizeof(T)) / 16 : 8;
     static constexpr int kStep = Traits<T>::kStep;
 
@@ -166,10 +165,9 @@ struct TileLoader {
         const int wave0 = __builtin_amdgcn_readfirstlane(tid & ~63);
 #pragma unroll
         for (int u = 0; u < kLoads; ++u)
-            if (u < kLeast || u * NT + wave0 < kChunks)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                    rs, (LdsPtr)(lds + (u * NT + wave0) * 16), 16,
-                    static_cast<int>(in ? off[u] : 0xFFFFFFF0u), 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rs, (LdsPtr)(lds + (u * NT + wave0) * 16), 16,
+                static_cast<int>(in ? off[u] : 0xFFFFFFF0u), 0, 0, 0);
     }
 };
 
@@ -317,9 +315,7 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
         // stages every load has one step to arrive.  Five pieces give A two steps: B(s + 2)
         // goes into A(s)'s piece after the meeting of step s, A(s + 3) into B(s)'s in the
         // first phase of step s + 1, so the loads are also spread (8192 x 4096 x 14336 in
-        // bf16: 815 us with two stages, 760 with the ring).  (Waves of a tile that is not
-        // whole loads per thread issue kLeast or kLoads of B.)
-        static_assert(decltype(la)::kLeast == kLoadsA, "whole loads of A");
+        // bf16: 815 us with two stages, 760 with the ring).
         auto step = [&](int s, auto turn) {
             constexpr int t = 2 * decltype(turn)::value;
             char *sa = st.p[t % 5], *sb = st.p[(t + 1) % 5];
@@ -342,7 +338,7 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
             lb.load(st.p[1], s_begin, tid);
             la.load(st.p[2], valid(s_begin + 1), tid);
             lb.load(st.p[3], valid(s_begin + 1), tid);
-            meet<kLoadsA + decltype(lb)::kLeast>();
+            meet<kLoadsA + kLoadsB>();
             read_phase(st.p[0], st.p[1], 0);
             for (int s = s_begin; s < s_end; s += 5) {
                 step(s, std::integral_constant<int, 0>{});
@@ -370,8 +366,6 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
             mul_phase(kPhases - 1);
             __builtin_amdgcn_sched_barrier(0);
         };
-        static_assert(decltype(la)::kLeast == kLoadsA && decltype(lb)::kLeast == kLoadsB,
-                      "whole loads");
         if (s_begin < s_end) {
 #pragma unroll
             for (int t = 0; t < NB; ++t) {
@@ -388,39 +382,32 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
             meet<0>();  // no load into LDS outlives the tile
         }
     }
-    // Outputs: 16 rows of up to four fragments at a time through a piece of LDS of the wave's
-    // own (in a stage, which is done with), so that a lane takes four consecutive j of
-    // always the same column group and a row leaves in one run.  The 16-byte chunks of row r
-    // are permuted by r: the 16 rows of a fragment otherwise start in the same bank.
-    constexpr int GF = FJ < 4 ? FJ : 4;
-    constexpr int kRow = GF * 4;  // 16-byte chunks of a row
-    static_assert(WI * WJ * GF * 1024 <= TI * kStepBytes, "the waves' pieces fit the buffer");
+    // Outputs: 16 rows at a time through a piece of LDS of the wave's own (in a stage,
+    // which is done with), so that a lane takes four consecutive j of always the same column group
+    // and a row leaves in one run.  The 16-byte chunks of row r are permuted by r: the 16
+    // rows of a fragment otherwise start in the same bank.
+    constexpr int kRow = FJ * 4;  // 16-byte chunks of a row
+    static_assert(WI * WJ * FJ * 1024 <= TI * kStepBytes, "the waves' pieces fit the buffer");
     static_assert(64 % kRow == 0, "whole rows per wave and turn");
-    char *piece = st.a[0] + wave * (GF * 1024);
+    char *piece = st.a[0] + wave * (FJ * 1024);
     const int l16 = lane & 15, g = lane >> 4;
     const int rr = lane / kRow, rc = lane % kRow;
+    const int64_t j = j0 + wj * FJ * 16 + rc * 4;
+    typename Epi::Column col(epi, j);
 #pragma unroll
-    for (int f0 = 0; f0 < FJ; f0 += GF) {
-        const bool in = FJ % GF == 0 || f0 * 4 + rc < FJ * 4;
-        const int64_t j = j0 + (wj * FJ + f0) * 16 + rc * 4;
-        typename Epi::Column col(epi, j);
+    for (int i = 0; i < FI; ++i) {
 #pragma unroll
-        for (int i = 0; i < FI; ++i) {
-#pragma unroll
-            for (int f = 0; f < GF; ++f)
-                if (f0 + f < FJ)
-                    *reinterpret_cast<f32x4 *>(piece + l16 * (GF * 64) +
-                                               (((f * 4 + g) ^ l16) % kRow) * 16) =
-                        acc[i][f0 + f];
-            __builtin_amdgcn_wave_barrier();
+        for (int f = 0; f < FJ; ++f)
+            *reinterpret_cast<f32x4 *>(piece + l16 * (FJ * 64) +
+                                       (((f * 4 + g) ^ l16) % kRow) * 16) = acc[i][f];
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
-            for (int r = rr; r < 16; r += 64 / kRow) {
-                const f32x4 v = *reinterpret_cast<const f32x4 *>(piece + r * (GF * 64) +
-                                                                 ((rc ^ r) % kRow) * 16);
-                if (in) epi.put(col, i0 + (wi * FI + i) * 16 + r, v);
-            }
-            __builtin_amdgcn_wave_barrier();
+        for (int r = rr; r < 16; r += 64 / kRow) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(piece + r * (FJ * 64) +
+                                                             ((rc ^ r) % kRow) * 16);
+            epi.put(col, i0 + (wi * FI + i) * 16 + r, v);
         }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 

@@ -331,16 +331,14 @@ __global__ __launch_bounds__(WI *WJ * 64) void gemm_kernel(Operand<T> A, Operand
                                                            int steps, int steps_per_split,
                                                            Epi epi, uint32_t ni, uint32_t nj) {
     static_assert(NB == 2 || NB == 4 || NB == gemm::kRing, "stages");
-    // (the ring's pieces hold either operand's tile)
-    constexpr int kBytesB = (NB == gemm::kRing ? TI : TJ) * gemm::kStepBytes;
     __shared__ __align__(16) char a0[TI * gemm::kStepBytes];
     __shared__ __align__(16) char a1[TI * gemm::kStepBytes];
-    __shared__ __align__(16) char b0[kBytesB];
-    __shared__ __align__(16) char b1[kBytesB];
+    __shared__ __align__(16) char b0[TJ * gemm::kStepBytes];
+    __shared__ __align__(16) char b1[TJ * gemm::kStepBytes];
     gemm::Stages<NB> st;
     st.a[0] = a0;
     if constexpr (NB == gemm::kRing) {
-        static_assert(TI >= TJ, "pieces of one size");
+        static_assert(TI == TJ, "pieces of one size");
         __shared__ __align__(16) char a2[TI * gemm::kStepBytes];
         st.p[0] = a0;
         st.p[1] = b0;
@@ -413,16 +411,13 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
                            dim3(256), 0, s, pe.part, pl.splits, A.rows, pl.part_ld, epi);
         return hipGetLastError();
     }
-    if constexpr (sizeof(T) == 2 && !BKM) {
-        if (pl.tile == kTile224)
-            return launch_tiles<T, AKM, BKM, 256, 224, 4, 2, gemm::kRing>(A, B, pl, epi, s);
-    }
     if constexpr (sizeof(T) == 2) {
         if (pl.tile == kTile256)
             return launch_tiles<T, AKM, BKM, 256, 256, 2, 4, gemm::kRing>(A, B, pl, epi, s);
+        if (pl.tile == kTile128)
+            return launch_tiles<T, AKM, BKM, 128, 128, 2, 2, 4>(A, B, pl, epi, s);
     }
-    if (pl.tile == kTile64) return launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 2>(A, B, pl, epi, s);
-    return launch_tiles<T, AKM, BKM, 128, 128, 2, 2, sizeof(T) == 2 ? 4 : 2>(A, B, pl, epi, s);
+    return launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 2>(A, B, pl, epi, s);
 }
 
 // ---------------------------------------------------------------- few rows of x
@@ -1183,46 +1178,55 @@ size_t linear_small_bytes(size_t size, int64_t N, int bt) {
 // Tile and splits of an I x J product over K.  The choice depends on sizes alone (and on
 // the 256 compute units of the part this library is built for), so the workspace query
 // and the call agree.
-//   256 x 256 tiles where they fill half the card: 8 waves, one workgroup per compute unit.
-// Tiles come in rounds of 256, so 256 x 224 ones, where B's rows are contiguous in k, are
-// taken where their rounds cost less (2048 x 14336 x 4096: 512 tiles in two rounds of 7/8 of
-// the work against 448 in two; 251 -> 244 us per call).
-//   128 x 128 where those fill the card (in 16-bit types with four stages, one workgroup per
-// compute unit: 1000 x 4096 x 4096 64 us per call against 67 with two stages), else
-// 64 x 128 with two stages and three workgroups per compute unit.
-//   Where 64 x 128 tiles are at most one per compute unit, k is split into about 512
-// workgroups (at least 4 steps each) and the shares, in fp32, are added by a second kernel
-// (512 x 4096 x 4096 in bf16: 57 us per call unsplit, 45 split; 160 rows: 40 and 32).
-GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K, bool k_contiguous) {
+//   64 x 128 tiles with two stages run three to a compute unit.  Where they are at most one
+// per unit, k is split into about 512 workgroups (at least 4 steps each) and the shares, in
+// fp32, are added by a second kernel (512 x 4096 x 4096 in bf16: 57 us per call unsplit, 45
+// split; 160 rows: 40 and 32).
+//   16-bit types also have 256 x 256 tiles (the ring) and 128 x 128 ones (four stages), one
+// to a compute unit.  Tiles come in rounds of 256; what a round costs, once and per step of
+// k, was fitted to calls with all three forced on the same shapes, and the cheapest is taken
+// (566 x 6912 x 2176 in bf16: 56 us per call with 64 x 128, 76 with 128 x 128, 70 with
+// 256 x 256; 2176 x 6912 x 576: 57, 72 and 40; 1024 x 4096 x 4096: 67, 63 and 99).
+//   In fp32 the matrix instruction is the bound whatever the tile, and the smallest wastes
+// least (566 x 6912 x 2176: 164 us against 288 with 128 x 128; 4096^3: 1087 against 1077).
+GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K) {
     constexpr int64_t kCus = 256;
     const auto tiles = [&](int64_t ti, int64_t tj) {
         return ((I + ti - 1) / ti) * ((J + tj - 1) / tj);
     };
+    const auto rounds = [&](int64_t n) { return static_cast<double>((n + kCus - 1) / kCus); };
     GemmPlan p{};
     const int64_t step = gemm::kStepBytes / static_cast<int64_t>(size);
+    p.tile = kTile64;
     p.steps = static_cast<int>((K + step - 1) / step);
-    p.splits = 1;
     p.part_ld = (J + 3) / 4 * 4;
-    if (size == 2 && tiles(256, 256) >= kCus / 2) {
-        const auto rounds = [&](int64_t n) { return (n + kCus - 1) / kCus; };
-        p.tile = k_contiguous && rounds(tiles(256, 224)) * 224 < rounds(tiles(256, 256)) * 256
-                     ? kTile224
-                     : kTile256;
-    } else if (tiles(128, 128) >= kCus) {
-        p.tile = kTile128;
-    } else {
-        p.tile = kTile64;
-        const int64_t n = tiles(64, 128);
-        int64_t s = n > 0 ? 2 * kCus / n : 1;
-        if (s > p.steps / 4) s = p.steps / 4;
-        if (s > 16) s = 16;
-        if (s > 1) p.splits = static_cast<int>(s);
-    }
-    p.steps_per_split = p.splits > 0 ? (p.steps + p.splits - 1) / p.splits : p.steps;
-    if (p.steps_per_split > 0)
-        p.splits = (p.steps + p.steps_per_split - 1) / p.steps_per_split;
-    if (p.splits < 1) p.splits = 1;
+    const int64_t n = tiles(64, 128);
+    int64_t s = n > 0 ? 2 * kCus / n : 1;
+    if (s > p.steps / 4) s = p.steps / 4;
+    if (s > 16) s = 16;
+    if (s < 1) s = 1;
+    p.steps_per_split = static_cast<int>((p.steps + s - 1) / s);
+    p.splits = p.steps_per_split > 0
+                   ? (p.steps + p.steps_per_split - 1) / p.steps_per_split
+                   : 1;
     p.part_bytes = p.splits > 1 ? static_cast<size_t>(p.splits) * I * p.part_ld * 4 : 0;
+    if (size == 2) {
+        // us; the shares are written and read at about 4 TB/s, and their kernel takes 5
+        const double r = rounds(n * p.splits);
+        double best = 4.0 + 1.5 * r + 0.33 * (r < 3 ? 3 : r) * p.steps_per_split +
+                      (p.splits > 1 ? 5.0 + 2.0 * p.part_bytes / 4e6 : 0.0);
+        const auto take = [&](int tile, double us) {
+            if (us >= best) return;
+            best = us;
+            p.tile = tile;
+            p.splits = 1;
+            p.steps_per_split = p.steps;
+            p.part_bytes = 0;
+        };
+        const double steps = p.steps;
+        take(kTile128, 4.0 + rounds(tiles(128, 128)) * (5.0 + 0.8 * steps));
+        take(kTile256, 7.0 + rounds(tiles(256, 256)) * (12.0 + 1.4 * steps));
+    }
     return p;
 }
 
@@ -1232,7 +1236,7 @@ LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N) {
     l.matrix = 0;
     l.rows = align_up(static_cast<size_t>(M) * l.ldn * size, 256);
     l.sums = l.rows + align_up(static_cast<size_t>(B) * l.ldn * size, 256);
-    l.forward = gemm_plan(size, B, M, l.ldn, true);
+    l.forward = gemm_plan(size, B, M, l.ldn);
     l.bytes = l.sums + align_up(l.forward.part_bytes, 256);
     return l;
 }
@@ -1252,8 +1256,8 @@ LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bo
     l.part = off;
     if (dbias) off += align_up(static_cast<size_t>(slope_slabs(B, M)) * M * sizeof(float), 256);
     l.sums = off;  // (the two products run one after the other)
-    l.dx = gemm_plan(size, B, l.ldn, M, false);
-    l.dw = gemm_plan(size, l.ldm, l.ldn, B, false);
+    l.dx = gemm_plan(size, B, l.ldn, M);
+    l.dw = gemm_plan(size, l.ldm, l.ldn, B);
     size_t sums = dx ? l.dx.part_bytes : 0;
     if (dw && l.dw.part_bytes > sums) sums = l.dw.part_bytes;
     off += align_up(sums, 256);

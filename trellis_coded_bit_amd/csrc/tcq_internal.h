@@ -136,13 +136,13 @@ struct LinearGrad {
 };
 // How a product is laid out: tile, steps of k, and how many workgroups share a tile's steps
 // (their fp32 shares, part_bytes in all, have rows of part_ld values).
-enum GemmTile : int { kTile64 = 0, kTile128 = 1, kTile256 = 2, kTile224 = 3 };
+enum GemmTile : int { kTile64 = 0, kTile128 = 1, kTile256 = 2 };
 struct GemmPlan {
     int tile, splits, steps, steps_per_split;
     int64_t part_ld;
     size_t part_bytes;
 };
-GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K, bool k_contiguous);
+GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K);
 // Workspace of a call: byte offsets of the decoded matrix (M x ldn), the staged or unpacked
 // input rows (B x ldn), the scaled gradient (B x ldm), the bias gradient's partial sums and
 // the products' shares.
