@@ -347,9 +347,10 @@ typedef enum {
  *   pre, ldp   : nullable device out, B x M: z, rounded to the layer's type (what
  *                tcq_act_pack and tcq_decode_linear_backward take)
  *   workspace  : >= what tcq_decode_linear_workspace_bytes reports
- * Outputs other than y == residual must not overlap inputs or one another.  Products and
- * sums are fp32 (those of 16-bit inputs exact products); z is not rounded before the
- * activation; each output is rounded once.  Repeated calls give identical results.
+ * Outputs other than y == residual must not overlap inputs or one another.  Products of
+ * 16-bit inputs are exact and sums fp32; fp32 products of large batches are taken to 2^-22
+ * (as six products of bf16 terms; numbers below 2^-109 to 2^-133).  z is not rounded before
+ * the activation; each output is rounded once.  Repeated calls give identical results.
  * N == 0 gives z = bias; M == 0 or B == 0 is a no-op.
  * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED, TCQ_EWORKSPACE, TCQ_EHIP.
  */

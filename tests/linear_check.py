@@ -5,7 +5,9 @@ Bounds count roundings: u = 2^-24 for fp32 arithmetic and half(t) = eps(t) / 2 r
 (plus half the spacing of subnormals) for a value stored in type t.  A product's sum of K
 terms reaches its result through at most K roundings in any order, each allowed a whole
 fp32 unit (2 u), since the matrix instruction's inner sums need not round to nearest:
-|sum - exact| <= 2 K u / (1 - 2 K u) * sum |terms|.
+|sum - exact| <= 2 K u / (1 - 2 K u) * sum |terms|.  fp32 products of
+large batches are sums of six exact products of bf16 terms each, which leave out less than
+2^-22 = 4 u of the product: 6 K roundings and 4 u more.
 """
 import math
 
@@ -26,8 +28,9 @@ def tiny(t):
     return f.tiny * f.eps / 2
 
 
-def gamma(K):
-    g = 2.0 * (K + 1) * U
+def gamma(K, t=None):
+    """Relative bound of a sum of K products of type t (None: plain fp32 terms)."""
+    g = 2.0 * (6 * K + 3 if t == torch.float32 else K + 1) * U
     return g / (1.0 - g)
 
 
@@ -93,7 +96,7 @@ def forward(W, x, a, b, name, res):
 
 def forward_bounds(z, y, mag, res, name, K, t):
     """Elementwise bounds on |z_gpu - z| and |y_gpu - y|."""
-    dz = gamma(K) * mag + 2 * U * z.abs()
+    dz = gamma(K, t) * mag + 2 * U * z.abs()
     # |act'| <= 1.13 for silu and gelu, 1 for the others
     dy = 1.13 * dz + act_error(z, name)
     if res is not None:

@@ -156,6 +156,43 @@ def test_linear_infinities_stay_infinities(L, k, V, T, dtype):
         assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -100, 2.0 ** -60, 1.0, 2.0 ** 60, 2.0 ** 100])
+def test_linear_f32_magnitudes(scale):
+    """fp32 over the type's range: the bound of six bf16 products each, and a relative rms
+    error of a few fp32 units, as a sum of fp32 products has."""
+    M, N, B = 130, 1024, 300
+    rng = np.random.default_rng(2)
+    w = Coded(17, M, N, 16, 2, 1, 256, torch.float32, False)
+    x = torch.from_numpy(rng.standard_normal((B, N)) * scale).float().cuda()
+    y = w.linear(x)
+    want = x.double() @ w.W.t()
+    mag = x.double().abs() @ w.W.abs().t()
+    lim = lc.gamma(N, torch.float32) * mag
+    ratio = float(((y.double() - want).abs() / lim).max())
+    rms = float((y.double() - want).square().mean().sqrt() / want.square().mean().sqrt())
+    _say(f"  f32 scale {scale:.3g}: worst error / bound {ratio:.3g}, relative rms {rms:.3g}")
+    assert ratio <= 1 and rms < 1e-6
+    dy = torch.from_numpy(rng.standard_normal((B, M)) * scale).float().cuda()
+    dx, _, _ = w.backward(dy, dbias=False)
+    want, mag = dy.double() @ w.W, dy.double().abs() @ w.W.abs()
+    assert bool(((dx.double() - want).abs() <= lc.gamma(M, torch.float32) * mag).all())
+
+
+def test_linear_f32_below_the_terms():
+    """Numbers whose smallest term falls below bf16's smallest: within 2^-133 each."""
+    M, N, B = 130, 256, 300
+    rng = np.random.default_rng(2)
+    w = Coded(18, M, N, 16, 2, 1, 256, torch.float32, False)
+    x = torch.from_numpy(rng.standard_normal((B, N)) * 2.0 ** -116).float().cuda()
+    y = w.linear(x)
+    want = x.double() @ w.W.t()
+    lim = lc.gamma(N, torch.float32) * (x.double().abs() @ w.W.abs().t())
+    lim = lim + 2.0 ** -133 * w.W.abs().sum(1) + lc.tiny(torch.float32) * 6 * N
+    ratio = float(((y.double() - want).abs() / lim).max())
+    _say(f"  f32 tiny: worst error / bound {ratio:.3g}")
+    assert ratio <= 1
+
+
 @pytest.mark.parametrize("L,k,V,T,M,N,B", [
     (8, 2, 1, 32, 32768, 32, 70000),       # more than 2^31 outputs
     (8, 2, 1, 32, 64, 32, 1),              # and the smallest
@@ -410,9 +447,9 @@ def test_backward_within_bounds(oracle_lib, shape, B, act, dtype):
     es = eg * a.double().abs() + 2 * lc.U * s.abs()
     es = es + lc.half(dtype) * (s.abs() + es) + lc.tiny(dtype)
     bdb = eg.sum(0) + lc.gamma(B) * (g.abs() + eg).sum(0)
-    bdx = es @ w.W.abs() + lc.gamma(M) * ((s.abs() + es) @ w.W.abs())
+    bdx = es @ w.W.abs() + lc.gamma(M, dtype) * ((s.abs() + es) @ w.W.abs())
     bdx = bdx + lc.half(dtype) * (gx.abs() + bdx) + lc.tiny(dtype)
-    bdw = es.t() @ x.abs() + lc.gamma(B) * ((s.abs() + es).t() @ x.abs())
+    bdw = es.t() @ x.abs() + lc.gamma(B, dtype) * ((s.abs() + es).t() @ x.abs())
     bdw = bdw + lc.half(dtype) * (gw.abs() + bdw) + lc.tiny(dtype)
     r = [float(((got.double() - want).abs() / lim).max())
          for got, want, lim in ((db, g.sum(0), bdb), (dx, gx, bdx), (dw, gw, bdw))]

@@ -253,6 +253,35 @@ struct Stages<kRing> {
     char *a[1];
 };
 
+// Hands out a wave's sums.  16 rows at a time go through a piece of LDS of the wave's own (in a
+// stage, which is done with), so that a lane takes four consecutive j of always the same
+// column group and a row leaves in one run.  The 16-byte chunks of row r are permuted by r:
+// the 16 rows of a fragment otherwise start in the same bank.
+template <int FI, int FJ, typename Epi>
+__device__ __forceinline__ void hand_out(const f32x4 (&acc)[FI][FJ], char *piece, int lane,
+                                         int64_t i0, int64_t j0, const Epi &epi) {
+    constexpr int kRow = FJ * 4;  // 16-byte chunks of a row
+    static_assert(64 % kRow == 0, "whole rows per wave and turn");
+    const int l16 = lane & 15, g = lane >> 4;
+    const int rr = lane / kRow, rc = lane % kRow;
+    typename Epi::Column col(epi, j0 + rc * 4);
+#pragma unroll
+    for (int i = 0; i < FI; ++i) {
+#pragma unroll
+        for (int f = 0; f < FJ; ++f)
+            *reinterpret_cast<f32x4 *>(piece + l16 * (FJ * 64) +
+                                       (((f * 4 + g) ^ l16) % kRow) * 16) = acc[i][f];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int r = rr; r < 16; r += 64 / kRow) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(piece + r * (FJ * 64) +
+                                                             ((rc ^ r) % kRow) * 16);
+            epi.put(col, i0 + i * 16 + r, v);
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 // Computes the tile's sums over steps s_begin .. s_end - 1 and hands it out in pieces of
 // four: Epi::Column col(epi, j) once per lane, then epi.put(col, i, D[i][j .. j + 3]) for its
 // rows; i and j may lie past I or J.
@@ -382,33 +411,174 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
             meet<0>();  // no load into LDS outlives the tile
         }
     }
-    // Outputs: 16 rows at a time through a piece of LDS of the wave's own (in a stage,
-    // which is done with), so that a lane takes four consecutive j of always the same column group
-    // and a row leaves in one run.  The 16-byte chunks of row r are permuted by r: the 16
-    // rows of a fragment otherwise start in the same bank.
-    constexpr int kRow = FJ * 4;  // 16-byte chunks of a row
     static_assert(WI * WJ * FJ * 1024 <= TI * kStepBytes, "the waves' pieces fit the buffer");
-    static_assert(64 % kRow == 0, "whole rows per wave and turn");
-    char *piece = st.a[0] + wave * (FJ * 1024);
-    const int l16 = lane & 15, g = lane >> 4;
-    const int rr = lane / kRow, rc = lane % kRow;
-    const int64_t j = j0 + wj * FJ * 16 + rc * 4;
-    typename Epi::Column col(epi, j);
+    hand_out(acc, st.a[0] + wave * (FJ * 1024), lane, i0 + wi * FI * 16, j0 + wj * FJ * 16, epi);
+}
+
+// ---------------------------------------------------------------- fp32 by bf16 terms
+//
+// The matrix cores multiply bf16 16 times as fast as fp32.  An fp32 number is the sum of three
+// bf16 numbers, x = x0 + x1 + x2, each the next eight bits of the significand (truncated, so
+// the differences are exact), and six of the nine products reach fp32's own accuracy:
+//     x y ~ x0 y0 + (x0 y1 + x1 y0) + (x1 y1 + x0 y2 + x2 y0),
+// the three left out being below 2^-22 |x y| together, 2^-24 on average.  Each product is exact
+// and the sums are fp32, in fewer additions than the fp32 instruction makes.  (A term below
+// 2^-133, bf16's smallest number, is lost, so numbers below 2^-109 keep fewer bits.)  The
+// operands stay fp32 in memory and LDS and are split in registers: about 50 VALU instructions
+// for a fragment, which meets FI or FJ others in six matrix instructions each.  VALU issue
+// bounds it: 70 % of the clocks at 4096^3 with 64 x 64 per wave, the matrix cores 52 %.  That
+// takes 0.77 ms (178 TFLOP/s); the fp32 instruction took 1.05 (its peak is 157 TFLOP/s), the
+// library's product 0.91.
+// An infinity has no such split (inf - inf, and inf times a zero term, are NaN): a step that
+// holds an infinity or a NaN is multiplied with the fp32 instruction instead.
+
+struct Terms {
+    s16x8 t[3];
+};
+
+// The terms of eight values; `wild` gathers whether any of them is an infinity or a NaN.
+__device__ __forceinline__ void split_terms(const f32x4 &lo, const f32x4 &hi, Terms &out,
+                                            bool &wild) {
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < FI; ++i) {
-#pragma unroll
-        for (int f = 0; f < FJ; ++f)
-            *reinterpret_cast<f32x4 *>(piece + l16 * (FJ * 64) +
-                                       (((f * 4 + g) ^ l16) % kRow) * 16) = acc[i][f];
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-        for (int r = rr; r < 16; r += 64 / kRow) {
-            const f32x4 v = *reinterpret_cast<const f32x4 *>(piece + r * (FJ * 64) +
-                                                             ((rc ^ r) % kRow) * 16);
-            epi.put(col, i0 + (wi * FI + i) * 16 + r, v);
-        }
-        __builtin_amdgcn_wave_barrier();
+    for (int k = 0; k < 4; ++k) {
+        x[k] = lo[k];
+        x[4 + k] = hi[k];
     }
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 p[3];
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+        uint32_t u[2][3];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float v = x[k + e];
+            const float v0 = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
+            const float r = v - v0;  // exact
+            const float v1 = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
+            u[e][0] = __float_as_uint(v);
+            u[e][1] = __float_as_uint(r);
+            u[e][2] = __float_as_uint(r - v1);  // exact, eight bits
+        }
+        top = __builtin_elementwise_maximum(
+            __builtin_elementwise_maximum(__builtin_fabsf(x[k]), __builtin_fabsf(x[k + 1])), top);
+#pragma unroll
+        for (int t = 0; t < 3; ++t)  // the upper halves of the pair
+            p[t][k / 2] = __builtin_amdgcn_perm(u[1][t], u[0][t], 0x07060302u);
+    }
+    wild = wild || !(top < __builtin_inff());
+#pragma unroll
+    for (int t = 0; t < 3; ++t) out.t[t] = __builtin_bit_cast(s16x8, p[t]);
+}
+
+// gemm_tile for fp32 operands, two stages, k in 32s.
+template <bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, typename Epi>
+__device__ __forceinline__ void gemm_tile_f32(const Operand<float> &A, const Operand<float> &B,
+                                              int64_t i0, int64_t j0, int s_begin, int s_end,
+                                              const Stages<2> &st, const Epi &epi) {
+    constexpr int NT = WI * WJ * 64;
+    constexpr int FI = TI / WI / 16, FJ = TJ / WJ / 16;
+    constexpr int FH = FI / 2;
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wi = wave / WJ, wj = wave % WJ;
+    TileLoader<float, AKM, TI, NT> la;
+    TileLoader<float, BKM, TJ, NT> lb;
+    la.init(A, i0, tid);
+    lb.init(B, j0, tid);
+    constexpr int kLoads = decltype(la)::kLoads + decltype(lb)::kLoads;
+    const FragReader<float, AKM, TI> ra{lane, wi * FI * 16};
+    const FragReader<float, BKM, TJ> rb{lane, wj * FJ * 16};
+    f32x4 acc[FI][FJ];
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 xa[FH][2], xb[FJ][2];  // values of the phase to come
+    auto read_a = [&](const char *ta, int half) {
+#pragma unroll
+        for (int i = 0; i < FH; ++i)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) xa[i][ks] = ra.read(ta, half * FH + i, ks);
+    };
+    auto read_b = [&](const char *tb) {
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) xb[j][ks] = rb.read(tb, j, ks);
+    };
+    Terms pa[FH], pb[FJ];
+    // Half the wave's rows against all its columns; k value 4 g + v of either 16 is lane
+    // group g's, for both operands.
+    auto mul_half = [&](int half) {
+        auto mac = [&](int s, int t) {
+#pragma unroll
+            for (int i = 0; i < FH; ++i)
+#pragma unroll
+                for (int j = 0; j < FJ; ++j)
+                    acc[half * FH + i][j] =
+                        Traits<__bf16>::mma(pb[j].t[s], pa[i].t[t], acc[half * FH + i][j]);
+        };
+        mac(2, 0);
+        mac(0, 2);
+        mac(1, 1);
+        mac(1, 0);
+        mac(0, 1);
+        mac(0, 0);
+    };
+    // The same with the fp32 instruction, from the tile in LDS.
+    auto mul_half_wild = [&](const char *ta, const char *tb, int half) {
+#pragma unroll 1
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int i = 0; i < FH; ++i)
+#pragma unroll
+                for (int j = 0; j < FJ; ++j)
+                    acc[half * FH + i][j] =
+                        Traits<float>::mma(rb.read(tb, j, ks), ra.read(ta, half * FH + i, ks),
+                                           acc[half * FH + i][j]);
+    };
+    auto step = [&](int s, char *ta, char *tb, const char *na, const char *nb) {
+        bool wild = false;
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) split_terms(xb[j][0], xb[j][1], pb[j], wild);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int i = 0; i < FH; ++i) split_terms(xa[i][0], xa[i][1], pa[i], wild);
+            const bool slow = __any(wild);
+            if (__builtin_expect(slow, 0)) mul_half_wild(ta, tb, half);
+            if (half == 0) {
+                read_a(ta, 1);
+            } else {
+                meet<0>();
+                la.load(ta, s + 2 < s_end ? s + 2 : kPastEnd, tid);
+                lb.load(tb, s + 2 < s_end ? s + 2 : kPastEnd, tid);
+                read_a(na, 0);
+                read_b(nb);
+            }
+            if (__builtin_expect(!slow, 1)) mul_half(half);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    if (s_begin < s_end) {
+        la.load(st.a[0], s_begin, tid);
+        lb.load(st.b[0], s_begin, tid);
+        la.load(st.a[1], s_begin + 1 < s_end ? s_begin + 1 : kPastEnd, tid);
+        lb.load(st.b[1], s_begin + 1 < s_end ? s_begin + 1 : kPastEnd, tid);
+        meet<kLoads>();
+        read_a(st.a[0], 0);
+        read_b(st.b[0]);
+        for (int s = s_begin; s < s_end; s += 2) {
+            step(s, st.a[0], st.b[0], st.a[1], st.b[1]);
+            step(s + 1, st.a[1], st.b[1], st.a[0], st.b[0]);
+        }
+        meet<0>();  // no load into LDS outlives the tile
+    }
+    static_assert(WI * WJ * FJ * 1024 <= TI * kStepBytes, "the waves' pieces fit the buffer");
+    hand_out(acc, st.a[0] + wave * (FJ * 1024), lane, i0 + wi * FI * 16, j0 + wj * FJ * 16, epi);
 }
 
 }  // namespace gemm

@@ -366,9 +366,11 @@ __global__ __launch_bounds__(WI *WJ * 64) void gemm_kernel(Operand<T> A, Operand
     const int s1 = s0 + steps_per_split < steps ? s0 + steps_per_split : steps;
     if constexpr (__is_same(Epi, PartEpilogue))
         epi.part += static_cast<int64_t>(blockIdx.y) * epi.I * epi.ld;
-    gemm::gemm_tile<T, AKM, BKM, TI, TJ, WI, WJ, NB>(A, B, static_cast<int64_t>(ti) * TI,
-                                                     static_cast<int64_t>(tj) * TJ, s0, s1, st,
-                                                     epi);
+    const int64_t i0 = static_cast<int64_t>(ti) * TI, j0 = static_cast<int64_t>(tj) * TJ;
+    if constexpr (sizeof(T) == 4)
+        gemm::gemm_tile_f32<AKM, BKM, TI, TJ, WI, WJ>(A, B, i0, j0, s0, s1, st, epi);
+    else
+        gemm::gemm_tile<T, AKM, BKM, TI, TJ, WI, WJ, NB>(A, B, i0, j0, s0, s1, st, epi);
 }
 
 // The splits' shares added in order, four values per thread, and handed to the epilogue.
@@ -414,9 +416,9 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
     if constexpr (sizeof(T) == 2) {
         if (pl.tile == kTile256)
             return launch_tiles<T, AKM, BKM, 256, 256, 2, 4, gemm::kRing>(A, B, pl, epi, s);
-        if (pl.tile == kTile128)
-            return launch_tiles<T, AKM, BKM, 128, 128, 2, 2, 4>(A, B, pl, epi, s);
     }
+    if (pl.tile == kTile128)
+        return launch_tiles<T, AKM, BKM, 128, 128, 2, 2, sizeof(T) == 2 ? 4 : 2>(A, B, pl, epi, s);
     return launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 2>(A, B, pl, epi, s);
 }
 
@@ -1187,8 +1189,9 @@ size_t linear_small_bytes(size_t size, int64_t N, int bt) {
 // k, was fitted to calls with all three forced on the same shapes, and the cheapest is taken
 // (566 x 6912 x 2176 in bf16: 56 us per call with 64 x 128, 76 with 128 x 128, 70 with
 // 256 x 256; 2176 x 6912 x 576: 57, 72 and 40; 1024 x 4096 x 4096: 67, 63 and 99).
-//   In fp32 the matrix instruction is the bound whatever the tile, and the smallest wastes
-// least (566 x 6912 x 2176: 164 us against 288 with 128 x 128; 4096^3: 1087 against 1077).
+//   fp32 has 128 x 128 ones with two stages, which split a fragment's values for twice as
+// many products but leave more of the card idle in a last round (566 x 6912 x 2176: 152 us
+// per call with 64 x 128, 200 with 128 x 128; 2176 x 6912 x 576: 145 and 127).
 GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K) {
     constexpr int64_t kCus = 256;
     const auto tiles = [&](int64_t ti, int64_t tj) {
@@ -1210,22 +1213,28 @@ GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K) {
                    ? (p.steps + p.steps_per_split - 1) / p.steps_per_split
                    : 1;
     p.part_bytes = p.splits > 1 ? static_cast<size_t>(p.splits) * I * p.part_ld * 4 : 0;
+    // us; the shares are written and read at about 4 TB/s, and their kernel takes 5
+    const double steps = p.steps;
+    const double r = rounds(n * p.splits);
+    double best = p.splits > 1 ? 5.0 + 2.0 * p.part_bytes / 4e6 : 0.0;
+    if (size == 2)
+        best += 4.0 + 1.5 * r + 0.33 * (r < 3 ? 3 : r) * p.steps_per_split;
+    else
+        best += 4.0 + r * (1.5 + 0.88 * p.steps_per_split);
+    const auto take = [&](int tile, double us) {
+        if (us >= best) return;
+        best = us;
+        p.tile = tile;
+        p.splits = 1;
+        p.steps_per_split = p.steps;
+        p.part_bytes = 0;
+    };
+    const double r128 = rounds(tiles(128, 128));
     if (size == 2) {
-        // us; the shares are written and read at about 4 TB/s, and their kernel takes 5
-        const double r = rounds(n * p.splits);
-        double best = 4.0 + 1.5 * r + 0.33 * (r < 3 ? 3 : r) * p.steps_per_split +
-                      (p.splits > 1 ? 5.0 + 2.0 * p.part_bytes / 4e6 : 0.0);
-        const auto take = [&](int tile, double us) {
-            if (us >= best) return;
-            best = us;
-            p.tile = tile;
-            p.splits = 1;
-            p.steps_per_split = p.steps;
-            p.part_bytes = 0;
-        };
-        const double steps = p.steps;
-        take(kTile128, 4.0 + rounds(tiles(128, 128)) * (5.0 + 0.8 * steps));
+        take(kTile128, 4.0 + r128 * (5.0 + 0.8 * steps));
         take(kTile256, 7.0 + rounds(tiles(256, 256)) * (12.0 + 1.4 * steps));
+    } else {
+        take(kTile128, 4.0 + r128 * (4.0 + 1.55 * steps));
     }
     return p;
 }
