@@ -430,7 +430,7 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
 //   Lane (row l16, group g) reads the K words of columns 32 g .. 32 g + 31 of a unit and the
 // word before them: the vector memory unit takes about four clocks per cache line of an
 // instruction, and a read per chunk (two or three words of 16 rows each) had bounded the
-// kernel (one row, 4096 x 14336 at k = 3: 45 us, now 18).  Its four chunks are aligned with
+// kernel (one row, 4096 x 14336 at k = 3: 45 us per call, now 18).  Its four chunks are aligned with
 // constant shifts and exchanged between the lane groups, so that in step s lane (l16, g)
 // holds columns 32 s + 8 g .. + 7, its piece of the matrix instruction's first operand,
 // decodes it from the table in LDS and multiplies with 16 rows of x.  Up to 16 rows of x
@@ -465,6 +465,9 @@ struct SmallShape {
     // tiles held at a time, and units held per tile (by the registers)
     static constexpr int TR = ONE || sizeof(T) == 4 || BT > 2 ? 1 : 2;
     static constexpr int UN = ONE || (sizeof(T) == 4 && BT > 4) ? 1 : 2;
+    // steps ahead that x is asked for (one less than a divisor of 4; by the registers)
+    static constexpr int kAhead =
+        BT == 1 ? 3 : (BT * static_cast<int>(sizeof(T)) <= 8 ? 1 : 0);
     // tiles and batch tiles whose sums meet at a time (16 KiB each, beside the table)
     static constexpr int kSumsR = ONE ? TR : 1;
     static constexpr int kSums = ONE && BT > 1 ? 2 : 1;
@@ -627,8 +630,22 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
             for (int t = 0; t < BT; ++t) acc[r][t] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
         if constexpr (ONE) {
+            // x is asked for kAhead steps before its use, the words a unit before
+            constexpr int kAhead = Sh::kAhead;
             uint32_t w[K + 1];
-            if (u_begin < u_end) request(rbits[0], rs0[0], u_begin, w);
+            Piece x[kAhead + 1][BT];
+            const uint32_t s_end = u_end * 4 < a.runs ? u_end * 4 : a.runs;
+            auto ask = [&](uint32_t s, Piece (&to)[BT]) {
+                if (s < s_end) {
+#pragma unroll
+                    for (int t = 0; t < BT; ++t) to[t] = read_x(s, t);
+                }
+            };
+            if (u_begin < u_end) {
+                request(rbits[0], rs0[0], u_begin, w);
+#pragma unroll
+                for (int s = 0; s < kAhead; ++s) ask(u_begin * 4 + s, x[s]);
+            }
             for (uint32_t u = u_begin; u < u_end; ++u) {
                 uint32_t n[4][C::NW];
                 align(w, n);
@@ -636,15 +653,13 @@ __global__ __launch_bounds__(kSmallWaves * 64) void small_kernel(SmallArgs a,
                 request(rbits[0], rs0[0], u + 1 < u_end ? u + 1 : u, w);
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
-                    if (u * 4 + s < a.runs) {
-                        Piece x[BT];
-#pragma unroll
-                        for (int t = 0; t < BT; ++t)
-                            x[t] = read_x(u * 4 + s, t);
+                    ask(u * 4 + s + kAhead, x[(s + kAhead) % (kAhead + 1)]);
+                    if (u * 4 + s < s_end) {
                         uint32_t val[kWords] = {};
                         decode(n[s], 0u, val);
 #pragma unroll
-                        for (int t = 0; t < BT; ++t) acc[0][t] = multiply(val, x[t], acc[0][t]);
+                        for (int t = 0; t < BT; ++t)
+                            acc[0][t] = multiply(val, x[s % (kAhead + 1)][t], acc[0][t]);
                     }
                 }
             }
@@ -1160,9 +1175,10 @@ size_t pad8(int64_t n) { return static_cast<size_t>((n + 7) / 8 * 8); }
 
 }  // namespace
 
-// Measured limits (us per call, decoded inside / through the workspace): tables of one part,
-// 4096 x 4096 in bf16, 128 rows 21 / 36, 256 rows 40 / 39; two parts, 14336 x 4096 V=2, 64 rows
-// 55 / 71, 128 rows 78 / 80; fp32, 4096 x 4096, 128 rows 62 / 77, 256 rows 116 / 112.
+// Up to 128 rows are decoded inside the product, 64 where a 16-bit table has several parts
+// (us per call, inside / through the workspace).  4096 x 4096 in bf16: 128 rows 22 / 32, and 256
+// would take 40 / 35; 14336 x 4096 V=2 in bf16: 64 rows 52 / 71, and 128 would take 78 / 74;
+// 4096 x 4096 in fp32: 128 rows 66 / 78, and 256 would take 116 / 85.
 int linear_small(size_t size, int64_t B, int64_t N, int L, int k, int V, int T) {
     const int kv = k * V;
     if (N <= 0 || T % 32 != 0 || kv > 4 || (V != 1 && V != 2 && V != 4)) return 0;
