@@ -397,6 +397,7 @@ int tcq_act_unpack(const int8_t *codes, int64_t ldq, const uint8_t *scale, int64
  *     s[b][r]  = g[b][r] row_scale[r]          rounded to the layer's type
  *     dx[b][c] = sum_r s[b][r] W_hat[r][c]
  *     dw[r][c] = sum_b s[b][r] x[b][c]         the gradient of W_hat (straight through to W)
+ * relu's g is dy where z > 0, 0 where z <= 0 (whatever dy holds) and NaN where z is NaN.
  * The residual's gradient is dy itself.  Sums are fp32 in a fixed order; outputs of the
  * layer's type are rounded once.
  *   dy, B, lddy : device, B x M of type dtype

@@ -457,6 +457,69 @@ def test_backward_within_bounds(oracle_lib, shape, B, act, dtype):
     assert max(r) <= 1
 
 
+def test_threads_with_tables_of_two_sizes():
+    """Two host threads on their own streams call one kernel at once, one with a table that
+    takes 128 KiB of LDS and one with a table of 2 KiB: both are launched, and right."""
+    import threading
+    dtype = torch.bfloat16
+    M, N = 64, 512
+    ws = [Coded(L, M, N, L, 2, 1, 256, dtype, True) for L in (16, 10)]
+    cases = [[(w, x, (x.double() @ w.W.t()).to(dtype)) for x in
+              (_ints(np.random.default_rng(B), B, N, dtype) for B in (3, 150))] for w in ws]
+    torch.cuda.synchronize()
+    errs = []
+
+    def work(mine):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(200):
+                    for w, x, want in mine:
+                        y = w.linear(x)
+                for w, x, want in mine:
+                    assert torch.equal(w.linear(x), want)
+                s.synchronize()
+        except Exception as e:  # reported below
+            errs.append(e)
+    ths = [threading.Thread(target=work, args=(mine,)) for mine in cases]
+    for t in ths:
+        t.start()
+    for t in ths:
+        t.join(timeout=60)
+    assert not any(t.is_alive() for t in ths) and not errs, errs
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_backward_relu_selects(dtype):
+    """Infinite and NaN dy at closed units leave no trace; a checkpoint group of z that
+    holds an infinity gives NaN, and no other group does."""
+    M, N, B = 96, 256, 40
+    w = Coded(8, M, N, 16, 2, 1, 256, dtype, True)
+    rng = np.random.default_rng(9)
+    z = torch.from_numpy(rng.choice([-2.0, -1.0, 0.0, 1.0, 2.0], size=(B, M))).to(dtype).cuda()
+    dy = _ints(rng, B, M, dtype)
+    x = _ints(rng, B, N, dtype)
+    clean = torch.where(z > 0, dy, torch.zeros_like(dy))
+    bad = torch.tensor([float("inf"), float("-inf"), float("nan")], dtype=dtype, device="cuda")
+    dy = torch.where(z > 0, dy, bad[torch.arange(M, device="cuda") % 3].expand(B, M))
+    xp = api.act_pack(x)
+    xv = api.act_unpack(xp, torch.float32).double()
+    dx, dw, db = w.backward(dy, act="relu", z=api.act_pack(z), x=xp)
+    s = clean.double()
+    # integers and multiples of 1/8: every sum is an fp32 number in any order
+    assert torch.equal(dx, (s @ w.W).to(dtype))
+    assert torch.equal(dw, (s.t() @ xv).to(dtype))
+    assert torch.equal(db, s.sum(0).float())
+    z[3, 40] = float("inf")                       # columns 32 .. 63 of row 3
+    dx, dw, db = w.backward(dy, act="relu", z=api.act_pack(z), x=xp)
+    lost = (torch.arange(M, device="cuda") // 32) == 1
+    assert torch.equal(torch.isnan(db), lost)
+    assert torch.equal(torch.isnan(dx).all(1), torch.arange(B, device="cuda") == 3)
+    assert torch.equal(torch.isnan(dw).all(1), lost) and not torch.isnan(dw[~lost]).any()
+    rows = torch.arange(B, device="cuda") != 3
+    assert torch.equal(dx[rows], (s @ w.W).to(dtype)[rows])
+
+
 def test_gradients_against_differences():
     """fp32: the gradients of sum(y G) in x, W_hat and bias against central differences of
     the float64 layer.  x is a small integer, which its checkpoint holds exactly; z is not

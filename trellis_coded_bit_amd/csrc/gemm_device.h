@@ -10,11 +10,11 @@
 // A workgroup computes a TI x TJ tile of D over steps of 128 bytes of k per row (64 16-bit or
 // 32 fp32 values).  Both operand tiles of a step go from global memory straight into LDS
 // (buffer_load_dwordx4 ... lds), in NB stages: the loads of the next NB - 1 steps are in
-// flight while a step is multiplied (or in a ring of five pieces).  The stages are separate LDS variables, and the loop is
-// unrolled over them, so that the compiler sees that reads of one cannot touch the loads
-// into the others and does not wait for those.  Rows past I or J and k past K read as zeros:
-// a buffer descriptor ends with the operand's last row, and lanes past K get an offset
-// past its end.
+// flight while a step is multiplied (or in a ring of five pieces).  The stages are separate
+// LDS variables, and the loop is unrolled over them, so that the compiler sees that reads of
+// one cannot touch the loads into the others and does not wait for those.  Rows past I or J
+// and k past K read as zeros: a buffer descriptor ends with the operand's last row, and lanes
+// past K get an offset past its end.
 //
 // LDS layout.  A k-contiguous tile has rows of 128 bytes, eight 16-byte chunks; chunk c of
 // row r sits in slot c ^ ((r >> 1) & 7), so the 16 rows that a fragment read touches lie in

@@ -2,7 +2,7 @@
 // rows x, with the trellis-coded matrix W_hat decoded inside the call, and its gradients.
 //
 // The matrix is decoded once into the workspace, in the layer's type, and multiplied on the
-// matrix cores (gemm_device.h).  With the table in the layer's own type a decoded weight is
+// matrix cores (gemm_device.h); for few rows it is decoded inside the product.  With the table in the layer's own type a decoded weight is
 // a table entry copied bit for bit, so every product is exact and the sums are fp32: the
 // outputs' own rounding is the only one to 16 bits in the forward pass.  The backward pass
 // rounds the incoming gradient times the activation's slope and the row scale once, to the
@@ -430,8 +430,8 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
 //   Lane (row l16, group g) reads the K words of columns 32 g .. 32 g + 31 of a unit and the
 // word before them: the vector memory unit takes about four clocks per cache line of an
 // instruction, and a read per chunk (two or three words of 16 rows each) had bounded the
-// kernel (one row, 4096 x 14336 at k = 3: 45 us per call, now 18).  Its four chunks are aligned with
-// constant shifts and exchanged between the lane groups, so that in step s lane (l16, g)
+// kernel (one row, 4096 x 14336 at k = 3: 45 us per call, now 18).  Its four chunks are
+// aligned with constant shifts and exchanged between the lane groups, so that in step s lane (l16, g)
 // holds columns 32 s + 8 g .. + 7, its piece of the matrix instruction's first operand,
 // decodes it from the table in LDS and multiplies with 16 rows of x.  Up to 16 rows of x
 // are read as they are (any alignment); more are first laid out by pack_rows_kernel in the
@@ -804,7 +804,7 @@ __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__
             for (int e = 0; e < 8; ++e) {
                 float g = static_cast<float>(d.v[e]);
                 if constexpr (ACT != TCQ_ACT_NONE)
-                    if (e < left) g *= act_slope<ACT>(code_value(z.v[e], ez));
+                    if (e < left) g = act_grad<ACT>(g, code_value(z.v[e], ez));
                 sum[e] += g;
                 o.v[e] = static_cast<T>(g * sc[e]);
             }
@@ -922,11 +922,12 @@ const void *chunk_kernel(int kv, int V, bool one) {
     return nullptr;
 }
 
-// Raises the dynamic LDS limit of a kernel.  Set on every launch: the attribute belongs to
-// the function on the current device, and nothing is kept between calls.
-hipError_t allow_lds(const void *kern, size_t bytes) {
-    return hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(bytes));
+// Raises the dynamic LDS limit of a kernel to all of a compute unit's.  Set on every launch: the
+// attribute belongs to the function on the current device, and nothing is kept between
+// calls.  Always the same number: with a call's own size, another thread's call of the same
+// kernel with a smaller table could lower it before this one is launched.
+hipError_t allow_lds(const void *kern) {
+    return hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
 }
 
 template <typename T>
@@ -969,7 +970,7 @@ hipError_t decode_matrix(const CodedMatrix &w, T *out, int64_t ld, hipStream_t s
         const int64_t per = (a.chunks_per_wg + kChunkThreads - 1) / kChunkThreads;
         const int64_t turns = (per + rt - 1) / rt;
         a.rows = static_cast<int>((per + turns - 1) / turns);
-        hipError_t e = allow_lds(kern, lds);
+        hipError_t e = allow_lds(kern);
         if (e != hipSuccess) return e;
         T *o = out;
         void *args[] = {&a, &o};
@@ -1046,7 +1047,8 @@ hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, char *ws, hi
     a.vec = (reinterpret_cast<uintptr_t>(w.table) & 15) == 0;
     hipError_t e;
     if constexpr (BT > 1) {
-        const int64_t pieces = static_cast<int64_t>(a.runs) * BT * static_cast<int64_t>(sizeof(T) / 2) * 64;
+        const int64_t pieces =
+            static_cast<int64_t>(a.runs) * BT * static_cast<int64_t>(sizeof(T) / 2) * 64;
         hipLaunchKernelGGL((pack_rows_kernel<T, BT>), dim3(grid_for(pieces, 256, 1 << 16)),
                            dim3(256), 0, s, static_cast<const T *>(c.x), c.B, c.ldx, pieces,
                            reinterpret_cast<uint4 *>(ws));
@@ -1065,7 +1067,7 @@ hipError_t forward_small(const CodedMatrix &w, const LinearCall &c, char *ws, hi
     const size_t lds = a.red + sums;
     const void *kern = one ? small_kernel_of<T, BT, true>(kv, w.V)
                            : small_kernel_of<T, BT, false>(kv, w.V);
-    e = allow_lds(kern, lds);
+    e = allow_lds(kern);
     if (e != hipSuccess) return e;
     const int64_t turns = ((w.M + 15) / 16 + tr - 1) / tr;
     const int64_t slots = static_cast<int64_t>(cu_count()) * (lds <= (80 << 10) ? 2 : 1);
@@ -1176,9 +1178,9 @@ size_t pad8(int64_t n) { return static_cast<size_t>((n + 7) / 8 * 8); }
 }  // namespace
 
 // Up to 128 rows are decoded inside the product, 64 where a 16-bit table has several parts
-// (us per call, inside / through the workspace).  4096 x 4096 in bf16: 128 rows 22 / 32, and 256
-// would take 40 / 35; 14336 x 4096 V=2 in bf16: 64 rows 52 / 71, and 128 would take 78 / 74;
-// 4096 x 4096 in fp32: 128 rows 66 / 78, and 256 would take 116 / 85.
+// (us per call, inside at the limit / through the workspace with one row more).  4096 x 4096 in
+// bf16: 22 / 32; 14336 x 4096 V=2 in bf16: 52 / 71; 4096 x 4096 in fp32: 66 / 78.  Beyond it,
+// inside / through the workspace: 256 rows of the first 40 / 35, 128 rows of the second 78 / 74.
 int linear_small(size_t size, int64_t B, int64_t N, int L, int k, int V, int T) {
     const int kv = k * V;
     if (N <= 0 || T % 32 != 0 || kv > 4 || (V != 1 && V != 2 && V != 4)) return 0;

@@ -53,20 +53,22 @@ __device__ __forceinline__ float act_value(float z) {
     return z;
 }
 
-// act'(z), in fp32 (relu: 1 for z > 0, else 0).
+// g act'(z), in fp32.  relu selects (0 at z <= 0, whatever g holds there), and a NaN z gives
+// NaN as the other activations do: a checkpoint's group with an infinity stands for NaN,
+// which must not pass for closed units.
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-    if constexpr (ACT == TCQ_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+__device__ __forceinline__ float act_grad(float g, float z) {
+    if constexpr (ACT == TCQ_ACT_RELU) return z > 0.0f ? g : (z <= 0.0f ? 0.0f : z);
     if constexpr (ACT == TCQ_ACT_SILU) {
         const float s = sigmoid(z);
-        return s * __builtin_fmaf(z, 1.0f - s, 1.0f);
+        return g * (s * __builtin_fmaf(z, 1.0f - s, 1.0f));
     }
     if constexpr (ACT == TCQ_ACT_GELU) {
         float e;
         const float c = normal_cdf(z, e);
-        return __builtin_fmaf(z, 0.39894228040143268f * e, c);
+        return g * __builtin_fmaf(z, 0.39894228040143268f * e, c);
     }
-    return 1.0f;
+    return g;
 }
 
 // f(std::integral_constant<int, ACT>) for a uniform act.
