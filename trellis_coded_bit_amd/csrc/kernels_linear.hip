@@ -405,8 +405,11 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
     if (A.rows <= 0 || B.rows <= 0) return hipSuccess;
     if (pl.splits > 1) {
         const PartEpilogue pe{reinterpret_cast<float *>(part), pl.part_ld, A.rows, B.rows};
-        // (only 64 x 128 tiles are split)
-        const hipError_t e = launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 2>(A, B, pl, pe, s);
+        // (256 x 256 tiles are not split)
+        const hipError_t e =
+            pl.tile == kTile128
+                ? launch_tiles<T, AKM, BKM, 128, 128, 2, 2, sizeof(T) == 2 ? 4 : 2>(A, B, pl, pe, s)
+                : launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 2>(A, B, pl, pe, s);
         if (e != hipSuccess) return e;
         const int64_t quads = A.rows * (pl.part_ld / 4);
         hipLaunchKernelGGL(split_sum_kernel<Epi>, dim3(static_cast<unsigned>((quads + 255) / 256)),
@@ -1179,8 +1182,8 @@ size_t pad8(int64_t n) { return static_cast<size_t>((n + 7) / 8 * 8); }
 
 // Up to 128 rows are decoded inside the product, 64 where a 16-bit table has several parts
 // (us per call, inside at the limit / through the workspace with one row more).  4096 x 4096 in
-// bf16: 22 / 32; 14336 x 4096 V=2 in bf16: 52 / 71; 4096 x 4096 in fp32: 66 / 78.  Beyond it,
-// inside / through the workspace: 256 rows of the first 40 / 35, 128 rows of the second 78 / 74.
+// bf16: 22 / 32; 14336 x 4096 V=2 in bf16: 52 / 69; 4096 x 4096 in fp32: 67 / 80.  Beyond it,
+// inside / through the workspace: 256 rows of the first 40 / 35, 128 rows of the second 78 / 72.
 int linear_small(size_t size, int64_t B, int64_t N, int L, int k, int V, int T) {
     const int kv = k * V;
     if (N <= 0 || T % 32 != 0 || kv > 4 || (V != 1 && V != 2 && V != 4)) return 0;
@@ -1198,18 +1201,22 @@ size_t linear_small_bytes(size_t size, int64_t N, int bt) {
 // Tile and splits of an I x J product over K.  The choice depends on sizes alone (and on
 // the 256 compute units of the part this library is built for), so the workspace query
 // and the call agree.
-//   64 x 128 tiles with two stages run three to a compute unit.  Where they are at most one
-// per unit, k is split into about 512 workgroups (at least 4 steps each) and the shares, in
-// fp32, are added by a second kernel (512 x 4096 x 4096 in bf16: 57 us per call unsplit, 45
-// split; 160 rows: 40 and 32).
+//   64 x 128 tiles with two stages run three to a compute unit.  Where there are few, k is
+// split into about 512 workgroups (at least 4 steps each) and the shares, in fp32, are added
+// by a second kernel (512 x 4096 x 4096 in bf16: 57 us per call unsplit, 45 split; 160 rows: 40
+// and 32).
 //   16-bit types also have 256 x 256 tiles (the ring) and 128 x 128 ones (four stages), one
 // to a compute unit.  Tiles come in rounds of 256; what a round costs, once and per step of
 // k, was fitted to calls with all three forced on the same shapes, and the cheapest is taken
 // (566 x 6912 x 2176 in bf16: 56 us per call with 64 x 128, 76 with 128 x 128, 70 with
 // 256 x 256; 2176 x 6912 x 576: 57, 72 and 40; 1024 x 4096 x 4096: 67, 63 and 99).
-//   fp32 has 128 x 128 ones with two stages, which split a fragment's values for twice as
+//   fp32 has 128 x 128 ones with two stages, two to a compute unit, which split a fragment's values for twice as
 // many products but leave more of the card idle in a last round (566 x 6912 x 2176: 152 us
 // per call with 64 x 128, 200 with 128 x 128; 2176 x 6912 x 576: 145 and 127).
+//   128 x 128 tiles are split over k too, into 256 workgroups of a 16-bit type and 512 in fp32,
+// where two share a compute unit (1000 x 2048 x 2048 as 64 x 128 and 128 x 128, both split: 39
+// and 34 us per call in bf16, 82 and 75 in fp32, where 256 workgroups take 86; 200 x 14336 x
+// 4096 in fp32: 330 and 268; 333 x 2048 x 2048: 30 and 32 in bf16, 51 and 51 in fp32).
 GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K) {
     constexpr int64_t kCus = 256;
     const auto tiles = [&](int64_t ti, int64_t tj) {
@@ -1218,43 +1225,57 @@ GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K) {
     const auto rounds = [&](int64_t n) { return static_cast<double>((n + kCus - 1) / kCus); };
     GemmPlan p{};
     const int64_t step = gemm::kStepBytes / static_cast<int64_t>(size);
-    p.tile = kTile64;
     p.steps = static_cast<int>((K + step - 1) / step);
     p.part_ld = (J + 3) / 4 * 4;
-    const int64_t n = tiles(64, 128);
-    int64_t s = n > 0 ? 2 * kCus / n : 1;
-    if (s > p.steps / 4) s = p.steps / 4;
-    if (s > 16) s = 16;
-    if (s < 1) s = 1;
-    p.steps_per_split = static_cast<int>((p.steps + s - 1) / s);
-    p.splits = p.steps_per_split > 0
-                   ? (p.steps + p.steps_per_split - 1) / p.steps_per_split
-                   : 1;
-    p.part_bytes = p.splits > 1 ? static_cast<size_t>(p.splits) * I * p.part_ld * 4 : 0;
-    // us; the shares are written and read at about 4 TB/s, and their kernel takes 5
-    const double steps = p.steps;
-    const double r = rounds(n * p.splits);
-    double best = p.splits > 1 ? 5.0 + 2.0 * p.part_bytes / 4e6 : 0.0;
-    if (size == 2)
-        best += 4.0 + 1.5 * r + 0.33 * (r < 3 ? 3 : r) * p.steps_per_split;
-    else
-        best += 4.0 + r * (1.5 + 0.88 * p.steps_per_split);
-    const auto take = [&](int tile, double us) {
-        if (us >= best) return;
-        best = us;
-        p.tile = tile;
-        p.splits = 1;
-        p.steps_per_split = p.steps;
-        p.part_bytes = 0;
+    // n tiles with k split into about `most` workgroups
+    const auto split = [&](int tile, int64_t n, int64_t most) {
+        GemmPlan q = p;
+        q.tile = tile;
+        int64_t s = n > 0 ? most / n : 1;
+        if (s > q.steps / 4) s = q.steps / 4;
+        if (s > 16) s = 16;
+        if (s < 1) s = 1;
+        q.steps_per_split = static_cast<int>((q.steps + s - 1) / s);
+        q.splits = q.steps_per_split > 0
+                       ? (q.steps + q.steps_per_split - 1) / q.steps_per_split
+                       : 1;
+        q.part_bytes = q.splits > 1 ? static_cast<size_t>(q.splits) * I * q.part_ld * 4 : 0;
+        return q;
     };
-    const double r128 = rounds(tiles(128, 128));
+    // us; the shares are read at about 4 TB/s, and their kernel takes 3 more
+    const auto join = [](const GemmPlan &q) {
+        return q.splits > 1 ? 3.0 + q.part_bytes / 4e6 : 0.0;
+    };
+    GemmPlan best{};
+    double least = 0.0;
+    const auto take = [&](const GemmPlan &q, double us) {
+        us += join(q);
+        if (best.splits != 0 && us >= least) return;
+        least = us;
+        best = q;
+    };
+    const int64_t n64 = tiles(64, 128), n128 = tiles(128, 128);
+    const GemmPlan s64 = split(kTile64, n64, 2 * kCus);
+    const double r = rounds(n64 * s64.splits);
     if (size == 2) {
-        take(kTile128, 4.0 + r128 * (5.0 + 0.8 * steps));
-        take(kTile256, 7.0 + rounds(tiles(256, 256)) * (12.0 + 1.4 * steps));
+        take(s64, 4.0 + 1.5 * r + 0.33 * (r < 3 ? 3 : r) * s64.steps_per_split);
+        take(split(kTile128, n128, n128), 4.0 + rounds(n128) * (5.0 + 0.8 * p.steps));
+        take(split(kTile256, 1, 1), 7.0 + rounds(tiles(256, 256)) * (12.0 + 1.4 * p.steps));
+        const GemmPlan q = split(kTile128, n128, kCus);
+        if (q.splits > 1) take(q, 9.0 + 0.8 * q.steps_per_split);
     } else {
-        take(kTile128, 4.0 + r128 * (4.0 + 1.55 * steps));
+        take(s64, 4.0 + r * (1.5 + 0.88 * s64.steps_per_split));
+        // rounds of two to a compute unit, the last of one where that is enough
+        const auto pairs = [&](const GemmPlan &q) {
+            const int64_t n = n128 * q.splits, left = n % (2 * kCus);
+            return 4.0 + (n / (2 * kCus) + (left > kCus)) * (8.0 + 2.6 * q.steps_per_split) +
+                   (left > 0 && left <= kCus ? 4.0 + 2.0 * q.steps_per_split : 0.0);
+        };
+        const GemmPlan whole = split(kTile128, n128, n128), q = split(kTile128, n128, 2 * kCus);
+        take(whole, pairs(whole));
+        if (q.splits > 1) take(q, pairs(q));
     }
-    return p;
+    return best;
 }
 
 LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N) {
