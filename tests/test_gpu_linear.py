@@ -457,6 +457,29 @@ def test_backward_within_bounds(oracle_lib, shape, B, act, dtype):
     assert max(r) <= 1
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("L,k,V,T,M,N,B", [
+    (16, 2, 1, 256, 2047, 2048, 1001), (16, 2, 1, 256, 1023, 2048, 1500),
+    (16, 1, 1, 17, 2047, 17 * 121, 1001)])
+def test_exact_middle_sizes(L, k, V, T, M, N, B, dtype):
+    """Sizes between few tiles and many, where each of the three products is split over its
+    sum in some type: forward and backward."""
+    _say(f"exact middle sizes M={M} N={N} B={B} {dtype}")
+    rng = np.random.default_rng(M + B)
+    w = Coded(B, M, N, L, k, V, T, dtype, True)
+    x = _ints(rng, B, N, dtype)
+    _exact_forward(w, x, rng, dtype, "relu", True, True)
+    dy = _ints(rng, B, M, dtype, 2)
+    zp, xp = api.act_pack(_ints(rng, B, M, dtype)), api.act_pack(x)
+    z, xv = api.act_unpack(zp, torch.float32).double(), api.act_unpack(xp, torch.float32).double()
+    g, s, gx, gw = _grad_reference(w, dy, None, "relu", z, xv, dtype, False)
+    dx, dw, db = w.backward(dy, act="relu", z=zp, x=xp)
+    torch.cuda.synchronize()
+    assert torch.equal(db.double(), g.sum(0))
+    assert torch.equal(dx, gx.to(dtype))
+    assert torch.equal(dw, gw.to(dtype))
+
+
 def test_threads_with_tables_of_two_sizes():
     """Two host threads on their own streams call one kernel at once, one with a table that
     takes 128 KiB of LDS and one with a table of 2 KiB: both are launched, and right."""
