@@ -8,37 +8,16 @@
 // the whole group NaN.
 #include <hip/hip_runtime.h>
 
-#include "linear_device.h"
+#include "checkpoint_device.h"
 #include "tcq.h"
 #include "tcq_internal.h"
 
 namespace tcq {
 namespace {
 
-constexpr int kGroup = 32;
-
-// Eight consecutive values per thread; four neighbouring lanes share a group.  Global
-// loads and stores of any alignment are legal on this hardware, so rows may start anywhere.
-struct Index {
-    uint32_t cpr;      // eights per row: 4 per group
-    int64_t total;     // rows x cpr
-};
-
-// Row r and eight c of flat index i (32-bit division where the total allows it).
-template <bool SMALL>
-__device__ __forceinline__ void split(int64_t i, uint32_t cpr, int64_t &r, uint32_t &c) {
-    if constexpr (SMALL) {
-        const uint32_t q = static_cast<uint32_t>(i) / cpr;
-        r = q;
-        c = static_cast<uint32_t>(i) - q * cpr;
-    } else {
-        r = i / cpr;
-        c = static_cast<uint32_t>(i - r * cpr);
-    }
-}
-
+// Eight consecutive values per thread; four neighbouring lanes share a group.
 template <typename T, bool SMALL>
-__global__ __launch_bounds__(256) void act_pack_kernel(const T *__restrict__ X, Index ix,
+__global__ __launch_bounds__(256) void act_pack_kernel(const T *__restrict__ X, Pieces ix,
                                                        int64_t cols, int64_t ldx,
                                                        int8_t *__restrict__ codes, int64_t ldq,
                                                        uint8_t *__restrict__ scale) {
@@ -94,53 +73,9 @@ __global__ __launch_bounds__(256) void act_pack_kernel(const T *__restrict__ X, 
     }
 }
 
-// 16 bytes of output per thread (8 values of a 16-bit type, 4 of fp32), so that a wave's
-// stores fill whole lines; they bypass the caches (16384 x 14336 in bf16: 121 us against 166
-// with plain stores; with two 16-byte pieces per thread, 357 against 241 in fp32).  out's
-// columns cols .. padded - 1 are zeros.  cpr counts the pieces of a padded row.
 template <typename T, bool SMALL>
-__global__ __launch_bounds__(256) void act_unpack_kernel(const int8_t *__restrict__ codes,
-                                                         int64_t ldq,
-                                                         const uint8_t *__restrict__ scale,
-                                                         Index ix, int64_t cols,
-                                                         T *__restrict__ out, int64_t ldo,
-                                                         int64_t padded) {
-    constexpr int P = 16 / static_cast<int>(sizeof(T));
-    typedef uint32_t Store __attribute__((ext_vector_type(4), aligned(1)));
-    const int64_t groups = (cols + kGroup - 1) / kGroup;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < ix.total;
-         i += static_cast<int64_t>(gridDim.x) * 256) {
-        int64_t r;
-        uint32_t c;
-        split<SMALL>(i, ix.cpr, r, c);
-        const int64_t col = static_cast<int64_t>(c) * P;
-        const int left = cols - col < P ? static_cast<int>(cols - col) : P;  // may be <= 0
-        const int8_t *q = codes + r * ldq + col;
-        const int e = left > 0 ? scale[r * groups + c / (kGroup / P)] : 0;
-        float v[P];
-        if (left == P) {
-            struct __attribute__((packed)) Words { uint32_t w[P / 4]; };
-            const Words t = *reinterpret_cast<const Words *>(q);
-#pragma unroll
-            for (int k = 0; k < P; ++k)
-                v[k] = code_value(static_cast<int8_t>(t.w[k / 4] >> (8 * (k % 4))), e);
-        } else {
-#pragma unroll
-            for (int k = 0; k < P; ++k) v[k] = k < left ? code_value(q[k], e) : 0.0f;
-        }
-        T *o = out + r * ldo + col;
-        if (col + P <= padded) {
-            struct alignas(16) Piece { T v[P]; } s;
-#pragma unroll
-            for (int k = 0; k < P; ++k) s.v[k] = static_cast<T>(v[k]);
-            __builtin_nontemporal_store(__builtin_bit_cast(Store, s),
-                                        reinterpret_cast<Store *>(o));
-        } else {
-#pragma unroll
-            for (int k = 0; k < P; ++k)
-                if (col + k < padded) o[k] = static_cast<T>(v[k]);
-        }
-    }
+__global__ __launch_bounds__(256) void act_unpack_kernel(UnpackArgs a, T *__restrict__ out) {
+    act_unpack<T, SMALL>(a, out, blockIdx.x, gridDim.x);
 }
 
 unsigned grid_for(int64_t work, int64_t per) {
@@ -153,7 +88,7 @@ template <typename T>
 hipError_t pack(const void *X, int64_t rows, int64_t cols, int64_t ldx, int8_t *codes,
                 int64_t ldq, uint8_t *scale, hipStream_t s) {
     const int64_t groups = (cols + kGroup - 1) / kGroup;
-    const Index ix{static_cast<uint32_t>(groups * 4), rows * groups * 4};
+    const Pieces ix{static_cast<uint32_t>(groups * 4), rows * groups * 4};
     const auto kern = ix.total < (int64_t{1} << 32) ? act_pack_kernel<T, true>
                                                     : act_pack_kernel<T, false>;
     hipLaunchKernelGGL(kern, dim3(grid_for(ix.total, 256)), dim3(256), 0, s,
@@ -164,13 +99,11 @@ hipError_t pack(const void *X, int64_t rows, int64_t cols, int64_t ldx, int8_t *
 template <typename T>
 hipError_t unpack(const int8_t *codes, int64_t ldq, const uint8_t *scale, int64_t rows,
                   int64_t cols, void *out, int64_t ldo, int64_t padded, hipStream_t s) {
-    constexpr int64_t P = 16 / sizeof(T);
-    const int64_t cpr = (padded + P - 1) / P;
-    const Index ix{static_cast<uint32_t>(cpr), rows * cpr};
-    const auto kern = ix.total < (int64_t{1} << 32) ? act_unpack_kernel<T, true>
-                                                    : act_unpack_kernel<T, false>;
-    hipLaunchKernelGGL(kern, dim3(grid_for(ix.total, 256)), dim3(256), 0, s, codes, ldq, scale,
-                       ix, cols, static_cast<T *>(out), ldo, padded);
+    const UnpackArgs a = unpack_args<T>(codes, ldq, scale, rows, cols, ldo, padded);
+    const auto kern = a.ix.total < (int64_t{1} << 32) ? act_unpack_kernel<T, true>
+                                                      : act_unpack_kernel<T, false>;
+    hipLaunchKernelGGL(kern, dim3(grid_for(a.ix.total, 256)), dim3(256), 0, s, a,
+                       static_cast<T *>(out));
     return hipGetLastError();
 }
 

@@ -9,6 +9,7 @@
 // layer's type, because both of its products read it through the matrix cores.
 #include <hip/hip_runtime.h>
 
+#include "checkpoint_device.h"
 #include "decode_device.h"
 #include "gemm_device.h"
 #include "linear_device.h"
@@ -829,12 +830,11 @@ __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__
 
 // sum[c] = part[0][c] + part[1][c] + ...: each of four waves adds a run of slabs in order, then
 // the four sums in order; 64 columns per workgroup.
-__global__ __launch_bounds__(256) void slab_sum_kernel(const float *__restrict__ part,
-                                                       int64_t slabs, int64_t M,
-                                                       float *__restrict__ sum) {
+__device__ __forceinline__ void slab_sum(const float *__restrict__ part, int64_t slabs, int64_t M,
+                                         float *__restrict__ sum, uint32_t block) {
     __shared__ float red[4][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+    const int64_t c = static_cast<int64_t>(block) * 64 + lane;
     const int64_t i0 = w * slabs / 4, i1 = (w + 1) * slabs / 4;
     float s = 0.0f;
     if (c < M) {
@@ -844,6 +844,26 @@ __global__ __launch_bounds__(256) void slab_sum_kernel(const float *__restrict__
     red[w][lane] = s;
     __syncthreads();
     if (w == 0 && c < M) sum[c] = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
+}
+
+__global__ __launch_bounds__(256) void slab_sum_kernel(const float *__restrict__ part,
+                                                       int64_t slabs, int64_t M,
+                                                       float *__restrict__ sum) {
+    slab_sum(part, slabs, M, sum, blockIdx.x);
+}
+
+// slab_sum and act_unpack, which know nothing of each other, side by side in one launch: the
+// first `sums` workgroups take the sums.
+template <typename T, bool SMALL>
+__global__ __launch_bounds__(256) void slab_sum_unpack_kernel(const float *__restrict__ part,
+                                                              int64_t slabs, int64_t M,
+                                                              float *__restrict__ sum,
+                                                              uint32_t sums, UnpackArgs a,
+                                                              T *__restrict__ out) {
+    if (blockIdx.x < sums)
+        slab_sum(part, slabs, M, sum, blockIdx.x);
+    else
+        act_unpack<T, SMALL>(a, out, blockIdx.x - sums, gridDim.x - sums);
 }
 
 // ---------------------------------------------------------------- host side
@@ -1140,11 +1160,29 @@ hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStre
                             dim3(256), args, 0, s);
         if (e != hipSuccess) return e;
     }
-    if (c.dbias && w.M > 0) {
-        hipLaunchKernelGGL(slab_sum_kernel, dim3(static_cast<unsigned>((w.M + 63) / 64)),
-                           dim3(256), 0, s, reinterpret_cast<const float *>(ws + lay.part),
+    // x's checkpoint is unpacked for dw; the bias' sums go along in the same launch
+    const bool unpack = c.dw && c.B > 0 && w.M > 0 && w.N > 0;
+    const bool sum = c.dbias && w.M > 0;
+    const float *part = reinterpret_cast<const float *>(ws + lay.part);
+    T *X = reinterpret_cast<T *>(ws + lay.rows);
+    const uint32_t sums = static_cast<uint32_t>((w.M + 63) / 64);
+    if (unpack && sum) {
+        const UnpackArgs a =
+            unpack_args<T>(c.xq, c.ldxq, c.xe, c.B, w.N, lay.ldn, lay.ldn);
+        const auto kern = a.ix.total < (int64_t{1} << 32) ? slab_sum_unpack_kernel<T, true>
+                                                          : slab_sum_unpack_kernel<T, false>;
+        hipLaunchKernelGGL(kern, dim3(sums + grid_for(a.ix.total, 256, 1 << 20)), dim3(256), 0,
+                           s, part, slabs, w.M, c.dbias, sums, a, X);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    } else if (sum) {
+        hipLaunchKernelGGL(slab_sum_kernel, dim3(sums), dim3(256), 0, s, part,
                            c.B > 0 ? slabs : 0, w.M, c.dbias);
         e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    } else if (unpack) {
+        e = launch_act_unpack(c.xq, c.ldxq, c.xe, c.B, w.N, dtype_of<T>(), X, lay.ldn, lay.ldn,
+                              s);
         if (e != hipSuccess) return e;
     }
     if (c.dx && c.B > 0 && w.N > 0) {
@@ -1160,12 +1198,6 @@ hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStre
         if (e != hipSuccess) return e;
     }
     if (c.dw && w.M > 0 && w.N > 0) {
-        T *X = reinterpret_cast<T *>(ws + lay.rows);
-        if (c.B > 0) {
-            e = launch_act_unpack(c.xq, c.ldxq, c.xe, c.B, w.N, dtype_of<T>(), X, lay.ldn,
-                                  lay.ldn, s);
-            if (e != hipSuccess) return e;
-        }
         const PlainEpilogue<T> epi{static_cast<T *>(c.dw), c.lddw, w.M, w.N,
                                    four_aligned(static_cast<T *>(c.dw), c.lddw)};
         const Operand<T> A{S, lay.ldm, lay.ldm, c.B};
