@@ -394,12 +394,14 @@ int tcq_act_unpack(const int8_t *codes, int64_t ldq, const uint8_t *scale, int64
  * 8-bit checkpoints of z and x:
  *     g[b][r]  = dy[b][r] act'(z[b][r])        z, x: the values the checkpoints stand for
  *     dbias[r] = sum_b g[b][r]
- *     s[b][r]  = g[b][r] row_scale[r]          rounded to the layer's type
+ *     s[b][r]  = g[b][r] row_scale[r]
  *     dx[b][c] = sum_r s[b][r] W_hat[r][c]
  *     dw[r][c] = sum_b s[b][r] x[b][c]         the gradient of W_hat (straight through to W)
  * relu's g is dy where z > 0, 0 where z <= 0 (whatever dy holds) and NaN where z is NaN.
  * The residual's gradient is dy itself.  Sums are fp32 in a fixed order; outputs of the
- * layer's type are rounded once.
+ * layer's type are rounded once.  g and s are fp32; a 16-bit type's products read s as two
+ * numbers of the type, within 2^-16 (bf16) or 2^-22 (fp16) of its value, in fp16 not below
+ * 2^-34 of the largest |row_scale| (of 1 without).
  *   dy, B, lddy : device, B x M of type dtype
  *   z_codes, ldz, z_scale : device checkpoint of z (B x M); not read with TCQ_ACT_NONE
  *   x_codes, ldx, x_scale : device checkpoint of x (B x N); read for dw only

@@ -27,6 +27,10 @@
 //
 // The matrix instruction takes B(j, .) as its first operand, so a lane ends up with four
 // consecutive j of one row i: outputs leave in 8- or 16-byte pieces.
+//
+// A 16-bit operand A can be held in two terms, A = high + 2^-kLowShift low, each stored like A
+// (TERMS = 2).  The steps then run over k twice, first with the low term, and between the two
+// the sums are scaled by 2^-kLowShift, which is exact: no second set of sums is needed.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -53,7 +57,13 @@ struct Operand {
     int64_t ld;
     int64_t rows;
     int64_t k;
+    int64_t low = 0;  // bytes from p to the low term, where there are two
 };
+
+// An fp16 remainder may fall below the type's smallest number, so it is held 2^11 times as
+// large (at most 16 of a number below 65504, 2^15 then); bf16 has the exponents of fp32.
+template <typename T>
+constexpr int kLowShift = __is_same(T, _Float16) ? 11 : 0;
 
 constexpr int kStepBytes = 128;  // bytes of k per row and step
 constexpr int kPastEnd = -1;     // a step that reads as zeros
@@ -104,8 +114,9 @@ __device__ __forceinline__ int kmajor_key(int kk) {
     return kk >> 2 & 3;
 }
 
-// The per-thread part of an operand's tile loads: TR rows by one step, NT threads.
-template <typename T, bool KM, int TR, int NT>
+// The per-thread part of an operand's tile loads: TR rows by one step, NT threads.  TERMS = 2:
+// steps from `half` on are those of the high term (an operand of one term has them twice).
+template <typename T, bool KM, int TR, int NT, int TERMS = 1>
 struct TileLoader {
     static constexpr int kChunks = TR * (kStepBytes / 16);  // 16-byte chunks of a tile
     static constexpr int kLoads = kChunks / NT;
@@ -119,10 +130,14 @@ struct TileLoader {
     int64_t k;              // valid k
     uint32_t off[kLoads];   // byte offsets of this thread's chunks within the tile
     int kchunk;             // k-contiguous: first k of this thread's chunks within a step
+    int half;               // steps of a term
+    int64_t low;            // bytes from base to the low term's tile
 
     __device__ __forceinline__ void init(const Operand<T> &o, int64_t row0, int tid) {
         constexpr int kPer16 = 16 / static_cast<int>(sizeof(T));
         k = o.k;
+        half = static_cast<int>((k + kStep - 1) / kStep);
+        low = o.low;
         if constexpr (KM) {
             base = reinterpret_cast<const char *>(o.p + row0);
             left = ((o.k - 1) * o.ld + o.rows - row0) * static_cast<int64_t>(sizeof(T));
@@ -155,12 +170,19 @@ struct TileLoader {
 
     // Step s's tile into lds (every wave writes its own 1 KiB pieces).
     __device__ __forceinline__ void load(char *lds, int s, int tid) const {
+        const char *from = base;
+        if constexpr (TERMS == 2) {
+            if (s >= half)
+                s -= half;
+            else
+                from += low;
+        }
         const int64_t at = s == kPastEnd ? 0 : s * step_bytes;
         int64_t bytes = s == kPastEnd ? 0 : left - at;
         if (bytes > 0xFFFFFF00ll) bytes = 0xFFFFFF00ll;
         if (bytes < 0) bytes = 0;
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char *>(base + at), 0, static_cast<int>(bytes), 0x00020000);
+            const_cast<char *>(from + at), 0, static_cast<int>(bytes), 0x00020000);
         const bool in = KM || s * static_cast<int64_t>(kStep) + kchunk < k;
         const int wave0 = __builtin_amdgcn_readfirstlane(tid & ~63);
 #pragma unroll
@@ -285,7 +307,8 @@ __device__ __forceinline__ void hand_out(const f32x4 (&acc)[FI][FJ], char *piece
 // Computes the tile's sums over steps s_begin .. s_end - 1 and hands it out in pieces of
 // four: Epi::Column col(epi, j) once per lane, then epi.put(col, i, D[i][j .. j + 3]) for its
 // rows; i and j may lie past I or J.
-template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, int NB, typename Epi>
+template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, int NB, int TERMS,
+          typename Epi>
 __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> &B, int64_t i0,
                                           int64_t j0, int s_begin, int s_end,
                                           const Stages<NB> &st, const Epi &epi) {
@@ -297,8 +320,8 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wi = wave / WJ, wj = wave % WJ;
-    TileLoader<T, AKM, TI, NT> la;
-    TileLoader<T, BKM, TJ, NT> lb;
+    TileLoader<T, AKM, TI, NT, TERMS> la;
+    TileLoader<T, BKM, TJ, NT, TERMS> lb;
     la.init(A, i0, tid);
     lb.init(B, j0, tid);
     const FragReader<T, AKM, TI> ra{lane, wi * FI * 16};
@@ -339,6 +362,18 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
     constexpr int kLoadsA = decltype(la)::kLoads, kLoadsB = decltype(lb)::kLoads;
     // (a step past s_end loads nothing that is there)
     auto valid = [&](int s) { return s < s_end ? s : kPastEnd; };
+    // Two terms: the sums of the low one are scaled before the high one's first step, or at the
+    // end where this tile's steps do not reach it.
+    constexpr bool kScaled = TERMS == 2 && kLowShift<T> != 0;
+    const int scale_at = kScaled && la.half < s_end ? la.half : kPastEnd;
+    auto scale_low = [&] {
+#pragma unroll
+        for (int i = 0; i < FI; ++i)
+#pragma unroll
+            for (int j = 0; j < FJ; ++j)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][j][v] *= 1.0f / (1 << kLowShift<T>);
+    };
     if constexpr (NB == kRing) {
         // Two whole steps of a 256 x 256 tile take 128 of the 160 KiB of LDS, and with two
         // stages every load has one step to arrive.  Five pieces give A two steps: B(s + 2)
@@ -350,6 +385,8 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
             char *sa = st.p[t % 5], *sb = st.p[(t + 1) % 5];
             const char *na = st.p[(t + 2) % 5], *nb = st.p[(t + 3) % 5];
             la.load(st.p[(t + 4) % 5], valid(s + 2), tid);
+            if constexpr (kScaled)
+                if (s == scale_at) scale_low();
 #pragma unroll
             for (int ph = 0; ph + 1 < kPhases; ++ph) {
                 read_phase(sa, sb, ph + 1);
@@ -382,6 +419,8 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
         // Step s from (ta, tb); (na, nb) hold step s + 1 from the meeting on.  Steps past
         // s_end multiply zeros.  At a meeting the stages after the next one are in flight.
         auto step = [&](int s, char *ta, char *tb, const char *na, const char *nb) {
+            if constexpr (kScaled)
+                if (s == scale_at) scale_low();
 #pragma unroll
             for (int ph = 0; ph + 1 < kPhases; ++ph) {
                 read_phase(ta, tb, ph + 1);
@@ -411,6 +450,8 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
             meet<0>();  // no load into LDS outlives the tile
         }
     }
+    if constexpr (kScaled)
+        if (scale_at == kPastEnd && s_begin < la.half) scale_low();
     static_assert(WI * WJ * FJ * 1024 <= TI * kStepBytes, "the waves' pieces fit the buffer");
     hand_out(acc, st.a[0] + wave * (FJ * 1024), lane, i0 + wi * FI * 16, j0 + wj * FJ * 16, epi);
 }

@@ -4,9 +4,12 @@
 // The matrix is decoded once into the workspace, in the layer's type, and multiplied on the
 // matrix cores (gemm_device.h); for few rows it is decoded inside the product.  With the table in the layer's own type a decoded weight is
 // a table entry copied bit for bit, so every product is exact and the sums are fp32: the
-// outputs' own rounding is the only one to 16 bits in the forward pass.  The backward pass
-// rounds the incoming gradient times the activation's slope and the row scale once, to the
-// layer's type, because both of its products read it through the matrix cores.
+// outputs' own rounding is the only one to 16 bits.  The backward pass holds the incoming
+// gradient times the activation's slope and the row scale in two terms of a 16-bit type, since
+// its products read it through the matrix cores: rounded to one term, dx and dw were off by 1.4
+// times their own rounding, and in fp16 the row scale (about 1 / sqrt N) pushed small gradients
+// among the subnormals (11 % off at a gradient of 1e-5).  It costs a second pass over k
+// (4096 x 4096 x 4096: 220-257 us a product, 113-119 with one term).
 #include <hip/hip_runtime.h>
 
 #include "checkpoint_device.h"
@@ -298,17 +301,26 @@ struct LayerEpilogue {
     }
 };
 
+// The sums times 2^*exponent (NULL: 1), rounded once.
 template <typename T>
 struct PlainEpilogue {
     T *y;
     int64_t ldy, I, J;
     int vec_y;
+    const int *exponent;
     struct Column {
         int64_t j;
-        __device__ __forceinline__ Column(const PlainEpilogue &, int64_t j_) : j(j_) {}
+        int e;
+        __device__ __forceinline__ Column(const PlainEpilogue &p, int64_t j_)
+            : j(j_), e(p.exponent ? *p.exponent : 0) {}
     };
     __device__ __forceinline__ void put(const Column &c, int64_t i, f32x4 s) const {
-        if (i < I && c.j < J) store4(y + i * ldy + c.j, c.j, J, vec_y, s);
+        if (i >= I || c.j >= J) return;
+        if constexpr (gemm::kLowShift<T> != 0) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) s[v] = __builtin_amdgcn_ldexpf(s[v], c.e);
+        }
+        store4(y + i * ldy + c.j, c.j, J, vec_y, s);
     }
 };
 
@@ -327,7 +339,8 @@ struct PartEpilogue {
 
 // ---------------------------------------------------------------- products
 
-template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, int NB, typename Epi>
+template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, int NB, int TERMS,
+          typename Epi>
 __global__ __launch_bounds__(WI *WJ * 64) void gemm_kernel(Operand<T> A, Operand<T> B,
                                                            int steps, int steps_per_split,
                                                            Epi epi, uint32_t ni, uint32_t nj) {
@@ -371,7 +384,7 @@ __global__ __launch_bounds__(WI *WJ * 64) void gemm_kernel(Operand<T> A, Operand
     if constexpr (sizeof(T) == 4)
         gemm::gemm_tile_f32<AKM, BKM, TI, TJ, WI, WJ>(A, B, i0, j0, s0, s1, st, epi);
     else
-        gemm::gemm_tile<T, AKM, BKM, TI, TJ, WI, WJ, NB>(A, B, i0, j0, s0, s1, st, epi);
+        gemm::gemm_tile<T, AKM, BKM, TI, TJ, WI, WJ, NB, TERMS>(A, B, i0, j0, s0, s1, st, epi);
 }
 
 // The splits' shares added in order, four values per thread, and handed to the epilogue.
@@ -389,18 +402,19 @@ __global__ __launch_bounds__(256) void split_sum_kernel(const float *__restrict_
     epi.put(col, i, s);
 }
 
-template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, int NB, typename Epi>
+template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, int NB, int TERMS,
+          typename Epi>
 hipError_t launch_tiles(const Operand<T> &A, const Operand<T> &B, const GemmPlan &pl,
                         const Epi &epi, hipStream_t s) {
     const uint32_t ni = static_cast<uint32_t>((A.rows + TI - 1) / TI);
     const uint32_t nj = static_cast<uint32_t>((B.rows + TJ - 1) / TJ);
-    hipLaunchKernelGGL((gemm_kernel<T, AKM, BKM, TI, TJ, WI, WJ, NB, Epi>),
+    hipLaunchKernelGGL((gemm_kernel<T, AKM, BKM, TI, TJ, WI, WJ, NB, TERMS, Epi>),
                        dim3(ni * nj, static_cast<unsigned>(pl.splits)), dim3(WI * WJ * 64), 0, s,
                        A, B, pl.steps, pl.steps_per_split, epi, ni, nj);
     return hipGetLastError();
 }
 
-template <typename T, bool AKM, bool BKM, typename Epi>
+template <typename T, bool AKM, bool BKM, int TERMS, typename Epi>
 hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan &pl,
                        const Epi &epi, char *part, hipStream_t s) {
     if (A.rows <= 0 || B.rows <= 0) return hipSuccess;
@@ -409,8 +423,9 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
         // (256 x 256 tiles are not split)
         const hipError_t e =
             pl.tile == kTile128
-                ? launch_tiles<T, AKM, BKM, 128, 128, 2, 2, sizeof(T) == 2 ? 4 : 2>(A, B, pl, pe, s)
-                : launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 2>(A, B, pl, pe, s);
+                ? launch_tiles<T, AKM, BKM, 128, 128, 2, 2, sizeof(T) == 2 ? 4 : 2, TERMS>(
+                      A, B, pl, pe, s)
+                : launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 2, TERMS>(A, B, pl, pe, s);
         if (e != hipSuccess) return e;
         const int64_t quads = A.rows * (pl.part_ld / 4);
         hipLaunchKernelGGL(split_sum_kernel<Epi>, dim3(static_cast<unsigned>((quads + 255) / 256)),
@@ -419,11 +434,13 @@ hipError_t launch_gemm(const Operand<T> &A, const Operand<T> &B, const GemmPlan 
     }
     if constexpr (sizeof(T) == 2) {
         if (pl.tile == kTile256)
-            return launch_tiles<T, AKM, BKM, 256, 256, 2, 4, gemm::kRing>(A, B, pl, epi, s);
+            return launch_tiles<T, AKM, BKM, 256, 256, 2, 4, gemm::kRing, TERMS>(A, B, pl, epi,
+                                                                                 s);
     }
     if (pl.tile == kTile128)
-        return launch_tiles<T, AKM, BKM, 128, 128, 2, 2, sizeof(T) == 2 ? 4 : 2>(A, B, pl, epi, s);
-    return launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 2>(A, B, pl, epi, s);
+        return launch_tiles<T, AKM, BKM, 128, 128, 2, 2, sizeof(T) == 2 ? 4 : 2, TERMS>(A, B, pl,
+                                                                                        epi, s);
+    return launch_tiles<T, AKM, BKM, 64, 128, 1, 4, 2, TERMS>(A, B, pl, epi, s);
 }
 
 // ---------------------------------------------------------------- few rows of x
@@ -763,15 +780,61 @@ struct SlopeArgs {
     int64_t ld;              // of the result: a multiple of 8, columns past M are zeros
     float *part;             // [slabs][M] sums of dy act'(z) over a slab's rows, or NULL
     int64_t rows_per_slab;
+    // fp16 in two terms: the largest |scale| is among tops[0 .. ntops - 1] (bit patterns; 1
+    // without), and the power of two that out is to be multiplied by goes to *exponent
+    const uint32_t *tops;
+    int ntops;
+    int *exponent;
 };
 
-// out = dy act'(z) scale rounded to T; part = sums over a slab's rows of dy act'(z), in fp32
-// (each of the four waves adds every fourth row, then the four sums in order).  Eight
-// columns per thread: memory-bound but for gelu.
-template <typename T, int ACT>
-__global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__ out) {
+// tops[block] = largest finite |scale[i]| of the block's share, as a bit pattern.
+constexpr int kTops = 64;
+__global__ __launch_bounds__(256) void scale_top_kernel(const float *__restrict__ scale,
+                                                        int64_t M, uint32_t *__restrict__ tops) {
+    __shared__ uint32_t red[4];
+    uint32_t top = 0;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < M;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        const uint32_t m = __float_as_uint(scale[i]) & 0x7FFFFFFFu;
+        if (m < 0x7F800000u && m > top) top = m;
+    }
+    for (int d = 32; d; d >>= 1) {
+        const uint32_t o = __shfl_xor(top, d);
+        top = top > o ? top : o;
+    }
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 4; ++w) top = top > red[w] ? top : red[w];
+        tops[blockIdx.x] = top;
+    }
+}
+
+// out = dy act'(z) scale in T, or in two terms of T; part = sums over a slab's rows of
+// dy act'(z), in fp32 (each of the four waves adds every fourth row, then the four sums in
+// order).  Eight columns per thread: memory-bound but for gelu.
+//   Two terms hold a number x as high = T(x), low = T((x - high) 2^kLowShift): half(T)^2 of x.
+// fp16 takes x = dy act'(z) scale 2^-e with |scale 2^-e| in [1/4, 1/2) for the largest |scale|,
+// so |x| stays below 1.13 / 2 of fp16's largest number, and what low cannot hold is below 2^-36.
+template <typename T, int ACT, int TERMS>
+__global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__ out,
+                                                    T *__restrict__ out_low) {
+    constexpr int kLow = gemm::kLowShift<T>;
     __shared__ float red[4][8][65];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    int exponent = 0;
+    if constexpr (TERMS == 2 && kLow != 0) {
+        uint32_t top = a.tops ? (lane < a.ntops ? a.tops[lane] : 0u) : __float_as_uint(1.0f);
+        for (int d = 32; d; d >>= 1) {
+            const uint32_t o = __shfl_xor(top, d);
+            top = top > o ? top : o;
+        }
+        // top below 2^(its exponent field - 126) (subnormals: the smallest normal exponent's)
+        const int field = static_cast<int>(top >> 23);
+        exponent = (field > 1 ? field : 1) - 125;
+        if (a.exponent && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+            *a.exponent = exponent;
+    }
     const int64_t c0 = (static_cast<int64_t>(blockIdx.x) * 64 + lane) * 8;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.rows_per_slab;
     const int64_t r1 = r0 + a.rows_per_slab < a.B ? r0 + a.rows_per_slab : a.B;
@@ -783,6 +846,8 @@ __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__
     for (int e = 0; e < 8; ++e) {
         sum[e] = 0.0f;
         sc[e] = a.scale && e < left ? a.scale[c0 + e] : 1.0f;
+        if constexpr (TERMS == 2 && kLow != 0)
+            sc[e] = __builtin_amdgcn_ldexpf(sc[e], -exponent);
     }
     if (c0 < a.ld) {
 #pragma unroll 2
@@ -803,16 +868,27 @@ __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__
                 }
             }
             if constexpr (ACT != TCQ_ACT_NONE) ez = left > 0 ? a.ze[r * groups + c0 / 32] : 0;
-            struct alignas(8 * sizeof(T)) Eight { T v[8]; } o;
+            struct alignas(8 * sizeof(T)) Eight { T v[8]; } o, low;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float g = static_cast<float>(d.v[e]);
                 if constexpr (ACT != TCQ_ACT_NONE)
                     if (e < left) g = act_grad<ACT>(g, code_value(z.v[e], ez));
                 sum[e] += g;
-                o.v[e] = static_cast<T>(g * sc[e]);
+                const float x = g * sc[e];
+                o.v[e] = static_cast<T>(x);
+                if constexpr (TERMS == 2) {
+                    const float high = static_cast<float>(o.v[e]);
+                    float rest = x - high;
+                    if constexpr (kLow != 0) rest *= 1 << kLow;
+                    // an infinity or a NaN is the high term's alone
+                    low.v[e] = static_cast<T>(__builtin_fabsf(high) < __builtin_inff() ? rest : 0.0f);
+                }
             }
-            if (out) *reinterpret_cast<Eight *>(out + r * a.ld + c0) = o;
+            if (out) {
+                *reinterpret_cast<Eight *>(out + r * a.ld + c0) = o;
+                if constexpr (TERMS == 2) *reinterpret_cast<Eight *>(out_low + r * a.ld + c0) = low;
+            }
         }
     }
     if (!a.part) return;
@@ -898,14 +974,22 @@ int64_t slope_slabs(int64_t B, int64_t M) {
     return s < 1 ? 1 : s;
 }
 
-template <typename T>
+template <typename T, int TERMS>
 const void *slope_kernel_of(int act) {
     switch (act) {
-        case TCQ_ACT_RELU: return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_RELU>);
-        case TCQ_ACT_SILU: return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_SILU>);
-        case TCQ_ACT_GELU: return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_GELU>);
-        default: return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_NONE>);
+        case TCQ_ACT_RELU:
+            return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_RELU, TERMS>);
+        case TCQ_ACT_SILU:
+            return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_SILU, TERMS>);
+        case TCQ_ACT_GELU:
+            return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_GELU, TERMS>);
+        default: return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_NONE, TERMS>);
     }
+}
+
+// Terms of a 16-bit type that the scaled gradient is held in: one where it is dy itself or zero.
+int grad_terms(const LinearGrad &c) {
+    return c.row_scale || c.act == TCQ_ACT_SILU || c.act == TCQ_ACT_GELU ? 2 : 1;
 }
 
 // Compute units of the current device (asked on every call: devices of one process, such
@@ -1131,14 +1215,20 @@ hipError_t forward(const CodedMatrix &w, const LinearCall &c, char *ws, hipStrea
     const LayerEpilogue<T> epi = layer_epilogue<T>(w, c);
     const Operand<T> A{x, ldx, c.B, K};
     const Operand<T> Bm{W, lay.ldn, w.M, K};
-    return launch_gemm<T, false, false>(A, Bm, lay.forward, epi, ws + lay.sums, s);
+    return launch_gemm<T, false, false, 1>(A, Bm, lay.forward, epi, ws + lay.sums, s);
 }
 
-template <typename T>
+template <typename T, int TERMS>
 hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStream_t s) {
-    const LinearLayout lay = linear_grad_layout(sizeof(T), c.B, w.M, w.N, c.dx, c.dw, c.dbias);
+    const LinearLayout lay =
+        linear_grad_layout(sizeof(T), c.B, w.M, w.N, c.dx, c.dw, c.dbias, TERMS);
     hipError_t e;
     T *S = reinterpret_cast<T *>(ws + lay.grad);
+    T *low = reinterpret_cast<T *>(ws + lay.low);
+    // the power of two that fp16 sums are to be multiplied by
+    uint32_t *tops = reinterpret_cast<uint32_t *>(ws + lay.tops);
+    int *exponent =
+        TERMS == 2 && gemm::kLowShift<T> != 0 ? reinterpret_cast<int *>(tops + kTops) : nullptr;
     const int64_t slabs = slope_slabs(c.B, w.M);
     if (c.B > 0 && w.M > 0) {
         SlopeArgs a{};
@@ -1154,8 +1244,17 @@ hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStre
         a.part = c.dbias ? reinterpret_cast<float *>(ws + lay.part) : nullptr;
         a.rows_per_slab = (c.B + slabs - 1) / slabs;
         T *out = c.dx || c.dw ? S : nullptr;
-        void *args[] = {&a, &out};
-        e = hipLaunchKernel(slope_kernel_of<T>(c.act),
+        a.exponent = out ? exponent : nullptr;
+        if (a.exponent && c.row_scale) {
+            a.tops = tops;
+            a.ntops = static_cast<int>(grid_for(w.M, 2048, kTops));
+            hipLaunchKernelGGL(scale_top_kernel, dim3(static_cast<unsigned>(a.ntops)), dim3(256),
+                               0, s, c.row_scale, w.M, tops);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        void *args[] = {&a, &out, &low};
+        e = hipLaunchKernel(slope_kernel_of<T, TERMS>(c.act),
                             dim3(static_cast<unsigned>((lay.ldm / 8 + 63) / 64),
                                  static_cast<unsigned>(slabs)),
                             dim3(256), args, 0, s);
@@ -1186,27 +1285,38 @@ hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStre
                               s);
         if (e != hipSuccess) return e;
     }
+    const int64_t to_low = static_cast<int64_t>(lay.low) - static_cast<int64_t>(lay.grad);
     if (c.dx && c.B > 0 && w.N > 0) {
         T *W = reinterpret_cast<T *>(ws + lay.matrix);
         e = decode_matrix(w, W, lay.ldn, s);
         if (e != hipSuccess) return e;
         const PlainEpilogue<T> epi{static_cast<T *>(c.dx), c.lddx, c.B, w.N,
-                                   four_aligned(static_cast<T *>(c.dx), c.lddx)};
-        const Operand<T> A{S, lay.ldm, c.B, w.M > 0 ? lay.ldm : 0};
+                                   four_aligned(static_cast<T *>(c.dx), c.lddx),
+                                   c.B > 0 && w.M > 0 ? exponent : nullptr};
+        const Operand<T> A{S, lay.ldm, c.B, w.M > 0 ? lay.ldm : 0, to_low};
         // (columns past N are zeros and not stored; rows past M read as zeros)
         const Operand<T> Bm{W, lay.ldn, lay.ldn, w.M};
-        e = launch_gemm<T, false, true>(A, Bm, lay.dx, epi, ws + lay.sums, s);
+        e = launch_gemm<T, false, true, TERMS>(A, Bm, lay.dx, epi, ws + lay.sums, s);
         if (e != hipSuccess) return e;
     }
     if (c.dw && w.M > 0 && w.N > 0) {
         const PlainEpilogue<T> epi{static_cast<T *>(c.dw), c.lddw, w.M, w.N,
-                                   four_aligned(static_cast<T *>(c.dw), c.lddw)};
-        const Operand<T> A{S, lay.ldm, lay.ldm, c.B};
+                                   four_aligned(static_cast<T *>(c.dw), c.lddw),
+                                   c.B > 0 ? exponent : nullptr};
+        const Operand<T> A{S, lay.ldm, lay.ldm, c.B, to_low};
         const Operand<T> Bm{X, lay.ldn, lay.ldn, c.B};
-        e = launch_gemm<T, true, true>(A, Bm, lay.dw, epi, ws + lay.sums, s);
+        e = launch_gemm<T, true, true, TERMS>(A, Bm, lay.dw, epi, ws + lay.sums, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+template <typename T>
+hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStream_t s) {
+    if constexpr (sizeof(T) == 2) {
+        if (grad_terms(c) == 2) return backward<T, 2>(w, c, ws, s);
+    }
+    return backward<T, 1>(w, c, ws, s);
 }
 
 size_t pad8(int64_t n) { return static_cast<size_t>((n + 7) / 8 * 8); }
@@ -1250,7 +1360,7 @@ size_t linear_small_bytes(size_t size, int64_t N, int bt) {
 // where two share a compute unit (1000 x 2048 x 2048 as 64 x 128 and 128 x 128, both split: 39
 // and 34 us per call in bf16, 82 and 75 in fp32, where 256 workgroups take 86; 200 x 14336 x
 // 4096 in fp32: 330 and 268; 333 x 2048 x 2048: 30 and 32 in bf16, 51 and 51 in fp32).
-GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K) {
+GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K, int terms) {
     constexpr int64_t kCus = 256;
     const auto tiles = [&](int64_t ti, int64_t tj) {
         return ((I + ti - 1) / ti) * ((J + tj - 1) / tj);
@@ -1258,7 +1368,7 @@ GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K) {
     const auto rounds = [&](int64_t n) { return static_cast<double>((n + kCus - 1) / kCus); };
     GemmPlan p{};
     const int64_t step = gemm::kStepBytes / static_cast<int64_t>(size);
-    p.steps = static_cast<int>((K + step - 1) / step);
+    p.steps = static_cast<int>((K + step - 1) / step) * terms;
     p.part_ld = (J + 3) / 4 * 4;
     // n tiles with k split into about `most` workgroups
     const auto split = [&](int tile, int64_t n, int64_t most) {
@@ -1317,13 +1427,13 @@ LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N) {
     l.matrix = 0;
     l.rows = align_up(static_cast<size_t>(M) * l.ldn * size, 256);
     l.sums = l.rows + align_up(static_cast<size_t>(B) * l.ldn * size, 256);
-    l.forward = gemm_plan(size, B, M, l.ldn);
+    l.forward = gemm_plan(size, B, M, l.ldn, 1);
     l.bytes = l.sums + align_up(l.forward.part_bytes, 256);
     return l;
 }
 
 LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bool dx, bool dw,
-                                bool dbias) {
+                                bool dbias, int terms) {
     LinearLayout l{};
     l.ldn = static_cast<int64_t>(pad8(N));
     l.ldm = static_cast<int64_t>(pad8(M));
@@ -1332,15 +1442,27 @@ LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bo
     if (dx) off += align_up(static_cast<size_t>(M) * l.ldn * size, 256);
     l.grad = off;
     if (dx || dw) off += align_up(static_cast<size_t>(B) * l.ldm * size, 256);
+    // (the query does not know whether a call needs the second term)
+    l.low = off;
+    if ((dx || dw) && size == 2) off += align_up(static_cast<size_t>(B) * l.ldm * size, 256);
+    l.tops = off;
+    if ((dx || dw) && size == 2) off += align_up((kTops + 1) * sizeof(uint32_t), 256);
     l.rows = off;
     if (dw) off += align_up(static_cast<size_t>(B) * l.ldn * size, 256);
     l.part = off;
     if (dbias) off += align_up(static_cast<size_t>(slope_slabs(B, M)) * M * sizeof(float), 256);
     l.sums = off;  // (the two products run one after the other)
-    l.dx = gemm_plan(size, B, l.ldn, M);
-    l.dw = gemm_plan(size, l.ldm, l.ldn, B);
-    size_t sums = dx ? l.dx.part_bytes : 0;
-    if (dw && l.dw.part_bytes > sums) sums = l.dw.part_bytes;
+    size_t sums = 0;
+    for (int t = 1; t <= (size == 2 ? 2 : 1); ++t) {
+        const GemmPlan gx = gemm_plan(size, B, l.ldn, M, t);
+        const GemmPlan gw = gemm_plan(size, l.ldm, l.ldn, B, t);
+        if (dx && gx.part_bytes > sums) sums = gx.part_bytes;
+        if (dw && gw.part_bytes > sums) sums = gw.part_bytes;
+        if (t == terms) {
+            l.dx = gx;
+            l.dw = gw;
+        }
+    }
     off += align_up(sums, 256);
     l.bytes = off;
     return l;

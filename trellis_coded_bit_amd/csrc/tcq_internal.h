@@ -142,12 +142,12 @@ struct GemmPlan {
     int64_t part_ld;
     size_t part_bytes;
 };
-GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K);
+GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K, int terms);
 // Workspace of a call: byte offsets of the decoded matrix (M x ldn), the staged or unpacked
-// input rows (B x ldn), the scaled gradient (B x ldm), the bias gradient's partial sums and
-// the products' shares.
+// input rows (B x ldn), the scaled gradient's terms (B x ldm each) and the row scale's
+// largest value, the bias gradient's partial sums and the products' shares.
 struct LinearLayout {
-    size_t matrix, rows, grad, part, sums, bytes;
+    size_t matrix, rows, grad, low, tops, part, sums, bytes;
     int64_t ldn, ldm;
     GemmPlan forward, dx, dw;
 };
@@ -157,7 +157,7 @@ int linear_small(size_t size, int64_t B, int64_t N, int L, int k, int V, int T);
 size_t linear_small_bytes(size_t size, int64_t N, int bt);
 LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N);
 LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bool dx, bool dw,
-                                bool dbias);
+                                bool dbias, int terms);
 hipError_t launch_linear(const CodedMatrix &w, const LinearCall &c, char *ws, hipStream_t s);
 hipError_t launch_linear_grad(const CodedMatrix &w, const LinearGrad &c, char *ws,
                               hipStream_t s);

@@ -220,7 +220,7 @@ extern "C" int tcq_decode_linear_backward_workspace_bytes(int dtype, int64_t B, 
         set_error("%s: bytes is NULL", fn);
         return TCQ_EINVAL;
     }
-    *bytes = linear_grad_layout(size_of(dtype), B, M, N, dx != 0, dw != 0, dbias != 0).bytes;
+    *bytes = linear_grad_layout(size_of(dtype), B, M, N, dx != 0, dw != 0, dbias != 0, 1).bytes;
     return TCQ_OK;
 }
 
@@ -264,7 +264,8 @@ extern "C" int tcq_decode_linear_backward(
     }
     rc = check_workspace(
         fn, workspace, workspace_bytes,
-        linear_grad_layout(size, B, M, N, dx != nullptr, dw != nullptr, dbias != nullptr).bytes);
+        linear_grad_layout(size, B, M, N, dx != nullptr, dw != nullptr, dbias != nullptr, 1)
+            .bytes);
     if (rc != TCQ_OK) return rc;
     const CodedMatrix w{bitstream, start_state, codebook, M, N, L, k, V, T};
     const LinearGrad c{dtype, act, dy, B, lddy, row_scale, z_codes, ldz, z_scale, x_codes, ldx,
