@@ -348,9 +348,10 @@ typedef enum {
  *                tcq_act_pack and tcq_decode_linear_backward take)
  *   workspace  : >= what tcq_decode_linear_workspace_bytes reports
  * Outputs other than y == residual must not overlap inputs or one another.  Products of
- * 16-bit inputs are exact and sums fp32; fp32 products of large batches are taken to 2^-22
- * (as six products of bf16 terms; numbers below 2^-109 to 2^-133).  z is not rounded before
- * the activation; each output is rounded once.  Repeated calls give identical results.
+ * 16-bit inputs are exact and sums fp32.  fp32 products are fp32 arithmetic for B <= 128 with
+ * T a multiple of 32, kV <= 4 and V != 3; elsewhere each is the sum of six exact products of
+ * bf16 terms, less than 2^-22 of it left out (numbers below 2^-109: to 2^-133).  z is not rounded
+ * before the activation; each output is rounded once.  Repeated calls give identical results.
  * N == 0 gives z = bias; M == 0 or B == 0 is a no-op.
  * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED, TCQ_EWORKSPACE, TCQ_EHIP.
  */
@@ -401,7 +402,8 @@ int tcq_act_unpack(const int8_t *codes, int64_t ldq, const uint8_t *scale, int64
  * The residual's gradient is dy itself.  Sums are fp32 in a fixed order; outputs of the
  * layer's type are rounded once.  g and s are fp32; a 16-bit type's products read s as two
  * numbers of the type, within 2^-16 (bf16) or 2^-22 (fp16) of its value, in fp16 not below
- * 2^-34 of the largest |row_scale| (of 1 without).
+ * 2^-34 of the largest |row_scale| (of 1 without).  fp32 products are those of bf16 terms that
+ * tcq_decode_linear names, at every B.
  *   dy, B, lddy : device, B x M of type dtype
  *   z_codes, ldz, z_scale : device checkpoint of z (B x M); not read with TCQ_ACT_NONE
  *   x_codes, ldx, x_scale : device checkpoint of x (B x N); read for dw only

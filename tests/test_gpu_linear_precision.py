@@ -149,3 +149,119 @@ def test_gradients_of_odd_row_scales():
         dx, dw, _ = w.backward(dy, row_scale=small, x=xp)
         assert bool((dx.double().abs() <= 2.0 ** -120).all())
         assert bool((dw.double().abs() <= 2.0 ** -120).all())
+
+
+# M, N, B whose fp32 products take 64 x 128 tiles, 128 x 128 ones, and both with k split; a
+# generic decode before them
+F32_SIZES = [(16, 2, 1, 256, 130, 512, 300), (16, 2, 1, 256, 2047, 2048, 1001),
+             (16, 2, 1, 256, 4096, 1024, 1100), (8, 1, 1, 20, 300, 500, 140)]
+
+
+def _f32_table(w, values):
+    """The layer with a table of its own and its float64 matrix."""
+    w.table = values.to(F32).contiguous()
+    M, N, L, k, V, T = w.shape
+    w.W = api.decode(w.bits, w.s0, w.table, M, N, L, k, V, T).double()
+    return w
+
+
+@pytest.mark.parametrize("L,k,V,T,M,N,B", F32_SIZES)
+def test_f32_single_products(L, k, V, T, M, N, B):
+    """One product per output, of numbers whose significands are full of ones or random: left
+    out is less than (1 + 2^-9) 2^-23 of it, and of its three orders of partial sums (2^-13,
+    2^-6 and 1 of it) each may lose a whole unit of 2^-23."""
+    lim = 2.0 ** -23 * (2 + 2.0 ** -9 + 2.0 ** -6 + 2.0 ** -13)
+    rng = np.random.default_rng(M)
+    w = Coded(M + B, M, N, L, k, V, T, F32, False)
+
+    def ones(*size):
+        # 1.0000000 1111111 11111111 in binary and neighbours, random ones among them
+        u = np.where(rng.random(size) < 0.5, 0x3F80FFFF - rng.integers(0, 3, size=size),
+                     0x3F800000 + rng.integers(0, 1 << 23, size=size))
+        return torch.from_numpy(u.astype(np.int32)).cuda().view(F32)
+    w = _f32_table(w, ones(1 << L, V))
+    x = torch.zeros(B, N, device="cuda")
+    at = torch.from_numpy(rng.integers(0, N, B)).cuda()
+    x[torch.arange(B, device="cuda"), at] = ones(B)
+    want = x.double() @ w.W.t()
+    y = float(((w.linear(x).double() - want) / want).abs().max())
+    dy = torch.zeros(B, M, device="cuda")
+    at = torch.from_numpy(rng.integers(0, M, B)).cuda()
+    dy[torch.arange(B, device="cuda"), at] = ones(B)
+    want = dy.double() @ w.W
+    dx = float(((w.backward(dy, dbias=False)[0].double() - want) / want).abs().max())
+    _say(f"f32 single products M={M} N={N} B={B}: in units of 2^-23 {y * 2 ** 23:.3g} (y), "
+         f"{dx * 2 ** 23:.3g} (dx), limit {lim * 2 ** 23:.3g}")
+    assert max(y, dx) <= lim
+
+
+@pytest.mark.parametrize("L,k,V,T,M,N,B", F32_SIZES)
+def test_f32_keeps_all_bits(L, k, V, T, M, N, B):
+    """Integers of 20 bits on either side of each product, three terms of 2 more bits to a
+    sum: every product and sum is an fp32 number, so every output must be exact."""
+    rng = np.random.default_rng(N)
+
+    def sparse(rows, cols, values):
+        t = torch.zeros(rows, cols, device="cuda")
+        at = torch.from_numpy(rng.integers(0, cols, (rows, 3))).cuda()
+        return t.scatter_(1, at, torch.from_numpy(values.astype(np.float32)).cuda())
+
+    def wide(*size):
+        return rng.integers(-(1 << 20) + 1, 1 << 20, size)
+
+    def narrow(*size):
+        return rng.choice([-4, -2, -1, 1, 2, 4], size)
+    w = Coded(M + B, M, N, L, k, V, T, F32, False)
+    for table, value in ((narrow, wide), (wide, narrow)):
+        w = _f32_table(w, torch.from_numpy(table(1 << L, V).astype(np.float32)).cuda())
+        x = sparse(B, N, value(B, 3))
+        assert torch.equal(w.linear(x).double(), x.double() @ w.W.t())
+        dy = sparse(B, M, value(B, 3))
+        assert torch.equal(w.backward(dy, dbias=False)[0].double(), dy.double() @ w.W)
+    # dw: three rows of the batch to each row of the matrix
+    dy = sparse(M, B, wide(M, 3)).t().contiguous()
+    xp = api.act_pack(torch.from_numpy(narrow(B, N).astype(np.float32)).cuda())
+    _, dw, _ = w.backward(dy, dx=False, dbias=False, x=xp)
+    xv = api.act_unpack(xp, F32).double()
+    assert torch.equal(dw.double(), dy.double().t() @ xv)
+
+
+@pytest.mark.parametrize("L,k,V,T,M,N,B", F32_SIZES)
+def test_f32_rms(L, k, V, T, M, N, B):
+    """N(0, 1) values: a random walk of K whole units 2^-23 over partial sums that grow like
+    the root of their count is sqrt(K / 2) of them (halved: they are spread over a unit); two
+    more for the products."""
+    rng = np.random.default_rng(B)
+    w = Coded(M + B, M, N, L, k, V, T, F32, False)
+
+    def normal(*size):
+        return torch.from_numpy(rng.standard_normal(size)).float().cuda()
+    x, dy = normal(B, N), normal(B, M)
+    xp = api.act_pack(x)
+    xv = api.act_unpack(xp, F32).double()
+    dx, dw, _ = w.backward(dy, x=xp)
+    for name, got, want, K in (("y", w.linear(x), x.double() @ w.W.t(), N),
+                               ("dx", dx, dy.double() @ w.W, M),
+                               ("dw", dw, dy.double().t() @ xv, B)):
+        rms = float((got.double() - want).square().mean().sqrt() / want.square().mean().sqrt())
+        lim = (np.sqrt(K / 2) + 2) * 2.0 ** -24
+        _say(f"f32 rms {name} M={M} N={N} B={B}: {rms:.3g}, limit {lim:.3g}")
+        assert rms <= lim
+
+
+def test_f32_near_the_largest_numbers():
+    """Numbers whose first 16-bit term rounds past the largest: finite products, exact."""
+    L, k, V, T, M, N, B = 16, 2, 1, 256, 130, 512, 300
+    rng = np.random.default_rng(4)
+    w = Coded(3, M, N, L, k, V, T, F32, False)
+    w = _f32_table(w, torch.from_numpy(
+        rng.choice([-0.5, -0.25, 0.25, 0.5], (1 << L, V)).astype(np.float32)).cuda())
+    top = torch.finfo(F32).max
+    x = torch.zeros(B, N, device="cuda")
+    at = torch.from_numpy(rng.integers(0, N, B)).cuda()
+    x[torch.arange(B, device="cuda"), at] = torch.from_numpy(
+        rng.choice([top, -top, 0.999 * top, 0.998 * top], B).astype(np.float32)).cuda()
+    assert torch.equal(w.linear(x).double(), x.double() @ w.W.t())
+    dy = torch.zeros(B, M, device="cuda")
+    dy[:, 5] = top
+    assert torch.equal(w.backward(dy, dbias=False)[0].double(), dy.double() @ w.W)

@@ -459,25 +459,29 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
 // ---------------------------------------------------------------- fp32 by bf16 terms
 //
 // The matrix cores multiply bf16 16 times as fast as fp32.  An fp32 number is the sum of three
-// bf16 numbers, x = x0 + x1 + x2, each the next eight bits of the significand (truncated, so
-// the differences are exact), and six of the nine products reach fp32's own accuracy:
-//     x y ~ x0 y0 + (x0 y1 + x1 y0) + (x1 y1 + x0 y2 + x2 y0),
-// the three left out being below 2^-22 |x y| together, 2^-24 on average.  Each product is exact
-// and the sums are fp32, in fewer additions than the fp32 instruction makes.  (A term below
-// 2^-133, bf16's smallest number, is lost, so numbers below 2^-109 keep fewer bits.)  The
-// operands stay fp32 in memory and LDS and are split in registers: about 50 VALU instructions
+// bf16 numbers, x = x0 + x1 + x2, and six of the nine products reach fp32's own accuracy:
+//     x y ~ x0 y0 + (x0 y1 + x1 y0) + (x1 y1 + x0 y2 + x2 y0).
+// x0 is x rounded to nearest, x1 the next eight bits of the rest, x2 what remains (the
+// differences are exact).  With 1 <= |x| < 2, |x1| <= 2^-8 and |x2| < 2^-16, so the three left
+// out are below (1 + 2^-9) 2^-23 |x y| together, of either sign.  (With x0 truncated they
+// reach 2^-7 and 2^-15: 1.96 2^-22 was left out of the square of 1 + 2^-7 - 2^-23, always
+// towards zero.  All three rounded: 2^-24, but 4096^3 took 819 us against 808, and 785
+// with all truncated.)  Each product is exact and the sums are fp32, in fewer additions than
+// the fp32 instruction makes.  (What is below 2^-133, bf16's smallest number, is lost, so numbers
+// below 2^-109 keep fewer bits.)  The operands stay fp32 in memory and LDS and are split in registers: about 50 VALU instructions
 // for a fragment, which meets FI or FJ others in six matrix instructions each.  VALU issue
 // bounds it: 70 % of the clocks at 4096^3 with 64 x 64 per wave, the matrix cores 52 %.  That
-// takes 0.77 ms (178 TFLOP/s); the fp32 instruction took 1.05 (its peak is 157 TFLOP/s), the
+// takes 0.79 ms (174 TFLOP/s); the fp32 instruction took 1.05 (its peak is 157 TFLOP/s), the
 // library's product 0.91.
-// An infinity has no such split (inf - inf, and inf times a zero term, are NaN): a step that
-// holds an infinity or a NaN is multiplied with the fp32 instruction instead.
+// An infinity has no such split (inf - inf, and inf times a zero term, are NaN), nor has a number
+// whose x0 would round to one: a step that holds an infinity, a NaN or a magnitude from
+// (2 - 2^-8) 2^127 on is multiplied with the fp32 instruction instead.
 
 struct Terms {
     s16x8 t[3];
 };
 
-// The terms of eight values; `wild` gathers whether any of them is an infinity or a NaN.
+// The terms of eight values; `wild` gathers whether any of them has no terms.
 __device__ __forceinline__ void split_terms(const f32x4 &lo, const f32x4 &hi, Terms &out,
                                             bool &wild) {
     float x[8];
@@ -491,24 +495,26 @@ __device__ __forceinline__ void split_terms(const f32x4 &lo, const f32x4 &hi, Te
     float top = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
-        uint32_t u[2][3];
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        const uint32_t b = __builtin_bit_cast(
+            uint32_t, __builtin_convertvector((f32x2{x[k], x[k + 1]}), bf16x2));
+        p[0][k / 2] = b;
+        uint32_t u[2][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const float v = x[k + e];
-            const float v0 = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
-            const float r = v - v0;  // exact
-            const float v1 = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
-            u[e][0] = __float_as_uint(v);
-            u[e][1] = __float_as_uint(r);
-            u[e][2] = __float_as_uint(r - v1);  // exact, eight bits
+            // the differences are exact, and the last has eight bits
+            const float r = x[k + e] - __uint_as_float(e ? b & 0xFFFF0000u : b << 16);
+            u[e][0] = __float_as_uint(r);
+            u[e][1] = __float_as_uint(r - __uint_as_float(u[e][0] & 0xFFFF0000u));
         }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)  // the upper halves of the pair
+            p[1 + t][k / 2] = __builtin_amdgcn_perm(u[1][t], u[0][t], 0x07060302u);
         top = __builtin_elementwise_maximum(
             __builtin_elementwise_maximum(__builtin_fabsf(x[k]), __builtin_fabsf(x[k + 1])), top);
-#pragma unroll
-        for (int t = 0; t < 3; ++t)  // the upper halves of the pair
-            p[t][k / 2] = __builtin_amdgcn_perm(u[1][t], u[0][t], 0x07060302u);
     }
-    wild = wild || !(top < __builtin_inff());
+    wild = wild || !(top < 0x1.FFp127f);
 #pragma unroll
     for (int t = 0; t < 3; ++t) out.t[t] = __builtin_bit_cast(s16x8, p[t]);
 }
