@@ -351,7 +351,8 @@ typedef enum {
  * 16-bit inputs are exact and sums fp32.  fp32 products are fp32 arithmetic for B <= 128 with
  * T a multiple of 32, kV <= 4 and V != 3; elsewhere each is the sum of six exact products of
  * bf16 terms, less than 2^-22 of it left out (numbers below 2^-109: to 2^-133).  z is not rounded
- * before the activation; each output is rounded once.  Repeated calls give identical results.
+ * before the activation; each output is rounded once.  Repeated calls give identical results,
+ * and a row of y depends on no other row of x, infinities and NaN in one included.
  * N == 0 gives z = bias; M == 0 or B == 0 is a no-op.
  * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED, TCQ_EWORKSPACE, TCQ_EHIP.
  */

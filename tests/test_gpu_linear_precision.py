@@ -265,3 +265,39 @@ def test_f32_near_the_largest_numbers():
     dy = torch.zeros(B, M, device="cuda")
     dy[:, 5] = top
     assert torch.equal(w.backward(dy, dbias=False)[0].double(), dy.double() @ w.W)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("L,k,V,T,M,N,B", F32_SIZES + [(16, 2, 1, 256, 150, 512, 1),
+                                                       (16, 2, 1, 256, 150, 512, 50)])
+def test_rows_do_not_see_their_neighbours(L, k, V, T, M, N, B, dtype):
+    """Bit for bit: an infinity, a NaN or the largest number in a row of x or dy changes that
+    row's outputs (y, dx) alone, in a column of dy or a group of x that row or group of dw."""
+    rng = np.random.default_rng(B + M)
+    w = Coded(M + B, M, N, L, k, V, T, dtype, False)
+
+    def normal(*size):
+        return torch.from_numpy(rng.standard_normal(size)).to(dtype).cuda()
+    a = torch.from_numpy(rng.standard_normal(M) / np.sqrt(N)).float().cuda()
+    x, dy = normal(B, N), normal(B, M)
+
+    def run(x, dy):
+        dx, dw, _ = w.backward(dy, row_scale=a, x=api.act_pack(x))
+        return w.linear(x, row_scale=a), dx, dw
+    y, dx, dw = run(x, dy)
+    for bad in (float("inf"), float("nan"), torch.finfo(dtype).max):
+        row, col, out = B // 2, int(rng.integers(0, N)), int(rng.integers(0, M))
+        xb, db = x.clone(), dy.clone()
+        xb[row, col] = bad
+        got = run(xb, dy)
+        rows = torch.arange(B, device="cuda") != row
+        cols = torch.arange(N, device="cuda") // 32 != col // 32
+        _say(f"neighbours M={M} N={N} B={B} {dtype} {bad}")
+        assert torch.equal(got[0][rows], y[rows]) and not torch.equal(got[0][row], y[row])
+        assert torch.equal(got[1], dx) and torch.equal(got[2][:, cols], dw[:, cols])
+        db[row, out] = bad
+        got = run(x, db)
+        keep = torch.arange(M, device="cuda") != out
+        assert torch.equal(got[0], y) and torch.equal(got[1][rows], dx[rows])
+        assert not torch.equal(got[1][row], dx[row])
+        assert torch.equal(got[2][keep], dw[keep]) and not torch.equal(got[2][out], dw[out])

@@ -474,16 +474,26 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
 // takes 0.79 ms (174 TFLOP/s); the fp32 instruction took 1.05 (its peak is 157 TFLOP/s), the
 // library's product 0.91.
 // An infinity has no such split (inf - inf, and inf times a zero term, are NaN), nor has a number
-// whose x0 would round to one: a step that holds an infinity, a NaN or a magnitude from
-// (2 - 2^-8) 2^127 on is multiplied with the fp32 instruction instead.
+// whose x0 would round to one.  A step that holds an infinity, a NaN or a magnitude from
+// (2 - 2^-8) 2^127 on is multiplied both ways, and the outputs whose own row of A or B holds it
+// take the fp32 instruction's sums: an output depends on its two rows alone.
 
 struct Terms {
     s16x8 t[3];
 };
 
-// The terms of eight values; `wild` gathers whether any of them has no terms.
-__device__ __forceinline__ void split_terms(const f32x4 &lo, const f32x4 &hi, Terms &out,
-                                            bool &wild) {
+// Whether any of eight values has no terms.
+__device__ __forceinline__ bool has_no_terms(const f32x4 &lo, const f32x4 &hi) {
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        top = __builtin_elementwise_maximum(
+            __builtin_elementwise_maximum(__builtin_fabsf(lo[k]), __builtin_fabsf(hi[k])), top);
+    return !(top < 0x1.FFp127f);
+}
+
+// The terms of eight values.
+__device__ __forceinline__ void split_terms(const f32x4 &lo, const f32x4 &hi, Terms &out) {
     float x[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -492,7 +502,6 @@ __device__ __forceinline__ void split_terms(const f32x4 &lo, const f32x4 &hi, Te
     }
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     u32x4 p[3];
-    float top = 0.0f;
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
         typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -511,10 +520,7 @@ __device__ __forceinline__ void split_terms(const f32x4 &lo, const f32x4 &hi, Te
 #pragma unroll
         for (int t = 0; t < 2; ++t)  // the upper halves of the pair
             p[1 + t][k / 2] = __builtin_amdgcn_perm(u[1][t], u[0][t], 0x07060302u);
-        top = __builtin_elementwise_maximum(
-            __builtin_elementwise_maximum(__builtin_fabsf(x[k]), __builtin_fabsf(x[k + 1])), top);
     }
-    wild = wild || !(top < 0x1.FFp127f);
 #pragma unroll
     for (int t = 0; t < 3; ++t) out.t[t] = __builtin_bit_cast(s16x8, p[t]);
 }
@@ -575,28 +581,55 @@ __device__ __forceinline__ void gemm_tile_f32(const Operand<float> &A, const Ope
         mac(0, 1);
         mac(0, 0);
     };
-    // The same with the fp32 instruction, from the tile in LDS.
-    auto mul_half_wild = [&](const char *ta, const char *tb, int half) {
-#pragma unroll 1
-        for (int ks = 0; ks < 2; ++ks)
+    // Bit r: row r of a fragment has a value without terms (its 32 k are in four lanes).
+    auto wild_rows = [&](const f32x4 &lo, const f32x4 &hi) {
+        uint64_t m = __ballot(has_no_terms(lo, hi));
+        m |= m >> 32;
+        m |= m >> 16;
+        return static_cast<uint32_t>(m) & 0xFFFFu;
+    };
+    // Rows with such a value: their outputs take the fp32 instruction's sums, from the tile in
+    // LDS, and zeros replace the values to be split.  A lane's four outputs are row l16 of
+    // A with rows 4 g .. 4 g + 3 of B.
+    auto mul_wild = [&](const char *ta, const char *tb, int half) {
 #pragma unroll
-            for (int i = 0; i < FH; ++i)
+        for (int i = 0; i < FH; ++i) {
+            const f32x4 a0 = ra.read(ta, half * FH + i, 0), a1 = ra.read(ta, half * FH + i, 1);
+            const bool wild_a = wild_rows(a0, a1) >> (lane & 15) & 1;
+            if (wild_a) xa[i][0] = xa[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < FJ; ++j)
-                    acc[half * FH + i][j] =
-                        Traits<float>::mma(rb.read(tb, j, ks), ra.read(ta, half * FH + i, ks),
-                                           acc[half * FH + i][j]);
+            for (int j = 0; j < FJ; ++j) {
+                const f32x4 b0 = rb.read(tb, j, 0), b1 = rb.read(tb, j, 1);
+                const uint32_t rows = wild_rows(b0, b1);
+                if (half == 0 && i == 0 && (rows >> (lane & 15) & 1))
+                    xb[j][0] = xb[j][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+                const uint32_t wild_b = rows >> (lane >> 4) * 4;
+                const f32x4 f = Traits<float>::mma(
+                    b1, a1, Traits<float>::mma(b0, a0, f32x4{0.f, 0.f, 0.f, 0.f}));
+                f32x4 &c = acc[half * FH + i][j];
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    if (wild_a || (wild_b >> v & 1)) c[v] += f[v];
+                __builtin_amdgcn_sched_barrier(0);  // (one at a time: this path's registers)
+            }
+        }
     };
     auto step = [&](int s, char *ta, char *tb, const char *na, const char *nb) {
-        bool wild = false;
+        bool wild_b = false;
 #pragma unroll
-        for (int j = 0; j < FJ; ++j) split_terms(xb[j][0], xb[j][1], pb[j], wild);
+        for (int j = 0; j < FJ; ++j) wild_b |= has_no_terms(xb[j][0], xb[j][1]);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
+            bool wild = wild_b;
 #pragma unroll
-            for (int i = 0; i < FH; ++i) split_terms(xa[i][0], xa[i][1], pa[i], wild);
-            const bool slow = __any(wild);
-            if (__builtin_expect(slow, 0)) mul_half_wild(ta, tb, half);
+            for (int i = 0; i < FH; ++i) wild |= has_no_terms(xa[i][0], xa[i][1]);
+            if (__builtin_expect(__any(wild), 0)) mul_wild(ta, tb, half);
+            if (half == 0) {
+#pragma unroll
+                for (int j = 0; j < FJ; ++j) split_terms(xb[j][0], xb[j][1], pb[j]);
+            }
+#pragma unroll
+            for (int i = 0; i < FH; ++i) split_terms(xa[i][0], xa[i][1], pa[i]);
             if (half == 0) {
                 read_a(ta, 1);
             } else {
@@ -606,7 +639,7 @@ __device__ __forceinline__ void gemm_tile_f32(const Operand<float> &A, const Ope
                 read_a(na, 0);
                 read_b(nb);
             }
-            if (__builtin_expect(!slow, 1)) mul_half(half);
+            mul_half(half);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
