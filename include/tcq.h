@@ -347,7 +347,8 @@ typedef enum {
  *   pre, ldp   : nullable device out, B x M: z, rounded to the layer's type (what
  *                tcq_act_pack and tcq_decode_linear_backward take)
  *   workspace  : >= what tcq_decode_linear_workspace_bytes reports
- * Outputs other than y == residual must not overlap inputs or one another.  Products of
+ * Outputs other than y == residual must not overlap inputs or one another (y or pre over x,
+ * the residual or each other: TCQ_EINVAL).  Products of
  * 16-bit inputs are exact and sums fp32.  fp32 products are fp32 arithmetic for B <= 128 with
  * T a multiple of 32, kV <= 4 and V != 3; elsewhere each is the sum of six exact products of
  * bf16 terms, less than 2^-22 of it left out (numbers below 2^-109: to 2^-133).  z is not rounded
@@ -383,6 +384,7 @@ int tcq_decode_linear(const uint32_t *bitstream, const uint32_t *start_state,
  *   codes, ldq, scale  : as written by tcq_act_pack
  *   out, ldo           : device out of type dtype, ldo >= cols.  Values are exact in fp32
  *                        and bf16; fp16 holds those of fp16 inputs exactly and rounds others.
+ * Outputs that overlap inputs or one another are refused (TCQ_EINVAL).
  * rows == 0 or cols == 0 is a no-op.
  * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED (rows or cols above 2^31 - 1), TCQ_EHIP.
  */
@@ -414,6 +416,7 @@ int tcq_act_unpack(const int8_t *codes, int64_t ldq, const uint8_t *scale, int64
  *   dbias       : nullable device out, M floats
  *   workspace   : >= what the workspace query reports for the same outputs (nonzero
  *                 dx, dw, dbias: wanted)
+ * Outputs must not overlap inputs or one another (dx, dw and dbias: TCQ_EINVAL).
  * B == 0 gives dw = 0 and dbias = 0, M == 0 gives dx = 0.  At least one output is wanted.
  * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED, TCQ_EWORKSPACE, TCQ_EHIP.
  */

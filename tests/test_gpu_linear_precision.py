@@ -11,7 +11,7 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("no GPU visible", allow_module_level=True)
 
-from trellis_coded_bit_amd import api  # noqa: E402
+from trellis_coded_bit_amd import _lib, api  # noqa: E402
 
 import linear_check as lc  # noqa: E402
 from test_gpu_linear import Coded, _grad_reference  # noqa: E402
@@ -301,3 +301,25 @@ def test_rows_do_not_see_their_neighbours(L, k, V, T, M, N, B, dtype):
         assert torch.equal(got[0], y) and torch.equal(got[1][rows], dx[rows])
         assert not torch.equal(got[1][row], dx[row])
         assert torch.equal(got[2][keep], dw[keep]) and not torch.equal(got[2][out], dw[out])
+
+
+@pytest.mark.parametrize("B", [1, 40, 200])
+def test_columns_of_one_buffer(B):
+    """x, the residual, the output and guards as column ranges of one matrix; x itself as the
+    output is refused."""
+    M, N, dtype = 256, 256, BF16
+    rng = np.random.default_rng(B)
+    w = Coded(5, M, N, 16, 2, 1, 256, dtype, True)
+    buf = torch.from_numpy(rng.integers(-8, 9, (B, 1024)).astype(np.float32)).to(dtype).cuda()
+    x, out, res = buf[:, 8:264], buf[:, 264:520], buf[:, 520:776]
+    keep = buf.clone()
+    want = (x.double() @ w.W.t() + res.double()).to(dtype)
+    w.linear(x, residual=res, out=out)
+    assert torch.equal(out, want)
+    out.copy_(keep[:, 264:520])
+    assert torch.equal(buf, keep)
+    for bad in (x, buf[:, 9:265], buf[:, 519:775]):
+        with pytest.raises(_lib.TcqError) as e:
+            w.linear(x, residual=res, out=bad)
+        assert e.value.status == _lib.TCQ_EINVAL
+    assert torch.equal(buf, keep)

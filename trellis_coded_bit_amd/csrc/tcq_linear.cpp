@@ -1,6 +1,7 @@
 // libtcq C ABI of the coded linear layer and the 8-bit checkpoints: argument checks and
 // workspace sizes.  The numeric steps run in kernels_linear.hip and kernels_checkpoint.hip.
 #include "tcq.h"
+#include "region.h"
 #include "tcq_internal.h"
 
 using namespace tcq;
@@ -61,6 +62,12 @@ int check_matrix(const char *fn, const char *name, const void *p, int64_t ld, in
         return TCQ_EINVAL;
     }
     return TCQ_OK;
+}
+
+int check_apart(const char *fn, const Region &out, const Region &other) {
+    if (!out.p || !other.p || !overlap(out, other)) return TCQ_OK;
+    set_error("%s: %s and %s overlap", fn, out.name, other.name);
+    return TCQ_EINVAL;
 }
 
 int check_coded(const char *fn, const void *bits, const void *s0, const void *table,
@@ -167,6 +174,15 @@ extern "C" int tcq_decode_linear(const uint32_t *bitstream, const uint32_t *star
     rc = check_workspace(fn, workspace, workspace_bytes,
                          forward_bytes(dtype, B, M, N, L, k, V, T));
     if (rc != TCQ_OK) return rc;
+    const Region rx = region("x", N > 0 ? x : nullptr, B, ldx, N, size);
+    const Region ry = region("y", y, B, ldy, M, size), rp = region("pre", pre, B, ldp, M, size);
+    const Region rr = region("residual", residual == y ? nullptr : residual, B, ldr, M, size);
+    rc = check_apart(fn, ry, rx);
+    if (rc == TCQ_OK) rc = check_apart(fn, ry, rr);
+    if (rc == TCQ_OK) rc = check_apart(fn, rp, rx);
+    if (rc == TCQ_OK) rc = check_apart(fn, rp, ry);
+    if (rc == TCQ_OK) rc = check_apart(fn, rp, rr);
+    if (rc != TCQ_OK) return rc;
     const CodedMatrix w{bitstream, start_state, codebook, M, N, L, k, V, T};
     const LinearCall c{dtype, act, x, B, ldx, row_scale, bias, residual, ldr, y, ldy, pre, ldp};
     const hipError_t e = launch_linear(w, c, static_cast<char *>(workspace), stream);
@@ -184,6 +200,12 @@ extern "C" int tcq_act_pack(const void *X, int dtype, int64_t rows, int64_t cols
     rc = check_matrix(fn, "X", X, ldx, cols, size_of(dtype));
     if (rc == TCQ_OK) rc = check_matrix(fn, "codes", codes, ldq, cols, 1);
     if (rc == TCQ_OK) rc = check_matrix(fn, "scale", scale, 0, 0, 1);
+    const Region rX = region("X", X, rows, ldx, cols, size_of(dtype));
+    const Region rq = region("codes", codes, rows, ldq, cols, 1);
+    const Region rs = region("scale", scale, 1, 0, rows * ((cols + 31) / 32), 1);
+    if (rc == TCQ_OK) rc = check_apart(fn, rq, rX);
+    if (rc == TCQ_OK) rc = check_apart(fn, rs, rX);
+    if (rc == TCQ_OK) rc = check_apart(fn, rs, rq);
     if (rc != TCQ_OK) return rc;
     const hipError_t e = launch_act_pack(X, dtype, rows, cols, ldx, codes, ldq, scale, stream);
     if (e != hipSuccess) return hip_fail(fn, "checkpoint launch", e);
@@ -201,6 +223,10 @@ extern "C" int tcq_act_unpack(const int8_t *codes, int64_t ldq, const uint8_t *s
     rc = check_matrix(fn, "codes", codes, ldq, cols, 1);
     if (rc == TCQ_OK) rc = check_matrix(fn, "scale", scale, 0, 0, 1);
     if (rc == TCQ_OK) rc = check_matrix(fn, "out", out, ldo, cols, size_of(dtype));
+    const Region ro = region("out", out, rows, ldo, cols, size_of(dtype));
+    if (rc == TCQ_OK) rc = check_apart(fn, ro, region("codes", codes, rows, ldq, cols, 1));
+    if (rc == TCQ_OK)
+        rc = check_apart(fn, ro, region("scale", scale, 1, 0, rows * ((cols + 31) / 32), 1));
     if (rc != TCQ_OK) return rc;
     const hipError_t e =
         launch_act_unpack(codes, ldq, scale, rows, cols, dtype, out, ldo, cols, stream);
@@ -266,6 +292,13 @@ extern "C" int tcq_decode_linear_backward(
         fn, workspace, workspace_bytes,
         linear_grad_layout(size, B, M, N, dx != nullptr, dw != nullptr, dbias != nullptr, 1)
             .bytes);
+    if (rc != TCQ_OK) return rc;
+    const Region rdx = region("dx", N > 0 ? dx : nullptr, B, lddx, N, size);
+    const Region rdw = region("dw", N > 0 ? dw : nullptr, M, lddw, N, size);
+    const Region rdb = region("dbias", dbias, 1, 0, M, sizeof(float));
+    rc = check_apart(fn, rdx, rdw);
+    if (rc == TCQ_OK) rc = check_apart(fn, rdx, rdb);
+    if (rc == TCQ_OK) rc = check_apart(fn, rdw, rdb);
     if (rc != TCQ_OK) return rc;
     const CodedMatrix w{bitstream, start_state, codebook, M, N, L, k, V, T};
     const LinearGrad c{dtype, act, dy, B, lddy, row_scale, z_codes, ldz, z_scale, x_codes, ldx,
