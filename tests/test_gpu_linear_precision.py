@@ -323,3 +323,43 @@ def test_columns_of_one_buffer(B):
             w.linear(x, residual=res, out=bad)
         assert e.value.status == _lib.TCQ_EINVAL
     assert torch.equal(buf, keep)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("act", ["none", "relu"])
+def test_two_terms_of_one_number(act, dtype):
+    """Products dy row_scale that fp32 rounds to the middle between two numbers of the type,
+    from either side: the low term must belong to the high one that is stored.  A second row of
+    the matrix takes the high term away (its row scale is 1), so dx is the low term."""
+    rng = np.random.default_rng(13)
+    bits = 12 if dtype == F16 else 9  # of a middle: one more than the type's
+    dy, a = [], []
+    for _ in range(40):
+        v = torch.from_numpy(rng.uniform(1, 2, 1 << 17)).to(dtype).float().numpy()
+        f = rng.uniform(0.25, 1, 1 << 17).astype(np.float32)
+        exact = v.astype(np.float64) * f
+        p = exact.astype(np.float32)
+        m = np.frexp(p.astype(np.float64))[0] * 2.0 ** bits
+        hit = (m == np.rint(m)) & (np.rint(m) % 2 == 1) & (exact != p)
+        dy += list(v[hit][:8])
+        a += list(f[hit][:8])
+    R = len(dy)
+    assert R > 50
+    M, N = R + 1, 64
+    w = Coded(1, M, N, 8, 2, 1, 64, dtype, False)
+    w.table = torch.ones_like(w.table)
+    scale = torch.ones(M, device="cuda")
+    scale[:R] = torch.tensor(np.array(a), device="cuda")
+    g = torch.zeros(R, M, dtype=dtype, device="cuda")
+    v = torch.tensor(np.array(dy), device="cuda")
+    at = torch.arange(R, device="cuda")
+    s = v * scale[:R]
+    high = s.to(dtype)
+    g[at, at] = v.to(dtype)
+    g[at, R] = -high
+    z = api.act_pack(torch.ones(R, M, dtype=dtype, device="cuda"))
+    dx = w.backward(g, row_scale=scale, act=act, z=z, dbias=False)[0]
+    want = (v.double() * scale[:R].double() - high.double())[:, None].expand(R, N)
+    lim = (4 * lc.U + lc.half(dtype) ** 2) * s.double().abs()[:, None]
+    lim = lim + lc.half(dtype) * (want.abs() + lim) + lc.tiny(dtype)
+    assert bool(((dx.double() - want).abs() <= lim).all())

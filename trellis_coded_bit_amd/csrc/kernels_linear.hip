@@ -820,6 +820,8 @@ template <typename T, int ACT, int TERMS>
 __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__ out,
                                                     T *__restrict__ out_low) {
     constexpr int kLow = gemm::kLowShift<T>;
+    constexpr bool kTwo = TERMS == 2;
+    constexpr float kBig = 1 << kLow;
     __shared__ float red[4][8][65];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     int exponent = 0;
@@ -845,9 +847,10 @@ __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         sum[e] = 0.0f;
-        sc[e] = a.scale && e < left ? a.scale[c0 + e] : 1.0f;
+        // (0 past M: a power of two times 1 may be an infinity)
+        sc[e] = e < left ? (a.scale ? a.scale[c0 + e] : 1.0f) : 0.0f;
         if constexpr (TERMS == 2 && kLow != 0)
-            sc[e] = __builtin_amdgcn_ldexpf(sc[e], -exponent);
+            sc[e] = __builtin_amdgcn_ldexpf(sc[e], kLow - exponent);
     }
     if (c0 < a.ld) {
 #pragma unroll 2
@@ -875,12 +878,15 @@ __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__
                 if constexpr (ACT != TCQ_ACT_NONE)
                     if (e < left) g = act_grad<ACT>(g, code_value(z.v[e], ez));
                 sum[e] += g;
-                const float x = g * sc[e];
-                o.v[e] = static_cast<T>(x);
+                const float x = g * sc[e];  // (two terms: times 2^kLow)
+                // Every step from x on is exact but for the two roundings to T.  (The compiler
+                // takes the product before a rounding to fp16 exactly where it can, in one
+                // use of x and not in another: with x - T(x) the low term belonged to
+                // another high one where x is halfway.)
+                o.v[e] = static_cast<T>(kTwo ? x * (1.0f / kBig) : x);
                 if constexpr (TERMS == 2) {
                     const float high = static_cast<float>(o.v[e]);
-                    float rest = x - high;
-                    if constexpr (kLow != 0) rest *= 1 << kLow;
+                    const float rest = __builtin_fmaf(high, -kBig, x);
                     // an infinity or a NaN is the high term's alone
                     low.v[e] = static_cast<T>(__builtin_fabsf(high) < __builtin_inff() ? rest : 0.0f);
                 }
