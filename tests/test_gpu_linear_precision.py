@@ -325,6 +325,63 @@ def test_columns_of_one_buffer(B):
     assert torch.equal(buf, keep)
 
 
+def _terms_of_slope(z, act):
+    """The two terms of act'(z), whose magnitudes bound its rounding."""
+    if act == "silu":
+        s = torch.sigmoid(z)
+        return s, z * s * torch.sigmoid(-z)
+    return 0.5 * torch.erfc(-z / np.sqrt(2.0)), z * torch.exp(-z * z / 2) / np.sqrt(2 * np.pi)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("B", [1, 20, 200])
+def test_activations_keep_small_values(B, act, dtype):
+    """act and its slope relative to their value, where it is far below |z| too: in fp32 to
+    2^-20 (16 units; the formulas' roundings in fp32 arithmetic stay below 9), in 16-bit types
+    to 2^-16 and the output's own rounding, from 2^-119 on.  z comes as the bias (x = 0) and
+    as a checkpoint, dy is 1."""
+    M, N = 6000, 256
+    rng = np.random.default_rng(B)
+    rel = 2.0 ** -20 if dtype == F32 else 2.0 ** -16
+    for lo, hi in ((-8, -2), (-2, 2), (-14, 9), (-90, 90), (-1e4, 1e4)):
+        w = Coded(3, M, N, 8, 2, 1, 64, dtype, True)
+        z = torch.from_numpy(rng.uniform(lo, hi, M)).float().cuda()
+        y = w.linear(torch.zeros(B, N, dtype=dtype, device="cuda"), bias=z, act=act)
+        want = lc.act(z.double(), act)
+        lim = rel * want.abs() + 2.0 ** -119
+        lim = lim + lc.half(dtype) * (want.abs() + lim) + lc.tiny(dtype)
+        r = float(((y.double() - want).abs() / lim).max())
+        assert torch.equal(y, y[:1].expand(B, M))
+        zp = api.act_pack(z.to(dtype).expand(B, M).contiguous())
+        zv = api.act_unpack(zp, F32)[0].double()
+        one = torch.zeros(B, M, dtype=dtype, device="cuda")
+        one[B // 2] = 1
+        db = w.backward(one, act=act, z=zp, dx=False)[2]
+        first, second = _terms_of_slope(zv, act)
+        lim = rel * (first.abs() + second.abs()) + 2.0 ** -119
+        rs = float(((db.double() - first - second).abs() / lim).max())
+        _say(f"small values B={B} {act} {dtype} [{lo}, {hi}]: worst error / bound {r:.3g}, "
+             f"slope {rs:.3g}")
+        assert max(r, rs) <= 1
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_activations_of_infinities(dtype):
+    """z of +inf gives +inf, a NaN stays one, the largest finite numbers give themselves or 0."""
+    M, N = 64, 256
+    w = Coded(3, M, N, 8, 2, 1, 64, dtype, True)
+    top = torch.finfo(dtype).max
+    z = torch.zeros(M, device="cuda")
+    z[:5] = torch.tensor([float("inf"), float("nan"), top, -top, float("-inf")])
+    for act in ("silu", "gelu", "relu"):
+        for B in (1, 200):
+            y = w.linear(torch.zeros(B, N, dtype=dtype, device="cuda"), bias=z, act=act).float()
+            assert bool((y[:, 0] == float("inf")).all()) and bool(torch.isnan(y[:, 1]).all())
+            assert bool((y[:, 2] == top).all()) and bool((y[:, 3] == 0).all())
+            assert bool((y[:, 5:] == 0).all())
+
+
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("act", ["none", "relu"])
 def test_two_terms_of_one_number(act, dtype):

@@ -281,7 +281,7 @@ struct LayerEpilogue {
         if (pre) store4(pre + i * ldp + c.j, c.j, J, vec_p, z);
         with_act(act, [&](auto a) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = act_value<decltype(a)::value>(z[e]);
+            for (int e = 0; e < 4; ++e) o[e] = act_value<decltype(a)::value, sizeof(T) == 4>(z[e]);
         });
         if (res) {
             const f32x4 r = load4(res + i * ldr + c.j, c.j, J, vec_r);
@@ -295,7 +295,7 @@ struct LayerEpilogue {
         const float z = __builtin_fmaf(scale ? scale[j] : 1.0f, s, bias ? bias[j] : 0.0f);
         if (pre) pre[i * ldp + j] = static_cast<T>(z);
         float o = 0.0f;
-        with_act(act, [&](auto a) { o = act_value<decltype(a)::value>(z); });
+        with_act(act, [&](auto a) { o = act_value<decltype(a)::value, sizeof(T) == 4>(z); });
         if (res) o += static_cast<float>(res[i * ldr + j]);
         y[i * ldy + j] = static_cast<T>(o);
     }
@@ -876,7 +876,7 @@ __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__
             for (int e = 0; e < 8; ++e) {
                 float g = static_cast<float>(d.v[e]);
                 if constexpr (ACT != TCQ_ACT_NONE)
-                    if (e < left) g = act_grad<ACT>(g, code_value(z.v[e], ez));
+                    if (e < left) g = act_grad<ACT, sizeof(T) == 4>(g, code_value(z.v[e], ez));
                 sum[e] += g;
                 const float x = g * sc[e];  // (two terms: times 2^kLow)
                 // Every step from x on is exact but for the two roundings to T.  (The compiler
