@@ -346,7 +346,8 @@ typedef enum {
  *   y, ldy     : device out, B x M, ldy >= M
  *   pre, ldp   : nullable device out, B x M: z, rounded to the layer's type (what
  *                tcq_act_pack and tcq_decode_linear_backward take)
- *   workspace  : >= what tcq_decode_linear_workspace_bytes reports
+ *   workspace  : >= what tcq_decode_linear_workspace_bytes reports (never less for a larger
+ *                B: a workspace of the largest batch serves every smaller one)
  * Outputs other than y == residual must not overlap inputs or one another (y or pre over x,
  * the residual or each other: TCQ_EINVAL).  Products of
  * 16-bit inputs are exact and sums fp32.  fp32 products are fp32 arithmetic for B <= 128 with
@@ -417,7 +418,7 @@ int tcq_act_unpack(const int8_t *codes, int64_t ldq, const uint8_t *scale, int64
  *   dw, lddw    : nullable device out, M x N
  *   dbias       : nullable device out, M floats
  *   workspace   : >= what the workspace query reports for the same outputs (nonzero
- *                 dx, dw, dbias: wanted)
+ *                 dx, dw, dbias: wanted; never less for a larger B)
  * Outputs must not overlap inputs or one another (dx, dw and dbias: TCQ_EINVAL).
  * B == 0 gives dw = 0 and dbias = 0, M == 0 gives dx = 0.  At least one output is wanted.
  * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED, TCQ_EWORKSPACE, TCQ_EHIP.

@@ -420,3 +420,26 @@ def test_two_terms_of_one_number(act, dtype):
     lim = (4 * lc.U + lc.half(dtype) ** 2) * s.double().abs()[:, None]
     lim = lim + lc.half(dtype) * (want.abs() + lim) + lc.tiny(dtype)
     assert bool(((dx.double() - want).abs() <= lim).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_one_workspace_for_all_batches(dtype):
+    """The workspace of the largest batch serves the smaller ones, whichever way they take."""
+    M, N, most = 512, 1024, 2100
+    rng = np.random.default_rng(1)
+    w = Coded(5, M, N, 16, 2, 1, 256, dtype, True)
+    x = torch.from_numpy(rng.integers(-8, 9, (most, N)).astype(np.float32)).to(dtype).cuda()
+    dy = torch.from_numpy(rng.integers(-2, 3, (most, M)).astype(np.float32)).to(dtype).cuda()
+    dt = api._DTYPES[dtype]
+    ws = api.Workspace(_lib.tcq_decode_linear_workspace_bytes(dt, most, *w.shape))
+    wb = api.Workspace(_lib.tcq_decode_linear_backward_workspace_bytes(dt, most, *w.shape, True,
+                                                                       True, True))
+    for B in (most, 1025, 520, 513, 512, 300, 129, 128, 40, 3, 1):
+        y = w.linear(x[:B], workspace=ws)
+        assert torch.equal(y, (x[:B].double() @ w.W.t()).to(dtype))
+        xp = api.act_pack(x[:B])
+        xv = api.act_unpack(xp, F32).double()
+        dx, dw, db = w.backward(dy[:B], x=xp, workspace=wb)
+        g = dy[:B].double()
+        assert torch.equal(dx, (g @ w.W).to(dtype)) and torch.equal(dw, (g.t() @ xv).to(dtype))
+        assert torch.equal(db.double(), g.sum(0))

@@ -1366,23 +1366,28 @@ size_t linear_small_bytes(size_t size, int64_t N, int bt) {
 // where two share a compute unit (1000 x 2048 x 2048 as 64 x 128 and 128 x 128, both split: 39
 // and 34 us per call in bf16, 82 and 75 in fp32, where 256 workgroups take 86; 200 x 14336 x
 // 4096 in fp32: 330 and 268; 333 x 2048 x 2048: 30 and 32 in bf16, 51 and 51 in fp32).
+constexpr int64_t kCus = 256, kMostSplits = 16, kLeastSteps = 4;
+
+int64_t gemm_steps(size_t size, int64_t K, int terms) {
+    const int64_t step = gemm::kStepBytes / static_cast<int64_t>(size);
+    return (K + step - 1) / step * terms;
+}
+
 GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K, int terms) {
-    constexpr int64_t kCus = 256;
     const auto tiles = [&](int64_t ti, int64_t tj) {
         return ((I + ti - 1) / ti) * ((J + tj - 1) / tj);
     };
     const auto rounds = [&](int64_t n) { return static_cast<double>((n + kCus - 1) / kCus); };
     GemmPlan p{};
-    const int64_t step = gemm::kStepBytes / static_cast<int64_t>(size);
-    p.steps = static_cast<int>((K + step - 1) / step) * terms;
+    p.steps = static_cast<int>(gemm_steps(size, K, terms));
     p.part_ld = (J + 3) / 4 * 4;
     // n tiles with k split into about `most` workgroups
     const auto split = [&](int tile, int64_t n, int64_t most) {
         GemmPlan q = p;
         q.tile = tile;
         int64_t s = n > 0 ? most / n : 1;
-        if (s > q.steps / 4) s = q.steps / 4;
-        if (s > 16) s = 16;
+        if (s > q.steps / kLeastSteps) s = q.steps / kLeastSteps;
+        if (s > kMostSplits) s = kMostSplits;
         if (s < 1) s = 1;
         q.steps_per_split = static_cast<int>((q.steps + s - 1) / s);
         q.splits = q.steps_per_split > 0
@@ -1427,6 +1432,20 @@ GemmPlan gemm_plan(size_t size, int64_t I, int64_t J, int64_t K, int terms) {
     return best;
 }
 
+// Room for a product's shares: at least the plan's part_bytes, and never less for a larger I or
+// K, although a larger product may not be split at all, so that a workspace of one batch
+// serves every smaller one.  n tiles of 64 x 128 or 128 x 128 are split into at most 2 kCus or
+// kCus workgroups (2 kCus in fp32), so no plan's shares are larger than theirs.
+size_t gemm_shares(size_t size, int64_t I, int64_t J, int64_t K, int terms) {
+    const int64_t most = size == 2 ? kCus * 128 * 128 : 2 * kCus * 128 * 128;
+    static_assert(2 * kCus * 64 * 128 <= kCus * 128 * 128, "the larger of the two");
+    int64_t s = gemm_steps(size, K, terms) / kLeastSteps;
+    if (s > kMostSplits) s = kMostSplits;
+    if (s < 2) return 0;
+    const int64_t values = s * I * ((J + 3) / 4 * 4);
+    return static_cast<size_t>(values < most ? values : most) * sizeof(float);
+}
+
 LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N) {
     LinearLayout l{};
     l.ldn = static_cast<int64_t>(pad8(N));
@@ -1434,7 +1453,7 @@ LinearLayout linear_layout(size_t size, int64_t B, int64_t M, int64_t N) {
     l.rows = align_up(static_cast<size_t>(M) * l.ldn * size, 256);
     l.sums = l.rows + align_up(static_cast<size_t>(B) * l.ldn * size, 256);
     l.forward = gemm_plan(size, B, M, l.ldn, 1);
-    l.bytes = l.sums + align_up(l.forward.part_bytes, 256);
+    l.bytes = l.sums + align_up(gemm_shares(size, B, M, l.ldn, 1), 256);
     return l;
 }
 
@@ -1458,18 +1477,12 @@ LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bo
     l.part = off;
     if (dbias) off += align_up(static_cast<size_t>(slope_slabs(B, M)) * M * sizeof(float), 256);
     l.sums = off;  // (the two products run one after the other)
-    size_t sums = 0;
-    for (int t = 1; t <= (size == 2 ? 2 : 1); ++t) {
-        const GemmPlan gx = gemm_plan(size, B, l.ldn, M, t);
-        const GemmPlan gw = gemm_plan(size, l.ldm, l.ldn, B, t);
-        if (dx && gx.part_bytes > sums) sums = gx.part_bytes;
-        if (dw && gw.part_bytes > sums) sums = gw.part_bytes;
-        if (t == terms) {
-            l.dx = gx;
-            l.dw = gw;
-        }
-    }
-    off += align_up(sums, 256);
+    l.dx = gemm_plan(size, B, l.ldn, M, terms);
+    l.dw = gemm_plan(size, l.ldm, l.ldn, B, terms);
+    const int most = size == 2 ? 2 : 1;
+    const size_t gx = dx ? gemm_shares(size, B, l.ldn, M, most) : 0;
+    const size_t gw = dw ? gemm_shares(size, l.ldm, l.ldn, B, most) : 0;
+    off += align_up(gx > gw ? gx : gw, 256);
     l.bytes = off;
     return l;
 }
