@@ -483,7 +483,9 @@ struct SmallArgs {
 
 template <typename T, int BT, bool ONE>
 struct SmallShape {
-    // tiles held at a time, and units held per tile (by the registers)
+    // tiles held at a time, and units held per tile (by the registers: 1024 threads have 128
+    // each, and with a table of several parts the instances of fp32 above 32 rows (and one of
+    // 17 to 32) and of 16 bits up to 32 rows spill 2 to 18 of them, 27 of all 130)
     static constexpr int TR = ONE || sizeof(T) == 4 || BT > 2 ? 1 : 2;
     static constexpr int UN = ONE || (sizeof(T) == 4 && BT > 4) ? 1 : 2;
     // steps ahead that x is asked for (one less than a divisor of 4; by the registers)
@@ -982,15 +984,16 @@ int64_t slope_slabs(int64_t B, int64_t M) {
 
 template <typename T, int TERMS>
 const void *slope_kernel_of(int act) {
-    switch (act) {
-        case TCQ_ACT_RELU:
-            return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_RELU, TERMS>);
-        case TCQ_ACT_SILU:
+    // (silu and gelu take two terms of a 16-bit type)
+    if constexpr (sizeof(T) == 4 || TERMS == 2) {
+        if (act == TCQ_ACT_SILU)
             return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_SILU, TERMS>);
-        case TCQ_ACT_GELU:
+        if (act == TCQ_ACT_GELU)
             return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_GELU, TERMS>);
-        default: return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_NONE, TERMS>);
     }
+    if (act == TCQ_ACT_RELU)
+        return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_RELU, TERMS>);
+    return reinterpret_cast<const void *>(slope_kernel<T, TCQ_ACT_NONE, TERMS>);
 }
 
 // Terms of a 16-bit type that the scaled gradient is held in: one where it is dy itself or zero.
@@ -1120,9 +1123,9 @@ LayerEpilogue<T> layer_epilogue(const CodedMatrix &w, const LinearCall &c) {
 
 template <typename T, int BT, bool ONE>
 const void *small_kernel_of(int kv, int V) {
-// (a 16-bit table of V = 1 always fits one part)
-#define TCQ_SMALL_CASE(KV_, V_)                        \
-    if constexpr (ONE || V_ > 1 || sizeof(T) == 4)     \
+// (a 16-bit table of V = 1 always fits one part, and one of several goes up to 64 rows)
+#define TCQ_SMALL_CASE(KV_, V_)                                      \
+    if constexpr (ONE || sizeof(T) == 4 || (V_ > 1 && BT <= 4))      \
         if (kv == KV_ && V == V_)                      \
             return reinterpret_cast<const void *>(small_kernel<T, KV_, V_, BT, ONE>);
     TCQ_SMALL_CASE(1, 1)
