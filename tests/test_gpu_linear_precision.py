@@ -443,3 +443,17 @@ def test_one_workspace_for_all_batches(dtype):
         g = dy[:B].double()
         assert torch.equal(dx, (g @ w.W).to(dtype)) and torch.equal(dw, (g.t() @ xv).to(dtype))
         assert torch.equal(db.double(), g.sum(0))
+
+
+def test_workspace_of_another_device():
+    """A workspace in host memory is refused before the call."""
+    w = Coded(5, 64, 512, 16, 2, 1, 256, F16, True)
+    x = torch.ones(300, 512, dtype=F16, device="cuda")
+    dy = torch.ones(300, 64, dtype=F16, device="cuda")
+    ws = api.Workspace(1 << 24, "cpu")
+    with pytest.raises(AssertionError, match="workspace"):
+        w.linear(x, workspace=ws)
+    with pytest.raises(AssertionError, match="workspace"):
+        w.backward(dy, workspace=ws)
+    ws = api.Workspace(1 << 24)
+    assert torch.equal(w.linear(x, workspace=ws), w.linear(x))

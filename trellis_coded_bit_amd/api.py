@@ -201,6 +201,14 @@ def _rows(t: torch.Tensor, name: str, rows: int, cols: int, dtype: torch.dtype,
     return max(ld, 1)
 
 
+def _workspace(workspace: Workspace | None, device: torch.device) -> tuple[int | None, int]:
+    """Address and size of a call's workspace, which the tensors' device must hold."""
+    if workspace is None:
+        return None, 0
+    assert workspace.buf.device == device, f"workspace: on {device}"
+    return workspace.ptr, workspace.nbytes
+
+
 def _vector(t: torch.Tensor | None, name: str, n: int, device: torch.device) -> int | None:
     if t is None:
         return None
@@ -231,7 +239,8 @@ def decode_linear(bitstream: torch.Tensor, start_state: torch.Tensor, codebook: 
     """act(row_scale (x W_hat^T) + bias) + residual for x [B, N] in float32, float16 or
     bfloat16 and the coded matrix W_hat [M, N] (codebook in x's type); [B, M], or with
     ``pre`` the pair of it and the pre-activation.  act: none, relu, silu or gelu.  ``out``
-    may be ``residual``."""
+    may be ``residual``, but not overlap x.  The outputs carry no autograd graph, whatever x
+    requires: the gradients are decode_linear_backward's."""
     dev, dt = x.device, x.dtype
     assert x.is_cuda and x.dim() == 2 and dt in _DTYPES
     B = x.shape[0]
@@ -251,8 +260,7 @@ def decode_linear(bitstream: torch.Tensor, start_state: torch.Tensor, codebook: 
             None if residual is None else residual.data_ptr(),
             M if residual is None else _rows(residual, "residual", B, M, dt, dev),
             y.data_ptr(), ldy, None if z is None else z.data_ptr(), M,
-            None if workspace is None else workspace.ptr,
-            0 if workspace is None else workspace.nbytes, _stream_of(dev))
+            *_workspace(workspace, dev), _stream_of(dev))
     return y if z is None else (y, z)
 
 
@@ -345,7 +353,6 @@ def decode_linear_backward(bitstream: torch.Tensor, start_state: torch.Tensor,
                 x.codes.data_ptr() if x is not None else None, ldx,
                 x.scale.data_ptr() if x is not None else None,
                 None if gx is None else gx.data_ptr(), N, None if gw is None else gw.data_ptr(),
-                N, None if gb is None else gb.data_ptr(),
-                None if workspace is None else workspace.ptr,
-                0 if workspace is None else workspace.nbytes, _stream_of(dev))
+                N, None if gb is None else gb.data_ptr(), *_workspace(workspace, dev),
+                _stream_of(dev))
     return gx, gw, gb
