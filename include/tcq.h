@@ -412,7 +412,8 @@ int tcq_act_unpack(const int8_t *codes, int64_t ldq, const uint8_t *scale, int64
  * tcq_decode_linear names, at every B.
  *   dy, B, lddy : device, B x M of type dtype
  *   z_codes, ldz, z_scale : device checkpoint of z (B x M); not read with TCQ_ACT_NONE
- *   x_codes, ldx, x_scale : device checkpoint of x (B x N); read for dw only
+ *   x_codes, ldx, x_scale : device checkpoint of x (B x N); read for dw only, in the layer's
+ *                 type (fp16 rounds what a checkpoint of another type's values holds)
  *   dx, lddx    : nullable device out, B x N (bitstream, start_state and codebook are read
  *                 for dx only)
  *   dw, lddw    : nullable device out, M x N

@@ -470,8 +470,8 @@ __device__ __forceinline__ void gemm_tile(const Operand<T> &A, const Operand<T> 
 // the fp32 instruction makes.  (What is below 2^-133, bf16's smallest number, is lost, so numbers
 // below 2^-109 keep fewer bits.)  The operands stay fp32 in memory and LDS and are split in registers: about 50 VALU instructions
 // for a fragment, which meets FI or FJ others in six matrix instructions each.  VALU issue
-// bounds it: 70 % of the clocks at 4096^3 with 64 x 64 per wave, the matrix cores 52 %.  That
-// takes 0.79 ms (174 TFLOP/s); the fp32 instruction took 1.05 (its peak is 157 TFLOP/s), the
+// bounds it: 68 % of the clocks at 4096^3 with 64 x 64 per wave, the matrix cores 49 %.  A call
+// takes 0.81 ms (170 TFLOP/s); the fp32 instruction took 1.05 (its peak is 157 TFLOP/s), the
 // library's product 0.91.
 // An infinity has no such split (inf - inf, and inf times a zero term, are NaN), nor has a number
 // whose x0 would round to one.  A step that holds an infinity, a NaN or a magnitude from

@@ -9,7 +9,7 @@
 // its products read it through the matrix cores: rounded to one term, dx and dw were off by 1.4
 // times their own rounding, and in fp16 the row scale (about 1 / sqrt N) pushed small gradients
 // among the subnormals (11 % off at a gradient of 1e-5).  It costs a second pass over k
-// (4096 x 4096 x 4096: 220-257 us a product, 113-119 with one term).
+// (4096 x 4096 x 4096: 220-255 us a product, 113-119 with one term).
 #include <hip/hip_runtime.h>
 
 #include "checkpoint_device.h"
@@ -1001,8 +1001,9 @@ int grad_terms(const LinearGrad &c) {
     return c.row_scale || c.act == TCQ_ACT_SILU || c.act == TCQ_ACT_GELU ? 2 : 1;
 }
 
-// Compute units of the current device (asked on every call: devices of one process, such
-// as partitions of one GPU, need not have the same count).
+// Compute units of the current device, for grids whose workgroups share work in any number
+// (asked on every call: devices of one process, such as partitions of one GPU, need not have
+// the same count; gemm_plan's tiles and splits decide how sums are rounded, and do not ask).
 int cu_count() {
     int dev = 0, n = 0;
     if (hipGetDevice(&dev) == hipSuccess &&
@@ -1354,9 +1355,11 @@ size_t linear_small_bytes(size_t size, int64_t N, int bt) {
 // the 256 compute units of the part this library is built for), so the workspace query
 // and the call agree.
 //   64 x 128 tiles with two stages run three to a compute unit.  Where there are few, k is
-// split into about 512 workgroups (at least 4 steps each) and the shares, in fp32, are added
-// by a second kernel (512 x 4096 x 4096 in bf16: 57 us per call unsplit, 45 split; 160 rows: 40
-// and 32).
+// split into about 512 workgroups and the shares, in fp32, are added by a second kernel (512 x
+// 4096 x 4096 in bf16: 57 us per call unsplit, 45 split; 160 rows: 40 and 32).  A split has at
+// least 4 steps (with at least 2 / 4 / 8, bf16, in a graph: 300 x 1024 x 1024 18.0 / 15.3 / 15.8
+// us, 150 x 2048 x 512 14.4 / 13.8 / 14.8), and there are at most 16 (with 8 / 16 / 32: 200 x 256 x
+// 14336 34.3 / 29.2 / 30.9 us in bf16, 84 / 56 / 46 in fp32).
 //   16-bit types also have 256 x 256 tiles (the ring) and 128 x 128 ones (four stages), one
 // to a compute unit.  Tiles come in rounds of 256; what a round costs, once and per step of
 // k, was fitted to calls with all three forced on the same shapes, and the cheapest is taken
