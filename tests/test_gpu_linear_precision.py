@@ -457,3 +457,54 @@ def test_workspace_of_another_device():
         w.backward(dy, workspace=ws)
     ws = api.Workspace(1 << 24)
     assert torch.equal(w.linear(x, workspace=ws), w.linear(x))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_gradients_of_spread_row_scales(dtype):
+    """Row scales over 24 powers of two in one matrix."""
+    M, N, B = 300, 512, 60
+    rng = np.random.default_rng(21)
+    w = Coded(6, M, N, 16, 2, 1, 256, dtype, False)
+
+    def normal(*size):
+        return torch.from_numpy(rng.standard_normal(size)).to(dtype).cuda()
+    a = torch.from_numpy(rng.standard_normal(M) * 2.0 ** rng.integers(-18, 7, M)).float().cuda()
+    r = _gradients(w, normal(B, M), a, "gelu", normal(B, M), normal(B, N), dtype)
+    _say(f"spread row scales {dtype}: worst error / bound dx {r[0]:.3g}, dw {r[1]:.3g}")
+    assert max(r) <= 1
+
+
+@pytest.mark.parametrize("B", [5, 300])
+def test_row_scale_changes_between_replays(B):
+    """fp16 gradients in a captured graph: the power of two comes from the row scale of the
+    moment, and every replay equals the eager call."""
+    M, N, dtype = 384, 512, F16
+    w = Coded(4, M, N, 16, 2, 1, 256, dtype, False)
+    g = torch.Generator("cuda").manual_seed(B)
+
+    def normal(*size):
+        return torch.randn(*size, generator=g, device="cuda")
+    dy, a = normal(B, M).to(dtype), normal(M)
+    zp, xp = api.act_pack(normal(B, M).to(dtype)), api.act_pack(normal(B, N).to(dtype))
+
+    def step():
+        return w.backward(dy, row_scale=a, act="silu", z=zp, x=xp)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for size in (2.0 ** -12, 1.0, 3000.0, 2.0 ** -5):
+        a.copy_(normal(M) * size)
+        dy.copy_(normal(B, M) / max(size, 1.0))
+        want = step()
+        torch.cuda.synchronize()
+        assert bool(torch.isfinite(want[0]).all())
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for p, q in zip(outs, want):
+            assert torch.equal(p, q), size

@@ -6,7 +6,7 @@ import subprocess
 
 import pytest
 
-from trellis_coded_bit_amd import build
+from trellis_coded_bit_amd import _lib, build
 
 SIXTEEN = {"DF16_", "DF16b"}
 
@@ -14,6 +14,7 @@ SIXTEEN = {"DF16_", "DF16b"}
 def _instances(kernel):
     if not shutil.which("nm"):
         pytest.skip("nm is not here")
+    _lib.load()
     names = subprocess.run(["nm", build.LIB], capture_output=True, text=True, check=True).stdout
     found = set()
     for m in re.finditer(r"_ZN3tcq12_GLOBAL__N_1\d+(?:__device_stub__)?" + kernel +
