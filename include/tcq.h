@@ -349,13 +349,13 @@ typedef enum {
  *   workspace  : >= what tcq_decode_linear_workspace_bytes reports (never less for a larger
  *                B: a workspace of the largest batch serves every smaller one)
  * Outputs other than y == residual must not overlap inputs or one another (y or pre over x,
- * the residual or each other: TCQ_EINVAL).  Products of
- * 16-bit inputs are exact and sums fp32.  fp32 products are fp32 arithmetic for B <= 128 with
- * T a multiple of 32, kV <= 4 and V != 3; elsewhere each is the sum of six exact products of
- * bf16 terms, less than 2^-22 of it left out (numbers below 2^-109: to 2^-133).  z is not rounded
- * before the activation; act is evaluated in fp32 to 2^-20 of its value (2^-16 for 16-bit types)
- * where that is above 2^-119; each output is rounded once.  Repeated calls give identical results,
- * and a row of y depends on no other row of x, infinities and NaN in one included.
+ * the residual or each other: TCQ_EINVAL).  Products of 16-bit inputs are exact and sums fp32.
+ * fp32 products are fp32 arithmetic for B <= 128 with T a multiple of 32, kV <= 4 and V != 3;
+ * elsewhere each is the sum of six exact products of bf16 terms, less than 2^-22 of it left out
+ * (numbers below 2^-109: to 2^-133).  z is not rounded before the activation; act is evaluated
+ * in fp32, to 2^-20 of its value (2^-16 for 16-bit types) where that is above 2^-119; each
+ * output is rounded once.  Repeated calls give identical results, and a row of y depends on
+ * no other row of x, infinities and NaN in one included.
  * N == 0 gives z = bias; M == 0 or B == 0 is a no-op.
  * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED, TCQ_EWORKSPACE, TCQ_EHIP.
  */
@@ -405,11 +405,12 @@ int tcq_act_unpack(const int8_t *codes, int64_t ldq, const uint8_t *scale, int64
  *     dw[r][c] = sum_b s[b][r] x[b][c]         the gradient of W_hat (straight through to W)
  * relu's g is dy where z > 0, 0 where z <= 0 (whatever dy holds) and NaN where z is NaN.
  * The residual's gradient is dy itself.  Sums are fp32 in a fixed order; outputs of the
- * layer's type are rounded once.  act' is evaluated in fp32 to 2^-20 of its terms (2^-16 for
- * 16-bit types) where they are above 2^-119.  g and s are fp32; a 16-bit type's products read s as two
- * numbers of the type, within 2^-16 (bf16) or 2^-22 (fp16) of its value, in fp16 not below
- * 2^-34 of the largest |row_scale| (of 1 without).  fp32 products are those of bf16 terms that
- * tcq_decode_linear names, at every B.
+ * layer's type are rounded once.  act' is evaluated in fp32, to 2^-20 of its terms (2^-16 for
+ * 16-bit types) where they are above 2^-119.  g and s are fp32; a 16-bit type's products read s
+ * as two numbers of the type, within 2^-16 (bf16) or 2^-22 (fp16) of its value, in fp16 not
+ * below 2^-34 of the largest |row_scale| (of 1 without).  fp32 products are those of bf16
+ * terms that tcq_decode_linear names, at every B.  (With two numbers an infinite codebook entry
+ * gives NaN in dx where one gives an infinity.)
  *   dy, B, lddy : device, B x M of type dtype
  *   z_codes, ldz, z_scale : device checkpoint of z (B x M); not read with TCQ_ACT_NONE
  *   x_codes, ldx, x_scale : device checkpoint of x (B x N); read for dw only, in the layer's

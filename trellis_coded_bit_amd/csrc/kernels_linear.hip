@@ -2,9 +2,9 @@
 // rows x, with the trellis-coded matrix W_hat decoded inside the call, and its gradients.
 //
 // The matrix is decoded once into the workspace, in the layer's type, and multiplied on the
-// matrix cores (gemm_device.h); for few rows it is decoded inside the product.  With the table in the layer's own type a decoded weight is
-// a table entry copied bit for bit, so every product is exact and the sums are fp32: the
-// outputs' own rounding is the only one to 16 bits.  The backward pass holds the incoming
+// matrix cores (gemm_device.h); for few rows it is decoded inside the product.  With the table
+// in the layer's own type a decoded weight is a table entry copied bit for bit, so every
+// product is exact and the sums are fp32: the outputs' own rounding is the only one to 16 bits.  The backward pass holds the incoming
 // gradient times the activation's slope and the row scale in two terms of a 16-bit type, since
 // its products read it through the matrix cores: rounded to one term, dx and dw were off by 1.4
 // times their own rounding, and in fp16 the row scale (about 1 / sqrt N) pushed small gradients
@@ -1365,9 +1365,10 @@ size_t linear_small_bytes(size_t size, int64_t N, int bt) {
 // k, was fitted to calls with all three forced on the same shapes, and the cheapest is taken
 // (566 x 6912 x 2176 in bf16: 56 us per call with 64 x 128, 76 with 128 x 128, 70 with
 // 256 x 256; 2176 x 6912 x 576: 57, 72 and 40; 1024 x 4096 x 4096: 67, 63 and 99).
-//   fp32 has 128 x 128 ones with two stages, two to a compute unit, which split a fragment's values for twice as
-// many products but leave more of the card idle in a last round (566 x 6912 x 2176: 152 us
-// per call with 64 x 128, 200 with 128 x 128; 2176 x 6912 x 576: 145 and 127).
+//   fp32 has 128 x 128 ones with two stages, two to a compute unit, which split a fragment's
+// values for twice as many products but leave more of the card idle in a last round (566 x
+// 6912 x 2176: 152 us per call with 64 x 128, 200 with 128 x 128; 2176 x 6912 x 576: 145 and
+// 127).
 //   128 x 128 tiles are split over k too, into 256 workgroups of a 16-bit type and 512 in fp32,
 // where two share a compute unit (1000 x 2048 x 2048 as 64 x 128 and 128 x 128, both split: 39
 // and 34 us per call in bf16, 82 and 75 in fp32, where 256 workgroups take 86; 200 x 14336 x
