@@ -437,6 +437,105 @@ int tcq_decode_linear_backward(const uint32_t *bitstream, const uint32_t *start_
                                void *dw, int64_t lddw, float *dbias, void *workspace,
                                size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Microscaled operators: matrices whose rows are held in groups of 32 consecutive values (the
+ * last one may be shorter) that share one scale byte e for 2^(e - 127), with 4- or 8-bit floating
+ * point codes:
+ *   TCQ_FP4 (E2M1): 0, 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives (sign in bit 3), two codes to
+ *           a byte, the even column in the low four bits;
+ *   TCQ_FP8 (E4M3): sign, four exponent bits (bias 7), three mantissa bits; largest 448; a byte
+ *           of 0x7F or 0xFF is NaN (never written).
+ * A group's e is max(E - t, 0), E the exponent field of its largest magnitude as an fp32 number
+ * and t = 2 (fp4) or 8 (fp8); a value's code is the nearest of the format's to x 2^(127 - e), ties
+ * to even, clamped to +-6 or +-448.  A group with an infinity or a NaN gets e = 255 and stands
+ * for NaN throughout; a group of zeros gets e = 0.
+ * Rows of codes consist of whole groups (16 or 32 bytes each) whose codes behind the last
+ * column are zeros, and start on multiples of 16 bytes (address and leading dimension, in
+ * bytes); scale bytes are rows x ceil(cols / 32) without gaps.
+ */
+typedef enum { TCQ_FP4 = 0, TCQ_FP8 = 1 } tcq_mx_format;
+
+/*
+ * tcq_mx_pack
+ *   X, rows, cols, ldx : device input of type dtype, ldx >= cols
+ *   format             : tcq_mx_format
+ *   codes, ldq         : device out, rows of ceil(cols / 32) groups, ldq bytes apart
+ *   scale              : device out, rows x ceil(cols / 32) bytes
+ * tcq_mx_unpack
+ *   codes, ldq, scale  : as written by tcq_mx_pack
+ *   out, ldo           : device out of type dtype, ldo >= cols.  Values are exact in fp32, and in
+ *                        bf16 from 2^-133 on; fp16 holds those of fp16 inputs exactly and rounds
+ *                        others.
+ * Outputs that overlap inputs or one another are refused (TCQ_EINVAL).
+ * rows == 0 or cols == 0 is a no-op.
+ * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED (rows or cols above 2^31 - 1), TCQ_EHIP.
+ */
+int tcq_mx_pack(const void *X, int dtype, int64_t rows, int64_t cols, int64_t ldx, int format,
+                uint8_t *codes, int64_t ldq, uint8_t *scale, hipStream_t stream);
+int tcq_mx_unpack(const uint8_t *codes, int64_t ldq, const uint8_t *scale, int64_t rows,
+                  int64_t cols, int format, int dtype, void *out, int64_t ldo,
+                  hipStream_t stream);
+
+/*
+ * tcq_mx_linear -- y = xq W^T + bias + residual for B rows and the M x N matrix W of TCQ_FP4 codes:
+ *     y[b][r] = sum_c W[r][c] xq[b][c] + bias[r] + residual[b][r]
+ * with xq the values that x's codes stand for.
+ *   w_codes, ldw, w_scale : device, W as written by tcq_mx_pack (M x N, TCQ_FP4)
+ *   dtype      : type of x, residual and y
+ *   x, B, ldx  : nullable device, B x N: quantised to `format` inside the call, as tcq_mx_pack does
+ *   x_codes, ldxq, x_scale : with x, nullable (both or none) device out: its codes and scale bytes,
+ *                for the backward pass; without x, device input: xq itself
+ *   bias       : nullable device, M floats
+ *   residual   : nullable device, B x M, ldr >= M; may be y itself (with ldr == ldy)
+ *   y, ldy     : device out, B x M, ldy >= M
+ *   workspace  : >= what tcq_mx_linear_workspace_bytes reports (never less for a larger B)
+ * Outputs other than y == residual must not overlap inputs or one another (TCQ_EINVAL).
+ * Products are exact and sums fp32; y is rounded once.  (8-bit rows are multiplied as bf16
+ * numbers, which end at 2^-133: scale bytes below 3 lose some of the smallest codes.)  Repeated
+ * calls give identical results, and a row of y depends on no other row of x, NaN groups included.
+ * N == 0 gives y = bias + residual; M == 0 or B == 0 is a no-op.
+ * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED (the limits of the coded linear layer), TCQ_EWORKSPACE,
+ * TCQ_EHIP.
+ */
+int tcq_mx_linear_workspace_bytes(int format, int64_t B, int64_t M, int64_t N, size_t *bytes);
+int tcq_mx_linear(const uint8_t *w_codes, int64_t ldw, const uint8_t *w_scale, int64_t M,
+                  int64_t N, int dtype, const void *x, int64_t B, int64_t ldx, int format,
+                  uint8_t *x_codes, int64_t ldxq, uint8_t *x_scale, const float *bias,
+                  const void *residual, int64_t ldr, void *y, int64_t ldy, void *workspace,
+                  size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * tcq_mx_linear_backward -- gradients of tcq_mx_linear, straight through the quantisation of x:
+ *     dx[b][c] = sum_r dy[b][r] W[r][c]
+ *     dw[r][c] = sum_b dy[b][r] xq[b][c]         the gradient of W's values
+ *     dbias[r] = sum_b dy[b][r]
+ * The residual's gradient is dy itself.  Products of 16-bit types are exact, fp32 products those
+ * of bf16 terms that tcq_decode_linear names; sums are fp32 in a fixed order, and outputs of the
+ * layer's type are rounded once.  fp16 reads W and xq times a power of two that brings the
+ * largest of their values below 2^16: values below 2^-36 of it lose bits.  bf16 reads those below
+ * 2^-133 as zero.
+ *   dtype       : type of dy, dx and dw
+ *   dy, B, lddy : device, B x M
+ *   w_codes, ldw, w_scale  : device, W (read for dx only)
+ *   format, x_codes, ldxq, x_scale : device, xq as tcq_mx_linear keeps it (read for dw only)
+ *   dx, lddx    : nullable device out, B x N
+ *   dw, lddw    : nullable device out, M x N
+ *   dbias       : nullable device out, M floats
+ *   workspace   : >= what the workspace query reports for the same outputs (nonzero dx, dw,
+ *                 dbias: wanted; never less for a larger B)
+ * Outputs must not overlap inputs or one another (TCQ_EINVAL).
+ * B == 0 gives dw = 0 and dbias = 0, M == 0 gives dx = 0.  At least one output is wanted.
+ * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED, TCQ_EWORKSPACE, TCQ_EHIP.
+ */
+int tcq_mx_linear_backward_workspace_bytes(int dtype, int64_t B, int64_t M, int64_t N, int dx,
+                                           int dw, int dbias, size_t *bytes);
+int tcq_mx_linear_backward(const uint8_t *w_codes, int64_t ldw, const uint8_t *w_scale,
+                           int64_t M, int64_t N, int dtype, const void *dy, int64_t B,
+                           int64_t lddy, int format, const uint8_t *x_codes, int64_t ldxq,
+                           const uint8_t *x_scale, void *dx, int64_t lddx, void *dw,
+                           int64_t lddw, float *dbias, void *workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

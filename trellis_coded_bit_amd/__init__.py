@@ -22,6 +22,12 @@ from ._lib import (  # noqa: F401
     tcq_act_unpack,
     tcq_decode_linear_backward_workspace_bytes,
     tcq_decode_linear_backward,
+    tcq_mx_pack,
+    tcq_mx_unpack,
+    tcq_mx_linear_workspace_bytes,
+    tcq_mx_linear,
+    tcq_mx_linear_backward_workspace_bytes,
+    tcq_mx_linear_backward,
     tcq_encode,
     tcq_encode_timed,
     tcq_encode_workspace_bytes,

@@ -24,6 +24,7 @@ TCQ_ENOMEM = -5
 # tcq_dtype and tcq_act
 TCQ_F32, TCQ_F16, TCQ_BF16 = 0, 1, 2
 TCQ_ACT_NONE, TCQ_ACT_RELU, TCQ_ACT_SILU, TCQ_ACT_GELU = 0, 1, 2, 3
+TCQ_FP4, TCQ_FP8 = 0, 1  # tcq_mx_format
 
 EXPORTED = ("tcq_version", "tcq_last_error", "tcq_make_codebook",
             "tcq_encode_workspace_bytes", "tcq_encode_workspace_min_bytes", "tcq_encode",
@@ -33,7 +34,9 @@ EXPORTED = ("tcq_version", "tcq_last_error", "tcq_make_codebook",
             "tcq_l16_stream_probe_bytes", "tcq_l16_stream_probe",
             "tcq_decode_linear_workspace_bytes", "tcq_decode_linear", "tcq_act_pack",
             "tcq_act_unpack", "tcq_decode_linear_backward_workspace_bytes",
-            "tcq_decode_linear_backward")
+            "tcq_decode_linear_backward", "tcq_mx_pack", "tcq_mx_unpack",
+            "tcq_mx_linear_workspace_bytes", "tcq_mx_linear",
+            "tcq_mx_linear_backward_workspace_bytes", "tcq_mx_linear_backward")
 
 _lib = None
 
@@ -116,6 +119,21 @@ def load():
     lib.tcq_decode_linear_backward.argtypes = [vp, vp, vp, *shape, i32, vp, i64, i64, vp, i32,
                                                vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp,
                                                vp, sz, vp]
+    lib.tcq_mx_pack.restype = i32
+    lib.tcq_mx_pack.argtypes = [vp, i32, i64, i64, i64, i32, vp, i64, vp, vp]
+    lib.tcq_mx_unpack.restype = i32
+    lib.tcq_mx_unpack.argtypes = [vp, i64, vp, i64, i64, i32, i32, vp, i64, vp]
+    lib.tcq_mx_linear_workspace_bytes.restype = i32
+    lib.tcq_mx_linear_workspace_bytes.argtypes = [i32, i64, i64, i64, ctypes.POINTER(sz)]
+    lib.tcq_mx_linear.restype = i32
+    lib.tcq_mx_linear.argtypes = [vp, i64, vp, i64, i64, i32, vp, i64, i64, i32, vp, i64, vp, vp,
+                                  vp, i64, vp, i64, vp, sz, vp]
+    lib.tcq_mx_linear_backward_workspace_bytes.restype = i32
+    lib.tcq_mx_linear_backward_workspace_bytes.argtypes = [i32, i64, i64, i64, i32, i32, i32,
+                                                           ctypes.POINTER(sz)]
+    lib.tcq_mx_linear_backward.restype = i32
+    lib.tcq_mx_linear_backward.argtypes = [vp, i64, vp, i64, i64, i32, vp, i64, i64, i32, vp, i64,
+                                           vp, vp, i64, vp, i64, vp, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -324,3 +342,58 @@ def tcq_decode_linear_backward(bitstream: int | None, start_state: int | None,
                z_scale or None, x_codes or None, ldx, x_scale or None, dx or None, lddx,
                dw or None, lddw, dbias or None, workspace or None, workspace_bytes,
                stream or None))
+
+
+def tcq_mx_pack(X: int, dtype: int, rows: int, cols: int, ldx: int, format: int, codes: int,
+                ldq: int, scale: int, stream: int | None) -> None:
+    _check("tcq_mx_pack",
+           load().tcq_mx_pack(X, dtype, rows, cols, ldx, format, codes, ldq, scale,
+                              stream or None))
+
+
+def tcq_mx_unpack(codes: int, ldq: int, scale: int, rows: int, cols: int, format: int,
+                  dtype: int, out: int, ldo: int, stream: int | None) -> None:
+    _check("tcq_mx_unpack",
+           load().tcq_mx_unpack(codes, ldq, scale, rows, cols, format, dtype, out, ldo,
+                                stream or None))
+
+
+def tcq_mx_linear_workspace_bytes(format: int, B: int, M: int, N: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check("tcq_mx_linear_workspace_bytes",
+           load().tcq_mx_linear_workspace_bytes(format, B, M, N, ctypes.byref(b)))
+    return int(b.value)
+
+
+def tcq_mx_linear(w_codes: int, ldw: int, w_scale: int, M: int, N: int, dtype: int,
+                  x: int | None, B: int, ldx: int, format: int, x_codes: int | None, ldxq: int,
+                  x_scale: int | None, bias: int | None, residual: int | None, ldr: int, y: int,
+                  ldy: int, workspace: int | None, workspace_bytes: int,
+                  stream: int | None) -> None:
+    _check("tcq_mx_linear",
+           load().tcq_mx_linear(w_codes, ldw, w_scale, M, N, dtype, x or None, B, ldx, format,
+                                x_codes or None, ldxq, x_scale or None, bias or None,
+                                residual or None, ldr, y, ldy, workspace or None,
+                                workspace_bytes, stream or None))
+
+
+def tcq_mx_linear_backward_workspace_bytes(dtype: int, B: int, M: int, N: int, dx: bool,
+                                           dw: bool, dbias: bool) -> int:
+    b = ctypes.c_size_t(0)
+    _check("tcq_mx_linear_backward_workspace_bytes",
+           load().tcq_mx_linear_backward_workspace_bytes(dtype, B, M, N, int(dx), int(dw),
+                                                         int(dbias), ctypes.byref(b)))
+    return int(b.value)
+
+
+def tcq_mx_linear_backward(w_codes: int | None, ldw: int, w_scale: int | None, M: int, N: int,
+                           dtype: int, dy: int, B: int, lddy: int, format: int,
+                           x_codes: int | None, ldxq: int, x_scale: int | None, dx: int | None,
+                           lddx: int, dw: int | None, lddw: int, dbias: int | None,
+                           workspace: int | None, workspace_bytes: int,
+                           stream: int | None) -> None:
+    _check("tcq_mx_linear_backward",
+           load().tcq_mx_linear_backward(w_codes or None, ldw, w_scale or None, M, N, dtype, dy, B,
+                                         lddy, format, x_codes or None, ldxq, x_scale or None,
+                                         dx or None, lddx, dw or None, lddw, dbias or None,
+                                         workspace or None, workspace_bytes, stream or None))

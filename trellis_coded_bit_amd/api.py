@@ -356,3 +356,143 @@ def decode_linear_backward(bitstream: torch.Tensor, start_state: torch.Tensor,
                 N, None if gb is None else gb.data_ptr(), *_workspace(workspace, dev),
                 _stream_of(dev))
     return gx, gw, gb
+
+
+_FORMATS = {"fp4": _lib.TCQ_FP4, "fp8": _lib.TCQ_FP8}
+MX_GROUP = 32  # consecutive values of a row that share a scale byte
+
+
+def _group_bytes(format: str) -> int:
+    return 16 if format == "fp4" else 32
+
+
+@dataclass
+class MxPacked:
+    """A microscaled matrix [rows, cols] (see tcq_mx_pack)."""
+    codes: torch.Tensor  # uint8 [rows, ceil(cols / 32) * 16 ("fp4") or * 32 ("fp8")]
+    scale: torch.Tensor  # uint8 [rows, ceil(cols / 32)]
+    cols: int
+    format: str = "fp4"
+
+    def check(self, name: str, rows: int, cols: int, device: torch.device) -> int:
+        groups = -(-cols // MX_GROUP)
+        assert self.format in _FORMATS, f"{name}: format is none of {tuple(_FORMATS)}"
+        assert self.cols == cols, f"{name}: {self.cols} columns, not {cols}"
+        assert self.scale.device == device and self.scale.dtype == torch.uint8 and \
+            self.scale.shape == (rows, groups) and self.scale.is_contiguous(), \
+            f"{name}: scale bytes [{rows}, {groups}] on {device}"
+        return _rows(self.codes, name, rows, groups * _group_bytes(self.format), torch.uint8,
+                     device)
+
+
+def _mx_empty(rows: int, cols: int, format: str, device: torch.device) -> MxPacked:
+    groups = -(-cols // MX_GROUP)
+    return MxPacked(torch.empty((rows, groups * _group_bytes(format)), dtype=torch.uint8,
+                                device=device),
+                    torch.empty((rows, groups), dtype=torch.uint8, device=device), cols, format)
+
+
+def mx_pack(x: torch.Tensor, format: str = "fp4") -> MxPacked:
+    """x [rows, cols] (float32, float16 or bfloat16) in groups of 32 values with a power-of-two
+    scale each and 4-bit (E2M1, "fp4") or 8-bit (E4M3, "fp8") floating point codes."""
+    assert x.is_cuda and x.dim() == 2 and x.dtype in _DTYPES and format in _FORMATS
+    rows, cols = x.shape
+    ldx = _rows(x, "x", rows, cols, x.dtype, x.device)
+    with _on(x.device):
+        p = _mx_empty(rows, cols, format, x.device)
+        _lib.tcq_mx_pack(x.data_ptr(), _DTYPES[x.dtype], rows, cols, ldx, _FORMATS[format],
+                         p.codes.data_ptr(), p.codes.shape[1], p.scale.data_ptr(),
+                         _stream_of(x.device))
+    return p
+
+
+def mx_unpack(packed: MxPacked, dtype: torch.dtype) -> torch.Tensor:
+    """The values that a microscaled matrix stands for, [rows, cols] in float32, float16 or
+    bfloat16."""
+    assert packed.codes.is_cuda and packed.codes.dim() == 2 and dtype in _DTYPES
+    rows, cols, dev = packed.codes.shape[0], packed.cols, packed.codes.device
+    ldq = packed.check("packed", rows, cols, dev)
+    with _on(dev):
+        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+        _lib.tcq_mx_unpack(packed.codes.data_ptr(), ldq, packed.scale.data_ptr(), rows, cols,
+                           _FORMATS[packed.format], _DTYPES[dtype], out.data_ptr(), max(cols, 1),
+                           _stream_of(dev))
+    return out
+
+
+def mx_linear(x: torch.Tensor | MxPacked, w: MxPacked, bias: torch.Tensor | None = None,
+              residual: torch.Tensor | None = None, x_format: str = "fp8", keep: bool = False,
+              dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+              workspace: Workspace | None = None
+              ) -> torch.Tensor | tuple[torch.Tensor, MxPacked]:
+    """xq w^T + bias + residual for the microscaled matrix w [M, N] ("fp4"); [B, M].  x [B, N] in
+    float32, float16 or bfloat16 is quantised to ``x_format`` inside the call (with ``keep`` the
+    result is the pair of y and that MxPacked, which mx_linear_backward takes), or is an MxPacked
+    already, with ``dtype`` the output's type.  ``out`` may be ``residual``, but not overlap x.
+    The outputs carry no autograd graph."""
+    packed = isinstance(x, MxPacked)
+    first = x.codes if packed else x
+    dev = first.device
+    dt = dtype if packed else x.dtype
+    assert first.is_cuda and first.dim() == 2 and dt in _DTYPES and dtype in (None, dt)
+    assert w.format == "fp4" and w.codes.dim() == 2, "w: an fp4 matrix"
+    assert not (packed and keep), "keep: x is packed already"
+    B, M, N = first.shape[0], w.codes.shape[0], w.cols
+    ldw = w.check("w", M, N, dev)
+    format = x.format if packed else x_format
+    assert format in _FORMATS, f"x_format is none of {tuple(_FORMATS)}"
+    b = _vector(bias, "bias", M, dev)
+    with _on(dev):
+        q = x if packed else (_mx_empty(B, N, format, dev) if keep else None)
+        ldq = N if q is None else q.check("x", B, N, dev)
+        ldx = N if packed else _rows(x, "x", B, N, dt, dev)
+        y = torch.empty((B, M), dtype=dt, device=dev) if out is None else out
+        ldy = M if out is None else _rows(out, "out", B, M, dt, dev)
+        if workspace is None:
+            n = _lib.tcq_mx_linear_workspace_bytes(_FORMATS[format], B, M, N)
+            workspace = Workspace(n, dev) if n else None
+        _lib.tcq_mx_linear(
+            w.codes.data_ptr(), ldw, w.scale.data_ptr(), M, N, _DTYPES[dt],
+            None if packed else x.data_ptr(), B, ldx, _FORMATS[format],
+            None if q is None else q.codes.data_ptr(), ldq,
+            None if q is None else q.scale.data_ptr(), b,
+            None if residual is None else residual.data_ptr(),
+            M if residual is None else _rows(residual, "residual", B, M, dt, dev), y.data_ptr(),
+            ldy, *_workspace(workspace, dev), _stream_of(dev))
+    return (y, q) if keep else y
+
+
+def mx_linear_backward(dy: torch.Tensor, w: MxPacked, x: MxPacked | None = None, dx: bool = True,
+                       dbias: bool = True, workspace: Workspace | None = None
+                       ) -> tuple[torch.Tensor | None, torch.Tensor | None,
+                                  torch.Tensor | None]:
+    """Gradients (dx [B, N], dw [M, N], dbias [M]) of mx_linear from dy [B, M] and the quantised
+    input x (dw is computed where it is given), straight through the quantisation.  dw is the
+    gradient of w's values; the residual's gradient is dy."""
+    dev, dt = dy.device, dy.dtype
+    assert dy.is_cuda and dy.dim() == 2 and dt in _DTYPES
+    assert dx or dbias or x is not None, "no gradient is wanted"
+    assert w.format == "fp4" and w.codes.dim() == 2, "w: an fp4 matrix"
+    B, M, N = dy.shape[0], w.codes.shape[0], w.cols
+    lddy = _rows(dy, "dy", B, M, dt, dev)
+    ldw = w.check("w", M, N, dev)
+    ldq = N if x is None else x.check("x", B, N, dev)
+    with _on(dev):
+        gx = torch.empty((B, N), dtype=dt, device=dev) if dx else None
+        gw = torch.empty((M, N), dtype=dt, device=dev) if x is not None else None
+        gb = torch.empty(M, dtype=torch.float32, device=dev) if dbias else None
+        if workspace is None:
+            n = _lib.tcq_mx_linear_backward_workspace_bytes(_DTYPES[dt], B, M, N, dx,
+                                                            x is not None, dbias)
+            workspace = Workspace(n, dev) if n else None
+        # an output of no elements has no address and nothing to be written
+        if any(t is not None and t.numel() for t in (gx, gw, gb)):
+            _lib.tcq_mx_linear_backward(
+                w.codes.data_ptr(), ldw, w.scale.data_ptr(), M, N, _DTYPES[dt], dy.data_ptr(), B,
+                lddy, _FORMATS["fp8" if x is None else x.format],
+                None if x is None else x.codes.data_ptr(), ldq,
+                None if x is None else x.scale.data_ptr(), None if gx is None else gx.data_ptr(),
+                N, None if gw is None else gw.data_ptr(), N,
+                None if gb is None else gb.data_ptr(), *_workspace(workspace, dev),
+                _stream_of(dev))
+    return gx, gw, gb

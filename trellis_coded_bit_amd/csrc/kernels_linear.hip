@@ -15,6 +15,7 @@
 #include "checkpoint_device.h"
 #include "decode_device.h"
 #include "gemm_device.h"
+#include "linear_epilogue.h"
 #include "linear_device.h"
 #include "tcq.h"
 #include "tcq_internal.h"
@@ -218,125 +219,6 @@ __global__ __launch_bounds__(256) void stage_kernel(const T *__restrict__ x, int
     }
 }
 
-// ---------------------------------------------------------------- epilogues
-
-template <typename T>
-__device__ __forceinline__ void store4(T *p, int64_t j, int64_t J, bool vec, f32x4 v) {
-    struct alignas(4 * sizeof(T)) Four { T v[4]; } o;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o.v[e] = static_cast<T>(v[e]);
-    if (vec && j + 4 <= J) {
-        *reinterpret_cast<Four *>(p) = o;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (j + e < J) p[e] = o.v[e];
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ f32x4 load4(const T *p, int64_t j, int64_t J, bool vec) {
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (vec && j + 4 <= J) {
-        struct alignas(4 * sizeof(T)) Four { T v[4]; };
-        const Four o = *reinterpret_cast<const Four *>(p);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(o.v[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (j + e < J) v[e] = static_cast<float>(p[e]);
-    }
-    return v;
-}
-
-// y = act(scale s + bias) + residual, z = scale s + bias, in fp32, rounded once each.
-template <typename T>
-struct LayerEpilogue {
-    const float *scale;
-    const float *bias;
-    const T *res;
-    T *y;
-    T *pre;
-    int64_t ldr, ldy, ldp;
-    int64_t I, J;
-    int act;
-    int vec_y, vec_r, vec_p;  // four consecutive values are aligned
-
-    struct Column {
-        int64_t j;
-        f32x4 a, b;
-        __device__ __forceinline__ Column(const LayerEpilogue &e, int64_t j_) : j(j_) {
-            a = f32x4{1.f, 1.f, 1.f, 1.f};
-            b = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (e.scale && j < e.J) a = load4(e.scale + j, j, e.J, false);
-            if (e.bias && j < e.J) b = load4(e.bias + j, j, e.J, false);
-        }
-    };
-    __device__ __forceinline__ void put(const Column &c, int64_t i, f32x4 s) const {
-        if (i >= I || c.j >= J) return;
-        f32x4 z, o;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = __builtin_fmaf(c.a[e], s[e], c.b[e]);
-        if (pre) store4(pre + i * ldp + c.j, c.j, J, vec_p, z);
-        with_act(act, [&](auto a) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = act_value<decltype(a)::value, sizeof(T) == 4>(z[e]);
-        });
-        if (res) {
-            const f32x4 r = load4(res + i * ldr + c.j, c.j, J, vec_r);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] += r[e];
-        }
-        store4(y + i * ldy + c.j, c.j, J, vec_y, o);
-    }
-    __device__ __forceinline__ void put_one(int64_t i, int64_t j, float s) const {
-        if (i >= I || j >= J) return;
-        const float z = __builtin_fmaf(scale ? scale[j] : 1.0f, s, bias ? bias[j] : 0.0f);
-        if (pre) pre[i * ldp + j] = static_cast<T>(z);
-        float o = 0.0f;
-        with_act(act, [&](auto a) { o = act_value<decltype(a)::value, sizeof(T) == 4>(z); });
-        if (res) o += static_cast<float>(res[i * ldr + j]);
-        y[i * ldy + j] = static_cast<T>(o);
-    }
-};
-
-// The sums times 2^*exponent (NULL: 1), rounded once.
-template <typename T>
-struct PlainEpilogue {
-    T *y;
-    int64_t ldy, I, J;
-    int vec_y;
-    const int *exponent;
-    struct Column {
-        int64_t j;
-        int e;
-        __device__ __forceinline__ Column(const PlainEpilogue &p, int64_t j_)
-            : j(j_), e(p.exponent ? *p.exponent : 0) {}
-    };
-    __device__ __forceinline__ void put(const Column &c, int64_t i, f32x4 s) const {
-        if (i >= I || c.j >= J) return;
-        if constexpr (gemm::kLowShift<T> != 0) {
-#pragma unroll
-            for (int v = 0; v < 4; ++v) s[v] = __builtin_amdgcn_ldexpf(s[v], c.e);
-        }
-        store4(y + i * ldy + c.j, c.j, J, vec_y, s);
-    }
-};
-
-// One split's share of the sums over k, in fp32: part[split][i][j], rows of ld values.
-struct PartEpilogue {
-    float *part;
-    int64_t ld, I, J;
-    struct Column {
-        int64_t j;
-        __device__ __forceinline__ Column(const PartEpilogue &, int64_t j_) : j(j_) {}
-    };
-    __device__ __forceinline__ void put(const Column &c, int64_t i, f32x4 s) const {
-        if (i < I && c.j < J) *reinterpret_cast<f32x4 *>(part + i * ld + c.j) = s;
-    }
-};
-
 // ---------------------------------------------------------------- products
 
 template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, int NB, int TERMS,
@@ -385,21 +267,6 @@ __global__ __launch_bounds__(WI *WJ * 64) void gemm_kernel(Operand<T> A, Operand
         gemm::gemm_tile_f32<AKM, BKM, TI, TJ, WI, WJ>(A, B, i0, j0, s0, s1, st, epi);
     else
         gemm::gemm_tile<T, AKM, BKM, TI, TJ, WI, WJ, NB, TERMS>(A, B, i0, j0, s0, s1, st, epi);
-}
-
-// The splits' shares added in order, four values per thread, and handed to the epilogue.
-template <typename Epi>
-__global__ __launch_bounds__(256) void split_sum_kernel(const float *__restrict__ part, int splits,
-                                                        int64_t I, int64_t ld, Epi epi) {
-    const int64_t quads = ld / 4;
-    const int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (q >= I * quads) return;
-    const int64_t i = q / quads, j = (q - i * quads) * 4;
-    const float *p = part + i * ld + j;
-    f32x4 s = *reinterpret_cast<const f32x4 *>(p);
-    for (int v = 1; v < splits; ++v) s += *reinterpret_cast<const f32x4 *>(p + v * I * ld);
-    const typename Epi::Column col(epi, j);
-    epi.put(col, i, s);
 }
 
 template <typename T, bool AKM, bool BKM, int TI, int TJ, int WI, int WJ, int NB, int TERMS,
@@ -953,11 +820,6 @@ __global__ __launch_bounds__(256) void slab_sum_unpack_kernel(const float *__res
 
 // ---------------------------------------------------------------- host side
 
-template <typename T>
-bool four_aligned(const T *p, int64_t ld) {
-    return (reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T))) == 0 && ld % 4 == 0;
-}
-
 // Whether rows of p can be read 16 bytes at a time by the product: aligned, and the
 // contiguous extent a whole number of 16-byte pieces.
 bool sixteen_aligned(const void *p, int64_t ld, int64_t extent, size_t size) {
@@ -1321,6 +1183,81 @@ hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStre
     return hipSuccess;
 }
 
+// dx = dy W, dw = dy^T X and dbias = sum of dy's rows for dense W (M x ldn) and X (B x ldn), whose
+// columns past N are zeros.  dy is read where it lies if its rows are whole 16-byte pieces;
+// otherwise slope_kernel copies it on its way through the bias' sums.
+template <typename T>
+hipError_t dense_grad(const DenseGrad &c, char *ws, hipStream_t s) {
+    const DenseGradLayout lay = dense_grad_layout(sizeof(T), c.B, c.M, c.N, c.dx, c.dw, c.dbias);
+    const bool direct = sixteen_aligned(c.dy, c.lddy, c.M, sizeof(T));
+    T *copy = reinterpret_cast<T *>(ws + lay.grad);
+    T *out = direct || (!c.dx && !c.dw) ? nullptr : copy, *low = nullptr;
+    const T *S = direct ? static_cast<const T *>(c.dy) : copy;
+    const int64_t lds = direct ? c.lddy : lay.ldm, wide = direct ? c.M : lay.ldm;
+    const int64_t slabs = slope_slabs(c.B, c.M);
+    hipError_t e;
+    if (c.B > 0 && c.M > 0 && (out || c.dbias)) {
+        SlopeArgs a{};
+        a.dy = c.dy;
+        a.B = c.B;
+        a.M = c.M;
+        a.lddy = c.lddy;
+        a.ld = lay.ldm;
+        a.part = c.dbias ? reinterpret_cast<float *>(ws + lay.part) : nullptr;
+        a.rows_per_slab = (c.B + slabs - 1) / slabs;
+        void *args[] = {&a, &out, &low};
+        e = hipLaunchKernel(slope_kernel_of<T, 1>(TCQ_ACT_NONE),
+                            dim3(static_cast<unsigned>((lay.ldm / 8 + 63) / 64),
+                                 static_cast<unsigned>(slabs)),
+                            dim3(256), args, 0, s);
+        if (e != hipSuccess) return e;
+    }
+    if (c.dbias && c.M > 0) {
+        hipLaunchKernelGGL(slab_sum_kernel, dim3(static_cast<unsigned>((c.M + 63) / 64)),
+                           dim3(256), 0, s, reinterpret_cast<const float *>(ws + lay.part),
+                           c.B > 0 ? slabs : 0, c.M, c.dbias);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (c.dx && c.B > 0 && c.N > 0) {
+        const PlainEpilogue<T> epi{static_cast<T *>(c.dx), c.lddx, c.B, c.N,
+                                   four_aligned(static_cast<T *>(c.dx), c.lddx),
+                                   c.M > 0 ? c.w_exponent : nullptr};
+        const Operand<T> A{S, lds, c.B, c.M > 0 ? wide : 0};
+        const Operand<T> W{static_cast<const T *>(c.w), lay.ldn, lay.ldn, c.M};
+        e = launch_gemm<T, false, true, 1>(A, W, gemm_plan(sizeof(T), c.B, lay.ldn, c.M, 1), epi,
+                                           ws + lay.sums, s);
+        if (e != hipSuccess) return e;
+    }
+    if (c.dw && c.M > 0 && c.N > 0) {
+        const PlainEpilogue<T> epi{static_cast<T *>(c.dw), c.lddw, c.M, c.N,
+                                   four_aligned(static_cast<T *>(c.dw), c.lddw),
+                                   c.B > 0 ? c.x_exponent : nullptr};
+        const Operand<T> A{S, lds, wide, c.B};
+        const Operand<T> X{static_cast<const T *>(c.x), lay.ldn, lay.ldn, c.B};
+        e = launch_gemm<T, true, true, 1>(A, X, gemm_plan(sizeof(T), wide, lay.ldn, c.B, 1), epi,
+                                          ws + lay.sums, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <typename T>
+LayerEpilogue<T> dense_epilogue(const DenseProduct &c) {
+    LayerEpilogue<T> e{};
+    e.bias = c.bias;
+    e.res = static_cast<const T *>(c.residual);
+    e.y = static_cast<T *>(c.y);
+    e.ldr = c.ldr;
+    e.ldy = c.ldy;
+    e.I = c.B;
+    e.J = c.M;
+    e.act = TCQ_ACT_NONE;
+    e.vec_y = four_aligned(e.y, e.ldy);
+    e.vec_r = e.res && four_aligned(e.res, e.ldr);
+    return e;
+}
+
 template <typename T>
 hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStream_t s) {
     if constexpr (sizeof(T) == 2) {
@@ -1492,6 +1429,47 @@ LinearLayout linear_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bo
     off += align_up(gx > gw ? gx : gw, 256);
     l.bytes = off;
     return l;
+}
+
+hipError_t launch_dense_product(const DenseProduct &c, char *ws, hipStream_t s) {
+    const GemmPlan pl = gemm_plan(2, c.B, c.M, c.K, 1);
+    const Operand<__bf16> A{reinterpret_cast<const __bf16 *>(c.x), c.ldx, c.B, c.K};
+    const Operand<__bf16> W{reinterpret_cast<const __bf16 *>(c.w), c.ldw, c.M, c.K};
+    switch (c.dtype) {
+        case TCQ_F32:
+            return launch_gemm<__bf16, false, false, 1>(A, W, pl, dense_epilogue<float>(c), ws, s);
+        case TCQ_F16:
+            return launch_gemm<__bf16, false, false, 1>(A, W, pl, dense_epilogue<_Float16>(c), ws,
+                                                        s);
+        default:
+            return launch_gemm<__bf16, false, false, 1>(A, W, pl, dense_epilogue<__bf16>(c), ws,
+                                                        s);
+    }
+}
+
+DenseGradLayout dense_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bool dx, bool dw,
+                                  bool dbias) {
+    DenseGradLayout l{};
+    l.ldn = static_cast<int64_t>(pad8(N));
+    l.ldm = static_cast<int64_t>(pad8(M));
+    size_t off = 0;
+    l.grad = off;
+    if (dx || dw) off += align_up(static_cast<size_t>(B) * l.ldm * size, 256);
+    l.part = off;
+    if (dbias) off += align_up(static_cast<size_t>(slope_slabs(B, M)) * M * sizeof(float), 256);
+    l.sums = off;
+    const size_t gx = dx ? gemm_shares(size, B, l.ldn, M, 1) : 0;
+    const size_t gw = dw ? gemm_shares(size, l.ldm, l.ldn, B, 1) : 0;
+    l.bytes = off + align_up(gx > gw ? gx : gw, 256);
+    return l;
+}
+
+hipError_t launch_dense_grad(const DenseGrad &c, char *ws, hipStream_t s) {
+    switch (c.dtype) {
+        case TCQ_F32: return dense_grad<float>(c, ws, s);
+        case TCQ_F16: return dense_grad<_Float16>(c, ws, s);
+        default: return dense_grad<__bf16>(c, ws, s);
+    }
 }
 
 hipError_t launch_linear(const CodedMatrix &w, const LinearCall &c, char *ws, hipStream_t s) {

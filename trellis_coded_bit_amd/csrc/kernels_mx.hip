@@ -1,0 +1,200 @@
+// Microscaled quantisation (tcq_mx_pack, tcq_mx_unpack).  A group of 32 consecutive values of a
+// row has the scale byte e = max(E - t, 0), E the exponent field of its largest magnitude as an
+// fp32 number and t = 2 (E2M1) or 8 (E4M3), and each value the code nearest to x 2^(127 - e),
+// ties to even, clamped to 6 or 448.  Multiplying by a power of two is exact, so a code has one
+// rounding.  E = 255 (an infinity or a NaN) gives e = 255, which stands for NaN throughout.
+//   Both directions are bound by memory: one pass, eight values or 16 bytes of output a thread.
+#include <hip/hip_runtime.h>
+
+#include "checkpoint_device.h"
+#include "mx_device.h"
+#include "tcq_internal.h"
+
+namespace tcq {
+namespace {
+
+struct MxPackArgs {
+    const void *x;
+    int64_t cols, ldx;
+    Pieces ix;          // pieces of eight values, whole groups
+    uint8_t *codes;     // rows of ldq bytes, or NULL
+    int64_t ldq;
+    uint8_t *scale;     // rows x groups, or NULL
+    __bf16 *values;     // the values the codes stand for, rows of ldv, or NULL
+    int64_t ldv;
+};
+
+// Eight consecutive values per thread; four neighbouring lanes share a group.
+template <typename T, int FMT, bool SMALL>
+__global__ __launch_bounds__(256) void mx_pack_kernel(MxPackArgs a) {
+    const T *X = static_cast<const T *>(a.x);
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < a.ix.total;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        int64_t r;
+        uint32_t c;
+        split<SMALL>(i, a.ix.cpr, r, c);
+        const int64_t col = static_cast<int64_t>(c) * 8;
+        const int left = a.cols - col < 8 ? static_cast<int>(a.cols - col) : 8;  // may be <= 0
+        float x[8];
+        if (left == 8) {
+            const Packed<T> p = *reinterpret_cast<const Packed<T> *>(X + r * a.ldx + col);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = static_cast<float>(p.v[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = k < left ? static_cast<float>(X[r * a.ldx + col + k]) : 0.0f;
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t m = __float_as_uint(x[k]) & 0x7FFFFFFFu;
+            top = top > m ? top : m;
+        }
+        // (total and the grid are multiples of 4: a group's lanes are here together)
+        const int e = mx::scale_byte<FMT>(mx::group_top(top));
+        uint32_t w[2];
+        mx::encode8<FMT>(x, e, w);
+        if (a.codes) {
+            uint8_t *q = a.codes + r * a.ldq + static_cast<int64_t>(c) * mx::bytes<FMT>(8);
+            if constexpr (FMT == TCQ_FP4)
+                *reinterpret_cast<uint32_t *>(q) = w[0];
+            else
+                *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+        }
+        if (a.scale && (c & 3) == 0) a.scale[i >> 2] = static_cast<uint8_t>(e);
+        if (a.values) {
+            const float s = mx::scale_of(e);
+            uint32_t v[4];
+            mx::decode_word_bf16<FMT>(w[0], s, v);
+            if constexpr (FMT == TCQ_FP8) mx::decode_word_bf16<FMT>(w[1], s, v + 2);
+            *reinterpret_cast<uint4 *>(a.values + r * a.ldv + col) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
+}
+
+struct MxUnpackArgs {
+    const uint8_t *codes;
+    int64_t ldq;
+    const uint8_t *scale;
+    int64_t cols, ldo;
+    Pieces ix;          // pieces of 16 bytes of output
+    int64_t padded;     // columns cols .. padded - 1 become zeros
+    int shift;          // the values are multiplied by 2^shift
+    const int *shift_at;  // its address instead, or NULL
+};
+
+// 16 bytes of output per thread (8 values of a 16-bit type, 4 of fp32), stored past the caches.
+template <typename T, int FMT, bool SMALL>
+__device__ __forceinline__ void mx_unpack(const MxUnpackArgs &a, T *__restrict__ out,
+                                          uint32_t block, uint32_t blocks) {
+    constexpr int P = 16 / static_cast<int>(sizeof(T));
+    typedef uint32_t Store __attribute__((ext_vector_type(4), aligned(1)));
+    const int64_t groups = (a.cols + mx::kGroup - 1) / mx::kGroup;
+    const int shift = a.shift_at ? *a.shift_at : a.shift;
+    for (int64_t i = static_cast<int64_t>(block) * 256 + threadIdx.x; i < a.ix.total;
+         i += static_cast<int64_t>(blocks) * 256) {
+        int64_t r;
+        uint32_t c;
+        split<SMALL>(i, a.ix.cpr, r, c);
+        const int64_t col = static_cast<int64_t>(c) * P;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+        if (col < a.cols) {
+            // (whole groups of codes are there)
+            const uint8_t *q = a.codes + r * a.ldq + static_cast<int64_t>(c) * mx::bytes<FMT>(P);
+            const float s = mx::scale_of(a.scale[r * groups + c / (mx::kGroup / P)]);
+            if constexpr (FMT == TCQ_FP4 && P == 8) {
+                mx::decode_word<FMT>(*reinterpret_cast<const uint32_t *>(q), s, v);
+            } else if constexpr (FMT == TCQ_FP4) {
+                mx::decode_word<FMT>(*reinterpret_cast<const uint16_t *>(q), s, v);
+            } else {
+#pragma unroll
+                for (int h = 0; h < P / 4; ++h)
+                    mx::decode_word<FMT>(reinterpret_cast<const uint32_t *>(q)[h], s, v + 4 * h);
+            }
+        }
+        T *o = out + r * a.ldo + col;
+        struct alignas(16) Piece { T v[P]; } st;
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+            st.v[k] = static_cast<T>(
+                col + k < a.cols ? (sizeof(T) == 2 ? __builtin_amdgcn_ldexpf(v[k], shift) : v[k])
+                                 : 0.0f);
+        if (col + P <= a.padded) {
+            __builtin_nontemporal_store(__builtin_bit_cast(Store, st),
+                                        reinterpret_cast<Store *>(o));
+        } else {
+#pragma unroll
+            for (int k = 0; k < P; ++k)
+                if (col + k < a.padded) o[k] = st.v[k];
+        }
+    }
+}
+
+template <typename T, int FMT, bool SMALL>
+__global__ __launch_bounds__(256) void mx_unpack_kernel(MxUnpackArgs a, T *__restrict__ out) {
+    mx_unpack<T, FMT, SMALL>(a, out, blockIdx.x, gridDim.x);
+}
+
+unsigned grid_for(int64_t work, int64_t per) {
+    int64_t g = (work + per - 1) / per;
+    if (g > (1 << 20)) g = 1 << 20;
+    return static_cast<unsigned>(g < 1 ? 1 : g);
+}
+
+template <typename T, int FMT>
+hipError_t pack(MxPackArgs a, hipStream_t s) {
+    const auto kern = a.ix.total < (int64_t{1} << 32) ? mx_pack_kernel<T, FMT, true>
+                                                      : mx_pack_kernel<T, FMT, false>;
+    hipLaunchKernelGGL(kern, dim3(grid_for(a.ix.total, 256)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename T, int FMT>
+hipError_t unpack(const MxMatrix &m, int64_t rows, int64_t cols, void *out, int64_t ldo,
+                  int64_t padded, const int *shift_at, hipStream_t s) {
+    constexpr int64_t P = 16 / sizeof(T);
+    const int64_t cpr = (padded + P - 1) / P;
+    const MxUnpackArgs a{m.codes, m.ld,  m.scale, cols, ldo, {static_cast<uint32_t>(cpr), rows * cpr},
+                         padded,  0, shift_at};
+    const auto kern = a.ix.total < (int64_t{1} << 32) ? mx_unpack_kernel<T, FMT, true>
+                                                      : mx_unpack_kernel<T, FMT, false>;
+    hipLaunchKernelGGL(kern, dim3(grid_for(a.ix.total, 256)), dim3(256), 0, s, a,
+                       static_cast<T *>(out));
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx_pack(const void *X, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                          int format, uint8_t *codes, int64_t ldq, uint8_t *scale,
+                          uint16_t *values, int64_t ldv, hipStream_t s) {
+    const int64_t cpr = (cols + mx::kGroup - 1) / mx::kGroup * 4;
+    const MxPackArgs a{X,     cols, ldx, {static_cast<uint32_t>(cpr), rows * cpr},
+                       codes, ldq,  scale, reinterpret_cast<__bf16 *>(values), ldv};
+    const bool fp4 = format == TCQ_FP4;
+    switch (dtype) {
+        case TCQ_F32: return fp4 ? pack<float, TCQ_FP4>(a, s) : pack<float, TCQ_FP8>(a, s);
+        case TCQ_F16: return fp4 ? pack<_Float16, TCQ_FP4>(a, s) : pack<_Float16, TCQ_FP8>(a, s);
+        default: return fp4 ? pack<__bf16, TCQ_FP4>(a, s) : pack<__bf16, TCQ_FP8>(a, s);
+    }
+}
+
+hipError_t launch_mx_unpack(const MxMatrix &m, int64_t rows, int64_t cols, int dtype, void *out,
+                            int64_t ldo, int64_t padded, const int *shift_at, hipStream_t s) {
+    const bool fp4 = m.format == TCQ_FP4;
+#define TCQ_UNPACK(T)                                                                     \
+    (fp4 ? unpack<T, TCQ_FP4>(m, rows, cols, out, ldo, padded, shift_at, s)               \
+         : unpack<T, TCQ_FP8>(m, rows, cols, out, ldo, padded, shift_at, s))
+    switch (dtype) {
+        case TCQ_F32: return TCQ_UNPACK(float);
+        case TCQ_F16: return TCQ_UNPACK(_Float16);
+        default: return TCQ_UNPACK(__bf16);
+    }
+#undef TCQ_UNPACK
+}
+
+}  // namespace tcq

@@ -1,0 +1,832 @@
+// The microscaled linear layer: y = xq W^T + bias + residual for a matrix W of 4-bit codes and
+// rows xq quantised to 4 or 8 bits, and its gradients.
+//
+// A product of two E2M1 codes is a multiple of 1/4 below 37, so the matrix instruction that
+// takes both operands as codes with their scale bytes adds a group's 32 products exactly, and the
+// groups in fp32.  Its E4M3 form does not: it aligns eight products to the largest and drops
+// what lies 2^-13 below (256 + 2^-6 gives 256), so 8-bit rows are multiplied as bf16 numbers,
+// which hold every code times its scale, with exact products and fp32 sums.
+#include <hip/hip_runtime.h>
+
+#include "gemm_device.h"
+#include "linear_epilogue.h"
+#include "mx_device.h"
+#include "tcq.h"
+#include "tcq_internal.h"
+
+namespace tcq {
+namespace gemm {
+
+// Two 4-bit codes: k is counted in bytes, 128 to a step, and a fragment is a group of a row.
+struct CodePair {
+    uint8_t b;
+};
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+template <>
+struct Traits<CodePair> {
+    static constexpr int kStep = 128;
+    static constexpr int kSub = 2;  // 128 codes each
+    using Frag = i32x4;
+};
+
+}  // namespace gemm
+
+namespace {
+
+using gemm::CodePair;
+using gemm::i32x4;
+using gemm::i32x8;
+using gemm::Operand;
+using gemm::s16x8;
+
+__device__ __forceinline__ i32x8 wide(const i32x4 &v) {
+    return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
+}
+
+// c += codes of a and b, a's scale in byte OA of sa and b's in byte OB of sb (16 rows of 128
+// codes each: lane l holds group l / 16 of row l % 16 of either, and the group's scale).
+template <int OA, int OB>
+__device__ __forceinline__ f32x4 mma_fp4(const i32x4 &a, uint32_t sa, const i32x4 &b, uint32_t sb,
+                                         const f32x4 &c) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(a), wide(b), c, 4, 4, OA,
+                                                            static_cast<int>(sa), OB,
+                                                            static_cast<int>(sb));
+}
+// The same for bytes known once the loops around are unrolled.
+__device__ __forceinline__ f32x4 mma_fp4_at(int oa, int ob, const i32x4 &a, uint32_t sa,
+                                            const i32x4 &b, uint32_t sb, const f32x4 &c) {
+    switch (oa * 4 + ob) {
+#define TCQ_AT(A, B) \
+    case A * 4 + B: return mma_fp4<A, B>(a, sa, b, sb, c);
+#define TCQ_ROW(A) TCQ_AT(A, 0) TCQ_AT(A, 1) TCQ_AT(A, 2) TCQ_AT(A, 3)
+        TCQ_ROW(0) TCQ_ROW(1) TCQ_ROW(2) TCQ_ROW(3)
+#undef TCQ_ROW
+#undef TCQ_AT
+    }
+    return c;
+}
+
+// ---------------------------------------------------------------- large batches, 4-bit rows
+
+// Scale bytes in the order in which the product's lanes take them: 128 rows by one step (eight
+// groups) are 1 KiB, lane l's 16 bytes at 16 l hold, for row 16 f + l % 16 of the tile, f = 0
+// .. 7, groups l / 16 and 4 + l / 16 of the step in bytes 2 f and 2 f + 1.  So a wave reads
+// a step's scales in one contiguous access per operand.  Rows and groups past the end get 1.
+struct ScaleArgs {
+    const uint8_t *scale;
+    int64_t rows, groups;
+    int64_t steps;
+    uint8_t *out;
+    int64_t lanes;   // 64 x tiles x steps
+};
+__device__ __forceinline__ void order_scales(const ScaleArgs &a, int64_t q) {
+    const int lane = static_cast<int>(q & 63);
+    const int64_t ts = q >> 6;
+    const int64_t tile = ts / a.steps, step = ts - tile * a.steps;
+    const int64_t g0 = step * 8 + (lane >> 4), row0 = tile * 128 + (lane & 15);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int f = 0; f < 8; ++f) {
+        const int64_t row = row0 + 16 * f;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            const int64_t g = g0 + 4 * ks;
+            const uint32_t e =
+                row < a.rows && g < a.groups ? a.scale[row * a.groups + g] : 127u;
+            w[f / 2] |= e << (8 * (2 * (f % 2) + ks));
+        }
+    }
+    reinterpret_cast<uint4 *>(a.out)[q] = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__global__ __launch_bounds__(256) void order_scales_kernel(ScaleArgs x, ScaleArgs w) {
+    const int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (q < x.lanes)
+        order_scales(x, q);
+    else if (q - x.lanes < w.lanes)
+        order_scales(w, q - x.lanes);
+}
+
+// The ordered scales of N fragments (16 rows each) of one operand, from row r0 on.
+template <int F>
+struct ScaleReader {
+    static constexpr int kWords = F / 2;
+    const char *base;   // this lane's bytes at step 0
+    __device__ __forceinline__ ScaleReader(const uint8_t *scales, int64_t r0, int64_t steps,
+                                           int lane) {
+        base = reinterpret_cast<const char *>(scales) + (r0 / 128) * steps * 1024 + lane * 16 +
+               (r0 % 128) / 8;
+    }
+    __device__ __forceinline__ void read(int s, uint32_t (&w)[kWords]) const {
+        if constexpr (kWords == 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(base + s * 1024ll);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2 *>(base + s * 1024ll);
+            w[0] = v.x, w[1] = v.y;
+        }
+    }
+};
+
+// A TI x TJ tile of A B^T over the steps s_begin .. s_end - 1 of 256 codes, as gemm_tile's (loads
+// straight into LDS, NB stages or a ring of five pieces, phases of half a wave's rows), with
+// the scales of the step to come read from memory into registers.
+template <int TI, int TJ, int WI, int WJ, int NB, typename Epi>
+__device__ __forceinline__ void mx_tile(const Operand<CodePair> &A, const uint8_t *as,
+                                        const Operand<CodePair> &B, const uint8_t *bs,
+                                        int64_t steps, int64_t i0, int64_t j0, int s_begin,
+                                        int s_end, const gemm::Stages<NB> &st, const Epi &epi) {
+    constexpr int NT = WI * WJ * 64;
+    constexpr int FI = TI / WI / 16, FJ = TJ / WJ / 16, FH = FI / 2;
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wi = wave / WJ, wj = wave % WJ;
+    gemm::TileLoader<CodePair, false, TI, NT> la;
+    gemm::TileLoader<CodePair, false, TJ, NT> lb;
+    la.init(A, i0, tid);
+    lb.init(B, j0, tid);
+    const gemm::FragReader<CodePair, false, TI> ra{lane, wi * FI * 16};
+    const gemm::FragReader<CodePair, false, TJ> rb{lane, wj * FJ * 16};
+    const ScaleReader<FI> rsa(as, i0 + wi * FI * 16, steps, lane);
+    const ScaleReader<FJ> rsb(bs, j0 + wj * FJ * 16, steps, lane);
+    f32x4 acc[FI][FJ];
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    i32x4 fa[2][FH], fb[2][FJ];
+    uint32_t sa[FI / 2], sb[FJ / 2], na_s[FI / 2], nb_s[FJ / 2];
+    auto read_phase = [&](const char *ta, const char *tb, int ph) {
+        const int ks = ph / 2, half = ph % 2;
+        if (half == 0) {
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) fb[ks % 2][j] = rb.read(tb, j, ks);
+        }
+#pragma unroll
+        for (int i = 0; i < FH; ++i) fa[ph % 2][i] = ra.read(ta, half * FH + i, ks);
+    };
+    auto mul_phase = [&](int ph) {
+        const int ks = ph / 2, half = ph % 2;
+#pragma unroll
+        for (int i = 0; i < FH; ++i)
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) {
+                const int fi = half * FH + i;
+                f32x4 &c = acc[fi][j];
+                c = mma_fp4_at(2 * (j % 2) + ks, 2 * (fi % 2) + ks, fb[ks % 2][j], sb[j / 2],
+                               fa[ph % 2][i], sa[fi / 2], c);
+            }
+    };
+    constexpr int kPhases = 4;
+    constexpr int kLoadsA = decltype(la)::kLoads, kLoadsB = decltype(lb)::kLoads;
+    auto valid = [&](int s) { return s < s_end ? s : gemm::kPastEnd; };
+    auto clamped = [&](int s) { return s < s_end ? s : s_end - 1; };
+    auto next_scales = [&](int s) {
+        rsa.read(clamped(s), na_s);
+        rsb.read(clamped(s), nb_s);
+    };
+    auto take_scales = [&] {
+#pragma unroll
+        for (int i = 0; i < FI / 2; ++i) sa[i] = na_s[i];
+#pragma unroll
+        for (int j = 0; j < FJ / 2; ++j) sb[j] = nb_s[j];
+    };
+    if (s_begin < s_end) {
+        next_scales(s_begin);
+        if constexpr (NB == gemm::kRing) {
+            auto step = [&](int s, auto turn) {
+                constexpr int t = 2 * decltype(turn)::value;
+                char *ta = st.p[t % 5], *tb = st.p[(t + 1) % 5];
+                const char *na = st.p[(t + 2) % 5], *nb = st.p[(t + 3) % 5];
+                take_scales();
+                next_scales(s + 1);
+                la.load(st.p[(t + 4) % 5], valid(s + 2), tid);
+#pragma unroll
+                for (int ph = 0; ph + 1 < kPhases; ++ph) {
+                    read_phase(ta, tb, ph + 1);
+                    mul_phase(ph);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                gemm::meet<kLoadsA>();
+                lb.load(ta, valid(s + 2), tid);
+                read_phase(na, nb, 0);
+                mul_phase(kPhases - 1);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            la.load(st.p[0], s_begin, tid);
+            lb.load(st.p[1], s_begin, tid);
+            la.load(st.p[2], valid(s_begin + 1), tid);
+            lb.load(st.p[3], valid(s_begin + 1), tid);
+            gemm::meet<kLoadsA + kLoadsB>();
+            read_phase(st.p[0], st.p[1], 0);
+            for (int s = s_begin; s < s_end; s += 5) {
+                step(s, std::integral_constant<int, 0>{});
+                if (s + 1 < s_end) step(s + 1, std::integral_constant<int, 1>{});
+                if (s + 2 < s_end) step(s + 2, std::integral_constant<int, 2>{});
+                if (s + 3 < s_end) step(s + 3, std::integral_constant<int, 3>{});
+                if (s + 4 < s_end) step(s + 4, std::integral_constant<int, 4>{});
+            }
+        } else {
+            auto step = [&](int s, char *ta, char *tb, const char *na, const char *nb) {
+                take_scales();
+                next_scales(s + 1);
+#pragma unroll
+                for (int ph = 0; ph + 1 < kPhases; ++ph) {
+                    read_phase(ta, tb, ph + 1);
+                    mul_phase(ph);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                gemm::meet<(NB - 2) * (kLoadsA + kLoadsB)>();
+                la.load(ta, valid(s + NB), tid);
+                lb.load(tb, valid(s + NB), tid);
+                read_phase(na, nb, 0);
+                mul_phase(kPhases - 1);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+#pragma unroll
+            for (int t = 0; t < NB; ++t) {
+                la.load(st.a[t], valid(s_begin + t), tid);
+                lb.load(st.b[t], valid(s_begin + t), tid);
+            }
+            gemm::meet<(NB - 1) * (kLoadsA + kLoadsB)>();
+            read_phase(st.a[0], st.b[0], 0);
+            for (int s = s_begin; s < s_end; s += NB) {
+#pragma unroll
+                for (int t = 0; t < NB; ++t)
+                    step(s + t, st.a[t], st.b[t], st.a[(t + 1) % NB], st.b[(t + 1) % NB]);
+            }
+        }
+        gemm::meet<0>();  // no load into LDS outlives the tile
+    }
+    static_assert(WI * WJ * FJ * 1024 <= TI * gemm::kStepBytes, "the waves' pieces fit the buffer");
+    gemm::hand_out(acc, st.a[0] + wave * (FJ * 1024), lane, i0 + wi * FI * 16, j0 + wj * FJ * 16,
+                   epi);
+}
+
+template <int TI, int TJ, int WI, int WJ, int NB, typename Epi>
+__global__ __launch_bounds__(WI *WJ * 64) void mx_gemm_kernel(Operand<CodePair> A,
+                                                              const uint8_t *as,
+                                                              Operand<CodePair> B,
+                                                              const uint8_t *bs, int steps,
+                                                              int steps_per_split, Epi epi,
+                                                              uint32_t ni, uint32_t nj) {
+    static_assert(NB == 4 || NB == gemm::kRing, "stages");
+    __shared__ __align__(16) char a0[TI * gemm::kStepBytes];
+    __shared__ __align__(16) char a1[TI * gemm::kStepBytes];
+    __shared__ __align__(16) char a2[TI * gemm::kStepBytes];
+    __shared__ __align__(16) char b0[TJ * gemm::kStepBytes];
+    __shared__ __align__(16) char b1[TJ * gemm::kStepBytes];
+    gemm::Stages<NB> st;
+    st.a[0] = a0;
+    if constexpr (NB == gemm::kRing) {
+        static_assert(TI == TJ, "pieces of one size");
+        st.p[0] = a0, st.p[1] = b0, st.p[2] = a1, st.p[3] = b1, st.p[4] = a2;
+    } else {
+        __shared__ __align__(16) char a3[TI * gemm::kStepBytes];
+        __shared__ __align__(16) char b2[TJ * gemm::kStepBytes];
+        __shared__ __align__(16) char b3[TJ * gemm::kStepBytes];
+        st.a[1] = a1, st.a[2] = a2, st.a[3] = a3;
+        st.b[0] = b0, st.b[1] = b1, st.b[2] = b2, st.b[3] = b3;
+    }
+    uint32_t ti, tj;
+    gemm::tile_of(blockIdx.x, ni, nj, ti, tj);
+    const int s0 = blockIdx.y * steps_per_split;
+    const int s1 = s0 + steps_per_split < steps ? s0 + steps_per_split : steps;
+    if constexpr (__is_same(Epi, PartEpilogue))
+        epi.part += static_cast<int64_t>(blockIdx.y) * epi.I * epi.ld;
+    mx_tile<TI, TJ, WI, WJ, NB>(A, as, B, bs, steps, static_cast<int64_t>(ti) * TI,
+                                static_cast<int64_t>(tj) * TJ, s0, s1, st, epi);
+}
+
+// ---------------------------------------------------------------- few rows of x
+
+// y for at most 16 BT rows of x: a workgroup of 16 waves takes 16 rows of W, whose columns the
+// waves share in units of 128 (four groups, one to each 16 lanes).  W is read once, 16 bytes a
+// lane, straight into the matrix instruction's operand: as codes with 4-bit rows; with 8-bit
+// ones a group's 32 codes become four bf16 fragments, fragment j holding columns 8 j .. 8 j + 7
+// of the lane's group, which is another order of k than memory's and the same for both operands.
+//   DENSE: x comes as it is (few values) and is quantised into LDS by every workgroup, in the
+// form the products read.  The waves' sums meet in LDS and are added in wave order.
+constexpr int kMxWaves = 16;
+constexpr int kMxUnits = 4;   // units of a wave's loads in flight
+
+struct MxSmallArgs {
+    const uint8_t *w, *ws;
+    int64_t ldw;
+    int64_t M;
+    int N, groups, units;
+    const void *x;
+    int64_t ldx;
+    const uint8_t *xq, *xs;
+    int64_t ldq;
+    int B;
+    int ldl;       // bytes of a row of x in LDS (DENSE)
+};
+
+template <typename T, int FMT, int BT, bool DENSE>
+__global__ __launch_bounds__(kMxWaves * 64) void mx_small_kernel(MxSmallArgs a,
+                                                                 LayerEpilogue<T> epi) {
+    extern __shared__ __align__(16) char lds[];
+    const int tid = threadIdx.x;
+    const int lane = tid & 63, l16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * 16;
+    const int64_t row = j0 + l16 < a.M ? j0 + l16 : a.M - 1;
+    const uint8_t *wr = a.w + row * a.ldw;
+    const uint8_t *wsr = a.ws + row * a.groups;
+    const int u0 = wave * a.units / kMxWaves, u1 = (wave + 1) * a.units / kMxWaves;
+    i32x4 wc[kMxUnits];
+    uint32_t we[kMxUnits];
+    // (groups past the end: codes of zero, a scale of 1)
+    auto load_w = [&](int u, i32x4 &c, uint32_t &e) {
+        const int grp = u * 4 + g;
+        const bool in = u < u1 && grp < a.groups;
+        c = i32x4{0, 0, 0, 0};
+        e = 127;
+        if (in) {
+            c = *reinterpret_cast<const i32x4 *>(wr + grp * 16);
+            e = wsr[grp];
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < kMxUnits; ++k) load_w(u0 + k, wc[k], we[k]);
+    char *xscale = lds + a.B * a.ldl;  // (DENSE, 4-bit: scale bytes, units x 4 to a row)
+    if constexpr (DENSE) {
+        // four lanes to a group; groups up to whole units
+        const int per = a.units * 16;
+        const T *X = static_cast<const T *>(a.x);
+        for (int i = tid; i < a.B * per; i += kMxWaves * 64) {
+            const int r = i / per, c = i - r * per;
+            const int left = a.N - c * 8;  // may be <= 0
+            float v[8];
+            if (left >= 8) {
+                const Packed<T> p = *reinterpret_cast<const Packed<T> *>(X + r * a.ldx + c * 8);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = static_cast<float>(p.v[k]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    v[k] = k < left ? static_cast<float>(X[r * a.ldx + c * 8 + k]) : 0.0f;
+            }
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t m = __float_as_uint(v[k]) & 0x7FFFFFFFu;
+                top = top > m ? top : m;
+            }
+            const int e = mx::scale_byte<FMT>(mx::group_top(top));
+            uint32_t q[2];
+            mx::encode8<FMT>(v, e, q);
+            if constexpr (FMT == TCQ_FP4) {
+                *reinterpret_cast<uint32_t *>(lds + r * a.ldl + c * 4) = q[0];
+                if ((c & 3) == 0) xscale[r * a.units * 4 + (c >> 2)] = static_cast<char>(e);
+            } else {
+                uint32_t o[4];
+                mx::decode_word_bf16<FMT>(q[0], mx::scale_of(e), o);
+                mx::decode_word_bf16<FMT>(q[1], mx::scale_of(e), o + 2);
+                *reinterpret_cast<uint4 *>(lds + r * a.ldl + c * 16) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        __syncthreads();
+    }
+    f32x4 acc[BT];
+#pragma unroll
+    for (int b = 0; b < BT; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](int u, const i32x4 &c, uint32_t e) {
+        const int grp = u * 4 + g;
+        if constexpr (FMT == TCQ_FP4) {
+#pragma unroll
+            for (int b = 0; b < BT; ++b) {
+                const int r = b * 16 + l16;
+                i32x4 xc = {0, 0, 0, 0};
+                uint32_t xe = 127;
+                if (r < a.B && grp < a.groups) {
+                    if constexpr (DENSE) {
+                        xc = *reinterpret_cast<const i32x4 *>(lds + r * a.ldl + grp * 16);
+                        xe = static_cast<uint8_t>(xscale[r * a.units * 4 + grp]);
+                    } else {
+                        xc = *reinterpret_cast<const i32x4 *>(a.xq + r * a.ldq + grp * 16);
+                        xe = a.xs[static_cast<int64_t>(r) * a.groups + grp];
+                    }
+                }
+                acc[b] = mma_fp4<0, 0>(c, e, xc, xe, acc[b]);
+            }
+        } else {
+            s16x8 wf[4];
+            const float s = mx::scale_of(static_cast<int>(e));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t o[4];
+                mx::decode_word_bf16<TCQ_FP4>(static_cast<uint32_t>(c[j]), s, o);
+                wf[j] = __builtin_bit_cast(s16x8, (i32x4{static_cast<int>(o[0]), static_cast<int>(o[1]),
+                                                        static_cast<int>(o[2]), static_cast<int>(o[3])}));
+            }
+#pragma unroll
+            for (int b = 0; b < BT; ++b) {
+                const int r = b * 16 + l16;
+                s16x8 xf[4];
+                if constexpr (DENSE) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        xf[j] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+                        if (r < a.B)
+                            xf[j] = *reinterpret_cast<const s16x8 *>(lds + r * a.ldl + grp * 64 +
+                                                                     j * 16);
+                    }
+                } else {
+                    i32x4 x0 = {0, 0, 0, 0}, x1 = x0;
+                    int xe = 127;
+                    if (r < a.B && grp < a.groups) {
+                        const uint8_t *p = a.xq + r * a.ldq + grp * 32;
+                        x0 = *reinterpret_cast<const i32x4 *>(p);
+                        x1 = *reinterpret_cast<const i32x4 *>(p + 16);
+                        xe = a.xs[static_cast<int64_t>(r) * a.groups + grp];
+                    }
+                    const float xsc = mx::scale_of(xe);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const i32x4 &src = j < 2 ? x0 : x1;
+                        uint32_t o[4];
+                        mx::decode_word_bf16<TCQ_FP8>(static_cast<uint32_t>(src[2 * (j % 2)]), xsc,
+                                                      o);
+                        mx::decode_word_bf16<TCQ_FP8>(static_cast<uint32_t>(src[2 * (j % 2) + 1]),
+                                                      xsc, o + 2);
+                        xf[j] = __builtin_bit_cast(
+                            s16x8, (i32x4{static_cast<int>(o[0]), static_cast<int>(o[1]),
+                                          static_cast<int>(o[2]), static_cast<int>(o[3])}));
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[b] = gemm::Traits<__bf16>::mma(wf[j], xf[j], acc[b]);
+            }
+        }
+    };
+    for (int u = u0; u < u1; u += kMxUnits) {
+#pragma unroll
+        for (int k = 0; k < kMxUnits; ++k) {
+            const i32x4 c = wc[k];
+            const uint32_t e = we[k];
+            load_w(u + kMxUnits + k, wc[k], we[k]);
+            if (u + k < u1) multiply(u + k, c, e);
+        }
+    }
+    // The waves' sums: 16 BT x 16 values each, value (row j of W, row b of x) of a tile in word
+    // (j / 4 * 16 + b) * 4 + j % 4.
+    if constexpr (DENSE) __syncthreads();
+    float *red = reinterpret_cast<float *>(lds);
+#pragma unroll
+    for (int b = 0; b < BT; ++b)
+        *reinterpret_cast<f32x4 *>(red + ((wave * BT + b) * 64 + lane) * 4) = acc[b];
+    __syncthreads();
+    for (int i = tid; i < BT * 256; i += kMxWaves * 64) {
+        const int j = i & 15, b = i >> 4;
+        const int at = (b >> 4) * 256 + ((j >> 2) * 16 + (b & 15)) * 4 + (j & 3);
+        float s = red[at];
+#pragma unroll
+        for (int v = 1; v < kMxWaves; ++v) s += red[v * BT * 256 + at];
+        epi.put_one(b, j0 + j, s);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+constexpr int kMxMostSmall = 128;          // rows of x that mx_small_kernel takes
+constexpr int kMxDenseBytes = 96 << 10;    // LDS for x quantised in the kernel
+
+size_t pad(int64_t n, int64_t to) { return static_cast<size_t>((n + to - 1) / to * to); }
+
+int64_t groups_of(int64_t n) { return (n + mx::kGroup - 1) / mx::kGroup; }
+
+template <typename T>
+LayerEpilogue<T> mx_epilogue(const MxLinearCall &c) {
+    LayerEpilogue<T> e{};
+    e.bias = c.bias;
+    e.res = static_cast<const T *>(c.residual);
+    e.y = static_cast<T *>(c.y);
+    e.ldr = c.ldr;
+    e.ldy = c.ldy;
+    e.I = c.B;
+    e.J = c.M;
+    e.act = TCQ_ACT_NONE;
+    e.vec_y = four_aligned(e.y, e.ldy);
+    e.vec_r = e.res && four_aligned(e.res, e.ldr);
+    return e;
+}
+
+// LDS row of x quantised in the kernel: whole units, 16 bytes more so that rows start in
+// different banks.
+int dense_row(int format, int64_t units) {
+    return static_cast<int>(units * (format == TCQ_FP4 ? 64 : 256) + 16);
+}
+int64_t dense_bytes(int format, int64_t B, int64_t units) {
+    return B * (dense_row(format, units) + (format == TCQ_FP4 ? units * 4 : 0));
+}
+bool small_dense(const MxLinearCall &c) {
+    const int64_t units = (groups_of(c.N) + 3) / 4;
+    return c.x && !c.keep && c.B <= 16 && dense_bytes(c.xq.format, c.B, units) <= kMxDenseBytes;
+}
+
+template <typename T, int FMT, int BT, bool DENSE>
+hipError_t launch_small_as(const MxSmallArgs &a, const LayerEpilogue<T> &epi, hipStream_t s) {
+    const int64_t sums = int64_t{kMxWaves} * BT * 1024;
+    const int64_t dense = DENSE ? dense_bytes(FMT, a.B, a.units) : 0;
+    // (the limit is one of the kernel, not of the call: threads with x of two sizes share it)
+    const void *kern = reinterpret_cast<const void *>(mx_small_kernel<T, FMT, BT, DENSE>);
+    const hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             DENSE ? kMxDenseBytes : static_cast<int>(sums));
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((mx_small_kernel<T, FMT, BT, DENSE>),
+                       dim3(static_cast<unsigned>((a.M + 15) / 16)), dim3(kMxWaves * 64),
+                       static_cast<unsigned>(sums > dense ? sums : dense), s, a, epi);
+    return hipGetLastError();
+}
+
+template <typename T, int FMT>
+hipError_t launch_small(MxSmallArgs a, const LayerEpilogue<T> &epi, hipStream_t s) {
+    if (a.x) return launch_small_as<T, FMT, 1, true>(a, epi, s);
+    if (a.B <= 16) return launch_small_as<T, FMT, 1, false>(a, epi, s);
+    if (a.B <= 32) return launch_small_as<T, FMT, 2, false>(a, epi, s);
+    if (a.B <= 64) return launch_small_as<T, FMT, 4, false>(a, epi, s);
+    return launch_small_as<T, FMT, 8, false>(a, epi, s);
+}
+
+// Tile and splits of the product of B rows of 4-bit codes with M over `steps` steps: 256 x 256
+// tiles where they fill the 256 compute units, else 128 x 128 with k split.
+struct MxPlan {
+    bool big;
+    int splits, steps, steps_per_split;
+    int64_t part_ld;
+};
+constexpr int64_t kMxCus = 256, kMxMostSplits = 16;
+MxPlan mx_plan(int64_t B, int64_t M, int64_t steps) {
+    MxPlan p{};
+    p.steps = static_cast<int>(steps);
+    p.part_ld = (M + 3) / 4 * 4;
+    p.splits = 1;
+    p.steps_per_split = p.steps;
+    const int64_t n256 = ((B + 255) / 256) * ((M + 255) / 256);
+    p.big = n256 >= kMxCus / 2;
+    if (p.big) return p;
+    const int64_t n = ((B + 127) / 128) * ((M + 127) / 128);
+    int64_t s = kMxCus / n;
+    if (s > steps / 4) s = steps / 4;
+    if (s > kMxMostSplits) s = kMxMostSplits;
+    if (s < 1) s = 1;
+    p.steps_per_split = static_cast<int>((steps + s - 1) / s);
+    p.splits = p.steps_per_split > 0 ? (p.steps + p.steps_per_split - 1) / p.steps_per_split : 1;
+    return p;
+}
+// Room for the shares, never less for a larger B.
+size_t mx_shares(int64_t B, int64_t M, int64_t steps) {
+    int64_t s = steps / 4 < kMxMostSplits ? steps / 4 : kMxMostSplits;
+    if (s < 2) return 0;
+    const int64_t values = s * B * ((M + 3) / 4 * 4), most = kMxCus * 128 * 128;
+    return static_cast<size_t>(values < most ? values : most) * sizeof(float);
+}
+
+template <int TI, int TJ, int WI, int WJ, int NB, typename Epi>
+hipError_t launch_mx_tiles(const Operand<CodePair> &A, const uint8_t *as,
+                           const Operand<CodePair> &W, const uint8_t *ws, const MxPlan &p,
+                           const Epi &epi, hipStream_t s) {
+    const uint32_t ni = static_cast<uint32_t>((A.rows + TI - 1) / TI);
+    const uint32_t nj = static_cast<uint32_t>((W.rows + TJ - 1) / TJ);
+    hipLaunchKernelGGL((mx_gemm_kernel<TI, TJ, WI, WJ, NB, Epi>),
+                       dim3(ni * nj, static_cast<unsigned>(p.splits)), dim3(WI * WJ * 64), 0, s, A,
+                       as, W, ws, p.steps, p.steps_per_split, epi, ni, nj);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t large_fp4(const MxLinearCall &c, const MxMatrix &x, const MxLayout &lay, char *ws,
+                     hipStream_t s) {
+    const int64_t groups = groups_of(c.N), steps = (groups + 7) / 8;
+    const int64_t xt = (c.B + 127) / 128, wt = (c.M + 127) / 128;
+    uint8_t *xs = reinterpret_cast<uint8_t *>(ws + lay.xs);
+    uint8_t *wsc = xs + pad(xt, 2) * steps * 1024;
+    // (256 x 256 tiles read whole pairs of 128 rows)
+    const ScaleArgs sx{x.scale, c.B, groups, steps, xs,
+                       static_cast<int64_t>(pad(xt, 2)) * steps * 64};
+    const ScaleArgs sw{c.w.scale, c.M, groups, steps, wsc,
+                       static_cast<int64_t>(pad(wt, 2)) * steps * 64};
+    hipError_t e;
+    if (steps > 0) {
+        hipLaunchKernelGGL(order_scales_kernel,
+                           dim3(static_cast<unsigned>((sx.lanes + sw.lanes + 255) / 256)),
+                           dim3(256), 0, s, sx, sw);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    const Operand<CodePair> A{reinterpret_cast<const CodePair *>(x.codes), x.ld, c.B, groups * 16};
+    const Operand<CodePair> W{reinterpret_cast<const CodePair *>(c.w.codes), c.w.ld, c.M,
+                              groups * 16};
+    const MxPlan p = mx_plan(c.B, c.M, steps);
+    const LayerEpilogue<T> epi = mx_epilogue<T>(c);
+    if (p.big) return launch_mx_tiles<256, 256, 2, 4, gemm::kRing>(A, xs, W, wsc, p, epi, s);
+    if (p.splits == 1) return launch_mx_tiles<128, 128, 2, 2, 4>(A, xs, W, wsc, p, epi, s);
+    const PartEpilogue pe{reinterpret_cast<float *>(ws + lay.parts), p.part_ld, c.B, c.M};
+    e = launch_mx_tiles<128, 128, 2, 2, 4>(A, xs, W, wsc, p, pe, s);
+    if (e != hipSuccess) return e;
+    const int64_t quads = c.B * (p.part_ld / 4);
+    hipLaunchKernelGGL(split_sum_kernel<LayerEpilogue<T>>,
+                       dim3(static_cast<unsigned>((quads + 255) / 256)), dim3(256), 0, s, pe.part,
+                       p.splits, c.B, p.part_ld, epi);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t linear(const MxLinearCall &c, char *ws, hipStream_t s) {
+    const MxLayout lay = mx_linear_layout(c.xq.format, c.B, c.M, c.N);
+    const bool fp4 = c.xq.format == TCQ_FP4, small = c.B <= kMxMostSmall;
+    const bool dense = small && small_dense(c);
+    MxMatrix x = c.xq;
+    uint16_t *xvals = reinterpret_cast<uint16_t *>(ws + lay.xvals);
+    // (large batches of 8-bit rows are read as the bf16 numbers that the codes stand for)
+    const bool values = !small && !fp4;
+    hipError_t e;
+    if (c.x && !dense) {
+        if (!c.keep) {
+            x.codes = reinterpret_cast<uint8_t *>(ws + lay.codes);
+            x.ld = lay.ldq;
+            x.scale = reinterpret_cast<uint8_t *>(ws + lay.scale);
+        }
+        const bool codes = c.keep || !values;
+        e = launch_mx_pack(c.x, c.dtype, c.B, c.N, c.ldx, c.xq.format,
+                           codes ? const_cast<uint8_t *>(x.codes) : nullptr, x.ld,
+                           codes ? const_cast<uint8_t *>(x.scale) : nullptr,
+                           values ? xvals : nullptr, lay.ldn, s);
+        if (e != hipSuccess) return e;
+    }
+    if (small) {
+        const int64_t groups = groups_of(c.N);
+        MxSmallArgs a{};
+        a.w = c.w.codes;
+        a.ws = c.w.scale;
+        a.ldw = c.w.ld;
+        a.M = c.M;
+        a.N = static_cast<int>(c.N);
+        a.groups = static_cast<int>(groups);
+        a.units = static_cast<int>((groups + 3) / 4);
+        a.x = dense ? c.x : nullptr;
+        a.ldx = c.ldx;
+        a.xq = x.codes;
+        a.xs = x.scale;
+        a.ldq = x.ld;
+        a.B = static_cast<int>(c.B);
+        a.ldl = dense ? dense_row(c.xq.format, a.units) : 0;
+        const LayerEpilogue<T> epi = mx_epilogue<T>(c);
+        return fp4 ? launch_small<T, TCQ_FP4>(a, epi, s) : launch_small<T, TCQ_FP8>(a, epi, s);
+    }
+    if (fp4) return large_fp4<T>(c, x, lay, ws, s);
+    if (!c.x) {
+        e = launch_mx_unpack(x, c.B, c.N, TCQ_BF16, xvals, lay.ldn, lay.ldn, nullptr, s);
+        if (e != hipSuccess) return e;
+    }
+    uint16_t *wvals = reinterpret_cast<uint16_t *>(ws + lay.wvals);
+    e = launch_mx_unpack(c.w, c.M, c.N, TCQ_BF16, wvals, lay.ldn, lay.ldn, nullptr, s);
+    if (e != hipSuccess) return e;
+    const DenseProduct d{xvals,  wvals,      lay.ldn, lay.ldn, c.B, c.M, lay.ldn,
+                         c.dtype, c.bias, c.residual, c.ldr,   c.y, c.ldy};
+    return launch_dense_product(d, ws + lay.parts, s);
+}
+
+// ---------------------------------------------------------------- gradients
+
+// fp16 holds the values times the power of two that brings the largest finite scale's largest
+// code next to the type's own largest number (1.75 2^15), so that none overflows and only those
+// 2^-36 of it are rounded; the sums are multiplied by its inverse.
+struct TopArgs {
+    const uint8_t *scale;
+    int64_t n;
+    int *up, *down;   // the values' shift and the result's
+    int top;          // exponent of the largest code
+};
+__global__ __launch_bounds__(1024) void scale_shift_kernel(TopArgs w, TopArgs x) {
+    const TopArgs &a = blockIdx.x == 0 ? w : x;
+    __shared__ int red[16];
+    int top = 0;
+    for (int64_t i = threadIdx.x; i < a.n; i += 1024) {
+        const int e = a.scale[i];
+        if (e != 255 && e > top) top = e;
+    }
+    for (int d = 32; d; d >>= 1) {
+        const int o = __shfl_xor(top, d);
+        top = top > o ? top : o;
+    }
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int v = 1; v < 16; ++v) top = top > red[v] ? top : red[v];
+        *a.up = 127 + 15 - a.top - top;
+        *a.down = top + a.top - 127 - 15;
+    }
+}
+
+struct MxGradLayout {
+    size_t shifts, w, x, dense, bytes;
+    int64_t ldn;
+};
+MxGradLayout mx_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bool dx, bool dw,
+                            bool dbias) {
+    MxGradLayout l{};
+    l.ldn = static_cast<int64_t>(pad(N, 8));
+    size_t off = 0;
+    l.shifts = off;
+    if ((dx || dw) && size == 2) off += 256;
+    l.w = off;
+    if (dx) off += align_up(static_cast<size_t>(M) * l.ldn * size, 256);
+    l.x = off;
+    if (dw) off += align_up(static_cast<size_t>(B) * l.ldn * size, 256);
+    l.dense = off;
+    l.bytes = off + dense_grad_layout(size, B, M, N, dx, dw, dbias).bytes;
+    return l;
+}
+
+}  // namespace
+
+// Codes and scales of x, the ordered scales (4-bit rows) or the bf16 matrices (8-bit), and
+// shares: nothing is smaller for a larger B.
+MxLayout mx_linear_layout(int format, int64_t B, int64_t M, int64_t N) {
+    MxLayout l{};
+    const int64_t groups = groups_of(N), steps = (groups + 7) / 8;
+    const bool fp4 = format == TCQ_FP4, large = B > kMxMostSmall;
+    l.ldq = groups * (fp4 ? 16 : 32);
+    l.ldn = groups * mx::kGroup;
+    size_t off = 0;
+    l.codes = off;
+    off += align_up(static_cast<size_t>(B) * l.ldq, 256);
+    l.scale = off;
+    off += align_up(static_cast<size_t>(B) * groups, 256);
+    l.xs = l.wvals = l.xvals = l.parts = off;
+    if (large && fp4) {
+        const size_t tiles = pad((B + 127) / 128, 2) + pad((M + 127) / 128, 2);
+        off += tiles * steps * 1024;
+        l.parts = off;
+        off += align_up(mx_shares(B, M, steps), 256);
+    } else if (large) {
+        off += align_up(static_cast<size_t>(M) * l.ldn * 2, 256);
+        l.xvals = off;
+        off += align_up(static_cast<size_t>(B) * l.ldn * 2, 256);
+        l.parts = off;
+        off += align_up(gemm_shares(2, B, M, l.ldn, 1), 256);
+    }
+    l.bytes = off;
+    return l;
+}
+
+hipError_t launch_mx_linear(const MxLinearCall &c, char *ws, hipStream_t s) {
+    switch (c.dtype) {
+        case TCQ_F32: return linear<float>(c, ws, s);
+        case TCQ_F16: return linear<_Float16>(c, ws, s);
+        default: return linear<__bf16>(c, ws, s);
+    }
+}
+
+size_t mx_grad_bytes(int dtype, int64_t B, int64_t M, int64_t N, bool dx, bool dw, bool dbias) {
+    return mx_grad_layout(dtype == TCQ_F32 ? 4 : 2, B, M, N, dx, dw, dbias).bytes;
+}
+
+hipError_t launch_mx_grad(const MxGrad &c, char *ws, hipStream_t s) {
+    const MxGradLayout lay = mx_grad_layout(c.dtype == TCQ_F32 ? 4 : 2, c.B, c.M, c.N, c.dx, c.dw,
+                                            c.dbias);
+    int *shift = reinterpret_cast<int *>(ws + lay.shifts);  // w up, w down, x up, x down
+    const bool shifted = c.dtype == TCQ_F16;
+    const bool dx = c.dx && c.B > 0 && c.N > 0, dw = c.dw && c.M > 0 && c.N > 0;
+    const bool read_w = dx && c.M > 0, read_x = dw && c.B > 0;
+    hipError_t e;
+    if (shifted && (read_w || read_x)) {
+        const int64_t groups = groups_of(c.N);
+        const TopArgs w{c.w.scale, c.M * groups, shift, shift + 1, 2};
+        const TopArgs x{c.x.scale, c.B * groups, shift + 2, shift + 3,
+                        c.x.format == TCQ_FP4 ? 2 : 8};
+        // (the second is x's, the first w's, or x's alone)
+        hipLaunchKernelGGL(scale_shift_kernel, dim3(read_w && read_x ? 2 : 1), dim3(1024), 0, s,
+                           read_w ? w : x, x);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (read_w) {
+        e = launch_mx_unpack(c.w, c.M, c.N, c.dtype, ws + lay.w, lay.ldn, lay.ldn,
+                             shifted ? shift : nullptr, s);
+        if (e != hipSuccess) return e;
+    }
+    if (read_x) {
+        e = launch_mx_unpack(c.x, c.B, c.N, c.dtype, ws + lay.x, lay.ldn, lay.ldn,
+                             shifted ? shift + 2 : nullptr, s);
+        if (e != hipSuccess) return e;
+    }
+    const DenseGrad d{c.dtype, c.dy,
+                      c.B,     c.lddy,
+                      c.M,     c.N,
+                      ws + lay.w, ws + lay.x,
+                      shifted && read_w ? shift + 1 : nullptr,
+                      shifted && read_x ? shift + 3 : nullptr,
+                      dx ? c.dx : nullptr, c.lddx,
+                      dw ? c.dw : nullptr, c.lddw,
+                      c.dbias};
+    return launch_dense_grad(d, ws + lay.dense, s);
+}
+
+}  // namespace tcq

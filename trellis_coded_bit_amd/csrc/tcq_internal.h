@@ -162,6 +162,95 @@ hipError_t launch_linear(const CodedMatrix &w, const LinearCall &c, char *ws, hi
 hipError_t launch_linear_grad(const CodedMatrix &w, const LinearGrad &c, char *ws,
                               hipStream_t s);
 
+// Products of dense matrices with the tiles of the coded linear layer.
+//   bf16 x (B x K) and w (M x K), K a multiple of 8, rows of whole 16-byte pieces:
+//   y = x w^T + bias + residual in `dtype`; ws holds gemm_shares(2, B, M, K, 1) bytes.
+struct DenseProduct {
+    const uint16_t *x, *w;
+    int64_t ldx, ldw, B, M, K;
+    int dtype;
+    const float *bias;
+    const void *residual;
+    int64_t ldr;
+    void *y;
+    int64_t ldy;
+};
+size_t gemm_shares(size_t size, int64_t I, int64_t J, int64_t K, int terms);
+hipError_t launch_dense_product(const DenseProduct &c, char *ws, hipStream_t s);
+//   Gradients in `dtype` from dy (B x M) and dense w (M x ldn), x (B x ldn) in the workspace;
+//   fp16 products are multiplied by 2^*w_exponent (dx) and 2^*x_exponent (dw).
+struct DenseGradLayout {
+    size_t grad, part, sums, bytes;
+    int64_t ldn, ldm;
+};
+struct DenseGrad {
+    int dtype;
+    const void *dy;
+    int64_t B, lddy, M, N;
+    const void *w, *x;
+    const int *w_exponent, *x_exponent;
+    void *dx;
+    int64_t lddx;
+    void *dw;
+    int64_t lddw;
+    float *dbias;
+};
+DenseGradLayout dense_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bool dx, bool dw,
+                                  bool dbias);
+hipError_t launch_dense_grad(const DenseGrad &c, char *ws, hipStream_t s);
+
+// Microscaled matrices (codes, their leading dimension in bytes, scale bytes without gaps).
+struct MxMatrix {
+    const uint8_t *codes;
+    int64_t ld;
+    const uint8_t *scale;
+    int format;
+};
+// Codes and scale bytes, and, where values is not NULL, the bf16 numbers they stand for (up to
+// whole groups); codes and scale may be NULL.  Unpack also writes zeros to columns cols ..
+// padded - 1 and multiplies 16-bit values by 2^*shift_at (NULL: 1).
+hipError_t launch_mx_pack(const void *X, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                          int format, uint8_t *codes, int64_t ldq, uint8_t *scale,
+                          uint16_t *values, int64_t ldv, hipStream_t s);
+hipError_t launch_mx_unpack(const MxMatrix &m, int64_t rows, int64_t cols, int dtype, void *out,
+                            int64_t ldo, int64_t padded, const int *shift_at, hipStream_t s);
+// The microscaled linear layer and its gradients.
+struct MxLinearCall {
+    MxMatrix w;
+    int64_t M, N;
+    const void *x;           // dense, of type dtype, or NULL: xq is given
+    int64_t ldx;
+    MxMatrix xq;
+    bool keep;               // x is given and its codes are wanted in xq
+    int dtype;
+    int64_t B;
+    const float *bias;
+    const void *residual;
+    int64_t ldr;
+    void *y;
+    int64_t ldy;
+};
+struct MxLayout {
+    size_t codes, scale, xs, wvals, xvals, parts, bytes;
+    int64_t ldq;             // of the codes in the workspace
+    int64_t ldn;             // of unpacked rows
+};
+MxLayout mx_linear_layout(int format, int64_t B, int64_t M, int64_t N);
+hipError_t launch_mx_linear(const MxLinearCall &c, char *ws, hipStream_t s);
+struct MxGrad {
+    int dtype;
+    const void *dy;
+    int64_t B, lddy, M, N;
+    MxMatrix w, x;
+    void *dx;
+    int64_t lddx;
+    void *dw;
+    int64_t lddw;
+    float *dbias;
+};
+size_t mx_grad_bytes(int dtype, int64_t B, int64_t M, int64_t N, bool dx, bool dw, bool dbias);
+hipError_t launch_mx_grad(const MxGrad &c, char *ws, hipStream_t s);
+
 // 8-bit checkpoints (unpack also writes zeros to columns cols .. padded - 1 of out).
 hipError_t launch_act_pack(const void *X, int dtype, int64_t rows, int64_t cols, int64_t ldx,
                            int8_t *codes, int64_t ldq, uint8_t *scale, hipStream_t s);
