@@ -536,6 +536,84 @@ int tcq_mx_linear_backward(const uint8_t *w_codes, int64_t ldw, const uint8_t *w
                            int64_t lddw, float *dbias, void *workspace, size_t workspace_bytes,
                            hipStream_t stream);
 
+/*
+ * The paged cache of keys and values, held as microscaled codes.  A vector (one token's key or
+ * value of one head) is `dim` values, dim 64, 128 or 256, in dim / 32 groups; a page holds `page`
+ * tokens, a power of two up to 4096, of every head:
+ *   k_codes, v_codes : device [pages][heads][page] vectors of dim (TCQ_FP8) or dim / 2 (TCQ_FP4)
+ *                      bytes, 16-byte aligned
+ *   k_scale, v_scale : device [pages][heads][page][dim / 32] bytes
+ */
+typedef struct {
+    uint8_t *k_codes, *k_scale, *v_codes, *v_scale;
+    int64_t pages;
+    int heads, page, dim, format;
+} tcq_cache;
+
+/*
+ * A batch of sequences with new tokens.  The call's rows starts[s] .. starts[s + 1] - 1 are
+ * sequence s's newest tokens; with n of them, row starts[s] + i is its token at position
+ * lens[s] - n + i, which lies in page table[s][position / page], place position % page.
+ *   table  : device, seqs rows of width page numbers, ldt apart (ldt >= width)
+ *   lens   : device, seqs: the sequences' lengths, new tokens included
+ *   starts : device, seqs + 1, not decreasing, from 0 to at most the call's rows
+ * Sequences may be empty or have no new tokens.  Rows of the call behind starts[seqs] belong to
+ * nobody: they are neither read nor written.  A token whose position is negative or past width x
+ * page, or whose page number is not below `pages` (-1, for instance), is nowhere: it is not
+ * written, reads as zeros and is seen by no query.
+ */
+typedef struct {
+    const int32_t *table;
+    int64_t ldt, width;
+    const int32_t *lens, *starts;
+    int64_t seqs;
+} tcq_cache_batch;
+
+/*
+ * tcq_cache_write -- the new tokens' keys and values, quantised as tcq_mx_pack does, into their
+ * places.  (Where two rows of a call have the same place, what it holds is not specified.)
+ * tcq_cache_read  -- the values that the places of the batch's tokens stand for: with starts the
+ * running sum of lens, whole sequences.
+ *   dtype         : tcq_dtype of k and v
+ *   k, v          : device, rows x heads vectors, k_row and k_head (v_row, v_head) values apart
+ *   rows          : the call's rows, at most 2^23
+ * Outputs must not overlap inputs or one another (TCQ_EINVAL).  rows == 0 is a no-op.
+ * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED (limits: heads <= 1024, seqs <= 2^20), TCQ_EHIP.
+ */
+int tcq_cache_write(const tcq_cache *cache, const tcq_cache_batch *batch, int dtype,
+                    const void *k, int64_t k_row, int64_t k_head, const void *v, int64_t v_row,
+                    int64_t v_head, int64_t rows, hipStream_t stream);
+int tcq_cache_read(const tcq_cache *cache, const tcq_cache_batch *batch, int dtype, void *k,
+                   int64_t k_row, int64_t k_head, void *v, int64_t v_row, int64_t v_head,
+                   int64_t rows, hipStream_t stream);
+
+/*
+ * tcq_cache_attention -- attention of the new tokens over the cache, which holds them already:
+ * the query of position p in sequence s sees the sequence's keys j <= p,
+ *     o = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q . k_j)
+ * for each of q_heads query heads; head h reads the cache's head h / (q_heads / heads).  A query
+ * that sees no key gives zeros; a key or value group that stands for NaN reaches only the
+ * queries that see it.
+ *   q, o       : device, rows x q_heads vectors of dim values of type dtype, q_row and q_head (o_row,
+ *                o_head) values apart
+ *   q_heads    : a multiple of the cache's heads, at most 1024
+ *   scale      : between 2^-60 and 2^60 (1 / sqrt(dim), as a rule)
+ *   workspace  : >= what tcq_cache_attention_workspace_bytes reports
+ * Products of scores are exact and sums fp32; weights are held to 2^-8 (bf16), 2^-15 (fp16) or
+ * fp32 when they meet the values, and their sum to fp32; o is rounded once.  (As bf16 numbers,
+ * values below 2^-133 are lost: scale bytes below 3 in TCQ_FP8.)  How keys are shared
+ * out among workgroups depends on the batch's lengths, and with it the last bits of o; the same
+ * call gives the same bits.
+ * Outputs must not overlap inputs (TCQ_EINVAL).  rows == 0 is a no-op.
+ * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED, TCQ_EWORKSPACE, TCQ_EHIP.
+ */
+int tcq_cache_attention_workspace_bytes(int dim, int heads, int q_heads, int64_t seqs,
+                                        int64_t rows, size_t *bytes);
+int tcq_cache_attention(const tcq_cache *cache, const tcq_cache_batch *batch, int dtype,
+                        const void *q, int64_t q_row, int64_t q_head, int q_heads, int64_t rows,
+                        float scale, void *o, int64_t o_row, int64_t o_head, void *workspace,
+                        size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

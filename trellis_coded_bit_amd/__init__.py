@@ -28,6 +28,10 @@ from ._lib import (  # noqa: F401
     tcq_mx_linear,
     tcq_mx_linear_backward_workspace_bytes,
     tcq_mx_linear_backward,
+    tcq_cache_write,
+    tcq_cache_read,
+    tcq_cache_attention_workspace_bytes,
+    tcq_cache_attention,
     tcq_encode,
     tcq_encode_timed,
     tcq_encode_workspace_bytes,

@@ -36,7 +36,24 @@ EXPORTED = ("tcq_version", "tcq_last_error", "tcq_make_codebook",
             "tcq_act_unpack", "tcq_decode_linear_backward_workspace_bytes",
             "tcq_decode_linear_backward", "tcq_mx_pack", "tcq_mx_unpack",
             "tcq_mx_linear_workspace_bytes", "tcq_mx_linear",
-            "tcq_mx_linear_backward_workspace_bytes", "tcq_mx_linear_backward")
+            "tcq_mx_linear_backward_workspace_bytes", "tcq_mx_linear_backward",
+            "tcq_cache_write", "tcq_cache_read", "tcq_cache_attention_workspace_bytes",
+            "tcq_cache_attention")
+
+
+class TcqCache(ctypes.Structure):
+    """tcq_cache: device addresses and sizes of a paged cache."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("heads", ctypes.c_int), ("page", ctypes.c_int),
+                ("dim", ctypes.c_int), ("format", ctypes.c_int)]
+
+
+class TcqCacheBatch(ctypes.Structure):
+    """tcq_cache_batch: device addresses and sizes of a batch of sequences."""
+    _fields_ = [("table", ctypes.c_void_p), ("ldt", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("lens", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("seqs", ctypes.c_int64)]
+
 
 _lib = None
 
@@ -134,6 +151,17 @@ def load():
     lib.tcq_mx_linear_backward.restype = i32
     lib.tcq_mx_linear_backward.argtypes = [vp, i64, vp, i64, i64, i32, vp, i64, i64, i32, vp, i64,
                                            vp, vp, i64, vp, i64, vp, vp, sz, vp]
+    places = [ctypes.POINTER(TcqCache), ctypes.POINTER(TcqCacheBatch), i32]
+    lib.tcq_cache_write.restype = i32
+    lib.tcq_cache_write.argtypes = [*places, vp, i64, i64, vp, i64, i64, i64, vp]
+    lib.tcq_cache_read.restype = i32
+    lib.tcq_cache_read.argtypes = [*places, vp, i64, i64, vp, i64, i64, i64, vp]
+    lib.tcq_cache_attention_workspace_bytes.restype = i32
+    lib.tcq_cache_attention_workspace_bytes.argtypes = [i32, i32, i32, i64, i64,
+                                                        ctypes.POINTER(sz)]
+    lib.tcq_cache_attention.restype = i32
+    lib.tcq_cache_attention.argtypes = [*places, vp, i64, i64, i32, i64, ctypes.c_float, vp, i64,
+                                        i64, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -397,3 +425,38 @@ def tcq_mx_linear_backward(w_codes: int | None, ldw: int, w_scale: int | None, M
                                          lddy, format, x_codes or None, ldxq, x_scale or None,
                                          dx or None, lddx, dw or None, lddw, dbias or None,
                                          workspace or None, workspace_bytes, stream or None))
+
+
+def tcq_cache_write(cache: TcqCache, batch: TcqCacheBatch, dtype: int, k: int, k_row: int,
+                    k_head: int, v: int, v_row: int, v_head: int, rows: int,
+                    stream: int | None) -> None:
+    _check("tcq_cache_write",
+           load().tcq_cache_write(cache, batch, dtype, k, k_row, k_head, v, v_row, v_head, rows,
+                                  stream or None))
+
+
+def tcq_cache_read(cache: TcqCache, batch: TcqCacheBatch, dtype: int, k: int, k_row: int,
+                   k_head: int, v: int, v_row: int, v_head: int, rows: int,
+                   stream: int | None) -> None:
+    _check("tcq_cache_read",
+           load().tcq_cache_read(cache, batch, dtype, k, k_row, k_head, v, v_row, v_head, rows,
+                                 stream or None))
+
+
+def tcq_cache_attention_workspace_bytes(dim: int, heads: int, q_heads: int, seqs: int,
+                                        rows: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check("tcq_cache_attention_workspace_bytes",
+           load().tcq_cache_attention_workspace_bytes(dim, heads, q_heads, seqs, rows,
+                                                      ctypes.byref(b)))
+    return int(b.value)
+
+
+def tcq_cache_attention(cache: TcqCache, batch: TcqCacheBatch, dtype: int, q: int, q_row: int,
+                        q_head: int, q_heads: int, rows: int, scale: float, o: int, o_row: int,
+                        o_head: int, workspace: int | None, workspace_bytes: int,
+                        stream: int | None) -> None:
+    _check("tcq_cache_attention",
+           load().tcq_cache_attention(cache, batch, dtype, q, q_row, q_head, q_heads, rows, scale,
+                                      o, o_row, o_head, workspace or None, workspace_bytes,
+                                      stream or None))

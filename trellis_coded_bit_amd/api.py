@@ -496,3 +496,132 @@ def mx_linear_backward(dy: torch.Tensor, w: MxPacked, x: MxPacked | None = None,
                 None if gb is None else gb.data_ptr(), *_workspace(workspace, dev),
                 _stream_of(dev))
     return gx, gw, gb
+
+
+@dataclass
+class Cache:
+    """A paged cache of keys and values in microscaled codes (see tcq_cache).  Codes are uint8
+    [pages, heads, page, dim ("fp8") or dim / 2 ("fp4")], scale bytes uint8 [pages, heads, page,
+    dim / 32], all contiguous."""
+    k_codes: torch.Tensor
+    k_scale: torch.Tensor
+    v_codes: torch.Tensor
+    v_scale: torch.Tensor
+    format: str = "fp8"
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page: int, dim: int, format: str = "fp8",
+              device="cuda") -> "Cache":
+        """A cache of zeros."""
+        assert format in _FORMATS and dim % MX_GROUP == 0
+        width = dim if format == "fp8" else dim // 2
+        return cls(*(torch.zeros((pages, heads, page, w), dtype=torch.uint8, device=device)
+                     for w in (width, dim // MX_GROUP, width, dim // MX_GROUP)), format)
+
+    @property
+    def dim(self) -> int:
+        return self.k_scale.shape[3] * MX_GROUP
+
+    def c(self, device: torch.device) -> _lib.TcqCache:
+        """The C form; checks the tensors."""
+        assert self.format in _FORMATS, f"cache: format is none of {tuple(_FORMATS)}"
+        assert self.k_scale.dim() == 4, "cache: scale bytes [pages, heads, page, dim / 32]"
+        pages, heads, page, groups = self.k_scale.shape
+        width = groups * _group_bytes(self.format)
+        for t, w in ((self.k_codes, width), (self.k_scale, groups), (self.v_codes, width),
+                     (self.v_scale, groups)):
+            assert t.device == device and t.dtype == torch.uint8 and t.is_contiguous() and \
+                t.shape == (pages, heads, page, w), \
+                f"cache: contiguous uint8 [{pages}, {heads}, {page}, {w}] on {device}"
+        return _lib.TcqCache(self.k_codes.data_ptr(), self.k_scale.data_ptr(),
+                             self.v_codes.data_ptr(), self.v_scale.data_ptr(), pages, heads, page,
+                             groups * MX_GROUP, _FORMATS[self.format])
+
+
+def _batch(table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor,
+           device: torch.device) -> _lib.TcqCacheBatch:
+    assert table.dim() == 2, "table: [sequences, pages]"
+    seqs, width = table.shape
+    ldt = _rows(table, "table", seqs, width, torch.int32, device)
+    for t, name, n in ((lens, "lens", seqs), (starts, "starts", seqs + 1)):
+        assert t.device == device and t.dtype == torch.int32 and t.is_contiguous() and \
+            t.shape == (n,), f"{name}: {n} contiguous int32 values on {device}"
+    return _lib.TcqCacheBatch(table.data_ptr(), ldt, width, lens.data_ptr(), starts.data_ptr(),
+                              seqs)
+
+
+def _vectors(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, dtype: torch.dtype,
+             device: torch.device) -> tuple[int, int]:
+    """Checks rows x heads vectors whose values are contiguous; strides of rows and heads."""
+    assert t.device == device and t.dtype == dtype, f"{name}: {dtype} on {device}"
+    assert t.shape == (rows, heads, dim), \
+        f"{name}: shape {tuple(t.shape)}, not {(rows, heads, dim)}"
+    assert t.stride(2) == 1, f"{name}: vectors must be contiguous"
+    # a dimension of at most one element may carry any stride
+    head = t.stride(1) if heads > 1 else dim
+    row = t.stride(0) if rows > 1 else (heads - 1) * head + dim
+    assert head >= dim and row >= (heads - 1) * head + dim, f"{name}: vectors overlap"
+    return row, head
+
+
+def cache_write(cache: Cache, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
+                lens: torch.Tensor, starts: torch.Tensor) -> None:
+    """Quantises the new tokens' keys and values [rows, heads, dim] (float32, float16 or bfloat16)
+    into the cache.  Rows starts[s] .. starts[s + 1] - 1 are the newest tokens of sequence s,
+    whose length with them is lens[s]; its token at position p lies in page table[s, p // page].
+    table, lens and starts are int32 on the device."""
+    dev, dt = k.device, k.dtype
+    assert k.is_cuda and k.dim() == 3 and dt in _DTYPES
+    c, b = cache.c(dev), _batch(table, lens, starts, dev)
+    rows = k.shape[0]
+    ks = _vectors(k, "k", rows, c.heads, c.dim, dt, dev)
+    vs = _vectors(v, "v", rows, c.heads, c.dim, dt, dev)
+    with _on(dev):
+        _lib.tcq_cache_write(c, b, _DTYPES[dt], k.data_ptr(), *ks, v.data_ptr(), *vs, rows,
+                             _stream_of(dev))
+
+
+def cache_read(cache: Cache, table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor,
+               rows: int, dtype: torch.dtype,
+               out: tuple[torch.Tensor, torch.Tensor] | None = None
+               ) -> tuple[torch.Tensor, torch.Tensor]:
+    """Keys and values [rows, heads, dim] that the cache holds for the batch's tokens (see
+    cache_write; with starts the running sum of lens, whole sequences).  Rows behind starts[-1]
+    are not written."""
+    dev = cache.k_codes.device
+    assert cache.k_codes.is_cuda and dtype in _DTYPES and rows >= 0
+    c, b = cache.c(dev), _batch(table, lens, starts, dev)
+    with _on(dev):
+        k, v = out if out is not None else (
+            torch.empty((rows, c.heads, c.dim), dtype=dtype, device=dev) for _ in range(2))
+        ks = _vectors(k, "k", rows, c.heads, c.dim, dtype, dev)
+        vs = _vectors(v, "v", rows, c.heads, c.dim, dtype, dev)
+        _lib.tcq_cache_read(c, b, _DTYPES[dtype], k.data_ptr(), *ks, v.data_ptr(), *vs, rows,
+                            _stream_of(dev))
+    return k, v
+
+
+def cache_attention(q: torch.Tensor, cache: Cache, table: torch.Tensor, lens: torch.Tensor,
+                    starts: torch.Tensor, scale: float | None = None,
+                    out: torch.Tensor | None = None, workspace: Workspace | None = None
+                    ) -> torch.Tensor:
+    """Attention of the new tokens' queries q [rows, q_heads, dim] (float32, float16 or bfloat16)
+    over the cache, which holds their own keys and values already (see cache_write for table,
+    lens and starts): a query sees its sequence's keys up to its own position.  q_heads is a
+    multiple of the cache's heads; scale is 1 / sqrt(dim) unless given.  Rows behind starts[-1]
+    are not written.  The output carries no autograd graph."""
+    dev, dt = q.device, q.dtype
+    assert q.is_cuda and q.dim() == 3 and dt in _DTYPES
+    c, b = cache.c(dev), _batch(table, lens, starts, dev)
+    rows, heads, dim = q.shape
+    qs = _vectors(q, "q", rows, heads, c.dim, dt, dev)
+    with _on(dev):
+        o = torch.empty((rows, heads, dim), dtype=dt, device=dev) if out is None else out
+        os_ = _vectors(o, "out", rows, heads, c.dim, dt, dev)
+        if workspace is None:
+            n = _lib.tcq_cache_attention_workspace_bytes(c.dim, c.heads, heads, b.seqs, rows)
+            workspace = Workspace(n, dev) if n else None
+        _lib.tcq_cache_attention(c, b, _DTYPES[dt], q.data_ptr(), *qs, heads, rows,
+                                 c.dim ** -0.5 if scale is None else scale, o.data_ptr(), *os_,
+                                 *_workspace(workspace, dev), _stream_of(dev))
+    return o

@@ -22,7 +22,8 @@ SOURCES = ["tcq_api.cpp", "codebook.cpp", "kernels_generic.hip", "kernels_l16.hi
            "kernels_l16k3.hip", "kernels_l16h.hip", "kernels_ldlq.hip", "kernels_bcjr.hip",
            "kernels_preprocess.hip", "kernels_decode.hip", "tcq_noalloc.hip",
            "kernels_linear.hip", "kernels_checkpoint.hip", "tcq_linear.cpp",
-           "kernels_mx.hip", "kernels_mx_linear.hip", "tcq_mx.cpp"]
+           "kernels_mx.hip", "kernels_mx_linear.hip", "tcq_mx.cpp", "kernels_cache.hip",
+           "kernels_attention.hip", "tcq_cache.cpp"]
 
 # -ffp-contract=off: the encoder's fp32 recurrence is written with explicit fmaf and
 #   must not gain extra contractions.

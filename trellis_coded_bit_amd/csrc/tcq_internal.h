@@ -251,6 +251,36 @@ struct MxGrad {
 size_t mx_grad_bytes(int dtype, int64_t B, int64_t M, int64_t N, bool dx, bool dw, bool dbias);
 hipError_t launch_mx_grad(const MxGrad &c, char *ws, hipStream_t s);
 
+// The paged cache of keys and values, and attention over it.
+struct CacheShape {
+    uint8_t *k_codes, *k_scale, *v_codes, *v_scale;
+    int64_t pages;
+    int heads, page_log2, dim, format;
+};
+struct CacheBatch {
+    const int32_t *table;   // seqs x width page numbers, rows of ldt
+    int64_t ldt, width;
+    const int32_t *lens, *starts;
+    int64_t seqs;
+};
+struct CacheRows {
+    const void *p;          // rows x heads x dim values
+    int64_t row, head;      // strides in values
+};
+hipError_t launch_cache_move(bool write, const CacheShape &c, const CacheBatch &b, int dtype,
+                             const CacheRows &k, const CacheRows &v, int64_t rows, hipStream_t s);
+struct AttentionCall {
+    CacheShape c;
+    CacheBatch b;
+    int dtype;
+    CacheRows q, o;         // rows x (heads x group) x dim
+    int group;
+    int64_t rows;
+    float scale;
+};
+size_t attention_bytes(int dim, int heads, int group, int64_t seqs, int64_t rows);
+hipError_t launch_attention(const AttentionCall &c, char *ws, hipStream_t s);
+
 // 8-bit checkpoints (unpack also writes zeros to columns cols .. padded - 1 of out).
 hipError_t launch_act_pack(const void *X, int dtype, int64_t rows, int64_t cols, int64_t ldx,
                            int8_t *codes, int64_t ldq, uint8_t *scale, hipStream_t s);
