@@ -42,25 +42,26 @@ struct AttArgs {
     int64_t rows;
     float factor, factor_low;   // scale log2(e), and what it lacks
     float *part;                // shares: [slot][rows of a tile][dim], then maxima and sums
-    int64_t slots;
+    uint32_t slots;
     int both;                   // tiles of 16 rows serve sequences of up to 16 rows only, larger
                                 // tiles the others (0: this kernel serves every sequence)
 };
 
 // ---------------------------------------------------------------- items
 
-// What a launch of tiles of BQ rows and units of UNIT keys does with a sequence.
+// What a launch of tiles of BQ rows does with a sequence.
 struct Sequence {
-    int64_t tiles, units, chunks;
+    uint32_t tiles, units, chunks;
 };
 constexpr int kUnit = 128;      // keys: runs are whole units
 constexpr int kSmallRows = 16;
-constexpr int64_t kTargetSmall = 1024, kTargetLarge = 512;
+constexpr int kTargetSmall = 1024, kTargetLarge = 512;
 template <int BQ>
-constexpr int64_t target() {
+constexpr int target() {
     return BQ == kSmallRows ? kTargetSmall : kTargetLarge;
 }
 
+// (rows x group is below 2^28 and lengths below 2^31: 32 bits hold rows, keys and units)
 template <int BQ>
 __device__ __forceinline__ Sequence sequence(const AttArgs &a, int64_t s) {
     Sequence r{0, 0, 1};
@@ -68,80 +69,141 @@ __device__ __forceinline__ Sequence sequence(const AttArgs &a, int64_t s) {
     const cache::Span sp = cache::span_of(a.b, s, a.rows);
     const int64_t n = sp.end - sp.begin;
     if (n <= 0) return r;
-    const bool small = n * a.group <= kSmallRows;
+    const uint32_t rows = static_cast<uint32_t>(n) * static_cast<uint32_t>(a.group);
+    const bool small = rows <= kSmallRows;
     if (a.both && small != (BQ == kSmallRows)) return r;
-    r.tiles = (n * a.group + BQ - 1) / BQ;
+    r.tiles = (rows + BQ - 1) / BQ;
     int64_t keys = sp.first + n;  // the last row sees the keys before this
     const int64_t most = a.b.width << a.c.page_log2;
     keys = keys < 0 ? 0 : (keys < most ? keys : most);
-    r.units = (keys + kUnit - 1) / kUnit;
+    r.units = static_cast<uint32_t>((keys + kUnit - 1) / kUnit);
     return r;
 }
 
-__device__ __forceinline__ int64_t wave_sum(int64_t v) {
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-}
-__device__ __forceinline__ int64_t wave_prefix(int64_t v, int lane) {
+__device__ __forceinline__ uint32_t wave_prefix(uint32_t v, int lane) {
+#pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = __shfl_up(v, d);
+        const uint32_t o = __shfl_up(v, d);
         if (lane >= d) v += o;
     }
     return v;
 }
+__device__ __forceinline__ uint32_t of_lane(uint32_t v, int lane) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
+}
 
 // Units per run: the fewest with at most about the target number of runs in all.
 template <int BQ>
-__device__ __forceinline__ int64_t run_units(const AttArgs &a, int lane) {
-    int64_t total = 0;
+__device__ __forceinline__ uint32_t run_units(const AttArgs &a, int lane) {
+    uint64_t total = 0;
     for (int64_t s = 0; s < a.b.seqs; s += 64) {
         const Sequence q = sequence<BQ>(a, s + lane);
-        total += q.tiles * q.units;
+        total += static_cast<uint64_t>(q.tiles) * q.units;
     }
-    total = wave_sum(total) * a.c.heads;
-    const int64_t per = (total + target<BQ>() - 1) / target<BQ>();
-    return per > 1 ? per : 1;
+#pragma unroll
+    for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
+    uint64_t per = (total * a.c.heads + target<BQ>() - 1) / target<BQ>();
+    per = per > 1 ? per : 1;
+    per = per < (1u << 30) ? per : 1u << 30;  // (units are fewer)
+    return of_lane(static_cast<uint32_t>(per), 0);
 }
 
+// One of the pairs (tile, head) or items (pair, run of keys) of a launch; uniform in a wave.
 struct Item {
-    int64_t seq, tile, chunk, chunks;
-    int head;
-    int64_t slot;       // of its share (chunks > 1)
-    int64_t begin, end; // keys of the run
+    int64_t seq;
+    uint32_t tiles, chunks;     // of the sequence
+    uint32_t left;              // its number in the sequence
+    uint32_t slot;              // number of its share
 };
-
-// Item `index`, or false past the last.  Heads vary fastest, so that those of one sequence go
-// to different XCDs and a head's tiles to the same one, then tiles, later ones (more keys) first.
-template <int BQ>
-__device__ __forceinline__ bool item_of(const AttArgs &a, int64_t index, int lane, Item &it) {
-    const int64_t per = run_units<BQ>(a, lane);
-    int64_t slots = 0;
+// Item (PAIRS: pair with several runs) `index`, or false past the last.  (A launch has fewer than
+// 2^24: counts are cut to 2^25 so that 64 of them fit.)
+template <int BQ, bool PAIRS>
+__device__ __forceinline__ bool item_of(const AttArgs &a, uint32_t index, uint32_t per, int lane,
+                                        Item &it) {
+    uint32_t slots = 0;
     for (int64_t s = 0; s < a.b.seqs; s += 64) {
         Sequence q = sequence<BQ>(a, s + lane);
         q.chunks = q.units > per ? (q.units + per - 1) / per : 1;
-        const int64_t n = q.tiles * q.chunks * a.c.heads, shared = q.chunks > 1 ? n : 0;
-        const int64_t to = wave_prefix(n, lane), all = __shfl(to, 63);
+        const uint64_t pairs = static_cast<uint64_t>(q.tiles) * a.c.heads;
+        const uint64_t items = pairs * q.chunks, shares = q.chunks > 1 ? items : 0;
+        const auto cut = [](uint64_t v) {
+            return v < (1u << 25) ? static_cast<uint32_t>(v) : 1u << 25;
+        };
+        const uint32_t n = cut(PAIRS ? (q.chunks > 1 ? pairs : 0) : items);
+        const uint32_t to = wave_prefix(n, lane), all = of_lane(to, 63);
+        const uint32_t stop = wave_prefix(cut(shares), lane);
         if (index < all) {
-            const int64_t stop = wave_prefix(shared, lane);
             const int at = __popcll(__ballot(to <= index));  // lanes before the item's
-            const int64_t left = index - (__shfl(to, at) - __shfl(n, at));
-            const int64_t tiles = __shfl(q.tiles, at);
             it.seq = s + at;
-            it.chunks = __shfl(q.chunks, at);
-            it.slot = slots + __shfl(stop, at) - __shfl(shared, at) + left;
-            it.head = static_cast<int>(left % a.c.heads);
-            const int64_t rest = left / a.c.heads;
-            it.tile = tiles - 1 - rest % tiles;
-            it.chunk = rest / tiles;
-            it.begin = it.chunk * per * kUnit;
-            it.end = it.chunk + 1 < it.chunks ? it.begin + per * kUnit : INT64_MAX;
+            it.tiles = of_lane(q.tiles, at);
+            it.chunks = of_lane(q.chunks, at);
+            it.left = index - of_lane(to - n, at);
+            it.slot = slots + of_lane(stop - cut(shares), at) + it.left;
             return true;
         }
         index -= all;
-        slots += wave_sum(shared);
+        slots += of_lane(stop, 63);
     }
     return false;
 }
+
+// What a workgroup computes, uniform.  Heads vary fastest, so that those of one sequence go to
+// different XCDs and a head's tiles to the same one, then tiles, later ones (more keys) first.
+template <int BQ>
+struct Tile {
+    const int32_t *table;       // the sequence's pages
+    int head;
+    int64_t row0;               // the call's row of the sequence's first new token
+    uint32_t rows;              // query rows of the sequence: group to a token
+    uint32_t r0;                // the tile's first
+    int first;                  // position of the sequence's first new token
+    uint32_t begin, end;        // keys of the run that some row of the tile sees
+    uint32_t slot;
+    bool share;
+
+    __device__ __forceinline__ bool init(const AttArgs &a, uint32_t index, int lane) {
+        const uint32_t per = run_units<BQ>(a, lane);
+        Item it;
+        if (!item_of<BQ, false>(a, index, per, lane, it)) return false;
+        set(a, it);
+        share = it.chunks > 1;
+        slot = it.slot;
+        if (share && slot >= a.slots) return false;
+        const uint32_t chunk = it.left / a.c.heads / it.tiles;
+        const uint64_t from = static_cast<uint64_t>(chunk) * per * kUnit;
+        const uint64_t to = chunk + 1 < it.chunks ? from + static_cast<uint64_t>(per) * kUnit
+                                                  : uint64_t{1} << 31;
+        const uint32_t last = (r0 + BQ < rows ? r0 + BQ : rows) - 1;
+        int64_t keys = static_cast<int64_t>(first) + last / a.group + 1;
+        const int64_t most = a.b.width << a.c.page_log2;
+        keys = keys < most ? keys : most;
+        keys = keys < static_cast<int64_t>(to) ? keys : static_cast<int64_t>(to);
+        begin = static_cast<uint32_t>(from);
+        end = keys > 0 ? static_cast<uint32_t>(keys) : 0;
+        return true;
+    }
+    __device__ __forceinline__ void set(const AttArgs &a, const Item &it) {
+        const cache::Span sp = cache::span_of(a.b, it.seq, a.rows);
+        table = a.b.table + it.seq * a.b.ldt;
+        head = static_cast<int>(it.left % a.c.heads);
+        r0 = (it.tiles - 1 - it.left / a.c.heads % it.tiles) * BQ;
+        row0 = sp.begin;
+        rows = static_cast<uint32_t>(sp.end - sp.begin) * static_cast<uint32_t>(a.group);
+        // (positions before -2^24 are as good as -2^24: a sequence has at most 2^23 rows)
+        first = static_cast<int>(sp.first > -(1 << 24) ? sp.first : -(1 << 24));
+    }
+    // The last key that query row r sees, -1 for none.
+    __device__ __forceinline__ int sees(const AttArgs &a, uint32_t r) const {
+        const int64_t p = static_cast<int64_t>(first) + r / a.group;
+        return p < 0 ? -1 : (p < INT32_MAX ? static_cast<int>(p) : INT32_MAX);
+    }
+    // Offset of query row r's vector.
+    __device__ __forceinline__ int64_t at(const AttArgs &a, const CacheRows &x, uint32_t r) const {
+        const uint32_t i = r / a.group;
+        return (row0 + i) * x.row +
+               (static_cast<int64_t>(head) * a.group + (r - i * a.group)) * x.head;
+    }
+};
 
 // ---------------------------------------------------------------- numbers
 
@@ -171,27 +233,47 @@ constexpr int terms() {
     return sizeof(T) == 4 ? 3 : (__is_same(T, _Float16) ? 2 : 1);
 }
 
-// The largest (sum) over the four lanes that hold a query row's keys: lanes l, l ^ 16, l ^ 32.
+// The largest (sum) over the four lanes that hold a query row's keys: lanes l, l ^ 16, l ^ 32,
+// l ^ 48.  A swap of one register with itself leaves each half's values in all lanes.
+template <typename F>
+__device__ __forceinline__ float over_row(float v, const F &f) {
+    const uint32_t u = __float_as_uint(v);
+    const auto halves = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const float w = f(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
+    const uint32_t t = __float_as_uint(w);
+    const auto rows = __builtin_amdgcn_permlane16_swap(t, t, false, false);
+    return f(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
+}
 __device__ __forceinline__ float row_max(float v) {
-    v = __builtin_fmaxf(v, __shfl_xor(v, 16));
-    return __builtin_fmaxf(v, __shfl_xor(v, 32));
+    return over_row(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
 }
 __device__ __forceinline__ float row_sum(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    return over_row(v, [](float a, float b) { return a + b; });
 }
 
-// The running softmax of one query row per lane.
+// The running softmax of one query row per lane.  Weights are taken relative to a score that the
+// largest so far exceeds by at most kSlack (powers of two): sums and outputs are rescaled only
+// when it grows beyond, not at every tile with a new largest score.
 struct Softmax {
-    float top;    // the largest score so far times factor
+    static constexpr float kSlack = 8.0f;
+    float top;    // that score times factor, -inf before the first key
     float sum;    // of this lane's keys
     __device__ __forceinline__ void init() {
         top = -__builtin_inff();
         sum = 0.0f;
     }
-    // What p is taken relative to: 2^-top, and 1 before the first key.
     static __device__ __forceinline__ float safe(float t) {
         return t == -__builtin_inff() ? 0.0f : t;
+    }
+    // Takes a tile's largest score (times factor) along; true if anything is to be multiplied by
+    // alpha (in some lane).
+    __device__ __forceinline__ bool grow(float score, float &alpha) {
+        if (!__any(score > top + kSlack)) return false;
+        const float to = __builtin_fmaxf(score, top);
+        alpha = __builtin_amdgcn_exp2f(top - safe(to));
+        top = to;
+        sum *= alpha;
+        return true;
     }
 };
 
@@ -247,78 +329,83 @@ constexpr int64_t slot_floats() {
     return BQ * (D + 2);
 }
 
-// Four consecutive outputs d .. d + 3 of query row r of the tile: written as they are (a single
-// run) or as a share.
-template <typename T, int BQ, int D>
-struct Output {
-    const AttArgs &a;
-    const Item &it;
-    cache::Span sp;
-    float *slot;
-    __device__ __forceinline__ Output(const AttArgs &a_, const Item &it_, const cache::Span &sp_)
-        : a(a_), it(it_), sp(sp_) {
-        slot = it.chunks > 1 ? a.part + it.slot * slot_floats<BQ, D>() : nullptr;
-    }
-    __device__ __forceinline__ bool room() const { return it.chunks == 1 || it.slot < a.slots; }
-    __device__ __forceinline__ void put(int r, int d, f32x4 o, float top, float sum) const {
-        if (slot) {
-            *reinterpret_cast<f32x4 *>(slot + r * D + d) = o;
-            if (d == 0) {
-                slot[BQ * D + r] = top;
-                slot[BQ * D + BQ + r] = sum;
-            }
-            return;
-        }
-        store(a, it.seq, it.head, it.tile * BQ + r, sp, d, o, sum);
-    }
-    // (a row that saw no key: zeros)
-    static __device__ __forceinline__ void store(const AttArgs &a, int64_t, int head, int64_t r,
-                                                 const cache::Span &sp, int d, f32x4 o,
-                                                 float sum) {
-        const int64_t i = r / a.group, row = sp.begin + i;
-        if (row >= sp.end) return;
-        const int64_t h = static_cast<int64_t>(head) * a.group + (r - i * a.group);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        Packed<T, 4> p;
+// Four consecutive outputs d .. d + 3 of query row r of the sequence; a row that saw no key: zeros.
+template <typename T, int BQ>
+__device__ __forceinline__ void store(const AttArgs &a, const Tile<BQ> &t, uint32_t r, int d, f32x4 o,
+                                      float sum) {
+    if (r >= t.rows) return;
+    const float inv = 1.0f / sum;
+    Packed<T, 4> p;
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-            p.v[v] = static_cast<T>(sum == 0.0f ? 0.0f : o[v] * inv);
-        T *out = static_cast<T *>(const_cast<void *>(a.o.p)) + row * a.o.row + h * a.o.head + d;
-        *reinterpret_cast<Packed<T, 4> *>(out) = p;
+    for (int v = 0; v < 4; ++v) p.v[v] = static_cast<T>(sum == 0.0f ? 0.0f : o[v] * inv);
+    T *out = static_cast<T *>(const_cast<void *>(a.o.p)) + t.at(a, a.o, r) + d;
+    *reinterpret_cast<Packed<T, 4> *>(out) = p;
+}
+
+// The same for row r of the tile: as they are (a single run) or into its share.
+template <typename T, int BQ, int D>
+__device__ __forceinline__ void put(const AttArgs &a, const Tile<BQ> &t, int r, int d, f32x4 o,
+                                    float top, float sum) {
+    if (!t.share) {
+        store<T, BQ>(a, t, t.r0 + r, d, o, sum);
+        return;
     }
-};
+    float *slot = a.part + t.slot * slot_floats<BQ, D>();
+    *reinterpret_cast<f32x4 *>(slot + r * D + d) = o;
+    if (d == 0) {
+        slot[BQ * D + r] = top;
+        slot[BQ * D + BQ + r] = sum;
+    }
+}
 
 // The fragments of query row `r` (this lane's) in terms: place 8 f + v of lane group g holds d =
 // at(f) + v.
-template <typename T, int D, int TERMS, typename At>
-__device__ __forceinline__ void load_query(const AttArgs &a, const Item &it, const cache::Span &sp,
-                                           int64_t r, const At &at, s16x8 (&q)[TERMS][D / 32]) {
-    const int64_t i = r / a.group, row = sp.begin + i;
-    const int64_t h = static_cast<int64_t>(it.head) * a.group + (r - i * a.group);
-    const bool in = row < sp.end;
-    const T *x = static_cast<const T *>(a.q.p) + row * a.q.row + h * a.q.head;
+template <typename T, int D, int TERMS, int BQ, typename At>
+__device__ __forceinline__ void load_query(const AttArgs &a, const Tile<BQ> &t, uint32_t r,
+                                           const At &at, s16x8 (&q)[TERMS][D / 32]) {
+    const bool in = r < t.rows;
+    const T *x = static_cast<const T *>(a.q.p) + t.at(a, a.q, in ? r : t.rows - 1);
 #pragma unroll
     for (int f = 0; f < D / 32; ++f) {
-        float v[8];
-        if (in) {
-            const Packed<T> p = *reinterpret_cast<const Packed<T> *>(x + at(f));
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = static_cast<float>(p.v[k]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-        }
+        const Packed<T> p = *reinterpret_cast<const Packed<T> *>(x + at(f));
         u32x4 w[TERMS];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            uint32_t t[TERMS];
-            terms_of<TERMS>(v[2 * k], v[2 * k + 1], t);
+            uint32_t t2[TERMS];
+            terms_of<TERMS>(in ? static_cast<float>(p.v[2 * k]) : 0.0f,
+                            in ? static_cast<float>(p.v[2 * k + 1]) : 0.0f, t2);
 #pragma unroll
-            for (int n = 0; n < TERMS; ++n) w[n][k] = t[n];
+            for (int n = 0; n < TERMS; ++n) w[n][k] = t2[n];
         }
 #pragma unroll
         for (int n = 0; n < TERMS; ++n) q[n][f] = __builtin_bit_cast(s16x8, w[n]);
     }
+}
+
+// Cache rows of one head: codes and scale bytes of page p's place i lie at p pages and i rows
+// behind the head's first.
+struct HeadCache {
+    const uint8_t *k, *v, *ke, *ve;
+    uint32_t pages;
+    uint32_t code_page, scale_page;     // bytes of a page: below 2^30
+    int log2;
+    uint32_t mask;
+};
+template <int FMT, int D>
+__device__ __forceinline__ HeadCache head_cache(const AttArgs &a, int head) {
+    HeadCache h;
+    const int64_t row = static_cast<int64_t>(head) << a.c.page_log2;
+    h.k = a.c.k_codes + row * mx::bytes<FMT>(D);
+    h.v = a.c.v_codes + row * mx::bytes<FMT>(D);
+    h.ke = a.c.k_scale + row * (D / 32);
+    h.ve = a.c.v_scale + row * (D / 32);
+    h.pages = static_cast<uint32_t>(a.c.pages);
+    const uint32_t rows = static_cast<uint32_t>(a.c.heads) << a.c.page_log2;
+    h.code_page = rows * mx::bytes<FMT>(D);
+    h.scale_page = rows * (D / 32);
+    h.log2 = a.c.page_log2;
+    h.mask = (1u << a.c.page_log2) - 1;
+    return h;
 }
 
 // One 16 x 16 product over 32 keys or dims, smallest term first.
@@ -333,118 +420,123 @@ __device__ __forceinline__ f32x4 mma_terms(const s16x8 &x, const s16x8 (&y)[TERM
 
 // 16 query rows, four waves that take every fourth tile of 32 keys of the run, each with its own
 // softmax; joined in LDS.  Keys go from memory straight into the first operand of S^T (a lane
-// reads a run of D / 4 dims of its key), values through the wave's own piece of LDS.
+// reads a run of D / 4 dims of its key), values through the wave's own piece of LDS.  A tile's
+// codes are asked for while the one before is multiplied, its page numbers one earlier.
 template <typename T, int D, int FMT>
 __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
     constexpr int TERMS = terms<T>();
     constexpr int BQ = kSmallRows;
     constexpr int kRow = mx::bytes<FMT>(D);    // bytes of a cache row
     constexpr int kRun = kRow / 4;             // of it, one lane's
+    constexpr int kKLoads = kRun >= 16 ? kRun / 16 : 1;
     constexpr int kLanes = kRow / 16;          // lanes to a row of values
-    constexpr int kVLoads = 32 * kLanes / 64;
+    constexpr int kPerLoad = 64 / kLanes;      // rows of values to a load
+    constexpr int kVLoads = 32 / kPerLoad;
     constexpr int kGroups = D / 32;
+    constexpr int kKScales = kGroups > 4 ? 2 : 1;
     constexpr int kTiles = D / 16;             // tiles of 16 dims
+    constexpr int kWords = FMT == TCQ_FP4 ? 16 : 8;   // of bf16 pairs in 16 bytes of codes
     __shared__ __align__(16) char lds[4 * 32 * D * 2];
     __shared__ float tops[4][16], sums[4][16];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    Item it;
-    if (!item_of<BQ>(a, blockIdx.x, lane, it)) return;
-    const cache::Span sp = cache::span_of(a.b, it.seq, a.rows);
-    const Output<T, BQ, D> out(a, it, sp);
-    if (!out.room()) return;
-    const int64_t n_rows = (sp.end - sp.begin) * a.group;
-    const int64_t r0 = it.tile * BQ;
-    const int64_t last = r0 + BQ < n_rows ? r0 + BQ - 1 : n_rows - 1;
-    // keys that some row of the tile sees, and those that all do
-    const int64_t capacity = a.b.width << a.c.page_log2;
-    int64_t end = sp.first + last / a.group + 1;
-    end = end < capacity ? end : capacity;
-    end = end < it.end ? end : it.end;
-    const int64_t seen_by_all = sp.first + r0 / a.group + 1;
-    const int64_t mine = sp.first + (r0 + l16) / a.group;  // the last key that this lane's row sees
-
-    s16x8 q[TERMS][kGroups];
-    load_query<T, D, TERMS>(a, it, sp, r0 + l16, [&](int f) { return g * (D / 4) + 8 * f; }, q);
+    Tile<BQ> tile;
+    if (!tile.init(a, blockIdx.x, lane)) return;
+    const HeadCache hc = head_cache<FMT, D>(a, tile.head);
+    const int seen_by_all = tile.sees(a, tile.r0);
+    const int mine = tile.sees(a, tile.r0 + l16);
 
     char *vt = lds + wave * (32 * D * 2);
-    // the cache row of the tile's key t (0 .. 31) is held by lane t; -1: not there
-    auto rows_at = [&](int64_t base) {
-        const int64_t pos = base + (lane & 31);
-        if (pos >= end) return int64_t{-1};
-        const int64_t page = cache::page_of(a.b, a.c, it.seq, pos);
-        return page < 0 ? int64_t{-1} : cache::row_of(a.c, page, it.head, pos);
+    const int part = lane % kLanes;
+    // the page of key base + lane % 32
+    auto find = [&](uint32_t base) {
+        const uint32_t pos = base + (lane & 31);
+        return pos < tile.end ? tile.table[pos >> hc.log2] : -1;
     };
     struct Codes {
-        u32x4 k[2][kRun >= 16 ? kRun / 16 : 1];
-        int ke[2][kGroups > 4 ? 2 : 1];
+        u32x4 k[2][kKLoads];
+        int ke[2][kKScales];
         u32x4 v[kVLoads];
         int ve[kVLoads];
+        uint32_t there;      // bit t: key t of the tile is
     };
-    auto load = [&](int64_t row, Codes &c) {
+    auto load = [&](uint32_t base, int page, Codes &c) {
+        const bool whole = hc.log2 >= 5;   // (tiles start on multiples of 32: one page holds one)
+        c.there = static_cast<uint32_t>(__ballot(static_cast<uint32_t>(page) < hc.pages));
+        const uint32_t all = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(page));
+        auto page_at = [&](int t) {
+            return whole ? all : static_cast<uint32_t>(__shfl(page, t));
+        };
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t r = __shfl(row, 16 * h + l16);
-            const uint8_t *p = a.c.k_codes + r * kRow + g * kRun;
-            const uint8_t *e = a.c.k_scale + r * kGroups + (g * (D / 4)) / 32;
+            const int t = 16 * h + l16;
+            const uint32_t p = page_at(t), i = (base + t) & hc.mask;
 #pragma unroll
-            for (int j = 0; j < (kRun >= 16 ? kRun / 16 : 1); ++j) c.k[h][j] = u32x4{0, 0, 0, 0};
+            for (int j = 0; j < kKLoads; ++j) c.k[h][j] = u32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int j = 0; j < (kGroups > 4 ? 2 : 1); ++j) c.ke[h][j] = 127;
-            if (r >= 0) {
-                if constexpr (kRun >= 16) {
+            for (int j = 0; j < kKScales; ++j) c.ke[h][j] = 127;
+            if (c.there >> t & 1) {
+                const uint8_t *x = hc.k + static_cast<uint64_t>(p) * hc.code_page + i * kRow +
+                                   g * kRun;
+                const uint8_t *e = hc.ke + static_cast<uint64_t>(p) * hc.scale_page +
+                                   i * kGroups + (g * (D / 4)) / 32;
 #pragma unroll
-                    for (int j = 0; j < kRun / 16; ++j)
-                        c.k[h][j] = *reinterpret_cast<const u32x4 *>(p + 16 * j);
-                } else {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-                    c.k[h][0] = u32x4{w.x, w.y, 0, 0};
+                for (int j = 0; j < kKLoads; ++j) {
+                    if constexpr (kRun >= 16) {
+                        c.k[h][j] = *reinterpret_cast<const u32x4 *>(x + 16 * j);
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(x);
+                        c.k[h][j] = u32x4{w.x, w.y, 0, 0};
+                    }
                 }
 #pragma unroll
-                for (int j = 0; j < (kGroups > 4 ? 2 : 1); ++j) c.ke[h][j] = e[j];
+                for (int j = 0; j < kKScales; ++j) c.ke[h][j] = e[j];
             }
         }
 #pragma unroll
         for (int j = 0; j < kVLoads; ++j) {
-            const int64_t r = __shfl(row, j * (64 / kLanes) + lane / kLanes);
-            const int part = lane % kLanes;
+            const int t = j * kPerLoad + lane / kLanes;
+            const uint32_t p = page_at(t), i = (base + t) & hc.mask;
             c.v[j] = u32x4{0, 0, 0, 0};
             c.ve[j] = 127;
-            if (r >= 0) {
-                c.v[j] = *reinterpret_cast<const u32x4 *>(a.c.v_codes + r * kRow + part * 16);
-                c.ve[j] = a.c.v_scale[r * kGroups + part / (kLanes / kGroups)];
+            if (c.there >> t & 1) {
+                c.v[j] = *reinterpret_cast<const u32x4 *>(
+                    hc.v + static_cast<uint64_t>(p) * hc.code_page + i * kRow + part * 16);
+                c.ve[j] = hc.ve[static_cast<uint64_t>(p) * hc.scale_page + i * kGroups +
+                                part / (kLanes / kGroups)];
             }
         }
     };
 
+    uint32_t base = tile.begin + 32 * wave;
+    int page = find(base);
+    Codes now;
+    load(base, page, now);
+    page = find(base + 128);
+    s16x8 q[TERMS][kGroups];
+    load_query<T, D, TERMS>(a, tile, tile.r0 + l16, [&](int f) { return g * (D / 4) + 8 * f; }, q);
     f32x4 acc[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
     Softmax sm;
     sm.init();
-    int64_t base = it.begin + 32 * wave;
-    int64_t row = base < end ? rows_at(base) : -1;
-    Codes now;
-    if (base < end) load(row, now);
-    for (; base < end; base += 128) {
-        const uint32_t there = static_cast<uint32_t>(__ballot(row >= 0));
+    for (; base < tile.end; base += 128) {
+        const uint32_t there = now.there;
         // scores
         f32x4 s[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             s[h] = f32x4{0.f, 0.f, 0.f, 0.f};
             uint32_t w[D / 8];
-            if constexpr (FMT == TCQ_FP8) {
-#pragma unroll
-                for (int j = 0; j < kRun / 16; ++j)
-                    decode16<FMT>(now.k[h][j], mx::scale_of(now.ke[h][j / 2]), w + 8 * j);
-            } else if constexpr (kRun == 8) {
+            if constexpr (kRun < 16) {
                 mx::decode_word_bf16<FMT>(now.k[h][0][0], mx::scale_of(now.ke[h][0]), w);
                 mx::decode_word_bf16<FMT>(now.k[h][0][1], mx::scale_of(now.ke[h][0]), w + 4);
             } else {
+                // (16 bytes of fp8 are half a group)
 #pragma unroll
-                for (int j = 0; j < kRun / 16; ++j)
-                    decode16<FMT>(now.k[h][j], mx::scale_of(now.ke[h][j]), w + 16 * j);
+                for (int j = 0; j < kKLoads; ++j)
+                    decode16<FMT>(now.k[h][j], mx::scale_of(now.ke[h][FMT == TCQ_FP4 ? j : j / 2]),
+                                  w + kWords * j);
             }
 #pragma unroll
             for (int f = 0; f < kGroups; ++f) {
@@ -457,42 +549,35 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
             }
         }
         // values into LDS; what stands for NaN goes in as zero and is added below
-        bool wild = false;
+        uint32_t wild = 0;   // bit j
 #pragma unroll
         for (int j = 0; j < kVLoads; ++j) {
-            const int r = j * (64 / kLanes) + lane / kLanes, part = lane % kLanes;
-            wild |= now.ve[j] == 255;
-            const float sc = mx::scale_of(now.ve[j]);
-            constexpr int kWords = FMT == TCQ_FP4 ? 16 : 8;
-            uint32_t w[kWords];
-            decode16<FMT>(now.v[j], sc, w);
             if (now.ve[j] == 255) {
-#pragma unroll
-                for (int k = 0; k < kWords; ++k) w[k] = 0;
+                wild |= 1u << j;
+                now.v[j] = u32x4{0, 0, 0, 0};
+                now.ve[j] = 127;
             }
+            uint32_t w[kWords];
+            decode16<FMT>(now.v[j], mx::scale_of(now.ve[j]), w);
 #pragma unroll
             for (int u = 0; u < kWords / 8; ++u) {
-                u32x4 *p = reinterpret_cast<u32x4 *>(
-                    unit_at<D * 2>(vt, r, part * (kWords / 8) + u));
+                u32x4 *p = reinterpret_cast<u32x4 *>(unit_at<D * 2>(
+                    vt, j * kPerLoad + lane / kLanes, part * (kWords / 8) + u));
                 p[0] = u32x4{w[8 * u], w[8 * u + 1], w[8 * u + 2], w[8 * u + 3]};
                 p[1] = u32x4{w[8 * u + 4], w[8 * u + 5], w[8 * u + 6], w[8 * u + 7]};
             }
         }
-        int ve[kVLoads];
-#pragma unroll
-        for (int j = 0; j < kVLoads; ++j) ve[j] = now.ve[j];
-        // the next tile's codes
-        const int64_t next = base + 128;
-        const int64_t next_row = next < end ? rows_at(next) : -1;
-        if (next < end) load(next_row, now);
+        load(base + 128, page, now);
+        page = find(base + 256);
         // mask: keys that are not there, and those past this lane's row
         uint32_t sees = 0xFFu;  // bit 4 h + v: key 16 h + 4 g + v
-        if (there != 0xFFFFFFFFu || base + 32 > seen_by_all) {
+        if (there != 0xFFFFFFFFu || static_cast<int64_t>(base) + 31 > seen_by_all) {
             sees = 0;
+            const int to = mine - static_cast<int>(base);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int t = 16 * (i / 4) + 4 * g + i % 4;
-                if ((there >> t & 1) && base + t <= mine) sees |= 1u << i;
+                if ((there >> t & 1) && t <= to) sees |= 1u << i;
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -501,18 +586,19 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
         float top = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = __builtin_fmaxf(top, s[i / 4][i % 4]);
-        top = __builtin_fmaxf(row_max(top) * a.factor, sm.top);
-        const float ref = Softmax::safe(top);
-        const float alpha = __builtin_amdgcn_exp2f(sm.top - ref);
-        sm.top = top;
-        float p[8];
+        float alpha;
+        if (sm.grow(row_max(top) * a.factor, alpha)) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+            for (int t = 0; t < kTiles; ++t) acc[t] *= alpha;
+        }
+        const float ref = Softmax::safe(sm.top);
+        float p[8], add = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
             p[i] = weight<TERMS>(s[i / 4][i % 4], a.factor, a.factor_low, ref);
-        float add = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) add += p[i];
-        sm.sum = __builtin_fmaf(sm.sum, alpha, add);
+            add += p[i];
+        }
+        sm.sum += add;
         s16x8 pf[TERMS];
         {
             u32x4 w[TERMS];
@@ -526,10 +612,6 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
 #pragma unroll
             for (int n = 0; n < TERMS; ++n) pf[n] = __builtin_bit_cast(s16x8, w[n]);
         }
-        if (__any(alpha != 1.0f)) {
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) acc[t] *= alpha;
-        }
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
@@ -540,13 +622,11 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
         if (__builtin_expect(__any(wild), 0)) {
 #pragma unroll
             for (int j = 0; j < kVLoads; ++j) {
-                const int r = j * (64 / kLanes) + lane / kLanes, part = lane % kLanes;
-                constexpr int kUnits = FMT == TCQ_FP4 ? 2 : 1;
-                const uint32_t w = ve[j] == 255 ? 0x3F803F80u : 0u;
+                const uint32_t w = wild >> j & 1 ? 0x3F803F80u : 0u;
 #pragma unroll
-                for (int u = 0; u < kUnits; ++u) {
-                    u32x4 *d = reinterpret_cast<u32x4 *>(
-                        unit_at<D * 2>(vt, r, part * kUnits + u));
+                for (int u = 0; u < kWords / 8; ++u) {
+                    u32x4 *d = reinterpret_cast<u32x4 *>(unit_at<D * 2>(
+                        vt, j * kPerLoad + lane / kLanes, part * (kWords / 8) + u));
                     d[0] = d[1] = u32x4{w, w, w, w};
                 }
             }
@@ -567,7 +647,6 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
             }
             __builtin_amdgcn_wave_barrier();
         }
-        row = next_row;
     }
     // join the waves
     const float sum = row_sum(sm.sum);
@@ -595,94 +674,142 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
             total = __builtin_fmaf(sums[w][r], f, total);
             o += v * f;
         }
-        out.put(r, d4 * 4, o, top, total);
+        put<T, BQ, D>(a, tile, r, d4 * 4, o, top, total);
     }
 }
 
 // ---------------------------------------------------------------- many query rows
 
-// 128 query rows, two tiles of 16 to each of four waves, and tiles of 64 keys that the workgroup's
-// threads decode into LDS for all waves, with the next tile's codes on their way.
+// 128 query rows, two tiles of 16 to each of four waves.  The workgroup's threads decode tiles of
+// keys into LDS for all waves: while a tile is multiplied, the next one's codes, which arrived
+// during the tile before, go into the other half of LDS, and those of the one after are asked for.
 constexpr int kLargeRows = 128;
+// Two waves to a SIMD, one's softmax beside the other's products, where outputs, queries and
+// scores leave room for that in the registers.
+template <int D, int TERMS>
+constexpr int many_waves() {
+    return D / 2 + D / 4 * TERMS <= 128 ? 2 : 1;
+}
 
 template <typename T, int D, int FMT>
-__global__ __launch_bounds__(256) void attend_many_kernel(AttArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(
+    many_waves<D, terms<T>()>(), many_waves<D, terms<T>()>()))) void
+attend_many_kernel(AttArgs a) {
     constexpr int TERMS = terms<T>();
     constexpr int NQ = 2, BQ = kLargeRows;
     static_assert(BQ == 4 * NQ * 16, "four waves");
+    constexpr int KT = D == 256 ? 32 : 64;                     // keys of a tile
+    constexpr int kSub = KT / 16, kPairs = KT / 32;
     constexpr int kRow = mx::bytes<FMT>(D);
     constexpr int kLanes = kRow / 16;
     constexpr int kGroups = D / 32;
     constexpr int kTiles = D / 16;
-    constexpr int kPieces = 64 * kLanes;                       // of 16 bytes, of a tile
+    constexpr int kPieces = KT * kLanes;                       // of 16 bytes, of a tile
     constexpr int kLoads = (kPieces + 255) / 256;
     constexpr int kWords = FMT == TCQ_FP4 ? 16 : 8;            // of bf16 pairs to a piece
-    __shared__ __align__(16) char kt[64 * D * 2];
-    __shared__ __align__(16) char vt[64 * D * 2];
-    __shared__ unsigned long long absent_of[2];
-    __shared__ int wild_of[2];
+    constexpr int kTileBytes = KT * D * 2;
+    __shared__ __align__(16) char kt[2 * kTileBytes];
+    __shared__ __align__(16) char vt[2 * kTileBytes];
+    // of the tile at hand, the one being staged and the one before, in turn
+    __shared__ unsigned long long absent_of[3];
+    __shared__ int wild_of[3];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    Item it;
-    if (!item_of<BQ>(a, blockIdx.x, lane, it)) return;
-    const cache::Span sp = cache::span_of(a.b, it.seq, a.rows);
-    const Output<T, BQ, D> out(a, it, sp);
-    if (!out.room()) return;
-    const int64_t n_rows = (sp.end - sp.begin) * a.group;
-    const int64_t r0 = it.tile * BQ + wave * (NQ * 16);
-    const int64_t tile_last = it.tile * BQ + BQ < n_rows ? it.tile * BQ + BQ - 1 : n_rows - 1;
-    const int64_t capacity = a.b.width << a.c.page_log2;
-    int64_t end = sp.first + tile_last / a.group + 1;
-    end = end < capacity ? end : capacity;
-    end = end < it.end ? end : it.end;
-    const int64_t seen_by_all = sp.first + r0 / a.group + 1;
-    int64_t mine[NQ];
+    Tile<BQ> tile;
+    if (!tile.init(a, blockIdx.x, lane)) return;
+    const HeadCache hc = head_cache<FMT, D>(a, tile.head);
+    const uint32_t r0 = tile.r0 + wave * (NQ * 16);
+    const int seen_by_all = tile.sees(a, r0);
+    int mine[NQ];
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) mine[n] = sp.first + (r0 + 16 * n + l16) / a.group;
-    s16x8 q[NQ][TERMS][kGroups];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n)
-        load_query<T, D, TERMS>(a, it, sp, r0 + 16 * n + l16,
-                                [&](int f) { return 32 * f + 8 * g; }, q[n]);
+    for (int n = 0; n < NQ; ++n) mine[n] = tile.sees(a, r0 + 16 * n + l16);
 
-    // pieces of this thread: key p / kLanes, bytes 16 (p % kLanes) of its row
-    struct Codes {
-        int64_t row[kLoads];
-        u32x4 k[kLoads], v[kLoads];
-        int ke[kLoads], ve[kLoads];
-    } now;
-    auto find = [&](int64_t base) {
+    // Pieces of this thread: key p / kLanes of a tile, bytes 16 (p % kLanes) of its row.
+    const int part = tid % kLanes;
+    static_assert(256 % kLanes == 0, "a thread's pieces are the same part of their rows");
+    int32_t page[kLoads];   // of the keys to be asked for next
+    auto find = [&](uint32_t base) {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            const int p = j * 256 + tid;
-            const int64_t pos = base + p / kLanes;
-            now.row[j] = -1;
-            if (p < kPieces && pos < end) {
-                const int64_t page = cache::page_of(a.b, a.c, it.seq, pos);
-                if (page >= 0) now.row[j] = cache::row_of(a.c, page, it.head, pos);
-            }
+            const uint32_t pos = base + (j * 256 + tid) / kLanes;
+            page[j] = -1;
+            if ((kPieces % 256 == 0 || tid < kPieces) && pos < tile.end)
+                page[j] = tile.table[pos >> hc.log2];
         }
     };
-    auto load = [&] {
+    struct Codes {
+        u32x4 k[kLoads], v[kLoads];
+        int ke[kLoads], ve[kLoads];
+        uint32_t there;     // bit j
+    } now;
+    auto load = [&](uint32_t base) {
+        now.there = 0;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            const int part = (j * 256 + tid) % kLanes;
             now.k[j] = now.v[j] = u32x4{0, 0, 0, 0};
             now.ke[j] = now.ve[j] = 127;
-            if (now.row[j] >= 0) {
-                const int64_t at = now.row[j] * kRow + part * 16;
-                const int64_t e = now.row[j] * kGroups + part / (kLanes / kGroups);
-                now.k[j] = *reinterpret_cast<const u32x4 *>(a.c.k_codes + at);
-                now.v[j] = *reinterpret_cast<const u32x4 *>(a.c.v_codes + at);
-                now.ke[j] = a.c.k_scale[e];
-                now.ve[j] = a.c.v_scale[e];
+            const uint32_t p = static_cast<uint32_t>(page[j]);
+            if (p < hc.pages) {
+                const uint32_t i = (base + (j * 256 + tid) / kLanes) & hc.mask;
+                const uint64_t at = static_cast<uint64_t>(p) * hc.code_page + i * kRow + part * 16;
+                const uint64_t e = static_cast<uint64_t>(p) * hc.scale_page + i * kGroups +
+                                   part / (kLanes / kGroups);
+                now.k[j] = *reinterpret_cast<const u32x4 *>(hc.k + at);
+                now.v[j] = *reinterpret_cast<const u32x4 *>(hc.v + at);
+                now.ke[j] = hc.ke[e];
+                now.ve[j] = hc.ve[e];
+                now.there |= 1u << j;
             }
         }
     };
     // K: 16-byte chunks of a row permuted by the row
-    auto chunk_at = [&](int row, int chunk) {
-        return reinterpret_cast<u32x4 *>(kt + row * (D * 2) + (chunk ^ (row & 7)) * 16);
+    auto chunk_at = [&](int half, int row, int chunk) {
+        return reinterpret_cast<u32x4 *>(kt + half * kTileBytes + row * (D * 2) +
+                                         (chunk ^ (row & 7)) * 16);
     };
+    // The codes at hand into half `half` of LDS.  What stands for NaN in V goes in as zero and is
+    // added later; returns which pieces do (bit j).
+    auto stage = [&](int half, int turn) {
+        uint32_t wild = 0;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int p = j * 256 + tid, r = p / kLanes;
+            if (kPieces % 256 == 0 || p < kPieces) {
+                if (!(now.there >> j & 1)) atomicOr(&absent_of[turn], 1ull << r);
+                uint32_t w[kWords];
+                decode16<FMT>(now.k[j], mx::scale_of(now.ke[j]), w);
+#pragma unroll
+                for (int u = 0; u < kWords / 4; ++u)
+                    *chunk_at(half, r, part * (kWords / 4) + u) =
+                        u32x4{w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]};
+                if (now.ve[j] == 255) {
+                    wild |= 1u << j;
+                    now.v[j] = u32x4{0, 0, 0, 0};
+                }
+                decode16<FMT>(now.v[j], mx::scale_of(now.ve[j] == 255 ? 127 : now.ve[j]), w);
+#pragma unroll
+                for (int u = 0; u < kWords / 8; ++u) {
+                    u32x4 *d = reinterpret_cast<u32x4 *>(unit_at<D * 2>(
+                        vt + half * kTileBytes, r, part * (kWords / 8) + u));
+                    d[0] = u32x4{w[8 * u], w[8 * u + 1], w[8 * u + 2], w[8 * u + 3]};
+                    d[1] = u32x4{w[8 * u + 4], w[8 * u + 5], w[8 * u + 6], w[8 * u + 7]};
+                }
+            }
+        }
+        if (wild) wild_of[turn] = 1;
+        return wild;
+    };
+
+    if (tid < 3) absent_of[tid] = 0, wild_of[tid] = 0;
+    uint32_t base = tile.begin;
+    find(base);
+    load(base);
+    find(base + KT);
+    s16x8 q[NQ][TERMS][kGroups];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+        load_query<T, D, TERMS>(a, tile, r0 + 16 * n + l16,
+                                [&](int f) { return 32 * f + 8 * g; }, q[n]);
     f32x4 acc[NQ][kTiles];
     Softmax sm[NQ];
 #pragma unroll
@@ -691,66 +818,28 @@ __global__ __launch_bounds__(256) void attend_many_kernel(AttArgs a) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) acc[n][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    int64_t base = it.begin;
-    if (base < end) {
-        find(base);
-        load();
-    }
-    if (tid < 2) absent_of[tid] = 0, wild_of[tid] = 0;
+    __syncthreads();
+    uint32_t wild = stage(0, 0);
+    load(base + KT);
+    find(base + 2 * KT);
     __syncthreads();
     int turn = 0;
-    for (; base < end; base += 64, turn ^= 1) {
-        // codes into LDS
-        bool wild = false;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            const int p = j * 256 + tid;
-            const int r = p / kLanes, part = p % kLanes;
-            if (p < kPieces) {
-                if (now.row[j] < 0) atomicOr(&absent_of[turn], 1ull << r);
-                uint32_t w[kWords];
-                decode16<FMT>(now.k[j], mx::scale_of(now.ke[j]), w);
-#pragma unroll
-                for (int u = 0; u < kWords / 4; ++u)
-                    *chunk_at(r, part * (kWords / 4) + u) =
-                        u32x4{w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]};
-                decode16<FMT>(now.v[j], mx::scale_of(now.ve[j]), w);
-                if (now.ve[j] == 255) {
-                    wild = true;
-#pragma unroll
-                    for (int k = 0; k < kWords; ++k) w[k] = 0;
-                }
-#pragma unroll
-                for (int u = 0; u < kWords / 8; ++u) {
-                    u32x4 *d = reinterpret_cast<u32x4 *>(
-                        unit_at<D * 2>(vt, r, part * (kWords / 8) + u));
-                    d[0] = u32x4{w[8 * u], w[8 * u + 1], w[8 * u + 2], w[8 * u + 3]};
-                    d[1] = u32x4{w[8 * u + 4], w[8 * u + 5], w[8 * u + 6], w[8 * u + 7]};
-                }
-            }
-        }
-        if (__any(wild) && lane == 0) wild_of[turn] = 1;
-        int ve[kLoads];
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) ve[j] = now.ve[j];
-        __syncthreads();
-        const uint64_t there = ~absent_of[turn];
+    for (int half = 0; base < tile.end; base += KT, half ^= 1) {
+        const int next = turn == 2 ? 0 : turn + 1, before = turn == 0 ? 2 : turn - 1;
+        const uint64_t absent = absent_of[turn];
         const bool any_wild = wild_of[turn] != 0;
-        const int64_t next = base + 64;
-        if (next < end) {
-            find(next);
-            load();
-        }
-        // scores of 64 keys
-        f32x4 s[NQ][4];
+        if (tid == 0) absent_of[before] = 0, wild_of[before] = 0;
+        const uint32_t wild_here = wild;
+        // scores
+        f32x4 s[NQ][kSub];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
+        for (int h = 0; h < kSub; ++h) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n) s[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int f = 0; f < kGroups; ++f) {
                 const s16x8 x =
-                    __builtin_bit_cast(s16x8, *chunk_at(16 * h + l16, 4 * f + g));
+                    __builtin_bit_cast(s16x8, *chunk_at(half, 16 * h + l16, 4 * f + g));
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
                     s16x8 y[TERMS];
@@ -760,39 +849,46 @@ __global__ __launch_bounds__(256) void attend_many_kernel(AttArgs a) {
                 }
             }
         }
-        s16x8 pf[NQ][2][TERMS];
+        // (the other half was read before the last meeting)
+        wild = stage(half ^ 1, next);
+        load(base + 2 * KT);
+        find(base + 3 * KT);
+        s16x8 pf[NQ][kPairs][TERMS];
         uint32_t sees[NQ];
+        const bool partial = absent != 0 || static_cast<int64_t>(base) + KT - 1 > seen_by_all;
 #pragma unroll
         for (int n = 0; n < NQ; ++n) {
-            sees[n] = 0xFFFFu;  // bit 4 h + v: key 16 h + 4 g + v
-            if (there != ~0ull || base + 64 > seen_by_all) {
+            sees[n] = ~0u;  // bit 4 h + v: key 16 h + 4 g + v
+            if (partial) {
                 sees[n] = 0;
+                const int to = mine[n] - static_cast<int>(base);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < 4 * kSub; ++i) {
                     const int t = 16 * (i / 4) + 4 * g + i % 4;
-                    if ((there >> t & 1) && base + t <= mine[n]) sees[n] |= 1u << i;
+                    if (!(absent >> t & 1) && t <= to) sees[n] |= 1u << i;
                 }
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 4 * kSub; ++i)
                     if (!(sees[n] >> i & 1)) s[n][i / 4][i % 4] = -__builtin_inff();
             }
             float top = -__builtin_inff();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = __builtin_fmaxf(top, s[n][i / 4][i % 4]);
-            top = __builtin_fmaxf(row_max(top) * a.factor, sm[n].top);
-            const float ref = Softmax::safe(top);
-            const float alpha = __builtin_amdgcn_exp2f(sm[n].top - ref);
-            sm[n].top = top;
-            float add = 0.0f;
-            float p[16];
+            for (int i = 0; i < 4 * kSub; ++i) top = __builtin_fmaxf(top, s[n][i / 4][i % 4]);
+            float alpha;
+            if (sm[n].grow(row_max(top) * a.factor, alpha)) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+                for (int t = 0; t < kTiles; ++t) acc[n][t] *= alpha;
+            }
+            const float ref = Softmax::safe(sm[n].top);
+            float p[4 * kSub], add = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4 * kSub; ++i) {
                 p[i] = weight<TERMS>(s[n][i / 4][i % 4], a.factor, a.factor_low, ref);
                 add += p[i];
             }
-            sm[n].sum = __builtin_fmaf(sm[n].sum, alpha, add);
+            sm[n].sum += add;
 #pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
+            for (int k2 = 0; k2 < kPairs; ++k2) {
                 u32x4 w[TERMS];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -804,33 +900,29 @@ __global__ __launch_bounds__(256) void attend_many_kernel(AttArgs a) {
 #pragma unroll
                 for (int m = 0; m < TERMS; ++m) pf[n][k2][m] = __builtin_bit_cast(s16x8, w[m]);
             }
-            if (__any(alpha != 1.0f)) {
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) acc[n][t] *= alpha;
-            }
         }
+        const char *vh = vt + half * kTileBytes;
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
 #pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
-                const s16x8 x = read_across<D * 2>(vt, 32 * k2, t, lane);
+            for (int k2 = 0; k2 < kPairs; ++k2) {
+                const s16x8 x = read_across<D * 2>(vh, 32 * k2, t, lane);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) acc[n][t] = mma_terms<TERMS>(x, pf[n][k2], acc[n][t]);
             }
         }
-        if (tid == 0) absent_of[turn ^ 1] = 0, wild_of[turn ^ 1] = 0;
         __syncthreads();
-        // values that stand for NaN, as in attend_few_kernel
+        // Values that stand for NaN, as in attend_few_kernel: the same product over ones.
         if (__builtin_expect(any_wild, 0)) {
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
                 const int p = j * 256 + tid;
                 if (p < kPieces) {
-                    const uint32_t w = ve[j] == 255 ? 0x3F803F80u : 0u;
+                    const uint32_t w = wild_here >> j & 1 ? 0x3F803F80u : 0u;
 #pragma unroll
                     for (int u = 0; u < kWords / 8; ++u) {
-                        u32x4 *d = reinterpret_cast<u32x4 *>(
-                            unit_at<D * 2>(vt, p / kLanes, (p % kLanes) * (kWords / 8) + u));
+                        u32x4 *d = reinterpret_cast<u32x4 *>(unit_at<D * 2>(
+                            vt + half * kTileBytes, p / kLanes, part * (kWords / 8) + u));
                         d[0] = d[1] = u32x4{w, w, w, w};
                     }
                 }
@@ -839,7 +931,7 @@ __global__ __launch_bounds__(256) void attend_many_kernel(AttArgs a) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-                for (int k2 = 0; k2 < 2; ++k2) {
+                for (int k2 = 0; k2 < kPairs; ++k2) {
                     u32x4 ones;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -848,7 +940,7 @@ __global__ __launch_bounds__(256) void attend_many_kernel(AttArgs a) {
 #pragma unroll
                     for (int t = 0; t < kTiles; ++t) {
                         const f32x4 c = gemm::Traits<__bf16>::mma(
-                            read_across<D * 2>(vt, 32 * k2, t, lane),
+                            read_across<D * 2>(vh, 32 * k2, t, lane),
                             __builtin_bit_cast(s16x8, ones), f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
                         for (int v = 0; v < 4; ++v)
@@ -858,13 +950,15 @@ __global__ __launch_bounds__(256) void attend_many_kernel(AttArgs a) {
             }
             __syncthreads();
         }
+        turn = next;
     }
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
         const float sum = row_sum(sm[n].sum);
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
-            out.put(wave * (NQ * 16) + 16 * n + l16, 16 * t + 4 * g, acc[n][t], sm[n].top, sum);
+            put<T, BQ, D>(a, tile, wave * (NQ * 16) + 16 * n + l16, 16 * t + 4 * g, acc[n][t],
+                          sm[n].top, sum);
     }
 }
 
@@ -874,58 +968,39 @@ __global__ __launch_bounds__(256) void attend_many_kernel(AttArgs a) {
 // added in the order of the runs.
 constexpr int kJoinRows = 16;    // rows to a workgroup of four waves
 template <typename T, int D, int BQ>
-__device__ __forceinline__ void join(const AttArgs &a, int64_t block) {
+__device__ __forceinline__ void join(const AttArgs &a, uint32_t block) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     constexpr int kParts = BQ / kJoinRows;
-    // (tile of rows with several runs) number `block / kParts`
-    const int64_t per = run_units<BQ>(a, lane);
-    int64_t index = block / kParts, slots = 0;
-    for (int64_t s = 0; s < a.b.seqs; s += 64) {
-        Sequence q = sequence<BQ>(a, s + lane);
-        q.chunks = q.units > per ? (q.units + per - 1) / per : 1;
-        const int64_t pairs = q.chunks > 1 ? q.tiles * a.c.heads : 0, n = pairs * q.chunks;
-        const int64_t to = wave_prefix(pairs, lane), all = __shfl(to, 63);
-        if (index >= all) {
-            index -= all;
-            slots += wave_sum(n);
-            continue;
+    Item it;
+    const uint32_t per = run_units<BQ>(a, lane);
+    if (!item_of<BQ, true>(a, block / kParts, per, lane, it)) return;
+    Tile<BQ> tile;
+    tile.set(a, it);
+    // a pair's shares: one run's are a sequence's pairs apart
+    const uint32_t pairs = it.tiles * a.c.heads;
+    if (it.slot + static_cast<uint64_t>(it.chunks - 1) * pairs >= a.slots) return;
+    const float *slot = a.part + it.slot * slot_floats<BQ, D>();
+    const int64_t step = pairs * slot_floats<BQ, D>();
+    const int d = lane * 4;
+    for (int i = wave; i < kJoinRows; i += 4) {
+        const int r = static_cast<int>(block % kParts) * kJoinRows + i;
+        if (tile.r0 + r >= tile.rows) break;
+        float top = -__builtin_inff();
+        for (uint32_t c = lane; c < it.chunks; c += 64)
+            top = __builtin_fmaxf(top, slot[c * step + BQ * D + r]);
+#pragma unroll
+        for (int x = 32; x; x >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x));
+        const float ref = Softmax::safe(top);
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        float total = 0.0f;
+#pragma unroll 8
+        for (uint32_t c = 0; c < it.chunks; ++c) {
+            const float *p = slot + c * step;
+            const float f = __builtin_amdgcn_exp2f(p[BQ * D + r] - ref);
+            total = __builtin_fmaf(p[BQ * D + BQ + r], f, total);
+            if (d < D) o += *reinterpret_cast<const f32x4 *>(p + r * D + d) * f;
         }
-        const int64_t stop = wave_prefix(n, lane);
-        const int at = __popcll(__ballot(to <= index));
-        const int64_t left = index - (__shfl(to, at) - __shfl(pairs, at));
-        const int64_t tiles = __shfl(q.tiles, at), chunks = __shfl(q.chunks, at);
-        const int64_t heads = a.c.heads;
-        // slots of the pair: first + chunk (tiles x heads)
-        const int64_t first = slots + __shfl(stop, at) - __shfl(n, at) + left;
-        const int head = static_cast<int>(left % heads);
-        const int64_t tile = tiles - 1 - left / heads;
-        const int64_t stride = tiles * heads;
-        if (first + (chunks - 1) * stride >= a.slots) return;
-        const cache::Span sp = cache::span_of(a.b, s + at, a.rows);
-        for (int i = wave; i < kJoinRows; i += 4) {
-            const int r = static_cast<int>(block % kParts) * kJoinRows + i;
-            if (tile * BQ + r >= (sp.end - sp.begin) * a.group) break;
-            const float *slot = a.part + first * slot_floats<BQ, D>();
-            const int64_t step = stride * slot_floats<BQ, D>();
-            float top = -__builtin_inff();
-            for (int64_t c = lane; c < chunks; c += 64)
-                top = __builtin_fmaxf(top, slot[c * step + BQ * D + r]);
-            for (int d = 32; d; d >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-            const float ref = Softmax::safe(top);
-            const int d = lane * 4;
-            f32x4 o = {0.f, 0.f, 0.f, 0.f};
-            float total = 0.0f;
-#pragma unroll 4
-            for (int64_t c = 0; c < chunks; ++c) {
-                const float *p = slot + c * step;
-                const float f = __builtin_amdgcn_exp2f(p[BQ * D + r] - ref);
-                total = __builtin_fmaf(p[BQ * D + BQ + r], f, total);
-                if (d < D) o += *reinterpret_cast<const f32x4 *>(p + r * D + d) * f;
-            }
-            if (d < D)
-                Output<T, BQ, D>::store(a, s + at, head, tile * BQ + r, sp, d, o, total);
-        }
-        return;
+        if (d < D) store<T, BQ>(a, tile, tile.r0 + r, d, o, total);
     }
 }
 template <typename T, int D>
@@ -947,7 +1022,7 @@ bool few_only(int64_t rows, int group, int64_t seqs) {
 
 // Shares: a sequence has several runs only where they are whole runs of about total / target
 // units, so there are at most twice the target.
-constexpr int64_t kSlotsFew = 2 * kTargetSmall, kSlotsMany = 2 * kTargetLarge;
+constexpr int kSlotsFew = 2 * kTargetSmall, kSlotsMany = 2 * kTargetLarge;
 
 int64_t slot_bytes(int bq, int dim) { return int64_t{bq} * (dim + 2) * 4; }
 
@@ -959,7 +1034,7 @@ hipError_t attend(const AttArgs &base, char *ws, hipStream_t s) {
     few.both = many.both = !only;
     few.part = reinterpret_cast<float *>(ws);
     few.slots = kSlotsFew;
-    many.part = reinterpret_cast<float *>(ws + kSlotsFew * slot_bytes(kSmallRows, D));
+    many.part = reinterpret_cast<float *>(ws + int64_t{kSlotsFew} * slot_bytes(kSmallRows, D));
     many.slots = kSlotsMany;
     // tiles of all sequences: whole ones of the rows, and a part of one for each
     const int64_t qrows = base.rows * base.group;
