@@ -55,7 +55,7 @@ struct Sequence {
 };
 constexpr int kUnit = 128;      // keys: runs are whole units
 constexpr int kSmallRows = 16;
-constexpr int kTargetSmall = 1024, kTargetLarge = 512;
+constexpr int kTargetSmall = 1024, kTargetLarge = 256;
 template <int BQ>
 constexpr int target() {
     return BQ == kSmallRows ? kTargetSmall : kTargetLarge;
@@ -175,7 +175,7 @@ struct Tile {
                                                   : uint64_t{1} << 31;
         const uint32_t last = (r0 + BQ < rows ? r0 + BQ : rows) - 1;
         int64_t keys = static_cast<int64_t>(first) + last / a.group + 1;
-        const int64_t most = a.b.width << a.c.page_log2;
+        const int64_t most = a.c.pages > 0 ? a.b.width << a.c.page_log2 : 0;
         keys = keys < most ? keys : most;
         keys = keys < static_cast<int64_t>(to) ? keys : static_cast<int64_t>(to);
         begin = static_cast<uint32_t>(from);
@@ -288,29 +288,34 @@ __device__ __forceinline__ float weight(float s, float factor, float low, float 
     return __builtin_amdgcn_exp2f(e);
 }
 
-// Reads A = X^T (16 columns from unit `unit` of 32 bytes, 32 rows r0 ..) from a tile of X in LDS,
-// rows of W bytes, whose units are permuted by the row: row 4 g + i in place i and row 16 + 4 g
-// + i in place 4 + i of lane group g.
+// Tiles in LDS have rows of W bytes (D bf16 numbers) whose pieces are permuted by the low bits of
+// the row: a key's 16-byte chunks (read 16 rows at a time) and a value's 32-byte units (read
+// across, eight rows at a time).  The permutation is an exclusive or of the offset's bits, so one
+// offset per thread and an exclusive or with a constant give every address.
 template <int W>
-__device__ __forceinline__ s16x8 read_across(const char *lds, int r0, int unit, int lane) {
+struct Units {
+    static constexpr int kMask = W / 32 < 8 ? W / 32 - 1 : 7;
+    // Offset of unit 0 of row r; unit u's is it ^ 32 u.
+    static __device__ __forceinline__ int row(int r) { return r * W + (r & kMask) * 32; }
+    // What lane `lane` reads from to get 32 rows across: columns 16 u .. 16 u + 15 with ^ 32 u.
+    static __device__ __forceinline__ int across(int lane) {
+        const int l16 = lane & 15;
+        return row(4 * (lane >> 4) + (l16 >> 2)) + (l16 & 3) * 8;
+    }
+};
+// A = X^T of 16 columns and 32 rows: row 4 g + i of them in place i and row 16 + 4 g + i in place 4 +
+// i of lane group g.
+template <int W>
+__device__ __forceinline__ s16x8 read_across(const char *at) {
     typedef __attribute__((address_space(3))) s16x4 *P;
-    constexpr int kMask = W / 32 < 8 ? W / 32 - 1 : 7;
-    const int l16 = lane & 15, g = lane >> 4;
     s16x8 out;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int r = 16 * h + 4 * g + (l16 >> 2);
-        const char *p = lds + (r0 + r) * W + (unit ^ (r & kMask)) * 32 + (l16 & 3) * 8;
-        const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)p);
+        const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(at + h * 16 * W));
 #pragma unroll
         for (int v = 0; v < 4; ++v) out[h * 4 + v] = t[v];
     }
     return out;
-}
-template <int W>
-__device__ __forceinline__ char *unit_at(char *lds, int row, int unit) {
-    constexpr int kMask = W / 32 < 8 ? W / 32 - 1 : 7;
-    return lds + row * W + (unit ^ (row & kMask)) * 32;
 }
 
 // 16 bytes of codes (16 of fp8, 32 of fp4) to bf16 words.
@@ -416,6 +421,28 @@ __device__ __forceinline__ f32x4 mma_terms(const s16x8 &x, const s16x8 (&y)[TERM
     return c;
 }
 
+// acc += x p for a tile of values among which some stand for NaN, where a row does not see every key
+// (bit i of sees: the key in the lane's place i): a NaN reaches the rows that see its key, whatever
+// p, and no other (0 times NaN would).  The rows it reaches are those whose count of NaN keys, the
+// product of ones, is not zero.
+template <int TERMS>
+__device__ __forceinline__ void add_wild(const s16x8 &x, const s16x8 (&p)[TERMS], uint32_t sees,
+                                         f32x4 &acc) {
+    s16x8 clean, nan, ones;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool bad = (x[i] & 0x7FFF) > 0x7F80;
+        clean[i] = bad ? 0 : x[i];
+        nan[i] = bad ? 0x3F80 : 0;
+        ones[i] = sees >> i & 1 ? 0x3F80 : 0;
+    }
+    const f32x4 n = gemm::Traits<__bf16>::mma(nan, ones, f32x4{0.f, 0.f, 0.f, 0.f});
+    acc = mma_terms<TERMS>(clean, p, acc);
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        if (n[v] != 0.0f) acc[v] = __builtin_nanf("");
+}
+
 // ---------------------------------------------------------------- few query rows
 
 // 16 query rows, four waves that take every fourth tile of 32 keys of the run, each with its own
@@ -448,10 +475,15 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
 
     char *vt = lds + wave * (32 * D * 2);
     const int part = lane % kLanes;
-    // the page of key base + lane % 32
+    // (row j kPerLoad + lane / kLanes, whose low bits j takes part in)
+    auto to_lds = [&](int j) {
+        return Units<D * 2>::row(j * kPerLoad + lane / kLanes) ^ (part * (kWords / 8) * 32);
+    };
+    const int from_lds = Units<D * 2>::across(lane);
+    // the page of key base + lane % 32 (past the end: the last one's)
     auto find = [&](uint32_t base) {
         const uint32_t pos = base + (lane & 31);
-        return pos < tile.end ? tile.table[pos >> hc.log2] : -1;
+        return tile.table[(pos < tile.end ? pos : tile.end - 1) >> hc.log2];
     };
     struct Codes {
         u32x4 k[2][kKLoads];
@@ -460,9 +492,12 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
         int ve[kVLoads];
         uint32_t there;      // bit t: key t of the tile is
     };
+    // (keys that are not there read the cache's first bytes, and are masked)
     auto load = [&](uint32_t base, int page, Codes &c) {
         const bool whole = hc.log2 >= 5;   // (tiles start on multiples of 32: one page holds one)
-        c.there = static_cast<uint32_t>(__ballot(static_cast<uint32_t>(page) < hc.pages));
+        const bool in = static_cast<uint32_t>(page) < hc.pages && base + (lane & 31) < tile.end;
+        c.there = static_cast<uint32_t>(__ballot(in));
+        page = in ? page : 0;
         const uint32_t all = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(page));
         auto page_at = [&](int t) {
             return whole ? all : static_cast<uint32_t>(__shfl(page, t));
@@ -471,48 +506,41 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
         for (int h = 0; h < 2; ++h) {
             const int t = 16 * h + l16;
             const uint32_t p = page_at(t), i = (base + t) & hc.mask;
+            const uint8_t *x =
+                hc.k + static_cast<uint64_t>(p) * hc.code_page + i * kRow + g * kRun;
+            const uint8_t *e = hc.ke + static_cast<uint64_t>(p) * hc.scale_page + i * kGroups +
+                               (g * (D / 4)) / 32;
 #pragma unroll
-            for (int j = 0; j < kKLoads; ++j) c.k[h][j] = u32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < kKScales; ++j) c.ke[h][j] = 127;
-            if (c.there >> t & 1) {
-                const uint8_t *x = hc.k + static_cast<uint64_t>(p) * hc.code_page + i * kRow +
-                                   g * kRun;
-                const uint8_t *e = hc.ke + static_cast<uint64_t>(p) * hc.scale_page +
-                                   i * kGroups + (g * (D / 4)) / 32;
-#pragma unroll
-                for (int j = 0; j < kKLoads; ++j) {
-                    if constexpr (kRun >= 16) {
-                        c.k[h][j] = *reinterpret_cast<const u32x4 *>(x + 16 * j);
-                    } else {
-                        const uint2 w = *reinterpret_cast<const uint2 *>(x);
-                        c.k[h][j] = u32x4{w.x, w.y, 0, 0};
-                    }
+            for (int j = 0; j < kKLoads; ++j) {
+                if constexpr (kRun >= 16) {
+                    c.k[h][j] = *reinterpret_cast<const u32x4 *>(x + 16 * j);
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(x);
+                    c.k[h][j] = u32x4{w.x, w.y, 0, 0};
                 }
-#pragma unroll
-                for (int j = 0; j < kKScales; ++j) c.ke[h][j] = e[j];
             }
+#pragma unroll
+            for (int j = 0; j < kKScales; ++j) c.ke[h][j] = e[j];
         }
 #pragma unroll
         for (int j = 0; j < kVLoads; ++j) {
             const int t = j * kPerLoad + lane / kLanes;
             const uint32_t p = page_at(t), i = (base + t) & hc.mask;
-            c.v[j] = u32x4{0, 0, 0, 0};
-            c.ve[j] = 127;
-            if (c.there >> t & 1) {
-                c.v[j] = *reinterpret_cast<const u32x4 *>(
-                    hc.v + static_cast<uint64_t>(p) * hc.code_page + i * kRow + part * 16);
-                c.ve[j] = hc.ve[static_cast<uint64_t>(p) * hc.scale_page + i * kGroups +
-                                part / (kLanes / kGroups)];
-            }
+            c.v[j] = *reinterpret_cast<const u32x4 *>(
+                hc.v + static_cast<uint64_t>(p) * hc.code_page + i * kRow + part * 16);
+            c.ve[j] = hc.ve[static_cast<uint64_t>(p) * hc.scale_page + i * kGroups +
+                            part / (kLanes / kGroups)];
         }
     };
 
     uint32_t base = tile.begin + 32 * wave;
-    int page = find(base);
+    int page = 0;
     Codes now;
-    load(base, page, now);
-    page = find(base + 128);
+    if (tile.begin < tile.end) {
+        page = find(base);
+        load(base, page, now);
+        page = find(base + 128);
+    }
     s16x8 q[TERMS][kGroups];
     load_query<T, D, TERMS>(a, tile, tile.r0 + l16, [&](int f) { return g * (D / 4) + 8 * f; }, q);
     f32x4 acc[kTiles];
@@ -548,21 +576,21 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
                 s[h] = mma_terms<TERMS>(x, y, s[h]);
             }
         }
-        // values into LDS; what stands for NaN goes in as zero and is added below
-        uint32_t wild = 0;   // bit j
+        // values into LDS
+        bool wild = false;   // some stand for NaN
 #pragma unroll
         for (int j = 0; j < kVLoads; ++j) {
-            if (now.ve[j] == 255) {
-                wild |= 1u << j;
+            if (there != 0xFFFFFFFFu && !(there >> (j * kPerLoad + lane / kLanes) & 1)) {
                 now.v[j] = u32x4{0, 0, 0, 0};
                 now.ve[j] = 127;
             }
+            wild |= now.ve[j] == 255;
             uint32_t w[kWords];
             decode16<FMT>(now.v[j], mx::scale_of(now.ve[j]), w);
 #pragma unroll
             for (int u = 0; u < kWords / 8; ++u) {
-                u32x4 *p = reinterpret_cast<u32x4 *>(unit_at<D * 2>(
-                    vt, j * kPerLoad + lane / kLanes, part * (kWords / 8) + u));
+                u32x4 *p = reinterpret_cast<u32x4 *>(
+                    vt + (to_lds(j) ^ (u * 32)));
                 p[0] = u32x4{w[8 * u], w[8 * u + 1], w[8 * u + 2], w[8 * u + 3]};
                 p[1] = u32x4{w[8 * u + 4], w[8 * u + 5], w[8 * u + 6], w[8 * u + 7]};
             }
@@ -573,11 +601,12 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
         uint32_t sees = 0xFFu;  // bit 4 h + v: key 16 h + 4 g + v
         if (there != 0xFFFFFFFFu || static_cast<int64_t>(base) + 31 > seen_by_all) {
             sees = 0;
-            const int to = mine - static_cast<int>(base);
+            const int to = mine - static_cast<int>(base) - 4 * g;
+            const uint32_t here = there >> (4 * g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int t = 16 * (i / 4) + 4 * g + i % 4;
-                if ((there >> t & 1) && t <= to) sees |= 1u << i;
+                const int t = 16 * (i / 4) + i % 4;
+                if ((here >> t & 1) && t <= to) sees |= 1u << i;
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -613,40 +642,16 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
             for (int n = 0; n < TERMS; ++n) pf[n] = __builtin_bit_cast(s16x8, w[n]);
         }
         __builtin_amdgcn_wave_barrier();
+        if (__builtin_expect(__any(wild) && __any(sees != 0xFFu), 0)) {
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-            acc[t] = mma_terms<TERMS>(read_across<D * 2>(vt, 0, t, lane), pf, acc[t]);
-        __builtin_amdgcn_wave_barrier();
-        // A value that stands for NaN reaches the rows that see its key, whatever p: counted by
-        // the same product over ones.
-        if (__builtin_expect(__any(wild), 0)) {
+            for (int t = 0; t < kTiles; ++t)
+                add_wild<TERMS>(read_across<D * 2>(vt + (from_lds ^ (t * 32))), pf, sees, acc[t]);
+        } else {
 #pragma unroll
-            for (int j = 0; j < kVLoads; ++j) {
-                const uint32_t w = wild >> j & 1 ? 0x3F803F80u : 0u;
-#pragma unroll
-                for (int u = 0; u < kWords / 8; ++u) {
-                    u32x4 *d = reinterpret_cast<u32x4 *>(unit_at<D * 2>(
-                        vt, j * kPerLoad + lane / kLanes, part * (kWords / 8) + u));
-                    d[0] = d[1] = u32x4{w, w, w, w};
-                }
-            }
-            u32x4 ones;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                ones[k] = (sees >> (2 * k) & 1 ? 0x3F80u : 0u) |
-                          (sees >> (2 * k + 1) & 1 ? 0x3F800000u : 0u);
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                const f32x4 n = gemm::Traits<__bf16>::mma(read_across<D * 2>(vt, 0, t, lane),
-                                                          __builtin_bit_cast(s16x8, ones),
-                                                          f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    if (n[v] != 0.0f) acc[t][v] = __builtin_nanf("");
-            }
-            __builtin_amdgcn_wave_barrier();
+            for (int t = 0; t < kTiles; ++t)
+                acc[t] = mma_terms<TERMS>(read_across<D * 2>(vt + (from_lds ^ (t * 32))), pf, acc[t]);
         }
+        __builtin_amdgcn_wave_barrier();
     }
     // join the waves
     const float sum = row_sum(sm.sum);
@@ -680,24 +685,27 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
 
 // ---------------------------------------------------------------- many query rows
 
-// 128 query rows, two tiles of 16 to each of four waves.  The workgroup's threads decode tiles of
-// keys into LDS for all waves: while a tile is multiplied, the next one's codes, which arrived
-// during the tile before, go into the other half of LDS, and those of the one after are asked for.
-constexpr int kLargeRows = 128;
-// Two waves to a SIMD, one's softmax beside the other's products, where outputs, queries and
-// scores leave room for that in the registers.
+// Two tiles of 16 query rows to each wave.  The workgroup's threads decode tiles of keys into LDS
+// for all waves: while a tile is multiplied, the next one's codes, which arrived during the tile
+// before, go into LDS, and those of the one after are asked for.
+//   Where outputs, queries and scores leave room for two waves to a SIMD, a workgroup has eight
+// (256 rows).  The second four meet the others between their scores and their softmax, the first
+// four after the whole tile, so that one wave of a SIMD computes its softmax while the other
+// multiplies; values are kept for a tile longer for it.
 template <int D, int TERMS>
 constexpr int many_waves() {
-    return D / 2 + D / 4 * TERMS <= 128 ? 2 : 1;
+    return D / 2 + D / 4 * TERMS <= 128 ? 8 : 4;
+}
+template <typename T, int D>
+constexpr int many_rows() {
+    return many_waves<D, terms<T>()>() * 32;
 }
 
 template <typename T, int D, int FMT>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(
-    many_waves<D, terms<T>()>(), many_waves<D, terms<T>()>()))) void
-attend_many_kernel(AttArgs a) {
+__global__ __launch_bounds__((many_waves<D, terms<T>()>() * 64)) void attend_many_kernel(AttArgs a) {
     constexpr int TERMS = terms<T>();
-    constexpr int NQ = 2, BQ = kLargeRows;
-    static_assert(BQ == 4 * NQ * 16, "four waves");
+    constexpr int NW = many_waves<D, TERMS>(), NT = NW * 64;
+    constexpr int NQ = 2, BQ = NW * NQ * 16;
     constexpr int KT = D == 256 ? 32 : 64;                     // keys of a tile
     constexpr int kSub = KT / 16, kPairs = KT / 32;
     constexpr int kRow = mx::bytes<FMT>(D);
@@ -705,16 +713,17 @@ attend_many_kernel(AttArgs a) {
     constexpr int kGroups = D / 32;
     constexpr int kTiles = D / 16;
     constexpr int kPieces = KT * kLanes;                       // of 16 bytes, of a tile
-    constexpr int kLoads = (kPieces + 255) / 256;
+    constexpr int kLoads = (kPieces + NT - 1) / NT;
     constexpr int kWords = FMT == TCQ_FP4 ? 16 : 8;            // of bf16 pairs to a piece
     constexpr int kTileBytes = KT * D * 2;
     __shared__ __align__(16) char kt[2 * kTileBytes];
-    __shared__ __align__(16) char vt[2 * kTileBytes];
-    // of the tile at hand, the one being staged and the one before, in turn
-    __shared__ unsigned long long absent_of[3];
-    __shared__ int wild_of[3];
+    __shared__ __align__(16) char vt[3 * kTileBytes];
+    // of tile i in place i mod 4: the keys that are not there, whether a value stands for NaN
+    __shared__ unsigned long long absent_of[4];
+    __shared__ int wild_of[4];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const bool late = wave >= 4;
     Tile<BQ> tile;
     if (!tile.init(a, blockIdx.x, lane)) return;
     const HeadCache hc = head_cache<FMT, D>(a, tile.head);
@@ -726,15 +735,13 @@ attend_many_kernel(AttArgs a) {
 
     // Pieces of this thread: key p / kLanes of a tile, bytes 16 (p % kLanes) of its row.
     const int part = tid % kLanes;
-    static_assert(256 % kLanes == 0, "a thread's pieces are the same part of their rows");
+    static_assert(NT % kLanes == 0, "a thread's pieces are the same part of their rows");
     int32_t page[kLoads];   // of the keys to be asked for next
     auto find = [&](uint32_t base) {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            const uint32_t pos = base + (j * 256 + tid) / kLanes;
-            page[j] = -1;
-            if ((kPieces % 256 == 0 || tid < kPieces) && pos < tile.end)
-                page[j] = tile.table[pos >> hc.log2];
+            const uint32_t pos = base + (j * NT + tid) / kLanes;
+            page[j] = tile.table[(pos < tile.end ? pos : tile.end - 1) >> hc.log2];
         }
     };
     struct Codes {
@@ -742,69 +749,72 @@ attend_many_kernel(AttArgs a) {
         int ke[kLoads], ve[kLoads];
         uint32_t there;     // bit j
     } now;
+    // (keys that are not there read the cache's first bytes, and are masked)
     auto load = [&](uint32_t base) {
         now.there = 0;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            now.k[j] = now.v[j] = u32x4{0, 0, 0, 0};
-            now.ke[j] = now.ve[j] = 127;
-            const uint32_t p = static_cast<uint32_t>(page[j]);
-            if (p < hc.pages) {
-                const uint32_t i = (base + (j * 256 + tid) / kLanes) & hc.mask;
-                const uint64_t at = static_cast<uint64_t>(p) * hc.code_page + i * kRow + part * 16;
-                const uint64_t e = static_cast<uint64_t>(p) * hc.scale_page + i * kGroups +
-                                   part / (kLanes / kGroups);
-                now.k[j] = *reinterpret_cast<const u32x4 *>(hc.k + at);
-                now.v[j] = *reinterpret_cast<const u32x4 *>(hc.v + at);
-                now.ke[j] = hc.ke[e];
-                now.ve[j] = hc.ve[e];
+            const uint32_t pos = base + (j * NT + tid) / kLanes;
+            uint32_t p = static_cast<uint32_t>(page[j]);
+            if (p < hc.pages && pos < tile.end && (kPieces % NT == 0 || tid < kPieces))
                 now.there |= 1u << j;
-            }
+            else
+                p = 0;
+            const uint32_t i = pos & hc.mask;
+            const uint64_t at = static_cast<uint64_t>(p) * hc.code_page + i * kRow + part * 16;
+            const uint64_t e = static_cast<uint64_t>(p) * hc.scale_page + i * kGroups +
+                               part / (kLanes / kGroups);
+            now.k[j] = *reinterpret_cast<const u32x4 *>(hc.k + at);
+            now.v[j] = *reinterpret_cast<const u32x4 *>(hc.v + at);
+            now.ke[j] = hc.ke[e];
+            now.ve[j] = hc.ve[e];
         }
     };
-    // K: 16-byte chunks of a row permuted by the row
-    auto chunk_at = [&](int half, int row, int chunk) {
-        return reinterpret_cast<u32x4 *>(kt + half * kTileBytes + row * (D * 2) +
-                                         (chunk ^ (row & 7)) * 16);
-    };
-    // The codes at hand into half `half` of LDS.  What stands for NaN in V goes in as zero and is
-    // added later; returns which pieces do (bit j).
-    auto stage = [&](int half, int turn) {
-        uint32_t wild = 0;
+    const int row = tid / kLanes;   // of the first piece; the others are 8 n rows further
+    static_assert(NT / kLanes % 8 == 0, "and of the same permutation");
+    const int k_to = row * (D * 2) + ((part * (kWords / 4)) ^ (row & 7)) * 16;
+    const int v_to = Units<D * 2>::row(row) ^ (part * (kWords / 8) * 32);
+    const int k_from = l16 * (D * 2) + (g ^ (l16 & 7)) * 16;
+    const int v_from = Units<D * 2>::across(lane);
+    // The codes at hand, tile i's, into LDS.
+    auto stage = [&](int k_at, int v_at, int i) {
+        bool wild = false;
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
-            const int p = j * 256 + tid, r = p / kLanes;
-            if (kPieces % 256 == 0 || p < kPieces) {
-                if (!(now.there >> j & 1)) atomicOr(&absent_of[turn], 1ull << r);
+            if (kPieces % NT == 0 || tid < kPieces) {
+                if (!(now.there >> j & 1)) {
+                    now.v[j] = u32x4{0, 0, 0, 0};
+                    now.ve[j] = 127;
+                    atomicOr(&absent_of[i & 3], 1ull << (row + j * (NT / kLanes)));
+                }
+                char *k = kt + k_at + j * (NT / kLanes) * (D * 2);
+                char *v = vt + v_at + j * (NT / kLanes) * (D * 2);
                 uint32_t w[kWords];
                 decode16<FMT>(now.k[j], mx::scale_of(now.ke[j]), w);
 #pragma unroll
                 for (int u = 0; u < kWords / 4; ++u)
-                    *chunk_at(half, r, part * (kWords / 4) + u) =
+                    *reinterpret_cast<u32x4 *>(k + (k_to ^ (u * 16))) =
                         u32x4{w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]};
-                if (now.ve[j] == 255) {
-                    wild |= 1u << j;
-                    now.v[j] = u32x4{0, 0, 0, 0};
-                }
-                decode16<FMT>(now.v[j], mx::scale_of(now.ve[j] == 255 ? 127 : now.ve[j]), w);
+                wild |= now.ve[j] == 255;
+                decode16<FMT>(now.v[j], mx::scale_of(now.ve[j]), w);
 #pragma unroll
                 for (int u = 0; u < kWords / 8; ++u) {
-                    u32x4 *d = reinterpret_cast<u32x4 *>(unit_at<D * 2>(
-                        vt + half * kTileBytes, r, part * (kWords / 8) + u));
+                    u32x4 *d = reinterpret_cast<u32x4 *>(v + (v_to ^ (u * 32)));
                     d[0] = u32x4{w[8 * u], w[8 * u + 1], w[8 * u + 2], w[8 * u + 3]};
                     d[1] = u32x4{w[8 * u + 4], w[8 * u + 5], w[8 * u + 6], w[8 * u + 7]};
                 }
             }
         }
-        if (wild) wild_of[turn] = 1;
-        return wild;
+        if (wild) wild_of[i & 3] = 1;
     };
 
-    if (tid < 3) absent_of[tid] = 0, wild_of[tid] = 0;
+    if (tid < 4) absent_of[tid] = 0, wild_of[tid] = 0;
     uint32_t base = tile.begin;
-    find(base);
-    load(base);
-    find(base + KT);
+    if (base < tile.end) {
+        find(base);
+        load(base);
+        find(base + KT);
+    }
     s16x8 q[NQ][TERMS][kGroups];
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -819,17 +829,20 @@ attend_many_kernel(AttArgs a) {
         for (int t = 0; t < kTiles; ++t) acc[n][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     __syncthreads();
-    uint32_t wild = stage(0, 0);
-    load(base + KT);
-    find(base + 2 * KT);
+    if (base < tile.end) {
+        stage(0, 0, 0);
+        load(base + KT);
+        find(base + 2 * KT);
+    }
     __syncthreads();
-    int turn = 0;
-    for (int half = 0; base < tile.end; base += KT, half ^= 1) {
-        const int next = turn == 2 ? 0 : turn + 1, before = turn == 0 ? 2 : turn - 1;
-        const uint64_t absent = absent_of[turn];
-        const bool any_wild = wild_of[turn] != 0;
-        if (tid == 0) absent_of[before] = 0, wild_of[before] = 0;
-        const uint32_t wild_here = wild;
+    // Tile i is staged before meeting i - 1.  After meeting i the early waves are done with it, the
+    // late ones have its scores alone, so its keys may be overwritten (by tile i + 2) then, its
+    // values (by tile i + 3) and marks after meeting i + 1.
+    int v_now = 0, v_next = kTileBytes, v_last = 2 * kTileBytes;
+    for (int i = 0; base < tile.end; base += KT, ++i) {
+        const int k_now = i & 1 ? kTileBytes : 0;
+        if (tid == 0) absent_of[(i + 2) & 3] = 0, wild_of[(i + 2) & 3] = 0;
+        __builtin_amdgcn_s_setprio(1);
         // scores
         f32x4 s[NQ][kSub];
 #pragma unroll
@@ -838,8 +851,8 @@ attend_many_kernel(AttArgs a) {
             for (int n = 0; n < NQ; ++n) s[n][h] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int f = 0; f < kGroups; ++f) {
-                const s16x8 x =
-                    __builtin_bit_cast(s16x8, *chunk_at(half, 16 * h + l16, 4 * f + g));
+                const s16x8 x = *reinterpret_cast<const s16x8 *>(
+                    kt + ((k_now + k_from) ^ (f * 64)) + 16 * h * (D * 2));
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
                     s16x8 y[TERMS];
@@ -849,10 +862,13 @@ attend_many_kernel(AttArgs a) {
                 }
             }
         }
-        // (the other half was read before the last meeting)
-        wild = stage(half ^ 1, next);
+        __builtin_amdgcn_s_setprio(0);
+        stage(kTileBytes - k_now, v_next, i + 1);
         load(base + 2 * KT);
         find(base + 3 * KT);
+        if (late) __syncthreads();
+        const uint64_t absent = absent_of[i & 3];
+        const bool wild = wild_of[i & 3] != 0;
         s16x8 pf[NQ][kPairs][TERMS];
         uint32_t sees[NQ];
         const bool partial = absent != 0 || static_cast<int64_t>(base) + KT - 1 > seen_by_all;
@@ -861,11 +877,12 @@ attend_many_kernel(AttArgs a) {
             sees[n] = ~0u;  // bit 4 h + v: key 16 h + 4 g + v
             if (partial) {
                 sees[n] = 0;
-                const int to = mine[n] - static_cast<int>(base);
+                const int to = mine[n] - static_cast<int>(base) - 4 * g;
+                const uint64_t gone = absent >> (4 * g);
 #pragma unroll
                 for (int i = 0; i < 4 * kSub; ++i) {
-                    const int t = 16 * (i / 4) + 4 * g + i % 4;
-                    if (!(absent >> t & 1) && t <= to) sees[n] |= 1u << i;
+                    const int t = 16 * (i / 4) + i % 4;
+                    if (!(gone >> t & 1) && t <= to) sees[n] |= 1u << i;
                 }
 #pragma unroll
                 for (int i = 0; i < 4 * kSub; ++i)
@@ -901,56 +918,34 @@ attend_many_kernel(AttArgs a) {
                 for (int m = 0; m < TERMS; ++m) pf[n][k2][m] = __builtin_bit_cast(s16x8, w[m]);
             }
         }
-        const char *vh = vt + half * kTileBytes;
+        if (__builtin_expect(wild && partial, 0)) {
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
+            for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-            for (int k2 = 0; k2 < kPairs; ++k2) {
-                const s16x8 x = read_across<D * 2>(vh, 32 * k2, t, lane);
+                for (int k2 = 0; k2 < kPairs; ++k2)
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) acc[n][t] = mma_terms<TERMS>(x, pf[n][k2], acc[n][t]);
-            }
-        }
-        __syncthreads();
-        // Values that stand for NaN, as in attend_few_kernel: the same product over ones.
-        if (__builtin_expect(any_wild, 0)) {
+                    for (int n = 0; n < NQ; ++n)
+                        add_wild<TERMS>(read_across<D * 2>(vt + ((v_now + v_from) ^ (t * 32)) + 32 * k2 * (D * 2)), pf[n][k2],
+                                        sees[n] >> (8 * k2), acc[n][t]);
+        } else {
+            __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const int p = j * 256 + tid;
-                if (p < kPieces) {
-                    const uint32_t w = wild_here >> j & 1 ? 0x3F803F80u : 0u;
-#pragma unroll
-                    for (int u = 0; u < kWords / 8; ++u) {
-                        u32x4 *d = reinterpret_cast<u32x4 *>(unit_at<D * 2>(
-                            vt + half * kTileBytes, p / kLanes, part * (kWords / 8) + u));
-                        d[0] = d[1] = u32x4{w, w, w, w};
-                    }
-                }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
+            for (int t = 0; t < kTiles; ++t) {
 #pragma unroll
                 for (int k2 = 0; k2 < kPairs; ++k2) {
-                    u32x4 ones;
+                    const s16x8 x = read_across<D * 2>(vt + ((v_now + v_from) ^ (t * 32)) + 32 * k2 * (D * 2));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ones[k] = (sees[n] >> (8 * k2 + 2 * k) & 1 ? 0x3F80u : 0u) |
-                                  (sees[n] >> (8 * k2 + 2 * k + 1) & 1 ? 0x3F800000u : 0u);
-#pragma unroll
-                    for (int t = 0; t < kTiles; ++t) {
-                        const f32x4 c = gemm::Traits<__bf16>::mma(
-                            read_across<D * 2>(vh, 32 * k2, t, lane),
-                            __builtin_bit_cast(s16x8, ones), f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                        for (int v = 0; v < 4; ++v)
-                            if (c[v] != 0.0f) acc[n][t][v] = __builtin_nanf("");
-                    }
+                    for (int n = 0; n < NQ; ++n)
+                        acc[n][t] = mma_terms<TERMS>(x, pf[n][k2], acc[n][t]);
                 }
             }
-            __syncthreads();
+            __builtin_amdgcn_s_setprio(0);
         }
-        turn = next;
+        if (!late) __syncthreads();
+        const int v = v_last;
+        v_last = v_now;
+        v_now = v_next;
+        v_next = v;
     }
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -1008,7 +1003,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttArgs few, AttArgs many, ui
     if (blockIdx.x < blocks_few)
         join<T, D, kSmallRows>(few, blockIdx.x);
     else
-        join<T, D, kLargeRows>(many, blockIdx.x - blocks_few);
+        join<T, D, many_rows<T, D>()>(many, blockIdx.x - blocks_few);
 }
 
 // ---------------------------------------------------------------- host side
@@ -1024,6 +1019,7 @@ bool few_only(int64_t rows, int group, int64_t seqs) {
 // units, so there are at most twice the target.
 constexpr int kSlotsFew = 2 * kTargetSmall, kSlotsMany = 2 * kTargetLarge;
 
+constexpr int kMostRows = 256;   // of a tile
 int64_t slot_bytes(int bq, int dim) { return int64_t{bq} * (dim + 2) * 4; }
 
 template <typename T, int D, int FMT>
@@ -1034,12 +1030,13 @@ hipError_t attend(const AttArgs &base, char *ws, hipStream_t s) {
     few.both = many.both = !only;
     few.part = reinterpret_cast<float *>(ws);
     few.slots = kSlotsFew;
+    constexpr int kRows = many_rows<T, D>();
     many.part = reinterpret_cast<float *>(ws + int64_t{kSlotsFew} * slot_bytes(kSmallRows, D));
     many.slots = kSlotsMany;
     // tiles of all sequences: whole ones of the rows, and a part of one for each
     const int64_t qrows = base.rows * base.group;
     const int64_t few_tiles = only ? qrows / kSmallRows + base.b.seqs : base.b.seqs;
-    const int64_t many_tiles = qrows / kLargeRows + base.b.seqs;
+    const int64_t many_tiles = qrows / kRows + base.b.seqs;
     hipLaunchKernelGGL((attend_few_kernel<T, D, FMT>),
                        dim3(static_cast<unsigned>(few_tiles * heads + kTargetSmall)), dim3(256),
                        0, s, few);
@@ -1048,13 +1045,13 @@ hipError_t attend(const AttArgs &base, char *ws, hipStream_t s) {
     if (!only) {
         hipLaunchKernelGGL((attend_many_kernel<T, D, FMT>),
                            dim3(static_cast<unsigned>(many_tiles * heads + kTargetLarge)),
-                           dim3(256), 0, s, many);
+                           dim3(kRows * 2), 0, s, many);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     // (a pair of tile and head with several runs has two at least)
     const uint32_t few_blocks = kSlotsFew / 2;
-    const uint32_t many_blocks = only ? 0 : kSlotsMany / 2 * (kLargeRows / kJoinRows);
+    const uint32_t many_blocks = only ? 0 : kSlotsMany / 2 * (kRows / kJoinRows);
     hipLaunchKernelGGL((join_kernel<T, D>), dim3(few_blocks + many_blocks), dim3(256), 0, s, few,
                        many, few_blocks);
     return hipGetLastError();
@@ -1080,7 +1077,7 @@ size_t attention_bytes(int dim, int heads, int group, int64_t seqs, int64_t rows
     if (rows == 0 || seqs == 0) return 0;
     size_t n = static_cast<size_t>(kSlotsFew * slot_bytes(kSmallRows, dim));
     if (!few_only(rows, group, seqs))
-        n += static_cast<size_t>(kSlotsMany * slot_bytes(kLargeRows, dim));
+        n += static_cast<size_t>(kSlotsMany * slot_bytes(kMostRows, dim));
     return align_up(n, 256);
 }
 
