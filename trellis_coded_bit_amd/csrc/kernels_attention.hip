@@ -80,9 +80,9 @@ __device__ __forceinline__ Sequence sequence(const AttArgs &a, int64_t s) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t wave_prefix(uint32_t v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
+// Running sum over the lanes, of which `n` (uniform) at most are not zero; the last of 64 holds all.
+__device__ __forceinline__ uint32_t wave_prefix(uint32_t v, int lane, int n) {
+    for (int d = 1; d < n; d <<= 1) {
         const uint32_t o = __shfl_up(v, d);
         if (lane >= d) v += o;
     }
@@ -100,8 +100,9 @@ __device__ __forceinline__ uint32_t run_units(const AttArgs &a, int lane) {
         const Sequence q = sequence<BQ>(a, s + lane);
         total += static_cast<uint64_t>(q.tiles) * q.units;
     }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
+    // (a wave's first lanes hold everything where sequences are few)
+    const int n = a.b.seqs < 64 ? static_cast<int>(a.b.seqs) : 64;
+    for (int d = 1; d < n; d <<= 1) total += __shfl_xor(total, d);
     uint64_t per = (total * a.c.heads + target<BQ>() - 1) / target<BQ>();
     per = per > 1 ? per : 1;
     per = per < (1u << 30) ? per : 1u << 30;  // (units are fewer)
@@ -130,10 +131,12 @@ __device__ __forceinline__ bool item_of(const AttArgs &a, uint32_t index, uint32
             return v < (1u << 25) ? static_cast<uint32_t>(v) : 1u << 25;
         };
         const uint32_t n = cut(PAIRS ? (q.chunks > 1 ? pairs : 0) : items);
-        const uint32_t to = wave_prefix(n, lane), all = of_lane(to, 63);
-        const uint32_t stop = wave_prefix(cut(shares), lane);
+        const int used = a.b.seqs - s < 64 ? static_cast<int>(a.b.seqs - s) : 64;
+        const uint32_t to = wave_prefix(n, lane, used), all = of_lane(to, used - 1);
+        const uint32_t stop = wave_prefix(cut(shares), lane, used);
         if (index < all) {
-            const int at = __popcll(__ballot(to <= index));  // lanes before the item's
+            // lanes before the item's
+            const int at = __popcll(__ballot(lane < used && to <= index));
             it.seq = s + at;
             it.tiles = of_lane(q.tiles, at);
             it.chunks = of_lane(q.chunks, at);
@@ -142,7 +145,7 @@ __device__ __forceinline__ bool item_of(const AttArgs &a, uint32_t index, uint32
             return true;
         }
         index -= all;
-        slots += of_lane(stop, 63);
+        slots += of_lane(stop, used - 1);
     }
     return false;
 }
@@ -959,13 +962,18 @@ __global__ __launch_bounds__((many_waves<D, terms<T>()>() * 64)) void attend_man
 
 // ---------------------------------------------------------------- join of shares
 
-// Rows of tiles with several runs: a wave takes a row, its lanes four dims each; the shares are
-// added in the order of the runs.
-constexpr int kJoinRows = 16;    // rows to a workgroup of four waves
+// Rows of tiles with several runs.  D / 4 lanes take a row, four dims each; the four waves every
+// fourth run, eight at a time (their loads are on their way together), and their sums, each
+// relative to the wave's own largest score, are joined in the waves' order.
+constexpr int kJoinRows = 16;    // rows to a workgroup
 template <typename T, int D, int BQ>
 __device__ __forceinline__ void join(const AttArgs &a, uint32_t block) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     constexpr int kParts = BQ / kJoinRows;
+    constexpr int kRows = 256 / D;     // at a time
+    constexpr int kBatch = 8;
+    __shared__ f32x4 sums[4][64];
+    __shared__ float tops[4][64], totals[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     Item it;
     const uint32_t per = run_units<BQ>(a, lane);
     if (!item_of<BQ, true>(a, block / kParts, per, lane, it)) return;
@@ -976,26 +984,60 @@ __device__ __forceinline__ void join(const AttArgs &a, uint32_t block) {
     if (it.slot + static_cast<uint64_t>(it.chunks - 1) * pairs >= a.slots) return;
     const float *slot = a.part + it.slot * slot_floats<BQ, D>();
     const int64_t step = pairs * slot_floats<BQ, D>();
-    const int d = lane * 4;
-    for (int i = wave; i < kJoinRows; i += 4) {
-        const int r = static_cast<int>(block % kParts) * kJoinRows + i;
-        if (tile.r0 + r >= tile.rows) break;
-        float top = -__builtin_inff();
-        for (uint32_t c = lane; c < it.chunks; c += 64)
-            top = __builtin_fmaxf(top, slot[c * step + BQ * D + r]);
-#pragma unroll
-        for (int x = 32; x; x >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, x));
-        const float ref = Softmax::safe(top);
+    const int d = lane % (D / 4) * 4;
+    const int first = static_cast<int>(block % kParts) * kJoinRows;
+    for (int i = 0; i < kJoinRows && tile.r0 + first + i < tile.rows; i += kRows) {
+        const int r = first + i + lane / (D / 4);
+        float top = -__builtin_inff(), total = 0.0f;
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        float total = 0.0f;
-#pragma unroll 8
-        for (uint32_t c = 0; c < it.chunks; ++c) {
-            const float *p = slot + c * step;
-            const float f = __builtin_amdgcn_exp2f(p[BQ * D + r] - ref);
-            total = __builtin_fmaf(p[BQ * D + BQ + r], f, total);
-            if (d < D) o += *reinterpret_cast<const f32x4 *>(p + r * D + d) * f;
+        for (uint32_t c0 = wave; c0 < it.chunks; c0 += 4 * kBatch) {
+            float m[kBatch], l[kBatch];
+            f32x4 v[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const uint32_t c = c0 + 4 * k;
+                const float *p = slot + (c < it.chunks ? c : c0) * step;
+                m[k] = p[BQ * D + r];
+                l[k] = p[BQ * D + BQ + r];
+                v[k] = *reinterpret_cast<const f32x4 *>(p + r * D + d);
+                if (c >= it.chunks) m[k] = -__builtin_inff();
+            }
+            float to = top;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) to = __builtin_fmaxf(to, m[k]);
+            const float ref = Softmax::safe(to);
+            const float alpha = __builtin_amdgcn_exp2f(top - ref);
+            top = to;
+            total *= alpha;
+            o *= alpha;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (c0 + 4 * k < it.chunks) {  // (the others are repeats)
+                    const float f = __builtin_amdgcn_exp2f(m[k] - ref);
+                    total = __builtin_fmaf(l[k], f, total);
+                    o += v[k] * f;
+                }
+            }
         }
-        if (d < D) store<T, BQ>(a, tile, tile.r0 + r, d, o, total);
+        sums[wave][lane] = o;
+        tops[wave][lane] = top;
+        totals[wave][lane] = total;
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int w = 1; w < 4; ++w) top = __builtin_fmaxf(top, tops[w][lane]);
+            const float ref = Softmax::safe(top);
+            total = 0.0f;
+            o = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float f = __builtin_amdgcn_exp2f(tops[w][lane] - ref);
+                total = __builtin_fmaf(totals[w][lane], f, total);
+                o += sums[w][lane] * f;
+            }
+            store<T, BQ>(a, tile, tile.r0 + r, d, o, total);
+        }
+        __syncthreads();
     }
 }
 template <typename T, int D>
@@ -1050,8 +1092,12 @@ hipError_t attend(const AttArgs &base, char *ws, hipStream_t s) {
         if (e != hipSuccess) return e;
     }
     // (a pair of tile and head with several runs has two at least)
-    const uint32_t few_blocks = kSlotsFew / 2;
-    const uint32_t many_blocks = only ? 0 : kSlotsMany / 2 * (kRows / kJoinRows);
+    const auto blocks = [&](int64_t tiles, int slots, int rows) {
+        const int64_t pairs = tiles * heads < slots / 2 ? tiles * heads : slots / 2;
+        return static_cast<uint32_t>(pairs * (rows / kJoinRows));
+    };
+    const uint32_t few_blocks = blocks(few_tiles, kSlotsFew, kSmallRows);
+    const uint32_t many_blocks = only ? 0 : blocks(many_tiles, kSlotsMany, kRows);
     hipLaunchKernelGGL((join_kernel<T, D>), dim3(few_blocks + many_blocks), dim3(256), 0, s, few,
                        many, few_blocks);
     return hipGetLastError();

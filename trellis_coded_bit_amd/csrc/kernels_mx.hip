@@ -81,8 +81,7 @@ struct MxUnpackArgs {
     int64_t cols, ldo;
     Pieces ix;          // pieces of 16 bytes of output
     int64_t padded;     // columns cols .. padded - 1 become zeros
-    int shift;          // the values are multiplied by 2^shift
-    const int *shift_at;  // its address instead, or NULL
+    MxShift shift;      // (fp16; tops NULL: none)
 };
 
 // 16 bytes of output per thread (8 values of a 16-bit type, 4 of fp32), stored past the caches.
@@ -92,7 +91,16 @@ __device__ __forceinline__ void mx_unpack(const MxUnpackArgs &a, T *__restrict__
     constexpr int P = 16 / static_cast<int>(sizeof(T));
     typedef uint32_t Store __attribute__((ext_vector_type(4), aligned(1)));
     const int64_t groups = (a.cols + mx::kGroup - 1) / mx::kGroup;
-    const int shift = a.shift_at ? *a.shift_at : a.shift;
+    int shift = 0;
+    if constexpr (__is_same(T, _Float16)) {
+        if (a.shift.tops) {
+            int top = 0;
+#pragma unroll
+            for (int k = 0; k < kMxTops; ++k) top = top > a.shift.tops[k] ? top : a.shift.tops[k];
+            shift = 127 + 15 - (FMT == TCQ_FP4 ? 2 : 8) - top;
+            if (block == 0 && threadIdx.x == 0) *a.shift.down = -shift;
+        }
+    }
     for (int64_t i = static_cast<int64_t>(block) * 256 + threadIdx.x; i < a.ix.total;
          i += static_cast<int64_t>(blocks) * 256) {
         int64_t r;
@@ -121,8 +129,9 @@ __device__ __forceinline__ void mx_unpack(const MxUnpackArgs &a, T *__restrict__
 #pragma unroll
         for (int k = 0; k < P; ++k)
             st.v[k] = static_cast<T>(
-                col + k < a.cols ? (sizeof(T) == 2 ? __builtin_amdgcn_ldexpf(v[k], shift) : v[k])
-                                 : 0.0f);
+                col + k < a.cols
+                    ? (__is_same(T, _Float16) ? __builtin_amdgcn_ldexpf(v[k], shift) : v[k])
+                    : 0.0f);
         if (col + P <= a.padded) {
             __builtin_nontemporal_store(__builtin_bit_cast(Store, st),
                                         reinterpret_cast<Store *>(o));
@@ -155,11 +164,11 @@ hipError_t pack(MxPackArgs a, hipStream_t s) {
 
 template <typename T, int FMT>
 hipError_t unpack(const MxMatrix &m, int64_t rows, int64_t cols, void *out, int64_t ldo,
-                  int64_t padded, const int *shift_at, hipStream_t s) {
+                  int64_t padded, const MxShift *shift, hipStream_t s) {
     constexpr int64_t P = 16 / sizeof(T);
     const int64_t cpr = (padded + P - 1) / P;
     const MxUnpackArgs a{m.codes, m.ld,  m.scale, cols, ldo, {static_cast<uint32_t>(cpr), rows * cpr},
-                         padded,  0, shift_at};
+                         padded,  shift ? *shift : MxShift{nullptr, nullptr}};
     const auto kern = a.ix.total < (int64_t{1} << 32) ? mx_unpack_kernel<T, FMT, true>
                                                       : mx_unpack_kernel<T, FMT, false>;
     hipLaunchKernelGGL(kern, dim3(grid_for(a.ix.total, 256)), dim3(256), 0, s, a,
@@ -184,11 +193,11 @@ hipError_t launch_mx_pack(const void *X, int dtype, int64_t rows, int64_t cols, 
 }
 
 hipError_t launch_mx_unpack(const MxMatrix &m, int64_t rows, int64_t cols, int dtype, void *out,
-                            int64_t ldo, int64_t padded, const int *shift_at, hipStream_t s) {
+                            int64_t ldo, int64_t padded, const MxShift *shift, hipStream_t s) {
     const bool fp4 = m.format == TCQ_FP4;
 #define TCQ_UNPACK(T)                                                                     \
-    (fp4 ? unpack<T, TCQ_FP4>(m, rows, cols, out, ldo, padded, shift_at, s)               \
-         : unpack<T, TCQ_FP8>(m, rows, cols, out, ldo, padded, shift_at, s))
+    (fp4 ? unpack<T, TCQ_FP4>(m, rows, cols, out, ldo, padded, shift, s)               \
+         : unpack<T, TCQ_FP8>(m, rows, cols, out, ldo, padded, shift, s))
     switch (dtype) {
         case TCQ_F32: return TCQ_UNPACK(float);
         case TCQ_F16: return TCQ_UNPACK(_Float16);

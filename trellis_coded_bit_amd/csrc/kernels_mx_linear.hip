@@ -73,63 +73,136 @@ __device__ __forceinline__ f32x4 mma_fp4_at(int oa, int ob, const i32x4 &a, uint
 // groups) are 1 KiB, lane l's 16 bytes at 16 l hold, for row 16 f + l % 16 of the tile, f = 0
 // .. 7, groups l / 16 and 4 + l / 16 of the step in bytes 2 f and 2 f + 1.  So a wave reads
 // a step's scales in one contiguous access per operand.  Rows and groups past the end get 1.
+//   A thread takes a step of the eight rows l16, 16 + l16, ..: eight bytes of each, four pieces out.
 struct ScaleArgs {
     const uint8_t *scale;
     int64_t rows, groups;
-    int64_t steps;
+    uint32_t steps;
     uint8_t *out;
-    int64_t lanes;   // 64 x tiles x steps
+    int64_t work;    // tiles x 16 x steps
 };
 __device__ __forceinline__ void order_scales(const ScaleArgs &a, int64_t q) {
-    const int lane = static_cast<int>(q & 63);
-    const int64_t ts = q >> 6;
-    const int64_t tile = ts / a.steps, step = ts - tile * a.steps;
-    const int64_t g0 = step * 8 + (lane >> 4), row0 = tile * 128 + (lane & 15);
-    uint32_t w[4] = {0, 0, 0, 0};
+    const int64_t tl = q / a.steps;
+    const uint32_t step = static_cast<uint32_t>(q - tl * a.steps);
+    const int64_t tile = tl >> 4, row0 = tile * 128 + (tl & 15);
+    const int64_t g0 = static_cast<int64_t>(step) * 8;
+    uint32_t w[4][4];
+    struct __attribute__((packed)) Eight { uint32_t v[2]; };
+    Eight e[8];
 #pragma unroll
     for (int f = 0; f < 8; ++f) {
         const int64_t row = row0 + 16 * f;
+        e[f].v[0] = e[f].v[1] = 0x7F7F7F7Fu;
+        if (row < a.rows) {
+            const uint8_t *p = a.scale + row * a.groups + g0;
+            if (g0 + 8 <= a.groups) {
+                e[f] = *reinterpret_cast<const Eight *>(p);
+            } else {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            const int64_t g = g0 + 4 * ks;
-            const uint32_t e =
-                row < a.rows && g < a.groups ? a.scale[row * a.groups + g] : 127u;
-            w[f / 2] |= e << (8 * (2 * (f % 2) + ks));
+                for (int k = 0; k < 8; ++k)
+                    if (g0 + k < a.groups)
+                        e[f].v[k / 4] = (e[f].v[k / 4] & ~(255u << (8 * (k % 4)))) |
+                                        static_cast<uint32_t>(p[k]) << (8 * (k % 4));
+            }
         }
     }
-    reinterpret_cast<uint4 *>(a.out)[q] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int f = 0; f < 8; f += 2)
+            w[g][f / 2] = (e[f].v[0] >> (8 * g) & 255u) | (e[f].v[1] >> (8 * g) & 255u) << 8 |
+                          (e[f + 1].v[0] >> (8 * g) & 255u) << 16 |
+                          (e[f + 1].v[1] >> (8 * g) & 255u) << 24;
+    uint4 *out = reinterpret_cast<uint4 *>(a.out) + (tile * a.steps + step) * 64 + (tl & 15);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) out[g * 16] = make_uint4(w[g][0], w[g][1], w[g][2], w[g][3]);
 }
 __global__ __launch_bounds__(256) void order_scales_kernel(ScaleArgs x, ScaleArgs w) {
     const int64_t q = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (q < x.lanes)
+    if (q < x.work)
         order_scales(x, q);
-    else if (q - x.lanes < w.lanes)
-        order_scales(w, q - x.lanes);
+    else if (q - x.work < w.work)
+        order_scales(w, q - x.work);
 }
 
-// The ordered scales of N fragments (16 rows each) of one operand, from row r0 on.
+// The ordered scales of F fragments (16 rows each) of one operand, from row r0 on: a uniform address
+// and the lane's offset.
 template <int F>
 struct ScaleReader {
     static constexpr int kWords = F / 2;
-    const char *base;   // this lane's bytes at step 0
+    const uint8_t *base;
+    uint32_t off;
     __device__ __forceinline__ ScaleReader(const uint8_t *scales, int64_t r0, int64_t steps,
-                                           int lane) {
-        base = reinterpret_cast<const char *>(scales) + (r0 / 128) * steps * 1024 + lane * 16 +
-               (r0 % 128) / 8;
-    }
+                                           int lane)
+        : base(scales + (r0 / 128) * steps * 1024 + (r0 % 128) / 8), off(lane * 16) {}
     __device__ __forceinline__ void read(int s, uint32_t (&w)[kWords]) const {
+        const uint8_t *p = base + s * int64_t{1024};
         if constexpr (kWords == 4) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(base + s * 1024ll);
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + off);
             w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
         } else {
-            const uint2 v = *reinterpret_cast<const uint2 *>(base + s * 1024ll);
+            const uint2 v = *reinterpret_cast<const uint2 *>(p + off);
             w[0] = v.x, w[1] = v.y;
         }
     }
 };
 
+// The loads of a tile of TR rows by one step, as TileLoader's (chunk c of row r into slot c ^ (r >>
+// 1 & 7), zeros past the rows and past k), with one offset per thread: a thread's rows lie NT / 8
+// rows apart.  `renew` makes an offset a new value to the compiler, which otherwise holds every
+// sum with it in registers, 26 of them, and spills to make room; a spill's return waits for all
+// loads on their way.
+template <int TR, int NT>
+struct CodeLoader {
+    static constexpr int kLoads = TR * 8 / NT;
+    const char *base;     // uniform, as all but off and chunk
+    int64_t left;
+    uint32_t apart;
+    int k;
+    uint32_t off;
+    int chunk;            // this thread's first byte within a step
+    __device__ __forceinline__ CodeLoader(const Operand<CodePair> &o, int64_t row0, int tid) {
+        base = reinterpret_cast<const char *>(o.p + row0 * o.ld);
+        left = (o.rows - row0 - 1) * o.ld + o.k;
+        apart = static_cast<uint32_t>(NT / 8 * o.ld);
+        k = static_cast<int>(o.k);
+        const int r = tid / 8;
+        chunk = (tid % 8 ^ (r >> 1 & 7)) * 16;
+        off = static_cast<uint32_t>(r * o.ld) + chunk;
+    }
+    __device__ __forceinline__ void renew() { asm volatile("" : "+v"(off)); }
+    // Step s, or zeros from s_end on.  (No branch: matrix instructions would be moved past it, away
+    // from the reads that feed them.)
+    __device__ __forceinline__ void load(char *lds, int s, int s_end, int tid) const {
+        const int64_t at = s * int64_t{gemm::kStepBytes}, rest = left - at;
+        const uint32_t most = rest < 0xFFFFFF00ll ? static_cast<uint32_t>(rest) : 0xFFFFFF00u;
+        const uint32_t bytes = s < s_end ? most : 0u;
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char *>(base + at), 0, static_cast<int>(bytes), 0x00020000);
+        const bool in = chunk < k - static_cast<int>(at);
+        const int wave0 = __builtin_amdgcn_readfirstlane(tid & ~63);
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rs, (gemm::LdsPtr)(lds + (u * NT + wave0) * 16), 16,
+                static_cast<int>(in ? off + u * apart : 0xFFFFFFF0u), 0, 0, 0);
+    }
+};
+
+// Reads fragments of a tile as FragReader does, from one offset per lane: the slots of the two
+// halves of a step differ by an exclusive or with 64.
+struct SlotReader {
+    int at;
+    __device__ __forceinline__ SlotReader(int lane, int r0)
+        : at((r0 + (lane & 15)) * 128 + ((lane >> 4) ^ (lane >> 1 & 7)) * 16) {}
+    __device__ __forceinline__ void renew() { asm volatile("" : "+v"(at)); }
+    __device__ __forceinline__ i32x4 read(const char *lds, int f, int ks) const {
+        return *reinterpret_cast<const i32x4 *>(lds + (at ^ (ks * 64)) + f * 2048);
+    }
+};
+
 // A TI x TJ tile of A B^T over the steps s_begin .. s_end - 1 of 256 codes, as gemm_tile's (loads
-// straight into LDS, NB stages or a ring of five pieces, phases of half a wave's rows), with
+// straight into LDS, NB stages or a ring of five pieces, phases of some of a wave's rows), with
 // the scales of the step to come read from memory into registers.
 template <int TI, int TJ, int WI, int WJ, int NB, typename Epi>
 __device__ __forceinline__ void mx_tile(const Operand<CodePair> &A, const uint8_t *as,
@@ -137,17 +210,15 @@ __device__ __forceinline__ void mx_tile(const Operand<CodePair> &A, const uint8_
                                         int64_t steps, int64_t i0, int64_t j0, int s_begin,
                                         int s_end, const gemm::Stages<NB> &st, const Epi &epi) {
     constexpr int NT = WI * WJ * 64;
-    constexpr int FI = TI / WI / 16, FJ = TJ / WJ / 16, FH = FI / 2;
+    constexpr int FI = TI / WI / 16, FJ = TJ / WJ / 16;
+    constexpr int FH = 2, kParts = FI / FH, kPhases = 2 * kParts;  // fragments of A to a phase
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wi = wave / WJ, wj = wave % WJ;
-    gemm::TileLoader<CodePair, false, TI, NT> la;
-    gemm::TileLoader<CodePair, false, TJ, NT> lb;
-    la.init(A, i0, tid);
-    lb.init(B, j0, tid);
-    const gemm::FragReader<CodePair, false, TI> ra{lane, wi * FI * 16};
-    const gemm::FragReader<CodePair, false, TJ> rb{lane, wj * FJ * 16};
+    CodeLoader<TI, NT> la(A, i0, tid);
+    CodeLoader<TJ, NT> lb(B, j0, tid);
+    SlotReader ra(lane, wi * FI * 16), rb(lane, wj * FJ * 16);
     const ScaleReader<FI> rsa(as, i0 + wi * FI * 16, steps, lane);
     const ScaleReader<FJ> rsb(bs, j0 + wj * FJ * 16, steps, lane);
     f32x4 acc[FI][FJ];
@@ -158,29 +229,27 @@ __device__ __forceinline__ void mx_tile(const Operand<CodePair> &A, const uint8_
     i32x4 fa[2][FH], fb[2][FJ];
     uint32_t sa[FI / 2], sb[FJ / 2], na_s[FI / 2], nb_s[FJ / 2];
     auto read_phase = [&](const char *ta, const char *tb, int ph) {
-        const int ks = ph / 2, half = ph % 2;
-        if (half == 0) {
+        const int ks = ph / kParts, part = ph % kParts;
+        if (part == 0) {
 #pragma unroll
             for (int j = 0; j < FJ; ++j) fb[ks % 2][j] = rb.read(tb, j, ks);
         }
 #pragma unroll
-        for (int i = 0; i < FH; ++i) fa[ph % 2][i] = ra.read(ta, half * FH + i, ks);
+        for (int i = 0; i < FH; ++i) fa[ph % 2][i] = ra.read(ta, part * FH + i, ks);
     };
     auto mul_phase = [&](int ph) {
-        const int ks = ph / 2, half = ph % 2;
+        const int ks = ph / kParts, part = ph % kParts;
 #pragma unroll
         for (int i = 0; i < FH; ++i)
 #pragma unroll
             for (int j = 0; j < FJ; ++j) {
-                const int fi = half * FH + i;
+                const int fi = part * FH + i;
                 f32x4 &c = acc[fi][j];
                 c = mma_fp4_at(2 * (j % 2) + ks, 2 * (fi % 2) + ks, fb[ks % 2][j], sb[j / 2],
                                fa[ph % 2][i], sa[fi / 2], c);
             }
     };
-    constexpr int kPhases = 4;
     constexpr int kLoadsA = decltype(la)::kLoads, kLoadsB = decltype(lb)::kLoads;
-    auto valid = [&](int s) { return s < s_end ? s : gemm::kPastEnd; };
     auto clamped = [&](int s) { return s < s_end ? s : s_end - 1; };
     auto next_scales = [&](int s) {
         rsa.read(clamped(s), na_s);
@@ -201,7 +270,11 @@ __device__ __forceinline__ void mx_tile(const Operand<CodePair> &A, const uint8_
                 const char *na = st.p[(t + 2) % 5], *nb = st.p[(t + 3) % 5];
                 take_scales();
                 next_scales(s + 1);
-                la.load(st.p[(t + 4) % 5], valid(s + 2), tid);
+                ra.renew();
+                rb.renew();
+                la.renew();
+                lb.renew();
+                la.load(st.p[(t + 4) % 5], s + 2, s_end, tid);
 #pragma unroll
                 for (int ph = 0; ph + 1 < kPhases; ++ph) {
                     read_phase(ta, tb, ph + 1);
@@ -209,28 +282,37 @@ __device__ __forceinline__ void mx_tile(const Operand<CodePair> &A, const uint8_
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 gemm::meet<kLoadsA>();
-                lb.load(ta, valid(s + 2), tid);
+                lb.load(ta, s + 2, s_end, tid);
                 read_phase(na, nb, 0);
                 mul_phase(kPhases - 1);
                 __builtin_amdgcn_sched_barrier(0);
             };
-            la.load(st.p[0], s_begin, tid);
-            lb.load(st.p[1], s_begin, tid);
-            la.load(st.p[2], valid(s_begin + 1), tid);
-            lb.load(st.p[3], valid(s_begin + 1), tid);
+            la.load(st.p[0], s_begin, s_end, tid);
+            lb.load(st.p[1], s_begin, s_end, tid);
+            la.load(st.p[2], s_begin + 1, s_end, tid);
+            lb.load(st.p[3], s_begin + 1, s_end, tid);
             gemm::meet<kLoadsA + kLoadsB>();
             read_phase(st.p[0], st.p[1], 0);
-            for (int s = s_begin; s < s_end; s += 5) {
+            for (int s = s_begin;;) {
                 step(s, std::integral_constant<int, 0>{});
-                if (s + 1 < s_end) step(s + 1, std::integral_constant<int, 1>{});
-                if (s + 2 < s_end) step(s + 2, std::integral_constant<int, 2>{});
-                if (s + 3 < s_end) step(s + 3, std::integral_constant<int, 3>{});
-                if (s + 4 < s_end) step(s + 4, std::integral_constant<int, 4>{});
+                if (++s == s_end) break;
+                step(s, std::integral_constant<int, 1>{});
+                if (++s == s_end) break;
+                step(s, std::integral_constant<int, 2>{});
+                if (++s == s_end) break;
+                step(s, std::integral_constant<int, 3>{});
+                if (++s == s_end) break;
+                step(s, std::integral_constant<int, 4>{});
+                if (++s == s_end) break;
             }
         } else {
             auto step = [&](int s, char *ta, char *tb, const char *na, const char *nb) {
                 take_scales();
                 next_scales(s + 1);
+                ra.renew();
+                rb.renew();
+                la.renew();
+                lb.renew();
 #pragma unroll
                 for (int ph = 0; ph + 1 < kPhases; ++ph) {
                     read_phase(ta, tb, ph + 1);
@@ -238,16 +320,16 @@ __device__ __forceinline__ void mx_tile(const Operand<CodePair> &A, const uint8_
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 gemm::meet<(NB - 2) * (kLoadsA + kLoadsB)>();
-                la.load(ta, valid(s + NB), tid);
-                lb.load(tb, valid(s + NB), tid);
+                la.load(ta, s + NB, s_end, tid);
+                lb.load(tb, s + NB, s_end, tid);
                 read_phase(na, nb, 0);
                 mul_phase(kPhases - 1);
                 __builtin_amdgcn_sched_barrier(0);
             };
 #pragma unroll
             for (int t = 0; t < NB; ++t) {
-                la.load(st.a[t], valid(s_begin + t), tid);
-                lb.load(st.b[t], valid(s_begin + t), tid);
+                la.load(st.a[t], s_begin + t, s_end, tid);
+                lb.load(st.b[t], s_begin + t, s_end, tid);
             }
             gemm::meet<(NB - 1) * (kLoadsA + kLoadsB)>();
             read_phase(st.a[0], st.b[0], 0);
@@ -607,14 +689,14 @@ hipError_t large_fp4(const MxLinearCall &c, const MxMatrix &x, const MxLayout &l
     uint8_t *xs = reinterpret_cast<uint8_t *>(ws + lay.xs);
     uint8_t *wsc = xs + pad(xt, 2) * steps * 1024;
     // (256 x 256 tiles read whole pairs of 128 rows)
-    const ScaleArgs sx{x.scale, c.B, groups, steps, xs,
-                       static_cast<int64_t>(pad(xt, 2)) * steps * 64};
-    const ScaleArgs sw{c.w.scale, c.M, groups, steps, wsc,
-                       static_cast<int64_t>(pad(wt, 2)) * steps * 64};
+    const ScaleArgs sx{x.scale, c.B, groups, static_cast<uint32_t>(steps), xs,
+                       static_cast<int64_t>(pad(xt, 2)) * steps * 16};
+    const ScaleArgs sw{c.w.scale, c.M, groups, static_cast<uint32_t>(steps), wsc,
+                       static_cast<int64_t>(pad(wt, 2)) * steps * 16};
     hipError_t e;
     if (steps > 0) {
         hipLaunchKernelGGL(order_scales_kernel,
-                           dim3(static_cast<unsigned>((sx.lanes + sw.lanes + 255) / 256)),
+                           dim3(static_cast<unsigned>((sx.work + sw.work + 255) / 256)),
                            dim3(256), 0, s, sx, sw);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -696,20 +778,30 @@ hipError_t linear(const MxLinearCall &c, char *ws, hipStream_t s) {
 
 // fp16 holds the values times the power of two that brings the largest finite scale's largest
 // code next to the type's own largest number (1.75 2^15), so that none overflows and only those
-// 2^-36 of it are rounded; the sums are multiplied by its inverse.
+// 2^-36 of it are rounded; the sums are multiplied by its inverse.  tops[block] = the largest scale
+// byte but 255 of the block's share; whoever unpacks takes the largest of them.
 struct TopArgs {
     const uint8_t *scale;
     int64_t n;
-    int *up, *down;   // the values' shift and the result's
-    int top;          // exponent of the largest code
+    int *tops;
 };
-__global__ __launch_bounds__(1024) void scale_shift_kernel(TopArgs w, TopArgs x) {
-    const TopArgs &a = blockIdx.x == 0 ? w : x;
+__global__ __launch_bounds__(1024) void scale_tops_kernel(TopArgs w, TopArgs x) {
+    const TopArgs &a = blockIdx.y == 0 ? w : x;
     __shared__ int red[16];
     int top = 0;
-    for (int64_t i = threadIdx.x; i < a.n; i += 1024) {
-        const int e = a.scale[i];
-        if (e != 255 && e > top) top = e;
+    const auto take = [&](uint32_t e) {
+        if (e != 255 && static_cast<int>(e) > top) top = static_cast<int>(e);
+    };
+    struct __attribute__((packed)) Sixteen { uint32_t v[4]; };
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 1024 + threadIdx.x) * 16; i < a.n;
+         i += kMxTops * 1024 * 16) {
+        if (i + 16 <= a.n) {
+            const Sixteen q = *reinterpret_cast<const Sixteen *>(a.scale + i);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) take(q.v[k / 4] >> (8 * (k % 4)) & 255u);
+        } else {
+            for (int64_t k = i; k < a.n; ++k) take(a.scale[k]);
+        }
     }
     for (int d = 32; d; d >>= 1) {
         const int o = __shfl_xor(top, d);
@@ -719,8 +811,7 @@ __global__ __launch_bounds__(1024) void scale_shift_kernel(TopArgs w, TopArgs x)
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int v = 1; v < 16; ++v) top = top > red[v] ? top : red[v];
-        *a.up = 127 + 15 - a.top - top;
-        *a.down = top + a.top - 127 - 15;
+        a.tops[blockIdx.x] = top;
     }
 }
 
@@ -791,38 +882,39 @@ size_t mx_grad_bytes(int dtype, int64_t B, int64_t M, int64_t N, bool dx, bool d
 hipError_t launch_mx_grad(const MxGrad &c, char *ws, hipStream_t s) {
     const MxGradLayout lay = mx_grad_layout(c.dtype == TCQ_F32 ? 4 : 2, c.B, c.M, c.N, c.dx, c.dw,
                                             c.dbias);
-    int *shift = reinterpret_cast<int *>(ws + lay.shifts);  // w up, w down, x up, x down
+    int *tops = reinterpret_cast<int *>(ws + lay.shifts);   // W's, x's, and the two exponents
+    int *down = tops + 2 * kMxTops;
     const bool shifted = c.dtype == TCQ_F16;
     const bool dx = c.dx && c.B > 0 && c.N > 0, dw = c.dw && c.M > 0 && c.N > 0;
     const bool read_w = dx && c.M > 0, read_x = dw && c.B > 0;
     hipError_t e;
     if (shifted && (read_w || read_x)) {
         const int64_t groups = groups_of(c.N);
-        const TopArgs w{c.w.scale, c.M * groups, shift, shift + 1, 2};
-        const TopArgs x{c.x.scale, c.B * groups, shift + 2, shift + 3,
-                        c.x.format == TCQ_FP4 ? 2 : 8};
-        // (the second is x's, the first w's, or x's alone)
-        hipLaunchKernelGGL(scale_shift_kernel, dim3(read_w && read_x ? 2 : 1), dim3(1024), 0, s,
-                           read_w ? w : x, x);
+        const TopArgs w{c.w.scale, c.M * groups, tops};
+        const TopArgs x{c.x.scale, c.B * groups, tops + kMxTops};
+        hipLaunchKernelGGL(scale_tops_kernel, dim3(kMxTops, read_w && read_x ? 2 : 1), dim3(1024),
+                           0, s, read_w ? w : x, x);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (read_w) {
+        const MxShift shift{tops, down};
         e = launch_mx_unpack(c.w, c.M, c.N, c.dtype, ws + lay.w, lay.ldn, lay.ldn,
-                             shifted ? shift : nullptr, s);
+                             shifted ? &shift : nullptr, s);
         if (e != hipSuccess) return e;
     }
     if (read_x) {
+        const MxShift shift{tops + kMxTops, down + 1};
         e = launch_mx_unpack(c.x, c.B, c.N, c.dtype, ws + lay.x, lay.ldn, lay.ldn,
-                             shifted ? shift + 2 : nullptr, s);
+                             shifted ? &shift : nullptr, s);
         if (e != hipSuccess) return e;
     }
     const DenseGrad d{c.dtype, c.dy,
                       c.B,     c.lddy,
                       c.M,     c.N,
                       ws + lay.w, ws + lay.x,
-                      shifted && read_w ? shift + 1 : nullptr,
-                      shifted && read_x ? shift + 3 : nullptr,
+                      shifted && read_w ? down : nullptr,
+                      shifted && read_x ? down + 1 : nullptr,
                       dx ? c.dx : nullptr, c.lddx,
                       dw ? c.dw : nullptr, c.lddw,
                       c.dbias};

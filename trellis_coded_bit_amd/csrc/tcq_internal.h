@@ -208,12 +208,18 @@ struct MxMatrix {
 };
 // Codes and scale bytes, and, where values is not NULL, the bf16 numbers they stand for (up to
 // whole groups); codes and scale may be NULL.  Unpack also writes zeros to columns cols ..
-// padded - 1 and multiplies 16-bit values by 2^*shift_at (NULL: 1).
+// padded - 1, and with a shift multiplies fp16 values by the power of two that brings the largest
+// code of the largest scale byte below 2^16; its inverse's exponent goes to *down.
 hipError_t launch_mx_pack(const void *X, int dtype, int64_t rows, int64_t cols, int64_t ldx,
                           int format, uint8_t *codes, int64_t ldq, uint8_t *scale,
                           uint16_t *values, int64_t ldv, hipStream_t s);
+constexpr int kMxTops = 16;
+struct MxShift {
+    const int *tops;   // kMxTops scale bytes, the largest among them
+    int *down;
+};
 hipError_t launch_mx_unpack(const MxMatrix &m, int64_t rows, int64_t cols, int dtype, void *out,
-                            int64_t ldo, int64_t padded, const int *shift_at, hipStream_t s);
+                            int64_t ldo, int64_t padded, const MxShift *shift, hipStream_t s);
 // The microscaled linear layer and its gradients.
 struct MxLinearCall {
     MxMatrix w;
