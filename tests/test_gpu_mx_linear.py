@@ -49,8 +49,9 @@ def _inside(got, want, bound, what):
         f"{what}: {int(bad.sum())} outside, worst {float((off / bound).max()):.3g} of the bound"
 
 
-# few rows (quantised in the kernel or before it), 128 x 128 tiles whole and split, 256 x 256 ones
-SIZES = [(1, 1, 1), (1, 16, 32), (2, 17, 33), (5, 100, 130), (16, 48, 1000), (17, 64, 256),
+# few rows (quantised in the kernel or before it, in one share or several), 128 x 128 tiles whole
+# and split, 256 x 256 ones
+SIZES = [(513, 17, 96), (600, 70, 2100), (1000, 1100, 700), (1100, 2050, 520), (1, 1, 1), (1, 16, 32), (2, 17, 33), (5, 100, 130), (16, 48, 1000), (17, 64, 256),
          (33, 40, 515), (70, 130, 129), (128, 200, 544), (129, 130, 260), (300, 513, 1100),
          (1030, 2050, 200), (200, 144, 4096), (2049, 4000, 96), (3, 2000, 9000)]
 
@@ -100,7 +101,7 @@ def test_exact_sums(B, M, N, fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("B", [1, 9, 40, 150, 1000])
+@pytest.mark.parametrize("B", [1, 9, 40, 150, 1000, 6700])
 def test_scales_meet_their_groups(B, fmt):
     """One non-zero group of x at a time, every scale different: a scale that is read for another
     group, row or operand changes the result."""
@@ -121,7 +122,7 @@ def test_scales_meet_their_groups(B, fmt):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
-@pytest.mark.parametrize("B", [1, 20, 200, 2100])
+@pytest.mark.parametrize("B", [1, 20, 200, 7300])
 def test_nan_stays_in_its_row(B, dtype, fmt):
     M, N = 520, 256
     g = _gen(B)
@@ -167,10 +168,11 @@ def test_one_workspace_for_smaller_batches(fmt):
     w = _weights(g, M, N)
     from trellis_coded_bit_amd import _lib
     sizes = [_lib.tcq_mx_linear_workspace_bytes(api._FORMATS[fmt], B, M, N)
-             for B in (1, 16, 17, 128, 129, 200, 255, 256, 257, 1000, 5000)]
+             for B in (1, 16, 17, 128, 129, 200, 255, 256, 257, 512, 513, 1000, 5000,
+                       7000)]
     assert sizes == sorted(sizes)
     ws = api.Workspace(sizes[-1])
-    for B in (5000, 1, 129, 40):
+    for B in (7000, 1, 129, 40, 600):
         x = _randn(g, B, N).bfloat16()
         assert torch.equal(api.mx_linear(x, w, x_format=fmt, workspace=ws),
                            api.mx_linear(x, w, x_format=fmt))
@@ -192,7 +194,7 @@ def test_empty_sizes():
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("B", [1, 50, 300])
+@pytest.mark.parametrize("B", [1, 50, 300, 7200])
 def test_streams_and_graph(B, fmt):
     M, N = 256, 1024
     g = _gen(3)

@@ -22,6 +22,8 @@ struct MxPackArgs {
     uint8_t *scale;     // rows x groups, or NULL
     __bf16 *values;     // the values the codes stand for, rows of ldv, or NULL
     int64_t ldv;
+    MxOrder order;      // codes NULL: not wanted
+    uint32_t groups;    // of a row (pieces go on to whole pairs where an order is wanted)
 };
 
 // Eight consecutive values per thread; four neighbouring lanes share a group.
@@ -55,6 +57,21 @@ __global__ __launch_bounds__(256) void mx_pack_kernel(MxPackArgs a) {
         const int e = mx::scale_byte<FMT>(mx::group_top(top));
         uint32_t w[2];
         mx::encode8<FMT>(x, e, w);
+        if (a.order.codes) {
+            // pair, tile of 16 rows, group of the lane's two, (half,) lane; 16 bytes each
+            const uint32_t grp = c >> 2, part = c & 3, pair = grp >> 3, k = grp & 1;
+            const uint32_t lane = (grp & 7) / 2 * 16 + (static_cast<uint32_t>(r) & 15);
+            const int64_t at = static_cast<int64_t>(pair) * a.order.nbt + (r >> 4);
+            if constexpr (FMT == TCQ_FP4)
+                reinterpret_cast<uint32_t *>(a.order.codes)[((at * 2 + k) * 64 + lane) * 4 + part] =
+                    w[0];
+            else
+                reinterpret_cast<uint2 *>(
+                    a.order.codes)[(((at * 2 + k) * 2 + part / 2) * 64 + lane) * 2 + part % 2] =
+                    make_uint2(w[0], w[1]);
+            if (part == 0) a.order.scale[(at * 64 + lane) * 2 + k] = static_cast<uint8_t>(e);
+            if (grp >= a.groups) continue;
+        }
         if (a.codes) {
             uint8_t *q = a.codes + r * a.ldq + static_cast<int64_t>(c) * mx::bytes<FMT>(8);
             if constexpr (FMT == TCQ_FP4)
@@ -62,7 +79,7 @@ __global__ __launch_bounds__(256) void mx_pack_kernel(MxPackArgs a) {
             else
                 *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
         }
-        if (a.scale && (c & 3) == 0) a.scale[i >> 2] = static_cast<uint8_t>(e);
+        if (a.scale && (c & 3) == 0) a.scale[r * a.groups + (c >> 2)] = static_cast<uint8_t>(e);
         if (a.values) {
             const float s = mx::scale_of(e);
             uint32_t v[4];
@@ -180,10 +197,13 @@ hipError_t unpack(const MxMatrix &m, int64_t rows, int64_t cols, void *out, int6
 
 hipError_t launch_mx_pack(const void *X, int dtype, int64_t rows, int64_t cols, int64_t ldx,
                           int format, uint8_t *codes, int64_t ldq, uint8_t *scale,
-                          uint16_t *values, int64_t ldv, hipStream_t s) {
-    const int64_t cpr = (cols + mx::kGroup - 1) / mx::kGroup * 4;
-    const MxPackArgs a{X,     cols, ldx, {static_cast<uint32_t>(cpr), rows * cpr},
-                       codes, ldq,  scale, reinterpret_cast<__bf16 *>(values), ldv};
+                          uint16_t *values, int64_t ldv, const MxOrder *order, hipStream_t s) {
+    const int64_t groups = (cols + mx::kGroup - 1) / mx::kGroup;
+    const int64_t cpr = (order ? (groups + 7) / 8 * 8 : groups) * 4;
+    const MxPackArgs a{X, cols, ldx, {static_cast<uint32_t>(cpr), rows * cpr}, codes, ldq, scale,
+                       reinterpret_cast<__bf16 *>(values), ldv,
+                       order ? *order : MxOrder{nullptr, nullptr, 0},
+                       static_cast<uint32_t>(groups)};
     const bool fp4 = format == TCQ_FP4;
     switch (dtype) {
         case TCQ_F32: return fp4 ? pack<float, TCQ_FP4>(a, s) : pack<float, TCQ_FP8>(a, s);

@@ -383,60 +383,104 @@ __global__ __launch_bounds__(WI *WJ * 64) void mx_gemm_kernel(Operand<CodePair> 
 
 // ---------------------------------------------------------------- few rows of x
 
-// y for at most 16 BT rows of x: a workgroup of 16 waves takes 16 rows of W, whose columns the
-// waves share in units of 128 (four groups, one to each 16 lanes).  W is read once, 16 bytes a
-// lane, straight into the matrix instruction's operand: as codes with 4-bit rows; with 8-bit
-// ones a group's 32 codes become four bf16 fragments, fragment j holding columns 8 j .. 8 j + 7
-// of the lane's group, which is another order of k than memory's and the same for both operands.
+// y for 16 BT rows of x (blockIdx.y's).  A workgroup of eight waves takes 16 rows of W at a time; the
+// waves share their columns in pairs of 128 (eight groups).  W is read once, straight into the
+// matrix instruction's operand: lane (l16, g) reads groups 2 g and 2 g + 1 of a pair, 32 bytes of
+// row l16, so that an instruction touches a line of each row and the two scales are one access.
+// With 4-bit rows the codes are the operand; with 8-bit ones a group's 32 codes become four bf16
+// fragments, fragment j holding columns 8 j .. 8 j + 7 of the lane's group.  Either is another
+// order of k than memory's, the same for both operands.
+//   The next chunk's W, or the next rows', is on its way while one is multiplied and the waves' sums
+// meet in LDS (in wave order, in two halves by turns).
 //   DENSE: x comes as it is (few values) and is quantised into LDS by every workgroup, in the
-// form the products read.  The waves' sums meet in LDS and are added in wave order.
-constexpr int kMxWaves = 16;
-constexpr int kMxUnits = 4;   // units of a wave's loads in flight
+// form the products read.  Otherwise it comes in the order in which the lanes read it (one
+// contiguous KiB per instruction: 16 rows of codes as they lie cost an instruction 16 lines).
+constexpr int kMxWaves = 8;
 
 struct MxSmallArgs {
     const uint8_t *w, *ws;
     int64_t ldw;
     int64_t M;
-    int N, groups, units;
+    int N, groups, pairs, tiles;
     const void *x;
     int64_t ldx;
-    const uint8_t *xq, *xs;
-    int64_t ldq;
-    int B;
-    int ldl;       // bytes of a row of x in LDS (DENSE)
+    const uint8_t *xq;       // in order
+    const uint16_t *xs;
+    int B, nbt, per;         // tiles of 16 rows, in all and to a workgroup (at most BT)
+    int ldl;                 // bytes of a row of x in LDS (DENSE)
+    int red;                 // where the sums' halves start in LDS
 };
+
+template <int FMT>
+struct XFragment {
+    i32x4 q[FMT == TCQ_FP4 ? 1 : 2];   // a group's codes
+};
+
+// Four bf16 fragments of a group of 32 codes.
+template <int FMT>
+__device__ __forceinline__ void group_bf16(const i32x4 *q, float s, s16x8 (&f)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t o[4];
+        if constexpr (FMT == TCQ_FP4) {
+            mx::decode_word_bf16<FMT>(static_cast<uint32_t>(q[0][j]), s, o);
+        } else {
+            mx::decode_word_bf16<FMT>(static_cast<uint32_t>(q[j / 2][2 * (j % 2)]), s, o);
+            mx::decode_word_bf16<FMT>(static_cast<uint32_t>(q[j / 2][2 * (j % 2) + 1]), s, o + 2);
+        }
+        f[j] = __builtin_bit_cast(s16x8,
+                                  (i32x4{static_cast<int>(o[0]), static_cast<int>(o[1]),
+                                         static_cast<int>(o[2]), static_cast<int>(o[3])}));
+    }
+}
 
 template <typename T, int FMT, int BT, bool DENSE>
 __global__ __launch_bounds__(kMxWaves * 64) void mx_small_kernel(MxSmallArgs a,
                                                                  LayerEpilogue<T> epi) {
     extern __shared__ __align__(16) char lds[];
+    constexpr int U = 2;    // pairs of a chunk
     const int tid = threadIdx.x;
     const int lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * 16;
-    const int64_t row = j0 + l16 < a.M ? j0 + l16 : a.M - 1;
-    const uint8_t *wr = a.w + row * a.ldw;
-    const uint8_t *wsr = a.ws + row * a.groups;
-    const int u0 = wave * a.units / kMxWaves, u1 = (wave + 1) * a.units / kMxWaves;
-    i32x4 wc[kMxUnits];
-    uint32_t we[kMxUnits];
-    // (groups past the end: codes of zero, a scale of 1)
-    auto load_w = [&](int u, i32x4 &c, uint32_t &e) {
-        const int grp = u * 4 + g;
-        const bool in = u < u1 && grp < a.groups;
-        c = i32x4{0, 0, 0, 0};
-        e = 127;
-        if (in) {
-            c = *reinterpret_cast<const i32x4 *>(wr + grp * 16);
-            e = wsr[grp];
+    const int p0 = wave * a.pairs / kMxWaves, p1 = (wave + 1) * a.pairs / kMxWaves;
+    const int chunks = ((a.pairs + kMxWaves - 1) / kMxWaves + U - 1) / U;   // of the longest share
+    struct WPair {
+        i32x4 q[2];
+        uint32_t e;      // two scale bytes
+    };
+    WPair w[U];
+    // Pair p of the tile's rows, or zeros (groups past the end: codes of zero, scales of 1).
+    auto load_w = [&](int tile, int p, WPair &o) {
+        const int64_t j = static_cast<int64_t>(tile) * 16 + l16;
+        const int64_t row = j < a.M ? j : a.M - 1;
+        const int grp = p * 8 + 2 * g;
+        o.q[0] = o.q[1] = i32x4{0, 0, 0, 0};
+        o.e = 0x7F7Fu;
+        if (p >= p1 || tile >= a.tiles) return;
+        const uint8_t *q = a.w + row * a.ldw + grp * 16, *e = a.ws + row * a.groups + grp;
+        if (p * 8 + 8 <= a.groups) {
+            struct __attribute__((packed)) Two { uint16_t v; };
+            o.q[0] = *reinterpret_cast<const i32x4 *>(q);
+            o.q[1] = *reinterpret_cast<const i32x4 *>(q + 16);
+            o.e = reinterpret_cast<const Two *>(e)->v;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (grp + k < a.groups) {
+                    o.q[k] = *reinterpret_cast<const i32x4 *>(q + 16 * k);
+                    o.e = (o.e & ~(255u << (8 * k))) | static_cast<uint32_t>(e[k]) << (8 * k);
+                }
         }
     };
+    const int bt0 = blockIdx.y * a.per;    // the first of its tiles of rows
+    const int nbt = a.nbt - bt0 < a.per ? a.nbt - bt0 : a.per;
+    int tile = blockIdx.x;
 #pragma unroll
-    for (int k = 0; k < kMxUnits; ++k) load_w(u0 + k, wc[k], we[k]);
-    char *xscale = lds + a.B * a.ldl;  // (DENSE, 4-bit: scale bytes, units x 4 to a row)
+    for (int k = 0; k < U; ++k) load_w(tile, p0 + k, w[k]);
+    char *xscale = lds + a.B * a.ldl;  // (DENSE, 4-bit: scale bytes, pairs x 8 to a row)
     if constexpr (DENSE) {
-        // four lanes to a group; groups up to whole units
-        const int per = a.units * 16;
+        // four lanes to a group; groups up to whole pairs
+        const int per = a.pairs * 32;
         const T *X = static_cast<const T *>(a.x);
         for (int i = tid; i < a.B * per; i += kMxWaves * 64) {
             const int r = i / per, c = i - r * per;
@@ -462,7 +506,7 @@ __global__ __launch_bounds__(kMxWaves * 64) void mx_small_kernel(MxSmallArgs a,
             mx::encode8<FMT>(v, e, q);
             if constexpr (FMT == TCQ_FP4) {
                 *reinterpret_cast<uint32_t *>(lds + r * a.ldl + c * 4) = q[0];
-                if ((c & 3) == 0) xscale[r * a.units * 4 + (c >> 2)] = static_cast<char>(e);
+                if ((c & 3) == 0) xscale[r * a.pairs * 8 + (c >> 2)] = static_cast<char>(e);
             } else {
                 uint32_t o[4];
                 mx::decode_word_bf16<FMT>(q[0], mx::scale_of(e), o);
@@ -474,109 +518,145 @@ __global__ __launch_bounds__(kMxWaves * 64) void mx_small_kernel(MxSmallArgs a,
         __syncthreads();
     }
     f32x4 acc[BT];
+    auto multiply = [&](int p, const WPair &c) {
+        if constexpr (DENSE) {
+            static_assert(!DENSE || BT == 1, "one tile of rows");
+            const int grp = p * 8 + 2 * g;
 #pragma unroll
-    for (int b = 0; b < BT; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto multiply = [&](int u, const i32x4 &c, uint32_t e) {
-        const int grp = u * 4 + g;
-        if constexpr (FMT == TCQ_FP4) {
+            for (int k = 0; k < 2; ++k) {
+                if constexpr (FMT == TCQ_FP4) {
+                    i32x4 xq = {0, 0, 0, 0};
+                    uint32_t xe = 127;
+                    if (l16 < a.B) {
+                        xq = *reinterpret_cast<const i32x4 *>(lds + l16 * a.ldl + (grp + k) * 16);
+                        xe = static_cast<uint8_t>(xscale[l16 * a.pairs * 8 + grp + k]);
+                    }
+                    acc[0] = k == 0 ? mma_fp4<0, 0>(c.q[0], c.e, xq, xe, acc[0])
+                                    : mma_fp4<1, 0>(c.q[1], c.e, xq, xe, acc[0]);
+                } else {
+                    s16x8 wf[4];
+                    group_bf16<TCQ_FP4>(&c.q[k], mx::scale_of(c.e >> (8 * k) & 255), wf);
 #pragma unroll
-            for (int b = 0; b < BT; ++b) {
-                const int r = b * 16 + l16;
-                i32x4 xc = {0, 0, 0, 0};
-                uint32_t xe = 127;
-                if (r < a.B && grp < a.groups) {
-                    if constexpr (DENSE) {
-                        xc = *reinterpret_cast<const i32x4 *>(lds + r * a.ldl + grp * 16);
-                        xe = static_cast<uint8_t>(xscale[r * a.units * 4 + grp]);
-                    } else {
-                        xc = *reinterpret_cast<const i32x4 *>(a.xq + r * a.ldq + grp * 16);
-                        xe = a.xs[static_cast<int64_t>(r) * a.groups + grp];
+                    for (int j = 0; j < 4; ++j) {
+                        s16x8 xf = {0, 0, 0, 0, 0, 0, 0, 0};
+                        if (l16 < a.B)
+                            xf = *reinterpret_cast<const s16x8 *>(lds + l16 * a.ldl +
+                                                                  (grp + k) * 64 + j * 16);
+                        acc[0] = gemm::Traits<__bf16>::mma(wf[j], xf, acc[0]);
                     }
                 }
-                acc[b] = mma_fp4<0, 0>(c, e, xc, xe, acc[b]);
             }
         } else {
-            s16x8 wf[4];
-            const float s = mx::scale_of(static_cast<int>(e));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t o[4];
-                mx::decode_word_bf16<TCQ_FP4>(static_cast<uint32_t>(c[j]), s, o);
-                wf[j] = __builtin_bit_cast(s16x8, (i32x4{static_cast<int>(o[0]), static_cast<int>(o[1]),
-                                                        static_cast<int>(o[2]), static_cast<int>(o[3])}));
-            }
+            constexpr int kHalves = FMT == TCQ_FP4 ? 1 : 2;
+            XFragment<FMT> x[BT][2];
+            uint32_t xe[BT];
 #pragma unroll
             for (int b = 0; b < BT; ++b) {
-                const int r = b * 16 + l16;
-                s16x8 xf[4];
-                if constexpr (DENSE) {
+                // (tiles of rows past the last repeat it: their sums are not stored)
+                const int t = bt0 + (b < nbt ? b : nbt - 1);
+                const int64_t at = static_cast<int64_t>(p) * a.nbt + t;
+                const i32x4 *q = reinterpret_cast<const i32x4 *>(a.xq) + at * (128 * kHalves) + lane;
+                xe[b] = a.xs[at * 64 + lane];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        xf[j] = s16x8{0, 0, 0, 0, 0, 0, 0, 0};
-                        if (r < a.B)
-                            xf[j] = *reinterpret_cast<const s16x8 *>(lds + r * a.ldl + grp * 64 +
-                                                                     j * 16);
-                    }
-                } else {
-                    i32x4 x0 = {0, 0, 0, 0}, x1 = x0;
-                    int xe = 127;
-                    if (r < a.B && grp < a.groups) {
-                        const uint8_t *p = a.xq + r * a.ldq + grp * 32;
-                        x0 = *reinterpret_cast<const i32x4 *>(p);
-                        x1 = *reinterpret_cast<const i32x4 *>(p + 16);
-                        xe = a.xs[static_cast<int64_t>(r) * a.groups + grp];
-                    }
-                    const float xsc = mx::scale_of(xe);
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const i32x4 &src = j < 2 ? x0 : x1;
-                        uint32_t o[4];
-                        mx::decode_word_bf16<TCQ_FP8>(static_cast<uint32_t>(src[2 * (j % 2)]), xsc,
-                                                      o);
-                        mx::decode_word_bf16<TCQ_FP8>(static_cast<uint32_t>(src[2 * (j % 2) + 1]),
-                                                      xsc, o + 2);
-                        xf[j] = __builtin_bit_cast(
-                            s16x8, (i32x4{static_cast<int>(o[0]), static_cast<int>(o[1]),
-                                          static_cast<int>(o[2]), static_cast<int>(o[3])}));
+                    for (int h = 0; h < kHalves; ++h) x[b][k].q[h] = q[(k * kHalves + h) * 64];
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                s16x8 wf[4];
+                if constexpr (FMT == TCQ_FP8)
+                    group_bf16<TCQ_FP4>(&c.q[k], mx::scale_of(c.e >> (8 * k) & 255), wf);
+#pragma unroll
+                for (int b = 0; b < BT; ++b) {
+                    if constexpr (FMT == TCQ_FP4) {
+                        acc[b] = k == 0 ? mma_fp4<0, 0>(c.q[0], c.e, x[b][0].q[0], xe[b], acc[b])
+                                        : mma_fp4<1, 1>(c.q[1], c.e, x[b][1].q[0], xe[b], acc[b]);
+                    } else {
+                        s16x8 xf[4];
+                        group_bf16<TCQ_FP8>(x[b][k].q, mx::scale_of(xe[b] >> (8 * k) & 255), xf);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            acc[b] = gemm::Traits<__bf16>::mma(wf[j], xf[j], acc[b]);
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[b] = gemm::Traits<__bf16>::mma(wf[j], xf[j], acc[b]);
             }
         }
     };
-    for (int u = u0; u < u1; u += kMxUnits) {
+    for (int turn = 0; tile < a.tiles; tile += gridDim.x, turn ^= 1) {
 #pragma unroll
-        for (int k = 0; k < kMxUnits; ++k) {
-            const i32x4 c = wc[k];
-            const uint32_t e = we[k];
-            load_w(u + kMxUnits + k, wc[k], we[k]);
-            if (u + k < u1) multiply(u + k, c, e);
+        for (int b = 0; b < BT; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < chunks; ++c) {
+            const bool last = c + 1 == chunks;
+            const int next = last ? tile + static_cast<int>(gridDim.x) : tile;
+            const int from = last ? p0 : p0 + (c + 1) * U;
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const WPair now = w[k];
+                load_w(next, from + k, w[k]);
+                if (p0 + c * U + k < p1) multiply(p0 + c * U + k, now);
+            }
+        }
+        // The waves' sums: 16 BT x 16 values each, value (row j of W, row b of x) of a tile in word
+        // (j / 4 * 16 + b) * 4 + j % 4.
+        float *red = reinterpret_cast<float *>(lds + a.red) + turn * (kMxWaves * BT * 256);
+#pragma unroll
+        for (int b = 0; b < BT; ++b)
+            *reinterpret_cast<f32x4 *>(red + ((wave * BT + b) * 64 + lane) * 4) = acc[b];
+        __syncthreads();
+        for (int i = tid; i < nbt * 256; i += kMxWaves * 64) {
+            const int j = i & 15, b = i >> 4;
+            const int at = (b >> 4) * 256 + ((j >> 2) * 16 + (b & 15)) * 4 + (j & 3);
+            float s = red[at];
+#pragma unroll
+            for (int v = 1; v < kMxWaves; ++v) s += red[v * BT * 256 + at];
+            epi.put_one(bt0 * 16 + b, static_cast<int64_t>(tile) * 16 + j, s);
         }
     }
-    // The waves' sums: 16 BT x 16 values each, value (row j of W, row b of x) of a tile in word
-    // (j / 4 * 16 + b) * 4 + j % 4.
-    if constexpr (DENSE) __syncthreads();
-    float *red = reinterpret_cast<float *>(lds);
-#pragma unroll
-    for (int b = 0; b < BT; ++b)
-        *reinterpret_cast<f32x4 *>(red + ((wave * BT + b) * 64 + lane) * 4) = acc[b];
-    __syncthreads();
-    for (int i = tid; i < BT * 256; i += kMxWaves * 64) {
-        const int j = i & 15, b = i >> 4;
-        const int at = (b >> 4) * 256 + ((j >> 2) * 16 + (b & 15)) * 4 + (j & 3);
-        float s = red[at];
-#pragma unroll
-        for (int v = 1; v < kMxWaves; ++v) s += red[v * BT * 256 + at];
-        epi.put_one(b, j0 + j, s);
-    }
+}
+
+// Codes of B rows as they lie into the order in which mx_small_kernel's lanes read them: pair, tile of
+// 16 rows, group of the lane's two, half (8-bit), lane; scales: pair, tile, lane, group.  16
+// bytes a thread.
+template <int FMT>
+__global__ __launch_bounds__(256) void order_rows_kernel(const uint8_t *__restrict__ codes,
+                                                         int64_t ld,
+                                                         const uint8_t *__restrict__ scale, int B,
+                                                         int groups, MxOrder out, int64_t work) {
+    constexpr int kHalves = FMT == TCQ_FP4 ? 1 : 2;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= work) return;
+    const int lane = static_cast<int>(i & 63), h = static_cast<int>((i >> 6) % kHalves);
+    const int64_t rest = (i >> 6) / kHalves;
+    const int k = static_cast<int>(rest & 1), t = static_cast<int>((rest >> 1) % out.nbt);
+    const int64_t p = (rest >> 1) / out.nbt;
+    const int r = t * 16 + (lane & 15), grp = static_cast<int>(p) * 8 + 2 * (lane >> 4) + k;
+    const bool in = r < B && grp < groups;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (in)
+        v = *reinterpret_cast<const uint4 *>(codes + r * ld +
+                                             (static_cast<int64_t>(grp) * kHalves + h) * 16);
+    reinterpret_cast<uint4 *>(out.codes)[i] = v;
+    if (h == 0)
+        out.scale[((p * out.nbt + t) * 64 + lane) * 2 + k] =
+            in ? scale[static_cast<int64_t>(r) * groups + grp] : 127;
 }
 
 // ---------------------------------------------------------------- host side
 
-constexpr int kMxMostSmall = 128;          // rows of x that mx_small_kernel takes
+// Whether mx_small_kernel takes B rows of x; never one batch and not a smaller one (us per call in
+// a graph, it / the tiled product).  4-bit rows up to 128, and beyond while a row of W's tiles and
+// of x's shares makes at most 896 workgroup turns: 256 x 2048 x 2048 8.7 / 17.3, 384 x 4096 x 4096
+// 24.1 / 26.2, 128 x 14336 x 4096 26.6 / 25.7 (with one row more); 512 x 4096 x 4096 31.0 / 27.0.  8-bit
+// rows, whose tiled product needs W in 16 bits, up to 512: 160 x 4096 x 4096 23.1 / 37.5, 512 x 4096
+// x 4096 44.1 / 44.8, 512 x 14336 x 4096 138 / 161.
+bool mx_small(int format, int64_t B, int64_t M) {
+    if (format == TCQ_FP8) return B <= 512;
+    return B <= 128 || (B + 127) / 128 * ((M + 15) / 16) <= 896;
+}
+
 constexpr int kMxDenseBytes = 96 << 10;    // LDS for x quantised in the kernel
+constexpr int64_t kMxDenseValues = 32768;  // and its values at most
 
 size_t pad(int64_t n, int64_t to) { return static_cast<size_t>((n + to - 1) / to * to); }
 
@@ -598,40 +678,49 @@ LayerEpilogue<T> mx_epilogue(const MxLinearCall &c) {
     return e;
 }
 
-// LDS row of x quantised in the kernel: whole units, 16 bytes more so that rows start in
+int64_t pairs_of(int64_t groups) { return (groups + 7) / 8; }
+
+// LDS row of x quantised in the kernel: whole pairs, 16 bytes more so that rows start in
 // different banks.
-int dense_row(int format, int64_t units) {
-    return static_cast<int>(units * (format == TCQ_FP4 ? 64 : 256) + 16);
+int dense_row(int format, int64_t pairs) {
+    return static_cast<int>(pairs * (format == TCQ_FP4 ? 128 : 512) + 16);
 }
-int64_t dense_bytes(int format, int64_t B, int64_t units) {
-    return B * (dense_row(format, units) + (format == TCQ_FP4 ? units * 4 : 0));
+int64_t dense_bytes(int format, int64_t B, int64_t pairs) {
+    return align_up(B * (dense_row(format, pairs) + (format == TCQ_FP4 ? pairs * 8 : 0)), 16);
 }
 bool small_dense(const MxLinearCall &c) {
-    const int64_t units = (groups_of(c.N) + 3) / 4;
-    return c.x && !c.keep && c.B <= 16 && dense_bytes(c.xq.format, c.B, units) <= kMxDenseBytes;
+    return c.x && !c.keep && c.B <= 16 && c.B * c.N <= kMxDenseValues &&
+           dense_bytes(c.xq.format, c.B, pairs_of(groups_of(c.N))) <= kMxDenseBytes;
 }
 
 template <typename T, int FMT, int BT, bool DENSE>
-hipError_t launch_small_as(const MxSmallArgs &a, const LayerEpilogue<T> &epi, hipStream_t s) {
-    const int64_t sums = int64_t{kMxWaves} * BT * 1024;
-    const int64_t dense = DENSE ? dense_bytes(FMT, a.B, a.units) : 0;
+hipError_t launch_small_as(MxSmallArgs a, const LayerEpilogue<T> &epi, hipStream_t s) {
+    constexpr int kSums = 2 * kMxWaves * BT * 1024;
+    a.red = DENSE ? static_cast<int>(dense_bytes(FMT, a.B, a.pairs)) : 0;
     // (the limit is one of the kernel, not of the call: threads with x of two sizes share it)
     const void *kern = reinterpret_cast<const void *>(mx_small_kernel<T, FMT, BT, DENSE>);
     const hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                             DENSE ? kMxDenseBytes : static_cast<int>(sums));
+                                             (DENSE ? kMxDenseBytes : 0) + kSums);
     if (e != hipSuccess) return e;
+    // as many rounds of tiles for every workgroup
+    const int64_t most = (BT == 1 ? 2 : 1) * 256, rounds = (a.tiles + most - 1) / most;
+    const int64_t grid = (a.tiles + rounds - 1) / rounds;
+    const unsigned shares = static_cast<unsigned>((a.nbt + a.per - 1) / a.per);
     hipLaunchKernelGGL((mx_small_kernel<T, FMT, BT, DENSE>),
-                       dim3(static_cast<unsigned>((a.M + 15) / 16)), dim3(kMxWaves * 64),
-                       static_cast<unsigned>(sums > dense ? sums : dense), s, a, epi);
+                       dim3(static_cast<unsigned>(grid), shares),
+                       dim3(kMxWaves * 64), static_cast<unsigned>(a.red + kSums), s, a, epi);
     return hipGetLastError();
 }
 
 template <typename T, int FMT>
 hipError_t launch_small(MxSmallArgs a, const LayerEpilogue<T> &epi, hipStream_t s) {
+    // up to eight tiles of rows to a workgroup, and about as many for each
+    const int shares = (a.nbt + 7) / 8;
+    a.per = (a.nbt + shares - 1) / shares;
     if (a.x) return launch_small_as<T, FMT, 1, true>(a, epi, s);
-    if (a.B <= 16) return launch_small_as<T, FMT, 1, false>(a, epi, s);
-    if (a.B <= 32) return launch_small_as<T, FMT, 2, false>(a, epi, s);
-    if (a.B <= 64) return launch_small_as<T, FMT, 4, false>(a, epi, s);
+    if (a.per == 1) return launch_small_as<T, FMT, 1, false>(a, epi, s);
+    if (a.per == 2) return launch_small_as<T, FMT, 2, false>(a, epi, s);
+    if (a.per <= 4) return launch_small_as<T, FMT, 4, false>(a, epi, s);
     return launch_small_as<T, FMT, 8, false>(a, epi, s);
 }
 
@@ -721,12 +810,17 @@ hipError_t large_fp4(const MxLinearCall &c, const MxMatrix &x, const MxLayout &l
 template <typename T>
 hipError_t linear(const MxLinearCall &c, char *ws, hipStream_t s) {
     const MxLayout lay = mx_linear_layout(c.xq.format, c.B, c.M, c.N);
-    const bool fp4 = c.xq.format == TCQ_FP4, small = c.B <= kMxMostSmall;
+    const bool fp4 = c.xq.format == TCQ_FP4, small = mx_small(c.xq.format, c.B, c.M);
     const bool dense = small && small_dense(c);
     MxMatrix x = c.xq;
     uint16_t *xvals = reinterpret_cast<uint16_t *>(ws + lay.xvals);
-    // (large batches of 8-bit rows are read as the bf16 numbers that the codes stand for)
+    // (large batches of 8-bit rows are read as the bf16 numbers that the codes stand for, small ones
+    // of either in the order of mx_small_kernel's lanes)
     const bool values = !small && !fp4;
+    const int64_t groups = groups_of(c.N), pairs = pairs_of(groups);
+    const int nbt = static_cast<int>((c.B + 15) / 16);
+    const MxOrder order{reinterpret_cast<uint8_t *>(ws + lay.codes),
+                        reinterpret_cast<uint8_t *>(ws + lay.scale), nbt};
     hipError_t e;
     if (c.x && !dense) {
         if (!c.keep) {
@@ -734,15 +828,23 @@ hipError_t linear(const MxLinearCall &c, char *ws, hipStream_t s) {
             x.ld = lay.ldq;
             x.scale = reinterpret_cast<uint8_t *>(ws + lay.scale);
         }
-        const bool codes = c.keep || !values;
+        const bool codes = c.keep || (!values && !small);
         e = launch_mx_pack(c.x, c.dtype, c.B, c.N, c.ldx, c.xq.format,
                            codes ? const_cast<uint8_t *>(x.codes) : nullptr, x.ld,
                            codes ? const_cast<uint8_t *>(x.scale) : nullptr,
-                           values ? xvals : nullptr, lay.ldn, s);
+                           values ? xvals : nullptr, lay.ldn, small ? &order : nullptr, s);
         if (e != hipSuccess) return e;
     }
     if (small) {
-        const int64_t groups = groups_of(c.N);
+        if (!c.x && c.N > 0) {
+            const int64_t work = pairs * nbt * 128 * (fp4 ? 1 : 2);
+            hipLaunchKernelGGL(fp4 ? order_rows_kernel<TCQ_FP4> : order_rows_kernel<TCQ_FP8>,
+                               dim3(static_cast<unsigned>((work + 255) / 256)), dim3(256), 0, s,
+                               x.codes, x.ld, x.scale, static_cast<int>(c.B),
+                               static_cast<int>(groups), order, work);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
         MxSmallArgs a{};
         a.w = c.w.codes;
         a.ws = c.w.scale;
@@ -750,14 +852,15 @@ hipError_t linear(const MxLinearCall &c, char *ws, hipStream_t s) {
         a.M = c.M;
         a.N = static_cast<int>(c.N);
         a.groups = static_cast<int>(groups);
-        a.units = static_cast<int>((groups + 3) / 4);
+        a.pairs = static_cast<int>(pairs);
+        a.tiles = static_cast<int>((c.M + 15) / 16);
         a.x = dense ? c.x : nullptr;
         a.ldx = c.ldx;
-        a.xq = x.codes;
-        a.xs = x.scale;
-        a.ldq = x.ld;
+        a.xq = order.codes;
+        a.xs = reinterpret_cast<const uint16_t *>(order.scale);
         a.B = static_cast<int>(c.B);
-        a.ldl = dense ? dense_row(c.xq.format, a.units) : 0;
+        a.nbt = nbt;
+        a.ldl = dense ? dense_row(c.xq.format, pairs) : 0;
         const LayerEpilogue<T> epi = mx_epilogue<T>(c);
         return fp4 ? launch_small<T, TCQ_FP4>(a, epi, s) : launch_small<T, TCQ_FP8>(a, epi, s);
     }
@@ -842,14 +945,16 @@ MxGradLayout mx_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bool d
 MxLayout mx_linear_layout(int format, int64_t B, int64_t M, int64_t N) {
     MxLayout l{};
     const int64_t groups = groups_of(N), steps = (groups + 7) / 8;
-    const bool fp4 = format == TCQ_FP4, large = B > kMxMostSmall;
+    const bool fp4 = format == TCQ_FP4, large = !mx_small(format, B, M);
     l.ldq = groups * (fp4 ? 16 : 32);
     l.ldn = groups * mx::kGroup;
     size_t off = 0;
+    // (in the lanes' order whole tiles of 16 rows and whole pairs)
+    const int64_t rows = (B + 15) / 16 * 16, whole = pairs_of(groups) * 8;
     l.codes = off;
-    off += align_up(static_cast<size_t>(B) * l.ldq, 256);
+    off += align_up(static_cast<size_t>(rows) * whole * (fp4 ? 16 : 32), 256);
     l.scale = off;
-    off += align_up(static_cast<size_t>(B) * groups, 256);
+    off += align_up(static_cast<size_t>(rows) * whole, 256);
     l.xs = l.wvals = l.xvals = l.parts = off;
     if (large && fp4) {
         const size_t tiles = pad((B + 127) / 128, 2) + pad((M + 127) / 128, 2);

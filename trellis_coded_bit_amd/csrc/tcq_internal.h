@@ -210,9 +210,15 @@ struct MxMatrix {
 // whole groups); codes and scale may be NULL.  Unpack also writes zeros to columns cols ..
 // padded - 1, and with a shift multiplies fp16 values by the power of two that brings the largest
 // code of the largest scale byte below 2^16; its inverse's exponent goes to *down.
+// order: codes and scale bytes in the order in which the few-rows product reads them (whole tiles of
+// 16 rows, of which those past `rows` are left as they were, and whole pairs of 128 columns).
+struct MxOrder {
+    uint8_t *codes, *scale;
+    int nbt;            // tiles of 16 rows
+};
 hipError_t launch_mx_pack(const void *X, int dtype, int64_t rows, int64_t cols, int64_t ldx,
                           int format, uint8_t *codes, int64_t ldq, uint8_t *scale,
-                          uint16_t *values, int64_t ldv, hipStream_t s);
+                          uint16_t *values, int64_t ldv, const MxOrder *order, hipStream_t s);
 constexpr int kMxTops = 16;
 struct MxShift {
     const int *tops;   // kMxTops scale bytes, the largest among them

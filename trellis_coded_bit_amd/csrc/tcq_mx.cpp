@@ -99,7 +99,7 @@ extern "C" int tcq_mx_pack(const void *X, int dtype, int64_t rows, int64_t cols,
     if (rc == TCQ_OK) rc = check_apart(fn, rs, rq);
     if (rc != TCQ_OK) return rc;
     const hipError_t e = launch_mx_pack(X, dtype, rows, cols, ldx, format, codes, ldq, scale,
-                                        nullptr, 0, stream);
+                                        nullptr, 0, nullptr, stream);
     if (e != hipSuccess) return hip_fail(fn, "quantisation launch", e);
     return TCQ_OK;
 }
