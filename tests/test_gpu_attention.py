@@ -79,6 +79,7 @@ BATCHES = {
     "drafts": [(4, 100), (3, 3), (0, 50), (2, 257), (0, 0), (1, 600)],
     "chunk": [(70, 70)],
     "chunks": [(64, 64), (200, 513), (1, 300), (0, 9), (33, 1000), (17, 17)],
+    "both kinds": [(1, 90), (20, 150), (70, 333), (300, 700), (5, 64), (9, 40)],
     "no keys": [(3, 1), (5, 0), (2, -4), (40, 20)],
 }
 

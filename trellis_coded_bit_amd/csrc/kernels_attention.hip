@@ -43,8 +43,8 @@ struct AttArgs {
     float factor, factor_low;   // scale log2(e), and what it lacks
     float *part;                // shares: [slot][rows of a tile][dim], then maxima and sums
     uint32_t slots;
-    int both;                   // tiles of 16 rows serve sequences of up to 16 rows only, larger
-                                // tiles the others (0: this kernel serves every sequence)
+    int both;                   // tiles of 16 rows serve sequences of up to kFewRows rows only,
+                                // larger tiles the others (0: this kernel serves every sequence)
 };
 
 // ---------------------------------------------------------------- items
@@ -54,7 +54,11 @@ struct Sequence {
     uint32_t tiles, units, chunks;
 };
 constexpr int kUnit = 128;      // keys: runs are whole units
-constexpr int kSmallRows = 16;
+constexpr int kSmallRows = 16;      // query rows of the smaller tiles
+// Rows of a sequence that they serve beside the larger ones, which read keys less often but hold 128
+// or 256 rows (16 sequences of 2000 to 8000 keys, 32 query heads over 8, bf16: 32 rows 88 us with
+// small tiles, 155 with large; 64 rows 122 and 157; 96 rows 173 and 159).
+constexpr int kFewRows = 64;
 constexpr int kTargetSmall = 1024, kTargetLarge = 256;
 template <int BQ>
 constexpr int target() {
@@ -70,7 +74,7 @@ __device__ __forceinline__ Sequence sequence(const AttArgs &a, int64_t s) {
     const int64_t n = sp.end - sp.begin;
     if (n <= 0) return r;
     const uint32_t rows = static_cast<uint32_t>(n) * static_cast<uint32_t>(a.group);
-    const bool small = rows <= kSmallRows;
+    const bool small = rows <= kFewRows;
     if (a.both && small != (BQ == kSmallRows)) return r;
     r.tiles = (rows + BQ - 1) / BQ;
     int64_t keys = sp.first + n;  // the last row sees the keys before this
@@ -688,27 +692,16 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
 
 // ---------------------------------------------------------------- many query rows
 
-// Two tiles of 16 query rows to each wave.  The workgroup's threads decode tiles of keys into LDS
+// NQ tiles of 16 query rows to each of NW waves.  The workgroup's threads decode tiles of keys into LDS
 // for all waves: while a tile is multiplied, the next one's codes, which arrived during the tile
 // before, go into LDS, and those of the one after are asked for.
-//   Where outputs, queries and scores leave room for two waves to a SIMD, a workgroup has eight
-// (256 rows).  The second four meet the others between their scores and their softmax, the first
-// four after the whole tile, so that one wave of a SIMD computes its softmax while the other
+//   With eight waves the second four meet the others between their scores and their softmax, the
+// first four after the whole tile, so that one wave of a SIMD computes its softmax while the other
 // multiplies; values are kept for a tile longer for it.
-template <int D, int TERMS>
-constexpr int many_waves() {
-    return D / 2 + D / 4 * TERMS <= 128 ? 8 : 4;
-}
-template <typename T, int D>
-constexpr int many_rows() {
-    return many_waves<D, terms<T>()>() * 32;
-}
-
-template <typename T, int D, int FMT>
-__global__ __launch_bounds__((many_waves<D, terms<T>()>() * 64)) void attend_many_kernel(AttArgs a) {
+template <typename T, int D, int FMT, int NW, int NQ>
+__global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
     constexpr int TERMS = terms<T>();
-    constexpr int NW = many_waves<D, TERMS>(), NT = NW * 64;
-    constexpr int NQ = 2, BQ = NW * NQ * 16;
+    constexpr int NT = NW * 64, BQ = NW * NQ * 16;
     constexpr int KT = D == 256 ? 32 : 64;                     // keys of a tile
     constexpr int kSub = KT / 16, kPairs = KT / 32;
     constexpr int kRow = mx::bytes<FMT>(D);
@@ -1040,12 +1033,12 @@ __device__ __forceinline__ void join(const AttArgs &a, uint32_t block) {
         __syncthreads();
     }
 }
-template <typename T, int D>
+template <typename T, int D, int BQ>
 __global__ __launch_bounds__(256) void join_kernel(AttArgs few, AttArgs many, uint32_t blocks_few) {
     if (blockIdx.x < blocks_few)
         join<T, D, kSmallRows>(few, blockIdx.x);
     else
-        join<T, D, many_rows<T, D>()>(many, blockIdx.x - blocks_few);
+        join<T, D, BQ>(many, blockIdx.x - blocks_few);
 }
 
 // ---------------------------------------------------------------- host side
@@ -1064,43 +1057,61 @@ constexpr int kSlotsFew = 2 * kTargetSmall, kSlotsMany = 2 * kTargetLarge;
 constexpr int kMostRows = 256;   // of a tile
 int64_t slot_bytes(int bq, int dim) { return int64_t{bq} * (dim + 2) * 4; }
 
-template <typename T, int D, int FMT>
-hipError_t attend(const AttArgs &base, char *ws, hipStream_t s) {
+template <typename T, int D, int FMT, int NW, int NQ>
+hipError_t attend_as(const AttArgs &base, char *ws, hipStream_t s) {
+    constexpr int kRows = NW * NQ * 16;
     AttArgs few = base, many = base;
     const bool only = few_only(base.rows, base.group, base.b.seqs);
     const int64_t heads = base.c.heads;
     few.both = many.both = !only;
     few.part = reinterpret_cast<float *>(ws);
     few.slots = kSlotsFew;
-    constexpr int kRows = many_rows<T, D>();
     many.part = reinterpret_cast<float *>(ws + int64_t{kSlotsFew} * slot_bytes(kSmallRows, D));
     many.slots = kSlotsMany;
     // tiles of all sequences: whole ones of the rows, and a part of one for each
     const int64_t qrows = base.rows * base.group;
-    const int64_t few_tiles = only ? qrows / kSmallRows + base.b.seqs : base.b.seqs;
+    const int64_t few_tiles = qrows / kSmallRows + base.b.seqs;
+    const int64_t few_most = only ? few_tiles : base.b.seqs * (kFewRows / kSmallRows);
+    const int64_t tiles = few_tiles < few_most ? few_tiles : few_most;
     const int64_t many_tiles = qrows / kRows + base.b.seqs;
     hipLaunchKernelGGL((attend_few_kernel<T, D, FMT>),
-                       dim3(static_cast<unsigned>(few_tiles * heads + kTargetSmall)), dim3(256),
-                       0, s, few);
+                       dim3(static_cast<unsigned>(tiles * heads + kTargetSmall)), dim3(256), 0, s,
+                       few);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (!only) {
-        hipLaunchKernelGGL((attend_many_kernel<T, D, FMT>),
+        hipLaunchKernelGGL((attend_many_kernel<T, D, FMT, NW, NQ>),
                            dim3(static_cast<unsigned>(many_tiles * heads + kTargetLarge)),
-                           dim3(kRows * 2), 0, s, many);
+                           dim3(NW * 64), 0, s, many);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     // (a pair of tile and head with several runs has two at least)
-    const auto blocks = [&](int64_t tiles, int slots, int rows) {
-        const int64_t pairs = tiles * heads < slots / 2 ? tiles * heads : slots / 2;
+    const auto blocks = [&](int64_t n, int slots, int rows) {
+        const int64_t pairs = n * heads < slots / 2 ? n * heads : slots / 2;
         return static_cast<uint32_t>(pairs * (rows / kJoinRows));
     };
-    const uint32_t few_blocks = blocks(few_tiles, kSlotsFew, kSmallRows);
+    const uint32_t few_blocks = blocks(tiles, kSlotsFew, kSmallRows);
     const uint32_t many_blocks = only ? 0 : blocks(many_tiles, kSlotsMany, kRows);
-    hipLaunchKernelGGL((join_kernel<T, D>), dim3(few_blocks + many_blocks), dim3(256), 0, s, few,
-                       many, few_blocks);
+    hipLaunchKernelGGL((join_kernel<T, D, kRows>), dim3(few_blocks + many_blocks), dim3(256), 0, s,
+                       few, many, few_blocks);
     return hipGetLastError();
+}
+
+// Two tiles of query rows to a wave read a key from LDS half as often as one, but their outputs,
+// queries and scores need room, and sequences of up to 256 rows leave half of them idle.  us with
+// two / with one (16 or 32 query heads; chunks behind a history; eight waves):
+//   64 dims: bf16 904 / 840, fp16 1208 / 1388, fp32 1862 / 1659;
+//   128 dims: bf16 1349 / 1638, fp16 303 (spills) / 194, fp32 342 (four waves) / 234;
+//   256 dims (all spill, or four waves): bf16 494 / 282, fp16 890 / 351, fp32 1310 / 653;
+//   128 dims, bf16, 16 sequences of 256 rows 247 / 230, of 400 rows 344 / 362.
+template <typename T, int D, int FMT>
+hipError_t attend(const AttArgs &a, char *ws, hipStream_t s) {
+    constexpr bool kTwo = (D == 128 && terms<T>() == 1) || (D == 64 && terms<T>() == 2);
+    if constexpr (kTwo) {
+        if (a.rows * a.group > 256 * a.b.seqs) return attend_as<T, D, FMT, 8, 2>(a, ws, s);
+    }
+    return attend_as<T, D, FMT, 8, 1>(a, ws, s);
 }
 
 template <typename T>
