@@ -59,10 +59,17 @@ constexpr int kSmallRows = 16;      // query rows of the smaller tiles
 // or 256 rows (16 sequences of 2000 to 8000 keys, 32 query heads over 8, bf16: 32 rows 88 us with
 // small tiles, 155 with large; 64 rows 122 and 157; 96 rows 173 and 159).
 constexpr int kFewRows = 64;
+// About how many runs there are to be, given the tiles' units in all.  A compute unit holds one
+// workgroup of the larger tiles and two of the smaller ones: as many runs as fill the card once,
+// and of the smaller tiles twice as many where each still has 16 units, for the sequences'
+// different lengths (one token of 4 sequences of 2000 to 8000 keys, 8 heads of 128: 24 us with 512,
+// 30 with 1024; of 16 of 1000 to 16000: 84 and 77; of 64: 261 and 253; 512 tokens behind 32000: 319 us
+// with 256, 344 with 512).
 constexpr int kTargetSmall = 1024, kTargetLarge = 256;
 template <int BQ>
-constexpr int target() {
-    return BQ == kSmallRows ? kTargetSmall : kTargetLarge;
+__device__ __forceinline__ uint32_t target(uint64_t units) {
+    if (BQ != kSmallRows) return kTargetLarge;
+    return units < 16 * (kTargetSmall / 2) ? kTargetSmall / 2 : kTargetSmall;
 }
 
 // (rows x group is below 2^28 and lengths below 2^31: 32 bits hold rows, keys and units)
@@ -107,7 +114,9 @@ __device__ __forceinline__ uint32_t run_units(const AttArgs &a, int lane) {
     // (a wave's first lanes hold everything where sequences are few)
     const int n = a.b.seqs < 64 ? static_cast<int>(a.b.seqs) : 64;
     for (int d = 1; d < n; d <<= 1) total += __shfl_xor(total, d);
-    uint64_t per = (total * a.c.heads + target<BQ>() - 1) / target<BQ>();
+    total *= a.c.heads;
+    const uint32_t runs = target<BQ>(total);
+    uint64_t per = (total + runs - 1) / runs;
     per = per > 1 ? per : 1;
     per = per < (1u << 30) ? per : 1u << 30;  // (units are fewer)
     return of_lane(static_cast<uint32_t>(per), 0);
