@@ -465,8 +465,16 @@ __device__ __forceinline__ void add_wild(const s16x8 &x, const s16x8 (&p)[TERMS]
 // softmax; joined in LDS.  Keys go from memory straight into the first operand of S^T (a lane
 // reads a run of D / 4 dims of its key), values through the wave's own piece of LDS.  A tile's
 // codes are asked for while the one before is multiplied, its page numbers one earlier.
+//   Bound to two waves to a SIMD the compiler keeps the outputs out of the accumulation registers, whose
+// copies cost a tile 128 instructions (64 sequences, 4 heads of 128: fp32 over fp8 191 us, 145 with;
+// bf16 over fp4 100 and 96).  256 dims do not fit but for bf16 over fp4 (235 and 182; fp8 305 and 544).
 template <typename T, int D, int FMT>
-__global__ __launch_bounds__(256) void attend_few_kernel(AttArgs a) {
+constexpr int few_waves() {
+    return D < 256 || (FMT == TCQ_FP4 && terms<T>() == 1) ? 2 : 1;
+}
+template <typename T, int D, int FMT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(few_waves<T, D, FMT>()))) void
+attend_few_kernel(AttArgs a) {
     constexpr int TERMS = terms<T>();
     constexpr int BQ = kSmallRows;
     constexpr int kRow = mx::bytes<FMT>(D);    // bytes of a cache row

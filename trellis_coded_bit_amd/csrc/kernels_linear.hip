@@ -779,24 +779,6 @@ __global__ __launch_bounds__(256) void slope_kernel(SlopeArgs a, T *__restrict__
     }
 }
 
-// sum[c] = part[0][c] + part[1][c] + ...: each of four waves adds a run of slabs in order, then
-// the four sums in order; 64 columns per workgroup.
-__device__ __forceinline__ void slab_sum(const float *__restrict__ part, int64_t slabs, int64_t M,
-                                         float *__restrict__ sum, uint32_t block) {
-    __shared__ float red[4][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int64_t c = static_cast<int64_t>(block) * 64 + lane;
-    const int64_t i0 = w * slabs / 4, i1 = (w + 1) * slabs / 4;
-    float s = 0.0f;
-    if (c < M) {
-#pragma unroll 8
-        for (int64_t i = i0; i < i1; ++i) s += part[i * M + c];
-    }
-    red[w][lane] = s;
-    __syncthreads();
-    if (w == 0 && c < M) sum[c] = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
-}
-
 __global__ __launch_bounds__(256) void slab_sum_kernel(const float *__restrict__ part,
                                                        int64_t slabs, int64_t M,
                                                        float *__restrict__ sum) {
@@ -1183,17 +1165,15 @@ hipError_t backward(const CodedMatrix &w, const LinearGrad &c, char *ws, hipStre
     return hipSuccess;
 }
 
-// dx = dy W, dw = dy^T X and dbias = sum of dy's rows for dense W (M x ldn) and X (B x ldn), whose
-// columns past N are zeros.  dy is read where it lies if its rows are whole 16-byte pieces;
-// otherwise slope_kernel copies it on its way through the bias' sums.
+// dx = dy W and dw = dy^T X for dense W (M x ldn) and X (B x ldn), whose columns past N are zeros.
+// dy is read where it lies if its rows are whole 16-byte pieces; otherwise slope_kernel copies it
+// on its way through the bias' sums over slabs of rows.
 template <typename T>
-hipError_t dense_grad(const DenseGrad &c, char *ws, hipStream_t s) {
+hipError_t dense_slabs(const DenseGrad &c, char *ws, hipStream_t s) {
     const DenseGradLayout lay = dense_grad_layout(sizeof(T), c.B, c.M, c.N, c.dx, c.dw, c.dbias);
     const bool direct = sixteen_aligned(c.dy, c.lddy, c.M, sizeof(T));
     T *copy = reinterpret_cast<T *>(ws + lay.grad);
     T *out = direct || (!c.dx && !c.dw) ? nullptr : copy, *low = nullptr;
-    const T *S = direct ? static_cast<const T *>(c.dy) : copy;
-    const int64_t lds = direct ? c.lddy : lay.ldm, wide = direct ? c.M : lay.ldm;
     const int64_t slabs = slope_slabs(c.B, c.M);
     hipError_t e;
     if (c.B > 0 && c.M > 0 && (out || c.dbias)) {
@@ -1212,13 +1192,16 @@ hipError_t dense_grad(const DenseGrad &c, char *ws, hipStream_t s) {
                             dim3(256), args, 0, s);
         if (e != hipSuccess) return e;
     }
-    if (c.dbias && c.M > 0) {
-        hipLaunchKernelGGL(slab_sum_kernel, dim3(static_cast<unsigned>((c.M + 63) / 64)),
-                           dim3(256), 0, s, reinterpret_cast<const float *>(ws + lay.part),
-                           c.B > 0 ? slabs : 0, c.M, c.dbias);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
+    return hipSuccess;
+}
+
+template <typename T>
+hipError_t dense_grad(const DenseGrad &c, char *ws, hipStream_t s) {
+    const DenseGradLayout lay = dense_grad_layout(sizeof(T), c.B, c.M, c.N, c.dx, c.dw, c.dbias);
+    const bool direct = sixteen_aligned(c.dy, c.lddy, c.M, sizeof(T));
+    const T *S = direct ? static_cast<const T *>(c.dy) : reinterpret_cast<const T *>(ws + lay.grad);
+    const int64_t lds = direct ? c.lddy : lay.ldm, wide = direct ? c.M : lay.ldm;
+    hipError_t e;
     if (c.dx && c.B > 0 && c.N > 0) {
         const PlainEpilogue<T> epi{static_cast<T *>(c.dx), c.lddx, c.B, c.N,
                                    four_aligned(static_cast<T *>(c.dx), c.lddx),
@@ -1457,11 +1440,20 @@ DenseGradLayout dense_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, 
     if (dx || dw) off += align_up(static_cast<size_t>(B) * l.ldm * size, 256);
     l.part = off;
     if (dbias) off += align_up(static_cast<size_t>(slope_slabs(B, M)) * M * sizeof(float), 256);
+    l.slabs = B > 0 ? slope_slabs(B, M) : 0;
     l.sums = off;
     const size_t gx = dx ? gemm_shares(size, B, l.ldn, M, 1) : 0;
     const size_t gw = dw ? gemm_shares(size, l.ldm, l.ldn, B, 1) : 0;
     l.bytes = off + align_up(gx > gw ? gx : gw, 256);
     return l;
+}
+
+hipError_t launch_dense_slabs(const DenseGrad &c, char *ws, hipStream_t s) {
+    switch (c.dtype) {
+        case TCQ_F32: return dense_slabs<float>(c, ws, s);
+        case TCQ_F16: return dense_slabs<_Float16>(c, ws, s);
+        default: return dense_slabs<__bf16>(c, ws, s);
+    }
 }
 
 hipError_t launch_dense_grad(const DenseGrad &c, char *ws, hipStream_t s) {

@@ -7,7 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include "checkpoint_device.h"
-#include "mx_device.h"
+#include "mx_unpack_device.h"
 #include "tcq_internal.h"
 
 namespace tcq {
@@ -91,75 +91,6 @@ __global__ __launch_bounds__(256) void mx_pack_kernel(MxPackArgs a) {
     }
 }
 
-struct MxUnpackArgs {
-    const uint8_t *codes;
-    int64_t ldq;
-    const uint8_t *scale;
-    int64_t cols, ldo;
-    Pieces ix;          // pieces of 16 bytes of output
-    int64_t padded;     // columns cols .. padded - 1 become zeros
-    MxShift shift;      // (fp16; tops NULL: none)
-};
-
-// 16 bytes of output per thread (8 values of a 16-bit type, 4 of fp32), stored past the caches.
-template <typename T, int FMT, bool SMALL>
-__device__ __forceinline__ void mx_unpack(const MxUnpackArgs &a, T *__restrict__ out,
-                                          uint32_t block, uint32_t blocks) {
-    constexpr int P = 16 / static_cast<int>(sizeof(T));
-    typedef uint32_t Store __attribute__((ext_vector_type(4), aligned(1)));
-    const int64_t groups = (a.cols + mx::kGroup - 1) / mx::kGroup;
-    int shift = 0;
-    if constexpr (__is_same(T, _Float16)) {
-        if (a.shift.tops) {
-            int top = 0;
-#pragma unroll
-            for (int k = 0; k < kMxTops; ++k) top = top > a.shift.tops[k] ? top : a.shift.tops[k];
-            shift = 127 + 15 - (FMT == TCQ_FP4 ? 2 : 8) - top;
-            if (block == 0 && threadIdx.x == 0) *a.shift.down = -shift;
-        }
-    }
-    for (int64_t i = static_cast<int64_t>(block) * 256 + threadIdx.x; i < a.ix.total;
-         i += static_cast<int64_t>(blocks) * 256) {
-        int64_t r;
-        uint32_t c;
-        split<SMALL>(i, a.ix.cpr, r, c);
-        const int64_t col = static_cast<int64_t>(c) * P;
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-        if (col < a.cols) {
-            // (whole groups of codes are there)
-            const uint8_t *q = a.codes + r * a.ldq + static_cast<int64_t>(c) * mx::bytes<FMT>(P);
-            const float s = mx::scale_of(a.scale[r * groups + c / (mx::kGroup / P)]);
-            if constexpr (FMT == TCQ_FP4 && P == 8) {
-                mx::decode_word<FMT>(*reinterpret_cast<const uint32_t *>(q), s, v);
-            } else if constexpr (FMT == TCQ_FP4) {
-                mx::decode_word<FMT>(*reinterpret_cast<const uint16_t *>(q), s, v);
-            } else {
-#pragma unroll
-                for (int h = 0; h < P / 4; ++h)
-                    mx::decode_word<FMT>(reinterpret_cast<const uint32_t *>(q)[h], s, v + 4 * h);
-            }
-        }
-        T *o = out + r * a.ldo + col;
-        struct alignas(16) Piece { T v[P]; } st;
-#pragma unroll
-        for (int k = 0; k < P; ++k)
-            st.v[k] = static_cast<T>(
-                col + k < a.cols
-                    ? (__is_same(T, _Float16) ? __builtin_amdgcn_ldexpf(v[k], shift) : v[k])
-                    : 0.0f);
-        if (col + P <= a.padded) {
-            __builtin_nontemporal_store(__builtin_bit_cast(Store, st),
-                                        reinterpret_cast<Store *>(o));
-        } else {
-#pragma unroll
-            for (int k = 0; k < P; ++k)
-                if (col + k < a.padded) o[k] = st.v[k];
-        }
-    }
-}
-
 template <typename T, int FMT, bool SMALL>
 __global__ __launch_bounds__(256) void mx_unpack_kernel(MxUnpackArgs a, T *__restrict__ out) {
     mx_unpack<T, FMT, SMALL>(a, out, blockIdx.x, gridDim.x);
@@ -181,11 +112,8 @@ hipError_t pack(MxPackArgs a, hipStream_t s) {
 
 template <typename T, int FMT>
 hipError_t unpack(const MxMatrix &m, int64_t rows, int64_t cols, void *out, int64_t ldo,
-                  int64_t padded, const MxShift *shift, hipStream_t s) {
-    constexpr int64_t P = 16 / sizeof(T);
-    const int64_t cpr = (padded + P - 1) / P;
-    const MxUnpackArgs a{m.codes, m.ld,  m.scale, cols, ldo, {static_cast<uint32_t>(cpr), rows * cpr},
-                         padded,  shift ? *shift : MxShift{nullptr, nullptr}};
+                  int64_t padded, hipStream_t s) {
+    const MxUnpackArgs a = mx_unpack_args<T>(m, rows, cols, ldo, padded);
     const auto kern = a.ix.total < (int64_t{1} << 32) ? mx_unpack_kernel<T, FMT, true>
                                                       : mx_unpack_kernel<T, FMT, false>;
     hipLaunchKernelGGL(kern, dim3(grid_for(a.ix.total, 256)), dim3(256), 0, s, a,
@@ -213,11 +141,11 @@ hipError_t launch_mx_pack(const void *X, int dtype, int64_t rows, int64_t cols, 
 }
 
 hipError_t launch_mx_unpack(const MxMatrix &m, int64_t rows, int64_t cols, int dtype, void *out,
-                            int64_t ldo, int64_t padded, const MxShift *shift, hipStream_t s) {
+                            int64_t ldo, int64_t padded, hipStream_t s) {
     const bool fp4 = m.format == TCQ_FP4;
 #define TCQ_UNPACK(T)                                                                     \
-    (fp4 ? unpack<T, TCQ_FP4>(m, rows, cols, out, ldo, padded, shift, s)               \
-         : unpack<T, TCQ_FP8>(m, rows, cols, out, ldo, padded, shift, s))
+    (fp4 ? unpack<T, TCQ_FP4>(m, rows, cols, out, ldo, padded, s)               \
+         : unpack<T, TCQ_FP8>(m, rows, cols, out, ldo, padded, s))
     switch (dtype) {
         case TCQ_F32: return TCQ_UNPACK(float);
         case TCQ_F16: return TCQ_UNPACK(_Float16);

@@ -10,7 +10,7 @@
 
 #include "gemm_device.h"
 #include "linear_epilogue.h"
-#include "mx_device.h"
+#include "mx_unpack_device.h"
 #include "tcq.h"
 #include "tcq_internal.h"
 
@@ -866,11 +866,11 @@ hipError_t linear(const MxLinearCall &c, char *ws, hipStream_t s) {
     }
     if (fp4) return large_fp4<T>(c, x, lay, ws, s);
     if (!c.x) {
-        e = launch_mx_unpack(x, c.B, c.N, TCQ_BF16, xvals, lay.ldn, lay.ldn, nullptr, s);
+        e = launch_mx_unpack(x, c.B, c.N, TCQ_BF16, xvals, lay.ldn, lay.ldn, s);
         if (e != hipSuccess) return e;
     }
     uint16_t *wvals = reinterpret_cast<uint16_t *>(ws + lay.wvals);
-    e = launch_mx_unpack(c.w, c.M, c.N, TCQ_BF16, wvals, lay.ldn, lay.ldn, nullptr, s);
+    e = launch_mx_unpack(c.w, c.M, c.N, TCQ_BF16, wvals, lay.ldn, lay.ldn, s);
     if (e != hipSuccess) return e;
     const DenseProduct d{xvals,  wvals,      lay.ldn, lay.ldn, c.B, c.M, lay.ldn,
                          c.dtype, c.bias, c.residual, c.ldr,   c.y, c.ldy};
@@ -916,6 +916,60 @@ __global__ __launch_bounds__(1024) void scale_tops_kernel(TopArgs w, TopArgs x) 
         for (int v = 1; v < 16; ++v) top = top > red[v] ? top : red[v];
         a.tops[blockIdx.x] = top;
     }
+}
+
+// The bias' sums from their slabs, W's values and x's, which know nothing of one another, side by
+// side in one launch (509 x 2048 x 2048 bf16: three launches 11.6 us, one 5.4).
+struct ReadyArgs {
+    const float *part;
+    int64_t slabs, M;
+    float *sum;
+    uint32_t sums, w_blocks;    // workgroups of the first two; the others take x
+    MxUnpackArgs w, x;
+    void *w_out, *x_out;
+};
+template <typename T, int FMT, bool SMALL>
+__global__ __launch_bounds__(256) void grad_ready_kernel(ReadyArgs a) {
+    const uint32_t block = blockIdx.x;
+    if (block < a.sums)
+        slab_sum(a.part, a.slabs, a.M, a.sum, block);
+    else if (block - a.sums < a.w_blocks)
+        mx_unpack<T, TCQ_FP4, SMALL>(a.w, static_cast<T *>(a.w_out), block - a.sums, a.w_blocks);
+    else
+        mx_unpack<T, FMT, SMALL>(a.x, static_cast<T *>(a.x_out), block - a.sums - a.w_blocks,
+                                 gridDim.x - a.sums - a.w_blocks);
+}
+
+uint32_t unpack_blocks(int64_t pieces) {
+    const int64_t n = (pieces + 255) / 256;
+    return static_cast<uint32_t>(n < (1 << 20) ? n : 1 << 20);
+}
+
+template <typename T>
+hipError_t grad_ready(const MxGrad &c, ReadyArgs a, int64_t ldn, bool read_w, bool read_x,
+                      const int *tops, int *down, hipStream_t s) {
+    a.sums = c.dbias && c.M > 0 ? static_cast<uint32_t>((c.M + 63) / 64) : 0;
+    uint32_t x_blocks = 0;
+    if (read_w) {
+        a.w = mx_unpack_args<T>(c.w, c.M, c.N, ldn, ldn);
+        a.w_blocks = unpack_blocks(a.w.ix.total);
+        if (__is_same(T, _Float16)) a.w.shift = MxShift{tops, down};
+    }
+    if (read_x) {
+        a.x = mx_unpack_args<T>(c.x, c.B, c.N, ldn, ldn);
+        x_blocks = unpack_blocks(a.x.ix.total);
+        if (__is_same(T, _Float16)) a.x.shift = MxShift{tops + kMxTops, down + 1};
+    }
+    const uint32_t blocks = a.sums + a.w_blocks + x_blocks;
+    if (blocks == 0) return hipSuccess;
+    const bool small = a.w.ix.total < (int64_t{1} << 32) && a.x.ix.total < (int64_t{1} << 32);
+    const auto kern = c.x.format == TCQ_FP4
+                          ? (small ? grad_ready_kernel<T, TCQ_FP4, true>
+                                   : grad_ready_kernel<T, TCQ_FP4, false>)
+                          : (small ? grad_ready_kernel<T, TCQ_FP8, true>
+                                   : grad_ready_kernel<T, TCQ_FP8, false>);
+    hipLaunchKernelGGL(kern, dim3(blocks), dim3(256), 0, s, a);
+    return hipGetLastError();
 }
 
 struct MxGradLayout {
@@ -1002,18 +1056,6 @@ hipError_t launch_mx_grad(const MxGrad &c, char *ws, hipStream_t s) {
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    if (read_w) {
-        const MxShift shift{tops, down};
-        e = launch_mx_unpack(c.w, c.M, c.N, c.dtype, ws + lay.w, lay.ldn, lay.ldn,
-                             shifted ? &shift : nullptr, s);
-        if (e != hipSuccess) return e;
-    }
-    if (read_x) {
-        const MxShift shift{tops + kMxTops, down + 1};
-        e = launch_mx_unpack(c.x, c.B, c.N, c.dtype, ws + lay.x, lay.ldn, lay.ldn,
-                             shifted ? &shift : nullptr, s);
-        if (e != hipSuccess) return e;
-    }
     const DenseGrad d{c.dtype, c.dy,
                       c.B,     c.lddy,
                       c.M,     c.N,
@@ -1023,7 +1065,25 @@ hipError_t launch_mx_grad(const MxGrad &c, char *ws, hipStream_t s) {
                       dx ? c.dx : nullptr, c.lddx,
                       dw ? c.dw : nullptr, c.lddw,
                       c.dbias};
-    return launch_dense_grad(d, ws + lay.dense, s);
+    char *dense = ws + lay.dense;
+    e = launch_dense_slabs(d, dense, s);
+    if (e != hipSuccess) return e;
+    const DenseGradLayout dl = dense_grad_layout(c.dtype == TCQ_F32 ? 4 : 2, c.B, c.M, c.N, d.dx,
+                                                 d.dw, d.dbias);
+    ReadyArgs a{};
+    a.part = reinterpret_cast<const float *>(dense + dl.part);
+    a.slabs = dl.slabs;
+    a.M = c.M;
+    a.sum = c.dbias;
+    a.w_out = ws + lay.w;
+    a.x_out = ws + lay.x;
+    switch (c.dtype) {
+        case TCQ_F32: e = grad_ready<float>(c, a, lay.ldn, read_w, read_x, tops, down, s); break;
+        case TCQ_F16: e = grad_ready<_Float16>(c, a, lay.ldn, read_w, read_x, tops, down, s); break;
+        default: e = grad_ready<__bf16>(c, a, lay.ldn, read_w, read_x, tops, down, s); break;
+    }
+    if (e != hipSuccess) return e;
+    return launch_dense_grad(d, dense, s);
 }
 
 }  // namespace tcq

@@ -1,5 +1,5 @@
 // What becomes of a product's sums: the layer's outputs, plain outputs, or one split's share
-// (device code), and the kernel that joins shares.
+// (device code), the kernel that joins shares, and the sum of slabs.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -144,6 +144,24 @@ __global__ __launch_bounds__(256) void split_sum_kernel(const float *__restrict_
     for (int v = 1; v < splits; ++v) s += *reinterpret_cast<const f32x4 *>(p + v * I * ld);
     const typename Epi::Column col(epi, j);
     epi.put(col, i, s);
+}
+
+// sum[c] = part[0][c] + part[1][c] + ...: each of four waves adds a run of slabs in order, then
+// the four sums in order; 64 columns per workgroup.
+__device__ __forceinline__ void slab_sum(const float *__restrict__ part, int64_t slabs, int64_t M,
+                                         float *__restrict__ sum, uint32_t block) {
+    __shared__ float red[4][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t c = static_cast<int64_t>(block) * 64 + lane;
+    const int64_t i0 = w * slabs / 4, i1 = (w + 1) * slabs / 4;
+    float s = 0.0f;
+    if (c < M) {
+#pragma unroll 8
+        for (int64_t i = i0; i < i1; ++i) s += part[i * M + c];
+    }
+    red[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && c < M) sum[c] = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
 }
 
 template <typename T>

@@ -178,10 +178,11 @@ struct DenseProduct {
 size_t gemm_shares(size_t size, int64_t I, int64_t J, int64_t K, int terms);
 hipError_t launch_dense_product(const DenseProduct &c, char *ws, hipStream_t s);
 //   Gradients in `dtype` from dy (B x M) and dense w (M x ldn), x (B x ldn) in the workspace;
-//   fp16 products are multiplied by 2^*w_exponent (dx) and 2^*x_exponent (dw).
+//   fp16 products are multiplied by 2^*w_exponent (dx) and 2^*x_exponent (dw).  The first launch
+//   leaves dbias as the layout's slabs of partial sums (rows of M), the second takes the products.
 struct DenseGradLayout {
     size_t grad, part, sums, bytes;
-    int64_t ldn, ldm;
+    int64_t ldn, ldm, slabs;
 };
 struct DenseGrad {
     int dtype;
@@ -197,6 +198,7 @@ struct DenseGrad {
 };
 DenseGradLayout dense_grad_layout(size_t size, int64_t B, int64_t M, int64_t N, bool dx, bool dw,
                                   bool dbias);
+hipError_t launch_dense_slabs(const DenseGrad &c, char *ws, hipStream_t s);
 hipError_t launch_dense_grad(const DenseGrad &c, char *ws, hipStream_t s);
 
 // Microscaled matrices (codes, their leading dimension in bytes, scale bytes without gaps).
@@ -208,8 +210,7 @@ struct MxMatrix {
 };
 // Codes and scale bytes, and, where values is not NULL, the bf16 numbers they stand for (up to
 // whole groups); codes and scale may be NULL.  Unpack also writes zeros to columns cols ..
-// padded - 1, and with a shift multiplies fp16 values by the power of two that brings the largest
-// code of the largest scale byte below 2^16; its inverse's exponent goes to *down.
+// padded - 1.
 // order: codes and scale bytes in the order in which the few-rows product reads them (whole tiles of
 // 16 rows, of which those past `rows` are left as they were, and whole pairs of 128 columns).
 struct MxOrder {
@@ -225,7 +226,7 @@ struct MxShift {
     int *down;
 };
 hipError_t launch_mx_unpack(const MxMatrix &m, int64_t rows, int64_t cols, int dtype, void *out,
-                            int64_t ldo, int64_t padded, const MxShift *shift, hipStream_t s);
+                            int64_t ldo, int64_t padded, hipStream_t s);
 // The microscaled linear layer and its gradients.
 struct MxLinearCall {
     MxMatrix w;

@@ -120,7 +120,7 @@ extern "C" int tcq_mx_unpack(const uint8_t *codes, int64_t ldq, const uint8_t *s
     if (rc == TCQ_OK) rc = check_apart(fn, ro, scale_region("scale", scale, rows, cols));
     if (rc != TCQ_OK) return rc;
     const hipError_t e = launch_mx_unpack(MxMatrix{codes, ldq, scale, format}, rows, cols, dtype,
-                                          out, ldo, cols, nullptr, stream);
+                                          out, ldo, cols, stream);
     if (e != hipSuccess) return hip_fail(fn, "unpacking launch", e);
     return TCQ_OK;
 }
