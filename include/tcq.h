@@ -600,7 +600,7 @@ int tcq_cache_read(const tcq_cache *cache, const tcq_cache_batch *batch, int dty
  *   scale      : between 2^-60 and 2^60 (1 / sqrt(dim), as a rule)
  *   workspace  : >= what tcq_cache_attention_workspace_bytes reports
  * Products of scores are exact and sums fp32; weights are held to 2^-8 (bf16), 2^-15 (fp16) or
- * fp32 when they meet the values, and their sum to fp32; o is rounded once.  (As bf16 numbers,
+ * fp32 where they meet the values and are summed; o is rounded once.  (As bf16 numbers,
  * values below 2^-133 are lost: scale bytes below 3 in TCQ_FP8.)  How keys are shared
  * out among workgroups depends on the batch's lengths, and with it the last bits of o; the same
  * call gives the same bits.

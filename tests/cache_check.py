@@ -5,7 +5,10 @@ A score is off by gamma(D) of its terms' magnitudes, and by 16 fp32 roundings of
 its way through the factor, the running maximum and the exponential's argument; a weight by that
 in its exponent and 2^-21 of the exponential itself.  Weights meet the values rounded to their
 terms: one bf16 number has 8 bits, so half a step is 2^-8 of it; the first of two is cut off below
-2^-7 and the second rounds that by 2^-8 of it, 2^-15; three hold every bit of an fp32 number.  Sums over keys take one whole fp32 unit per
+2^-7 and the second rounds that by 2^-8 of it, 2^-15; three hold every bit of an fp32 number.  The
+weights' sum is that of the rounded ones: with errors of at most r in each, o = N / S is off by at
+most r sum p|v| / sum p from N and r |o| from S, each no more than r of the same size, and by second
+orders below r / 16 of it.  Sums over keys take one whole fp32 unit per
 key and eight per tile of 32 keys (rescaling).  Numerator and denominator count alike.
 """
 import math
@@ -84,7 +87,7 @@ def attention(q, k, v, first, scale, dtype, there=None):
             o = torch.where(sees.double() @ bad > 0, torch.full_like(o, math.nan), o)
         size = p @ vv.abs() / total
         ds = (mc.gamma(D) + 16 * U) * top
-        e = 2 * (torch.expm1(ds) + 2.0 ** -21) + ROUND[dtype] + \
+        e = 2 * (torch.expm1(ds) + 2.0 ** -21) + (2 + 1 / 16) * ROUND[dtype] + \
             4 * U * (length + 8 * (length // 32 + 4))
         out[:, h] = o
         bound[:, h] = e * size + half(dtype) * (o.abs() + e * size) + tiny(dtype)

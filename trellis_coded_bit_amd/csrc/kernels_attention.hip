@@ -6,8 +6,9 @@
 //
 // Every code times its scale is a bf16 number, so keys and values are multiplied as bf16 with
 // exact products and fp32 sums.  q and p are held in terms of bf16 whose sum they are: one for
-// bf16 queries (q is exact; p is rounded to 8 bits, half a step of the output's own type, while
-// its sum is taken unrounded), two for fp16 (q exact, p to 2^-15) and three for fp32 (both exact).
+// bf16 queries (q is exact; p is rounded to 8 bits, half a step of the output's own type, and its
+// sum is that of the rounded ones), two for fp16 (q exact, p to 2^-15) and three for fp32 (both
+// exact).
 //
 // Scores are computed transposed, S^T = K Q^T: a lane holds four keys of one query row, the same
 // row in every instruction, so a row's maximum and sum are the lane's own but for three other
@@ -249,7 +250,7 @@ constexpr int terms() {
     return sizeof(T) == 4 ? 3 : (__is_same(T, _Float16) ? 2 : 1);
 }
 
-// The largest (sum) over the four lanes that hold a query row's keys: lanes l, l ^ 16, l ^ 32,
+// f over the four lanes that hold a query row's keys: lanes l, l ^ 16, l ^ 32,
 // l ^ 48.  A swap of one register with itself leaves each half's values in all lanes.
 template <typename F>
 __device__ __forceinline__ float over_row(float v, const F &f) {
@@ -261,22 +262,39 @@ __device__ __forceinline__ float over_row(float v, const F &f) {
     return f(__uint_as_float(rows[0]), __uint_as_float(rows[1]));
 }
 __device__ __forceinline__ float row_max(float v) {
-    return over_row(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
+    return over_row(v, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
 }
-__device__ __forceinline__ float row_sum(float v) {
-    return over_row(v, [](float a, float b) { return a + b; });
+// The largest of N (NaN if one is: the row's outputs are NaN then, whatever the others are taken
+// relative to), without the canonicalising moves that fmaxf of a product's sums takes.
+template <int N>
+__device__ __forceinline__ float largest(const f32x4 (&s)[N / 4]) {
+    float top = __builtin_elementwise_maximum(s[0][0], s[0][1]);
+#pragma unroll
+    for (int i = 2; i < N; i += 2)
+        top = __builtin_elementwise_maximum(
+            __builtin_elementwise_maximum(s[i / 4][i % 4], s[i / 4][i % 4 + 1]), top);
+    return top;
 }
 
 // The running softmax of one query row per lane.  Weights are taken relative to a score that the
 // largest so far exceeds by at most kSlack (powers of two): sums and outputs are rescaled only
 // when it grows beyond, not at every tile with a new largest score.
+//   The sum is a product with ones, of the weights as they meet the values: their rounding then
+// cancels in part, and the sum of a row is in every lane that holds it.
 struct Softmax {
     static constexpr float kSlack = 8.0f;
     float top;    // that score times factor, -inf before the first key
-    float sum;    // of this lane's keys
+    f32x4 sum;    // four times the same
     __device__ __forceinline__ void init() {
         top = -__builtin_inff();
-        sum = 0.0f;
+        sum = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    template <int TERMS>
+    __device__ __forceinline__ void add(const s16x8 (&p)[TERMS]) {
+        constexpr short kOne = 0x3F80;
+        const s16x8 ones = {kOne, kOne, kOne, kOne, kOne, kOne, kOne, kOne};
+#pragma unroll
+        for (int n = TERMS - 1; n >= 0; --n) sum = gemm::Traits<__bf16>::mma(ones, p[n], sum);
     }
     static __device__ __forceinline__ float safe(float t) {
         return t == -__builtin_inff() ? 0.0f : t;
@@ -285,7 +303,7 @@ struct Softmax {
     // alpha (in some lane).
     __device__ __forceinline__ bool grow(float score, float &alpha) {
         if (!__any(score > top + kSlack)) return false;
-        const float to = __builtin_fmaxf(score, top);
+        const float to = score > top ? score : top;
         alpha = __builtin_amdgcn_exp2f(top - safe(to));
         top = to;
         sum *= alpha;
@@ -467,7 +485,7 @@ __device__ __forceinline__ void add_wild(const s16x8 &x, const s16x8 (&p)[TERMS]
 // codes are asked for while the one before is multiplied, its page numbers one earlier.
 //   Bound to two waves to a SIMD the compiler keeps the outputs out of the accumulation registers, whose
 // copies cost a tile 128 instructions (64 sequences, 4 heads of 128: fp32 over fp8 191 us, 145 with;
-// bf16 over fp4 100 and 96).  256 dims do not fit but for bf16 over fp4 (235 and 182; fp8 305 and 544).
+// bf16 over fp4 100 and 96).  256 dims do not fit but for bf16 over fp4 (235 and 196; fp8 305 and 544).
 template <typename T, int D, int FMT>
 constexpr int few_waves() {
     return D < 256 || (FMT == TCQ_FP4 && terms<T>() == 1) ? 2 : 1;
@@ -636,22 +654,16 @@ attend_few_kernel(AttArgs a) {
             for (int i = 0; i < 8; ++i)
                 if (!(sees >> i & 1)) s[i / 4][i % 4] = -__builtin_inff();
         }
-        float top = -__builtin_inff();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = __builtin_fmaxf(top, s[i / 4][i % 4]);
         float alpha;
-        if (sm.grow(row_max(top) * a.factor, alpha)) {
+        if (sm.grow(row_max(largest<8>(s)) * a.factor, alpha)) {
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) acc[t] *= alpha;
         }
         const float ref = Softmax::safe(sm.top);
-        float p[8], add = 0.0f;
+        float p[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 8; ++i)
             p[i] = weight<TERMS>(s[i / 4][i % 4], a.factor, a.factor_low, ref);
-            add += p[i];
-        }
-        sm.sum += add;
         s16x8 pf[TERMS];
         {
             u32x4 w[TERMS];
@@ -665,6 +677,7 @@ attend_few_kernel(AttArgs a) {
 #pragma unroll
             for (int n = 0; n < TERMS; ++n) pf[n] = __builtin_bit_cast(s16x8, w[n]);
         }
+        sm.add(pf);
         __builtin_amdgcn_wave_barrier();
         if (__builtin_expect(__any(wild) && __any(sees != 0xFFu), 0)) {
 #pragma unroll
@@ -678,10 +691,9 @@ attend_few_kernel(AttArgs a) {
         __builtin_amdgcn_wave_barrier();
     }
     // join the waves
-    const float sum = row_sum(sm.sum);
     if (g == 0) {
         tops[wave][l16] = sm.top;
-        sums[wave][l16] = sum;
+        sums[wave][l16] = sm.sum[0];
     }
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
@@ -757,6 +769,10 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
             page[j] = tile.table[(pos < tile.end ? pos : tile.end - 1) >> hc.log2];
         }
     };
+    // A wave's pieces of one turn are 64 / kLanes neighbouring keys: of one page, unless pages are
+    // smaller.
+    constexpr int kTogether = 64 / kLanes;
+    const bool whole = (1u << hc.log2) >= kTogether;
     struct Codes {
         u32x4 k[kLoads], v[kLoads];
         int ke[kLoads], ve[kLoads];
@@ -768,19 +784,33 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
             const uint32_t pos = base + (j * NT + tid) / kLanes;
-            uint32_t p = static_cast<uint32_t>(page[j]);
-            if (p < hc.pages && pos < tile.end && (kPieces % NT == 0 || tid < kPieces))
-                now.there |= 1u << j;
-            else
-                p = 0;
+            const bool mine = pos < tile.end && (kPieces % NT == 0 || tid < kPieces);
             const uint32_t i = pos & hc.mask;
-            const uint64_t at = static_cast<uint64_t>(p) * hc.code_page + i * kRow + part * 16;
-            const uint64_t e = static_cast<uint64_t>(p) * hc.scale_page + i * kGroups +
-                               part / (kLanes / kGroups);
-            now.k[j] = *reinterpret_cast<const u32x4 *>(hc.k + at);
-            now.v[j] = *reinterpret_cast<const u32x4 *>(hc.v + at);
-            now.ke[j] = hc.ke[e];
-            now.ve[j] = hc.ve[e];
+            const uint32_t at = i * kRow + part * 16;
+            const uint32_t e = i * kGroups + part / (kLanes / kGroups);
+            if (whole) {
+                const uint32_t p = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(page[j]));
+                const bool in = p < hc.pages;
+                const uint64_t code = in ? static_cast<uint64_t>(p) * hc.code_page : 0;
+                const uint64_t scale = in ? static_cast<uint64_t>(p) * hc.scale_page : 0;
+                if (in && mine) now.there |= 1u << j;
+                now.k[j] = *reinterpret_cast<const u32x4 *>(hc.k + code + at);
+                now.v[j] = *reinterpret_cast<const u32x4 *>(hc.v + code + at);
+                now.ke[j] = (hc.ke + scale)[e];
+                now.ve[j] = (hc.ve + scale)[e];
+            } else {
+                uint32_t p = static_cast<uint32_t>(page[j]);
+                if (p < hc.pages && mine)
+                    now.there |= 1u << j;
+                else
+                    p = 0;
+                const uint64_t code = static_cast<uint64_t>(p) * hc.code_page;
+                const uint64_t scale = static_cast<uint64_t>(p) * hc.scale_page;
+                now.k[j] = *reinterpret_cast<const u32x4 *>(hc.k + code + at);
+                now.v[j] = *reinterpret_cast<const u32x4 *>(hc.v + code + at);
+                now.ke[j] = hc.ke[scale + e];
+                now.ve[j] = hc.ve[scale + e];
+            }
         }
     };
     const int row = tid / kLanes;   // of the first piece; the others are 8 n rows further
@@ -901,22 +931,16 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
                 for (int i = 0; i < 4 * kSub; ++i)
                     if (!(sees[n] >> i & 1)) s[n][i / 4][i % 4] = -__builtin_inff();
             }
-            float top = -__builtin_inff();
-#pragma unroll
-            for (int i = 0; i < 4 * kSub; ++i) top = __builtin_fmaxf(top, s[n][i / 4][i % 4]);
             float alpha;
-            if (sm[n].grow(row_max(top) * a.factor, alpha)) {
+            if (sm[n].grow(row_max(largest<4 * kSub>(s[n])) * a.factor, alpha)) {
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) acc[n][t] *= alpha;
             }
             const float ref = Softmax::safe(sm[n].top);
-            float p[4 * kSub], add = 0.0f;
+            float p[4 * kSub];
 #pragma unroll
-            for (int i = 0; i < 4 * kSub; ++i) {
+            for (int i = 0; i < 4 * kSub; ++i)
                 p[i] = weight<TERMS>(s[n][i / 4][i % 4], a.factor, a.factor_low, ref);
-                add += p[i];
-            }
-            sm[n].sum += add;
 #pragma unroll
             for (int k2 = 0; k2 < kPairs; ++k2) {
                 u32x4 w[TERMS];
@@ -931,6 +955,10 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
                 for (int m = 0; m < TERMS; ++m) pf[n][k2][m] = __builtin_bit_cast(s16x8, w[m]);
             }
         }
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int k2 = 0; k2 < kPairs; ++k2) sm[n].add(pf[n][k2]);
         if (__builtin_expect(wild && partial, 0)) {
 #pragma unroll
             for (int t = 0; t < kTiles; ++t)
@@ -961,13 +989,11 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
         v_next = v;
     }
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        const float sum = row_sum(sm[n].sum);
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
             put<T, BQ, D>(a, tile, wave * (NQ * 16) + 16 * n + l16, 16 * t + 4 * g, acc[n][t],
-                          sm[n].top, sum);
-    }
+                          sm[n].top, sm[n].sum[0]);
 }
 
 // ---------------------------------------------------------------- join of shares
