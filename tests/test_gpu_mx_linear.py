@@ -53,7 +53,8 @@ def _inside(got, want, bound, what):
 # and split, 256 x 256 ones
 SIZES = [(513, 17, 96), (600, 70, 2100), (1000, 1100, 700), (1100, 2050, 520), (1, 1, 1), (1, 16, 32), (2, 17, 33), (5, 100, 130), (16, 48, 1000), (17, 64, 256),
          (33, 40, 515), (70, 130, 129), (128, 200, 544), (129, 130, 260), (300, 513, 1100),
-         (1030, 2050, 200), (200, 144, 4096), (2049, 4000, 96), (3, 2000, 9000)]
+         (1030, 2050, 200), (200, 144, 4096), (2049, 4000, 96), (3, 2000, 9000),
+         (130, 7300, 6190), (1150, 1700, 6300)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)

@@ -655,8 +655,10 @@ bool mx_small(int format, int64_t B, int64_t M) {
     return B <= 128 || (B + 127) / 128 * ((M + 15) / 16) <= 896;
 }
 
-constexpr int kMxDenseBytes = 96 << 10;    // LDS for x quantised in the kernel
-constexpr int64_t kMxDenseValues = 32768;  // and its values at most
+// Values of x that mx_small_kernel quantises by itself, in every workgroup, rather than a launch
+// before it (us per call in a graph, it / the two: fp8 1 x 4096 x 4096 5.6 / 7.1, 1 x 14336 x 4096 11.7 /
+// 12.9, 4 x 4096 x 4096 6.9 / 6.9, 8 x 4096 x 4096 8.7 / 7.0; fp4 16 x 2048 x 2048 7.4 / 6.0).
+constexpr int64_t kMxDenseValues = 16384;
 
 size_t pad(int64_t n, int64_t to) { return static_cast<size_t>((n + to - 1) / to * to); }
 
@@ -689,19 +691,21 @@ int64_t dense_bytes(int format, int64_t B, int64_t pairs) {
     return align_up(B * (dense_row(format, pairs) + (format == TCQ_FP4 ? pairs * 8 : 0)), 16);
 }
 bool small_dense(const MxLinearCall &c) {
-    return c.x && !c.keep && c.B <= 16 && c.B * c.N <= kMxDenseValues &&
-           dense_bytes(c.xq.format, c.B, pairs_of(groups_of(c.N))) <= kMxDenseBytes;
+    return c.x && !c.keep && c.B <= 16 && c.B * c.N <= kMxDenseValues;
 }
 
 template <typename T, int FMT, int BT, bool DENSE>
 hipError_t launch_small_as(MxSmallArgs a, const LayerEpilogue<T> &epi, hipStream_t s) {
+    // LDS: sums, and x quantised in the kernel, at most 2 kMxDenseValues + 16 x 526 bytes
     constexpr int kSums = 2 * kMxWaves * BT * 1024;
+    static_assert(!DENSE || kSums + 2 * kMxDenseValues + 16 * 526 <= 64 << 10, "");
     a.red = DENSE ? static_cast<int>(dense_bytes(FMT, a.B, a.pairs)) : 0;
-    // (the limit is one of the kernel, not of the call: threads with x of two sizes share it)
-    const void *kern = reinterpret_cast<const void *>(mx_small_kernel<T, FMT, BT, DENSE>);
-    const hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                             (DENSE ? kMxDenseBytes : 0) + kSums);
-    if (e != hipSuccess) return e;
+    if (kSums > 64 << 10) {
+        const void *kern = reinterpret_cast<const void *>(mx_small_kernel<T, FMT, BT, DENSE>);
+        const hipError_t e =
+            hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, kSums);
+        if (e != hipSuccess) return e;
+    }
     // as many rounds of tiles for every workgroup
     const int64_t most = (BT == 1 ? 2 : 1) * 256, rounds = (a.tiles + most - 1) / most;
     const int64_t grid = (a.tiles + rounds - 1) / rounds;
@@ -724,37 +728,34 @@ hipError_t launch_small(MxSmallArgs a, const LayerEpilogue<T> &epi, hipStream_t 
     return launch_small_as<T, FMT, 8, false>(a, epi, s);
 }
 
-// Tile and splits of the product of B rows of 4-bit codes with M over `steps` steps: 256 x 256
-// tiles where they fill the 256 compute units, else 128 x 128 with k split.
+// Tile and splits of the product of B rows of 4-bit codes with M over `steps` steps of 256 columns.
+// 256 x 256 tiles where they are at least half as many as compute units (us per call in a graph,
+// they / 128 x 128: 2048 x 4096 x 4096 47.0 / 48.1, 1024 x 4096 x 14336 47.9 / 79.2, 4096^3 55.6 / 84.0;
+// with 64 tiles, 1024 x 4096 x 4096, 43.0 / 29.0).  Else 128 x 128, whose columns are split in two
+// where at most half the compute units have a tile, if there are steps enough (512 x 14336 x 4096 38.9
+// split / 50.1 whole, 512 x 4096 x 4096, 16 steps, 27.6 / 26.1).  Tiles are never fewer than 113:
+// smaller products are mx_small_kernel's.
 struct MxPlan {
     bool big;
     int splits, steps, steps_per_split;
     int64_t part_ld;
 };
-constexpr int64_t kMxCus = 256, kMxMostSplits = 16;
+constexpr int64_t kMxHalf = 128;    // half the compute units
+constexpr int64_t kMxSplitSteps = 24;
 MxPlan mx_plan(int64_t B, int64_t M, int64_t steps) {
     MxPlan p{};
     p.steps = static_cast<int>(steps);
     p.part_ld = (M + 3) / 4 * 4;
-    p.splits = 1;
-    p.steps_per_split = p.steps;
-    const int64_t n256 = ((B + 255) / 256) * ((M + 255) / 256);
-    p.big = n256 >= kMxCus / 2;
-    if (p.big) return p;
-    const int64_t n = ((B + 127) / 128) * ((M + 127) / 128);
-    int64_t s = kMxCus / n;
-    if (s > steps / 4) s = steps / 4;
-    if (s > kMxMostSplits) s = kMxMostSplits;
-    if (s < 1) s = 1;
-    p.steps_per_split = static_cast<int>((steps + s - 1) / s);
-    p.splits = p.steps_per_split > 0 ? (p.steps + p.steps_per_split - 1) / p.steps_per_split : 1;
+    p.big = ((B + 255) / 256) * ((M + 255) / 256) >= kMxHalf;
+    const int64_t tiles = ((B + 127) / 128) * ((M + 127) / 128);
+    p.splits = !p.big && tiles <= kMxHalf && steps >= kMxSplitSteps ? 2 : 1;
+    p.steps_per_split = (p.steps + p.splits - 1) / p.splits;
     return p;
 }
 // Room for the shares, never less for a larger B.
 size_t mx_shares(int64_t B, int64_t M, int64_t steps) {
-    int64_t s = steps / 4 < kMxMostSplits ? steps / 4 : kMxMostSplits;
-    if (s < 2) return 0;
-    const int64_t values = s * B * ((M + 3) / 4 * 4), most = kMxCus * 128 * 128;
+    if (steps < kMxSplitSteps) return 0;
+    const int64_t values = 2 * B * ((M + 3) / 4 * 4), most = 2 * kMxHalf * 128 * 128;
     return static_cast<size_t>(values < most ? values : most) * sizeof(float);
 }
 
