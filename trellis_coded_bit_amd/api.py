@@ -524,28 +524,35 @@ class Cache:
 
     def c(self, device: torch.device) -> _lib.TcqCache:
         """The C form; checks the tensors."""
-        assert self.format in _FORMATS, f"cache: format is none of {tuple(_FORMATS)}"
-        assert self.k_scale.dim() == 4, "cache: scale bytes [pages, heads, page, dim / 32]"
-        pages, heads, page, groups = self.k_scale.shape
+        fmt = _FORMATS.get(self.format)
+        assert fmt is not None, f"cache: format is none of {tuple(_FORMATS)}"
+        kc, ks, vc, vs = self.k_codes, self.k_scale, self.v_codes, self.v_scale
+        scales, codes, u8 = ks.shape, kc.shape, torch.uint8
+        assert len(scales) == 4, "cache: scale bytes [pages, heads, page, dim / 32]"
+        pages, heads, page, groups = scales
         width = groups * _group_bytes(self.format)
-        for t, w in ((self.k_codes, width), (self.k_scale, groups), (self.v_codes, width),
-                     (self.v_scale, groups)):
-            assert t.device == device and t.dtype == torch.uint8 and t.is_contiguous() and \
-                t.shape == (pages, heads, page, w), \
-                f"cache: contiguous uint8 [{pages}, {heads}, {page}, {w}] on {device}"
-        return _lib.TcqCache(self.k_codes.data_ptr(), self.k_scale.data_ptr(),
-                             self.v_codes.data_ptr(), self.v_scale.data_ptr(), pages, heads, page,
-                             groups * MX_GROUP, _FORMATS[self.format])
+        assert codes == (pages, heads, page, width) and vs.shape == scales and \
+            vc.shape == codes and \
+            kc.device == device and ks.device == device and vc.device == device and \
+            vs.device == device and \
+            kc.dtype is u8 and ks.dtype is u8 and vc.dtype is u8 and vs.dtype is u8 and \
+            kc.is_contiguous() and ks.is_contiguous() and vc.is_contiguous() and \
+            vs.is_contiguous(), \
+            f"cache: contiguous uint8 [{pages}, {heads}, {page}, {width} and {groups}] on {device}"
+        return _lib.TcqCache(kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages,
+                             heads, page, groups * MX_GROUP, fmt)
 
 
 def _batch(table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor,
            device: torch.device) -> _lib.TcqCacheBatch:
-    assert table.dim() == 2, "table: [sequences, pages]"
-    seqs, width = table.shape
-    ldt = _rows(table, "table", seqs, width, torch.int32, device)
-    for t, name, n in ((lens, "lens", seqs), (starts, "starts", seqs + 1)):
-        assert t.device == device and t.dtype == torch.int32 and t.is_contiguous() and \
-            t.shape == (n,), f"{name}: {n} contiguous int32 values on {device}"
+    shape, i32 = table.shape, torch.int32
+    assert len(shape) == 2, "table: [sequences, pages]"
+    seqs, width = shape
+    ldt = _rows(table, "table", seqs, width, i32, device)
+    assert lens.device == device and lens.dtype is i32 and lens.shape == (seqs,) and \
+        lens.is_contiguous(), f"lens: {seqs} contiguous int32 values on {device}"
+    assert starts.device == device and starts.dtype is i32 and starts.shape == (seqs + 1,) and \
+        starts.is_contiguous(), f"starts: {seqs + 1} contiguous int32 values on {device}"
     return _lib.TcqCacheBatch(table.data_ptr(), ldt, width, lens.data_ptr(), starts.data_ptr(),
                               seqs)
 
@@ -556,10 +563,13 @@ def _vectors(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, dtype:
     assert t.device == device and t.dtype == dtype, f"{name}: {dtype} on {device}"
     assert t.shape == (rows, heads, dim), \
         f"{name}: shape {tuple(t.shape)}, not {(rows, heads, dim)}"
-    assert t.stride(2) == 1, f"{name}: vectors must be contiguous"
+    row, head, one = t.stride()
+    assert one == 1, f"{name}: vectors must be contiguous"
     # a dimension of at most one element may carry any stride
-    head = t.stride(1) if heads > 1 else dim
-    row = t.stride(0) if rows > 1 else (heads - 1) * head + dim
+    if heads <= 1:
+        head = dim
+    if rows <= 1:
+        row = (heads - 1) * head + dim
     assert head >= dim and row >= (heads - 1) * head + dim, f"{name}: vectors overlap"
     return row, head
 
@@ -592,10 +602,14 @@ def cache_read(cache: Cache, table: torch.Tensor, lens: torch.Tensor, starts: to
     assert cache.k_codes.is_cuda and dtype in _DTYPES and rows >= 0
     c, b = cache.c(dev), _batch(table, lens, starts, dev)
     with _on(dev):
-        k, v = out if out is not None else (
-            torch.empty((rows, c.heads, c.dim), dtype=dtype, device=dev) for _ in range(2))
-        ks = _vectors(k, "k", rows, c.heads, c.dim, dtype, dev)
-        vs = _vectors(v, "v", rows, c.heads, c.dim, dtype, dev)
+        heads, dim = c.heads, c.dim
+        if out is None:
+            k = torch.empty((rows, heads, dim), dtype=dtype, device=dev)
+            v = torch.empty_like(k)
+        else:
+            k, v = out
+        ks = _vectors(k, "k", rows, heads, dim, dtype, dev)
+        vs = _vectors(v, "v", rows, heads, dim, dtype, dev)
         _lib.tcq_cache_read(c, b, _DTYPES[dtype], k.data_ptr(), *ks, v.data_ptr(), *vs, rows,
                             _stream_of(dev))
     return k, v
@@ -616,8 +630,8 @@ def cache_attention(q: torch.Tensor, cache: Cache, table: torch.Tensor, lens: to
     rows, heads, dim = q.shape
     qs = _vectors(q, "q", rows, heads, c.dim, dt, dev)
     with _on(dev):
-        o = torch.empty((rows, heads, dim), dtype=dt, device=dev) if out is None else out
-        os_ = _vectors(o, "out", rows, heads, c.dim, dt, dev)
+        o = q.new_empty(q.shape) if out is None else out
+        os_ = _vectors(o, "out", rows, heads, dim, dt, dev)
         if workspace is None:
             n = _lib.tcq_cache_attention_workspace_bytes(c.dim, c.heads, heads, b.seqs, rows)
             workspace = Workspace(n, dev) if n else None
