@@ -485,7 +485,8 @@ __device__ __forceinline__ void add_wild(const s16x8 &x, const s16x8 (&p)[TERMS]
 // codes are asked for while the one before is multiplied, its page numbers one earlier.
 //   Bound to two waves to a SIMD the compiler keeps the outputs out of the accumulation registers, whose
 // copies cost a tile 128 instructions (64 sequences, 4 heads of 128: fp32 over fp8 191 us, 145 with;
-// bf16 over fp4 100 and 96).  256 dims do not fit but for bf16 over fp4 (235 and 196; fp8 305 and 544).
+// bf16 over fp4 99 and 96).  256 dims do not fit but for bf16 over fp4 (235 and 196; fp8 305 and 544).
+//   Bound by memory: 64 sequences of 1000 to 16000 keys, 8 heads of 128, fp8, 251 us at 4.6 TB/s.
 template <typename T, int D, int FMT>
 constexpr int few_waves() {
     return D < 256 || (FMT == TCQ_FP4 && terms<T>() == 1) ? 2 : 1;
@@ -727,6 +728,10 @@ attend_few_kernel(AttArgs a) {
 //   With eight waves the second four meet the others between their scores and their softmax, the
 // first four after the whole tile, so that one wave of a SIMD computes its softmax while the other
 // multiplies; values are kept for a tile longer for it.
+//   Bound by what two waves of a SIMD issue between two meetings: four chunks of 511 to 2048 tokens
+// behind 4000 to 16384, 32 query heads over 8 of 128, bf16, 1220 us (897 TF) with the matrix cores
+// busy for 38 % of the clocks, VALU for 42 and LDS for 37.  (Without the third of the latter that
+// are bank conflicts of the keys' reads it takes 1257 us.)
 template <typename T, int D, int FMT, int NW, int NQ>
 __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
     constexpr int TERMS = terms<T>();
@@ -1000,7 +1005,8 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
 
 // Rows of tiles with several runs.  D / 4 lanes take a row, four dims each; the four waves every
 // fourth run, eight at a time (their loads are on their way together), and their sums, each
-// relative to the wave's own largest score, are joined in the waves' order.
+// relative to the wave's own largest score, are joined in the waves' order.  3.8 us for one token
+// of 8 heads of 64, 9.2 for 64 tokens of 32 heads of 128 with 1024 runs.
 constexpr int kJoinRows = 16;    // rows to a workgroup
 template <typename T, int D, int BQ>
 __device__ __forceinline__ void join(const AttArgs &a, uint32_t block) {
@@ -1144,14 +1150,13 @@ hipError_t attend_as(const AttArgs &base, char *ws, hipStream_t s) {
 
 // Two tiles of query rows to a wave read a key from LDS half as often as one, but their outputs,
 // queries and scores need room, and sequences of up to 256 rows leave half of them idle.  us with
-// two / with one (16 or 32 query heads; chunks behind a history; eight waves):
-//   64 dims: bf16 904 / 840, fp16 1208 / 1388, fp32 1862 / 1659;
-//   128 dims: bf16 1349 / 1638, fp16 303 (spills) / 194, fp32 342 (four waves) / 234;
-//   256 dims (all spill, or four waves): bf16 494 / 282, fp16 890 / 351, fp32 1310 / 653;
-//   128 dims, bf16, 16 sequences of 256 rows 247 / 230, of 400 rows 344 / 362.
+// two / with one (four chunks of 511 to 2048 tokens behind 4000 to 16384, 32 query heads over 8):
+//   64 dims: bf16 911 / 847, fp16 1206 / 1186, fp32 2039 / 1704;
+//   128 dims: bf16 1237 / 1618, fp16 (spills) 2623 / 2060; 256 dims spill;
+//   16 sequences of 256 rows, 128 dims, bf16, 231 both, of 400 rows 316 / 361.
 template <typename T, int D, int FMT>
 hipError_t attend(const AttArgs &a, char *ws, hipStream_t s) {
-    constexpr bool kTwo = (D == 128 && terms<T>() == 1) || (D == 64 && terms<T>() == 2);
+    constexpr bool kTwo = D == 128 && terms<T>() == 1;
     if constexpr (kTwo) {
         if (a.rows * a.group > 256 * a.b.seqs) return attend_as<T, D, FMT, 8, 2>(a, ws, s);
     }

@@ -3,7 +3,9 @@
 // groups of 32 along the head's dimension, so a token touches no other token's bytes.
 //   Both are bound by memory, or by their launch for a few tokens: a wave takes one row of the call
 // (a token), looks its sequence and page up once, and moves all its heads, four pieces of eight
-// values per lane on their way together; a write's are asked for before the lookup.
+// values per lane on their way together; a write's are asked for before the lookup.  (Four prompts
+// into 4 bits 33 us, back 23, at 3.6 and 5.4 TB/s; a piece of eight values to a thread with its own
+// lookup 102 for both; 64 tokens 3.7 and 4.0.)
 #include <hip/hip_runtime.h>
 
 #include "cache_device.h"
