@@ -558,7 +558,7 @@ typedef struct {
  *   lens   : device, seqs: the sequences' lengths, new tokens included
  *   starts : device, seqs + 1, not decreasing, from 0 to at most the call's rows
  * Sequences may be empty or have no new tokens.  Rows of the call behind starts[seqs] belong to
- * nobody: they are neither read nor written.  A token whose position is negative or past width x
+ * nobody: they are not written, and what they hold is without effect.  A token whose position is negative or past width x
  * page, or whose page number is not below `pages` (-1, for instance), is nowhere: it is not
  * written, reads as zeros and is seen by no query.
  */
@@ -577,7 +577,8 @@ typedef struct {
  *   dtype         : tcq_dtype of k and v
  *   k, v          : device, rows x heads vectors, k_row and k_head (v_row, v_head) values apart
  *   rows          : the call's rows, at most 2^23
- * Outputs must not overlap inputs or one another (TCQ_EINVAL).  rows == 0 is a no-op.
+ * Outputs must not overlap inputs or one another, what lies between the heads of a row included
+ * (TCQ_EINVAL).  rows == 0 is a no-op.
  * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED (limits: heads <= 1024, seqs <= 2^20), TCQ_EHIP.
  */
 int tcq_cache_write(const tcq_cache *cache, const tcq_cache_batch *batch, int dtype,
@@ -603,8 +604,10 @@ int tcq_cache_read(const tcq_cache *cache, const tcq_cache_batch *batch, int dty
  * fp32 where they meet the values and are summed; o is rounded once.  (As bf16 numbers,
  * values below 2^-133 are lost: scale bytes below 3 in TCQ_FP8.)  How keys are shared
  * out among workgroups depends on the batch's lengths, and with it the last bits of o; the same
- * call gives the same bits.
- * Outputs must not overlap inputs (TCQ_EINVAL).  rows == 0 is a no-op.
+ * call gives the same bits.  (TCQ_FP8's NaN codes, which tcq_cache_write never writes, are not
+ * told apart like groups: a value's may reach queries of its sequence that do not see it.)
+ * Outputs must not overlap inputs, what lies between the heads of a row included (TCQ_EINVAL).
+ * rows == 0 is a no-op.
  * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED, TCQ_EWORKSPACE, TCQ_EHIP.
  */
 int tcq_cache_attention_workspace_bytes(int dim, int heads, int q_heads, int64_t seqs,

@@ -216,6 +216,28 @@ def test_pages_that_are_not_there(sizes):
     _inside(api.cache_attention(q, cache, *b.where), want, bound, "short table")
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("sizes", [[(1, 37), (3, 130)], [(90, 203), (1, 5)]])
+def test_places_that_nobody_wrote(sizes, fmt):
+    """NaN codes and scale bytes behind the sequences' ends and in pages of no sequence."""
+    g = _gen(9)
+    b = Batch(sizes, 16, g)
+    starts, total = b.whole()
+    k, v = _randn(g, total, 2, 128), _randn(g, total, 2, 128)
+    q = _randn(g, b.rows, 8, 128).bfloat16()
+    got = []
+    for code, scale in ((0, 0), (0xFF, 255), (0x7F, 127)):
+        cache = api.Cache.empty(b.pages, 2, 16, 128, fmt)
+        for t in (cache.k_codes, cache.v_codes):
+            t.fill_(code)
+        for t in (cache.k_scale, cache.v_scale):
+            t.fill_(scale)
+        api.cache_write(cache, k, v, b.table, b.lens, starts)
+        got.append(api.cache_attention(q, cache, *b.where))
+    assert bool(got[0].isfinite().all())
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
 def test_strides():
     """Queries, outputs and the table as slices of wider tensors."""
     g = _gen(6)
