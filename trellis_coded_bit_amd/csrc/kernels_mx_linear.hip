@@ -212,7 +212,8 @@ __device__ __forceinline__ void mx_tile(const Operand<CodePair> &A, const uint8_
                                         int s_end, const gemm::Stages<NB> &st, const Epi &epi) {
     constexpr int NT = WI * WJ * 64;
     constexpr int FI = TI / WI / 16, FJ = TJ / WJ / 16;
-    constexpr int FH = 2, kParts = FI / FH, kPhases = 2 * kParts;  // fragments of A to a phase
+    // fragments of A to a phase (two to a phase of 256 rows: 8192 x 4096 x 14336 224.9 us, four 223.2)
+    constexpr int FH = FI / 2, kParts = FI / FH, kPhases = 2 * kParts;
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -352,9 +353,10 @@ __device__ __forceinline__ void mx_tile(const Operand<CodePair> &A, const uint8_
 // one step on its way beside the two that are multiplied; 128 x 128: four waves of 64 x 64 and four
 // stages.  The phase before a meeting reads the next step's first fragments, and loads and
 // branches are kept out of the instructions' way.
-//   8192 x 4096 x 14336: 240 us, 4.0 PF (a library's product of the same type 291 us).  The matrix
-// cores are busy for 42 % of the clocks, LDS for 17, and the waves wait for 40 % of their time: bound
-// by one step's loads, reads and meeting, which its 64 instructions to a wave are too few to cover.
+//   8192 x 4096 x 14336: 216 us, 4.4 PF (a library's product of the same type 291 us).  The matrix
+// cores are busy for 42 % of the clocks under the profiler, LDS for 17, and the waves wait for 40 % of
+// their time, for a step's loads and meeting.  (Other phases, no order of reads and products, and
+// a raised wave priority around the products: all within 1 %.)
 template <int TI, int TJ, int WI, int WJ, int NB, typename Epi>
 __global__ __launch_bounds__(WI *WJ * 64) void mx_gemm_kernel(Operand<CodePair> A,
                                                               const uint8_t *as,
