@@ -670,7 +670,7 @@ bool mx_small(int format, int64_t B, int64_t M) {
 }
 
 // Values of x that mx_small_kernel quantises by itself, in every workgroup, rather than a launch
-// before it (us per call in a graph, it / the two: fp8 1 x 4096 x 4096 5.6 / 7.1, 1 x 14336 x 4096 11.7 /
+// before it (us per call in a graph, it / the two: fp8 1 x 4096 x 4096 5.6 / 7.1, 1 x 4096 x 14336 11.7 /
 // 12.9, 4 x 4096 x 4096 6.9 / 6.9, 8 x 4096 x 4096 8.7 / 7.0; fp4 16 x 2048 x 2048 7.4 / 6.0).
 constexpr int64_t kMxDenseValues = 16384;
 
@@ -744,9 +744,9 @@ hipError_t launch_small(MxSmallArgs a, const LayerEpilogue<T> &epi, hipStream_t 
 
 // Tile and splits of the product of B rows of 4-bit codes with M over `steps` steps of 256 columns.
 // 256 x 256 tiles where they are at least half as many as compute units (us per call in a graph,
-// they / 128 x 128: 2048 x 4096 x 4096 47.0 / 48.1, 1024 x 4096 x 14336 47.9 / 79.2, 4096^3 55.6 / 84.0;
+// they / 128 x 128: 2048 x 4096 x 4096 47.0 / 48.1, 1024 x 14336 x 4096 47.9 / 79.2, 4096^3 55.6 / 84.0;
 // with 64 tiles, 1024 x 4096 x 4096, 43.0 / 29.0).  Else 128 x 128, whose columns are split in two
-// where at most half the compute units have a tile, if there are steps enough (512 x 14336 x 4096 38.9
+// where at most half the compute units have a tile, if there are steps enough (512 x 4096 x 14336 38.9
 // split / 50.1 whole, 512 x 4096 x 4096, 16 steps, 27.6 / 26.1).  Tiles are never fewer than 113:
 // smaller products are mx_small_kernel's.
 struct MxPlan {
