@@ -1178,8 +1178,7 @@ hipError_t attend(const AttArgs &a, char *ws, hipStream_t s) {
 
 }  // namespace
 
-size_t attention_bytes(int dim, int heads, int group, int64_t seqs, int64_t rows) {
-    (void)heads;
+size_t attention_bytes(int dim, int group, int64_t seqs, int64_t rows) {
     if (rows == 0 || seqs == 0) return 0;
     size_t n = static_cast<size_t>(kSlotsFew * slot_bytes(kSmallRows, dim));
     if (!few_only(rows, group, seqs))

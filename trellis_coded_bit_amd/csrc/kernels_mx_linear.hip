@@ -17,18 +17,12 @@
 namespace tcq {
 namespace gemm {
 
-// Two 4-bit codes: k is counted in bytes, 128 to a step, and a fragment is a group of a row.
+// Two 4-bit codes: k is counted in bytes, 128 to a step (two instructions of 128 codes).
 struct CodePair {
     uint8_t b;
 };
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-template <>
-struct Traits<CodePair> {
-    static constexpr int kStep = 128;
-    static constexpr int kSub = 2;  // 128 codes each
-    using Frag = i32x4;
-};
 
 }  // namespace gemm
 

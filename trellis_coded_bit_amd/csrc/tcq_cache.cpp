@@ -223,7 +223,7 @@ extern "C" int tcq_cache_attention_workspace_bytes(int dim, int heads, int q_hea
         set_error("%s: bytes is NULL", fn);
         return TCQ_EINVAL;
     }
-    *bytes = attention_bytes(dim, heads, q_heads / heads, seqs, rows);
+    *bytes = attention_bytes(dim, q_heads / heads, seqs, rows);
     return TCQ_OK;
 }
 
@@ -251,7 +251,7 @@ extern "C" int tcq_cache_attention(const tcq_cache *cache, const tcq_cache_batch
     if (rc == TCQ_OK) rc = check_rows(fn, "o", o, o_row, o_head, q_heads, c.dim, size);
     if (rc != TCQ_OK) return rc;
     rc = check_workspace(fn, workspace, workspace_bytes,
-                         attention_bytes(c.dim, c.heads, q_heads / c.heads, b.seqs, rows));
+                         attention_bytes(c.dim, q_heads / c.heads, b.seqs, rows));
     if (rc != TCQ_OK) return rc;
     const Region ro = rows_region("o", o, rows, o_row, o_head, q_heads, c.dim, size);
     rc = check_apart(fn, ro, rows_region("q", q, rows, q_row, q_head, q_heads, c.dim, size));

@@ -291,7 +291,7 @@ struct AttentionCall {
     int64_t rows;
     float scale;
 };
-size_t attention_bytes(int dim, int heads, int group, int64_t seqs, int64_t rows);
+size_t attention_bytes(int dim, int group, int64_t seqs, int64_t rows);
 hipError_t launch_attention(const AttentionCall &c, char *ws, hipStream_t s);
 
 // 8-bit checkpoints (unpack also writes zeros to columns cols .. padded - 1 of out).
