@@ -270,6 +270,31 @@ def test_many_sequences():
         _inside(api.cache_attention(q, cache, *b.where), want, bound, f"{seqs} sequences")
 
 
+@pytest.mark.parametrize("lone", [True, False])
+def test_thousands_of_sequences(lone):
+    """Items found in running sums over more sequences than one turn of them takes, long ones cut
+    into runs among them; single tokens alone, and with chunks."""
+    g = _gen(10)
+    sizes = [(1 if s % 5 else 0, 1 + s * 37 % 90) for s in range(1100)]
+    sizes[3], sizes[1040] = (1, 9000), (1, 4000)
+    if not lone:
+        sizes[7], sizes[1030], sizes[1099] = (300, 3000), (150, 2000), (40, 40)
+    b = Batch(sizes, 16, g)
+    cache, k, v = _fill(b, 2, 64, "fp8", g)
+    q = _randn(g, b.rows, 8, 64).bfloat16()
+    want, bound = _expect(b, q, k, v, 0.125, torch.bfloat16)
+    out = api.cache_attention(q, cache, *b.where)
+    _inside(out, want, bound, "1100 sequences")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = api.cache_attention(q, cache, *b.where)
+    for _ in range(3):
+        o.fill_(NAN)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, out)
+
+
 def test_workspaces_streams_and_graphs():
     """Two graphs that share a workspace one after the other, another stream, a workspace larger than
     needed, full of NaN."""

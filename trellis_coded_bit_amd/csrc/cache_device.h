@@ -25,20 +25,24 @@ __device__ __forceinline__ Span span_of(const CacheBatch &b, int64_t s, int64_t 
     return r;
 }
 
-// The sequence that holds row `row` (uniform in a wave): how many of starts[1 .. seqs] are at most
-// row, found by 64 probes at a time.  seqs: none.
-__device__ __forceinline__ int64_t sequence_of(const CacheBatch &b, int64_t row, int lane) {
-    if (row < b.starts[0]) return b.seqs;
-    int64_t lo = 0, n = b.seqs;  // the answer is in [lo, lo + n]
+// How many of the n increasing v are at most x (uniform in a wave), found by 64 probes at a time.
+template <typename V>
+__device__ __forceinline__ int64_t at_most(const V *v, int64_t n, int64_t x, int lane) {
+    int64_t lo = 0;  // the answer is in [lo, lo + n]
     while (n > 0) {
         const int64_t step = (n + 63) / 64;
         const int64_t i = lo + (lane + 1) * step - 1;
-        const bool below = i < lo + n && b.starts[i + 1] <= row;
+        const bool below = i < lo + n && static_cast<int64_t>(v[i]) <= x;
         const int64_t skip = __popcll(__ballot(below)) * step;
         lo += skip;
         n = step - 1 < n - skip ? step - 1 : n - skip;
     }
     return lo;
+}
+
+// The sequence that holds row `row` (uniform in a wave).  seqs: none.
+__device__ __forceinline__ int64_t sequence_of(const CacheBatch &b, int64_t row, int lane) {
+    return row < b.starts[0] ? b.seqs : at_most(b.starts + 1, b.seqs, row, lane);
 }
 
 // The page of position pos of sequence s, or -1 where there is none.

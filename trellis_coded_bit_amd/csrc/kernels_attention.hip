@@ -15,8 +15,9 @@
 // lanes, and p is in place as the second operand of O^T = V^T P^T.  That product's order of
 // keys is the one the lanes hold them in, and V is read across through LDS in the same order.
 //
-// Work is cut into items (sequence, head, tile of query rows, run of keys) by every workgroup
-// from the lengths on the device, so that the host need not know them: runs are as long as lets
+// Work is cut into items (sequence, head, tile of query rows, run of keys) by every workgroup, or
+// by a kernel before for many sequences, from the lengths on the device, so that the host need not
+// know them: runs are as long as lets
 // about kTarget items remain.  A tile with one run writes its outputs, others their share, and
 // a second kernel joins shares in the order of the runs.
 #include <hip/hip_runtime.h>
@@ -44,6 +45,7 @@ struct AttArgs {
     float factor, factor_low;   // scale log2(e), and what it lacks
     float *part;                // shares: [slot][rows of a tile][dim], then maxima and sums
     uint32_t slots;
+    uint32_t *plan;             // see plan_kernel; NULL: workgroups scan the sequences themselves
     int both;                   // tiles of 16 rows serve sequences of up to kFewRows rows only,
                                 // larger tiles the others (0: this kernel serves every sequence)
 };
@@ -104,23 +106,41 @@ __device__ __forceinline__ uint32_t of_lane(uint32_t v, int lane) {
     return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
 }
 
-// Units per run: the fewest with at most about the target number of runs in all.
+// Units per run: the fewest with at most about the target number of runs in all, given the units
+// of all tiles of a head.
 template <int BQ>
-__device__ __forceinline__ uint32_t run_units(const AttArgs &a, int lane) {
-    uint64_t total = 0;
-    for (int64_t s = 0; s < a.b.seqs; s += 64) {
-        const Sequence q = sequence<BQ>(a, s + lane);
-        total += static_cast<uint64_t>(q.tiles) * q.units;
-    }
-    // (a wave's first lanes hold everything where sequences are few)
-    const int n = a.b.seqs < 64 ? static_cast<int>(a.b.seqs) : 64;
-    for (int d = 1; d < n; d <<= 1) total += __shfl_xor(total, d);
+__device__ __forceinline__ uint32_t run_units(const AttArgs &a, uint64_t total) {
     total *= a.c.heads;
     const uint32_t runs = target<BQ>(total);
     uint64_t per = (total + runs - 1) / runs;
     per = per > 1 ? per : 1;
-    per = per < (1u << 30) ? per : 1u << 30;  // (units are fewer)
-    return of_lane(static_cast<uint32_t>(per), 0);
+    return static_cast<uint32_t>(per < (1u << 30) ? per : 1u << 30);  // (units are fewer)
+}
+template <int BQ>
+__device__ __forceinline__ uint32_t run_units(const AttArgs &a, int lane) {
+    if (a.plan) return a.plan[0];
+    const Sequence q = sequence<BQ>(a, lane);
+    uint64_t total = static_cast<uint64_t>(q.tiles) * q.units;
+    // (a wave's first lanes hold everything)
+    for (int d = 1; d < a.b.seqs; d <<= 1) total += __shfl_xor(total, d);
+    return of_lane(run_units<BQ>(a, total), 0);
+}
+
+// Of a sequence: its pairs (tile, head) that have several runs, its items (pair, run) and those
+// items that are shares.
+struct Counts {
+    uint32_t pairs, items, shares;
+};
+// (A launch has fewer than 2^24 workgroups: counts are cut to 2^25 so that 64 of them fit.)
+template <int BQ>
+__device__ __forceinline__ Counts counts(const AttArgs &a, Sequence &q, uint32_t per) {
+    const auto cut = [](uint64_t v) {
+        return v < (1u << 25) ? static_cast<uint32_t>(v) : 1u << 25;
+    };
+    q.chunks = q.units > per ? (q.units + per - 1) / per : 1;
+    const uint64_t pairs = static_cast<uint64_t>(q.tiles) * a.c.heads;
+    const uint32_t items = cut(pairs * q.chunks);
+    return Counts{q.chunks > 1 ? cut(pairs) : 0, items, q.chunks > 1 ? items : 0};
 }
 
 // One of the pairs (tile, head) or items (pair, run of keys) of a launch; uniform in a wave.
@@ -130,38 +150,102 @@ struct Item {
     uint32_t left;              // its number in the sequence
     uint32_t slot;              // number of its share
 };
-// Item (PAIRS: pair with several runs) `index`, or false past the last.  (A launch has fewer than
-// 2^24: counts are cut to 2^25 so that 64 of them fit.)
+// Item (PAIRS: pair with several runs) `index`, or false past the last.
 template <int BQ, bool PAIRS>
 __device__ __forceinline__ bool item_of(const AttArgs &a, uint32_t index, uint32_t per, int lane,
                                         Item &it) {
-    uint32_t slots = 0;
-    for (int64_t s = 0; s < a.b.seqs; s += 64) {
-        Sequence q = sequence<BQ>(a, s + lane);
-        q.chunks = q.units > per ? (q.units + per - 1) / per : 1;
-        const uint64_t pairs = static_cast<uint64_t>(q.tiles) * a.c.heads;
-        const uint64_t items = pairs * q.chunks, shares = q.chunks > 1 ? items : 0;
-        const auto cut = [](uint64_t v) {
-            return v < (1u << 25) ? static_cast<uint32_t>(v) : 1u << 25;
-        };
-        const uint32_t n = cut(PAIRS ? (q.chunks > 1 ? pairs : 0) : items);
-        const int used = a.b.seqs - s < 64 ? static_cast<int>(a.b.seqs - s) : 64;
-        const uint32_t to = wave_prefix(n, lane, used), all = of_lane(to, used - 1);
-        const uint32_t stop = wave_prefix(cut(shares), lane, used);
-        if (index < all) {
-            // lanes before the item's
-            const int at = __popcll(__ballot(lane < used && to <= index));
-            it.seq = s + at;
-            it.tiles = of_lane(q.tiles, at);
-            it.chunks = of_lane(q.chunks, at);
-            it.left = index - of_lane(to - n, at);
-            it.slot = slots + of_lane(stop - cut(shares), at) + it.left;
-            return true;
-        }
-        index -= all;
-        slots += of_lane(stop, used - 1);
+    const int seqs = static_cast<int>(a.b.seqs);
+    if (a.plan) {
+        const uint32_t *pairs = a.plan + 4, *items = pairs + seqs, *shares = items + seqs;
+        const uint32_t *to = PAIRS ? pairs : items;
+        const int s = static_cast<int>(cache::at_most(to, seqs, index, lane));
+        if (s >= seqs) return false;
+        Sequence q = sequence<BQ>(a, s);
+        const Counts c = counts<BQ>(a, q, per);
+        it.seq = s;
+        it.tiles = of_lane(q.tiles, 0);
+        it.chunks = of_lane(q.chunks, 0);
+        it.left = of_lane(index - (to[s] - (PAIRS ? c.pairs : c.items)), 0);
+        it.slot = of_lane(shares[s] - c.shares, 0) + it.left;
+        return true;
     }
-    return false;
+    Sequence q = sequence<BQ>(a, lane);
+    const Counts c = counts<BQ>(a, q, per);
+    const uint32_t n = PAIRS ? c.pairs : c.items;
+    const uint32_t to = wave_prefix(n, lane, seqs);
+    if (index >= of_lane(to, seqs - 1)) return false;
+    const uint32_t stop = wave_prefix(c.shares, lane, seqs);
+    // lanes before the item's
+    const int at = __popcll(__ballot(lane < seqs && to <= index));
+    it.seq = at;
+    it.tiles = of_lane(q.tiles, at);
+    it.chunks = of_lane(q.chunks, at);
+    it.left = index - of_lane(to - n, at);
+    it.slot = of_lane(stop - c.shares, at) + it.left;
+    return true;
+}
+
+// Batches of more than 64 sequences: a workgroup for each size of tile writes the units of a run
+// and, over the sequences, running sums of their counts (cut to 2^31), in which the others search.
+// (One token of 256 sequences of 100 to 600 keys, 32 query heads over 8 of 128, 66 us, with scans of
+// them all in every workgroup 97; of 1024 240 and 623; of 4096 917 and 7350.)
+constexpr int kScanned = 64;
+constexpr int kPlanThreads = 1024;
+int64_t plan_words(int64_t seqs) { return seqs > kScanned ? 4 + (3 * seqs + 3) / 4 * 4 : 0; }
+template <int BQ>
+__device__ __forceinline__ void plan(const AttArgs &a) {
+    constexpr int kWaves = kPlanThreads / 64;
+    __shared__ uint64_t sums[3][kWaves];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    uint64_t total = 0;
+    for (int64_t s = tid; s < a.b.seqs; s += kPlanThreads) {
+        const Sequence q = sequence<BQ>(a, s);
+        total += static_cast<uint64_t>(q.tiles) * q.units;
+    }
+    for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+    if (lane == 0) sums[0][wave] = total;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kWaves; ++w) total += sums[0][w];
+    __syncthreads();
+    const uint32_t per = run_units<BQ>(a, total);
+    if (tid == 0) a.plan[0] = per;
+    uint64_t before[3] = {0, 0, 0};
+    for (int64_t s0 = 0; s0 < a.b.seqs; s0 += kPlanThreads) {
+        const int64_t s = s0 + tid;
+        Sequence q = sequence<BQ>(a, s);
+        const Counts c = counts<BQ>(a, q, per);
+        uint64_t v[3] = {c.pairs, c.items, c.shares};
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            for (int d = 1; d < 64; d <<= 1) {
+                const uint64_t o = __shfl_up(v[k], d);
+                if (lane >= d) v[k] += o;
+            }
+            if (lane == 63) sums[k][wave] = v[k];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            uint64_t all = 0;
+            for (int w = 0; w < kWaves; ++w) {
+                if (w == wave) v[k] += before[k] + all;
+                all += sums[k][w];
+            }
+            before[k] += all;
+            if (s < a.b.seqs)
+                a.plan[4 + k * a.b.seqs + s] =
+                    static_cast<uint32_t>(v[k] < (1u << 31) ? v[k] : 1u << 31);
+        }
+        __syncthreads();
+    }
+}
+template <int BQ>
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(AttArgs few, AttArgs many) {
+    if (blockIdx.x == 0)
+        plan<kSmallRows>(few);
+    else
+        plan<BQ>(many);
 }
 
 // What a workgroup computes, uniform.  Heads vary fastest, so that those of one sequence go to
@@ -1107,6 +1191,12 @@ constexpr int kSlotsFew = 2 * kTargetSmall, kSlotsMany = 2 * kTargetLarge;
 constexpr int kMostRows = 256;   // of a tile
 int64_t slot_bytes(int bq, int dim) { return int64_t{bq} * (dim + 2) * 4; }
 
+// Of the shares, a multiple of 16.
+int64_t parts_bytes(int dim, bool few) {
+    const int64_t n = kSlotsFew * slot_bytes(kSmallRows, dim);
+    return few ? n : n + kSlotsMany * slot_bytes(kMostRows, dim);
+}
+
 template <typename T, int D, int FMT, int NW, int NQ>
 hipError_t attend_as(const AttArgs &base, char *ws, hipStream_t s) {
     constexpr int kRows = NW * NQ * 16;
@@ -1117,6 +1207,15 @@ hipError_t attend_as(const AttArgs &base, char *ws, hipStream_t s) {
     few.part = reinterpret_cast<float *>(ws);
     few.slots = kSlotsFew;
     many.part = reinterpret_cast<float *>(ws + int64_t{kSlotsFew} * slot_bytes(kSmallRows, D));
+    if (base.b.seqs > kScanned) {
+        const int64_t words = plan_words(base.b.seqs);
+        few.plan = reinterpret_cast<uint32_t *>(ws + parts_bytes(D, only));
+        many.plan = few.plan + words;
+        hipLaunchKernelGGL((plan_kernel<kRows>), dim3(only ? 1 : 2), dim3(kPlanThreads), 0, s, few,
+                           many);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     many.slots = kSlotsMany;
     // tiles of all sequences: whole ones of the rows, and a part of one for each
     const int64_t qrows = base.rows * base.group;
@@ -1180,10 +1279,8 @@ hipError_t attend(const AttArgs &a, char *ws, hipStream_t s) {
 
 size_t attention_bytes(int dim, int group, int64_t seqs, int64_t rows) {
     if (rows == 0 || seqs == 0) return 0;
-    size_t n = static_cast<size_t>(kSlotsFew * slot_bytes(kSmallRows, dim));
-    if (!few_only(rows, group, seqs))
-        n += static_cast<size_t>(kSlotsMany * slot_bytes(kMostRows, dim));
-    return align_up(n, 256);
+    const int64_t n = parts_bytes(dim, few_only(rows, group, seqs)) + 8 * plan_words(seqs);
+    return align_up(static_cast<size_t>(n), 256);
 }
 
 hipError_t launch_attention(const AttentionCall &c, char *ws, hipStream_t s) {
