@@ -18,7 +18,7 @@
 // Work is cut into items (sequence, head, tile of query rows, run of keys) by every workgroup, or
 // by a kernel before for many sequences, from the lengths on the device, so that the host need not
 // know them: runs are as long as lets
-// about kTarget items remain.  A tile with one run writes its outputs, others their share, and
+// about the target number of them remain.  A tile with one run writes its outputs, others their share, and
 // a second kernel joins shares in the order of the runs.
 #include <hip/hip_runtime.h>
 
