@@ -118,7 +118,7 @@ __device__ __forceinline__ uint32_t run_units(const AttArgs &a, uint64_t total) 
 }
 template <int BQ>
 __device__ __forceinline__ uint32_t run_units(const AttArgs &a, int lane) {
-    if (a.plan) return a.plan[0];
+    if (__builtin_expect(a.plan != nullptr, 0)) return a.plan[0];
     const Sequence q = sequence<BQ>(a, lane);
     uint64_t total = static_cast<uint64_t>(q.tiles) * q.units;
     // (a wave's first lanes hold everything)
@@ -155,7 +155,7 @@ template <int BQ, bool PAIRS>
 __device__ __forceinline__ bool item_of(const AttArgs &a, uint32_t index, uint32_t per, int lane,
                                         Item &it) {
     const int seqs = static_cast<int>(a.b.seqs);
-    if (a.plan) {
+    if (__builtin_expect(a.plan != nullptr, 0)) {
         const uint32_t *pairs = a.plan + 4, *items = pairs + seqs, *shares = items + seqs;
         const uint32_t *to = PAIRS ? pairs : items;
         const int s = static_cast<int>(cache::at_most(to, seqs, index, lane));
@@ -813,9 +813,9 @@ attend_few_kernel(AttArgs a) {
 // first four after the whole tile, so that one wave of a SIMD computes its softmax while the other
 // multiplies; values are kept for a tile longer for it.
 //   Bound by what two waves of a SIMD issue between two meetings: four chunks of 511 to 2048 tokens
-// behind 4000 to 16384, 32 query heads over 8 of 128, bf16, 1220 us (897 TF) with the matrix cores
+// behind 4000 to 16384, 32 query heads over 8 of 128, bf16, 1240 us (882 TF) with the matrix cores
 // busy for 38 % of the clocks, VALU for 42 and LDS for 37.  (Without the third of the latter that
-// are bank conflicts of the keys' reads it takes 1257 us.)
+// are bank conflicts of the keys' reads it took 3 % more.)
 template <typename T, int D, int FMT, int NW, int NQ>
 __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
     constexpr int TERMS = terms<T>();
