@@ -5,10 +5,11 @@
 // a key is read once for all of them.
 //
 // Every code times its scale is a bf16 number, so keys and values are multiplied as bf16 with
-// exact products and fp32 sums.  q and p are held in terms of bf16 whose sum they are: one for
-// bf16 queries (q is exact; p is rounded to 8 bits, half a step of the output's own type, and its
-// sum is that of the rounded ones), two for fp16 (q exact, p to 2^-15) and three for fp32 (both
-// exact).
+// exact products and fp32 sums.  q and p are held in terms of bf16 whose sum they are: q exactly, in
+// one for bf16, two for fp16 and three for fp32.  p in three for fp32 (exact) and in two for 16-bit
+// queries (to 2^-15, far below the output's own rounding), but for bf16 queries in the larger tiles
+// in one (to 2^-8, half a step of the output's type): see attend_many_kernel.  The sum of p is
+// that of the rounded ones.
 //
 // Scores are computed transposed, S^T = K Q^T: a lane holds four keys of one query row, the same
 // row in every instruction, so a row's maximum and sum are the lane's own but for three other
@@ -329,9 +330,15 @@ __device__ __forceinline__ void terms_of(float a, float b, uint32_t (&w)[TERMS])
             __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
 }
 
+// Terms of q, and of p in the larger tiles.
 template <typename T>
 constexpr int terms() {
     return sizeof(T) == 4 ? 3 : (__is_same(T, _Float16) ? 2 : 1);
+}
+// Terms of p in the tiles of 16 rows.
+template <typename T>
+constexpr int few_weight_terms() {
+    return sizeof(T) == 4 ? 3 : 2;
 }
 
 // f over the four lanes that hold a query row's keys: lanes l, l ^ 16, l ^ 32,
@@ -570,7 +577,11 @@ __device__ __forceinline__ void add_wild(const s16x8 &x, const s16x8 (&p)[TERMS]
 //   Bound to two waves to a SIMD the compiler keeps the outputs out of the accumulation registers, whose
 // copies cost a tile 128 instructions (64 sequences, 4 heads of 128: fp32 over fp8 191 us, 145 with;
 // bf16 over fp4 99 and 96).  256 dims do not fit but for bf16 over fp4 (235 and 196; fp8 305 and 544).
-//   Bound by memory: 64 sequences of 1000 to 16000 keys, 8 heads of 128, fp8, 251 us at 4.6 TB/s.
+//   Bound by memory: 64 sequences of 1000 to 16000 keys, 8 heads of 128, fp8, 252 us at 4.6 TB/s.
+//   So bf16 queries' weights in two terms cost little, and leave the outputs' own rounding alone
+// (relative to the norm of float64 outputs 1.66e-3 there, the outputs' rounding itself, and 2.33e-3
+// with one term): 252 us with either, 64 sequences over fp4 96 and 94, 256 of 100 to 600 keys 68
+// and 67, 16 of 8 tokens 87 and 85, 256 dims over fp4 180 and 171.
 template <typename T, int D, int FMT>
 constexpr int few_waves() {
     return D < 256 || (FMT == TCQ_FP4 && terms<T>() == 1) ? 2 : 1;
@@ -579,6 +590,7 @@ template <typename T, int D, int FMT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(few_waves<T, D, FMT>()))) void
 attend_few_kernel(AttArgs a) {
     constexpr int TERMS = terms<T>();
+    constexpr int PT = few_weight_terms<T>();
     constexpr int BQ = kSmallRows;
     constexpr int kRow = mx::bytes<FMT>(D);    // bytes of a cache row
     constexpr int kRun = kRow / 4;             // of it, one lane's
@@ -748,30 +760,30 @@ attend_few_kernel(AttArgs a) {
         float p[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            p[i] = weight<TERMS>(s[i / 4][i % 4], a.factor, a.factor_low, ref);
-        s16x8 pf[TERMS];
+            p[i] = weight<PT>(s[i / 4][i % 4], a.factor, a.factor_low, ref);
+        s16x8 pf[PT];
         {
-            u32x4 w[TERMS];
+            u32x4 w[PT];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                uint32_t t[TERMS];
-                terms_of<TERMS>(p[2 * k], p[2 * k + 1], t);
+                uint32_t t[PT];
+                terms_of<PT>(p[2 * k], p[2 * k + 1], t);
 #pragma unroll
-                for (int n = 0; n < TERMS; ++n) w[n][k] = t[n];
+                for (int n = 0; n < PT; ++n) w[n][k] = t[n];
             }
 #pragma unroll
-            for (int n = 0; n < TERMS; ++n) pf[n] = __builtin_bit_cast(s16x8, w[n]);
+            for (int n = 0; n < PT; ++n) pf[n] = __builtin_bit_cast(s16x8, w[n]);
         }
         sm.add(pf);
         __builtin_amdgcn_wave_barrier();
         if (__builtin_expect(__any(wild) && __any(sees != 0xFFu), 0)) {
 #pragma unroll
             for (int t = 0; t < kTiles; ++t)
-                add_wild<TERMS>(read_across<D * 2>(vt + (from_lds ^ (t * 32))), pf, sees, acc[t]);
+                add_wild<PT>(read_across<D * 2>(vt + (from_lds ^ (t * 32))), pf, sees, acc[t]);
         } else {
 #pragma unroll
             for (int t = 0; t < kTiles; ++t)
-                acc[t] = mma_terms<TERMS>(read_across<D * 2>(vt + (from_lds ^ (t * 32))), pf, acc[t]);
+                acc[t] = mma_terms<PT>(read_across<D * 2>(vt + (from_lds ^ (t * 32))), pf, acc[t]);
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -816,6 +828,10 @@ attend_few_kernel(AttArgs a) {
 // behind 4000 to 16384, 32 query heads over 8 of 128, bf16, 1240 us (882 TF) with the matrix cores
 // busy for 38 % of the clocks, VALU for 42 and LDS for 37.  (Without the third of the latter that
 // are bank conflicts of the keys' reads it took 3 % more.)
+//   bf16 queries' weights meet the values as one bf16 number, as wide as the values: outputs are then
+// 1.4 times as far from those of float64 as their own rounding puts them (2.34e-3 of their norm,
+// 1.66e-3 with two terms).  Two terms took 1740 us there, at 64 dims 998 instead of 812, at 256
+// dims (four chunks of 511 to 1024 behind 4000 to 8192, 16 query heads over 4) 702 instead of 634.
 template <typename T, int D, int FMT, int NW, int NQ>
 __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
     constexpr int TERMS = terms<T>();
