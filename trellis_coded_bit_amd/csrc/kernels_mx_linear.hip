@@ -143,8 +143,8 @@ struct ScaleReader {
 };
 
 // The loads of a tile of TR rows by one step, as TileLoader's (chunk c of row r into slot c ^ (r >>
-// 1 & 7), zeros past the rows and past k), with one offset per thread: a thread's rows lie NT / 8
-// rows apart.  `renew` makes an offset a new value to the compiler, which otherwise holds every
+// 1 & 7), zeros past the rows and past k), with one offset of 32 bits per thread (rows at most
+// kMostPitch bytes apart): a thread's rows lie NT / 8 rows apart.  `renew` makes an offset a new value to the compiler, which otherwise holds every
 // sum with it in registers, 26 of them, and spills to make room; a spill's return waits for all
 // loads on their way.
 template <int TR, int NT>
@@ -816,10 +816,11 @@ hipError_t large_fp4(const MxLinearCall &c, const MxMatrix &x, const MxLayout &l
     return hipGetLastError();
 }
 
+// The layer for rows that mx_small_kernel takes, or not.
 template <typename T>
-hipError_t linear(const MxLinearCall &c, char *ws, hipStream_t s) {
-    const MxLayout lay = mx_linear_layout(c.xq.format, c.B, c.M, c.N);
-    const bool fp4 = c.xq.format == TCQ_FP4, small = mx_small(c.xq.format, c.B, c.M);
+hipError_t linear_rows(const MxLinearCall &c, const MxLayout &lay, bool small, char *ws,
+                       hipStream_t s) {
+    const bool fp4 = c.xq.format == TCQ_FP4;
     const bool dense = small && small_dense(c);
     MxMatrix x = c.xq;
     uint16_t *xvals = reinterpret_cast<uint16_t *>(ws + lay.xvals);
@@ -884,6 +885,38 @@ hipError_t linear(const MxLinearCall &c, char *ws, hipStream_t s) {
     const DenseProduct d{xvals,  wvals,      lay.ldn, lay.ldn, c.B, c.M, lay.ldn,
                          c.dtype, c.bias, c.residual, c.ldr,   c.y, c.ldy};
     return launch_dense_product(d, ws + lay.parts, s);
+}
+
+// Bytes between the rows of codes up to which a tile's offsets fit CodeLoader's 32 bits: 255
+// rows of it, and a row's last piece, lie below the largest extent of a buffer.  Codes further apart
+// are multiplied by mx_small_kernel, whose offsets have 64 bits, in pieces of so many rows that its
+// grid holds their shares.
+constexpr int64_t kMostPitch = 1 << 24;
+static_assert(255 * kMostPitch + 128 < 0xFFFFFF00ll, "offsets of a tile");
+constexpr int64_t kFarRows = 1 << 19;
+
+template <typename T>
+hipError_t linear(const MxLinearCall &c, char *ws, hipStream_t s) {
+    const MxLayout lay = mx_linear_layout(c.xq.format, c.B, c.M, c.N);
+    const bool small = mx_small(c.xq.format, c.B, c.M);
+    const bool far = c.w.ld > kMostPitch || ((!c.x || c.keep) && c.xq.ld > kMostPitch);
+    if (small || c.xq.format != TCQ_FP4 || !far || c.N == 0)
+        return linear_rows<T>(c, lay, small, ws, s);
+    const int64_t groups = groups_of(c.N);
+    for (int64_t b = 0; b < c.B; b += kFarRows) {
+        MxLinearCall p = c;
+        p.B = c.B - b < kFarRows ? c.B - b : kFarRows;
+        if (c.x) p.x = static_cast<const T *>(c.x) + b * c.ldx;
+        if (!c.x || c.keep) {
+            p.xq.codes += b * c.xq.ld;
+            p.xq.scale += b * groups;
+        }
+        if (c.residual) p.residual = static_cast<const T *>(c.residual) + b * c.ldr;
+        p.y = static_cast<T *>(c.y) + b * c.ldy;
+        const hipError_t e = linear_rows<T>(p, lay, true, ws, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 // ---------------------------------------------------------------- gradients
