@@ -611,7 +611,9 @@ int tcq_cache_read(const tcq_cache *cache, const tcq_cache_batch *batch, int dty
  * value's may reach queries of its sequence that do not see it.)
  * Outputs must not overlap inputs, what lies between the heads of a row included (TCQ_EINVAL).
  * rows == 0 is a no-op.
- * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED, TCQ_EWORKSPACE, TCQ_EHIP.
+ * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED (the cache's limits, and batches whose launches would not
+ * fit: rows x q_heads / 16 + seqs x heads of 2^24 - 4096 or, with more than 16 query rows to a
+ * sequence on average, rows x q_heads / 128 + seqs x heads of 2^23 - 256), TCQ_EWORKSPACE, TCQ_EHIP.
  */
 int tcq_cache_attention_workspace_bytes(int dim, int heads, int q_heads, int64_t seqs,
                                         int64_t rows, size_t *bytes);

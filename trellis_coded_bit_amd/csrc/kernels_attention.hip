@@ -1204,7 +1204,8 @@ bool few_only(int64_t rows, int group, int64_t seqs) {
 // units, so there are at most twice the target.
 constexpr int kSlotsFew = 2 * kTargetSmall, kSlotsMany = 2 * kTargetLarge;
 
-constexpr int kMostRows = 256;   // of a tile
+constexpr int kLeastRows = 128, kMostRows = 256;   // of a larger tile
+constexpr int kManyThreads = 512;                  // and its threads
 int64_t slot_bytes(int bq, int dim) { return int64_t{bq} * (dim + 2) * 4; }
 
 // Of the shares, a multiple of 16.
@@ -1216,6 +1217,7 @@ int64_t parts_bytes(int dim, bool few) {
 template <typename T, int D, int FMT, int NW, int NQ>
 hipError_t attend_as(const AttArgs &base, char *ws, hipStream_t s) {
     constexpr int kRows = NW * NQ * 16;
+    static_assert(kRows >= kLeastRows && kRows <= kMostRows && NW * 64 == kManyThreads, "a tile");
     AttArgs few = base, many = base;
     const bool only = few_only(base.rows, base.group, base.b.seqs);
     const int64_t heads = base.c.heads;
@@ -1297,6 +1299,11 @@ size_t attention_bytes(int dim, int group, int64_t seqs, int64_t rows) {
     if (rows == 0 || seqs == 0) return 0;
     const int64_t n = parts_bytes(dim, few_only(rows, group, seqs)) + 8 * plan_words(seqs);
     return align_up(static_cast<size_t>(n), 256);
+}
+
+int64_t attention_threads(int group, int heads, int64_t seqs, int64_t rows) {
+    if (few_only(rows, group, seqs)) return 0;
+    return ((rows * group / kLeastRows + seqs) * heads + kTargetLarge) * kManyThreads;
 }
 
 hipError_t launch_attention(const AttentionCall &c, char *ws, hipStream_t s) {

@@ -186,6 +186,12 @@ int check_heads(const char *fn, int q_heads, int heads, int64_t rows, int64_t se
                   (long long)seqs);
         return TCQ_EUNSUPPORTED;
     }
+    if (attention_threads(q_heads / heads, heads, seqs, rows) > UINT32_MAX) {
+        set_error("%s: outside the limits (rows x q_heads / 128 + seqs x heads below 2^23 - 256 with "
+                  "more than 16 query rows to a sequence on average): rows=%lld q_heads=%d "
+                  "seqs=%lld heads=%d", fn, (long long)rows, q_heads, (long long)seqs, heads);
+        return TCQ_EUNSUPPORTED;
+    }
     return TCQ_OK;
 }
 

@@ -292,6 +292,8 @@ struct AttentionCall {
     float scale;
 };
 size_t attention_bytes(int dim, int group, int64_t seqs, int64_t rows);
+// Threads of the launch of large tiles (0: there is none), at most.
+int64_t attention_threads(int group, int heads, int64_t seqs, int64_t rows);
 hipError_t launch_attention(const AttentionCall &c, char *ws, hipStream_t s);
 
 // 8-bit checkpoints (unpack also writes zeros to columns cols .. padded - 1 of out).
