@@ -632,22 +632,23 @@ __global__ __launch_bounds__(256) void order_rows_kernel(const uint8_t *__restri
                                                          const uint8_t *__restrict__ scale, int B,
                                                          int groups, MxOrder out, int64_t work) {
     constexpr int kHalves = FMT == TCQ_FP4 ? 1 : 2;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= work) return;
-    const int lane = static_cast<int>(i & 63), h = static_cast<int>((i >> 6) % kHalves);
-    const int64_t rest = (i >> 6) / kHalves;
-    const int k = static_cast<int>(rest & 1), t = static_cast<int>((rest >> 1) % out.nbt);
-    const int64_t p = (rest >> 1) / out.nbt;
-    const int r = t * 16 + (lane & 15), grp = static_cast<int>(p) * 8 + 2 * (lane >> 4) + k;
-    const bool in = r < B && grp < groups;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (in)
-        v = *reinterpret_cast<const uint4 *>(codes + r * ld +
-                                             (static_cast<int64_t>(grp) * kHalves + h) * 16);
-    reinterpret_cast<uint4 *>(out.codes)[i] = v;
-    if (h == 0)
-        out.scale[((p * out.nbt + t) * 64 + lane) * 2 + k] =
-            in ? scale[static_cast<int64_t>(r) * groups + grp] : 127;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < work;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int lane = static_cast<int>(i & 63), h = static_cast<int>((i >> 6) % kHalves);
+        const int64_t rest = (i >> 6) / kHalves;
+        const int k = static_cast<int>(rest & 1), t = static_cast<int>((rest >> 1) % out.nbt);
+        const int64_t p = (rest >> 1) / out.nbt;
+        const int r = t * 16 + (lane & 15), grp = static_cast<int>(p) * 8 + 2 * (lane >> 4) + k;
+        const bool in = r < B && grp < groups;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (in)
+            v = *reinterpret_cast<const uint4 *>(codes + r * ld +
+                                                 (static_cast<int64_t>(grp) * kHalves + h) * 16);
+        reinterpret_cast<uint4 *>(out.codes)[i] = v;
+        if (h == 0)
+            out.scale[((p * out.nbt + t) * 64 + lane) * 2 + k] =
+                in ? scale[static_cast<int64_t>(r) * groups + grp] : 127;
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -667,6 +668,12 @@ bool mx_small(int format, int64_t B, int64_t M) {
 // before it (us per call in a graph, it / the two: fp8 1 x 4096 x 4096 5.6 / 7.1, 1 x 4096 x 14336 11.7 /
 // 12.9, 4 x 4096 x 4096 6.9 / 6.9, 8 x 4096 x 4096 8.7 / 7.0; fp4 16 x 2048 x 2048 7.4 / 6.0).
 constexpr int64_t kMxDenseValues = 16384;
+
+// Workgroups of 256 threads, each of which takes every so many-th of `work` pieces.
+uint32_t blocks_for(int64_t work) {
+    const int64_t n = (work + 255) / 256;
+    return static_cast<uint32_t>(n < (1 << 20) ? n : 1 << 20);
+}
 
 size_t pad(int64_t n, int64_t to) { return static_cast<size_t>((n + to - 1) / to * to); }
 
@@ -849,9 +856,8 @@ hipError_t linear_rows(const MxLinearCall &c, const MxLayout &lay, bool small, c
         if (!c.x && c.N > 0) {
             const int64_t work = pairs * nbt * 128 * (fp4 ? 1 : 2);
             hipLaunchKernelGGL(fp4 ? order_rows_kernel<TCQ_FP4> : order_rows_kernel<TCQ_FP8>,
-                               dim3(static_cast<unsigned>((work + 255) / 256)), dim3(256), 0, s,
-                               x.codes, x.ld, x.scale, static_cast<int>(c.B),
-                               static_cast<int>(groups), order, work);
+                               dim3(blocks_for(work)), dim3(256), 0, s, x.codes, x.ld, x.scale,
+                               static_cast<int>(c.B), static_cast<int>(groups), order, work);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
         }
@@ -983,11 +989,6 @@ __global__ __launch_bounds__(256) void grad_ready_kernel(ReadyArgs a) {
                                  gridDim.x - a.sums - a.w_blocks);
 }
 
-uint32_t unpack_blocks(int64_t pieces) {
-    const int64_t n = (pieces + 255) / 256;
-    return static_cast<uint32_t>(n < (1 << 20) ? n : 1 << 20);
-}
-
 template <typename T>
 hipError_t grad_ready(const MxGrad &c, ReadyArgs a, int64_t ldn, bool read_w, bool read_x,
                       const int *tops, int *down, hipStream_t s) {
@@ -995,12 +996,12 @@ hipError_t grad_ready(const MxGrad &c, ReadyArgs a, int64_t ldn, bool read_w, bo
     uint32_t x_blocks = 0;
     if (read_w) {
         a.w = mx_unpack_args<T>(c.w, c.M, c.N, ldn, ldn);
-        a.w_blocks = unpack_blocks(a.w.ix.total);
+        a.w_blocks = blocks_for(a.w.ix.total);
         if (__is_same(T, _Float16)) a.w.shift = MxShift{tops, down};
     }
     if (read_x) {
         a.x = mx_unpack_args<T>(c.x, c.B, c.N, ldn, ldn);
-        x_blocks = unpack_blocks(a.x.ix.total);
+        x_blocks = blocks_for(a.x.ix.total);
         if (__is_same(T, _Float16)) a.x.shift = MxShift{tops + kMxTops, down + 1};
     }
     const uint32_t blocks = a.sums + a.w_blocks + x_blocks;
