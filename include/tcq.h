@@ -599,7 +599,8 @@ int tcq_cache_read(const tcq_cache *cache, const tcq_cache_batch *batch, int dty
  *                o_head) values apart
  *   q_heads    : a multiple of the cache's heads, at most 1024
  *   scale      : between 2^-60 and 2^60 (1 / sqrt(dim), as a rule)
- *   workspace  : >= what tcq_cache_attention_workspace_bytes reports
+ *   workspace  : >= what tcq_cache_attention_workspace_bytes reports (never less for more sequences
+ *                or rows)
  * Products of scores are exact and sums fp32; o is rounded once.  Weights are held in fp32 (fp32
  * queries) or to 2^-15 (16-bit ones) where they meet the values and are summed, but to 2^-8 for
  * bf16 queries of sequences of more than 64 rows (a token's query heads to each of the cache's

@@ -1301,6 +1301,13 @@ size_t attention_bytes(int dim, int group, int64_t seqs, int64_t rows) {
     return align_up(static_cast<size_t>(n), 256);
 }
 
+size_t attention_most_bytes(int dim, int group, int64_t seqs, int64_t rows) {
+    if (rows == 0 || seqs == 0) return 0;
+    // (the same rows may come in one sequence)
+    const int64_t n = parts_bytes(dim, few_only(rows, group, 1)) + 8 * plan_words(seqs);
+    return align_up(static_cast<size_t>(n), 256);
+}
+
 int64_t attention_threads(int group, int heads, int64_t seqs, int64_t rows) {
     if (few_only(rows, group, seqs)) return 0;
     return ((rows * group / kLeastRows + seqs) * heads + kTargetLarge) * kManyThreads;

@@ -229,7 +229,7 @@ extern "C" int tcq_cache_attention_workspace_bytes(int dim, int heads, int q_hea
         set_error("%s: bytes is NULL", fn);
         return TCQ_EINVAL;
     }
-    *bytes = attention_bytes(dim, q_heads / heads, seqs, rows);
+    *bytes = attention_most_bytes(dim, q_heads / heads, seqs, rows);
     return TCQ_OK;
 }
 

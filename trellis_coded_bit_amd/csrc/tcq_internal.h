@@ -291,7 +291,9 @@ struct AttentionCall {
     int64_t rows;
     float scale;
 };
+// Of this batch, and the most of it and every smaller one.
 size_t attention_bytes(int dim, int group, int64_t seqs, int64_t rows);
+size_t attention_most_bytes(int dim, int group, int64_t seqs, int64_t rows);
 // Threads of the launch of large tiles (0: there is none), at most.
 int64_t attention_threads(int group, int heads, int64_t seqs, int64_t rows);
 hipError_t launch_attention(const AttentionCall &c, char *ws, hipStream_t s);
