@@ -489,7 +489,8 @@ __device__ __forceinline__ void put(const AttArgs &a, const Tile<BQ> &t, int r, 
 }
 
 // The fragments of query row `r` (this lane's) in terms: place 8 f + v of lane group g holds d =
-// at(f) + v.
+// at(f) + v.  An infinity becomes NaN, as the row's outputs are: scores that are all -inf would
+// pass for keys that it does not see.  (Terms after the first are NaN by themselves there.)
 template <typename T, int D, int TERMS, int BQ, typename At>
 __device__ __forceinline__ void load_query(const AttArgs &a, const Tile<BQ> &t, uint32_t r,
                                            const At &at, s16x8 (&q)[TERMS][D / 32]) {
@@ -502,8 +503,13 @@ __device__ __forceinline__ void load_query(const AttArgs &a, const Tile<BQ> &t, 
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             uint32_t t2[TERMS];
-            terms_of<TERMS>(in ? static_cast<float>(p.v[2 * k]) : 0.0f,
-                            in ? static_cast<float>(p.v[2 * k + 1]) : 0.0f, t2);
+            float v0 = in ? static_cast<float>(p.v[2 * k]) : 0.0f;
+            float v1 = in ? static_cast<float>(p.v[2 * k + 1]) : 0.0f;
+            if constexpr (TERMS == 1) {
+                v0 = __builtin_fmaf(v0, 0.0f, v0);
+                v1 = __builtin_fmaf(v1, 0.0f, v1);
+            }
+            terms_of<TERMS>(v0, v1, t2);
 #pragma unroll
             for (int n = 0; n < TERMS; ++n) w[n][k] = t2[n];
         }
