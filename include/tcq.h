@@ -602,12 +602,14 @@ int tcq_cache_read(const tcq_cache *cache, const tcq_cache_batch *batch, int dty
  *   workspace  : >= what tcq_cache_attention_workspace_bytes reports (never less for more sequences
  *                or rows)
  * Products of scores are exact and sums fp32; o is rounded once.  Weights are held in fp32 (fp32
- * queries) or to 2^-15 (16-bit ones) where they meet the values and are summed, but to 2^-8 for
- * bf16 queries of sequences of more than 64 rows (a token's query heads to each of the cache's
- * count as rows) in batches of more than 16 on average: those outputs are about 1.4 times as far
- * from the exact ones as their own rounding would put them.  (As bf16 numbers, values below 2^-133
- * are lost: scale bytes below 3 in TCQ_FP8.)  How keys are shared out among workgroups depends on
- * the batch's lengths, and with it the last bits of o; the same call gives the same bits.
+ * queries) or to 2^-15 (16-bit ones) where they meet the values and are summed, but to 2^-11 of
+ * themselves or 2^-32 of the row's largest for bf16 queries of sequences of more than 64 rows (a
+ * token's query heads to each of the cache's count as rows) in batches of more than 16 on average
+ * (there too to 2^-15, in about 2.5 times the time, where the scale bytes of a head's values lie
+ * more than 15 below or 7 above those of a run's first keys).  (As bf16 numbers, values below
+ * 2^-133 are lost: scale bytes below 3 in TCQ_FP8.)  How keys are shared out among workgroups
+ * depends on the batch's lengths, and with it the last bits of o; the same call gives the same
+ * bits.
  * (TCQ_FP8's NaN codes, which tcq_cache_write never writes, are not told apart like groups: a
  * value's may reach queries of its sequence that do not see it.)
  * Outputs must not overlap inputs, what lies between the heads of a row included (TCQ_EINVAL).

@@ -5,11 +5,11 @@
 // a key is read once for all of them.
 //
 // Every code times its scale is a bf16 number, so keys and values are multiplied as bf16 with
-// exact products and fp32 sums.  q and p are held in terms of bf16 whose sum they are: q exactly, in
-// one for bf16, two for fp16 and three for fp32.  p in three for fp32 (exact) and in two for 16-bit
-// queries (to 2^-15, far below the output's own rounding), but for bf16 queries in the larger tiles
-// in one (to 2^-8, half a step of the output's type): see attend_many_kernel.  The sum of p is
-// that of the rounded ones.
+// exact products and fp32 sums.  q and p are held in terms of bf16 whose sum they are: q exactly,
+// in one for bf16, two for fp16 and three for fp32; p in three for fp32 (exact) and in two for
+// 16-bit queries (to 2^-15, far below the output's own rounding), but for bf16 queries in the
+// larger tiles as one fp16 number (to 2^-11), beside values in fp16: see attend_many.  The sum of
+// p is that of the rounded ones.
 //
 // Scores are computed transposed, S^T = K Q^T: a lane holds four keys of one query row, the same
 // row in every instruction, so a row's maximum and sum are the lane's own but for three other
@@ -17,10 +17,10 @@
 // keys is the one the lanes hold them in, and V is read across through LDS in the same order.
 //
 // Work is cut into items (sequence, head, tile of query rows, run of keys) by every workgroup, or
-// by a kernel before for many sequences, from the lengths on the device, so that the host need not
-// know them: runs are as long as lets
-// about the target number of them remain.  A tile with one run writes its outputs, others their share, and
-// a second kernel joins shares in the order of the runs.
+// by a kernel before for many sequences, from the lengths on the device, so that the host need
+// not know them: runs are as long as lets about the target number of them remain.  A tile with
+// one run writes its outputs, others their share, and a second kernel joins shares in the order
+// of the runs.
 #include <hip/hip_runtime.h>
 
 #include "cache_device.h"
@@ -46,6 +46,7 @@ struct AttArgs {
     float factor, factor_low;   // scale log2(e), and what it lacks
     float *part;                // shares: [slot][rows of a tile][dim], then maxima and sums
     uint32_t slots;
+    int *far;                   // whether attend_far_kernel has work (NULL: it does not come)
     uint32_t *plan;             // see plan_kernel; NULL: workgroups scan the sequences themselves
     int both;                   // tiles of 16 rows serve sequences of up to kFewRows rows only,
                                 // larger tiles the others (0: this kernel serves every sequence)
@@ -330,7 +331,20 @@ __device__ __forceinline__ void terms_of(float a, float b, uint32_t (&w)[TERMS])
             __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
 }
 
-// Terms of q, and of p in the larger tiles.
+// The same as numbers N: one fp16 number, or bf16 terms.
+template <typename N, int TERMS>
+__device__ __forceinline__ void numbers_of(float a, float b, uint32_t (&w)[TERMS]) {
+    if constexpr (__is_same(N, _Float16)) {
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+        static_assert(TERMS == 1, "one number");
+        w[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), f16x2));
+    } else {
+        terms_of<TERMS>(a, b, w);
+    }
+}
+
+// Terms of q, and of p in the larger tiles (bf16: see attend_many).
 template <typename T>
 constexpr int terms() {
     return sizeof(T) == 4 ? 3 : (__is_same(T, _Float16) ? 2 : 1);
@@ -339,6 +353,20 @@ constexpr int terms() {
 template <typename T>
 constexpr int few_weight_terms() {
     return sizeof(T) == 4 ? 3 : 2;
+}
+
+// One and infinity as bits of a 16-bit type.
+template <typename N>
+constexpr short kOne = __is_same(N, _Float16) ? 0x3C00 : 0x3F80;
+template <typename N>
+constexpr short kInf = __is_same(N, _Float16) ? 0x7C00 : 0x7F80;
+
+// One 16 x 16 product over 32 keys or dims, smallest term first.
+template <typename N, int TERMS>
+__device__ __forceinline__ f32x4 mma_terms(const s16x8 &x, const s16x8 (&y)[TERMS], f32x4 c) {
+#pragma unroll
+    for (int n = TERMS - 1; n >= 0; --n) c = gemm::Traits<N>::mma(x, y[n], c);
+    return c;
 }
 
 // f over the four lanes that hold a query row's keys: lanes l, l ^ 16, l ^ 32,
@@ -380,12 +408,11 @@ struct Softmax {
         top = -__builtin_inff();
         sum = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    template <int TERMS>
+    template <typename N, int TERMS>
     __device__ __forceinline__ void add(const s16x8 (&p)[TERMS]) {
-        constexpr short kOne = 0x3F80;
-        const s16x8 ones = {kOne, kOne, kOne, kOne, kOne, kOne, kOne, kOne};
-#pragma unroll
-        for (int n = TERMS - 1; n >= 0; --n) sum = gemm::Traits<__bf16>::mma(ones, p[n], sum);
+        constexpr short o = kOne<N>;
+        const s16x8 ones = {o, o, o, o, o, o, o, o};
+        sum = mma_terms<N, TERMS>(ones, p, sum);
     }
     static __device__ __forceinline__ float safe(float t) {
         return t == -__builtin_inff() ? 0.0f : t;
@@ -443,12 +470,17 @@ __device__ __forceinline__ s16x8 read_across(const char *at) {
     return out;
 }
 
-// 16 bytes of codes (16 of fp8, 32 of fp4) to bf16 words.
-template <int FMT>
+// 16 bytes of codes (16 of fp8, 32 of fp4) to words of two 16-bit numbers.
+template <int FMT, typename N = __bf16>
 __device__ __forceinline__ void decode16(const u32x4 &q, float s, uint32_t *w) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        mx::decode_word_bf16<FMT>(q[j], s, w + (FMT == TCQ_FP4 ? 4 : 2) * j);
+    for (int j = 0; j < 4; ++j) {
+        uint32_t *to = w + (FMT == TCQ_FP4 ? 4 : 2) * j;
+        if constexpr (__is_same(N, _Float16))
+            mx::decode_word_f16<FMT>(q[j], s, to);
+        else
+            mx::decode_word_bf16<FMT>(q[j], s, to);
+    }
 }
 
 // ---------------------------------------------------------------- outputs
@@ -544,31 +576,23 @@ __device__ __forceinline__ HeadCache head_cache(const AttArgs &a, int head) {
     return h;
 }
 
-// One 16 x 16 product over 32 keys or dims, smallest term first.
-template <int TERMS>
-__device__ __forceinline__ f32x4 mma_terms(const s16x8 &x, const s16x8 (&y)[TERMS], f32x4 c) {
-#pragma unroll
-    for (int n = TERMS - 1; n >= 0; --n) c = gemm::Traits<__bf16>::mma(x, y[n], c);
-    return c;
-}
-
 // acc += x p for a tile of values among which some stand for NaN, where a row does not see every key
 // (bit i of sees: the key in the lane's place i): a NaN reaches the rows that see its key, whatever
 // p, and no other (0 times NaN would).  The rows it reaches are those whose count of NaN keys, the
 // product of ones, is not zero.
-template <int TERMS>
+template <typename N, int TERMS>
 __device__ __forceinline__ void add_wild(const s16x8 &x, const s16x8 (&p)[TERMS], uint32_t sees,
                                          f32x4 &acc) {
     s16x8 clean, nan, ones;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const bool bad = (x[i] & 0x7FFF) > 0x7F80;
+        const bool bad = (x[i] & 0x7FFF) > kInf<N>;
         clean[i] = bad ? 0 : x[i];
-        nan[i] = bad ? 0x3F80 : 0;
-        ones[i] = sees >> i & 1 ? 0x3F80 : 0;
+        nan[i] = bad ? kOne<N> : 0;
+        ones[i] = sees >> i & 1 ? kOne<N> : 0;
     }
-    const f32x4 n = gemm::Traits<__bf16>::mma(nan, ones, f32x4{0.f, 0.f, 0.f, 0.f});
-    acc = mma_terms<TERMS>(clean, p, acc);
+    const f32x4 n = gemm::Traits<N>::mma(nan, ones, f32x4{0.f, 0.f, 0.f, 0.f});
+    acc = mma_terms<N, TERMS>(clean, p, acc);
 #pragma unroll
     for (int v = 0; v < 4; ++v)
         if (n[v] != 0.0f) acc[v] = __builtin_nanf("");
@@ -612,6 +636,7 @@ attend_few_kernel(AttArgs a) {
     __shared__ float tops[4][16], sums[4][16];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (a.far && blockIdx.x == 0 && tid == 0) *a.far = 0;  // (before the larger tiles' launch)
     Tile<BQ> tile;
     if (!tile.init(a, blockIdx.x, lane)) return;
     const HeadCache hc = head_cache<FMT, D>(a, tile.head);
@@ -718,7 +743,7 @@ attend_few_kernel(AttArgs a) {
                 s16x8 y[TERMS];
 #pragma unroll
                 for (int n = 0; n < TERMS; ++n) y[n] = q[n][f];
-                s[h] = mma_terms<TERMS>(x, y, s[h]);
+                s[h] = mma_terms<__bf16, TERMS>(x, y, s[h]);
             }
         }
         // values into LDS
@@ -780,16 +805,17 @@ attend_few_kernel(AttArgs a) {
 #pragma unroll
             for (int n = 0; n < PT; ++n) pf[n] = __builtin_bit_cast(s16x8, w[n]);
         }
-        sm.add(pf);
+        sm.add<__bf16>(pf);
         __builtin_amdgcn_wave_barrier();
         if (__builtin_expect(__any(wild) && __any(sees != 0xFFu), 0)) {
 #pragma unroll
             for (int t = 0; t < kTiles; ++t)
-                add_wild<PT>(read_across<D * 2>(vt + (from_lds ^ (t * 32))), pf, sees, acc[t]);
+                add_wild<__bf16, PT>(read_across<D * 2>(vt + (from_lds ^ (t * 32))), pf, sees, acc[t]);
         } else {
 #pragma unroll
             for (int t = 0; t < kTiles; ++t)
-                acc[t] = mma_terms<PT>(read_across<D * 2>(vt + (from_lds ^ (t * 32))), pf, acc[t]);
+                acc[t] = mma_terms<__bf16, PT>(read_across<D * 2>(vt + (from_lds ^ (t * 32))), pf,
+                                               acc[t]);
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -834,15 +860,35 @@ attend_few_kernel(AttArgs a) {
 // behind 4000 to 16384, 32 query heads over 8 of 128, bf16, 1240 us (882 TF) with the matrix cores
 // busy for 38 % of the clocks, VALU for 42 and LDS for 37.  (Without the third of the latter that
 // are bank conflicts of the keys' reads it took 3 % more.)
-//   bf16 queries' weights meet the values as one bf16 number, as wide as the values: outputs are then
-// 1.4 times as far from those of float64 as their own rounding puts them (2.34e-3 of their norm,
-// 1.66e-3 with two terms).  Two terms took 1740 us there, at 64 dims 998 instead of 812, at 256
-// dims (four chunks of 511 to 1024 behind 4000 to 8192, 16 query heads over 4) 702 instead of 634.
-template <typename T, int D, int FMT, int NW, int NQ>
-__global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
+//   bf16 queries' weights meet the values as one fp16 number each, lifted by 2^7, so to 2^-11 of
+// themselves or 2^-32 of the row's largest; values as the fp16 numbers that they are relative to
+// the first tile's largest scale byte.  Outputs are then as near float64's as their own rounding
+// and one per cent of it (1.67e-3 of their norm, 1.66e-3 with exact weights).  The four chunks
+// take 1283 us so, 1240 with weights of one bf16 number (2^-8: 2.34e-3) and 1740 with two; 64
+// dims 830, 816 and 998; 256 dims (four chunks of 511 to 1024 behind 4000 to 8192, 16 query heads
+// over 4) 605, 632 and 702.  Values whose scale bytes lie further apart than fp16's range:
+// attend_far_kernel.
+// What a workgroup's threads share.
+struct ManyLds {
+    char *kt, *vt;      // two tiles of keys, three of values
+    // of tile i in place i mod 4: the keys that are not there, whether a value stands for NaN
+    unsigned long long *absent_of;
+    int *wild_of;
+    int *top_of;        // the first tile's largest scale byte
+    int *far_of;        // whether a value is far from it
+};
+template <int D>
+constexpr int kManyKeys = D == 256 ? 32 : 64;      // of a tile
+
+// Item `index`, values and weights as numbers N, the weights in PT terms.  False: N is fp16, and
+// some value is no fp16 number; nothing is written then.
+template <typename T, typename N, int PT, int D, int FMT, int NW, int NQ>
+__device__ __forceinline__ bool attend_many(const AttArgs &a, const ManyLds &lds, uint32_t index,
+                                            int tid) {
     constexpr int TERMS = terms<T>();
+    constexpr bool kHalf = __is_same(N, _Float16);
     constexpr int NT = NW * 64, BQ = NW * NQ * 16;
-    constexpr int KT = D == 256 ? 32 : 64;                     // keys of a tile
+    constexpr int KT = kManyKeys<D>;
     constexpr int kSub = KT / 16, kPairs = KT / 32;
     constexpr int kRow = mx::bytes<FMT>(D);
     constexpr int kLanes = kRow / 16;
@@ -852,16 +898,14 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
     constexpr int kLoads = (kPieces + NT - 1) / NT;
     constexpr int kWords = FMT == TCQ_FP4 ? 16 : 8;            // of bf16 pairs to a piece
     constexpr int kTileBytes = KT * D * 2;
-    __shared__ __align__(16) char kt[2 * kTileBytes];
-    __shared__ __align__(16) char vt[3 * kTileBytes];
-    // of tile i in place i mod 4: the keys that are not there, whether a value stands for NaN
-    __shared__ unsigned long long absent_of[4];
-    __shared__ int wild_of[4];
-    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
+    // (fp16 weights, at most 2^8 past their reference, are lifted to below 2^15)
+    constexpr float kLift = kHalf ? 7.0f : 0.0f;
+    char *const kt = lds.kt, *const vt = lds.vt;
+    const int lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool late = wave >= 4;
     Tile<BQ> tile;
-    if (!tile.init(a, blockIdx.x, lane)) return;
+    if (!tile.init(a, index, lane)) return true;
     const HeadCache hc = head_cache<FMT, D>(a, tile.head);
     const uint32_t r0 = tile.r0 + wave * (NQ * 16);
     const int seen_by_all = tile.sees(a, r0);
@@ -930,45 +974,7 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
     const int v_to = Units<D * 2>::row(row) ^ (part * (kWords / 8) * 32);
     const int k_from = l16 * (D * 2) + (g ^ (l16 & 7)) * 16;
     const int v_from = Units<D * 2>::across(lane);
-    // The codes at hand, tile i's, into LDS.
-    auto stage = [&](int k_at, int v_at, int i) {
-        bool wild = false;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            if (kPieces % NT == 0 || tid < kPieces) {
-                if (!(now.there >> j & 1)) {
-                    now.v[j] = u32x4{0, 0, 0, 0};
-                    now.ve[j] = 127;
-                    atomicOr(&absent_of[i & 3], 1ull << (row + j * (NT / kLanes)));
-                }
-                char *k = kt + k_at + j * (NT / kLanes) * (D * 2);
-                char *v = vt + v_at + j * (NT / kLanes) * (D * 2);
-                uint32_t w[kWords];
-                decode16<FMT>(now.k[j], mx::scale_of(now.ke[j]), w);
-#pragma unroll
-                for (int u = 0; u < kWords / 4; ++u)
-                    *reinterpret_cast<u32x4 *>(k + (k_to ^ (u * 16))) =
-                        u32x4{w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]};
-                wild |= now.ve[j] == 255;
-                decode16<FMT>(now.v[j], mx::scale_of(now.ve[j]), w);
-#pragma unroll
-                for (int u = 0; u < kWords / 8; ++u) {
-                    u32x4 *d = reinterpret_cast<u32x4 *>(v + (v_to ^ (u * 32)));
-                    d[0] = u32x4{w[8 * u], w[8 * u + 1], w[8 * u + 2], w[8 * u + 3]};
-                    d[1] = u32x4{w[8 * u + 4], w[8 * u + 5], w[8 * u + 6], w[8 * u + 7]};
-                }
-            }
-        }
-        if (wild) wild_of[i & 3] = 1;
-    };
 
-    if (tid < 4) absent_of[tid] = 0, wild_of[tid] = 0;
-    uint32_t base = tile.begin;
-    if (base < tile.end) {
-        find(base);
-        load(base);
-        find(base + KT);
-    }
     s16x8 q[NQ][TERMS][kGroups];
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -982,20 +988,102 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) acc[n][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    int ref = 127;   // values are taken times 2^(127 - ref)
+    // The values at hand of piece j into LDS.
+    auto put_values = [&](int j, float scale, int v_at) {
+        char *v = vt + v_at + j * (NT / kLanes) * (D * 2);
+        uint32_t w[kWords];
+        decode16<FMT, N>(now.v[j], scale, w);
+#pragma unroll
+        for (int u = 0; u < kWords / 8; ++u) {
+            u32x4 *d = reinterpret_cast<u32x4 *>(v + (v_to ^ (u * 32)));
+            d[0] = u32x4{w[8 * u], w[8 * u + 1], w[8 * u + 2], w[8 * u + 3]};
+            d[1] = u32x4{w[8 * u + 4], w[8 * u + 5], w[8 * u + 6], w[8 * u + 7]};
+        }
+    };
+    // The codes at hand, tile i's, into LDS.
+    auto stage = [&](int k_at, int v_at, int i) {
+        bool rare = false;   // values that stand for NaN, or far from the first tile's
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            if (kPieces % NT == 0 || tid < kPieces) {
+                if (!(now.there >> j & 1)) {
+                    now.v[j] = u32x4{0, 0, 0, 0};
+                    now.ve[j] = 127;
+                    atomicOr(&lds.absent_of[i & 3], 1ull << (row + j * (NT / kLanes)));
+                }
+                char *k = kt + k_at + j * (NT / kLanes) * (D * 2);
+                uint32_t w[kWords];
+                decode16<FMT>(now.k[j], mx::scale_of(now.ke[j]), w);
+#pragma unroll
+                for (int u = 0; u < kWords / 4; ++u)
+                    *reinterpret_cast<u32x4 *>(k + (k_to ^ (u * 16))) =
+                        u32x4{w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]};
+                const int e = now.ve[j] - (kHalf ? ref - 127 : 0);
+                rare |= kHalf ? static_cast<uint32_t>(e - 127 - mx::kLowF16<FMT>) >
+                                    mx::kHighF16<FMT> - mx::kLowF16<FMT>
+                              : e == 255;
+                put_values(j, mx::scale_of(e), v_at);
+            }
+        }
+        if (__builtin_expect(__any(rare), 0)) {
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                if (kPieces % NT != 0 && tid >= kPieces) continue;
+                const int e = now.ve[j], by = e - ref;
+                if (e == 255) lds.wild_of[i & 3] = 1;
+                if constexpr (kHalf) {
+                    if (by >= mx::kLowF16<FMT> && by <= mx::kHighF16<FMT>) continue;
+                    // (codes of zero are that whatever the scale)
+                    constexpr uint32_t kSize = FMT == TCQ_FP4 ? 0x77777777u : 0x7F7F7F7Fu;
+                    const u32x4 c = now.v[j];
+                    if (e != 255 && ((c[0] | c[1] | c[2] | c[3]) & kSize) != 0) *lds.far_of = 1;
+                    put_values(j, mx::scale_of(e == 255 ? 255 : 127), v_at);
+                }
+            }
+        }
+    };
+
+    if (tid < 4) lds.absent_of[tid] = 0, lds.wild_of[tid] = 0;
+    if (kHalf && tid == 0) *lds.top_of = 0, *lds.far_of = 0;
+    uint32_t base = tile.begin;
+    if (base < tile.end) {
+        find(base);
+        load(base);
+        find(base + KT);
+    }
     __syncthreads();
+    if (kHalf) {
+        if (base < tile.end) {
+            int top = 0;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                if ((now.there >> j & 1) && now.ve[j] != 255 && now.ve[j] > top)
+                    top = now.ve[j];
+            for (int d = 32; d; d >>= 1) {
+                const int o = __shfl_xor(top, d);
+                top = top > o ? top : o;
+            }
+            if (lane == 0) atomicMax(lds.top_of, top);
+        }
+        __syncthreads();
+        // (values of zero say nothing: as for a largest one of 2)
+        ref = __builtin_amdgcn_readfirstlane(*lds.top_of);
+        ref = ref ? ref : (FMT == TCQ_FP4 ? 126 : 120);
+    }
     if (base < tile.end) {
         stage(0, 0, 0);
         load(base + KT);
         find(base + 2 * KT);
     }
     __syncthreads();
-    // Tile i is staged before meeting i - 1.  After meeting i the early waves are done with it, the
-    // late ones have its scores alone, so its keys may be overwritten (by tile i + 2) then, its
-    // values (by tile i + 3) and marks after meeting i + 1.
+    // Tile i is staged before meeting i - 1.  After meeting i the early waves are done with it,
+    // the late ones have its scores alone, so its keys may be overwritten (by tile i + 2) then,
+    // its values (by tile i + 3) and marks after meeting i + 1.
     int v_now = 0, v_next = kTileBytes, v_last = 2 * kTileBytes;
     for (int i = 0; base < tile.end; base += KT, ++i) {
         const int k_now = i & 1 ? kTileBytes : 0;
-        if (tid == 0) absent_of[(i + 2) & 3] = 0, wild_of[(i + 2) & 3] = 0;
+        if (tid == 0) lds.absent_of[(i + 2) & 3] = 0, lds.wild_of[(i + 2) & 3] = 0;
         __builtin_amdgcn_s_setprio(1);
         // scores
         f32x4 s[NQ][kSub];
@@ -1012,7 +1100,7 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
                     s16x8 y[TERMS];
 #pragma unroll
                     for (int m = 0; m < TERMS; ++m) y[m] = q[n][m][f];
-                    s[n][h] = mma_terms<TERMS>(x, y, s[n][h]);
+                    s[n][h] = mma_terms<__bf16, TERMS>(x, y, s[n][h]);
                 }
             }
         }
@@ -1021,9 +1109,9 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
         load(base + 2 * KT);
         find(base + 3 * KT);
         if (late) __syncthreads();
-        const uint64_t absent = absent_of[i & 3];
-        const bool wild = wild_of[i & 3] != 0;
-        s16x8 pf[NQ][kPairs][TERMS];
+        const uint64_t absent = lds.absent_of[i & 3];
+        const bool wild = lds.wild_of[i & 3] != 0;
+        s16x8 pf[NQ][kPairs][PT];
         uint32_t sees[NQ];
         const bool partial = absent != 0 || static_cast<int64_t>(base) + KT - 1 > seen_by_all;
 #pragma unroll
@@ -1043,33 +1131,38 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
                     if (!(sees[n] >> i & 1)) s[n][i / 4][i % 4] = -__builtin_inff();
             }
             float alpha;
-            if (sm[n].grow(row_max(largest<4 * kSub>(s[n])) * a.factor, alpha)) {
+            const float most = row_max(largest<4 * kSub>(s[n]));
+            if (sm[n].grow(kHalf ? __builtin_fmaf(most, a.factor, -kLift) : most * a.factor,
+                           alpha)) {
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) acc[n][t] *= alpha;
             }
-            const float ref = Softmax::safe(sm[n].top);
+            const float top = Softmax::safe(sm[n].top);
             float p[4 * kSub];
 #pragma unroll
             for (int i = 0; i < 4 * kSub; ++i)
-                p[i] = weight<TERMS>(s[n][i / 4][i % 4], a.factor, a.factor_low, ref);
+                p[i] = weight<PT>(s[n][i / 4][i % 4], a.factor, a.factor_low, top);
 #pragma unroll
             for (int k2 = 0; k2 < kPairs; ++k2) {
-                u32x4 w[TERMS];
+                u32x4 w[PT];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    uint32_t t[TERMS];
-                    terms_of<TERMS>(p[8 * k2 + 2 * k], p[8 * k2 + 2 * k + 1], t);
+                    uint32_t t[PT];
+                    numbers_of<N, PT>(p[8 * k2 + 2 * k], p[8 * k2 + 2 * k + 1], t);
 #pragma unroll
-                    for (int m = 0; m < TERMS; ++m) w[m][k] = t[m];
+                    for (int m = 0; m < PT; ++m) w[m][k] = t[m];
                 }
 #pragma unroll
-                for (int m = 0; m < TERMS; ++m) pf[n][k2][m] = __builtin_bit_cast(s16x8, w[m]);
+                for (int m = 0; m < PT; ++m) pf[n][k2][m] = __builtin_bit_cast(s16x8, w[m]);
             }
         }
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int k2 = 0; k2 < kPairs; ++k2) sm[n].add(pf[n][k2]);
+            for (int k2 = 0; k2 < kPairs; ++k2) sm[n].template add<N>(pf[n][k2]);
+        const auto value = [&](int t, int k2) {
+            return read_across<D * 2>(vt + ((v_now + v_from) ^ (t * 32)) + 32 * k2 * (D * 2));
+        };
         if (__builtin_expect(wild && partial, 0)) {
 #pragma unroll
             for (int t = 0; t < kTiles; ++t)
@@ -1077,18 +1170,18 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
                 for (int k2 = 0; k2 < kPairs; ++k2)
 #pragma unroll
                     for (int n = 0; n < NQ; ++n)
-                        add_wild<TERMS>(read_across<D * 2>(vt + ((v_now + v_from) ^ (t * 32)) + 32 * k2 * (D * 2)), pf[n][k2],
-                                        sees[n] >> (8 * k2), acc[n][t]);
+                        add_wild<N, PT>(value(t, k2), pf[n][k2], sees[n] >> (8 * k2),
+                                        acc[n][t]);
         } else {
             __builtin_amdgcn_s_setprio(1);
 #pragma unroll
             for (int t = 0; t < kTiles; ++t) {
 #pragma unroll
                 for (int k2 = 0; k2 < kPairs; ++k2) {
-                    const s16x8 x = read_across<D * 2>(vt + ((v_now + v_from) ^ (t * 32)) + 32 * k2 * (D * 2));
+                    const s16x8 x = value(t, k2);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n)
-                        acc[n][t] = mma_terms<TERMS>(x, pf[n][k2], acc[n][t]);
+                        acc[n][t] = mma_terms<N, PT>(x, pf[n][k2], acc[n][t]);
                 }
             }
             __builtin_amdgcn_s_setprio(0);
@@ -1099,13 +1192,63 @@ __global__ __launch_bounds__(NW * 64) void attend_many_kernel(AttArgs a) {
         v_now = v_next;
         v_next = v;
     }
+    // (every tile was staged before the last meeting)
+    if (kHalf && __builtin_expect(*lds.far_of != 0, 0)) return false;
+    if constexpr (kHalf) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                    acc[n][t][v] = __builtin_amdgcn_ldexpf(acc[n][t][v], ref - 127);
+    }
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
             put<T, BQ, D>(a, tile, wave * (NQ * 16) + 16 * n + l16, 16 * t + 4 * g, acc[n][t],
                           sm[n].top, sm[n].sum[0]);
+    return true;
 }
+
+template <typename T, int D>
+constexpr int many_waves() {
+    return D == 64 && sizeof(T) == 2 ? 4 : 2;
+}
+#define TCQ_MANY_LDS                                                                          \
+    constexpr int kTileBytes = kManyKeys<D> * D * 2;                                          \
+    __shared__ __align__(16) char kt[2 * kTileBytes];                                         \
+    __shared__ __align__(16) char vt[3 * kTileBytes];                                         \
+    __shared__ unsigned long long absent_of[4];                                               \
+    __shared__ int wild_of[4];                                                                \
+    __shared__ int top_of, far_of;                                                            \
+    const ManyLds lds{kt, vt, absent_of, wild_of, &top_of, &far_of}
+template <typename T, int D, int FMT, int NW, int NQ>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(many_waves<T, D>()))) void
+attend_many_kernel(AttArgs a) {
+    TCQ_MANY_LDS;
+    if constexpr (terms<T>() == 1) {
+        if (!attend_many<T, _Float16, 1, D, FMT, NW, NQ>(a, lds, blockIdx.x, threadIdx.x) &&
+            threadIdx.x == 0)
+            *a.far = 1;
+    } else {
+        attend_many<T, __bf16, terms<T>(), D, FMT, NW, NQ>(a, lds, blockIdx.x, threadIdx.x);
+    }
+}
+// All items again with bf16 values and weights of two terms, where a workgroup met values far
+// from one another (the four chunks then take 3350 us), otherwise nothing (2 us).  As another half
+// of attend_many_kernel it cost that one up to 9 %, by the order that its loop got.
+template <typename T, int D, int FMT, int NW, int NQ>
+__global__ __launch_bounds__(NW * 64) void attend_far_kernel(AttArgs a, uint32_t items) {
+    TCQ_MANY_LDS;
+    if (*a.far == 0) return;
+    for (uint32_t i = blockIdx.x; i < items; i += gridDim.x) {
+        attend_many<T, __bf16, 2, D, FMT, NW, NQ>(a, lds, i, threadIdx.x);
+        __syncthreads();
+    }
+}
+#undef TCQ_MANY_LDS
 
 // ---------------------------------------------------------------- join of shares
 
@@ -1212,6 +1355,7 @@ constexpr int kSlotsFew = 2 * kTargetSmall, kSlotsMany = 2 * kTargetLarge;
 
 constexpr int kLeastRows = 128, kMostRows = 256;   // of a larger tile
 constexpr int kManyThreads = 512;                  // and its threads
+constexpr uint32_t kFarGrid = 512;
 int64_t slot_bytes(int bq, int dim) { return int64_t{bq} * (dim + 2) * 4; }
 
 // Of the shares, a multiple of 16.
@@ -1241,6 +1385,10 @@ hipError_t attend_as(const AttArgs &base, char *ws, hipStream_t s) {
         if (e != hipSuccess) return e;
     }
     many.slots = kSlotsMany;
+    constexpr bool kFar = terms<T>() == 1;
+    if (kFar && !only)
+        few.far = many.far =
+            reinterpret_cast<int *>(ws + parts_bytes(D, only) + 8 * plan_words(base.b.seqs));
     // tiles of all sequences: whole ones of the rows, and a part of one for each
     const int64_t qrows = base.rows * base.group;
     const int64_t few_tiles = qrows / kSmallRows + base.b.seqs;
@@ -1258,6 +1406,14 @@ hipError_t attend_as(const AttArgs &base, char *ws, hipStream_t s) {
                            dim3(NW * 64), 0, s, many);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
+        if constexpr (kFar) {
+            const uint32_t items = static_cast<uint32_t>(many_tiles * heads + kTargetLarge);
+            hipLaunchKernelGGL((attend_far_kernel<T, D, FMT, NW, NQ>),
+                               dim3(items < kFarGrid ? items : kFarGrid), dim3(NW * 64), 0, s,
+                               many, items);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
     }
     // (a pair of tile and head with several runs has two at least)
     const auto blocks = [&](int64_t n, int slots, int rows) {
@@ -1303,14 +1459,16 @@ hipError_t attend(const AttArgs &a, char *ws, hipStream_t s) {
 
 size_t attention_bytes(int dim, int group, int64_t seqs, int64_t rows) {
     if (rows == 0 || seqs == 0) return 0;
-    const int64_t n = parts_bytes(dim, few_only(rows, group, seqs)) + 8 * plan_words(seqs);
+    const bool few = few_only(rows, group, seqs);
+    const int64_t n = parts_bytes(dim, few) + 8 * plan_words(seqs) + (few ? 0 : sizeof(int));
     return align_up(static_cast<size_t>(n), 256);
 }
 
 size_t attention_most_bytes(int dim, int group, int64_t seqs, int64_t rows) {
     if (rows == 0 || seqs == 0) return 0;
     // (the same rows may come in one sequence)
-    const int64_t n = parts_bytes(dim, few_only(rows, group, 1)) + 8 * plan_words(seqs);
+    const bool few = few_only(rows, group, 1);
+    const int64_t n = parts_bytes(dim, few) + 8 * plan_words(seqs) + (few ? 0 : sizeof(int));
     return align_up(static_cast<size_t>(n), 256);
 }
 

@@ -109,5 +109,23 @@ __device__ __forceinline__ void decode_word_bf16(uint32_t w, float s, uint32_t *
     }
 }
 
+// The same in fp16: exact for scales of 2^-23 .. 2^13 (fp4) or 2^-15 .. 2^7 (fp8).
+template <int FMT>
+__device__ __forceinline__ void decode_word_f16(uint32_t w, float s, uint32_t *v) {
+    if constexpr (FMT == TCQ_FP4) {
+        v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0));
+        v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1));
+        v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2));
+        v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3));
+    } else {
+        v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, false));
+        v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, true));
+    }
+}
+template <int FMT>
+constexpr int kLowF16 = FMT == TCQ_FP4 ? -23 : -15;
+template <int FMT>
+constexpr int kHighF16 = FMT == TCQ_FP4 ? 13 : 7;
+
 }  // namespace mx
 }  // namespace tcq
