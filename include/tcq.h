@@ -558,9 +558,9 @@ typedef struct {
  *   lens   : device, seqs: the sequences' lengths, new tokens included
  *   starts : device, seqs + 1, not decreasing, from 0 to at most the call's rows
  * Sequences may be empty or have no new tokens.  Rows of the call behind starts[seqs] belong to
- * nobody: they are not written, and what they hold is without effect.  A token whose position is negative or past width x
- * page, or whose page number is not below `pages` (-1, for instance), is nowhere: it is not
- * written, reads as zeros and is seen by no query.
+ * nobody: they are not written, and what they hold is without effect.  A token whose position is
+ * negative or past width x page, or whose page number is not below `pages` (-1, for instance), is
+ * nowhere: it is not written, reads as zeros and is seen by no query.
  */
 typedef struct {
     const int32_t *table;
@@ -575,7 +575,8 @@ typedef struct {
  * tcq_cache_read  -- the values that the places of the batch's tokens stand for: with starts the
  * running sum of lens, whole sequences.
  *   dtype         : tcq_dtype of k and v
- *   k, v          : device, rows x heads vectors, k_row and k_head (v_row, v_head) values apart
+ *   k, v          : device, rows x heads vectors, k_row and k_head (v_row, v_head) values apart:
+ *                   heads at least dim, rows at least what a row's heads extend over
  *   rows          : the call's rows, at most 2^23
  * Outputs must not overlap inputs or one another, what lies between the heads of a row included
  * (TCQ_EINVAL).  rows == 0 is a no-op.
@@ -595,8 +596,8 @@ int tcq_cache_read(const tcq_cache *cache, const tcq_cache_batch *batch, int dty
  * for each of q_heads query heads; head h reads the cache's head h / (q_heads / heads).  A query
  * that sees no key gives zeros; a key or value group that stands for NaN reaches only the
  * queries that see it.
- *   q, o       : device, rows x q_heads vectors of dim values of type dtype, q_row and q_head (o_row,
- *                o_head) values apart
+ *   q, o       : device, rows x q_heads vectors of dim values of type dtype, q_row and q_head
+ *                (o_row, o_head) values apart, as in tcq_cache_write
  *   q_heads    : a multiple of the cache's heads, at most 1024
  *   scale      : between 2^-60 and 2^60 (1 / sqrt(dim), as a rule)
  *   workspace  : >= what tcq_cache_attention_workspace_bytes reports (never less for more sequences
@@ -607,7 +608,8 @@ int tcq_cache_read(const tcq_cache *cache, const tcq_cache_batch *batch, int dty
  * token's query heads to each of the cache's count as rows) in batches of more than 16 on average
  * (there too to 2^-15, in about 2.5 times the time, where the scale bytes of a head's values lie
  * more than 15 below or 7 above those of a run's first keys).  (As bf16 numbers, values below
- * 2^-133 are lost: scale bytes below 3 in TCQ_FP8.)  How keys are shared out among workgroups
+ * 2^-133 are lost: scale bytes below 3 in TCQ_FP8.  Values of 2^120 over the number of keys and
+ * more may overflow the sums.)  How keys are shared out among workgroups
  * depends on the batch's lengths, and with it the last bits of o; the same call gives the same
  * bits.
  * (TCQ_FP8's NaN codes, which tcq_cache_write never writes, are not told apart like groups: a
@@ -616,7 +618,8 @@ int tcq_cache_read(const tcq_cache *cache, const tcq_cache_batch *batch, int dty
  * rows == 0 is a no-op.
  * Errors: TCQ_EINVAL, TCQ_EUNSUPPORTED (the cache's limits, and batches whose launches would not
  * fit: rows x q_heads / 16 + seqs x heads of 2^24 - 4096 or, with more than 16 query rows to a
- * sequence on average, rows x q_heads / 128 + seqs x heads of 2^23 - 256), TCQ_EWORKSPACE, TCQ_EHIP.
+ * sequence on average, rows x q_heads / 128 + seqs x heads of 2^23 - 256), TCQ_EWORKSPACE,
+ * TCQ_EHIP.
  */
 int tcq_cache_attention_workspace_bytes(int dim, int heads, int q_heads, int64_t seqs,
                                         int64_t rows, size_t *bytes);

@@ -144,3 +144,26 @@ def test_graph_whose_values_change():
         torch.cuda.synchronize()
         _check(o, b, q, mc.quantised(k, "fp8"), mc.quantised(v, "fp8"), f"far {far}")
         assert torch.equal(o, api.cache_attention(q, cache, *b.where))
+
+
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("dtype", [BF16, torch.float32])
+@pytest.mark.parametrize("sizes", [[(90, 200)], [(100, 6000)], [(1, 700), (4, 90)]])
+def test_values_of_any_size(sizes, dtype, fmt):
+    """Values whose sums, times 2^8 that weights may exceed their reference by, stay below fp32's
+    largest number, and values next to its least normal one: outputs scale with them, bit for bit."""
+    g = _gen(6)
+    b = Batch(sizes, 16, g)
+    _, total = b.whole()
+    k, v = _randn(g, total, 2, 64), _randn(g, total, 2, 64)
+    q = _randn(g, b.rows, 8, 64).to(dtype)
+    base = api.cache_attention(q, _write(b, k, v, fmt), *b.where).double()
+    top = 125 - 8 - 13
+    for power in (top, 60, -60, -100):
+        o = api.cache_attention(q, _write(b, k, v * 2.0 ** power, fmt), *b.where).double()
+        want = base * 2.0 ** power
+        # (outputs near zero are subnormal at the low end; sums of weights times values keep fewer
+        # bits only below 2^-126)
+        big = want.abs() >= 2.0 ** -112
+        assert torch.equal(o[big], want[big]), power
+        assert bool(o.isfinite().all())

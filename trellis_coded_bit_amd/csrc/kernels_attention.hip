@@ -1195,13 +1195,16 @@ __device__ __forceinline__ bool attend_many(const AttArgs &a, const ManyLds &lds
     // (every tile was staged before the last meeting)
     if (kHalf && __builtin_expect(*lds.far_of != 0, 0)) return false;
     if constexpr (kHalf) {
+        // (the lift leaves sums and outputs alike)
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
+        for (int n = 0; n < NQ; ++n) {
+            sm[n].sum[0] *= 0x1p-7f;
 #pragma unroll
             for (int t = 0; t < kTiles; ++t)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
-                    acc[n][t][v] = __builtin_amdgcn_ldexpf(acc[n][t][v], ref - 127);
+                    acc[n][t][v] = __builtin_amdgcn_ldexpf(acc[n][t][v], ref - 127 - 7);
+        }
     }
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
