@@ -864,9 +864,9 @@ attend_few_kernel(AttArgs a) {
 // themselves or 2^-32 of the row's largest; values as the fp16 numbers that they are relative to
 // the first tile's largest scale byte.  Outputs are then as near float64's as their own rounding
 // and one per cent of it (1.67e-3 of their norm, 1.66e-3 with exact weights).  The four chunks
-// take 1283 us so, 1240 with weights of one bf16 number (2^-8: 2.34e-3) and 1740 with two; 64
-// dims 830, 816 and 998; 256 dims (four chunks of 511 to 1024 behind 4000 to 8192, 16 query heads
-// over 4) 605, 632 and 702.  Values whose scale bytes lie further apart than fp16's range:
+// take 1290 us so, 1242 with weights of one bf16 number (2^-8: 2.34e-3) and 1740 with two; 64
+// dims 831, 822 and 998; 256 dims (four chunks of 511 to 1024 behind 4000 to 8192, 16 query heads
+// over 4) 598, 632 and 702.  Values whose scale bytes lie further apart than fp16's range:
 // attend_far_kernel.
 // What a workgroup's threads share.
 struct ManyLds {
@@ -976,10 +976,6 @@ __device__ __forceinline__ bool attend_many(const AttArgs &a, const ManyLds &lds
     const int v_from = Units<D * 2>::across(lane);
 
     s16x8 q[NQ][TERMS][kGroups];
-#pragma unroll
-    for (int n = 0; n < NQ; ++n)
-        load_query<T, D, TERMS>(a, tile, r0 + 16 * n + l16,
-                                [&](int f) { return 32 * f + 8 * g; }, q[n]);
     f32x4 acc[NQ][kTiles];
     Softmax sm[NQ];
 #pragma unroll
@@ -1052,6 +1048,10 @@ __device__ __forceinline__ bool attend_many(const AttArgs &a, const ManyLds &lds
         load(base);
         find(base + KT);
     }
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+        load_query<T, D, TERMS>(a, tile, r0 + 16 * n + l16,
+                                [&](int f) { return 32 * f + 8 * g; }, q[n]);
     __syncthreads();
     if (kHalf) {
         if (base < tile.end) {
