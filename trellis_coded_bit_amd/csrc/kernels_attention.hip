@@ -857,8 +857,8 @@ attend_few_kernel(AttArgs a) {
 // first four after the whole tile, so that one wave of a SIMD computes its softmax while the other
 // multiplies; values are kept for a tile longer for it.
 //   Bound by what two waves of a SIMD issue between two meetings: four chunks of 511 to 2048 tokens
-// behind 4000 to 16384, 32 query heads over 8 of 128, bf16, 1240 us (882 TF) with the matrix cores
-// busy for 38 % of the clocks, VALU for 42 and LDS for 37.  (Without the third of the latter that
+// behind 4000 to 16384, 32 query heads over 8 of 128, bf16, 1290 us (850 TF) with the matrix cores
+// busy for 37 % of the clocks, VALU for 43 and LDS for 35.  (Without the third of the latter that
 // are bank conflicts of the keys' reads it took 3 % more.)
 //   bf16 queries' weights meet the values as one fp16 number each, lifted by 2^7, so to 2^-11 of
 // themselves or 2^-32 of the row's largest; values as the fp16 numbers that they are relative to

@@ -347,7 +347,7 @@ __device__ __forceinline__ void mx_tile(const Operand<CodePair> &A, const uint8_
 // one step on its way beside the two that are multiplied; 128 x 128: four waves of 64 x 64 and four
 // stages.  The phase before a meeting reads the next step's first fragments, and loads and
 // branches are kept out of the instructions' way.
-//   8192 x 4096 x 14336: 216 us, 4.4 PF (a library's product of the same type 291 us).  The matrix
+//   8192 x 4096 x 14336: 226 us, 4.3 PF (a library's product of the same type 291 us).  The matrix
 // cores are busy for 42 % of the clocks under the profiler, LDS for 17, and the waves wait for 40 % of
 // their time, for a step's loads and meeting.  (Other phases, no order of reads and products, and
 // a raised wave priority around the products: all within 1 %.)
