@@ -1345,9 +1345,11 @@ __global__ __launch_bounds__(256) void join_kernel(AttArgs few, AttArgs many, ui
 // ---------------------------------------------------------------- host side
 
 // Batches of few rows to a sequence (on average up to 16) are all given to the kernel of 16 rows,
-// which saves the other's launch: 64 sequences of 4 tokens behind 4000, 4 query heads to each of 8,
-// 127 us so, 136 with both; 256 of 3 behind 2000 255 and 321; 256 of one behind 4000, and one of 512 among
-// them, 527 and 565, but 64 with one of 190 199 and 175.
+// which saves the other's launch (us so / with both, 4 query heads to each of 8 of 128, bf16): 64
+// sequences of 4 tokens behind 4000 130 / 139, 256 of 3 behind 2000 220 / 231, 256 of one behind
+// 4000 390 / 399.  A chunk among them is not seen: of 512 tokens behind 2000 among 300 of one token
+// 159 / 163, of 512 behind 4000 among 256 491 / 477, of 190 among 64 217 / 191, of 2048 among 700 of
+// 1000 keys 672 / 522.
 bool few_only(int64_t rows, int group, int64_t seqs) {
     return rows * group <= kSmallRows * seqs;
 }
@@ -1433,9 +1435,9 @@ hipError_t attend_as(const AttArgs &base, char *ws, hipStream_t s) {
 // Two tiles of query rows to a wave read a key from LDS half as often as one, but their outputs,
 // queries and scores need room, and sequences of up to 256 rows leave half of them idle.  us with
 // two / with one (four chunks of 511 to 2048 tokens behind 4000 to 16384, 32 query heads over 8):
-//   64 dims: bf16 911 / 847, fp16 1206 / 1186, fp32 2039 / 1704;
-//   128 dims: bf16 1237 / 1618, fp16 (spills) 2623 / 2060; 256 dims spill;
-//   16 sequences of 256 rows, 128 dims, bf16, 231 both, of 400 rows 316 / 361.
+//   64 dims: bf16 972 / 839, fp16 1206 / 1186, fp32 2039 / 1704;
+//   128 dims: bf16 1289 / 1605, fp16 (spills) 2623 / 2060; 256 dims spill;
+//   16 sequences of 256 rows, 128 dims, bf16, 229 both, of 400 rows 331 / 357.
 template <typename T, int D, int FMT>
 hipError_t attend(const AttArgs &a, char *ws, hipStream_t s) {
     constexpr bool kTwo = D == 128 && terms<T>() == 1;
