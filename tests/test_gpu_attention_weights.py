@@ -167,3 +167,28 @@ def test_values_of_any_size(sizes, dtype, fmt):
         big = want.abs() >= 2.0 ** -112
         assert torch.equal(o[big], want[big]), power
         assert bool(o.isfinite().all())
+
+
+@pytest.mark.parametrize("fmt,power", [("fp8", 9), ("fp4", 3), ("fp8", -119), ("fp4", -120)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_groups_of_zeros_beside_any_size(dim, fmt, power):
+    """Groups of zeros (scale byte 0) and of zeros with other bytes, where the first keys' largest
+    byte is 128 or next to 0: they stay zeros, and cost no other value a bit."""
+    g = _gen(7)
+    n, length = 80, 200
+    b = Batch([(n, length)], 16, g)
+    k, v = _randn(g, length, 2, dim), torch.rand(length, 2, dim, generator=g, device="cuda")
+    v = (v + 1.0) * 2.0 ** power * torch.sign(_randn(g, length, 2, dim))
+    v[:, :, 32:64] = 0.0
+    v[40:60] = 0.0
+    q = _randn(g, n, 8, dim).bfloat16()
+    cache = _write(b, k, v, fmt)
+    o = api.cache_attention(q, cache, *b.where)
+    _check(o, b, q, mc.quantised(k, fmt), mc.quantised(v, fmt), f"{power}")
+    assert float(o[:, :, 32:64].abs().max()) == 0
+    # (groups whose codes are all zero: small values have byte 0 as well)
+    zero = (cache.v_codes == 0).unflatten(3, (dim // 32, -1)).all(4)
+    assert bool((cache.v_scale[zero] == 0).all())
+    for byte in (1, 127, 200, 254):
+        cache.v_scale[zero] = byte
+        assert torch.equal(api.cache_attention(q, cache, *b.where), o), byte

@@ -483,6 +483,13 @@ __device__ __forceinline__ void decode16(const u32x4 &q, float s, uint32_t *w) {
     }
 }
 
+// Whether some of 16 bytes of codes is not zero.
+template <int FMT>
+__device__ __forceinline__ bool any_code(const u32x4 &c) {
+    constexpr uint32_t kSize = FMT == TCQ_FP4 ? 0x77777777u : 0x7F7F7F7Fu;
+    return ((c[0] | c[1] | c[2] | c[3]) & kSize) != 0;
+}
+
 // ---------------------------------------------------------------- outputs
 
 // Shares of a tile: BQ x D sums, then BQ maxima and BQ sums of weights.
@@ -864,9 +871,9 @@ attend_few_kernel(AttArgs a) {
 // themselves or 2^-32 of the row's largest; values as the fp16 numbers that they are relative to
 // the first tile's largest scale byte.  Outputs are then as near float64's as their own rounding
 // and one per cent of it (1.67e-3 of their norm, 1.66e-3 with exact weights).  The four chunks
-// take 1290 us so, 1242 with weights of one bf16 number (2^-8: 2.34e-3) and 1740 with two; 64
-// dims 831, 822 and 998; 256 dims (four chunks of 511 to 1024 behind 4000 to 8192, 16 query heads
-// over 4) 598, 632 and 702.  Values whose scale bytes lie further apart than fp16's range:
+// take 1292 us so, 1242 with weights of one bf16 number (2^-8: 2.34e-3) and 1740 with two; 64
+// dims 835, 822 and 998; 256 dims (four chunks of 511 to 1024 behind 4000 to 8192, 16 query heads
+// over 4) 603, 632 and 702.  Values whose scale bytes lie further apart than fp16's range:
 // attend_far_kernel.
 // What a workgroup's threads share.
 struct ManyLds {
@@ -1022,6 +1029,19 @@ __device__ __forceinline__ bool attend_many(const AttArgs &a, const ManyLds &lds
                 put_values(j, mx::scale_of(e), v_at);
             }
         }
+        if (!__any(rare)) return;
+        if constexpr (kHalf) {
+            // Codes of zero are that whatever the scale (but one that stands for NaN): heads padded with
+            // zeros come here in every tile.
+            rare = false;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int by = now.ve[j] - ref;
+                const bool none =
+                    !any_code<FMT>(now.v[j]) && now.ve[j] != 255 && (by & 255) != 128;
+                rare |= (by < mx::kLowF16<FMT> || by > mx::kHighF16<FMT>) && !none;
+            }
+        }
         if (__builtin_expect(__any(rare), 0)) {
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
@@ -1030,10 +1050,7 @@ __device__ __forceinline__ bool attend_many(const AttArgs &a, const ManyLds &lds
                 if (e == 255) lds.wild_of[i & 3] = 1;
                 if constexpr (kHalf) {
                     if (by >= mx::kLowF16<FMT> && by <= mx::kHighF16<FMT>) continue;
-                    // (codes of zero are that whatever the scale)
-                    constexpr uint32_t kSize = FMT == TCQ_FP4 ? 0x77777777u : 0x7F7F7F7Fu;
-                    const u32x4 c = now.v[j];
-                    if (e != 255 && ((c[0] | c[1] | c[2] | c[3]) & kSize) != 0) *lds.far_of = 1;
+                    if (e != 255 && any_code<FMT>(now.v[j])) *lds.far_of = 1;
                     put_values(j, mx::scale_of(e == 255 ? 255 : 127), v_at);
                 }
             }
@@ -1058,7 +1075,8 @@ __device__ __forceinline__ bool attend_many(const AttArgs &a, const ManyLds &lds
             int top = 0;
 #pragma unroll
             for (int j = 0; j < kLoads; ++j)
-                if ((now.there >> j & 1) && now.ve[j] != 255 && now.ve[j] > top)
+                if ((now.there >> j & 1) && now.ve[j] != 255 && now.ve[j] > top &&
+                    any_code<FMT>(now.v[j]))
                     top = now.ve[j];
             for (int d = 32; d; d >>= 1) {
                 const int o = __shfl_xor(top, d);
