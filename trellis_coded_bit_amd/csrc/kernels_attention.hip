@@ -60,16 +60,16 @@ struct Sequence {
 };
 constexpr int kUnit = 128;      // keys: runs are whole units
 constexpr int kSmallRows = 16;      // query rows of the smaller tiles
-// Rows of a sequence that they serve beside the larger ones, which read keys less often but hold 128
-// or 256 rows (16 sequences of 2000 to 8000 keys, 32 query heads over 8, bf16: 32 rows 88 us with
-// small tiles, 155 with large; 64 rows 122 and 157; 96 rows 173 and 159).
+// Rows of a sequence that they serve beside the larger ones, which read keys less often but hold
+// 128 or 256 rows (16 sequences of 2000 to 8000 keys, 32 query heads over 8, bf16: 32 rows 88 us
+// with small tiles, 155 with large; 64 rows 122 and 157; 96 rows 173 and 159).
 constexpr int kFewRows = 64;
 // About how many runs there are to be, given the tiles' units in all.  A compute unit holds one
 // workgroup of the larger tiles and two of the smaller ones: as many runs as fill the card once,
 // and of the smaller tiles twice as many where each still has 16 units, for the sequences'
 // different lengths (one token of 4 sequences of 2000 to 8000 keys, 8 heads of 128: 24 us with 512,
-// 30 with 1024; of 16 of 1000 to 16000: 84 and 77; of 64: 261 and 253; 512 tokens behind 32000: 319 us
-// with 256, 344 with 512).
+// 30 with 1024; of 16 of 1000 to 16000: 84 and 77; of 64: 261 and 253; 512 tokens behind 32000: 319
+// us with 256, 344 with 512).
 constexpr int kTargetSmall = 1024, kTargetLarge = 256;
 template <int BQ>
 __device__ __forceinline__ uint32_t target(uint64_t units) {
@@ -96,7 +96,8 @@ __device__ __forceinline__ Sequence sequence(const AttArgs &a, int64_t s) {
     return r;
 }
 
-// Running sum over the lanes, of which `n` (uniform) at most are not zero; the last of 64 holds all.
+// Running sum over the lanes, of which `n` (uniform) at most are not zero; the last of 64 holds
+// all.
 __device__ __forceinline__ uint32_t wave_prefix(uint32_t v, int lane, int n) {
     for (int d = 1; d < n; d <<= 1) {
         const uint32_t o = __shfl_up(v, d);
@@ -189,8 +190,8 @@ __device__ __forceinline__ bool item_of(const AttArgs &a, uint32_t index, uint32
 
 // Batches of more than 64 sequences: a workgroup for each size of tile writes the units of a run
 // and, over the sequences, running sums of their counts (cut to 2^31), in which the others search.
-// (One token of 256 sequences of 100 to 600 keys, 32 query heads over 8 of 128, 66 us, with scans of
-// them all in every workgroup 97; of 1024 240 and 623; of 4096 917 and 7350.)
+// (One token of 256 sequences of 100 to 600 keys, 32 query heads over 8 of 128, 66 us, with scans
+// of them all in every workgroup 97; of 1024 240 and 623; of 4096 917 and 7350.)
 constexpr int kScanned = 64;
 constexpr int kPlanThreads = 1024;
 int64_t plan_words(int64_t seqs) { return seqs > kScanned ? 4 + (3 * seqs + 3) / 4 * 4 : 0; }
@@ -455,8 +456,8 @@ struct Units {
         return row(4 * (lane >> 4) + (l16 >> 2)) + (l16 & 3) * 8;
     }
 };
-// A = X^T of 16 columns and 32 rows: row 4 g + i of them in place i and row 16 + 4 g + i in place 4 +
-// i of lane group g.
+// A = X^T of 16 columns and 32 rows: row 4 g + i of them in place i and row 16 + 4 g + i in place 4
+// + i of lane group g.
 template <int W>
 __device__ __forceinline__ s16x8 read_across(const char *at) {
     typedef __attribute__((address_space(3))) s16x4 *P;
@@ -583,10 +584,10 @@ __device__ __forceinline__ HeadCache head_cache(const AttArgs &a, int head) {
     return h;
 }
 
-// acc += x p for a tile of values among which some stand for NaN, where a row does not see every key
-// (bit i of sees: the key in the lane's place i): a NaN reaches the rows that see its key, whatever
-// p, and no other (0 times NaN would).  The rows it reaches are those whose count of NaN keys, the
-// product of ones, is not zero.
+// acc += x p for a tile of values among which some stand for NaN, where a row does not see every
+// key (bit i of sees: the key in the lane's place i): a NaN reaches the rows that see its key,
+// whatever p, and no other (0 times NaN would).  The rows it reaches are those whose count of NaN
+// keys, the product of ones, is not zero.
 template <typename N, int TERMS>
 __device__ __forceinline__ void add_wild(const s16x8 &x, const s16x8 (&p)[TERMS], uint32_t sees,
                                          f32x4 &acc) {
@@ -611,9 +612,10 @@ __device__ __forceinline__ void add_wild(const s16x8 &x, const s16x8 (&p)[TERMS]
 // softmax; joined in LDS.  Keys go from memory straight into the first operand of S^T (a lane
 // reads a run of D / 4 dims of its key), values through the wave's own piece of LDS.  A tile's
 // codes are asked for while the one before is multiplied, its page numbers one earlier.
-//   Bound to two waves to a SIMD the compiler keeps the outputs out of the accumulation registers, whose
-// copies cost a tile 128 instructions (64 sequences, 4 heads of 128: fp32 over fp8 191 us, 145 with;
-// bf16 over fp4 99 and 96).  256 dims do not fit but for bf16 over fp4 (235 and 196; fp8 305 and 544).
+//   Bound to two waves to a SIMD the compiler keeps the outputs out of the accumulation registers,
+// whose copies cost a tile 128 instructions (64 sequences, 4 heads of 128: fp32 over fp8 191 us,
+// 145 with; bf16 over fp4 99 and 96).  256 dims do not fit but for bf16 over fp4 (235 and 196; fp8
+// 305 and 544).
 //   Bound by memory: 64 sequences of 1000 to 16000 keys, 8 heads of 128, fp8, 252 us at 4.6 TB/s.
 //   So bf16 queries' weights in two terms cost little, and leave the outputs' own rounding alone
 // (relative to the norm of float64 outputs 1.66e-3 there, the outputs' rounding itself, and 2.33e-3
@@ -857,9 +859,9 @@ attend_few_kernel(AttArgs a) {
 
 // ---------------------------------------------------------------- many query rows
 
-// NQ tiles of 16 query rows to each of NW waves.  The workgroup's threads decode tiles of keys into LDS
-// for all waves: while a tile is multiplied, the next one's codes, which arrived during the tile
-// before, go into LDS, and those of the one after are asked for.
+// NQ tiles of 16 query rows to each of NW waves.  The workgroup's threads decode tiles of keys into
+// LDS for all waves: while a tile is multiplied, the next one's codes, which arrived during the
+// tile before, go into LDS, and those of the one after are asked for.
 //   With eight waves the second four meet the others between their scores and their softmax, the
 // first four after the whole tile, so that one wave of a SIMD computes its softmax while the other
 // multiplies; values are kept for a tile longer for it.
@@ -1031,8 +1033,8 @@ __device__ __forceinline__ bool attend_many(const AttArgs &a, const ManyLds &lds
         }
         if (!__any(rare)) return;
         if constexpr (kHalf) {
-            // Codes of zero are that whatever the scale (but one that stands for NaN): heads padded with
-            // zeros come here in every tile.
+            // Codes of zero are that whatever the scale (but one that stands for NaN): heads padded
+            // with zeros come here in every tile.
             rare = false;
 #pragma unroll
             for (int j = 0; j < kLoads; ++j) {
@@ -1366,8 +1368,8 @@ __global__ __launch_bounds__(256) void join_kernel(AttArgs few, AttArgs many, ui
 // which saves the other's launch (us so / with both, 4 query heads to each of 8 of 128, bf16): 64
 // sequences of 4 tokens behind 4000 130 / 139, 256 of 3 behind 2000 220 / 231, 256 of one behind
 // 4000 390 / 399.  A chunk among them is not seen: of 512 tokens behind 2000 among 300 of one token
-// 159 / 163, of 512 behind 4000 among 256 491 / 477, of 190 among 64 217 / 191, of 2048 among 700 of
-// 1000 keys 672 / 522.
+// 159 / 163, of 512 behind 4000 among 256 491 / 477, of 190 among 64 217 / 191, of 2048 among 700
+// of 1000 keys 672 / 522.
 bool few_only(int64_t rows, int group, int64_t seqs) {
     return rows * group <= kSmallRows * seqs;
 }

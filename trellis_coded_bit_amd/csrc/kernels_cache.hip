@@ -27,8 +27,8 @@ struct CacheMove {
 constexpr int kMoveThreads = 256;
 constexpr int kAhead = 4;
 
-// Where row `row` of the call lies in the cache: its page (-1: nowhere) and position, uniform in the
-// wave; false behind the last sequence.  64 sequences at most are searched with one access.
+// Where row `row` of the call lies in the cache: its page (-1: nowhere) and position, uniform in
+// the wave; false behind the last sequence.  64 sequences at most are searched with one access.
 __device__ __forceinline__ bool find(const CacheMove &a, int64_t row, int64_t &page,
                                      int64_t &pos) {
     const int lane = threadIdx.x & 63;

@@ -4,8 +4,8 @@
 // ties to even, clamped to 6 or 448.  Multiplying by a power of two is exact, so a code has one
 // rounding.  E = 255 (an infinity or a NaN) gives e = 255, which stands for NaN throughout.
 //   Both directions are bound by memory: one pass, eight values or 16 bytes of output a thread
-// (16384 x 14336 bf16 into 8 bits 129 us, back 126: 5.5 and 5.6 TB/s; 2048 x 2048 fp32 into 4 bits 4.2,
-// back 4.9, about twice a launch).
+// (16384 x 14336 bf16 into 8 bits 129 us, back 126: 5.5 and 5.6 TB/s; 2048 x 2048 fp32 into 4 bits
+// 4.2, back 4.9, about twice a launch).
 #include <hip/hip_runtime.h>
 
 #include "checkpoint_device.h"

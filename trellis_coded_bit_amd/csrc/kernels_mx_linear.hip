@@ -120,8 +120,8 @@ __global__ __launch_bounds__(256) void order_scales_kernel(ScaleArgs x, ScaleArg
         order_scales(w, q - x.work);
 }
 
-// The ordered scales of F fragments (16 rows each) of one operand, from row r0 on: a uniform address
-// and the lane's offset.
+// The ordered scales of F fragments (16 rows each) of one operand, from row r0 on: a uniform
+// address and the lane's offset.
 template <int F>
 struct ScaleReader {
     static constexpr int kWords = F / 2;
@@ -144,9 +144,9 @@ struct ScaleReader {
 
 // The loads of a tile of TR rows by one step, as TileLoader's (chunk c of row r into slot c ^ (r >>
 // 1 & 7), zeros past the rows and past k), with one offset of 32 bits per thread (rows at most
-// kMostPitch bytes apart): a thread's rows lie NT / 8 rows apart.  `renew` makes an offset a new value to the compiler, which otherwise holds every
-// sum with it in registers, 26 of them, and spills to make room; a spill's return waits for all
-// loads on their way.
+// kMostPitch bytes apart): a thread's rows lie NT / 8 rows apart.  `renew` makes an offset a new
+// value to the compiler, which otherwise holds every sum with it in registers, 26 of them, and
+// spills to make room; a spill's return waits for all loads on their way.
 template <int TR, int NT>
 struct CodeLoader {
     static constexpr int kLoads = TR * 8 / NT;
@@ -206,7 +206,8 @@ __device__ __forceinline__ void mx_tile(const Operand<CodePair> &A, const uint8_
                                         int s_end, const gemm::Stages<NB> &st, const Epi &epi) {
     constexpr int NT = WI * WJ * 64;
     constexpr int FI = TI / WI / 16, FJ = TJ / WJ / 16;
-    // fragments of A to a phase (two to a phase of 256 rows: 8192 x 4096 x 14336 224.9 us, four 223.2)
+    // fragments of A to a phase (two to a phase of 256 rows: 8192 x 4096 x 14336 224.9 us, four
+    // 223.2)
     constexpr int FH = FI / 2, kParts = FI / FH, kPhases = 2 * kParts;
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -343,14 +344,14 @@ __device__ __forceinline__ void mx_tile(const Operand<CodePair> &A, const uint8_
 }
 
 // A step is 256 columns: 128 bytes of each row's codes, which go into LDS as they are, and two
-// matrix instructions deep.  256 x 256 tiles: eight waves of 128 x 64 and a ring of five half stages,
-// one step on its way beside the two that are multiplied; 128 x 128: four waves of 64 x 64 and four
-// stages.  The phase before a meeting reads the next step's first fragments, and loads and
+// matrix instructions deep.  256 x 256 tiles: eight waves of 128 x 64 and a ring of five half
+// stages, one step on its way beside the two that are multiplied; 128 x 128: four waves of 64 x 64
+// and four stages.  The phase before a meeting reads the next step's first fragments, and loads and
 // branches are kept out of the instructions' way.
 //   8192 x 4096 x 14336: 226 us, 4.3 PF (a library's product of the same type 291 us).  The matrix
-// cores are busy for 42 % of the clocks under the profiler, LDS for 17, and the waves wait for 40 % of
-// their time, for a step's loads and meeting.  (Other phases, no order of reads and products, and
-// a raised wave priority around the products: all within 1 %.)
+// cores are busy for 42 % of the clocks under the profiler, LDS for 17, and the waves wait for 40 %
+// of their time, for a step's loads and meeting.  (Other phases, no order of reads and products,
+// and a raised wave priority around the products: all within 1 %.)
 template <int TI, int TJ, int WI, int WJ, int NB, typename Epi>
 __global__ __launch_bounds__(WI *WJ * 64) void mx_gemm_kernel(Operand<CodePair> A,
                                                               const uint8_t *as,
@@ -388,21 +389,21 @@ __global__ __launch_bounds__(WI *WJ * 64) void mx_gemm_kernel(Operand<CodePair> 
 
 // ---------------------------------------------------------------- few rows of x
 
-// y for 16 BT rows of x (blockIdx.y's).  A workgroup of eight waves takes 16 rows of W at a time; the
-// waves share their columns in pairs of 128 (eight groups).  W is read once, straight into the
+// y for 16 BT rows of x (blockIdx.y's).  A workgroup of eight waves takes 16 rows of W at a time;
+// the waves share their columns in pairs of 128 (eight groups).  W is read once, straight into the
 // matrix instruction's operand: lane (l16, g) reads groups 2 g and 2 g + 1 of a pair, 32 bytes of
 // row l16, so that an instruction touches a line of each row and the two scales are one access.
 // With 4-bit rows the codes are the operand; with 8-bit ones a group's 32 codes become four bf16
 // fragments, fragment j holding columns 8 j .. 8 j + 7 of the lane's group.  Either is another
 // order of k than memory's, the same for both operands.
-//   The next chunk's W, or the next rows', is on its way while one is multiplied and the waves' sums
-// meet in LDS (in wave order, in two halves by turns).
+//   The next chunk's W, or the next rows', is on its way while one is multiplied and the waves'
+// sums meet in LDS (in wave order, in two halves by turns).
 //   DENSE: x comes as it is (few values) and is quantised into LDS by every workgroup, in the
 // form the products read.  Otherwise it comes in the order in which the lanes read it (one
 // contiguous KiB per instruction: 16 rows of codes as they lie cost an instruction 16 lines).
-//   Bound by memory and its first answer: 1 x 14336 x 4096 with 8-bit rows 10.4 us (3.0 TB/s of W), of
-// which a launch that only ends takes 2; 100 x 4096 x 4096 with 4-bit rows 7.8, bound by reading the
-// rows again in all 256 workgroups.
+//   Bound by memory and its first answer: 1 x 14336 x 4096 with 8-bit rows 10.4 us (3.0 TB/s of W),
+// of which a launch that only ends takes 2; 100 x 4096 x 4096 with 4-bit rows 7.8, bound by reading
+// the rows again in all 256 workgroups.
 constexpr int kMxWaves = 8;
 
 struct MxSmallArgs {
@@ -623,8 +624,8 @@ __global__ __launch_bounds__(kMxWaves * 64) void mx_small_kernel(MxSmallArgs a,
     }
 }
 
-// Codes of B rows as they lie into the order in which mx_small_kernel's lanes read them: pair, tile of
-// 16 rows, group of the lane's two, half (8-bit), lane; scales: pair, tile, lane, group.  16
+// Codes of B rows as they lie into the order in which mx_small_kernel's lanes read them: pair, tile
+// of 16 rows, group of the lane's two, half (8-bit), lane; scales: pair, tile, lane, group.  16
 // bytes a thread.
 template <int FMT>
 __global__ __launch_bounds__(256) void order_rows_kernel(const uint8_t *__restrict__ codes,
@@ -656,17 +657,18 @@ __global__ __launch_bounds__(256) void order_rows_kernel(const uint8_t *__restri
 // Whether mx_small_kernel takes B rows of x; never one batch and not a smaller one (us per call in
 // a graph, it / the tiled product).  4-bit rows up to 128, and beyond while a row of W's tiles and
 // of x's shares makes at most 896 workgroup turns: 256 x 2048 x 2048 8.7 / 17.3, 384 x 4096 x 4096
-// 24.1 / 26.2, 128 x 14336 x 4096 26.6 / 25.7 (with one row more); 512 x 4096 x 4096 31.0 / 27.0.  8-bit
-// rows, whose tiled product needs W in 16 bits, up to 512: 160 x 4096 x 4096 23.1 / 37.5, 512 x 4096
-// x 4096 44.1 / 44.8, 512 x 14336 x 4096 138 / 161.
+// 24.1 / 26.2, 128 x 14336 x 4096 26.6 / 25.7 (with one row more); 512 x 4096 x 4096 31.0 / 27.0.
+// 8-bit rows, whose tiled product needs W in 16 bits, up to 512: 160 x 4096 x 4096 23.1 / 37.5, 512
+// x 4096 x 4096 44.1 / 44.8, 512 x 14336 x 4096 138 / 161.
 bool mx_small(int format, int64_t B, int64_t M) {
     if (format == TCQ_FP8) return B <= 512;
     return B <= 128 || (B + 127) / 128 * ((M + 15) / 16) <= 896;
 }
 
 // Values of x that mx_small_kernel quantises by itself, in every workgroup, rather than a launch
-// before it (us per call in a graph, it / the two: fp8 1 x 4096 x 4096 5.6 / 7.1, 1 x 4096 x 14336 11.7 /
-// 12.9, 4 x 4096 x 4096 6.9 / 6.9, 8 x 4096 x 4096 8.7 / 7.0; fp4 16 x 2048 x 2048 7.4 / 6.0).
+// before it (us per call in a graph, it / the two: fp8 1 x 4096 x 4096 5.6 / 7.1, 1 x 4096 x 14336
+// 11.7 / 12.9, 4 x 4096 x 4096 6.9 / 6.9, 8 x 4096 x 4096 8.7 / 7.0; fp4 16 x 2048 x 2048 7.4 /
+// 6.0).
 constexpr int64_t kMxDenseValues = 16384;
 
 // Workgroups of 256 threads, each of which takes every so many-th of `work` pieces.
@@ -745,11 +747,11 @@ hipError_t launch_small(MxSmallArgs a, const LayerEpilogue<T> &epi, hipStream_t 
 
 // Tile and splits of the product of B rows of 4-bit codes with M over `steps` steps of 256 columns.
 // 256 x 256 tiles where they are at least half as many as compute units (us per call in a graph,
-// they / 128 x 128: 2048 x 4096 x 4096 47.0 / 48.1, 1024 x 14336 x 4096 47.9 / 79.2, 4096^3 55.6 / 84.0;
-// with 64 tiles, 1024 x 4096 x 4096, 43.0 / 29.0).  Else 128 x 128, whose columns are split in two
-// where at most half the compute units have a tile, if there are steps enough (512 x 4096 x 14336 38.9
-// split / 50.1 whole, 512 x 4096 x 4096, 16 steps, 27.6 / 26.1).  Tiles are never fewer than 113:
-// smaller products are mx_small_kernel's.
+// they / 128 x 128: 2048 x 4096 x 4096 47.0 / 48.1, 1024 x 14336 x 4096 47.9 / 79.2, 4096^3 55.6 /
+// 84.0; with 64 tiles, 1024 x 4096 x 4096, 43.0 / 29.0).  Else 128 x 128, whose columns are split
+// in two where at most half the compute units have a tile, if there are steps enough (512 x 4096 x
+// 14336 38.9 split / 50.1 whole, 512 x 4096 x 4096, 16 steps, 27.6 / 26.1).  Tiles are never fewer
+// than 113: smaller products are mx_small_kernel's.
 struct MxPlan {
     bool big;
     int splits, steps, steps_per_split;
@@ -831,8 +833,8 @@ hipError_t linear_rows(const MxLinearCall &c, const MxLayout &lay, bool small, c
     const bool dense = small && small_dense(c);
     MxMatrix x = c.xq;
     uint16_t *xvals = reinterpret_cast<uint16_t *>(ws + lay.xvals);
-    // (large batches of 8-bit rows are read as the bf16 numbers that the codes stand for, small ones
-    // of either in the order of mx_small_kernel's lanes)
+    // (large batches of 8-bit rows are read as the bf16 numbers that the codes stand for, small
+    // ones of either in the order of mx_small_kernel's lanes)
     const bool values = !small && !fp4;
     const int64_t groups = groups_of(c.N), pairs = pairs_of(groups);
     const int nbt = static_cast<int>((c.B + 15) / 16);
@@ -893,9 +895,9 @@ hipError_t linear_rows(const MxLinearCall &c, const MxLayout &lay, bool small, c
     return launch_dense_product(d, ws + lay.parts, s);
 }
 
-// Bytes between the rows of codes up to which a tile's offsets fit CodeLoader's 32 bits: 255
-// rows of it, and a row's last piece, lie below the largest extent of a buffer.  Codes further apart
-// are multiplied by mx_small_kernel, whose offsets have 64 bits, in pieces of so many rows that its
+// Bytes between the rows of codes up to which a tile's offsets fit CodeLoader's 32 bits: 255 rows
+// of it, and a row's last piece, lie below the largest extent of a buffer.  Codes further apart are
+// multiplied by mx_small_kernel, whose offsets have 64 bits, in pieces of so many rows that its
 // grid holds their shares.
 constexpr int64_t kMostPitch = 1 << 24;
 static_assert(255 * kMostPitch + 128 < 0xFFFFFF00ll, "offsets of a tile");

@@ -211,8 +211,8 @@ struct MxMatrix {
 // Codes and scale bytes, and, where values is not NULL, the bf16 numbers they stand for (up to
 // whole groups); codes and scale may be NULL.  Unpack also writes zeros to columns cols ..
 // padded - 1.
-// order: codes and scale bytes in the order in which the few-rows product reads them (whole tiles of
-// 16 rows, of which those past `rows` are left as they were, and whole pairs of 128 columns).
+// order: codes and scale bytes in the order in which the few-rows product reads them (whole tiles
+// of 16 rows, of which those past `rows` are left as they were, and whole pairs of 128 columns).
 struct MxOrder {
     uint8_t *codes, *scale;
     int nbt;            // tiles of 16 rows
